@@ -1,0 +1,344 @@
+// The 8-bit prefix cache: quantisation of rows as they are written, read-back,
+// and the entry points of its attention.
+//
+// A cached row is hd E4M3 codes; a block of 64 rows of one (sequence, kv head)
+// shares a power-of-two scale 2^e.  A power of two costs no relative precision
+// (E4M3 is a floating-point format) and buys four things: the quotient x 2^-e
+// is exact, so a code is the correctly rounded value; code x scale is exact in
+// bf16; a block whose scale grows moves its codes without a second rounding
+// (but for subnormals); and attention can fold scales into exponents.
+#include <climits>
+
+#include "dg_kv8.cuh"
+
+namespace dg {
+namespace {
+
+// ----------------------------------------------------------------- append --
+struct Kv8AppendArgs {
+  const void *k, *v;      // bf16 [B][Hkv][n][hd]
+  uint8_t *K, *V, *Ke, *Ve;
+  const int *len, *counts;
+  int* status;
+  int B, n, Hkv, hd, cap, nblk;
+};
+
+constexpr int kAppendThreads = 256;
+
+// Smallest e with absmax <= 448 2^e, from absmax's bf16 bits: 448 = 1.75 2^8.
+DG_DEV int kv8_exponent(unsigned bits) {
+  const int E = (int)(bits >> 7), m = (int)(bits & 127u);
+  const int e = E - 127 - 8 + (m > 96 ? 1 : 0);
+  return E == 0 ? kKv8Emin : min(max(e, kKv8Emin), kKv8Emax);
+}
+
+// One CTA per (block of 64 cached rows, kv head and sequence, K or V): the new
+// rows that fall into the block stay in registers between the reduction of
+// their maximum and the rounding, so every input is read once.  16 values per
+// thread and chunk: two 16-byte loads, one 16-byte store.  Bound by memory.
+template <int HD>
+__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(Kv8AppendArgs a) {
+  pdl_wait();
+  constexpr int CPR = HD / 16;                                   // chunks per row
+  constexpr int NCH = kKv8Block * CPR;
+  constexpr int PER = (NCH + kAppendThreads - 1) / kAppendThreads;
+  __shared__ unsigned red[kAppendThreads / 32];
+  const int bh = blockIdx.y, b = bh / a.Hkv, tid = threadIdx.x;
+  const bool isv = blockIdx.z != 0;
+  const int len = a.len[b], n = a.counts ? a.counts[b] : a.n;
+  if (len < 0 || n < 0 || n > a.n || (long long)len + n > a.cap) {  // nothing of this sequence is written
+    if (tid == 0) atomicExch(a.status, (n < 0 || n > a.n) ? kStatusArg : kStatusCapacity);
+    return;
+  }
+  const int blk = len / kKv8Block + blockIdx.x;
+  const int row0 = blk * kKv8Block;                              // first cached row of the block
+  const int lo = max(len - row0, 0), hi = min(len + n - row0, kKv8Block);  // its new rows
+  if (hi <= lo) return;
+  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(isv ? a.v : a.k) + (size_t)bh * a.n * HD;
+  uint8_t* dst = (isv ? a.V : a.K) + ((size_t)bh * a.cap + row0) * HD;
+  uint8_t* ep = (isv ? a.Ve : a.Ke) + (size_t)bh * a.nblk + blk;
+
+  uint4 x[PER][2];
+  unsigned top = 0;                                              // two 16-bit maxima of |x|'s bits
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int c = p * kAppendThreads + tid, r = c / CPR;
+    const bool mine = c < NCH && r >= lo && r < hi;
+    x[p][0] = x[p][1] = make_uint4(0, 0, 0, 0);
+    if (mine) {
+      const uint4* s = reinterpret_cast<const uint4*>(src + (size_t)(row0 + r - len) * HD + (c % CPR) * 16);
+      x[p][0] = __ldcs(s);
+      x[p][1] = __ldcs(s + 1);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 w = x[p][h];
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                   __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+    }
+  }
+  auto block_max = [&](unsigned t) {
+    t = max(t & 0xffffu, t >> 16);
+    t = __reduce_max_sync(0xffffffffu, t);
+    if (tid % 32 == 0) red[tid / 32] = t;
+    __syncthreads();
+    t = red[tid % (kAppendThreads / 32)];
+    return __reduce_max_sync(0xffffffffu, t);
+  };
+  unsigned amax = block_max(top);
+  if (amax >= 0x7f80u) {
+    // An infinity or NaN among the values: the scale goes by the finite ones,
+    // infinities saturate, NaN is stored as zero, and the status word says so.
+    if (tid == 0) atomicExch(a.status, kStatusValue);
+    top = 0;
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&x[p][0]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const unsigned mag = (w[j] >> (16 * h)) & 0x7fffu;
+          if (mag > 0x7f80u) w[j] &= ~(0xffffu << (16 * h));
+          if (mag < 0x7f80u) top = max(top, mag);
+        }
+      }
+    }
+    __syncthreads();  // red is read above
+    amax = block_max(top);
+  }
+  int e = kv8_exponent(amax);
+  if (lo > 0) {
+    // Earlier rows share the block: its scale never shrinks, and where it
+    // grows their codes move to it.
+    const int was = (int)*ep - kKv8Bias;
+    if (e > was) {
+      const float f = pow2i(was - e);
+      for (int c = tid; c < lo * CPR; c += kAppendThreads) {
+        uint4 w = *reinterpret_cast<const uint4*>(dst + c * 16);
+        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t h0 = e4m3x2_f16x2(u[j]), h1 = e4m3x2_f16x2(u[j] >> 16);
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+          u[j] = pack_e4m3(f0.x * f, f0.y * f) | (pack_e4m3(f1.x * f, f1.y * f) << 16);
+        }
+        *reinterpret_cast<uint4*>(dst + c * 16) = w;
+      }
+    } else {
+      e = was;
+    }
+    __syncthreads();  // every thread has read *ep
+  }
+  if (tid == 0) *ep = (uint8_t)(e + kKv8Bias);
+  const float f = pow2i(-e);
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int c = p * kAppendThreads + tid, r = c / CPR;
+    if (c >= NCH || r < lo || r >= hi) continue;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[p][0]);
+    uint32_t q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = w[2 * j], t = w[2 * j + 1];
+      q[j] = pack_e4m3(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f) |
+             (pack_e4m3(__uint_as_float(t << 16) * f, __uint_as_float(t & 0xffff0000u) * f) << 16);
+    }
+    *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(q[0], q[1], q[2], q[3]);
+  }
+}
+
+// ------------------------------------------------------------------- read --
+struct Kv8ReadArgs {
+  const uint8_t *K, *V, *Ke, *Ve;
+  const int* len;
+  void *k, *v;            // bf16 [B][Hkv][pitch][hd]
+  int* status;
+  int B, Hkv, hd, cap, nblk, row0, n, pitch;
+};
+
+constexpr int kReadThreads = 256, kReadPer = 4;
+
+// Codes back to bf16 (exact): 16 codes per thread and chunk.  Bound by memory,
+// two thirds of it the writes.
+template <int HD>
+__global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(Kv8ReadArgs a) {
+  pdl_wait();
+  constexpr int CPR = HD / 16;
+  const int bh = blockIdx.y, b = bh / a.Hkv;
+  const bool isv = blockIdx.z != 0;
+  const int len = a.len[b];
+  if ((len < 0 || len > a.cap) && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.status, kStatusCapacity);
+  const long long rows = min(a.n, min(len, a.cap) - a.row0);     // rows of this sequence in the range
+  const uint8_t* src = (isv ? a.V : a.K) + ((size_t)bh * a.cap + a.row0) * HD;
+  const uint8_t* ep = (isv ? a.Ve : a.Ke) + (size_t)bh * a.nblk;
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(isv ? a.v : a.k) + (size_t)bh * a.pitch * HD;
+  const long long c0 = (long long)blockIdx.x * (kReadThreads * kReadPer) + threadIdx.x;
+  uint4 w[kReadPer];
+  int x[kReadPer];
+#pragma unroll
+  for (int p = 0; p < kReadPer; ++p) {
+    const long long c = c0 + p * kReadThreads;
+    if (c < rows * CPR) {
+      w[p] = __ldcs(reinterpret_cast<const uint4*>(src + c * 16));
+      x[p] = ep[(a.row0 + (int)(c / CPR)) / kKv8Block];
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kReadPer; ++p) {
+    const long long c = c0 + p * kReadThreads;
+    if (c >= rows * CPR) continue;
+    const float f = pow2i(x[p] - kKv8Bias);
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&w[p]);
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t h = e4m3x2_f16x2(u[j / 2] >> (16 * (j & 1)));
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      o[j] = pack_bf16(t.x * f, t.y * f);
+    }
+    uint4* d = reinterpret_cast<uint4*>(dst + c * 16);
+    d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// The checks every entry point of the cache shares.
+dg_status check_kv8(const dg_kv8_cache* c) {
+  if (!c || !c->K || !c->V || !c->K_exp || !c->V_exp || !c->len || !c->status) return DG_ERR_ARG;
+  if (c->B <= 0 || c->Hkv <= 0 || c->cap <= 0) return DG_ERR_ARG;
+  if (!aligned16(c->K) || !aligned16(c->V)) return DG_ERR_ARG;
+  if (c->hd != 32 && c->hd != 64 && c->hd != 128) return DG_ERR_SHAPE;
+  // grid.y holds one row per (sequence, kv head); TMA row coordinates are int32
+  if ((int64_t)c->B * c->Hkv > 65535 || (int64_t)c->B * c->Hkv * c->cap > INT32_MAX - 65536 || c->cap > (1 << 30))
+    return DG_ERR_SHAPE;
+  return DG_OK;
+}
+
+dg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DG_OK : DG_ERR_CUDA; }
+
+int kv8_blocks(int cap) { return cdiv(cap, kKv8Block); }
+
+struct Kv8Ws {
+  size_t part, ml, total;
+  int rows, tk, units, workers;
+};
+
+// Rows per unit and the workspace of an attention call.
+Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
+  Kv8Ws w{};
+  const int64_t R = (int64_t)(Hq / c->Hkv) * C;
+  w.rows = kv8_mma_rows(c->hd, R);
+  w.tk = kKv8Block;
+  w.workers = kKv8Ctas * kKv8Warps;
+  w.units = (int)(c->Hkv * ((R + w.rows - 1) / w.rows));
+  w.part = 0;
+  w.ml = align_up((size_t)2 * w.workers * w.rows * c->hd * 4, 256);
+  w.total = w.ml + align_up((size_t)2 * w.workers * w.rows * 8, 256);
+  return w;
+}
+
+dg_status check_kv8_attention(const dg_kv8_cache* c, int C, int Hq) {
+  dg_status s = check_kv8(c);
+  if (s) return s;
+  if (C <= 0 || Hq <= 0 || Hq % c->Hkv != 0) return DG_ERR_ARG;
+  // the bounds the denoising step and dg_attention_noalloc apply
+  if (C > 1024 || (int64_t)c->B * C > (1 << 20) || (int64_t)c->B * Hq > 65535) return DG_ERR_SHAPE;
+  return DG_OK;
+}
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" dg_status dg_kv8_append(const dg_kv8_cache* cache, const void* k, const void* v, int32_t n,
+                                   const int32_t* counts, void* stream) {
+  dg_status s = check_kv8(cache);
+  if (s) return s;
+  if (!k || !v || n <= 0 || !aligned16(k) || !aligned16(v)) return DG_ERR_ARG;
+  if (n > cache->cap) return DG_ERR_CAPACITY;
+  Kv8AppendArgs a{k, v, static_cast<uint8_t*>(cache->K), static_cast<uint8_t*>(cache->V),
+                  static_cast<uint8_t*>(cache->K_exp), static_cast<uint8_t*>(cache->V_exp), cache->len, counts,
+                  cache->status, cache->B, n, cache->Hkv, cache->hd, cache->cap, kv8_blocks(cache->cap)};
+  // blocks that n rows can touch, from any offset
+  const dim3 grid((n - 1 + kKv8Block - 1) / kKv8Block + 1, cache->B * cache->Hkv, 2);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (cache->hd) {
+    case 32: return from_cuda(launch_pdl(kv8_append_kernel<32>, grid, dim3(kAppendThreads), 0, st, a));
+    case 64: return from_cuda(launch_pdl(kv8_append_kernel<64>, grid, dim3(kAppendThreads), 0, st, a));
+  }
+  return from_cuda(launch_pdl(kv8_append_kernel<128>, grid, dim3(kAppendThreads), 0, st, a));
+}
+
+extern "C" dg_status dg_kv8_read(const dg_kv8_cache* cache, int32_t row0, int32_t n, void* k, void* v,
+                                 int32_t pitch, void* stream) {
+  dg_status s = check_kv8(cache);
+  if (s) return s;
+  if (!k || !v || row0 < 0 || n <= 0 || pitch < n || !aligned16(k) || !aligned16(v)) return DG_ERR_ARG;
+  if (row0 >= cache->cap) return DG_OK;  // no row there: nothing to write
+  Kv8ReadArgs a{static_cast<const uint8_t*>(cache->K), static_cast<const uint8_t*>(cache->V),
+                static_cast<const uint8_t*>(cache->K_exp), static_cast<const uint8_t*>(cache->V_exp), cache->len, k, v,
+                cache->status, cache->B, cache->Hkv, cache->hd, cache->cap, kv8_blocks(cache->cap), row0, n, pitch};
+  const int rows = n < cache->cap - row0 ? n : cache->cap - row0;
+  const dim3 grid(cdiv((int64_t)rows * (cache->hd / 16), kReadThreads * kReadPer), cache->B * cache->Hkv, 2);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (cache->hd) {
+    case 32: return from_cuda(launch_pdl(kv8_read_kernel<32>, grid, dim3(kReadThreads), 0, st, a));
+    case 64: return from_cuda(launch_pdl(kv8_read_kernel<64>, grid, dim3(kReadThreads), 0, st, a));
+  }
+  return from_cuda(launch_pdl(kv8_read_kernel<128>, grid, dim3(kReadThreads), 0, st, a));
+}
+
+extern "C" dg_status dg_kv8_attention_workspace(const dg_kv8_cache* cache, int32_t C, int32_t Hq, size_t* bytes) {
+  if (!bytes) return DG_ERR_ARG;
+  dg_status s = check_kv8_attention(cache, C, Hq);
+  if (s) return s;
+  *bytes = kv8_ws(cache, C, Hq).total;
+  return DG_OK;
+}
+
+extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, const void* k, const void* v, void* o,
+                                      int32_t C, int32_t Hq, int32_t causal, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  dg_status s = check_kv8_attention(cache, C, Hq);
+  if (s) return s;
+  if (!q || !o || !k != !v || !ws) return DG_ERR_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(k) || !aligned16(v)) return DG_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return DG_ERR_WORKSPACE;
+  const Kv8Ws w = kv8_ws(cache, C, Hq);
+  if (ws_bytes < w.total) return DG_ERR_WORKSPACE;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  Kv8AttnArgs a{};
+  a.q = q;
+  a.K = static_cast<const uint8_t*>(cache->K);
+  a.V = static_cast<const uint8_t*>(cache->V);
+  a.Ke = static_cast<const uint8_t*>(cache->K_exp);
+  a.Ve = static_cast<const uint8_t*>(cache->V_exp);
+  a.len = cache->len;
+  a.kn = k;
+  a.vn = v;
+  a.o = o;
+  a.part = reinterpret_cast<float*>(base + w.part);
+  a.ml = reinterpret_cast<float*>(base + w.ml);
+  a.status = cache->status;
+  a.B = cache->B;
+  a.C = C;
+  a.Hq = Hq;
+  a.Hkv = cache->Hkv;
+  a.hd = cache->hd;
+  a.cap = cache->cap;
+  a.nblk = kv8_blocks(cache->cap);
+  a.causal = causal != 0;
+  a.rows = w.rows;
+  a.tk = w.tk;
+  a.units = w.units;
+  a.workers = w.workers;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_kv8_attention_mma(a, st);
+  if (e == cudaSuccess) e = launch_kv8_merge(a, st);
+  return from_cuda(e);
+}

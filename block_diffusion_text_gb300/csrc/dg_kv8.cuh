@@ -1,0 +1,131 @@
+// Shared declarations of the 8-bit prefix cache: its layout, the division of
+// an attention call into pieces, and the launchers of its kernels.
+#pragma once
+
+#include "dg_common.cuh"
+#include "dg_internal.h"
+
+namespace dg {
+
+constexpr int kKv8Block = 64;             // cached tokens per scale
+constexpr int kKv8Bias = 127;             // exponent byte x: scale 2^(x - 127)
+constexpr int kKv8Emin = -64, kKv8Emax = 118;
+constexpr int kKv8Ctas = kTargetCtas;     // CTAs of an attention launch (one per SM)
+constexpr int kKv8Warps = 8;              // workers per CTA of the warp-MMA kernel
+constexpr int kStatusArg = 1, kStatusCapacity = 3;  // DG_ERR_ARG, DG_ERR_CAPACITY
+
+// One attention call.  A unit is one row tile of one (sequence, kv head): the
+// query rows of the group's heads, [B][Hkv][G C][hd] row-major as q lies in
+// memory, cut into tiles of `rows`.  A unit's keys are cut into tiles of `tk`:
+// first the cached rows, then (from a tile boundary on) the new ones.
+struct Kv8AttnArgs {
+  const void* q;             // bf16 [B][Hq][C][hd]
+  const uint8_t *K, *V;      // codes [B][Hkv][cap][hd]
+  const uint8_t *Ke, *Ve;    // exponent bytes [B][Hkv][nblk]
+  const int* len;            // [B]
+  const void *kn, *vn;       // bf16 [B][Hkv][C][hd] or null
+  void* o;                   // bf16 [B*C][Hq*hd]
+  float* part;               // fp32 [2 * workers][rows][hd]
+  float* ml;                 // fp32 [2 * workers][rows][2]: maximum (log2 units) and sum
+  int* status;
+  int B, C, Hq, Hkv, hd, cap, nblk;
+  int causal;
+  int rows, tk, units;       // rows per unit, keys per tile, units per sequence (Hkv * row tiles)
+  int workers;               // warps or CTAs that the tiles are dealt to
+};
+
+// All tiles of a call, in the order (sequence, unit, tile), are dealt to the
+// workers in equal contiguous shares, whatever the sequences' lengths: the
+// device computes the division from the lengths, so the host never reads them
+// and a captured graph follows a growing cache.  A unit cut by a share's
+// border is left in parts, merged by the merge kernel: a worker's part that
+// begins inside a unit goes to its slot 0 (there is one at most), the part of
+// a unit that it begins and does not finish to its slot 1.
+struct Kv8Seq {
+  int b, len;                // sequence and its cached rows
+  int nt;                    // tiles of each of its units
+  long long first;           // first tile (in the call's order) of its first unit
+};
+
+DG_DEV int kv8_len(const Kv8AttnArgs& a, int b) {
+  const int n = a.len[b];
+  return min(max(n, 0), a.cap);
+}
+DG_DEV int kv8_tiles(const Kv8AttnArgs& a, int len) {
+  return (len + a.tk - 1) / a.tk + (a.kn ? (a.C + a.tk - 1) / a.tk : 0);
+}
+// Tiles of the whole call (every lane of the calling warp gets the sum).
+DG_DEV long long kv8_total(const Kv8AttnArgs& a) {
+  const int lane = threadIdx.x & 31;
+  long long n = 0;
+  for (int b = lane; b < a.B; b += 32) n += (long long)kv8_tiles(a, kv8_len(a, b)) * a.units;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+DG_DEV long long kv8_share(const Kv8AttnArgs& a, long long total) {
+  const long long s = (total + a.workers - 1) / a.workers;
+  return s > 1 ? s : 1;
+}
+// The sequence that tile w of the call belongs to (w below the total; every
+// lane of the calling warp gets the answer).
+DG_DEV Kv8Seq kv8_locate(const Kv8AttnArgs& a, long long w) {
+  const int lane = threadIdx.x & 31;
+  long long base = 0;
+  Kv8Seq p{0, 0, 1, 0};
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int len = b < a.B ? kv8_len(a, b) : 0;
+    const int nt = b < a.B ? kv8_tiles(a, len) : 0;
+    long long incl = (long long)nt * a.units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, w < base + incl);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      p.b = b0 + src;
+      p.len = __shfl_sync(0xffffffffu, len, src);
+      p.nt = __shfl_sync(0xffffffffu, nt, src);
+      p.first = __shfl_sync(0xffffffffu, base + incl - (long long)nt * a.units, src);
+      return p;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return p;
+}
+
+// Output row of query row r (< G C) of kv head g of sequence b.
+DG_DEV __nv_bfloat16* kv8_out_row(const Kv8AttnArgs& a, int b, int g, int r) {
+  const int h = g * (a.Hq / a.Hkv) + r / a.C, i = r % a.C;
+  return reinterpret_cast<__nv_bfloat16*>(a.o) + (((size_t)b * a.C + i) * a.Hq + h) * a.hd;
+}
+
+// 2^e as a float, e clamped to the normal range.
+DG_DEV float pow2i(int e) { return __uint_as_float((unsigned)(min(max(e, -126), 127) + 127) << 23); }
+DG_DEV float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two E4M3 codes (low byte first) as two f16, exactly.
+DG_DEV uint32_t e4m3x2_f16x2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)codes));
+  return r;
+}
+// Two floats as E4M3 codes (low byte: lo), nearest even, saturating at 448.
+DG_DEV uint32_t pack_e4m3(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Rows per unit of the warp-MMA kernel for R query rows per kv head.
+int kv8_mma_rows(int hd, int64_t R);
+cudaError_t launch_kv8_attention_mma(const Kv8AttnArgs& a, cudaStream_t st);
+cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, cudaStream_t st);
+
+}  // namespace dg

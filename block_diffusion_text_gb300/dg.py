@@ -28,7 +28,8 @@ EXPORTS = ("dg_status_string", "dg_workspace_size", "dg_read_status", "dg_tau", 
            "dg_denoise_step", "dg_denoise_canvas", "dg_commit_block", "dg_debug_gemm",
            "dg_attention_noalloc", "dg_attention_noalloc_status", "dg_debug_wait_timeout",
            "dg_canvas_init_masked", "dg_denoise_step_masked", "dg_denoise_canvas_masked", "dg_prefill",
-           "dg_quantize_rows_e4m3")
+           "dg_quantize_rows_e4m3", "dg_kv8_append", "dg_kv8_read", "dg_kv8_attention_workspace",
+           "dg_kv8_attention")
 
 
 class DgError(RuntimeError):
@@ -66,6 +67,11 @@ class dg_step_debug(ct.Structure):
 class dg_step_out(ct.Structure):
     _fields_ = [(n, ct.c_void_p) for n in ("entropy", "argmax", "accept", "n_acc", "mean_H", "stop")] + [
         ("debug", ct.POINTER(dg_step_debug)), ("events", ct.POINTER(ct.c_void_p))]
+
+
+class dg_kv8_cache(ct.Structure):
+    _fields_ = [(n, ct.c_void_p) for n in ("K", "V", "K_exp", "V_exp", "len", "status")] + [
+        (n, ct.c_int32) for n in ("B", "Hkv", "cap", "hd")]
 
 
 # Kernel slots of one step (dg_step_out.events), in launch order.
@@ -129,6 +135,13 @@ def load():
             L.dg_attention_noalloc.argtypes = [ct.c_void_p, ct.c_void_p, ct.c_void_p, ct.c_int32, ct.c_int32,
                                                ct.c_void_p, ct.c_void_p, ct.c_void_p, ct.c_int32, ct.c_int32,
                                                ct.c_int32, ct.c_int32, ct.c_int32, ct.c_void_p]
+            L.dg_kv8_append.argtypes = [ct.c_void_p, ct.c_void_p, ct.c_void_p, ct.c_int32, ct.c_void_p, ct.c_void_p]
+            L.dg_kv8_read.argtypes = [ct.c_void_p, ct.c_int32, ct.c_int32, ct.c_void_p, ct.c_void_p, ct.c_int32,
+                                      ct.c_void_p]
+            L.dg_kv8_attention_workspace.argtypes = [ct.c_void_p, ct.c_int32, ct.c_int32, ct.POINTER(ct.c_size_t)]
+            L.dg_kv8_attention.argtypes = [ct.c_void_p, ct.c_void_p, ct.c_void_p, ct.c_void_p, ct.c_void_p,
+                                           ct.c_int32, ct.c_int32, ct.c_int32, ct.c_void_p, ct.c_size_t,
+                                           ct.c_void_p]
             _lib = L
     return _lib
 
@@ -451,3 +464,149 @@ def quantize_rows_e4m3(X: torch.Tensor, stream=None):
     _check(load().dg_quantize_rows_e4m3(_ptr(X), R, d, _ptr(Q), _ptr(sc), _stream(stream)),
            "dg_quantize_rows_e4m3")
     return Q, sc
+
+
+KV8_BLOCK = 64  # cached tokens per scale of the 8-bit cache
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+class Kv8Cache:
+    """An 8-bit prefix cache (dg_kv8_cache): E4M3 codes with a power-of-two scale per 64 rows and head.
+
+    K, V: uint8 [B, Hkv, cap, hd] codes; K_exp, V_exp: uint8 [B, Hkv, ceil(cap / 64)] exponent bytes (scale
+    2^(x - 127)); len: int32 [B], the rows each sequence holds; all on one CUDA device, contiguous, and kept by
+    this object.  No call advances len: after the appends of all layers do ``cache.len += n`` on the same stream.
+    status: int32 [1] device word, shared by the caches of a stack when given."""
+
+    def __init__(self, K, V, K_exp, V_exp, len, status=None):
+        _need(K.dim() == 4 and V.shape == K.shape and K.dtype == V.dtype == torch.uint8,
+              "K, V: uint8 codes [B, Hkv, cap, hd]")
+        B, Hkv, cap, hd = K.shape
+        nblk = -(-cap // KV8_BLOCK)
+        _need(K_exp.shape == V_exp.shape == (B, Hkv, nblk) and K_exp.dtype == V_exp.dtype == torch.uint8,
+              f"K_exp, V_exp: uint8 [{B}, {Hkv}, {nblk}]")
+        _need(len.shape == (B,) and len.dtype == torch.int32, f"len: int32 [{B}]")
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=K.device)
+        _need(status.shape == (1,) and status.dtype == torch.int32, "status: int32 [1]")
+        for t in (K, V, K_exp, V_exp, len, status):
+            _need(t.is_cuda and t.device == K.device and t.is_contiguous(),
+                  "the cache's tensors are contiguous and on one CUDA device")
+        self.K, self.V, self.K_exp, self.V_exp, self.len, self.status_word = K, V, K_exp, V_exp, len, status
+        self.B, self.Hkv, self.cap, self.hd = B, Hkv, cap, hd
+        self.device = K.device
+        self.s = dg_kv8_cache(*[t.data_ptr() for t in (K, V, K_exp, V_exp, len, status)], B, Hkv, cap, hd)
+        self._ref = ct.byref(self.s)
+        self._ws_bytes = {}
+
+    @classmethod
+    def empty(cls, B, Hkv, cap, hd, device="cuda"):
+        """A cache of `cap` rows per sequence that holds none yet."""
+        u8 = dict(dtype=torch.uint8, device=device)
+        nblk = -(-cap // KV8_BLOCK)
+        return cls(torch.zeros(B, Hkv, cap, hd, **u8), torch.zeros(B, Hkv, cap, hd, **u8),
+                   torch.zeros(B, Hkv, nblk, **u8), torch.zeros(B, Hkv, nblk, **u8),
+                   torch.zeros(B, dtype=torch.int32, device=device))
+
+    def status(self, stream=None) -> int:
+        """The device status word (synchronises the stream)."""
+        st = ct.c_int32()
+        _check(load().dg_read_status(_ptr(self.status_word), ct.byref(st), _stream(stream)), "dg_read_status")
+        return st.value
+
+    def workspace_bytes(self, C: int, Hq: int) -> int:
+        """Bytes of workspace of kv8_attention with C new tokens and Hq query heads."""
+        n = self._ws_bytes.get((C, Hq))
+        if n is None:
+            z = ct.c_size_t()
+            _check(load().dg_kv8_attention_workspace(self._ref, C, Hq, ct.byref(z)), "dg_kv8_attention_workspace")
+            n = self._ws_bytes[(C, Hq)] = z.value
+        return n
+
+    def _rows(self, t, heads, n, what):
+        if t.dtype != torch.bfloat16 or t.shape != (self.B, heads, n, self.hd) or t.device != self.device \
+                or not t.is_contiguous():
+            raise ValueError(f"{what}: contiguous bf16 [{self.B}, {heads}, {n}, {self.hd}] on {self.device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+    def _launch_stream(self, stream):
+        """The raw stream of a launch: the library launches on the current device, so that must be the cache's."""
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError(f"the cache lies on {self.device}, the current device is another")
+        return torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else stream.cuda_stream
+
+
+def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None,
+               stream=None) -> None:
+    """Quantise rows k, v (bf16 [B, Hkv, n, hd]) into the cache at rows len.. (dg_kv8_append).
+
+    counts: optional int32 [B], rows of each sequence (the rest is padding).  len is not advanced."""
+    n = k.shape[2] if k.dim() == 4 else -1
+    cache._rows(k, cache.Hkv, n, "k")
+    cache._rows(v, cache.Hkv, n, "v")
+    if counts is not None:
+        _need(counts.shape == (cache.B,) and counts.dtype == torch.int32 and counts.device == cache.device
+              and counts.is_contiguous(), f"counts: int32 [{cache.B}] on {cache.device}")
+    if n == 0:
+        return
+    _check(load().dg_kv8_append(cache._ref, k.data_ptr(), v.data_ptr(), n,
+                                None if counts is None else counts.data_ptr(), cache._launch_stream(stream)),
+           "dg_kv8_append")
+
+
+def kv8_read(cache: Kv8Cache, row0: int, n: int, out=None, stream=None):
+    """Rows row0 .. row0 + n of every sequence as bf16 (dg_kv8_read): (K, V), each [B, Hkv, n, hd].
+
+    out: optional (K, V) of at least n rows, e.g. the caches of a Model; rows at or past a sequence's length are
+    left as they are (zeros where this call makes the tensors)."""
+    st = cache._launch_stream(stream)
+    if out is None:
+        with torch.cuda.stream(stream):
+            K = torch.zeros(cache.B, cache.Hkv, n, cache.hd, dtype=torch.bfloat16, device=cache.device)
+            V = torch.zeros_like(K)
+    else:
+        K, V = out
+        pitch = K.shape[2] if K.dim() == 4 else -1
+        cache._rows(K, cache.Hkv, pitch, "out[0]")
+        cache._rows(V, cache.Hkv, pitch, "out[1]")
+    if n == 0:
+        return K, V
+    _check(load().dg_kv8_read(cache._ref, row0, n, K.data_ptr(), V.data_ptr(), K.shape[2], st), "dg_kv8_read")
+    return K, V
+
+
+def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+                  causal: bool = False, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Attention of C new tokens over the cached rows and their own k, v (dg_kv8_attention); o [B*C, Hq*hd].
+
+    q: bf16 [B, Hq, C, hd]; k, v: bf16 [B, Hkv, C, hd], or None for the cached rows alone.  ws: optional uint8
+    workspace of cache.workspace_bytes(C, Hq) bytes, not shared by calls that may overlap; by default one from
+    torch's allocator on the launching stream."""
+    if q.dim() != 4:
+        raise ValueError("q: bf16 [B, Hq, C, hd]")
+    Hq, C = q.shape[1], q.shape[2]
+    cache._rows(q, Hq, C, "q")
+    _need((k is None) == (v is None), "k and v come together")
+    if k is not None:
+        cache._rows(k, cache.Hkv, C, "k")
+        cache._rows(v, cache.Hkv, C, "v")
+    st = cache._launch_stream(stream)
+    nbytes = cache.workspace_bytes(C, Hq)
+    if out is None or ws is None:
+        with torch.cuda.stream(stream):  # memory of the launching stream (a no-op for None)
+            if out is None:
+                out = torch.empty(cache.B * C, Hq * cache.hd, dtype=torch.bfloat16, device=cache.device)
+            if ws is None:
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    _need(out.dtype == torch.bfloat16 and out.shape == (cache.B * C, Hq * cache.hd) and out.is_contiguous()
+          and out.device == cache.device, f"out: contiguous bf16 [{cache.B * C}, {Hq * cache.hd}]")
+    _need(ws.device == cache.device and ws.is_contiguous(), "ws: contiguous, on the cache's device")
+    _check(load().dg_kv8_attention(cache._ref, q.data_ptr(), None if k is None else k.data_ptr(),
+                                   None if v is None else v.data_ptr(), out.data_ptr(), C, Hq, int(causal),
+                                   ws.data_ptr(), ws.numel() * ws.element_size(), st), "dg_kv8_attention")
+    return out

@@ -389,6 +389,77 @@ DG_API dg_status dg_quantize_rows_e4m3(const void* X, int32_t R, int32_t d, void
  * DG_ERR_TIMEOUT if a bounded wait of that call ran out).  Allocates nothing.  */
 DG_API dg_status dg_attention_noalloc_status(int32_t* status, void* stream);
 
+/* 8-bit prefix cache.  Half the bytes of dg_kv_cache, for prefixes whose size or
+ * bandwidth bounds a deployment (the pages quote FP8 throughput, [SURV] §11;
+ * they describe no cache format, this one is the library's own).
+ *   K, V    uint8 [B][Hkv][cap][hd] device: E4M3 codes, 16-byte aligned, keys
+ *           already rotated by RoPE
+ *   K_exp, V_exp  uint8 [B][Hkv][ceil(cap / 64)] device: one exponent byte x per
+ *           block of 64 rows and head; a cached value is code * 2^(x - 127)
+ *   len     int32 [B] device: rows 0..len[b]-1 of sequence b are valid.  The
+ *           sequences' lengths are the device's: the calls below read them when
+ *           they run, so a captured graph follows a growing cache.  No call
+ *           writes them; the caller advances them once all layers are written.
+ *   status  int32 device word, zeroed by the caller before its first use; kernels
+ *           set DG_ERR_CAPACITY (a length outside [0, cap], or an append past
+ *           cap), DG_ERR_ARG (an append count outside [0, n]) or DG_ERR_VALUE (a
+ *           non-finite value appended); read it with dg_read_status
+ *   hd is 32, 64 or 128; B * Hkv <= 65535; B * Hkv * cap < 2^31 - 2^16.  The caches
+ *   of several layers are as many dg_kv8_cache structs sharing len and status.
+ * 2^(x - 127) is a power of two, so code * scale is exact in bf16 and a code is the
+ * value correctly rounded (nearest even) on its block's scale.               */
+typedef struct dg_kv8_cache {
+  void *K, *V;
+  void *K_exp, *V_exp;
+  const int32_t* len;
+  int32_t* status;
+  int32_t B, Hkv, cap, hd;
+} dg_kv8_cache;
+
+/* Quantises rows as they are written: row i < counts[b] of k, v (bf16
+ * [B][Hkv][n][hd], 16-byte aligned) becomes cached row len[b] + i of sequence b.
+ * counts: int32 [B] device, each in [0, n], or NULL for n rows each (rows past a
+ * sequence's count are padding: not read, nothing written for them).
+ * A block's scale is the smallest 2^e, -64 <= e <= 118, with its largest new
+ * magnitude <= 448 * 2^e; where the block holds earlier rows its scale never
+ * shrinks, and where it grows the earlier codes move to the new scale (rounded
+ * to nearest even: exact but for results below 2^-6).  Rows outside
+ * [len, len + count) of other blocks are left as they were, the bytes behind
+ * the last row too.  len is not advanced: appending again at the same len
+ * overwrites the rows.  Infinities are stored as +-448 and NaN as 0 on the scale
+ * of the finite values, with DG_ERR_VALUE in the status word.  A sequence
+ * whose rows do not fit (len + count > cap) is left untouched, with
+ * DG_ERR_CAPACITY there; n > cap is rejected at once.                         */
+DG_API dg_status dg_kv8_append(const dg_kv8_cache* cache, const void* k, const void* v, int32_t n,
+                               const int32_t* counts, void* stream);
+
+/* Reads rows back as bf16 (exact): cached row row0 + i, 0 <= i < n, of every
+ * (sequence, head) to row i of k, v (bf16 [B][Hkv][pitch][hd], pitch >= n, 16-byte
+ * aligned).  Rows at or past len[b] are not written.  With row0 = 0 and
+ * pitch = cap' the outputs are the K, V of a dg_kv_cache of capacity cap'.     */
+DG_API dg_status dg_kv8_read(const dg_kv8_cache* cache, int32_t row0, int32_t n, void* k, void* v, int32_t pitch,
+                             void* stream);
+
+/* Attention of C new tokens per sequence over the cached rows and, in bf16, the
+ * new tokens' own keys and values:
+ *   o = softmax(q [K_0..len-1 ; k]^T / sqrt hd) [V_0..len-1 ; v]
+ *   q bf16 [B][Hq][C][hd] (RoPE applied); k, v bf16 [B][Hkv][C][hd], or both NULL
+ *   (the cached rows alone, e.g. after an append with len advanced); o bf16
+ *   [B*C][Hq*hd] (written); all 16-byte aligned; query head h reads kv head
+ *   h / (Hq / Hkv).
+ * causal = 0: every new token sees every new token (the canvas of a denoising
+ * step); causal = 1: token i sees new tokens 0..i (a prompt piece).  C = 1 is the
+ * single-token form.  Sequences of any lengths share a call (0 included; the
+ * work is divided by keys, not by sequences); a row without any key is zero.
+ * k and v must be finite, the ones a causal mask hides included; what lies
+ * behind len is never used.  Bounds as dg_attention_noalloc: C <= 1024,
+ * B * C <= 2^20, B * Hq <= 65535.  ws: dg_kv8_attention_workspace bytes, 256-byte
+ * aligned, contents of no matter; calls (and graphs) that may overlap on the
+ * GPU need one each.                                                         */
+DG_API dg_status dg_kv8_attention_workspace(const dg_kv8_cache* cache, int32_t C, int32_t Hq, size_t* bytes);
+DG_API dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, const void* k, const void* v, void* o,
+                                  int32_t C, int32_t Hq, int32_t causal, void* ws, size_t ws_bytes, void* stream);
+
 /* Diagnostics of the bounded device waits (not a step of the method): runs
  * one kernel whose mbarrier wait is never satisfied.  The wait gives up after
  * its limit (2 s), records DG_ERR_TIMEOUT in a library status word, and the

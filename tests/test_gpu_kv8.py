@@ -1,0 +1,462 @@
+"""The 8-bit prefix cache through its public entry points: append and read bit for bit, attention within
+tolerances derived in kv8_ref.attention, against its definition in 64 bits."""
+import pytest
+import torch
+
+import kv8_ref
+from block_diffusion_text_gb300 import dg, synth
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(g, *shape, spread=0.5):
+    """bf16 rows of unit size with stronger and weaker channels and tokens."""
+    x = torch.randn(*shape, generator=g)
+    x = x * torch.exp(spread * torch.randn(shape[0], shape[1], 1, shape[3], generator=g))
+    return (x * torch.exp(spread * torch.randn(shape[0], shape[1], shape[2], 1, generator=g))).to(torch.bfloat16)
+
+
+def filled(g, B, H, cap, hd, lens, behind=0x7f):
+    """A cache on the GPU holding `lens` rows of random codes; every byte behind them is `behind` (NaN codes), and
+    the exponents of blocks without rows are 255."""
+    t = []
+    for _ in range(2):
+        c = (torch.randn(B, H, cap, hd, generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        e = (120 + torch.randint(-2, 3, (B, H, -(-cap // 64)), generator=g)).to(torch.uint8)
+        for b, n in enumerate(lens):
+            c[b, :, n:] = behind
+            e[b, :, -(-n // 64):] = 255
+        t += [c, e]
+    ln = torch.tensor(lens, dtype=torch.int32)
+    return dg.Kv8Cache(*[x.cuda() for x in (t[0], t[2], t[1], t[3], ln)])
+
+
+def state(c):
+    return [t.cpu() for t in (c.K, c.V, c.K_exp, c.V_exp, c.len)]
+
+
+def check_append(c, k, v, counts=None, status=0, **kw):
+    K, V, Ke, Ve, ln = state(c)
+    n = [k.shape[2]] * c.B if counts is None else counts
+    wK, wKe = kv8_ref.append(K, Ke, k, ln, n)
+    wV, wVe = kv8_ref.append(V, Ve, v, ln, n)
+    ct = None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda()
+    dg.kv8_append(c, k.cuda(), v.cuda(), counts=ct, **kw)
+    torch.cuda.synchronize()
+    gK, gV, gKe, gVe, gl = state(c)
+    assert torch.equal(gl, ln)
+    assert torch.equal(gKe, wKe) and torch.equal(gVe, wVe)
+    assert torch.equal(gK, wK) and torch.equal(gV, wV)
+    assert c.status() == status
+
+
+# ------------------------------------------------------------------ append ----
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("n,lens,cap", [(1, [0, 1, 63, 64, 65, 127], 200), (64, [0, 64, 1, 63, 100, 5], 190),
+                                        (63, [1, 0, 2, 64, 65, 30], 150), (200, [0, 7, 64, 120, 200, 33], 401),
+                                        (257, [3, 0, 63, 64, 143, 10], 400)])
+def test_append_is_exact(hd, n, lens, cap):
+    g = torch.Generator().manual_seed(n + hd)
+    c = filled(g, len(lens), 2, cap, hd, lens)
+    check_append(c, rows(g, len(lens), 2, n, hd), rows(g, len(lens), 2, n, hd, spread=2.0))
+
+
+@pytest.mark.parametrize("hd", [32, 128])
+def test_append_counts_leave_padding_out(hd):
+    """Counts from 0 to n; the padding rows hold NaN, which must not reach a scale or the status word."""
+    g = torch.Generator().manual_seed(5)
+    counts, lens = [0, 1, 70, 130, 5, 129], [10, 0, 60, 64, 63, 1]
+    c = filled(g, 6, 3, 300, hd, lens)
+    k, v = rows(g, 6, 3, 130, hd), rows(g, 6, 3, 130, hd)
+    for b, m in enumerate(counts):
+        k[b, :, m:] = float("nan")
+        v[b, :, m:] = float("inf")
+    check_append(c, k, v, counts)
+
+
+def test_append_token_by_token_grows_scales():
+    """150 tokens one by one, magnitudes rising and falling over many octaves: scales grow within a block and the
+    earlier codes move with them."""
+    g = torch.Generator().manual_seed(6)
+    c = filled(g, 2, 2, 256, 64, [0, 37])
+    for i in range(150):
+        x = rows(g, 2, 2, 1, 64) * float(torch.exp2(torch.randint(-14, 14, (1,), generator=g).float()))
+        check_append(c, x, x.flip(3))
+        c.len += 1
+
+
+def test_append_extremes():
+    """Zeros of both signs, subnormals, the largest values, ties between codes, and a block of zeros."""
+    g = torch.Generator().manual_seed(7)
+    tiny, big = 2.0 ** -133, 3.3895e38
+    pats = [torch.zeros(64), torch.full((64,), -0.0), torch.full((64,), tiny), torch.full((64,), big),
+            torch.full((64,), -big), torch.cat([torch.full((32,), big), torch.full((32,), 1.0)]),
+            torch.cat([torch.full((1,), 448.0), torch.arange(63) / 16.0]),        # ties at the codes' midpoints
+            torch.cat([torch.full((1,), 450.0), torch.arange(63) / 512.0]),       # one past 448: next scale
+            torch.full((64,), 2.0 ** -74), torch.full((64,), 448 * 2.0 ** -64), torch.full((64,), 449 * 2.0 ** -64)]
+    for start in (0, 13):
+        for x in pats:
+            c = filled(g, 1, 1, 128, 64, [start])
+            x = x.to(torch.bfloat16).reshape(1, 1, 1, 64)
+            check_append(c, x, -x)
+
+
+def test_append_non_finite_values():
+    """NaN is stored as 0, infinities saturate on the scale of the finite values, the status word says so."""
+    g = torch.Generator().manual_seed(8)
+    for start in (0, 20):
+        c = filled(g, 2, 2, 256, 128, [start, start])
+        k, v = rows(g, 2, 2, 100, 128), rows(g, 2, 2, 100, 128)
+        k[0, 1, 3, 7] = float("nan")
+        k[1, 0, 99, 127] = float("-inf")
+        v[1, 1, 50] = float("inf")
+        v[0, 0, 64:] = float("nan")
+        check_append(c, k, v, status=dg.DG_ERR_VALUE)
+
+
+def test_append_past_the_capacity_leaves_the_sequence():
+    g = torch.Generator().manual_seed(9)
+    c = filled(g, 3, 2, 100, 64, [90, 91, 0])
+    check_append(c, rows(g, 3, 2, 10, 64), rows(g, 3, 2, 10, 64), status=dg.DG_ERR_CAPACITY)
+    c = filled(g, 3, 2, 100, 64, [0, 0, 0])
+    c.len[1] = -5
+    check_append(c, rows(g, 3, 2, 10, 64), rows(g, 3, 2, 10, 64), status=dg.DG_ERR_CAPACITY)
+    c = filled(g, 2, 2, 100, 64, [0, 0])
+    K, V, Ke, Ve, ln = state(c)
+    k = rows(g, 2, 2, 10, 64).cuda()
+    dg.kv8_append(c, k, k, counts=torch.tensor([11, -1], dtype=torch.int32).cuda())
+    assert c.status() == dg.DG_ERR_ARG and torch.equal(c.K.cpu(), K) and torch.equal(c.V_exp.cpu(), Ve)
+    with pytest.raises(dg.DgError):
+        k = rows(g, 2, 2, 101, 64).cuda()
+        dg.kv8_append(c, k, k)
+
+
+# -------------------------------------------------------------------- read ----
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("row0,n,pitch", [(0, 1, 1), (0, 200, 200), (37, 100, 130), (64, 64, 64), (199, 30, 31),
+                                          (250, 5, 5)])
+def test_read_is_exact_and_keeps_other_rows(hd, row0, n, pitch):
+    g = torch.Generator().manual_seed(row0 + n)
+    lens = [200, 0, 1, 64, 137]
+    c = filled(g, 5, 2, 200, hd, lens)
+    K, V, Ke, Ve, _ = state(c)
+    out = [torch.full((5, 2, pitch, hd), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    got = dg.kv8_read(c, row0, n, out=out)
+    for o, t, codes, exps in zip(got, out, (K, V), (Ke, Ve)):
+        assert o is t
+        want = torch.full((5, 2, pitch, hd), 7.0, dtype=torch.float64)
+        val = kv8_ref.values(codes, exps)
+        for b, m in enumerate(lens):
+            last = min(m, row0 + n)
+            if last > row0:
+                want[b, :, :last - row0] = val[b, :, row0:last]
+        assert torch.equal(o.cpu().double(), want)
+    assert c.status() == 0
+
+
+def test_read_covers_every_code_and_extreme_scales():
+    for e in (63, 64, 120, 127, 200, 245):
+        codes = torch.arange(256, dtype=torch.uint8).reshape(1, 1, 4, 64)
+        codes[(codes & 0x7f) == 0x7f] = 0
+        c = dg.Kv8Cache(codes.cuda(), codes.flip(2).contiguous().cuda(),
+                        *[torch.full((1, 1, 1), e, dtype=torch.uint8).cuda() for _ in range(2)],
+                        torch.tensor([4], dtype=torch.int32).cuda())
+        K, V = dg.kv8_read(c, 0, 4)
+        assert torch.equal(K.cpu().double(), kv8_ref.values(codes, torch.full((1, 1, 1), e)))
+        assert torch.equal(V.cpu().double(), kv8_ref.values(codes.flip(2), torch.full((1, 1, 1), e)))
+
+
+def test_append_then_read_is_within_half_a_step():
+    """E4M3 keeps 2^-4 of a value in its normal range, and 2^-10 of the block's scale below it."""
+    g = torch.Generator().manual_seed(11)
+    c = dg.Kv8Cache.empty(2, 2, 300, 128)
+    k, v = rows(g, 2, 2, 300, 128), rows(g, 2, 2, 300, 128)
+    dg.kv8_append(c, k.cuda(), v.cuda())
+    c.len += 300
+    for got, x, e in zip(dg.kv8_read(c, 0, 300), (k, v), (c.K_exp, c.V_exp)):
+        scale = torch.exp2(e.cpu().double() - 127).repeat_interleave(64, -1)[..., :300, None]
+        bound = torch.maximum(2.0 ** -4 * x.double().abs(), 2.0 ** -10 * scale)
+        assert ((got.cpu().double() - x.double()).abs() <= bound).all()
+
+
+# --------------------------------------------------------------- attention ----
+def check_attention(c, q, k, v, causal, **kw):
+    K, V, Ke, Ve, ln = state(c)
+    want, tol = kv8_ref.attention(K, V, Ke, Ve, ln, q, k, v, causal)
+    dev = [None if t is None else t.cuda() for t in (q, k, v)]
+    got = dg.kv8_attention(c, *dev, causal=causal, **kw)
+    torch.cuda.synchronize()
+    off = (got.cpu().double() - want).abs()
+    assert torch.isfinite(got).all()
+    assert (off <= tol).all(), f"largest error over tolerance {float((off / tol).max()):.3f}"
+    assert c.status() == 0
+    return got
+
+
+CASES = [
+    # B, C, Hq, Hkv, hd, lens, causal, new tokens
+    (1, 1, 1, 1, 128, [1], False, False),
+    (1, 1, 1, 1, 32, [0], False, True),
+    (3, 1, 4, 2, 128, [0, 1, 63], False, False),
+    (6, 1, 8, 2, 128, [0, 64, 65, 127, 128, 2000], False, True),
+    (2, 1, 16, 1, 128, [700, 31], True, True),
+    (2, 1, 32, 1, 64, [129, 640], False, True),
+    (4, 1, 8, 8, 64, [5, 64, 0, 333], False, False),
+    (2, 1, 6, 2, 32, [1000, 33], False, True),
+    (2, 3, 8, 4, 128, [100, 4097], True, True),
+    (2, 5, 8, 2, 64, [50, 0], True, True),
+    (2, 17, 2, 1, 32, [32, 95], False, True),
+    (1, 16, 2, 1, 32, [32], False, True),
+    (3, 40, 4, 2, 64, [0, 63, 300], True, True),
+    (3, 33, 4, 2, 128, [0, 63, 300], False, True),
+    (2, 64, 8, 2, 128, [1, 1025], True, True),
+    (2, 100, 4, 4, 128, [128, 200], False, True),
+    (1, 128, 2, 1, 128, [0], True, True),
+    (2, 129, 2, 2, 128, [500, 0], True, True),
+    (2, 250, 8, 2, 128, [385, 77], True, True),
+    (1, 256, 16, 8, 128, [1024], False, True),
+    (2, 256, 2, 2, 128, [640, 1], False, False),
+    (1, 1000, 2, 2, 128, [130], True, True),
+    (1, 200, 3, 1, 64, [777], True, True),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=[f"b{c[0]}c{c[1]}q{c[2]}k{c[3]}h{c[4]}l{max(c[5])}{'c' * c[6]}{'n' * c[7]}"
+                                             for c in CASES])
+def test_attention(case):
+    B, C, Hq, Hkv, hd, lens, causal, new = case
+    g = torch.Generator().manual_seed(sum(lens) + C)
+    c = filled(g, B, Hkv, max(lens) + 3, hd, lens)
+    q = rows(g, B, Hq, C, hd)
+    k, v = (rows(g, B, Hkv, C, hd), rows(g, B, Hkv, C, hd)) if new else (None, None)
+    check_attention(c, q, k, v, causal)
+
+
+@pytest.mark.parametrize("C,hd", [(1, 128), (8, 64), (256, 128)])
+def test_attention_follows_scales_of_many_octaves(C, hd):
+    """Key and value scales that differ by many octaves from block to block, with small queries: the value scale is
+    part of the running maximum, the key scale of each block's softmax factor."""
+    g = torch.Generator().manual_seed(21)
+    lens = [640, 333]
+    c = filled(g, 2, 2, 640, hd, lens)
+    c.V_exp[:] = torch.randint(100, 150, tuple(c.V_exp.shape), generator=g).to(torch.uint8).cuda()
+    c.K_exp[:] = torch.randint(105, 121, tuple(c.K_exp.shape), generator=g).to(torch.uint8).cuda()
+    q = rows(g, 2, 4, C, hd)
+    check_attention(c, q, rows(g, 2, 2, C, hd) , rows(g, 2, 2, C, hd), False)
+
+
+@pytest.mark.parametrize("C,hd", [(1, 128), (1, 32), (256, 128)])
+def test_attention_of_peaked_rows(C, hd):
+    """Scores of some hundreds: almost all weight on one key, first in one row and last in another."""
+    g = torch.Generator().manual_seed(22)
+    c = filled(g, 1, 1, 500, hd, [451])
+    q = rows(g, 1, 2, C, hd) * 20
+    check_attention(c, q.to(torch.bfloat16), rows(g, 1, 1, C, hd), rows(g, 1, 1, C, hd), False)
+
+
+@pytest.mark.parametrize("C,hd", [(2, 128), (2, 64), (200, 128)])
+def test_attention_scales_queries_exactly(C, hd):
+    """Queries of 2^-40 and 2^30, zero rows among them, and one element 2^12 times the others: the power-of-two
+    scaling of a row keeps what its scores need."""
+    g = torch.Generator().manual_seed(23)
+    c = filled(g, 1, 2, 200, hd, [190])
+    for f in (2.0 ** -40, 1.0):
+        q = rows(g, 1, 4, C, hd) * f
+        q[0, 1, 0] = 0
+        q[0, 2, 1, 3] *= 2.0 ** 6
+        check_attention(c, q, rows(g, 1, 2, C, hd), rows(g, 1, 2, C, hd), False)
+    c.K_exp -= 30
+    q = rows(g, 1, 4, C, hd) * 2.0 ** 30
+    check_attention(c, q, None, None, False)
+
+
+def test_attention_without_any_key_is_zero():
+    g = torch.Generator().manual_seed(24)
+    for C, hd in ((1, 128), (5, 32), (200, 128)):
+        c = filled(g, 2, 1, 64, hd, [0, 0])
+        out = torch.full((2 * C, 2 * hd), 9.0, dtype=torch.bfloat16, device="cuda")
+        dg.kv8_attention(c, rows(g, 2, 2, C, hd).cuda(), out=out)
+        assert torch.count_nonzero(out).item() == 0
+
+
+def test_attention_writes_its_output_alone():
+    """Bytes around the output and behind the workspace keep their values; the cache is read only."""
+    g = torch.Generator().manual_seed(25)
+    for C in (1, 70):
+        c = filled(g, 2, 2, 400, 128, [399, 17])
+        before = state(c)
+        q, k, v = rows(g, 2, 4, C, 128).cuda(), rows(g, 2, 2, C, 128).cuda(), rows(g, 2, 2, C, 128).cuda()
+        need = c.workspace_bytes(C, 4)
+        ws = torch.full((need + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+        big = torch.full((2 * C + 2, 4 * 128), 3.0, dtype=torch.bfloat16, device="cuda")
+        dg.kv8_attention(c, q, k, v, out=big[1:-1], ws=ws[:need])
+        torch.cuda.synchronize()
+        assert (big[0] == 3).all() and (big[-1] == 3).all() and (ws[need:] == 0x5a).all()
+        assert all(torch.equal(x, y) for x, y in zip(before, state(c)))
+        assert torch.equal(big[1:-1], dg.kv8_attention(c, q, k, v))
+
+
+def test_results_repeat_bit_for_bit():
+    g = torch.Generator().manual_seed(26)
+    for C in (1, 256):
+        c = filled(g, 5, 2, 3000, 128, [3000, 1, 0, 1555, 64])
+        q, k, v = rows(g, 5, 8, C, 128).cuda(), rows(g, 5, 2, C, 128).cuda(), rows(g, 5, 2, C, 128).cuda()
+        first = dg.kv8_attention(c, q, k, v)
+        for _ in range(5):
+            assert torch.equal(first, dg.kv8_attention(c, q, k, v))
+
+
+def test_lengths_outside_the_cache_are_reported():
+    g = torch.Generator().manual_seed(27)
+    c = filled(g, 2, 1, 100, 64, [100, 100])
+    c.len[1] = 101
+    dg.kv8_attention(c, rows(g, 2, 1, 1, 64).cuda())
+    assert c.status() == dg.DG_ERR_CAPACITY
+    c.status_word.zero_()
+    dg.kv8_read(c, 0, 100)
+    assert c.status() == dg.DG_ERR_CAPACITY
+
+
+def test_offsets_past_32_bits():
+    """A cache of 4.7 GB of codes each for K and V, its last head past 2^32 bytes."""
+    g = torch.Generator().manual_seed(28)
+    B, H, hd, cap = 3, 8, 128, 1_530_000
+    assert (B * H - 1) * cap * hd > 2 ** 32
+    c = dg.Kv8Cache.empty(B, H, cap, hd)
+    k, v = rows(g, B, H, 200, hd), rows(g, B, H, 200, hd)
+    dg.kv8_append(c, k.cuda(), v.cuda())
+    c.len += 200
+    small = dg.Kv8Cache.empty(B, H, 200, hd)
+    dg.kv8_append(small, k.cuda(), v.cuda())
+    small.len += 200
+    assert torch.equal(c.K[:, :, :200], small.K) and torch.equal(c.V[:, :, :200], small.V)
+    for x, y in zip(dg.kv8_read(c, 0, 200), dg.kv8_read(small, 0, 200)):
+        assert torch.equal(x, y)
+    for C in (1, 64):
+        q = rows(g, B, 2 * H, C, hd).cuda()
+        assert torch.equal(dg.kv8_attention(c, q), dg.kv8_attention(small, q))
+
+
+# ----------------------------------------------------- streams and graphs ----
+def test_on_another_stream():
+    g = torch.Generator().manual_seed(31)
+    c = filled(g, 2, 2, 300, 128, [200, 77])
+    q, k, v = rows(g, 2, 4, 9, 128).cuda(), rows(g, 2, 2, 9, 128).cuda(), rows(g, 2, 2, 9, 128).cuda()
+    want = dg.kv8_attention(c, q, k, v)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = dg.kv8_attention(c, q, k, v, stream=st)
+    dg.kv8_append(c, k, v, stream=st)
+    K, V = dg.kv8_read(c, 0, 300, stream=st)
+    st.synchronize()
+    assert torch.equal(got, want)
+    K2, V2 = dg.kv8_read(c, 0, 300)
+    assert torch.equal(K, K2) and torch.equal(V, V2)
+
+
+def test_captured_decoding_follows_the_growing_cache():
+    """One token of two layers captured once and replayed 80 times: append and attention read the lengths on the
+    device, so the replays cross block borders and grow scales as eager calls do."""
+    g = torch.Generator().manual_seed(32)
+    B, Hq, Hkv, hd, steps, cap = 3, 4, 2, 128, 80, 200
+    start = [0, 60, 101]
+    eager = [filled(g, B, Hkv, cap, hd, start) for _ in range(2)]
+    ln = eager[0].len
+    eager = [dg.Kv8Cache(c.K, c.V, c.K_exp, c.V_exp, ln) for c in eager]
+    ln2 = ln.clone()
+    graph_c = [dg.Kv8Cache(c.K.clone(), c.V.clone(), c.K_exp.clone(), c.V_exp.clone(), ln2) for c in eager]
+    data = [[rows(g, B, h, steps, hd).cuda() for h in (Hq, Hkv, Hkv)] for _ in range(2)]
+
+    def token(caches, x):
+        out = []
+        for c, (q, k, v) in zip(caches, x):
+            out.append(dg.kv8_attention(c, q, k, v))
+            dg.kv8_append(c, k, v)
+        caches[0].len.add_(1)
+        return out
+
+    def at(i):
+        return [[t[:, :, i:i + 1].contiguous() for t in layer] for layer in data]
+
+    static = at(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    keep = [[t.clone() for t in (c.K, c.V, c.K_exp, c.V_exp)] for c in graph_c]
+    with torch.cuda.stream(side):
+        token(graph_c, static)
+    torch.cuda.current_stream().wait_stream(side)
+    ln2.copy_(ln)
+    for c, saved in zip(graph_c, keep):
+        for t, s in zip((c.K, c.V, c.K_exp, c.V_exp), saved):
+            t.copy_(s)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        outs = token(graph_c, static)
+    for i in range(steps):
+        x = at(i)
+        want = token(eager, x)
+        for s, t in zip(static, x):
+            for a, b in zip(s, t):
+                a.copy_(b)
+        gr.replay()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b), i
+    for a, b in zip(graph_c, eager):
+        assert all(torch.equal(x, y) for x, y in zip(state(a), state(b)))
+        assert a.status() == b.status() == 0
+
+
+def test_two_graphs_in_a_row_share_a_workspace():
+    g = torch.Generator().manual_seed(33)
+    c1, c2 = filled(g, 2, 2, 900, 128, [900, 3]), filled(g, 2, 2, 500, 128, [0, 499])
+    q = [rows(g, 2, 8, C, 128).cuda() for C in (1, 64)]
+    ws = torch.empty(max(c1.workspace_bytes(1, 8), c2.workspace_bytes(64, 8)), dtype=torch.uint8, device="cuda")
+    want = [dg.kv8_attention(c1, q[0]), dg.kv8_attention(c2, q[1])]
+    graphs, outs = [], []
+    for c, x in ((c1, q[0]), (c2, q[1])):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(dg.kv8_attention(c, x, ws=ws))
+        graphs.append(gr)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for gr in graphs:
+            gr.replay()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+# ---------------------------------------------------------------- together ----
+def test_prompt_blocks_and_tokens_together():
+    """A prompt in causal pieces, a canvas over it, its commit, then single tokens, ragged throughout: each call's
+    output is the attention over the rows read back so far and the new tokens' own keys and values."""
+    g = torch.Generator().manual_seed(41)
+    B, Hq, Hkv, hd = 3, 8, 2, 128
+    c = dg.Kv8Cache.empty(B, Hkv, 700, hd)
+    for C, causal, counts in ((130, True, [130, 7, 64]), (64, False, None), (130, True, [1, 130, 0]), (1, True, None),
+                              (1, True, None), (16, False, [16, 0, 3])):
+        q, k, v = rows(g, B, Hq, C, hd), rows(g, B, Hkv, C, hd), rows(g, B, Hkv, C, hd)
+        check_attention(c, q, k, v, causal)
+        check_append(c, k, v, counts)
+        c.len += C if counts is None else torch.tensor(counts, dtype=torch.int32).cuda()
+    assert c.len.tolist() == [130 + 64 + 1 + 2 + 16, 7 + 64 + 130 + 2, 64 + 64 + 2 + 3]
+
+
+def test_step_queries_over_the_model_cache_in_8_bits():
+    """The denoising step's own q, k, v over its prefix cache quantised: equal to the step's attention
+    (attention_noalloc) over the values read back into the model's bf16 cache."""
+    dims, seed = synth.workload("step_v32k_c256_p2k")
+    w = synth.make_weights(dims, seed, device="cuda")
+    model = dg.Model(dims, w)
+    canvas = dg.Canvas(*synth.make_canvas(dims, seed, device="cuda"))
+    d = dg.denoise_step(model, canvas, tau=0.8, b=0.1, seed=seed, step=0, debug=True)["debug"]
+    c = dg.Kv8Cache.empty(dims.B, dims.Hkv, model.cap, dims.hd)
+    dg.kv8_append(c, model.K, model.V)
+    c.len += dims.P
+    dg.kv8_read(c, 0, dims.P, out=(model.K, model.V))
+    want = dg.attention_noalloc(d["q"], model.K, model.V, dims.P, d["k"], d["v"])
+    check_attention(c, d["q"].cpu(), d["k"].cpu(), d["v"].cpu(), False)
+    got = dg.kv8_attention(c, d["q"], d["k"], d["v"])
+    # both are within 2^-8 of the output (bf16) and 2^-11 of sum p |v| of the same real values
+    A = (want.float().abs() * 2.0 ** -7 + 2.0 ** -10 * 4.0).double()
+    assert ((got.double() - want.double()).abs() <= A).all()
