@@ -223,21 +223,39 @@ dg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DG_OK : DG_ERR_CU
 int kv8_blocks(int cap) { return cdiv(cap, kKv8Block); }
 
 struct Kv8Ws {
-  size_t part, ml, total;
-  int rows, tk, units, workers;
+  size_t part, ml, qterms, qexp, kterms, vf16, kexp, vexp, total;
+  int rows, tk, units, workers, Cp;
+  bool tc;
 };
 
-// Rows per unit and the workspace of an attention call.
+// The kernel, its rows per unit, and the workspace of an attention call.
 Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   Kv8Ws w{};
   const int64_t R = (int64_t)(Hq / c->Hkv) * C;
-  w.rows = kv8_mma_rows(c->hd, R);
-  w.tk = kKv8Block;
-  w.workers = kKv8Ctas * kKv8Warps;
+  w.tc = c->hd == 128 && R > 16;
+  w.rows = w.tc ? 256 : kv8_mma_rows(c->hd, R);
+  w.tk = w.tc ? 128 : kKv8Block;
+  w.workers = w.tc ? kKv8Ctas : kKv8Ctas * kKv8Warps;
   w.units = (int)(c->Hkv * ((R + w.rows - 1) / w.rows));
-  w.part = 0;
-  w.ml = align_up((size_t)2 * w.workers * w.rows * c->hd * 4, 256);
-  w.total = w.ml + align_up((size_t)2 * w.workers * w.rows * 8, 256);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  w.part = take((size_t)2 * w.workers * w.rows * c->hd * 4);
+  w.ml = take((size_t)2 * w.workers * w.rows * 8);
+  if (w.tc) {
+    w.Cp = cdiv(C, 128) * 128;
+    const size_t qrows = (size_t)c->B * Hq * C, krows = (size_t)c->B * c->Hkv * w.Cp;
+    w.qterms = take(2 * qrows * 128);
+    w.qexp = take(4 * qrows);
+    w.kterms = take(2 * krows * 128);
+    w.vf16 = take(2 * krows * 128);
+    w.kexp = take(krows / kKv8Block);
+    w.vexp = take(krows / kKv8Block);
+  }
+  w.total = off;
   return w;
 }
 
@@ -338,7 +356,14 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   a.units = w.units;
   a.workers = w.workers;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_kv8_attention_mma(a, st);
+  cudaError_t e;
+  if (w.tc) {
+    Kv8Prep pp{base + w.qterms, reinterpret_cast<int*>(base + w.qexp), base + w.kterms, base + w.vf16, base + w.kexp,
+               base + w.vexp, cache->B * Hq * C, cache->B * cache->Hkv * w.Cp, w.Cp};
+    e = launch_kv8_attention_tc(a, pp, st);
+  } else {
+    e = launch_kv8_attention_mma(a, st);
+  }
   if (e == cudaSuccess) e = launch_kv8_merge(a, st);
   return from_cuda(e);
 }

@@ -123,9 +123,21 @@ DG_DEV uint32_t pack_e4m3(float lo, float hi) {
   return r;
 }
 
+// The forms of queries and new tokens that the tensor-core kernel reads, made
+// by its first launch in the call's workspace.
+struct Kv8Prep {
+  uint8_t* qterms;           // E4M3 [2 terms][qrows][128]
+  int* qexp;                 // [qrows] exponent of a row's scale
+  uint8_t* kterms;           // E4M3 [2 terms][krows][128], krows = B Hkv Cp
+  uint8_t* vf16;             // f16 [krows][128]
+  uint8_t *kexp, *vexp;      // exponent bytes [B][Hkv][Cp / 64]
+  int qrows, krows, Cp;      // Cp: new tokens padded to whole tiles
+};
+
 // Rows per unit of the warp-MMA kernel for R query rows per kv head.
 int kv8_mma_rows(int hd, int64_t R);
 cudaError_t launch_kv8_attention_mma(const Kv8AttnArgs& a, cudaStream_t st);
+cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cudaStream_t st);
 cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, cudaStream_t st);
 
 }  // namespace dg

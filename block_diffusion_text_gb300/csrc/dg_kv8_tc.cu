@@ -1,0 +1,621 @@
+// Tensor-core (tcgen05 + TMA) attention over the 8-bit prefix cache for many
+// query rows per kv head (canvases and prompt pieces), head dim 128.
+//
+// A CTA owns 256 query rows (two tiles of 128) of one (sequence, kv head) and a
+// run of 128-key tiles; the tiles of a call are dealt to the CTAs in equal
+// shares (dg_kv8.cuh), parts are merged by kv8_merge_kernel.  What the 8-bit
+// cache changes against the bf16 kernel (dg_attn_tc.cu):
+//  - S = Q K^T runs on kind::f8f6f4, so the key codes go from TMA into the MMA
+//    as they lie in memory.  A query row is split into two E4M3 terms, q 2^-x =
+//    hi + lo: a bf16 has 8 significant bits and each term holds 4, so the split
+//    is exact for elements down to 2^-10 of the row's largest and off by
+//    2^-10 / 224 of the largest below (its own bf16 rounding is 2^-9 of each).
+//    Two products at twice the 16-bit rate cost what one 16-bit product costs.
+//  - P V runs in f16: p' is rounded to f16 (2^-12), once, where bf16 would need
+//    two terms; the value codes become f16 (exact) in shared memory, by four
+//    warps that do nothing else.
+//  - Block scales never touch the codes: 2^ke joins the softmax factor of its 64
+//    columns and 2^ve the exponent of the probability (the running maximum is
+//    that of s + ve), whose share of the row sum is taken back.
+// The new tokens' bf16 keys and values are brought into the same forms by
+// kv8_prep_kernel: keys as two E4M3 terms on a scale per 64 tokens (four
+// products), values as f16 on such a scale (exact to 2^-22 of the block's
+// largest).
+//
+// Warp roles (16 warps, one CTA per SM; registers moved to the softmax warps):
+//   warp 0       TMA: Q terms per piece, K tiles into a ring of 16 KB slots (a
+//                new tile takes two), V codes into their own ring (new tiles:
+//                f16, straight to the MMA's buffer)
+//   warp 1       MMA: S_0 S_1 | PV_0 S_0' PV_1 S_1' | ..., so that one row tile's
+//                softmax runs under the other's products
+//   warps 4-7    V codes to f16
+//   warps 8-15   softmax, one thread per row; P over S in TMEM
+#include <cfloat>
+
+#include "dg_kv8.cuh"
+
+namespace dg {
+namespace {
+
+constexpr int kHD = 128;
+constexpr int kTK = 128;                   // keys per tile
+constexpr int kThreads = 512;
+constexpr int kNK = 4, kNV = 2;            // ring depths: K slots, V code and f16 slots
+constexpr float kHeadroom = 8.0f;          // p' of a row's maximum is 2^8 ..
+constexpr float kLazy = 6.0f;              // .. to 2^14: O is rescaled when the maximum grew by more than 2^6
+
+struct Smem {
+  static constexpr int kQ = 128 * kHD;               // one term of one row tile
+  static constexpr int kK = kTK * kHD;               // one tile of codes
+  static constexpr int kBox = kTK * 128;             // 64 f16 columns of a tile
+  static constexpr int kF16 = 2 * kBox;
+  static constexpr int oK = 4 * kQ;
+  static constexpr int oVc = oK + kNK * kK;
+  static constexpr int oVf = oVc + kNV * kK;
+  static constexpr int oBar = oVf + kNV * kF16;
+  static constexpr int kTotal = oBar + 512;
+};
+static_assert(Smem::kTotal <= 232448, "shared memory of one CTA");
+
+// TMEM: S_t at 128 t (P_t over its first 64 columns), O_t at 256 + 128 t.
+constexpr int kColO = 256;
+
+DG_DEV void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum)
+      : "memory");
+}
+template <int N>
+DG_DEV void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+DG_DEV void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+DG_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One piece of a CTA's share: tiles t0..t1-1 of one unit.
+struct Piece {
+  int b, hk, row0, len, t0, t1, nt, ntc;
+  DG_DEV int tiles() const { return t1 - t0; }
+  DG_DEV bool fresh(int j) const { return t0 + j >= ntc; }  // tile j of the piece holds new tokens
+};
+DG_DEV Piece piece_at(const Kv8AttnArgs& a, long long w, long long w1) {
+  const Kv8Seq sq = kv8_locate(a, w);
+  const int per = a.units / a.Hkv;
+  const int unit = (int)((w - sq.first) / sq.nt);
+  Piece p;
+  p.b = sq.b;
+  p.hk = unit / per;
+  p.row0 = unit % per * 256;
+  p.len = sq.len;
+  p.t0 = (int)((w - sq.first) % sq.nt);
+  p.t1 = (int)min((long long)sq.nt, p.t0 + (w1 - w));
+  p.nt = sq.nt;
+  p.ntc = (sq.len + kTK - 1) / kTK;
+  return p;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                       const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mKn,
+                       const __grid_constant__ CUtensorMap mVn, Kv8AttnArgs a, Kv8Prep pp, float scale_log2) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0) {  // uniform over the CTA: return before any barrier
+    if (threadIdx.x == 0) atomicExch(a.status, kStatusTimeout);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::oBar);
+  uint64_t* qfull = bars;
+  uint64_t* qempty = qfull + 1;
+  uint64_t* kfull = qempty + 1;      // [kNK]
+  uint64_t* kempty = kfull + kNK;    // [kNK]
+  uint64_t* cfull = kempty + kNK;    // [kNV] V codes (or new f16 values) have landed
+  uint64_t* cempty = cfull + kNV;    // [kNV] V codes have been read
+  uint64_t* vfull = cempty + kNV;    // [kNV] f16 values ready for the MMA
+  uint64_t* vempty = vfull + kNV;    // [kNV]
+  uint64_t* sfull = vempty + kNV;    // [2]
+  uint64_t* pready = sfull + 2;      // [2 tiles][2 halves]
+  uint64_t* pvdone = pready + 4;     // [2]
+  uint64_t* ofree = pvdone + 2;      // [2] the piece's output has been read from TMEM
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ofree + 2);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* status = a.status;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    for (int s = 0; s < kNK; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+    }
+    for (int s = 0; s < kNV; ++s) {
+      mbar_init(&cfull[s], 1);
+      mbar_init(&cempty[s], 128);
+      mbar_init(&vfull[s], 128);
+      mbar_init(&vempty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sfull[t], 1);
+      mbar_init(&pready[2 * t], 128);
+      mbar_init(&pready[2 * t + 1], 128);
+      mbar_init(&pvdone[t], 1);
+      mbar_init(&ofree[t], 128);
+    }
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  const long long total = kv8_total(a), share = kv8_share(a, total);
+  const long long w0 = blockIdx.x * share, w1 = min(total, w0 + share);
+  const int grp_rows = a.Hq / a.Hkv * a.C;
+
+  if (warp < 4) {
+    reg_dec<96>();
+    if (warp == 0) {
+      if (blockIdx.x == 0)
+        for (int b = lane; b < a.B; b += 32)
+          if (a.len[b] < 0 || a.len[b] > a.cap) atomicExch(status, kStatusCapacity);
+      if (lane == 0) {
+        tma_prefetch(&mQ);
+        tma_prefetch(&mK);
+        tma_prefetch(&mV);
+      }
+      bool ok = true;
+      int kslot = 0, kpar = 1, J = 0, np = 0;  // slot counters run on through the pieces
+      for (long long w = w0; w < w1 && ok; ++np) {
+        const Piece p = piece_at(a, w, w1);
+        if (lane == 0) {
+          const int bh = p.b * a.Hkv + p.hk;
+          ok = mbar_wait(qempty, (np & 1) ^ 1, status, abort);
+          if (ok) {
+            const int qrow = bh * grp_rows + p.row0;
+            mbar_arrive_expect_tx(qfull, 4 * Smem::kQ);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int term = 0; term < 2; ++term)
+                tma_load_2d(smem + (2 * t + term) * Smem::kQ, &mQ, qfull, 0, term * pp.qrows + qrow + 128 * t);
+          }
+          for (int j = 0; j < p.tiles() && ok; ++j, ++J) {
+            const bool fresh = p.fresh(j);
+            const int key = (p.t0 + j - (fresh ? p.ntc : 0)) * kTK;
+            for (int term = 0; term < (fresh ? 2 : 1) && ok; ++term) {
+              if (!(ok = mbar_wait(&kempty[kslot], kpar, status, abort))) break;
+              mbar_arrive_expect_tx(&kfull[kslot], Smem::kK);
+              tma_load_2d(smem + Smem::oK + kslot * Smem::kK, fresh ? &mKn : &mK, &kfull[kslot], 0,
+                          fresh ? term * pp.krows + bh * pp.Cp + key : bh * a.cap + key);
+              if (++kslot == kNK) {
+                kslot = 0;
+                kpar ^= 1;
+              }
+            }
+            if (!ok) break;
+            const int s = J % kNV, par = ((J / kNV) & 1) ^ 1;
+            if (!(ok = mbar_wait(&cempty[s], par, status, abort))) break;
+            if (fresh) {
+              if (!(ok = mbar_wait(&vempty[s], par, status, abort))) break;
+              uint8_t* dst = smem + Smem::oVf + s * Smem::kF16;
+              mbar_arrive_expect_tx(&cfull[s], Smem::kF16);
+              tma_load_2d(dst, &mVn, &cfull[s], 0, bh * pp.Cp + key);
+              tma_load_2d(dst + Smem::kBox, &mVn, &cfull[s], 64, bh * pp.Cp + key);
+            } else {
+              mbar_arrive_expect_tx(&cfull[s], Smem::kK);
+              tma_load_2d(smem + Smem::oVc + s * Smem::kK, &mV, &cfull[s], 0, bh * a.cap + key);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        w += p.tiles();
+      }
+    } else if (warp == 1) {
+      constexpr uint32_t idS = idesc_e4m3(128, kTK);
+      constexpr uint32_t idPV = idesc_f16(128, kHD, true);
+      bool ok = true;
+      int kslot = 0, kpar = 0, J = 0, np = 0;
+      for (long long w = w0; w < w1 && ok; ++np) {
+        const Piece p = piece_at(a, w, w1);
+        if (lane == 0) {
+          const int n = p.tiles();
+          int slots[2] = {0, 0};  // K slots of the tile whose S is being issued
+          auto wait_k = [&](int j) -> bool {
+            for (int term = 0; term < (p.fresh(j) ? 2 : 1); ++term) {
+              if (!mbar_wait(&kfull[kslot], kpar, status, abort)) return false;
+              slots[term] = kslot;
+              if (++kslot == kNK) {
+                kslot = 0;
+                kpar ^= 1;
+              }
+            }
+            tc_fence_after();
+            return true;
+          };
+          auto issue_S = [&](int t, int j) {
+            const int nk = p.fresh(j) ? 2 : 1;
+            for (int term = 0; term < 2 * nk; ++term) {
+              const uint32_t sq = smem_u32(smem + (2 * t + (term & 1)) * Smem::kQ);
+              const uint32_t sk = smem_u32(smem + Smem::oK + slots[term >> 1] * Smem::kK);
+#pragma unroll
+              for (int kk = 0; kk < kHD / 32; ++kk)
+                umma_e4m3(tmem + 128 * t, sdesc_sw128(sq + kk * 32, 16, 1024), sdesc_sw128(sk + kk * 32, 16, 1024),
+                          idS, (term | kk) ? 1u : 0u);
+            }
+            umma_commit(&sfull[t]);
+            if (t == 1)
+              for (int i = 0; i < nk; ++i) umma_commit(&kempty[slots[i]]);
+          };
+          auto issue_PV = [&](int t, int j) -> bool {
+            const int s = (J + j) % kNV;
+            if (t == 0 && !mbar_wait(&vfull[s], ((J + j) / kNV) & 1, status, abort)) return false;
+            if (j == 0 && np > 0 && !mbar_wait(&ofree[t], (np - 1) & 1, status, abort)) return false;
+            const uint32_t sv = smem_u32(smem + Smem::oVf + s * Smem::kF16);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              if (!mbar_wait(&pready[2 * t + hf], (J + j) & 1, status, abort)) return false;
+              tc_fence_after();
+#pragma unroll
+              for (int k4 = 0; k4 < kTK / 32; ++k4) {
+                const int kk = hf * (kTK / 32) + k4;
+                umma_bf16_ts(tmem + kColO + 128 * t, tmem + 128 * t + 8 * kk, sdesc_sw128(sv + kk * 2048, Smem::kBox, 1024),
+                             idPV, (j > 0 || kk > 0) ? 1u : 0u);
+              }
+            }
+            umma_commit(&pvdone[t]);
+            if (t == 1) umma_commit(&vempty[s]);
+            return true;
+          };
+          ok = mbar_wait(qfull, np & 1, status, abort) && wait_k(0);
+          if (ok) {
+            issue_S(0, 0);
+            issue_S(1, 0);
+            if (n == 1) umma_commit(qempty);
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            if (!(ok = issue_PV(0, j))) break;
+            if (j + 1 < n) {
+              if (!(ok = wait_k(j + 1))) break;
+              issue_S(0, j + 1);
+            }
+            if (!(ok = issue_PV(1, j))) break;
+            if (j + 1 < n) {
+              issue_S(1, j + 1);
+              if (j + 2 == n) umma_commit(qempty);
+            }
+          }
+          J += n;
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        w += p.tiles();
+      }
+    }
+  } else if (warp < 8) {
+    reg_dec<64>();
+    const int tid = threadIdx.x - 128;
+    bool ok = true;
+    int J = 0;
+    for (long long w = w0; w < w1 && ok;) {
+      const Piece p = piece_at(a, w, w1);
+      for (int j = 0; j < p.tiles(); ++j, ++J) {
+        const int s = J % kNV, par = (J / kNV) & 1;
+        if (!(ok = mbar_wait_warp(&cfull[s], par, status, abort))) break;
+        if (!p.fresh(j)) {
+          if (!(ok = mbar_wait_warp(&vempty[s], par ^ 1, status, abort))) break;
+          const uint8_t* src = smem + Smem::oVc + s * Smem::kK;
+          uint8_t* dst = smem + Smem::oVf + s * Smem::kF16;
+          const int valid = p.len - (p.t0 + j) * kTK;
+#pragma unroll
+          for (int it = 0; it < kTK * 8 / 128; ++it) {
+            const int id = it * 128 + tid, row = id / 8, c = id % 8;
+            uint4 v = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
+            if (row >= valid) v = make_uint4(0, 0, 0, 0);  // what lies behind the sequence never enters an MMA
+            uint4 h[2];
+            h[0] = make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16));
+            h[1] = make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w), e4m3x2_f16x2(v.w >> 16));
+            uint8_t* d = dst + (c / 4) * Smem::kBox + row * 128;
+            const int ch = (c % 4) * 2, f = c / 4;  // the two boxes' lanes store their halves in opposite order: no bank conflicts
+            *reinterpret_cast<uint4*>(d + (((ch + f) ^ (row & 7)) << 4)) = f ? h[1] : h[0];
+            *reinterpret_cast<uint4*>(d + (((ch + 1 - f) ^ (row & 7)) << 4)) = f ? h[0] : h[1];
+          }
+          fence_async_smem();
+        }
+        mbar_arrive(&cempty[s]);
+        mbar_arrive(&vfull[s]);
+      }
+      w += p.tiles();
+    }
+  } else {
+    reg_inc<176>();
+    const int t = (warp - 8) / 4, q4 = warp & 3;
+    const int r = q4 * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + kColO + 128 * t;
+    bool ok = true;
+    int J = 0;
+    for (long long w = w0; w < w1 && ok;) {
+      const Piece p = piece_at(a, w, w1);
+      const int n = p.tiles(), bh = p.b * a.Hkv + p.hk;
+      const int ridx = p.row0 + 128 * t + r;
+      const bool valid_row = ridx < grp_rows;
+      const int qx = valid_row ? pp.qexp[(size_t)bh * grp_rows + ridx] : 0;
+      const int qi = valid_row ? ridx % a.C : 0;
+      // exponents of the tile's two blocks: key 0, key 1, value 0, value 1
+      auto exps = [&](int j, int (&e)[4]) {
+        const bool fresh = p.fresh(j);
+        const int i = (p.t0 + j - (fresh ? p.ntc : 0)) * 2, nb = fresh ? pp.Cp / kKv8Block : a.nblk;
+        const uint8_t* ke = (fresh ? pp.kexp : a.Ke) + (size_t)bh * nb;
+        const uint8_t* ve = (fresh ? pp.vexp : a.Ve) + (size_t)bh * nb;
+        const int i1 = min(i + 1, nb - 1);
+        e[0] = ke[i];
+        e[1] = ke[i1];
+        e[2] = ve[i];
+        e[3] = ve[i1];
+      };
+      int ex[4], en[4];
+      exps(0, en);
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < n; ++j) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ex[k] = en[k] - kKv8Bias;
+        if (j + 1 < n) exps(j + 1, en);
+        if (!(ok = mbar_wait_warp(&sfull[t], (J + j) & 1, status, abort))) break;
+        tc_fence_after();
+        float sv[kTK];
+#pragma unroll
+        for (int c = 0; c < kTK / 32; ++c) tmem_ld32_async(tS + 32 * c, *reinterpret_cast<float(*)[32]>(sv + 32 * c));
+        tmem_wait_ld();
+        const bool fresh = p.fresh(j);
+        const int key0 = (p.t0 + j - (fresh ? p.ntc : 0)) * kTK;
+        int lim = (fresh ? a.C : p.len) - key0;
+        if (fresh && a.causal) lim = min(lim, qi - key0 + 1);
+        if (__any_sync(0xffffffffu, lim < kTK)) {
+#pragma unroll
+          for (int c = 0; c < kTK; ++c)
+            if (c >= lim) sv[c] = -INFINITY;
+        }
+        const float c0 = scale_log2 * pow2i(qx + ex[0]), c1 = scale_log2 * pow2i(qx + ex[1]);
+        const float v0 = (float)ex[2], v1 = (float)ex[3];
+        float mx;
+        {
+          float h[2][2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float* s = sv + 64 * b;
+            float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]);
+#pragma unroll
+            for (int c = 4; c < 64; c += 4) {
+              x0 = fmax3(x0, s[c], s[c + 1]);
+              x1 = fmax3(x1, s[c + 2], s[c + 3]);
+            }
+            h[b][0] = x0;
+            h[b][1] = x1;
+          }
+          mx = fmaxf(fmaf(fmaxf(h[0][0], h[0][1]), c0, v0), fmaf(fmaxf(h[1][0], h[1][1]), c1, v1));
+        }
+        if (j == 0) {
+          m_run = mx;
+        } else {
+          const bool need = mx > m_run + kLazy;
+          if (__any_sync(0xffffffffu, need)) {
+            // O_t must hold P_t V of tile j - 1 before it is rescaled
+            if (!(ok = mbar_wait_warp(&pvdone[t], (J + j - 1) & 1, status, abort))) break;
+            tc_fence_after();
+            const float corr = need ? ex2_approx(m_run - mx) : 1.0f;
+#pragma unroll 1
+            for (int c = 0; c < kHD / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st16(tO + 16 * c, o);
+            }
+            if (need) {
+              l_run *= corr;
+              m_run = mx;
+            }
+          }
+        }
+        const float mm = m_run == -INFINITY ? 0.f : m_run - kHeadroom;
+        const float off[2] = {v0 - mm, v1 - mm}, cc[2] = {c0, c1};
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {  // the tile's two blocks of 64 keys: 32 columns of P each
+          const uint64_t sc2 = f2_pack(cc[b], cc[b]), of2 = f2_pack(off[b], off[b]);
+          uint64_t rs[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t hw[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float t0, t1;
+              f2_unpack(f2_fma(f2_pack(sv[64 * b + 32 * c + 2 * e], sv[64 * b + 32 * c + 2 * e + 1]), sc2, of2), t0, t1);
+              const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+              rs[e & 1] = f2_add(rs[e & 1], f2_pack(p0, p1));
+              hw[e] = pack_f16(p0, p1);
+            }
+            tmem_st16(tS + 32 * b + 16 * c, hw);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&pready[2 * t + b]);
+          float x0, x1;
+          f2_unpack(f2_add(rs[0], rs[1]), x0, x1);
+          l_run = fmaf(x0 + x1, pow2i(-ex[2 + b]), l_run);
+        }
+      }
+      if (!ok || !(ok = mbar_wait_warp(&pvdone[t], (J + n - 1) & 1, status, abort))) break;
+      tc_fence_after();
+      const bool whole = p.t0 == 0 && p.t1 == p.nt;
+      const size_t prow = ((size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1)) * 256 + 128 * t + r;
+      const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
+      __nv_bfloat16* orow = valid_row ? kv8_out_row(a, p.b, p.hk, ridx) : nullptr;
+#pragma unroll 1
+      for (int c = 0; c < kHD / 32; ++c) {
+        float o[32];
+        tmem_ld32(tO + 32 * c, o);
+        if (c == kHD / 32 - 1) {
+          tc_fence_before();
+          mbar_arrive(&ofree[t]);
+        }
+        if (!valid_row) continue;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[q] = make_uint4(pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv), pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                                pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv), pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.part + prow * kHD + 32 * c);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          if (c == 0)
+            *reinterpret_cast<float2*>(a.ml + prow * 2) =
+                make_float2(m_run == -INFINITY ? m_run : m_run - kHeadroom, l_run);
+        }
+      }
+      J += n;
+      w += n;
+    }
+  }
+  __syncthreads();
+  if (*abort) {  // copies in flight land before the CTA's shared memory goes
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------- prep --
+// Two E4M3 terms of eight scaled values.
+DG_DEV void split8(const float (&x)[8], uint2& hi, uint2& lo) {
+  uint32_t h[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t c0 = pack_e4m3(x[4 * i], x[4 * i + 1]), c1 = pack_e4m3(x[4 * i + 2], x[4 * i + 3]);
+    const uint32_t w0 = e4m3x2_f16x2(c0), w1 = e4m3x2_f16x2(c1);
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w0));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w1));
+    h[i] = c0 | (c1 << 16);
+    l[i] = pack_e4m3(x[4 * i] - f0.x, x[4 * i + 1] - f0.y) |
+           (pack_e4m3(x[4 * i + 2] - f1.x, x[4 * i + 3] - f1.y) << 16);
+  }
+  hi = make_uint2(h[0], h[1]);
+  lo = make_uint2(l[0], l[1]);
+}
+DG_DEV void unpack8(const uint4& w, float f, float (&x)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16) * f;
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * f;
+  }
+}
+DG_DEV unsigned abs_top(const uint4& w) {
+  return __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+}
+// Exponent that brings a largest magnitude (bf16 bits) into (224, 448].
+DG_DEV int top_exponent(unsigned bits) {
+  const int E = (int)(bits >> 7), m = (int)(bits & 127u);
+  return E == 0 ? kKv8Emin : min(max(E - 127 - 8 + (m > 96 ? 1 : 0), kKv8Emin), kKv8Emax);
+}
+
+// q to two E4M3 terms and a scale per row (16 lanes a row, 8 elements a lane);
+// new keys to two E4M3 terms and new values to f16, with a scale per 64 tokens
+// (one CTA per block, zeros behind the last token).
+__global__ void __launch_bounds__(256) kv8_prep_kernel(Kv8AttnArgs a, Kv8Prep pp, int kv_ctas) {
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= kv_ctas) {
+    const long long row = (long long)(blockIdx.x - kv_ctas) * 16 + tid / 16;
+    const bool there = row < pp.qrows;
+    const uint4 w = there ? *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + row * kHD +
+                                                            (tid % 16) * 8)
+                          : make_uint4(0, 0, 0, 0);
+    unsigned top = abs_top(w);
+    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = top_exponent(top);
+    float x[8];
+    unpack8(w, pow2i(-e), x);
+    uint2 hi, lo;
+    split8(x, hi, lo);
+    if (!there) return;
+    *reinterpret_cast<uint2*>(pp.qterms + row * kHD + (tid % 16) * 8) = hi;
+    *reinterpret_cast<uint2*>(pp.qterms + ((size_t)pp.qrows + row) * kHD + (tid % 16) * 8) = lo;
+    if (tid % 16 == 0) pp.qexp[row] = e;
+    return;
+  }
+  __shared__ unsigned red[8];
+  const int nb = pp.Cp / kKv8Block, isv = blockIdx.x & 1, blk = (blockIdx.x >> 1) % nb, bh = (blockIdx.x >> 1) / nb;
+  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(isv ? a.vn : a.kn) + (size_t)bh * a.C * kHD;
+  uint4 w[4];
+  unsigned top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = blk * kKv8Block + i * 16 + tid / 16;
+    w[i] = row < a.C ? *reinterpret_cast<const uint4*>(src + (size_t)row * kHD + (tid % 16) * 8) : make_uint4(0, 0, 0, 0);
+    top = __vmaxu2(top, abs_top(w[i]));
+  }
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+  if (tid % 32 == 0) red[tid / 32] = top;
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, red[tid % 8]);
+  const int e = top_exponent(top);
+  if (tid == 0) (isv ? pp.vexp : pp.kexp)[(size_t)bh * nb + blk] = (uint8_t)(e + kKv8Bias);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const size_t row = (size_t)bh * pp.Cp + blk * kKv8Block + i * 16 + tid / 16;
+    float x[8];
+    unpack8(w[i], pow2i(-e), x);
+    if (isv) {
+      *reinterpret_cast<uint4*>(pp.vf16 + row * kHD * 2 + (tid % 16) * 16) =
+          make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]), pack_f16(x[6], x[7]));
+    } else {
+      uint2 hi, lo;
+      split8(x, hi, lo);
+      *reinterpret_cast<uint2*>(pp.kterms + row * kHD + (tid % 16) * 8) = hi;
+      *reinterpret_cast<uint2*>(pp.kterms + ((size_t)pp.krows + row) * kHD + (tid % 16) * 8) = lo;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cudaStream_t st) {
+  const uint64_t cached = (uint64_t)a.B * a.Hkv * a.cap;
+  CUtensorMap mQ, mK, mV, mKn, mVn;
+  if (!make_tmap_2d(&mQ, pp.qterms, kHD, 2 * (uint64_t)pp.qrows, kHD, kHD, 128, true) ||
+      !make_tmap_2d(&mK, a.K, kHD, cached, kHD, kHD, kTK, true) ||
+      !make_tmap_2d(&mV, a.V, kHD, cached, kHD, kHD, kTK, true))
+    return cudaErrorInvalidValue;
+  mKn = mK;  // without new tokens neither is used
+  mVn = mV;
+  if (a.kn && (!make_tmap_2d(&mKn, pp.kterms, kHD, 2 * (uint64_t)pp.krows, kHD, kHD, kTK, true) ||
+               !make_tmap_2d(&mVn, pp.vf16, kHD, (uint64_t)pp.krows, kHD * 2, 64, kTK)))
+    return cudaErrorInvalidValue;
+  cudaError_t e = set_smem_once<kv8_attn_tc_kernel>(Smem::kTotal);
+  if (e != cudaSuccess) return e;
+  const int kv_ctas = a.kn ? 2 * a.B * a.Hkv * (pp.Cp / kKv8Block) : 0;
+  e = launch_pdl(kv8_prep_kernel, dim3(kv_ctas + cdiv(pp.qrows, 16)), dim3(256), 0, st, a, pp, kv_ctas);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv8_attn_tc_kernel, dim3(kKv8Ctas), dim3(kThreads), Smem::kTotal, st, mQ, mK, mV, mKn, mVn, a, pp,
+                    1.4426950408889634f / sqrtf((float)kHD));
+}
+
+}  // namespace dg
