@@ -22,7 +22,7 @@
 // products), values as f16 on such a scale (exact to 2^-22 of the block's
 // largest).
 //
-// Warp roles (16 warps, one CTA per SM; registers moved to the softmax warps):
+// Warp roles (16 warps, one CTA per SM):
 //   warp 0       TMA: Q terms per piece, K tiles into a ring of 16 KB slots (a
 //                new tile takes two), V codes into their own ring (new tiles:
 //                f16, straight to the MMA's buffer)
@@ -60,20 +60,52 @@ static_assert(Smem::kTotal <= 232448, "shared memory of one CTA");
 // TMEM: S_t at 128 t (P_t over its first 64 columns), O_t at 256 + 128 t.
 constexpr int kColO = 256;
 
-DG_DEV void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+// The MMA warp runs as one: every lane reaches these, one elected lane issues.
+// With the election inside, the descriptors stay in uniform registers: 39
+// cycles an MMA from issue to issue against 57 in a branch of lane 0 alone
+// (measured alone; an MMA of this kernel takes the tensor core 64).
+DG_DEV void mma_s(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum)
       : "memory");
 }
-template <int N>
-DG_DEV void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+DG_DEV void mma_pv(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum)
+      : "memory");
 }
-template <int N>
-DG_DEV void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+DG_DEV void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+// Shared-memory descriptors (128-byte swizzle, 1024 bytes between 8-row groups)
+// as a low word, address and leading offset, and a high word they all share.
+DG_DEV uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | (lbo >> 4 << 16); }
+DG_DEV uint64_t desc64(uint32_t lo) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "n"(hi));
+  return d;
+}
+// D (+)= (Q_hi + Q_lo) K^T: the two terms of a query tile lie behind one another.
+DG_DEV void s_terms(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc, uint32_t accum) {
+#pragma unroll
+  for (int term = 0; term < 2; ++term)
+#pragma unroll
+    for (int kk = 0; kk < kHD / 32; ++kk)
+      mma_s(d, desc64(q + term * (Smem::kQ >> 4) + 2 * kk), desc64(k + 2 * kk), idesc, (term | kk) ? 1u : accum);
+}
+// Bounded wait of a whole warp whose usual case, the phase is complete, costs
+// one try (63 cycles against 171 for mbar_wait_warp's loops, measured alone).
+DG_DEV bool wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return mbar_wait_warp(bar, parity, status, abort);
 }
 DG_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -135,16 +167,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kNV; ++s) {
       mbar_init(&cfull[s], 1);
-      mbar_init(&cempty[s], 128);
-      mbar_init(&vfull[s], 128);
+      mbar_init(&cempty[s], 4);
+      mbar_init(&vfull[s], 4);
       mbar_init(&vempty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
-      mbar_init(&pready[2 * t], 128);
-      mbar_init(&pready[2 * t + 1], 128);
+      mbar_init(&pready[2 * t], 4);
+      mbar_init(&pready[2 * t + 1], 4);
       mbar_init(&pvdone[t], 1);
-      mbar_init(&ofree[t], 128);
+      mbar_init(&ofree[t], 4);
     }
     *abort = 0;
     fence_mbar_init();
@@ -164,7 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int grp_rows = a.Hq / a.Hkv * a.C;
 
   if (warp < 4) {
-    reg_dec<96>();
     if (warp == 0) {
       if (blockIdx.x == 0)
         for (int b = lane; b < a.B; b += 32)
@@ -224,85 +255,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       constexpr uint32_t idS = idesc_e4m3(128, kTK);
       constexpr uint32_t idPV = idesc_f16(128, kHD, true);
+      // The whole warp waits, one lane issues.  Descriptors differ in their low
+      // word alone (address / 16); nothing here is indexed dynamically, so that
+      // the issue never waits on local memory.
+      const uint32_t lo_q = desc_lo(smem_u32(smem), 16), lo_k = desc_lo(smem_u32(smem + Smem::oK), 16);
+      const uint32_t lo_v = desc_lo(smem_u32(smem + Smem::oVf), Smem::kBox);
       bool ok = true;
       int kslot = 0, kpar = 0, J = 0, np = 0;
       for (long long w = w0; w < w1 && ok; ++np) {
         const Piece p = piece_at(a, w, w1);
-        if (lane == 0) {
-          const int n = p.tiles();
-          int slots[2] = {0, 0};  // K slots of the tile whose S is being issued
-          auto wait_k = [&](int j) -> bool {
-            for (int term = 0; term < (p.fresh(j) ? 2 : 1); ++term) {
-              if (!mbar_wait(&kfull[kslot], kpar, status, abort)) return false;
-              slots[term] = kslot;
-              if (++kslot == kNK) {
-                kslot = 0;
-                kpar ^= 1;
+        const int n = p.tiles(), jfresh = p.ntc - p.t0;  // tiles from jfresh on hold new tokens
+        int ka = 0, kb = 0;                              // K slots of the tile whose S is being issued
+        auto wait_k = [&](int& k) -> bool {
+          k = kslot;
+          const bool r = wait(&kfull[kslot], kpar, status, abort);
+          if (++kslot == kNK) {
+            kslot = 0;
+            kpar ^= 1;
+          }
+          return r;
+        };
+        ok = wait(qfull, np & 1, status, abort);
+        // Step j: for each row tile P V of key tile j, then S of tile j + 1.  One
+        // copy of the code, with no unrolling past an operand tile: the warp
+        // runs through it once in some thousand cycles, between the softmax
+        // warps' code, and pays for every line that it has to fetch again.
+#pragma unroll 1
+        for (int j = -1; j < n && ok; ++j) {
+          const int s = (J + j) & 1;
+          const bool next = j + 1 < n, fresh = j + 1 >= jfresh;
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            if (j >= 0) {
+              if (t == 0 && !(ok = wait(&vfull[s], ((J + j) / kNV) & 1, status, abort))) break;
+              if (j == 0 && np > 0 && !(ok = wait(&ofree[t], (np - 1) & 1, status, abort))) break;
+              const uint32_t d = tmem + kColO + 128 * t;
+              uint32_t v = lo_v + s * (Smem::kF16 >> 4), pt = tmem + 128 * t;
+#pragma unroll 1
+              for (int hf = 0; hf < 2; ++hf, v += (kTK / 32) * (2048 >> 4), pt += kTK / 4) {
+                if (!(ok = wait(&pready[2 * t + hf], (J + j) & 1, status, abort))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k4 = 0; k4 < kTK / 32; ++k4)
+                  mma_pv(d, pt + 8 * k4, desc64(v + k4 * (2048 >> 4)), idPV, (j | hf | k4) ? 1u : 0u);
               }
+              if (!ok) break;
+              commit(&pvdone[t]);
+              if (t == 1) commit(&vempty[s]);
             }
-            tc_fence_after();
-            return true;
-          };
-          auto issue_S = [&](int t, int j) {
-            const int nk = p.fresh(j) ? 2 : 1;
-            for (int term = 0; term < 2 * nk; ++term) {
-              const uint32_t sq = smem_u32(smem + (2 * t + (term & 1)) * Smem::kQ);
-              const uint32_t sk = smem_u32(smem + Smem::oK + slots[term >> 1] * Smem::kK);
-#pragma unroll
-              for (int kk = 0; kk < kHD / 32; ++kk)
-                umma_e4m3(tmem + 128 * t, sdesc_sw128(sq + kk * 32, 16, 1024), sdesc_sw128(sk + kk * 32, 16, 1024),
-                          idS, (term | kk) ? 1u : 0u);
-            }
-            umma_commit(&sfull[t]);
-            if (t == 1)
-              for (int i = 0; i < nk; ++i) umma_commit(&kempty[slots[i]]);
-          };
-          auto issue_PV = [&](int t, int j) -> bool {
-            const int s = (J + j) % kNV;
-            if (t == 0 && !mbar_wait(&vfull[s], ((J + j) / kNV) & 1, status, abort)) return false;
-            if (j == 0 && np > 0 && !mbar_wait(&ofree[t], (np - 1) & 1, status, abort)) return false;
-            const uint32_t sv = smem_u32(smem + Smem::oVf + s * Smem::kF16);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              if (!mbar_wait(&pready[2 * t + hf], (J + j) & 1, status, abort)) return false;
+            if (next) {
+              if (t == 0 && !(ok = wait_k(ka) && (!fresh || wait_k(kb)))) break;
               tc_fence_after();
-#pragma unroll
-              for (int k4 = 0; k4 < kTK / 32; ++k4) {
-                const int kk = hf * (kTK / 32) + k4;
-                umma_bf16_ts(tmem + kColO + 128 * t, tmem + 128 * t + 8 * kk, sdesc_sw128(sv + kk * 2048, Smem::kBox, 1024),
-                             idPV, (j > 0 || kk > 0) ? 1u : 0u);
+              uint32_t k = lo_k + ka * (Smem::kK >> 4);
+#pragma unroll 1
+              for (int term = 0; term <= (fresh ? 1 : 0); ++term, k = lo_k + kb * (Smem::kK >> 4))
+                s_terms(tmem + 128 * t, lo_q + t * (2 * Smem::kQ >> 4), k, idS, term);
+              commit(&sfull[t]);
+              if (t == 1) {
+                commit(&kempty[ka]);
+                if (fresh) commit(&kempty[kb]);
+                if (j + 2 == n) commit(qempty);
               }
             }
-            umma_commit(&pvdone[t]);
-            if (t == 1) umma_commit(&vempty[s]);
-            return true;
-          };
-          ok = mbar_wait(qfull, np & 1, status, abort) && wait_k(0);
-          if (ok) {
-            issue_S(0, 0);
-            issue_S(1, 0);
-            if (n == 1) umma_commit(qempty);
           }
-          for (int j = 0; j < n && ok; ++j) {
-            if (!(ok = issue_PV(0, j))) break;
-            if (j + 1 < n) {
-              if (!(ok = wait_k(j + 1))) break;
-              issue_S(0, j + 1);
-            }
-            if (!(ok = issue_PV(1, j))) break;
-            if (j + 1 < n) {
-              issue_S(1, j + 1);
-              if (j + 2 == n) umma_commit(qempty);
-            }
-          }
-          J += n;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        w += p.tiles();
+        J += n;
+        w += n;
       }
     }
   } else if (warp < 8) {
-    reg_dec<64>();
     const int tid = threadIdx.x - 128;
     bool ok = true;
     int J = 0;
@@ -310,9 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Piece p = piece_at(a, w, w1);
       for (int j = 0; j < p.tiles(); ++j, ++J) {
         const int s = J % kNV, par = (J / kNV) & 1;
-        if (!(ok = mbar_wait_warp(&cfull[s], par, status, abort))) break;
+        if (!(ok = wait(&cfull[s], par, status, abort))) break;
         if (!p.fresh(j)) {
-          if (!(ok = mbar_wait_warp(&vempty[s], par ^ 1, status, abort))) break;
+          if (!(ok = wait(&vempty[s], par ^ 1, status, abort))) break;
           const uint8_t* src = smem + Smem::oVc + s * Smem::kK;
           uint8_t* dst = smem + Smem::oVf + s * Smem::kF16;
           const int valid = p.len - (p.t0 + j) * kTK;
@@ -331,13 +352,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_async_smem();
         }
-        mbar_arrive(&cempty[s]);
-        mbar_arrive(&vfull[s]);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&cempty[s]);
+          mbar_arrive(&vfull[s]);
+        }
       }
       w += p.tiles();
     }
   } else {
-    reg_inc<176>();
     const int t = (warp - 8) / 4, q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
@@ -370,39 +393,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) ex[k] = en[k] - kKv8Bias;
         if (j + 1 < n) exps(j + 1, en);
-        if (!(ok = mbar_wait_warp(&sfull[t], (J + j) & 1, status, abort))) break;
+        if (!(ok = wait(&sfull[t], (J + j) & 1, status, abort))) break;
         tc_fence_after();
-        float sv[kTK];
-#pragma unroll
-        for (int c = 0; c < kTK / 32; ++c) tmem_ld32_async(tS + 32 * c, *reinterpret_cast<float(*)[32]>(sv + 32 * c));
-        tmem_wait_ld();
         const bool fresh = p.fresh(j);
         const int key0 = (p.t0 + j - (fresh ? p.ntc : 0)) * kTK;
-        int lim = (fresh ? a.C : p.len) - key0;
+        int lim = (fresh ? a.C : p.len) - key0;  // columns of the tile that this row sees
         if (fresh && a.causal) lim = min(lim, qi - key0 + 1);
-        if (__any_sync(0xffffffffu, lim < kTK)) {
+        // Two passes over the scores, 64 columns (one block's scales) at a
+        // time: kept in registers between them they would need twice the
+        // registers and unrolled code that no instruction cache holds.
+        auto load = [&](int b, float (&s)[64]) {
+          tmem_ld32_async(tS + 64 * b, *reinterpret_cast<float(*)[32]>(s));
+          tmem_ld32_async(tS + 64 * b + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+          tmem_wait_ld();
+          if (__any_sync(0xffffffffu, lim < 64 * b + 64)) {
 #pragma unroll
-          for (int c = 0; c < kTK; ++c)
-            if (c >= lim) sv[c] = -INFINITY;
-        }
-        const float c0 = scale_log2 * pow2i(qx + ex[0]), c1 = scale_log2 * pow2i(qx + ex[1]);
-        const float v0 = (float)ex[2], v1 = (float)ex[3];
-        float mx;
-        {
-          float h[2][2];
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float* s = sv + 64 * b;
-            float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]);
-#pragma unroll
-            for (int c = 4; c < 64; c += 4) {
-              x0 = fmax3(x0, s[c], s[c + 1]);
-              x1 = fmax3(x1, s[c + 2], s[c + 3]);
-            }
-            h[b][0] = x0;
-            h[b][1] = x1;
+            for (int c = 0; c < 64; ++c)
+              if (64 * b + c >= lim) s[c] = -INFINITY;
           }
-          mx = fmaxf(fmaf(fmaxf(h[0][0], h[0][1]), c0, v0), fmaf(fmaxf(h[1][0], h[1][1]), c1, v1));
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+          float s[64];
+          load(b, s);
+          float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]), x2 = fmaxf(s[4], s[5]), x3 = fmaxf(s[6], s[7]);
+#pragma unroll
+          for (int c = 8; c < 64; c += 8) {
+            x0 = fmax3(x0, s[c], s[c + 1]);
+            x1 = fmax3(x1, s[c + 2], s[c + 3]);
+            x2 = fmax3(x2, s[c + 4], s[c + 5]);
+            x3 = fmax3(x3, s[c + 6], s[c + 7]);
+          }
+          const int ke = b ? ex[1] : ex[0], ve = b ? ex[3] : ex[2];
+          mx = fmaxf(mx, fmaf(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), scale_log2 * pow2i(qx + ke), (float)ve));
         }
         if (j == 0) {
           m_run = mx;
@@ -410,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool need = mx > m_run + kLazy;
           if (__any_sync(0xffffffffu, need)) {
             // O_t must hold P_t V of tile j - 1 before it is rescaled
-            if (!(ok = mbar_wait_warp(&pvdone[t], (J + j - 1) & 1, status, abort))) break;
+            if (!(ok = wait(&pvdone[t], (J + j - 1) & 1, status, abort))) break;
             tc_fence_after();
             const float corr = need ? ex2_approx(m_run - mx) : 1.0f;
 #pragma unroll 1
@@ -428,33 +452,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float mm = m_run == -INFINITY ? 0.f : m_run - kHeadroom;
-        const float off[2] = {v0 - mm, v1 - mm}, cc[2] = {c0, c1};
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {  // the tile's two blocks of 64 keys: 32 columns of P each
-          const uint64_t sc2 = f2_pack(cc[b], cc[b]), of2 = f2_pack(off[b], off[b]);
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {  // 32 columns of P each
+          float s[64];
+          load(b, s);
+          const int ke = b ? ex[1] : ex[0], ve = b ? ex[3] : ex[2];
+          const float c = scale_log2 * pow2i(qx + ke), off = (float)ve - mm;
+          const uint64_t c2 = f2_pack(c, c), off2 = f2_pack(off, off);
           uint64_t rs[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int h = 0; h < 2; ++h) {
             uint32_t hw[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float t0, t1;
-              f2_unpack(f2_fma(f2_pack(sv[64 * b + 32 * c + 2 * e], sv[64 * b + 32 * c + 2 * e + 1]), sc2, of2), t0, t1);
+              f2_unpack(f2_fma(f2_pack(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), c2, off2), t0, t1);
               const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
               rs[e & 1] = f2_add(rs[e & 1], f2_pack(p0, p1));
               hw[e] = pack_f16(p0, p1);
             }
-            tmem_st16(tS + 32 * b + 16 * c, hw);
+            tmem_st16(tS + 32 * b + 16 * h, hw);
           }
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&pready[2 * t + b]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pready[2 * t + b]);
           float x0, x1;
           f2_unpack(f2_add(rs[0], rs[1]), x0, x1);
-          l_run = fmaf(x0 + x1, pow2i(-ex[2 + b]), l_run);
+          l_run = fmaf(x0 + x1, pow2i(-ve), l_run);
         }
       }
-      if (!ok || !(ok = mbar_wait_warp(&pvdone[t], (J + n - 1) & 1, status, abort))) break;
+      if (!ok || !(ok = wait(&pvdone[t], (J + n - 1) & 1, status, abort))) break;
       tc_fence_after();
       const bool whole = p.t0 == 0 && p.t1 == p.nt;
       const size_t prow = ((size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1)) * 256 + 128 * t + r;
@@ -466,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tO + 32 * c, o);
         if (c == kHD / 32 - 1) {
           tc_fence_before();
-          mbar_arrive(&ofree[t]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ofree[t]);
         }
         if (!valid_row) continue;
         if (whole) {
