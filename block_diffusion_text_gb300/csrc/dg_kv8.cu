@@ -224,7 +224,7 @@ int kv8_blocks(int cap) { return cdiv(cap, kKv8Block); }
 
 struct Kv8Ws {
   size_t part, ml, qterms, qexp, kterms, vf16, kexp, vexp, total;
-  int rows, tk, units, workers, Cp;
+  int rows, tk, units, workers, prows, Cp;
   bool tc;
 };
 
@@ -237,14 +237,15 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   w.tk = w.tc ? 128 : kKv8Block;
   w.workers = w.tc ? kKv8Ctas : kKv8Ctas * kKv8Warps;
   w.units = (int)(c->Hkv * ((R + w.rows - 1) / w.rows));
+  w.prows = (int)(R < w.rows ? R : w.rows);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes, 256);
     return o;
   };
-  w.part = take((size_t)2 * w.workers * w.rows * c->hd * 4);
-  w.ml = take((size_t)2 * w.workers * w.rows * 8);
+  w.part = take((size_t)2 * w.workers * w.prows * c->hd * 4);
+  w.ml = take((size_t)2 * w.workers * w.prows * 8);
   if (w.tc) {
     w.Cp = cdiv(C, 128) * 128;
     const size_t qrows = (size_t)c->B * Hq * C, krows = (size_t)c->B * c->Hkv * w.Cp;
@@ -341,7 +342,7 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   a.vn = v;
   a.o = o;
   a.part = reinterpret_cast<float*>(base + w.part);
-  a.ml = reinterpret_cast<float*>(base + w.ml);
+  a.ml = reinterpret_cast<float2*>(base + w.ml);
   a.status = cache->status;
   a.B = cache->B;
   a.C = C;
@@ -355,6 +356,7 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   a.tk = w.tk;
   a.units = w.units;
   a.workers = w.workers;
+  a.prows = w.prows;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (w.tc) {

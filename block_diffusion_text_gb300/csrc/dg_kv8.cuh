@@ -25,13 +25,14 @@ struct Kv8AttnArgs {
   const int* len;            // [B]
   const void *kn, *vn;       // bf16 [B][Hkv][C][hd] or null
   void* o;                   // bf16 [B*C][Hq*hd]
-  float* part;               // fp32 [2 * workers][rows][hd]
-  float* ml;                 // fp32 [2 * workers][rows][2]: maximum (log2 units) and sum
+  float* part;               // fp32 [2 * workers][hd / 4][prows][4]
+  float2* ml;                // [2 * workers][prows]: maximum (log2 units) and sum
   int* status;
   int B, C, Hq, Hkv, hd, cap, nblk;
   int causal;
   int rows, tk, units;       // rows per unit, keys per tile, units per sequence (Hkv * row tiles)
   int workers;               // warps or CTAs that the tiles are dealt to
+  int prows;                 // rows of a part: min(rows, G C)
 };
 
 // All tiles of a call, in the order (sequence, unit, tile), are dealt to the
@@ -48,11 +49,23 @@ struct Kv8Seq {
 };
 
 DG_DEV int kv8_len(const Kv8AttnArgs& a, int b) {
-  const int n = a.len[b];
+  const int n = __ldcg(a.len + b);
   return min(max(n, 0), a.cap);
 }
 DG_DEV int kv8_tiles(const Kv8AttnArgs& a, int len) {
   return (len + a.tk - 1) / a.tk + (a.kn ? (a.C + a.tk - 1) / a.tk : 0);
+}
+// a / b for a, b >= 0 (b > 0): the 64-bit division of the hardware's 32-bit one
+// costs some hundred cycles, and a call's tiles hardly ever need it.
+DG_DEV long long kv8_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+// Four columns (4 c4 ..) of row r of a part: consecutive rows lie side by side,
+// so that the kernels that hold a row in a thread write whole lines, and the
+// merge reads a part from end to end.
+DG_DEV float4* kv8_part(const Kv8AttnArgs& a, size_t slot, int c4, int r) {
+  return reinterpret_cast<float4*>(a.part) + (slot * (a.hd / 4) + c4) * a.prows + r;
 }
 // Tiles of the whole call (every lane of the calling warp gets the sum).
 DG_DEV long long kv8_total(const Kv8AttnArgs& a) {
@@ -64,7 +77,7 @@ DG_DEV long long kv8_total(const Kv8AttnArgs& a) {
   return n;
 }
 DG_DEV long long kv8_share(const Kv8AttnArgs& a, long long total) {
-  const long long s = (total + a.workers - 1) / a.workers;
+  const long long s = kv8_div(total + a.workers - 1, a.workers);
   return s > 1 ? s : 1;
 }
 // The sequence that tile w of the call belongs to (w below the total; every

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
 
   for (long long w = worker * share; w < w1;) {
     const Kv8Seq sq = kv8_locate(a, w);
-    const int unit = (int)((w - sq.first) / sq.nt), t0 = (int)((w - sq.first) % sq.nt);
+    const int unit = (int)kv8_div(w - sq.first, sq.nt), t0 = (int)(w - sq.first - (long long)unit * sq.nt);
     const int t1 = (int)min((long long)sq.nt, t0 + (w1 - w));
     const int hk = unit / row_tiles, row0 = unit % row_tiles * (16 * MT);
     const int ntc = (sq.len + kKv8Block - 1) / kKv8Block;
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
 
     // Output, or a part of it: lane (g, t) holds columns 2 t NV .. + 2 NV of rows g and g + 8.
     const bool whole = t0 == 0 && t1 == sq.nt;
-    const size_t slot = ((size_t)worker * 2 + (t0 > 0 ? 0 : 1)) * (16 * MT);
+    const size_t slot = (size_t)worker * 2 + (t0 > 0 ? 0 : 1);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -452,18 +452,16 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
             for (int n = 0; n < NV; n += 2)
               dst[(e * NV + n) / 2] = pack_bf16(acc.o[mt][n][2 * hr + e] * inv, acc.o[mt][n + 1][2 * hr + e] * inv);
         } else {
-          float* dst = a.part + (slot + r) * HD + 2 * t * NV;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int n = 0; n < NV; n += 4)
-              *reinterpret_cast<float4*>(dst + e * NV + n) =
+              *kv8_part(a, slot, ((2 * t + e) * NV + n) / 4, r) =
                   make_float4(acc.o[mt][n][2 * hr + e], acc.o[mt][n + 1][2 * hr + e], acc.o[mt][n + 2][2 * hr + e],
                               acc.o[mt][n + 3][2 * hr + e]);
           if (t == 0) {
             const float m = acc.m[mt][hr];
-            *reinterpret_cast<float2*>(a.ml + (slot + r) * 2) =
-                make_float2(m == -INFINITY ? m : m - kHeadroom, l);
+            a.ml[slot * a.prows + r] = make_float2(m == -INFINITY ? m : m - kHeadroom, l);
           }
         }
       }
@@ -472,65 +470,68 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
   }
 }
 
-// Merge of the parts of one output row per warp: the shares' borders are
-// recomputed, a unit that one worker finished is already written, and one
-// without any key (an empty sequence without new tokens) gets zeros.
+// Merge of the parts.  A thread makes four columns of one output row, a warp 32
+// consecutive float4 of a unit's parts; the shares' borders are recomputed, a
+// unit that one worker finished is already written, and one without any key
+// (an empty sequence without new tokens) gets zeros.  What it reads before
+// pdl_wait, the lengths, no kernel of the call writes, and the attention
+// kernel lets this one start only once it has itself waited for its
+// predecessors; they are read past the first-level cache.
 template <int HD>
 __global__ void __launch_bounds__(256) kv8_merge_kernel(Kv8AttnArgs a) {
-  pdl_wait();
-  constexpr int VEC = HD / 32;
+  constexpr int C4 = HD / 4;
   const int lane = threadIdx.x % 32;
-  const long long row = (long long)blockIdx.x * 8 + threadIdx.x / 32;  // ((b Hkv + g) G C + r)
   const int grp_rows = a.Hq / a.Hkv * a.C;
-  if (row >= (long long)a.B * a.Hkv * grp_rows) return;
-  const int r = (int)(row % grp_rows);
-  const int bh = (int)(row / grp_rows), b = bh / a.Hkv, hk = bh % a.Hkv;
+  const int per = (a.prows * C4 + 31) / 32;  // warps per unit
+  const long long wid = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  const long long all = kv8_div(wid, per);
+  const int b = (int)kv8_div(all, a.units), unit = (int)(all - (long long)b * a.units);
+  if (b >= a.B) return;
+  const int item = (int)(wid - all * per) * 32 + lane;
+  const int row_tiles = a.units / a.Hkv, hk = unit / row_tiles;
+  const int c4 = item / a.prows, rr = item - c4 * a.prows, r = unit % row_tiles * a.rows + rr;
+  const bool mine = c4 < C4 && r < grp_rows;
   const int nt = kv8_tiles(a, kv8_len(a, b));
-  __nv_bfloat16* dst = kv8_out_row(a, b, hk, r) + lane * VEC;
-  if (nt == 0) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) dst[e] = __float2bfloat16_rn(0.f);
-    return;
-  }
   const long long total = kv8_total(a), share = kv8_share(a, total);
   long long first = 0;
   for (int i = lane; i < b; i += 32) first += (long long)kv8_tiles(a, kv8_len(a, i)) * a.units;
 #pragma unroll
   for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-  first += (long long)(hk * (a.units / a.Hkv) + r / a.rows) * nt;
-  const int c0 = (int)(first / share), c1 = (int)((first + nt - 1) / share);
-  if (c0 == c1) return;
-  const int rr = r % a.rows;
-  auto slot = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * a.rows + rr; };
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.ml[slot(c) * 2]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, acc[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  for (int base = c0; base <= c1; base += 32) {
-    const int c = base + lane;
-    float wgt = 0.f;
-    if (c <= c1) {
-      const float2 v = *reinterpret_cast<const float2*>(a.ml + slot(c) * 2);
-      wgt = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
-      L += v.x == -INFINITY ? 0.f : wgt * v.y;
-    }
-    const int n = min(32, c1 - base + 1);
+  first += (long long)unit * nt;
+  const int c0 = (int)kv8_div(first, share), c1 = (int)kv8_div(first + max(nt, 1) - 1, share);
+  pdl_wait();
+  if (!mine || (nt > 0 && c0 == c1)) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = 0.f;
+  if (nt > 0) {
+    // part 0 is the unit's beginning (slot 1 of its worker), the others slots 0
+    const float2* ml = a.ml + (size_t)c0 * 2 * a.prows + rr;
+    const float4* src = kv8_part(a, (size_t)c0 * 2, c4, rr);
+    const size_t mstep = 2 * (size_t)a.prows, pstep = mstep * C4;
+    const float2 ml0 = ml[a.prows];
+    const float4 v0 = src[(size_t)C4 * a.prows];
+    const int n = c1 - c0;
+    float M = ml0.x;
+#pragma unroll 4
+    for (int i = 1; i <= n; ++i) M = fmaxf(M, ml[i * mstep].x);
+    const float w0 = ml0.x == -INFINITY ? 0.f : exp2f(ml0.x - M);
+    L = w0 * ml0.y;
+    acc = make_float4(v0.x * w0, v0.y * w0, v0.z * w0, v0.w * w0);
 #pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float ws = __shfl_sync(0xffffffffu, wgt, i);
-      const float* src = a.part + slot(base + i) * HD + lane * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] = fmaf(src[e], ws, acc[e]);
+    for (int i = 1; i <= n; ++i) {
+      const float2 p = ml[i * mstep];
+      const float4 v = src[i * pstep];
+      const float w = p.x == -INFINITY ? 0.f : exp2f(p.x - M);
+      L = fmaf(w, p.y, L);
+      acc.x = fmaf(v.x, w, acc.x);
+      acc.y = fmaf(v.y, w, acc.y);
+      acc.z = fmaf(v.z, w, acc.z);
+      acc.w = fmaf(v.w, w, acc.w);
     }
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   const float inv = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) dst[e] = __float2bfloat16_rn(acc[e] * inv);
+  *reinterpret_cast<uint2*>(kv8_out_row(a, b, hk, r) + 4 * c4) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 template <int HD, int MT>
@@ -557,7 +558,8 @@ cudaError_t launch_kv8_attention_mma(const Kv8AttnArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, cudaStream_t st) {
-  const dim3 grid(cdiv((int64_t)a.B * a.Hq * a.C, 8)), block(256);
+  const int64_t per = ((int64_t)a.prows * (a.hd / 4) + 31) / 32;
+  const dim3 grid(cdiv((int64_t)a.B * a.units * per, 8)), block(256);
   switch (a.hd) {
     case 32: return launch_pdl(kv8_merge_kernel<32>, grid, block, 0, st, a);
     case 64: return launch_pdl(kv8_merge_kernel<64>, grid, block, 0, st, a);

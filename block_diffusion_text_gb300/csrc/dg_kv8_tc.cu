@@ -118,13 +118,13 @@ struct Piece {
 DG_DEV Piece piece_at(const Kv8AttnArgs& a, long long w, long long w1) {
   const Kv8Seq sq = kv8_locate(a, w);
   const int per = a.units / a.Hkv;
-  const int unit = (int)((w - sq.first) / sq.nt);
+  const int unit = (int)kv8_div(w - sq.first, sq.nt);
   Piece p;
   p.b = sq.b;
   p.hk = unit / per;
   p.row0 = unit % per * 256;
   p.len = sq.len;
-  p.t0 = (int)((w - sq.first) % sq.nt);
+  p.t0 = (int)(w - sq.first - (long long)unit * sq.nt);
   p.t1 = (int)min((long long)sq.nt, p.t0 + (w1 - w));
   p.nt = sq.nt;
   p.ntc = (sq.len + kTK - 1) / kTK;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || !(ok = wait(&pvdone[t], (J + n - 1) & 1, status, abort))) break;
       tc_fence_after();
       const bool whole = p.t0 == 0 && p.t1 == p.nt;
-      const size_t prow = ((size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1)) * 256 + 128 * t + r;
+      const size_t slot = (size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1);
       const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
       __nv_bfloat16* orow = valid_row ? kv8_out_row(a, p.b, p.hk, ridx) : nullptr;
 #pragma unroll 1
@@ -505,12 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[q] = make_uint4(pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv), pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
                                 pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv), pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
         } else {
-          float4* dst = reinterpret_cast<float4*>(a.part + prow * kHD + 32 * c);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          for (int q = 0; q < 8; ++q)
+            *kv8_part(a, slot, 8 * c + q, 128 * t + r) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           if (c == 0)
-            *reinterpret_cast<float2*>(a.ml + prow * 2) =
-                make_float2(m_run == -INFINITY ? m_run : m_run - kHeadroom, l_run);
+            a.ml[slot * a.prows + 128 * t + r] = make_float2(m_run == -INFINITY ? m_run : m_run - kHeadroom, l_run);
         }
       }
       J += n;
