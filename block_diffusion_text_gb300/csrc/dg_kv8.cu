@@ -236,7 +236,7 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   w.rows = w.tc ? 256 : kv8_mma_rows(c->hd, R);
   w.tk = w.tc ? 128 : kKv8Block;
   w.workers = w.tc ? kKv8Ctas : kKv8Ctas * kKv8Warps;
-  w.units = (int)(c->Hkv * ((R + w.rows - 1) / w.rows));
+  w.units = (int)(c->Hkv * ((R + w.rows - 1) / w.rows));  // at most 65535 * 64 by the checks before
   w.prows = (int)(R < w.rows ? R : w.rows);
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -266,6 +266,11 @@ dg_status check_kv8_attention(const dg_kv8_cache* c, int C, int Hq) {
   if (C <= 0 || Hq <= 0 || Hq % c->Hkv != 0) return DG_ERR_ARG;
   // the bounds the denoising step and dg_attention_noalloc apply
   if (C > 1024 || (int64_t)c->B * C > (1 << 20) || (int64_t)c->B * Hq > 65535) return DG_ERR_SHAPE;
+  // tiles, and warps of the merge, are counted in 32 bits
+  const Kv8Ws w = kv8_ws(c, C, Hq);
+  const int64_t tiles = (int64_t)c->B * w.units * (cdiv(c->cap, w.tk) + cdiv(C, w.tk));
+  const int64_t warps = (int64_t)c->B * w.units * cdiv((int64_t)w.prows * c->hd, 128);
+  if (tiles > INT32_MAX - 65536 || warps > INT32_MAX - 65536) return DG_ERR_SHAPE;
   return DG_OK;
 }
 

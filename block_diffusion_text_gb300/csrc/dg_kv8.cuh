@@ -45,7 +45,7 @@ struct Kv8AttnArgs {
 struct Kv8Seq {
   int b, len;                // sequence and its cached rows
   int nt;                    // tiles of each of its units
-  long long first;           // first tile (in the call's order) of its first unit
+  int first;                 // first tile (in the call's order) of its first unit
 };
 
 DG_DEV int kv8_len(const Kv8AttnArgs& a, int b) {
@@ -55,45 +55,38 @@ DG_DEV int kv8_len(const Kv8AttnArgs& a, int b) {
 DG_DEV int kv8_tiles(const Kv8AttnArgs& a, int len) {
   return (len + a.tk - 1) / a.tk + (a.kn ? (a.C + a.tk - 1) / a.tk : 0);
 }
-// a / b for a, b >= 0 (b > 0): the 64-bit division of the hardware's 32-bit one
-// costs some hundred cycles, and a call's tiles hardly ever need it.
-DG_DEV long long kv8_div(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
-  return a / b;
-}
 // Four columns (4 c4 ..) of row r of a part: consecutive rows lie side by side,
 // so that the kernels that hold a row in a thread write whole lines, and the
 // merge reads a part from end to end.
 DG_DEV float4* kv8_part(const Kv8AttnArgs& a, size_t slot, int c4, int r) {
   return reinterpret_cast<float4*>(a.part) + (slot * (a.hd / 4) + c4) * a.prows + r;
 }
-// Tiles of the whole call (every lane of the calling warp gets the sum).
-DG_DEV long long kv8_total(const Kv8AttnArgs& a) {
+// Tiles of the whole call, below 2^31 - 2^16 by the entry point's check (every lane of the calling warp gets the sum).
+DG_DEV int kv8_total(const Kv8AttnArgs& a) {
   const int lane = threadIdx.x & 31;
-  long long n = 0;
-  for (int b = lane; b < a.B; b += 32) n += (long long)kv8_tiles(a, kv8_len(a, b)) * a.units;
+  int n = 0;
+  for (int b = lane; b < a.B; b += 32) n += kv8_tiles(a, kv8_len(a, b)) * a.units;
 #pragma unroll
   for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n;
 }
-DG_DEV long long kv8_share(const Kv8AttnArgs& a, long long total) {
-  const long long s = kv8_div(total + a.workers - 1, a.workers);
-  return s > 1 ? s : 1;
+DG_DEV int kv8_share(const Kv8AttnArgs& a, int total) {
+  return max((total + a.workers - 1) / a.workers, 1);
 }
 // The sequence that tile w of the call belongs to (w below the total; every
 // lane of the calling warp gets the answer).
-DG_DEV Kv8Seq kv8_locate(const Kv8AttnArgs& a, long long w) {
+DG_DEV Kv8Seq kv8_locate(const Kv8AttnArgs& a, int w) {
   const int lane = threadIdx.x & 31;
-  long long base = 0;
+  int base = 0;
   Kv8Seq p{0, 0, 1, 0};
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
     const int len = b < a.B ? kv8_len(a, b) : 0;
     const int nt = b < a.B ? kv8_tiles(a, len) : 0;
-    long long incl = (long long)nt * a.units;
+    int incl = nt * a.units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, w < base + incl);
@@ -102,7 +95,7 @@ DG_DEV Kv8Seq kv8_locate(const Kv8AttnArgs& a, long long w) {
       p.b = b0 + src;
       p.len = __shfl_sync(0xffffffffu, len, src);
       p.nt = __shfl_sync(0xffffffffu, nt, src);
-      p.first = __shfl_sync(0xffffffffu, base + incl - (long long)nt * a.units, src);
+      p.first = __shfl_sync(0xffffffffu, base + incl - nt * a.units, src);
       return p;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);

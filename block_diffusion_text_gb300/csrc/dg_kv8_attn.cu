@@ -148,14 +148,14 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
     for (int b = lane; b < a.B; b += 32)
       if (a.len[b] < 0 || a.len[b] > a.cap) atomicExch(a.status, kStatusCapacity);
   }
-  const long long total = kv8_total(a), share = kv8_share(a, total);
-  const long long w1 = min(total, (worker + 1) * share);
+  const int total = kv8_total(a), share = kv8_share(a, total);
+  const int w1 = (int)min((long long)total, (worker + 1ll) * share);
   const int grp_rows = a.Hq / a.Hkv * a.C, row_tiles = a.units / a.Hkv;
 
-  for (long long w = worker * share; w < w1;) {
+  for (int w = (int)min((long long)w1, (long long)worker * share); w < w1;) {
     const Kv8Seq sq = kv8_locate(a, w);
-    const int unit = (int)kv8_div(w - sq.first, sq.nt), t0 = (int)(w - sq.first - (long long)unit * sq.nt);
-    const int t1 = (int)min((long long)sq.nt, t0 + (w1 - w));
+    const int unit = (w - sq.first) / sq.nt, t0 = w - sq.first - unit * sq.nt;
+    const int t1 = min(sq.nt, t0 + (w1 - w));
     const int hk = unit / row_tiles, row0 = unit % row_tiles * (16 * MT);
     const int ntc = (sq.len + kKv8Block - 1) / kKv8Block;
     const int tc1 = min(t1, ntc);  // cached tiles of the piece end here
@@ -483,22 +483,21 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(Kv8AttnArgs a) {
   const int lane = threadIdx.x % 32;
   const int grp_rows = a.Hq / a.Hkv * a.C;
   const int per = (a.prows * C4 + 31) / 32;  // warps per unit
-  const long long wid = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  const long long all = kv8_div(wid, per);
-  const int b = (int)kv8_div(all, a.units), unit = (int)(all - (long long)b * a.units);
+  const unsigned wid = blockIdx.x * 8 + threadIdx.x / 32, all = wid / per;
+  const int b = (int)(all / a.units), unit = (int)(all - (unsigned)b * a.units);
   if (b >= a.B) return;
   const int item = (int)(wid - all * per) * 32 + lane;
   const int row_tiles = a.units / a.Hkv, hk = unit / row_tiles;
   const int c4 = item / a.prows, rr = item - c4 * a.prows, r = unit % row_tiles * a.rows + rr;
   const bool mine = c4 < C4 && r < grp_rows;
   const int nt = kv8_tiles(a, kv8_len(a, b));
-  const long long total = kv8_total(a), share = kv8_share(a, total);
-  long long first = 0;
-  for (int i = lane; i < b; i += 32) first += (long long)kv8_tiles(a, kv8_len(a, i)) * a.units;
+  const int total = kv8_total(a), share = kv8_share(a, total);
+  int first = 0;
+  for (int i = lane; i < b; i += 32) first += kv8_tiles(a, kv8_len(a, i)) * a.units;
 #pragma unroll
   for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-  first += (long long)unit * nt;
-  const int c0 = (int)kv8_div(first, share), c1 = (int)kv8_div(first + max(nt, 1) - 1, share);
+  first += unit * nt;
+  const int c0 = first / share, c1 = (first + max(nt, 1) - 1) / share;
   pdl_wait();
   if (!mine || (nt > 0 && c0 == c1)) return;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -115,17 +115,17 @@ struct Piece {
   DG_DEV int tiles() const { return t1 - t0; }
   DG_DEV bool fresh(int j) const { return t0 + j >= ntc; }  // tile j of the piece holds new tokens
 };
-DG_DEV Piece piece_at(const Kv8AttnArgs& a, long long w, long long w1) {
+DG_DEV Piece piece_at(const Kv8AttnArgs& a, int w, int w1) {
   const Kv8Seq sq = kv8_locate(a, w);
   const int per = a.units / a.Hkv;
-  const int unit = (int)kv8_div(w - sq.first, sq.nt);
+  const int unit = (w - sq.first) / sq.nt;
   Piece p;
   p.b = sq.b;
   p.hk = unit / per;
   p.row0 = unit % per * 256;
   p.len = sq.len;
-  p.t0 = (int)(w - sq.first - (long long)unit * sq.nt);
-  p.t1 = (int)min((long long)sq.nt, p.t0 + (w1 - w));
+  p.t0 = w - sq.first - unit * sq.nt;
+  p.t1 = min(sq.nt, p.t0 + (w1 - w));
   p.nt = sq.nt;
   p.ntc = (sq.len + kTK - 1) / kTK;
   return p;
@@ -153,29 +153,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pready = sfull + 2;      // [2 tiles][2 halves]
   uint64_t* pvdone = pready + 4;     // [2]
   uint64_t* ofree = pvdone + 2;      // [2] the piece's output has been read from TMEM
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ofree + 2);
+  uint64_t* turn = ofree + 2;        // [2] row tile t's MMA warp may issue
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* status = a.status;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
+    mbar_init(qempty, 2);
     for (int s = 0; s < kNK; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+      mbar_init(&kempty[s], 2);
     }
     for (int s = 0; s < kNV; ++s) {
       mbar_init(&cfull[s], 1);
       mbar_init(&cempty[s], 4);
       mbar_init(&vfull[s], 4);
-      mbar_init(&vempty[s], 1);
+      mbar_init(&vempty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
       mbar_init(&pready[2 * t], 4);
       mbar_init(&pready[2 * t + 1], 4);
       mbar_init(&pvdone[t], 1);
+      mbar_init(&turn[t], 1);
       mbar_init(&ofree[t], 4);
     }
     *abort = 0;
@@ -191,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
-  const long long total = kv8_total(a), share = kv8_share(a, total);
-  const long long w0 = blockIdx.x * share, w1 = min(total, w0 + share);
+  const int total = kv8_total(a), share = kv8_share(a, total);
+  const int w0 = min(total, (int)blockIdx.x * share), w1 = min(total, w0 + share);
   const int grp_rows = a.Hq / a.Hkv * a.C;
 
   if (warp < 4) {
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bool ok = true;
       int kslot = 0, kpar = 1, J = 0, np = 0;  // slot counters run on through the pieces
-      for (long long w = w0; w < w1 && ok; ++np) {
+      for (int w = w0; w < w1 && ok; ++np) {
         const Piece p = piece_at(a, w, w1);
         if (lane == 0) {
           const int bh = p.b * a.Hkv + p.hk;
@@ -252,20 +254,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         w += p.tiles();
       }
-    } else if (warp == 1) {
+    } else if (warp < 3) {
+      const int t = warp - 1;
       constexpr uint32_t idS = idesc_e4m3(128, kTK);
       constexpr uint32_t idPV = idesc_f16(128, kHD, true);
-      // The whole warp waits, one lane issues.  Descriptors differ in their low
-      // word alone (address / 16); nothing here is indexed dynamically, so that
-      // the issue never waits on local memory.
-      const uint32_t lo_q = desc_lo(smem_u32(smem), 16), lo_k = desc_lo(smem_u32(smem + Smem::oK), 16);
+      const uint32_t lo_q = desc_lo(smem_u32(smem + 2 * t * Smem::kQ), 16), lo_k = desc_lo(smem_u32(smem + Smem::oK), 16);
       const uint32_t lo_v = desc_lo(smem_u32(smem + Smem::oVf), Smem::kBox);
+      const uint32_t tS = tmem + 128 * t, tO = tmem + kColO + 128 * t;
       bool ok = true;
-      int kslot = 0, kpar = 0, J = 0, np = 0;
-      for (long long w = w0; w < w1 && ok; ++np) {
+      int kslot = 0, kpar = 0, J = 0, np = 0, step = 0;
+      for (int w = w0; w < w1 && ok; ++np) {
         const Piece p = piece_at(a, w, w1);
         const int n = p.tiles(), jfresh = p.ntc - p.t0;  // tiles from jfresh on hold new tokens
-        int ka = 0, kb = 0;                              // K slots of the tile whose S is being issued
+        int ka = 0, kb = 0;                              // K slots of tile j + 1
         auto wait_k = [&](int& k) -> bool {
           k = kslot;
           const bool r = wait(&kfull[kslot], kpar, status, abort);
@@ -276,47 +277,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           return r;
         };
         ok = wait(qfull, np & 1, status, abort);
-        // Step j: for each row tile P V of key tile j, then S of tile j + 1.  One
-        // copy of the code, with no unrolling past an operand tile: the warp
-        // runs through it once in some thousand cycles, between the softmax
-        // warps' code, and pays for every line that it has to fetch again.
+        // Step j: P_t V of key tile j, then S_t of tile j + 1.  The two warps take
+        // turns, step by step, which keeps the row tiles' softmax phases apart
+        // (left alone they fall into step, and the tensor core idles while both
+        // wait); each does its waiting and committing during the other's turn.
+        // A commit covers all MMAs of its thread before it, so S_t of tile j + 1
+        // also says that P_t V of tile j is done.
 #pragma unroll 1
-        for (int j = -1; j < n && ok; ++j) {
+        for (int j = -1; j < n && ok; ++j, ++step) {
           const int s = (J + j) & 1;
           const bool next = j + 1 < n, fresh = j + 1 >= jfresh;
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t) {
-            if (j >= 0) {
-              if (t == 0 && !(ok = wait(&vfull[s], ((J + j) / kNV) & 1, status, abort))) break;
-              if (j == 0 && np > 0 && !(ok = wait(&ofree[t], (np - 1) & 1, status, abort))) break;
-              const uint32_t d = tmem + kColO + 128 * t;
-              uint32_t v = lo_v + s * (Smem::kF16 >> 4), pt = tmem + 128 * t;
-#pragma unroll 1
-              for (int hf = 0; hf < 2; ++hf, v += (kTK / 32) * (2048 >> 4), pt += kTK / 4) {
-                if (!(ok = wait(&pready[2 * t + hf], (J + j) & 1, status, abort))) break;
-                tc_fence_after();
+          if (next && !(ok = wait_k(ka) && (!fresh || wait_k(kb)))) break;
+          if (j >= 0) {
+            if (!(ok = wait(&vfull[s], ((J + j) / kNV) & 1, status, abort))) break;
+            if (j == 0 && np > 0 && !(ok = wait(&ofree[t], (np - 1) & 1, status, abort))) break;
+            if (!(ok = wait(&pready[2 * t], (J + j) & 1, status, abort))) break;
+          }
+          if (!(ok = wait(&turn[t], (step & 1) ^ 1 ^ t, status, abort))) break;
+          tc_fence_after();
+          if (j >= 0) {
+            const uint32_t v = lo_v + s * (Smem::kF16 >> 4);
 #pragma unroll
-                for (int k4 = 0; k4 < kTK / 32; ++k4)
-                  mma_pv(d, pt + 8 * k4, desc64(v + k4 * (2048 >> 4)), idPV, (j | hf | k4) ? 1u : 0u);
-              }
-              if (!ok) break;
-              commit(&pvdone[t]);
-              if (t == 1) commit(&vempty[s]);
-            }
-            if (next) {
-              if (t == 0 && !(ok = wait_k(ka) && (!fresh || wait_k(kb)))) break;
-              tc_fence_after();
-              uint32_t k = lo_k + ka * (Smem::kK >> 4);
+            for (int k4 = 0; k4 < kTK / 32; ++k4)
+              mma_pv(tO, tS + 8 * k4, desc64(v + k4 * (2048 >> 4)), idPV, (j | k4) ? 1u : 0u);
+            if (!(ok = wait(&pready[2 * t + 1], (J + j) & 1, status, abort))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k4 = kTK / 32; k4 < kTK / 16; ++k4)
+              mma_pv(tO, tS + 8 * k4, desc64(v + k4 * (2048 >> 4)), idPV, 1u);
+          }
+          if (next) {
+            uint32_t k = lo_k + ka * (Smem::kK >> 4);
 #pragma unroll 1
-              for (int term = 0; term <= (fresh ? 1 : 0); ++term, k = lo_k + kb * (Smem::kK >> 4))
-                s_terms(tmem + 128 * t, lo_q + t * (2 * Smem::kQ >> 4), k, idS, term);
-              commit(&sfull[t]);
-              if (t == 1) {
-                commit(&kempty[ka]);
-                if (fresh) commit(&kempty[kb]);
-                if (j + 2 == n) commit(qempty);
-              }
-            }
+            for (int term = 0; term <= (fresh ? 1 : 0); ++term, k = lo_k + kb * (Smem::kK >> 4)) s_terms(tS, lo_q, k, idS, term);
+          }
+          if (lane == 0) mbar_arrive(&turn[t ^ 1]);
+          commit(next ? &sfull[t] : &pvdone[t]);
+          if (j >= 0) commit(&vempty[s]);
+          if (next) {
+            commit(&kempty[ka]);
+            if (fresh) commit(&kempty[kb]);
+            if (j + 2 == n) commit(qempty);
           }
         }
         J += n;
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x - 128;
     bool ok = true;
     int J = 0;
-    for (long long w = w0; w < w1 && ok;) {
+    for (int w = w0; w < w1 && ok;) {
       const Piece p = piece_at(a, w, w1);
       for (int j = 0; j < p.tiles(); ++j, ++J) {
         const int s = J % kNV, par = (J / kNV) & 1;
@@ -366,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + kColO + 128 * t;
     bool ok = true;
-    int J = 0;
-    for (long long w = w0; w < w1 && ok;) {
+    int J = 0, np = 0;
+    for (int w = w0; w < w1 && ok; ++np) {
       const Piece p = piece_at(a, w, w1);
       const int n = p.tiles(), bh = p.b * a.Hkv + p.hk;
       const int ridx = p.row0 + 128 * t + r;
@@ -433,9 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const bool need = mx > m_run + kLazy;
           if (__any_sync(0xffffffffu, need)) {
-            // O_t must hold P_t V of tile j - 1 before it is rescaled
-            if (!(ok = wait(&pvdone[t], (J + j - 1) & 1, status, abort))) break;
-            tc_fence_after();
             const float corr = need ? ex2_approx(m_run - mx) : 1.0f;
 #pragma unroll 1
             for (int c = 0; c < kHD / 16; ++c) {
@@ -482,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run = fmaf(x0 + x1, pow2i(-ve), l_run);
         }
       }
-      if (!ok || !(ok = wait(&pvdone[t], (J + n - 1) & 1, status, abort))) break;
+      if (!ok || !(ok = wait(&pvdone[t], np & 1, status, abort))) break;
       tc_fence_after();
       const bool whole = p.t0 == 0 && p.t1 == p.nt;
       const size_t slot = (size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1);
