@@ -222,10 +222,12 @@ dg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DG_OK : DG_ERR_CU
 
 int kv8_blocks(int cap) { return cdiv(cap, kKv8Block); }
 
+constexpr int kLocalTiles = 64;
+
 struct Kv8Ws {
   size_t part, ml, qterms, qexp, kterms, vf16, kexp, vexp, total;
   int rows, tk, units, workers, prows, Cp;
-  bool tc;
+  bool tc, local;
 };
 
 // The kernel, its rows per unit, and the workspace of an attention call.
@@ -244,6 +246,10 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
     off = align_up(off + bytes, 256);
     return o;
   };
+  // A short cache's units are finished by one CTA each: no parts in memory, no
+  // merge kernel.
+  w.local = !w.tc && cdiv(c->cap, w.tk) + cdiv(C, w.tk) <= kLocalTiles;
+  if (w.local) return w;
   w.part = take((size_t)2 * w.workers * w.prows * c->hd * 4);
   w.ml = take((size_t)2 * w.workers * w.prows * 8);
   if (w.tc) {
@@ -330,11 +336,11 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
                                       void* stream) {
   dg_status s = check_kv8_attention(cache, C, Hq);
   if (s) return s;
-  if (!q || !o || !k != !v || !ws) return DG_ERR_ARG;
+  if (!q || !o || !k != !v) return DG_ERR_ARG;
   if (!aligned16(q) || !aligned16(o) || !aligned16(k) || !aligned16(v)) return DG_ERR_ARG;
-  if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return DG_ERR_WORKSPACE;
   const Kv8Ws w = kv8_ws(cache, C, Hq);
-  if (ws_bytes < w.total) return DG_ERR_WORKSPACE;
+  if (w.total > 0 && !ws) return DG_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < w.total) return DG_ERR_WORKSPACE;
   uint8_t* base = static_cast<uint8_t*>(ws);
   Kv8AttnArgs a{};
   a.q = q;
@@ -362,6 +368,7 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   a.units = w.units;
   a.workers = w.workers;
   a.prows = w.prows;
+  a.local = w.local;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (w.tc) {
@@ -371,6 +378,6 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   } else {
     e = launch_kv8_attention_mma(a, st);
   }
-  if (e == cudaSuccess) e = launch_kv8_merge(a, st);
+  if (e == cudaSuccess && !w.local) e = launch_kv8_merge(a, st);
   return from_cuda(e);
 }

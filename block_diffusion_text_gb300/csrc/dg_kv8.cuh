@@ -33,6 +33,7 @@ struct Kv8AttnArgs {
   int rows, tk, units;       // rows per unit, keys per tile, units per sequence (Hkv * row tiles)
   int workers;               // warps or CTAs that the tiles are dealt to
   int prows;                 // rows of a part: min(rows, G C)
+  int local;                 // warp-MMA kernel: one CTA per unit, its warps' parts merged in shared memory
 };
 
 // All tiles of a call, in the order (sequence, unit, tile), are dealt to the

@@ -39,7 +39,8 @@ struct Ring {
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kStages = HD == 128 ? 3 : HD == 64 ? 6 : 8;
   static constexpr int kWarp = kStages * kStage;
-  static constexpr int kSmem = kKv8Warps * kWarp;
+  static constexpr int oMl = kKv8Warps * kWarp;  // float2 [warps][32 rows]
+  static constexpr int kSmem = oMl + kKv8Warps * 32 * 8;
 };
 
 // 16-byte chunk c of row r of a step lies at chunk c ^ swz(r): the fragment
@@ -148,14 +149,31 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
     for (int b = lane; b < a.B; b += 32)
       if (a.len[b] < 0 || a.len[b] > a.cap) atomicExch(a.status, kStatusCapacity);
   }
-  const int total = kv8_total(a), share = kv8_share(a, total);
-  const int w1 = (int)min((long long)total, (worker + 1ll) * share);
+  int w = blockIdx.x, w1 = w + 1;  // local: the CTA's unit
+  if (!a.local) {
+    const int total = kv8_total(a), share = kv8_share(a, total);
+    w1 = (int)min((long long)total, (worker + 1ll) * share);
+    w = (int)min((long long)w1, (long long)worker * share);
+  }
   const int grp_rows = a.Hq / a.Hkv * a.C, row_tiles = a.units / a.Hkv;
 
-  for (int w = (int)min((long long)w1, (long long)worker * share); w < w1;) {
-    const Kv8Seq sq = kv8_locate(a, w);
-    const int unit = (w - sq.first) / sq.nt, t0 = w - sq.first - unit * sq.nt;
-    const int t1 = min(sq.nt, t0 + (w1 - w));
+  while (w < w1) {
+    Kv8Seq sq;
+    int unit, t0, t1;
+    if (a.local) {
+      sq.b = w / a.units;
+      sq.len = kv8_len(a, sq.b);
+      sq.nt = kv8_tiles(a, sq.len);
+      unit = w - sq.b * a.units;
+      const int chunk = (sq.nt + kKv8Warps - 1) / kKv8Warps;
+      t0 = min(warp * chunk, sq.nt);
+      t1 = min(t0 + chunk, sq.nt);
+    } else {
+      sq = kv8_locate(a, w);
+      unit = (w - sq.first) / sq.nt;
+      t0 = w - sq.first - unit * sq.nt;
+      t1 = min(sq.nt, t0 + (w1 - w));
+    }
     const int hk = unit / row_tiles, row0 = unit % row_tiles * (16 * MT);
     const int ntc = (sq.len + kKv8Block - 1) / kKv8Block;
     const int tc1 = min(t1, ntc);  // cached tiles of the piece end here
@@ -431,6 +449,54 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
       }
     }
 
+    if (a.local) {
+      // every warp's output and (maximum, sum) to its own ring, then all
+      // threads merge: four columns of a row each
+      float* mine = reinterpret_cast<float*>(ring);
+      float2* ml = reinterpret_cast<float2*>(smem + R::oMl);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          float l = acc.l[mt][hr];
+          l += __shfl_xor_sync(0xffffffffu, l, 1);
+          l += __shfl_xor_sync(0xffffffffu, l, 2);
+          const int r = mt * 16 + hr * 8 + g;
+          if (t == 0) ml[warp * 32 + r] = make_float2(acc.m[mt][hr], l);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int n = 0; n < NV; n += 4)
+              *reinterpret_cast<float4*>(mine + r * HD + (2 * t + e) * NV + n) =
+                  make_float4(acc.o[mt][n][2 * hr + e], acc.o[mt][n + 1][2 * hr + e], acc.o[mt][n + 2][2 * hr + e],
+                              acc.o[mt][n + 3][2 * hr + e]);
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.prows * (HD / 4); i += 32 * kKv8Warps) {
+        const int r = i / (HD / 4), c4 = i % (HD / 4);
+        if (row0 + r >= grp_rows) break;
+        float M = -INFINITY, L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kKv8Warps; ++k) M = fmaxf(M, ml[k * 32 + r].x);
+#pragma unroll
+        for (int k = 0; k < kKv8Warps; ++k) {
+          const float2 p = ml[k * 32 + r];
+          const float wk = p.x == -INFINITY ? 0.f : ex2_approx(p.x - M);
+          const float4 x = *reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4);
+          L = fmaf(wk, p.y, L);
+          v.x = fmaf(wk, x.x, v.x);
+          v.y = fmaf(wk, x.y, v.y);
+          v.z = fmaf(wk, x.z, v.z);
+          v.w = fmaf(wk, x.w, v.w);
+        }
+        const float inv = L == 0.f ? 0.f : 1.0f / L;
+        *reinterpret_cast<uint2*>(kv8_out_row(a, sq.b, hk, row0 + r) + 4 * c4) =
+            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+      }
+      return;
+    }
     // Output, or a part of it: lane (g, t) holds columns 2 t NV .. + 2 NV of rows g and g + 8.
     const bool whole = t0 == 0 && t1 == sq.nt;
     const size_t slot = (size_t)worker * 2 + (t0 > 0 ? 0 : 1);
@@ -537,7 +603,7 @@ template <int HD, int MT>
 cudaError_t run_mma(const Kv8AttnArgs& a, cudaStream_t st) {
   cudaError_t e = set_smem_once<kv8_attn_kernel<HD, MT>>(Ring<HD>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_attn_kernel<HD, MT>, dim3(kKv8Ctas), dim3(32 * kKv8Warps), Ring<HD>::kSmem, st, a,
+  return launch_pdl(kv8_attn_kernel<HD, MT>, dim3(a.local ? a.B * a.units : kKv8Ctas), dim3(32 * kKv8Warps), Ring<HD>::kSmem, st, a,
                     1.4426950408889634f / sqrtf((float)HD));
 }
 

@@ -501,7 +501,7 @@ class Kv8Cache:
         self.device = K.device
         self.s = dg_kv8_cache(*[t.data_ptr() for t in (K, V, K_exp, V_exp, len, status)], B, Hkv, cap, hd)
         self._ref = ct.byref(self.s)
-        self._ws_bytes = {}
+        self._ws_bytes, self._ws = {}, {}
 
     @classmethod
     def empty(cls, B, Hkv, cap, hd, device="cuda"):
@@ -526,6 +526,24 @@ class Kv8Cache:
             _check(load().dg_kv8_attention_workspace(self._ref, C, Hq, ct.byref(z)), "dg_kv8_attention_workspace")
             n = self._ws_bytes[(C, Hq)] = z.value
         return n
+
+    def _workspace(self, C, Hq, st, stream):
+        """(pointer, bytes) of a workspace for a call on the stream with handle st.
+
+        One per stream, kept: the calls of a stream run one after another.  Under graph capture one from the
+        graph's own pool, so that graphs that overlap share none."""
+        n = self.workspace_bytes(C, Hq)
+        if n == 0:
+            return None, 0
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._workspace(C, Hq, st, None)
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(n, dtype=torch.uint8, device=self.device).data_ptr(), n
+        t = self._ws.get(st)
+        if t is None or t.numel() < n:
+            t = self._ws[st] = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return t.data_ptr(), n
 
     def _rows(self, t, heads, n, what):
         if t.dtype != torch.bfloat16 or t.shape != (self.B, heads, n, self.hd) or t.device != self.device \
@@ -585,28 +603,33 @@ def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = Non
     """Attention of C new tokens over the cached rows and their own k, v (dg_kv8_attention); o [B*C, Hq*hd].
 
     q: bf16 [B, Hq, C, hd]; k, v: bf16 [B, Hkv, C, hd], or None for the cached rows alone.  ws: optional uint8
-    workspace of cache.workspace_bytes(C, Hq) bytes, not shared by calls that may overlap; by default one from
-    torch's allocator on the launching stream."""
+    workspace of cache.workspace_bytes(C, Hq) bytes, not shared by calls that may overlap; by default the cache keeps
+    one for each stream, and a captured call takes one from the graph's pool."""
     if q.dim() != 4:
         raise ValueError("q: bf16 [B, Hq, C, hd]")
-    Hq, C = q.shape[1], q.shape[2]
+    _, Hq, C, _ = q.shape
     cache._rows(q, Hq, C, "q")
     _need((k is None) == (v is None), "k and v come together")
+    kp = vp = None
     if k is not None:
         cache._rows(k, cache.Hkv, C, "k")
         cache._rows(v, cache.Hkv, C, "v")
+        kp, vp = k.data_ptr(), v.data_ptr()
     st = cache._launch_stream(stream)
-    nbytes = cache.workspace_bytes(C, Hq)
-    if out is None or ws is None:
-        with torch.cuda.stream(stream):  # memory of the launching stream (a no-op for None)
-            if out is None:
-                out = torch.empty(cache.B * C, Hq * cache.hd, dtype=torch.bfloat16, device=cache.device)
-            if ws is None:
-                ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
-    _need(out.dtype == torch.bfloat16 and out.shape == (cache.B * C, Hq * cache.hd) and out.is_contiguous()
-          and out.device == cache.device, f"out: contiguous bf16 [{cache.B * C}, {Hq * cache.hd}]")
-    _need(ws.device == cache.device and ws.is_contiguous(), "ws: contiguous, on the cache's device")
-    _check(load().dg_kv8_attention(cache._ref, q.data_ptr(), None if k is None else k.data_ptr(),
-                                   None if v is None else v.data_ptr(), out.data_ptr(), C, Hq, int(causal),
-                                   ws.data_ptr(), ws.numel() * ws.element_size(), st), "dg_kv8_attention")
+    if ws is None:
+        wp, wn = cache._workspace(C, Hq, st, stream)
+    else:
+        _need(ws.device == cache.device and ws.is_contiguous(), "ws: contiguous, on the cache's device")
+        wp, wn = ws.data_ptr(), ws.numel() * ws.element_size()
+    shape = (cache.B * C, Hq * cache.hd)
+    if out is not None:
+        _need(out.dtype == torch.bfloat16 and out.shape == shape and out.is_contiguous() and out.device == cache.device,
+              f"out: contiguous bf16 {list(shape)}")
+    elif stream is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    else:
+        with torch.cuda.stream(stream):
+            out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    _check(load().dg_kv8_attention(cache._ref, q.data_ptr(), kp, vp, out.data_ptr(), C, Hq, 1 if causal else 0, wp, wn, st),
+           "dg_kv8_attention")
     return out

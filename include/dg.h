@@ -453,9 +453,9 @@ DG_API dg_status dg_kv8_read(const dg_kv8_cache* cache, int32_t row0, int32_t n,
  * work is divided by keys, not by sequences); a row without any key is zero.
  * k and v must be finite, the ones a causal mask hides included; what lies
  * behind len is never used.  Bounds as dg_attention_noalloc: C <= 1024,
- * B * C <= 2^20, B * Hq <= 65535.  ws: dg_kv8_attention_workspace bytes, 256-byte
- * aligned, contents of no matter; calls (and graphs) that may overlap on the
- * GPU need one each.                                                         */
+ * B * C <= 2^20, B * Hq <= 65535.  ws: dg_kv8_attention_workspace bytes (0 for a
+ * short cache: ws may be NULL then), 256-byte aligned, contents of no matter;
+ * calls (and graphs) that may overlap on the GPU need one each.              */
 DG_API dg_status dg_kv8_attention_workspace(const dg_kv8_cache* cache, int32_t C, int32_t Hq, size_t* bytes);
 DG_API dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, const void* k, const void* v, void* o,
                                   int32_t C, int32_t Hq, int32_t causal, void* ws, size_t ws_bytes, void* stream);

@@ -218,6 +218,11 @@ CASES = [
     (2, 256, 2, 2, 128, [640, 1], False, False),
     (1, 1000, 2, 2, 128, [130], True, True),
     (1, 200, 3, 1, 64, [777], True, True),
+    # caches long enough that a sequence's keys are shared out over many warps
+    (3, 1, 8, 2, 64, [5000, 0, 4200], True, True),
+    (2, 17, 2, 1, 32, [4500, 100], False, True),
+    (4, 1, 4, 4, 128, [6000, 1, 0, 3333], False, False),
+    (2, 9, 2, 2, 64, [4097, 4096], True, True),
 ]
 
 
