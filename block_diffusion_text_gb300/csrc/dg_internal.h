@@ -84,9 +84,9 @@ cudaError_t set_smem_once(int bytes) {
 }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (bf16, or
-// with u8 set 8-bit codes; 128-byte swizzle).
+// with u8 set 8-bit codes; swizzle over 128, 64 or 32 bytes).
 bool make_tmap_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
-                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, bool u8 = false);
+                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, bool u8 = false, int swizzle = 128);
 
 // ------------------------------------------------------------- launchers --
 struct StopCtl {

@@ -237,7 +237,7 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   w.tc = c->hd == 128 && R > 16;
   w.rows = w.tc ? 256 : kv8_mma_rows(c->hd, R);
   w.tk = w.tc ? 128 : kKv8Block;
-  w.workers = w.tc ? kKv8Ctas : kKv8Ctas * kKv8Warps;
+  w.workers = w.tc ? kKv8Ctas : kKv8Ctas * kv8_mma_warps(c->hd, w.rows);
   w.units = (int)(c->Hkv * ((R + w.rows - 1) / w.rows));  // at most 65535 * 64 by the checks before
   w.prows = (int)(R < w.rows ? R : w.rows);
   size_t off = 0;

@@ -11,7 +11,9 @@ constexpr int kKv8Block = 64;             // cached tokens per scale
 constexpr int kKv8Bias = 127;             // exponent byte x: scale 2^(x - 127)
 constexpr int kKv8Emin = -64, kKv8Emax = 118;
 constexpr int kKv8Ctas = kTargetCtas;     // CTAs of an attention launch (one per SM)
-constexpr int kKv8Warps = 8;              // workers per CTA of the warp-MMA kernel
+// Warps (workers) per CTA of the warp-MMA kernel for units of `rows` rows: as
+// many as their registers allow.
+constexpr int kv8_mma_warps(int hd, int rows) { return rows * hd <= 1024 ? 12 : 8; }
 constexpr int kStatusArg = 1, kStatusCapacity = 3;  // DG_ERR_ARG, DG_ERR_CAPACITY
 
 // One attention call.  A unit is one row tile of one (sequence, kv head): the
@@ -123,11 +125,50 @@ DG_DEV uint32_t e4m3x2_f16x2(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)codes));
   return r;
 }
+// Four codes as four f16: the low two in lo, the high two in hi.
+DG_DEV void e4m3x4_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
 // Two floats as E4M3 codes (low byte: lo), nearest even, saturating at 448.
 DG_DEV uint32_t pack_e4m3(float lo, float hi) {
   unsigned short r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Two E4M3 terms of eight scaled values.
+DG_DEV void split8(const float (&x)[8], uint2& hi, uint2& lo) {
+  uint32_t h[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t c0 = pack_e4m3(x[4 * i], x[4 * i + 1]), c1 = pack_e4m3(x[4 * i + 2], x[4 * i + 3]);
+    const uint32_t w0 = e4m3x2_f16x2(c0), w1 = e4m3x2_f16x2(c1);
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w0));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w1));
+    h[i] = c0 | (c1 << 16);
+    l[i] = pack_e4m3(x[4 * i] - f0.x, x[4 * i + 1] - f0.y) |
+           (pack_e4m3(x[4 * i + 2] - f1.x, x[4 * i + 3] - f1.y) << 16);
+  }
+  hi = make_uint2(h[0], h[1]);
+  lo = make_uint2(l[0], l[1]);
+}
+DG_DEV void unpack8(const uint4& w, float f, float (&x)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16) * f;
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * f;
+  }
+}
+DG_DEV unsigned abs_top(const uint4& w) {
+  return __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+}
+// Exponent that brings a largest magnitude (bf16 bits) into (224, 448].
+DG_DEV int top_exponent(unsigned bits) {
+  const int E = (int)(bits >> 7), m = (int)(bits & 127u);
+  return E == 0 ? kKv8Emin : min(max(E - 127 - 8 + (m > 96 ? 1 : 0), kKv8Emin), kKv8Emax);
 }
 
 // The forms of queries and new tokens that the tensor-core kernel reads, made

@@ -2,16 +2,23 @@
 // tokens, short canvases, head dims 32 and 64), and the merge of the parts.
 //
 // A warp is a worker: it streams its share of key tiles through a ring of its
-// own in shared memory (cp.async, no barrier shared with other warps) and
-// keeps queries, running maximum and sum, and the output of 16 MT rows in
-// registers.  Work for single tokens is bound by the bytes of the cache, so
-// what counts is loads in flight (24 KB a warp) and few instructions per code:
+// own in shared memory (TMA, no barrier shared with other warps) and keeps
+// queries, running maximum and sum, and the output of 8 NT rows in registers.
+// Work for single tokens is bound by the bytes of the cache, so what counts is
+// loads in flight, warps to cover each other's latencies, and few instructions
+// per code:
+//  - Both products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so that
+//    keys and output columns fill the 16 rows of mma.sync m16n8k16 and the
+//    query rows its 8 columns: one token's group of up to 8 heads costs half
+//    the MMAs, registers and exponentials of the untransposed form.
 //  - The codes go from shared memory into the MMA fragments in one conversion
 //    (two E4M3 to two f16, exact).  The fragments' index maps make that
 //    possible: the sum over the head dim may run in any order, so lane t of a
 //    quad owns the contiguous quarter t of a key row; the output columns may
 //    be dealt in any order, so lane group g owns the contiguous eighth g of a
-//    value row.
+//    value row.  (E4M3 MMAs of this shape would spare the conversion of the
+//    keys; with operands that change they took longer, 36 against 14 cycles
+//    each in this loop, measured.)
 //  - Block scales never touch the codes.  The key scale joins the softmax
 //    factor; the value scale 2^e joins the exponent of the probability,
 //    p' = 2^(s + e - m), so that P' V sums codes, with m the running maximum of
@@ -32,91 +39,126 @@ namespace {
 constexpr float kHeadroom = 8.0f;  // p' of a row's maximum is 2^8 ..
 constexpr float kLazy = 4.0f;      // .. to 2^12: the maximum is followed when it grows by more than 2^4
 constexpr int kStep = 32;          // keys per step
+constexpr int kMT = kStep / 16;    // their m-tiles
 
-template <int HD>
+// W warps with a ring of kStages steps each.
+template <int HD, int W>
 struct Ring {
   static constexpr int kHalf = kStep * HD;     // codes of K (or V) of one step
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = HD == 128 ? 3 : HD == 64 ? 6 : 8;
+  static constexpr int kStages = (W == 8 ? 24576 : 16384) / kStage;
   static constexpr int kWarp = kStages * kStage;
-  static constexpr int oMl = kKv8Warps * kWarp;  // float2 [warps][32 rows]
-  static constexpr int kSmem = oMl + kKv8Warps * 32 * 8;
+  static constexpr int oMl = W * kWarp;           // float2 [warps][32 rows]
+  static constexpr int oBar = oMl + W * 32 * 8;   // mbarriers [warps][stages]
+  static constexpr int kSmem = oBar + W * kStages * 8 + 16;
 };
 
-// 16-byte chunk c of row r of a step lies at chunk c ^ swz(r): the fragment
-// reads of eight lanes then fall into eight different bank groups (hd 128).
+// 16-byte chunk c of row r of a step lies at chunk c ^ swz(r), the swizzle of
+// the TMA copies over hd bytes: the fragment reads of eight lanes then fall
+// into eight different bank groups (hd 128).
 template <int HD>
 DG_DEV int swz(int r) {
   return HD == 128 ? (r & 7) : HD == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
 }
 
-template <int HD, int MT>
+// The MMAs without the order that volatile asm keeps: the scheduler may move
+// conversions and independent products between dependent ones.
+DG_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+DG_DEV void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8x8 matrix of 16-bit elements transposed across the warp: an accumulator
+// fragment's rows become the columns of a B fragment.
+DG_DEV uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// Bounded wait of a whole warp, one try first and the loops out of line.
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  return mbar_wait_warp(bar, parity, status, abort);
+}
+DG_DEV bool wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_more(bar, parity, status, abort);
+}
+
+// Rows 2t and 2t + 1 of each n-tile; o: columns g HD / 8 + 2 i (elements 0, 1)
+// and + 2 i + 1 (elements 2, 3).
+template <int HD, int NT>
 struct Acc {
-  float o[MT][HD / 8][4];
-  float m[MT][2], l[MT][2];
+  float o[NT][HD / 16][4];
+  float m[NT][2], l[NT][2];
 };
 
-// One step's scores to probabilities: s (raw products; rows g and g + 8 of
-// each m-tile, keys nt * 8 + 2t, + 1) become p' = 2^(s c + ev - m + headroom).
-template <int HD, int MT>
-DG_DEV void softmax_step(float (&s)[MT][kStep / 8][4], const float (&c)[MT][2], float ev, float inv_ev,
-                         Acc<HD, MT>& acc) {
-  float mx[MT][2];
+// One step's scores to probabilities: s (raw products; keys 16 mt + g and + 8,
+// rows 2t and 2t + 1 of each n-tile) become p' = 2^(s c + ev - m + headroom).
+template <int HD, int NT>
+DG_DEV void softmax_step(float (&s)[kMT][NT][4], const float (&c)[NT][2], float ev, float inv_ev, Acc<HD, NT>& acc) {
+  float mx[NT][2];
   bool need = false;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      float v = -INFINITY;
+    for (int e = 0; e < 2; ++e) {
+      float v = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
 #pragma unroll
-      for (int nt = 0; nt < kStep / 8; ++nt) v = fmaxf(v, fmaxf(s[mt][nt][2 * hr], s[mt][nt][2 * hr + 1]));
-      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-      mx[mt][hr] = fmaf(v, c[mt][hr], ev);
-      need |= mx[mt][hr] > acc.m[mt][hr] + kLazy;
+      for (int mt = 1; mt < kMT; ++mt) v = fmax3(v, s[mt][nt][e], s[mt][nt][2 + e]);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+      mx[nt][e] = fmaf(v, c[nt][e], ev);
+      need |= mx[nt][e] > acc.m[nt][e] + kLazy;
     }
   }
   if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) {
+      float corr[2];
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const float mn = fmaxf(mx[mt][hr], acc.m[mt][hr]);
-        const float corr = mn > acc.m[mt][hr] ? ex2_approx(acc.m[mt][hr] - mn) : 1.0f;
-        acc.m[mt][hr] = mn;
-        acc.l[mt][hr] *= corr;
-#pragma unroll
-        for (int n = 0; n < HD / 8; ++n) {
-          acc.o[mt][n][2 * hr] *= corr;
-          acc.o[mt][n][2 * hr + 1] *= corr;
-        }
+      for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(mx[nt][e], acc.m[nt][e]);
+        corr[e] = mn > acc.m[nt][e] ? ex2_approx(acc.m[nt][e] - mn) : 1.0f;
+        acc.m[nt][e] = mn;
+        acc.l[nt][e] *= corr[e];
       }
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc.o[nt][i][k] *= corr[k & 1];
     }
   }
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      const float m = acc.m[mt][hr];
+    for (int e = 0; e < 2; ++e) {
+      const float m = acc.m[nt][e];
       const float off = ev - (m == -INFINITY ? 0.0f : m - kHeadroom);
       float sum = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < kStep / 8; ++nt) {
+      for (int mt = 0; mt < kMT; ++mt) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float p = ex2_approx(fmaf(s[mt][nt][2 * hr + e], c[mt][hr], off));
-          s[mt][nt][2 * hr + e] = p;
+        for (int h = 0; h < 2; ++h) {
+          const float p = ex2_approx(fmaf(s[mt][nt][2 * h + e], c[nt][e], off));
+          s[mt][nt][2 * h + e] = p;
           sum += p;
         }
       }
-      acc.l[mt][hr] = fmaf(sum, inv_ev, acc.l[mt][hr]);
+      acc.l[nt][e] = fmaf(sum, inv_ev, acc.l[nt][e]);
     }
   }
 }
 
-// Words of the fragment slices: NB bytes from shared memory at p.
+// NB bytes of a fragment slice from shared memory.
 template <int NB>
-DG_DEV void lds(uint32_t (&w)[NB / 4], const uint8_t* p) {
+DG_DEV void lds(uint32_t* w, const uint8_t* p) {
   if constexpr (NB == 4) {
     w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else if constexpr (NB == 8) {
@@ -132,18 +174,36 @@ DG_DEV void lds(uint32_t (&w)[NB / 4], const uint8_t* p) {
   }
 }
 
-template <int HD, int MT>
-__global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs a, float scale_log2) {
-  pdl_wait();
-  pdl_trigger();  // the merge waits for this kernel's completion all the same
-  using R = Ring<HD>;
+template <int HD, int NT, int W>
+__global__ void __launch_bounds__(32 * W, 1)
+    kv8_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, Kv8AttnArgs a,
+                    float scale_log2) {
+  using R = Ring<HD, W>;
   constexpr int SL = HD / 4;   // elements of a key row per quad lane
-  constexpr int KS = HD / 16;  // k16 steps of Q K^T
-  constexpr int NV = HD / 8;   // n-tiles of P V; columns per lane group
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int KS = HD / 16;  // k16 steps of K Q^T, m-tiles of V^T P^T
+  constexpr int NV = HD / 8;   // columns of a value row per lane group
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0) {  // uniform over the CTA
+    if (threadIdx.x == 0) atomicExch(a.status, kStatusTimeout);
+    return;
+  }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   uint8_t* ring = smem + warp * R::kWarp;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::oBar) + warp * R::kStages;
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + R::oBar + W * R::kStages * 8);
   const int worker = warp * gridDim.x + blockIdx.x;  // consecutive shares on different SMs
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    tma_prefetch(&mK);
+    tma_prefetch(&mV);
+  }
+  if (lane == 0) {
+    for (int i = 0; i < R::kStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();  // the merge waits for this kernel's completion all the same
 
   if (worker == 0) {
     for (int b = lane; b < a.B; b += 32)
@@ -156,8 +216,10 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
     w = (int)min((long long)w1, (long long)worker * share);
   }
   const int grp_rows = a.Hq / a.Hkv * a.C, row_tiles = a.units / a.Hkv;
+  int slot = 0, par = 0;  // the ring's stage to read next, and its barrier's parity
+  bool ok = true;
 
-  while (w < w1) {
+  while (w < w1 && ok) {
     Kv8Seq sq;
     int unit, t0, t1;
     if (a.local) {
@@ -165,7 +227,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
       sq.len = kv8_len(a, sq.b);
       sq.nt = kv8_tiles(a, sq.len);
       unit = w - sq.b * a.units;
-      const int chunk = (sq.nt + kKv8Warps - 1) / kKv8Warps;
+      const int chunk = (sq.nt + W - 1) / W;
       t0 = min(warp * chunk, sq.nt);
       t1 = min(t0 + chunk, sq.nt);
     } else {
@@ -174,86 +236,75 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
       t0 = w - sq.first - unit * sq.nt;
       t1 = min(sq.nt, t0 + (w1 - w));
     }
-    const int hk = unit / row_tiles, row0 = unit % row_tiles * (16 * MT);
+    const int hk = unit / row_tiles, row0 = unit % row_tiles * (8 * NT);
     const int ntc = (sq.len + kKv8Block - 1) / kKv8Block;
     const int tc1 = min(t1, ntc);  // cached tiles of the piece end here
     const size_t bh = (size_t)sq.b * a.Hkv + hk;
-    const uint8_t* Kg = a.K + bh * a.cap * HD;
-    const uint8_t* Vg = a.V + bh * a.cap * HD;
     const uint8_t* Ke = a.Ke + bh * a.nblk;
     const uint8_t* Ve = a.Ve + bh * a.nblk;
     const int nsteps = max(tc1 - t0, 0) * (kKv8Block / kStep);
 
-    // Step i of the piece into its stage.  Rows past the sequence's end are
-    // filled with zeros: what lies behind it never enters an MMA.
-    auto issue = [&](int i) {
-      if (i < nsteps) {
-        const int key0 = t0 * kKv8Block + i * kStep;
-        const int valid = sq.len - key0;
-        uint8_t* dst = ring + (i % R::kStages) * R::kStage;
-        constexpr int CPR = HD / 16;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint8_t* src = (kv ? Vg : Kg) + (size_t)key0 * HD;
-#pragma unroll
-          for (int p = 0; p < kStep * CPR / 32; ++p) {
-            const int idx = p * 32 + lane, r = idx / CPR, c = idx % CPR;
-            const bool there = r < valid;
-            cp_async16(dst + kv * R::kHalf + r * HD + ((c ^ swz<HD>(r)) * 16), there ? src + r * HD + c * 16 : Kg,
-                       there);
-          }
-        }
+    // Step i of the piece into the ring, `ahead` stages past the one to read next.
+    auto issue = [&](int i, int ahead) {
+      if (i < nsteps && lane == 0) {
+        int st = slot + ahead;
+        if (st >= R::kStages) st -= R::kStages;
+        uint8_t* dst = ring + st * R::kStage;
+        const int row = (int)bh * a.cap + t0 * kKv8Block + i * kStep;
+        mbar_arrive_expect_tx(&full[st], R::kStage);
+        tma_load_2d(dst, &mK, &full[st], 0, row);
+        tma_load_2d(dst + R::kHalf, &mV, &full[st], 0, row);
       }
-      cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < R::kStages - 1; ++i) issue(i);
+    for (int i = 0; i < R::kStages; ++i) issue(i, i);
 
-    // Queries: rows g and g + 8 of each m-tile, elements t SL + 4 j .. + 3.
-    uint32_t qf[MT][KS][4];
-    int qi[MT][2];    // position of the row's token among the new ones
-    int qx[MT][2];
-    const __nv_bfloat16* qrow[MT][2];
+    // Queries: row g of each n-tile, elements t SL + 4 j .. + 3 of step j, as f16
+    // on the power-of-two scale of the row.
+    uint32_t qf[NT][KS][2];
+    int qx[NT][2];    // exponents of rows 2t and 2t + 1
+    int qi[NT][2];    // their tokens' positions among the new ones
+    const __nv_bfloat16* qrow[NT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g;
+      const bool there = r < grp_rows;
+      qrow[nt] = there ? reinterpret_cast<const __nv_bfloat16*>(a.q) + (bh * grp_rows + r) * HD + t * SL : nullptr;
+      uint2 raw[KS];
+      unsigned top = 0;
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const int r = row0 + mt * 16 + hr * 8 + g;
-        const bool there = r < grp_rows;
-        qi[mt][hr] = there ? r % a.C : 0;
-        qrow[mt][hr] = there ? reinterpret_cast<const __nv_bfloat16*>(a.q) + (bh * grp_rows + r) * HD + t * SL : nullptr;
-        uint2 raw[KS];
-        unsigned top = 0;
+      for (int j = 0; j < KS; ++j) {
+        raw[j] = there ? *reinterpret_cast<const uint2*>(qrow[nt] + 4 * j) : make_uint2(0, 0);
+        top = __vmaxu2(top, __vmaxu2(raw[j].x & 0x7fff7fffu, raw[j].y & 0x7fff7fffu));
+      }
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int x = top < 128 ? 0 : max((int)(top >> 7) - 127 - 13, -100);
+      const float f = pow2i(-x);
 #pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          raw[j] = there ? *reinterpret_cast<const uint2*>(qrow[mt][hr] + 4 * j) : make_uint2(0, 0);
-          top = __vmaxu2(top, __vmaxu2(raw[j].x & 0x7fff7fffu, raw[j].y & 0x7fff7fffu));
-        }
-        top = max(top & 0xffffu, top >> 16);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int x = top < 128 ? 0 : max((int)(top >> 7) - 127 - 13, -100);
-        qx[mt][hr] = x;
-        const float f = pow2i(-x);
+      for (int j = 0; j < KS; ++j) {
+        qf[nt][j][0] = pack_f16(__uint_as_float(raw[j].x << 16) * f, __uint_as_float(raw[j].x & 0xffff0000u) * f);
+        qf[nt][j][1] = pack_f16(__uint_as_float(raw[j].y << 16) * f, __uint_as_float(raw[j].y & 0xffff0000u) * f);
+      }
 #pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          qf[mt][j][hr] = pack_f16(__uint_as_float(raw[j].x << 16) * f, __uint_as_float(raw[j].x & 0xffff0000u) * f);
-          qf[mt][j][2 + hr] = pack_f16(__uint_as_float(raw[j].y << 16) * f, __uint_as_float(raw[j].y & 0xffff0000u) * f);
-        }
+      for (int e = 0; e < 2; ++e) {
+        qx[nt][e] = __shfl_sync(0xffffffffu, x, (2 * t + e) * 4);
+        qi[nt][e] = (row0 + nt * 8 + 2 * t + e) % a.C;
       }
     }
-    Acc<HD, MT> acc;
+    Acc<HD, NT> acc;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        acc.m[mt][hr] = -INFINITY;
-        acc.l[mt][hr] = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        acc.m[nt][e] = -INFINITY;
+        acc.l[nt][e] = 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < NV; ++n)
+      for (int i = 0; i < KS; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc.o[mt][n][e] = 0.f;
+        for (int k = 0; k < 4; ++k) acc.o[nt][i][k] = 0.f;
     }
 
     int ke_next = 0, ve_next = 0, ke = 0, ve = 0;
@@ -263,7 +314,6 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
     }
 #pragma unroll 1
     for (int i = 0; i < nsteps; ++i) {
-      issue(i + R::kStages - 1);
       if (i % (kKv8Block / kStep) == 0) {
         ke = ke_next - kKv8Bias;
         ve = ve_next - kKv8Bias;
@@ -273,97 +323,99 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
           ve_next = Ve[nx];
         }
       }
-      cp_async_wait<R::kStages - 1>();
-      __syncwarp();
+      if (!(ok = wait(&full[slot], par, a.status, abort))) break;
       const int valid = sq.len - (t0 * kKv8Block + i * kStep);
       if (valid > 0) {
-        const uint8_t* sk = ring + (i % R::kStages) * R::kStage;
+        const uint8_t* sk = ring + slot * R::kStage;
         const uint8_t* sv = sk + R::kHalf;
-        float s[MT][kStep / 8][4];
+        float s[kMT][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < kStep / 8; ++nt) {
-          const int r = nt * 8 + g;
-          uint32_t kw[SL / 4];
-          if constexpr (HD == 128) {
-            uint32_t h0[4], h1[4];
-            lds<16>(h0, sk + r * HD + (((2 * t) ^ swz<HD>(r)) * 16));
-            lds<16>(h1, sk + r * HD + (((2 * t + 1) ^ swz<HD>(r)) * 16));
+        for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              kw[j] = h0[j];
-              kw[4 + j] = h1[j];
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[mt][nt][k] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          uint32_t kw[2][SL / 4];  // keys 16 mt + g and + 8
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = 16 * mt + 8 * h + g;
+            if constexpr (HD == 128) {
+              lds<16>(&kw[h][0], sk + r * HD + (((2 * t) ^ swz<HD>(r)) * 16));
+              lds<16>(&kw[h][4], sk + r * HD + (((2 * t + 1) ^ swz<HD>(r)) * 16));
+            } else if constexpr (HD == 64) {
+              lds<16>(&kw[h][0], sk + r * HD + ((t ^ swz<HD>(r)) * 16));
+            } else {
+              lds<8>(&kw[h][0], sk + r * HD + (((t / 2) ^ swz<HD>(r)) * 16) + (t & 1) * 8);
             }
-          } else if constexpr (HD == 64) {
-            lds<16>(kw, sk + r * HD + ((t ^ swz<HD>(r)) * 16));
-          } else {
-            lds<8>(kw, sk + r * HD + (((t / 2) ^ swz<HD>(r)) * 16) + (t & 1) * 8);
           }
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
-#pragma unroll
           for (int j = 0; j < KS; ++j) {
-            const uint32_t b0 = e4m3x2_f16x2(kw[j]), b1 = e4m3x2_f16x2(kw[j] >> 16);
+            uint32_t ka[4];
+            e4m3x4_f16x4(kw[0][j], ka[0], ka[2]);
+            e4m3x4_f16x4(kw[1][j], ka[1], ka[3]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma_f16_16816(s[mt][nt], qf[mt][j], b0, b1);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(s[mt][nt], ka, qf[nt][j][0], qf[nt][j][1]);
           }
         }
         if (valid < kStep) {
 #pragma unroll
-          for (int nt = 0; nt < kStep / 8; ++nt)
+          for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (nt * 8 + 2 * t + (e & 1) >= valid) {
+            for (int k = 0; k < 4; ++k)
+              if (16 * mt + g + 8 * (k >> 1) >= valid) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) s[mt][nt][e] = -INFINITY;
+                for (int nt = 0; nt < NT; ++nt) s[mt][nt][k] = -INFINITY;
               }
         }
-        float c[MT][2];
+        float c[NT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int hr = 0; hr < 2; ++hr) c[mt][hr] = scale_log2 * pow2i(qx[mt][hr] + ke);
-        softmax_step<HD, MT>(s, c, (float)ve, pow2i(-ve), acc);
+          for (int e = 0; e < 2; ++e) c[nt][e] = scale_log2 * pow2i(qx[nt][e] + ke);
+        softmax_step<HD, NT>(s, c, (float)ve, pow2i(-ve), acc);
 #pragma unroll
-        for (int k2 = 0; k2 < kStep / 16; ++k2) {
-          uint32_t pa[MT][4];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            pa[mt][0] = pack_f16(s[mt][2 * k2][0], s[mt][2 * k2][1]);
-            pa[mt][1] = pack_f16(s[mt][2 * k2][2], s[mt][2 * k2][3]);
-            pa[mt][2] = pack_f16(s[mt][2 * k2 + 1][0], s[mt][2 * k2 + 1][1]);
-            pa[mt][3] = pack_f16(s[mt][2 * k2 + 1][2], s[mt][2 * k2 + 1][3]);
-          }
-          uint32_t vw[4][NV / 4];  // rows 2t, 2t + 1, 2t + 8, 2t + 9; the lane group's columns
+        for (int mt = 0; mt < kMT; ++mt) {
+          uint32_t vw[4][NV / 4];  // keys 2t, 2t + 1, 2t + 8, 2t + 9; the lane group's columns
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int r = 16 * k2 + 2 * t + (q & 1) + 8 * (q >> 1);
+            const int r = 16 * mt + 2 * t + (q & 1) + 8 * (q >> 1);
             if constexpr (HD == 128)
               lds<16>(vw[q], sv + r * HD + ((g ^ swz<HD>(r)) * 16));
             else if constexpr (HD == 64)
               lds<8>(vw[q], sv + r * HD + (((g / 2) ^ swz<HD>(r)) * 16) + (g & 1) * 8);
             else
               lds<4>(vw[q], sv + r * HD + (((g / 4) ^ swz<HD>(r)) * 16) + (g & 3) * 4);
+            if (valid < kStep && r >= valid) {  // what lies behind the sequence never enters an MMA
+#pragma unroll
+              for (int n = 0; n < NV / 4; ++n) vw[q][n] = 0;
+            }
+          }
+          uint32_t pb[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            pb[nt][0] = transpose8x8(pack_f16(s[mt][nt][0], s[mt][nt][1]));
+            pb[nt][1] = transpose8x8(pack_f16(s[mt][nt][2], s[mt][nt][3]));
           }
 #pragma unroll
-          for (int n = 0; n < NV; n += 2) {  // two n-tiles from one byte interleave of two rows
-            const uint32_t sel = (n & 2) ? 0x7362u : 0x5140u;
-            const uint32_t x0 = __byte_perm(vw[0][n / 4], vw[1][n / 4], sel);
-            const uint32_t x1 = __byte_perm(vw[2][n / 4], vw[3][n / 4], sel);
-            const uint32_t b00 = e4m3x2_f16x2(x0), b01 = e4m3x2_f16x2(x1);
-            const uint32_t b10 = e4m3x2_f16x2(x0 >> 16), b11 = e4m3x2_f16x2(x1 >> 16);
+          for (int i = 0; i < KS; ++i) {  // two columns of four keys from two byte interleaves
+            const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+            uint32_t va[4];
+            e4m3x4_f16x4(__byte_perm(vw[0][i / 2], vw[1][i / 2], sel), va[0], va[1]);
+            e4m3x4_f16x4(__byte_perm(vw[2][i / 2], vw[3][i / 2], sel), va[2], va[3]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma_f16_16816(acc.o[mt][n], pa[mt], b00, b01);
-              mma_f16_16816(acc.o[mt][n + 1], pa[mt], b10, b11);
-            }
+            for (int nt = 0; nt < NT; ++nt) mma_f16(acc.o[nt][i], va, pb[nt][0], pb[nt][1]);
           }
         }
       }
       __syncwarp();  // the stage may be filled again
+      issue(i + R::kStages, 0);
+      if (++slot == R::kStages) {
+        slot = 0;
+        par ^= 1;
+      }
     }
-    cp_async_wait<0>();
 
     // New tokens, in bf16, straight from global memory: a call has few of
     // them where this kernel is used.
@@ -372,118 +424,112 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
 #pragma unroll 1
     for (int key0 = (max(t0, ntc) - ntc) * kKv8Block, end = min((t1 - ntc) * kKv8Block, a.C); key0 < end;
          key0 += kStep) {
-      float s[MT][kStep / 8][4];
+      float s[kMT][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < kStep / 8; ++nt) {
-        const int key = key0 + nt * 8 + g;
-        uint2 kw[KS];
+      for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[mt][nt][k] = 0.f;
+        const int kg = key0 + 16 * mt + g;
 #pragma unroll
         for (int j = 0; j < KS; j += 2) {
-          const uint4 v = key < a.C ? *reinterpret_cast<const uint4*>(kn + (size_t)key * HD + t * SL + 4 * j)
-                                    : make_uint4(0, 0, 0, 0);
-          kw[j] = make_uint2(v.x, v.y);
-          kw[j + 1] = make_uint2(v.z, v.w);
-        }
+          uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0;
+          if (kg < a.C) k0 = *reinterpret_cast<const uint4*>(kn + (size_t)kg * HD + t * SL + 4 * j);
+          if (kg + 8 < a.C) k1 = *reinterpret_cast<const uint4*>(kn + (size_t)(kg + 8) * HD + t * SL + 4 * j);
+          const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint2 r0 = make_uint2(0, 0), r1 = r0;
-            if (qrow[mt][0]) r0 = *reinterpret_cast<const uint2*>(qrow[mt][0] + 4 * j);
-            if (qrow[mt][1]) r1 = *reinterpret_cast<const uint2*>(qrow[mt][1] + 4 * j);
-            const uint32_t qa[4] = {r0.x, r1.x, r0.y, r1.y};
-            mma_bf16_16816(s[mt][nt], qa, kw[j].x, kw[j].y);
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint4 qv = qrow[nt] ? *reinterpret_cast<const uint4*>(qrow[nt] + 4 * j) : make_uint4(0, 0, 0, 0);
+            mma_bf16(s[mt][nt], a0, qv.x, qv.y);
+            mma_bf16(s[mt][nt], a1, qv.z, qv.w);
           }
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int kk = key0 + nt * 8 + 2 * t + (e & 1);
-            if (kk >= a.C || (a.causal && kk > qi[mt][e >> 1])) s[mt][nt][e] = -INFINITY;
+          for (int k = 0; k < 4; ++k) {
+            const int kk = kg + 8 * (k >> 1);
+            if (kk >= a.C || (a.causal && kk > qi[nt][k & 1])) s[mt][nt][k] = -INFINITY;
           }
       }
-      float c[MT][2];
+      float c[NT][2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) c[mt][0] = c[mt][1] = scale_log2;
-      softmax_step<HD, MT>(s, c, 0.f, 1.f, acc);
+      for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = scale_log2;
+      softmax_step<HD, NT>(s, c, 0.f, 1.f, acc);
 #pragma unroll
-      for (int k2 = 0; k2 < kStep / 16; ++k2) {
-        uint32_t ph[MT][4], pl[MT][4];
+      for (int mt = 0; mt < kMT; ++mt) {
+        uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float p0 = s[mt][2 * k2 + (q >> 1)][2 * (q & 1)], p1 = s[mt][2 * k2 + (q >> 1)][2 * (q & 1) + 1];
-            ph[mt][q] = pack_bf16(p0, p1);
-            pl[mt][q] = pack_bf16(p0 - __uint_as_float(ph[mt][q] << 16),
-                                  p1 - __uint_as_float(ph[mt][q] & 0xffff0000u));
+          for (int h = 0; h < 2; ++h) {
+            const float p0 = s[mt][nt][2 * h], p1 = s[mt][nt][2 * h + 1];
+            const uint32_t hi = pack_bf16(p0, p1);
+            ph[nt][h] = transpose8x8(hi);
+            pl[nt][h] = transpose8x8(pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u)));
           }
         }
         const __nv_bfloat16* vr[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int key = key0 + 16 * k2 + 2 * t + (q & 1) + 8 * (q >> 1);
+          const int key = key0 + 16 * mt + 2 * t + (q & 1) + 8 * (q >> 1);
           vr[q] = key < a.C ? vn + (size_t)key * HD + g * NV : nullptr;
         }
 #pragma unroll
-        for (int n = 0; n < NV; n += 2) {
+        for (int i = 0; i < KS; ++i) {
           uint32_t vw[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) vw[q] = vr[q] ? *reinterpret_cast<const uint32_t*>(vr[q] + n) : 0u;
+          for (int q = 0; q < 4; ++q) vw[q] = vr[q] ? *reinterpret_cast<const uint32_t*>(vr[q] + 2 * i) : 0u;
+          const uint32_t va[4] = {__byte_perm(vw[0], vw[1], 0x5410u), __byte_perm(vw[0], vw[1], 0x7632u),
+                                  __byte_perm(vw[2], vw[3], 0x5410u), __byte_perm(vw[2], vw[3], 0x7632u)};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t sel = e ? 0x7632u : 0x5410u;
-            const uint32_t b0 = __byte_perm(vw[0], vw[1], sel), b1 = __byte_perm(vw[2], vw[3], sel);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma_bf16_16816(acc.o[mt][n + e], ph[mt], b0, b1);
-              mma_bf16_16816(acc.o[mt][n + e], pl[mt], b0, b1);
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16(acc.o[nt][i], va, ph[nt][0], ph[nt][1]);
+            mma_bf16(acc.o[nt][i], va, pl[nt][0], pl[nt][1]);
           }
         }
       }
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], o);
 
+    // four columns (4 k .. of the lane group's NV) of row 2t + e
+    auto out4 = [&](int nt, int e, int k) {
+      return make_float4(acc.o[nt][2 * k][e], acc.o[nt][2 * k][2 + e], acc.o[nt][2 * k + 1][e], acc.o[nt][2 * k + 1][2 + e]);
+    };
     if (a.local) {
-      // every warp's output and (maximum, sum) to its own ring, then all
-      // threads merge: four columns of a row each
+      // every warp's output and (maximum, sum) to shared memory, the output to
+      // its own ring; then all threads merge, four columns of a row each
       float* mine = reinterpret_cast<float*>(ring);
       float2* ml = reinterpret_cast<float2*>(smem + R::oMl);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          float l = acc.l[mt][hr];
-          l += __shfl_xor_sync(0xffffffffu, l, 1);
-          l += __shfl_xor_sync(0xffffffffu, l, 2);
-          const int r = mt * 16 + hr * 8 + g;
-          if (t == 0) ml[warp * 32 + r] = make_float2(acc.m[mt][hr], l);
+        for (int e = 0; e < 2; ++e) {
+          const int r = nt * 8 + 2 * t + e;
+          if (g == 0) ml[warp * 32 + r] = make_float2(acc.m[nt][e], acc.l[nt][e]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < NV; n += 4)
-              *reinterpret_cast<float4*>(mine + r * HD + (2 * t + e) * NV + n) =
-                  make_float4(acc.o[mt][n][2 * hr + e], acc.o[mt][n + 1][2 * hr + e], acc.o[mt][n + 2][2 * hr + e],
-                              acc.o[mt][n + 3][2 * hr + e]);
+          for (int k = 0; k < NV / 4; ++k) *reinterpret_cast<float4*>(mine + r * HD + g * NV + 4 * k) = out4(nt, e, k);
         }
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < a.prows * (HD / 4); i += 32 * kKv8Warps) {
+      if (*abort) break;
+      for (int i = threadIdx.x; i < a.prows * (HD / 4); i += 32 * W) {
         const int r = i / (HD / 4), c4 = i % (HD / 4);
         if (row0 + r >= grp_rows) break;
         float M = -INFINITY, L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kKv8Warps; ++k) M = fmaxf(M, ml[k * 32 + r].x);
+        for (int k = 0; k < W; ++k) M = fmaxf(M, ml[k * 32 + r].x);
 #pragma unroll
-        for (int k = 0; k < kKv8Warps; ++k) {
+        for (int k = 0; k < W; ++k) {
           const float2 p = ml[k * 32 + r];
-          const float wk = p.x == -INFINITY ? 0.f : ex2_approx(p.x - M);
+          const float wk = p.x == -INFINITY ? 0.f : exp2f(p.x - M);  // as the merge kernel
           const float4 x = *reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4);
           L = fmaf(wk, p.y, L);
           v.x = fmaf(wk, x.x, v.x);
@@ -495,44 +541,38 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) kv8_attn_kernel(Kv8AttnArgs
         *reinterpret_cast<uint2*>(kv8_out_row(a, sq.b, hk, row0 + r) + 4 * c4) =
             make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
       }
-      return;
+      break;
     }
-    // Output, or a part of it: lane (g, t) holds columns 2 t NV .. + 2 NV of rows g and g + 8.
+    if (!ok) break;
     const bool whole = t0 == 0 && t1 == sq.nt;
-    const size_t slot = (size_t)worker * 2 + (t0 > 0 ? 0 : 1);
+    const size_t part = (size_t)worker * 2 + (t0 > 0 ? 0 : 1);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        float l = acc.l[mt][hr];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int r = mt * 16 + hr * 8 + g;
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * t + e;
         if (row0 + r >= grp_rows) continue;
+        const float l = acc.l[nt][e];
         if (whole) {
           const float inv = l == 0.f ? 0.f : 1.0f / l;
-          uint32_t* dst = reinterpret_cast<uint32_t*>(kv8_out_row(a, sq.b, hk, row0 + r) + 2 * t * NV);
+          uint2* dst = reinterpret_cast<uint2*>(kv8_out_row(a, sq.b, hk, row0 + r) + g * NV);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < NV; n += 2)
-              dst[(e * NV + n) / 2] = pack_bf16(acc.o[mt][n][2 * hr + e] * inv, acc.o[mt][n + 1][2 * hr + e] * inv);
+          for (int k = 0; k < NV / 4; ++k) {
+            const float4 v = out4(nt, e, k);
+            dst[k] = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+          }
         } else {
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < NV; n += 4)
-              *kv8_part(a, slot, ((2 * t + e) * NV + n) / 4, r) =
-                  make_float4(acc.o[mt][n][2 * hr + e], acc.o[mt][n + 1][2 * hr + e], acc.o[mt][n + 2][2 * hr + e],
-                              acc.o[mt][n + 3][2 * hr + e]);
-          if (t == 0) {
-            const float m = acc.m[mt][hr];
-            a.ml[slot * a.prows + r] = make_float2(m == -INFINITY ? m : m - kHeadroom, l);
-          }
+          for (int k = 0; k < NV / 4; ++k) *kv8_part(a, part, (g * NV) / 4 + k, r) = out4(nt, e, k);
+          if (g == 0) a.ml[part * a.prows + r] = make_float2(acc.m[nt][e], l);
         }
       }
     }
     w += t1 - t0;
+  }
+  if (*abort) {  // copies in flight land before the CTA's shared memory goes
+    const uint64_t start = globaltimer();
+    while (globaltimer() - start < 2000000ull) __nanosleep(1000);
   }
 }
 
@@ -599,25 +639,40 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(Kv8AttnArgs a) {
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
-template <int HD, int MT>
+template <int HD, int NT>
 cudaError_t run_mma(const Kv8AttnArgs& a, cudaStream_t st) {
-  cudaError_t e = set_smem_once<kv8_attn_kernel<HD, MT>>(Ring<HD>::kSmem);
+  constexpr int W = kv8_mma_warps(HD, 8 * NT);
+  using R = Ring<HD, W>;
+  cudaError_t e = set_smem_once<kv8_attn_kernel<HD, NT, W>>(R::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_attn_kernel<HD, MT>, dim3(a.local ? a.B * a.units : kKv8Ctas), dim3(32 * kKv8Warps), Ring<HD>::kSmem, st, a,
-                    1.4426950408889634f / sqrtf((float)HD));
+  const uint64_t rows = (uint64_t)a.B * a.Hkv * a.cap;
+  CUtensorMap mK, mV;
+  if (!make_tmap_2d(&mK, a.K, HD, rows, HD, HD, kStep, true, HD) ||
+      !make_tmap_2d(&mV, a.V, HD, rows, HD, HD, kStep, true, HD))
+    return cudaErrorInvalidValue;
+  return launch_pdl(kv8_attn_kernel<HD, NT, W>, dim3(a.local ? a.B * a.units : kKv8Ctas), dim3(32 * W), R::kSmem, st, mK,
+                    mV, a, 1.4426950408889634f / sqrtf((float)HD));
+}
+
+template <int HD>
+cudaError_t run_rows(const Kv8AttnArgs& a, cudaStream_t st) {
+  if (a.rows == 8) return run_mma<HD, 1>(a, st);
+  if (a.rows == 16) return run_mma<HD, 2>(a, st);
+  if constexpr (HD < 128) return run_mma<HD, 4>(a, st);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-// 16 rows, or 32 where the registers hold them and there are more than 16:
-// the codes are then read and converted once for both row tiles.
-int kv8_mma_rows(int hd, int64_t R) { return hd == 128 || R <= 16 ? 16 : 32; }
+// As many rows as the registers hold: the codes are read and converted once for
+// all of a unit's rows.
+int kv8_mma_rows(int hd, int64_t R) { return R <= 8 ? 8 : R <= 16 || hd == 128 ? 16 : 32; }
 
 cudaError_t launch_kv8_attention_mma(const Kv8AttnArgs& a, cudaStream_t st) {
   switch (a.hd) {
-    case 32: return a.rows == 16 ? run_mma<32, 1>(a, st) : run_mma<32, 2>(a, st);
-    case 64: return a.rows == 16 ? run_mma<64, 1>(a, st) : run_mma<64, 2>(a, st);
-    case 128: return run_mma<128, 1>(a, st);
+    case 32: return run_rows<32>(a, st);
+    case 64: return run_rows<64>(a, st);
+    case 128: return run_rows<128>(a, st);
   }
   return cudaErrorInvalidValue;
 }

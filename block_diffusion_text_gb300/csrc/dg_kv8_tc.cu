@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 8; ++q)
             *kv8_part(a, slot, 8 * c + q, 128 * t + r) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           if (c == 0)
-            a.ml[slot * a.prows + 128 * t + r] = make_float2(m_run == -INFINITY ? m_run : m_run - kHeadroom, l_run);
+            a.ml[slot * a.prows + 128 * t + r] = make_float2(m_run, l_run);
         }
       }
       J += n;
@@ -526,39 +526,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------- prep --
-// Two E4M3 terms of eight scaled values.
-DG_DEV void split8(const float (&x)[8], uint2& hi, uint2& lo) {
-  uint32_t h[2], l[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t c0 = pack_e4m3(x[4 * i], x[4 * i + 1]), c1 = pack_e4m3(x[4 * i + 2], x[4 * i + 3]);
-    const uint32_t w0 = e4m3x2_f16x2(c0), w1 = e4m3x2_f16x2(c1);
-    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w0));
-    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w1));
-    h[i] = c0 | (c1 << 16);
-    l[i] = pack_e4m3(x[4 * i] - f0.x, x[4 * i + 1] - f0.y) |
-           (pack_e4m3(x[4 * i + 2] - f1.x, x[4 * i + 3] - f1.y) << 16);
-  }
-  hi = make_uint2(h[0], h[1]);
-  lo = make_uint2(l[0], l[1]);
-}
-DG_DEV void unpack8(const uint4& w, float f, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16) * f;
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * f;
-  }
-}
-DG_DEV unsigned abs_top(const uint4& w) {
-  return __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-}
-// Exponent that brings a largest magnitude (bf16 bits) into (224, 448].
-DG_DEV int top_exponent(unsigned bits) {
-  const int E = (int)(bits >> 7), m = (int)(bits & 127u);
-  return E == 0 ? kKv8Emin : min(max(E - 127 - 8 + (m > 96 ? 1 : 0), kKv8Emin), kKv8Emax);
-}
-
 // q to two E4M3 terms and a scale per row (16 lanes a row, 8 elements a lane);
 // new keys to two E4M3 terms and new values to f16, with a scale per 64 tokens
 // (one CTA per block, zeros behind the last token).
