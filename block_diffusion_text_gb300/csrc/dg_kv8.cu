@@ -272,11 +272,11 @@ dg_status check_kv8_attention(const dg_kv8_cache* c, int C, int Hq) {
   if (C <= 0 || Hq <= 0 || Hq % c->Hkv != 0) return DG_ERR_ARG;
   // the bounds the denoising step and dg_attention_noalloc apply
   if (C > 1024 || (int64_t)c->B * C > (1 << 20) || (int64_t)c->B * Hq > 65535) return DG_ERR_SHAPE;
-  // tiles, and warps of the merge, are counted in 32 bits
+  // tiles, and CTAs of the merge, are counted in 32 bits
   const Kv8Ws w = kv8_ws(c, C, Hq);
   const int64_t tiles = (int64_t)c->B * w.units * (cdiv(c->cap, w.tk) + cdiv(C, w.tk));
-  const int64_t warps = (int64_t)c->B * w.units * cdiv((int64_t)w.prows * c->hd, 128);
-  if (tiles > INT32_MAX - 65536 || warps > INT32_MAX - 65536) return DG_ERR_SHAPE;
+  const int64_t ctas = (int64_t)c->B * w.units * cdiv((int64_t)w.prows * c->hd, 128);
+  if (tiles > INT32_MAX - 65536 || ctas > INT32_MAX - 65536) return DG_ERR_SHAPE;
   return DG_OK;
 }
 

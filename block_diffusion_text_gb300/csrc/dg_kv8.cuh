@@ -64,27 +64,31 @@ DG_DEV int kv8_tiles(const Kv8AttnArgs& a, int len) {
 DG_DEV float4* kv8_part(const Kv8AttnArgs& a, size_t slot, int c4, int r) {
   return reinterpret_cast<float4*>(a.part) + (slot * (a.hd / 4) + c4) * a.prows + r;
 }
-// Tiles of the whole call, below 2^31 - 2^16 by the entry point's check (every lane of the calling warp gets the sum).
-DG_DEV int kv8_total(const Kv8AttnArgs& a) {
+// What a warp knows of the call's division: the lengths of the first 32
+// sequences, one in each lane (most calls have no more, and read them once).
+struct Kv8Plan {
+  int len;                   // of sequence `lane`
+  int total, share;          // tiles of the call (below 2^31 - 2^16 by the entry point's check), and of a worker
+};
+DG_DEV Kv8Plan kv8_plan(const Kv8AttnArgs& a) {
   const int lane = threadIdx.x & 31;
-  int n = 0;
-  for (int b = lane; b < a.B; b += 32) n += kv8_tiles(a, kv8_len(a, b)) * a.units;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
-}
-DG_DEV int kv8_share(const Kv8AttnArgs& a, int total) {
-  return max((total + a.workers - 1) / a.workers, 1);
+  Kv8Plan p;
+  p.len = lane < a.B ? kv8_len(a, lane) : 0;
+  int n = lane < a.B ? kv8_tiles(a, p.len) * a.units : 0;
+  for (int b = lane + 32; b < a.B; b += 32) n += kv8_tiles(a, kv8_len(a, b)) * a.units;
+  p.total = __reduce_add_sync(0xffffffffu, n);
+  p.share = max((p.total + a.workers - 1) / a.workers, 1);
+  return p;
 }
 // The sequence that tile w of the call belongs to (w below the total; every
 // lane of the calling warp gets the answer).
-DG_DEV Kv8Seq kv8_locate(const Kv8AttnArgs& a, int w) {
+DG_DEV Kv8Seq kv8_locate(const Kv8AttnArgs& a, const Kv8Plan& plan, int w) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   Kv8Seq p{0, 0, 1, 0};
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    const int len = b < a.B ? kv8_len(a, b) : 0;
+    const int len = b0 == 0 ? plan.len : b < a.B ? kv8_len(a, b) : 0;
     const int nt = b < a.B ? kv8_tiles(a, len) : 0;
     int incl = nt * a.units;
 #pragma unroll
@@ -184,6 +188,10 @@ struct Kv8Prep {
 
 // Rows per unit of the warp-MMA kernel for R query rows per kv head.
 int kv8_mma_rows(int hd, int64_t R);
+// Parts i = s mod kMergeSlices of a unit are summed by slice s of the merge, the
+// slices in order: one order of additions wherever the parts are merged.
+constexpr int kMergeSlices = 8;
+
 cudaError_t launch_kv8_attention_mma(const Kv8AttnArgs& a, cudaStream_t st);
 cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cudaStream_t st);
 cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, cudaStream_t st);

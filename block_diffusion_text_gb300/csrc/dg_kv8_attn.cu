@@ -156,6 +156,20 @@ DG_DEV void softmax_step(float (&s)[kMT][NT][4], const float (&c)[NT][2], float 
   }
 }
 
+// Parts of four output columns and the row sum, on the maximum M of all parts.
+struct Kv8Sum {
+  float l = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  DG_DEV void add(const float2& ml, float M, const float4& x) {
+    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+    l = fmaf(w, ml.y, l);
+    v.x = fmaf(w, x.x, v.x);
+    v.y = fmaf(w, x.y, v.y);
+    v.z = fmaf(w, x.z, v.z);
+    v.w = fmaf(w, x.w, v.w);
+  }
+};
+
 // NB bytes of a fragment slice from shared memory.
 template <int NB>
 DG_DEV void lds(uint32_t* w, const uint8_t* p) {
@@ -210,10 +224,11 @@ __global__ void __launch_bounds__(32 * W, 1)
       if (a.len[b] < 0 || a.len[b] > a.cap) atomicExch(a.status, kStatusCapacity);
   }
   int w = blockIdx.x, w1 = w + 1;  // local: the CTA's unit
+  Kv8Plan plan{};
   if (!a.local) {
-    const int total = kv8_total(a), share = kv8_share(a, total);
-    w1 = (int)min((long long)total, (worker + 1ll) * share);
-    w = (int)min((long long)w1, (long long)worker * share);
+    plan = kv8_plan(a);
+    w1 = (int)min((long long)plan.total, (worker + 1ll) * plan.share);
+    w = (int)min((long long)w1, (long long)worker * plan.share);
   }
   const int grp_rows = a.Hq / a.Hkv * a.C, row_tiles = a.units / a.Hkv;
   int slot = 0, par = 0;  // the ring's stage to read next, and its barrier's parity
@@ -231,7 +246,7 @@ __global__ void __launch_bounds__(32 * W, 1)
       t0 = min(warp * chunk, sq.nt);
       t1 = min(t0 + chunk, sq.nt);
     } else {
-      sq = kv8_locate(a, w);
+      sq = kv8_locate(a, plan, w);
       unit = (w - sq.first) / sq.nt;
       t0 = w - sq.first - unit * sq.nt;
       t1 = min(sq.nt, t0 + (w1 - w));
@@ -527,15 +542,16 @@ __global__ void __launch_bounds__(32 * W, 1)
 #pragma unroll
         for (int k = 0; k < W; ++k) M = fmaxf(M, ml[k * 32 + r].x);
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-          const float2 p = ml[k * 32 + r];
-          const float wk = p.x == -INFINITY ? 0.f : exp2f(p.x - M);  // as the merge kernel
-          const float4 x = *reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4);
-          L = fmaf(wk, p.y, L);
-          v.x = fmaf(wk, x.x, v.x);
-          v.y = fmaf(wk, x.y, v.y);
-          v.z = fmaf(wk, x.z, v.z);
-          v.w = fmaf(wk, x.w, v.w);
+        for (int sl = 0; sl < kMergeSlices; ++sl) {  // the merge kernel's order of additions
+          Kv8Sum s;
+#pragma unroll
+          for (int k = sl; k < W; k += kMergeSlices)
+            s.add(ml[k * 32 + r], M, *reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4));
+          L += s.l;
+          v.x += s.v.x;
+          v.y += s.v.y;
+          v.z += s.v.z;
+          v.w += s.v.w;
         }
         const float inv = L == 0.f ? 0.f : 1.0f / L;
         *reinterpret_cast<uint2*>(kv8_out_row(a, sq.b, hk, row0 + r) + 4 * c4) =
@@ -576,67 +592,84 @@ __global__ void __launch_bounds__(32 * W, 1)
   }
 }
 
-// Merge of the parts.  A thread makes four columns of one output row, a warp 32
-// consecutive float4 of a unit's parts; the shares' borders are recomputed, a
-// unit that one worker finished is already written, and one without any key
-// (an empty sequence without new tokens) gets zeros.  What it reads before
-// pdl_wait, the lengths, no kernel of the call writes, and the attention
-// kernel lets this one start only once it has itself waited for its
-// predecessors; they are read past the first-level cache.
-template <int HD>
-__global__ void __launch_bounds__(256) kv8_merge_kernel(Kv8AttnArgs a) {
+// Merge of the parts.  32 consecutive float4 of a unit's output, lane by lane,
+// are made by S warps that share the parts: S = 8 for single tokens, whose units
+// have some 50 parts of few rows (one warp alone would wait for them round by
+// round: 15 us for 4 sequences of 131072 rows), S = 1 for the 256-row units of
+// the tensor-core kernel, which have few parts and items enough.  The shares'
+// borders are recomputed; a unit that one worker finished is already written,
+// and one without any key (an empty sequence without new tokens) gets zeros.
+// What it reads before pdl_wait, the lengths, no kernel of the call writes, and
+// the attention kernel lets this one start only once it has itself waited for
+// its predecessors; they are read past the first-level cache.
+constexpr int kMergeWarps = 8;
+
+template <int HD, int S>
+__global__ void __launch_bounds__(32 * kMergeWarps) kv8_merge_kernel(Kv8AttnArgs a) {
   constexpr int C4 = HD / 4;
-  const int lane = threadIdx.x % 32;
+  __shared__ float top[S][32];
+  __shared__ Kv8Sum sums[S][32];
+  const int lane = threadIdx.x % 32, slice = threadIdx.x / 32 % S;
   const int grp_rows = a.Hq / a.Hkv * a.C;
-  const int per = (a.prows * C4 + 31) / 32;  // warps per unit
-  const unsigned wid = blockIdx.x * 8 + threadIdx.x / 32, all = wid / per;
+  const unsigned group = blockIdx.x * (kMergeWarps / S) + threadIdx.x / (32 * S);
+  const unsigned per = (a.prows * C4 + 31) / 32, all = group / per;  // groups of 32 per unit; the unit
   const int b = (int)(all / a.units), unit = (int)(all - (unsigned)b * a.units);
   if (b >= a.B) return;
-  const int item = (int)(wid - all * per) * 32 + lane;
+  const int item = (int)(group - all * per) * 32 + lane;
   const int row_tiles = a.units / a.Hkv, hk = unit / row_tiles;
   const int c4 = item / a.prows, rr = item - c4 * a.prows, r = unit % row_tiles * a.rows + rr;
   const bool mine = c4 < C4 && r < grp_rows;
   const int nt = kv8_tiles(a, kv8_len(a, b));
-  const int total = kv8_total(a), share = kv8_share(a, total);
+  const Kv8Plan plan = kv8_plan(a);
   int first = 0;
-  for (int i = lane; i < b; i += 32) first += kv8_tiles(a, kv8_len(a, i)) * a.units;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-  first += unit * nt;
-  const int c0 = first / share, c1 = (first + max(nt, 1) - 1) / share;
+  for (int i = lane; i < b; i += 32) first += kv8_tiles(a, i < 32 ? plan.len : kv8_len(a, i)) * a.units;
+  first = __reduce_add_sync(0xffffffffu, first) + unit * nt;
+  const int c0 = first / plan.share, n = (first + max(nt, 1) - 1) / plan.share - c0;
   pdl_wait();
-  if (!mine || (nt > 0 && c0 == c1)) return;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f;
+  if (nt > 0 && n == 0) return;  // uniform over the warps that meet below
+  // part 0 is the unit's beginning (slot 1 of its worker), the others slots 0
+  const size_t mstep = 2 * (size_t)a.prows, pstep = mstep * C4;
+  const float2* ml = a.ml + c0 * mstep + (mine ? rr : 0);
+  const float4* src = kv8_part(a, (size_t)c0 * 2, mine ? c4 : 0, mine ? rr : 0);
+  const size_t slot1 = a.prows;
+  float M = -INFINITY;
   if (nt > 0) {
-    // part 0 is the unit's beginning (slot 1 of its worker), the others slots 0
-    const float2* ml = a.ml + (size_t)c0 * 2 * a.prows + rr;
-    const float4* src = kv8_part(a, (size_t)c0 * 2, c4, rr);
-    const size_t mstep = 2 * (size_t)a.prows, pstep = mstep * C4;
-    const float2 ml0 = ml[a.prows];
-    const float4 v0 = src[(size_t)C4 * a.prows];
-    const int n = c1 - c0;
-    float M = ml0.x;
 #pragma unroll 4
-    for (int i = 1; i <= n; ++i) M = fmaxf(M, ml[i * mstep].x);
-    const float w0 = ml0.x == -INFINITY ? 0.f : exp2f(ml0.x - M);
-    L = w0 * ml0.y;
-    acc = make_float4(v0.x * w0, v0.y * w0, v0.z * w0, v0.w * w0);
-#pragma unroll 8
-    for (int i = 1; i <= n; ++i) {
-      const float2 p = ml[i * mstep];
-      const float4 v = src[i * pstep];
-      const float w = p.x == -INFINITY ? 0.f : exp2f(p.x - M);
-      L = fmaf(w, p.y, L);
-      acc.x = fmaf(v.x, w, acc.x);
-      acc.y = fmaf(v.y, w, acc.y);
-      acc.z = fmaf(v.z, w, acc.z);
-      acc.w = fmaf(v.w, w, acc.w);
+    for (int i = slice; i <= n; i += S) M = fmaxf(M, ml[i * mstep + (i ? 0 : slot1)].x);
+  }
+  if constexpr (S > 1) {
+    top[slice][lane] = M;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < S; ++k) M = fmaxf(M, top[k][lane]);
+  }
+  Kv8Sum s;
+  if (nt > 0) {
+#pragma unroll 4
+    for (int i = slice; i <= n; i += S)
+      s.add(ml[i * mstep + (i ? 0 : slot1)], M, src[i * pstep + (i ? 0 : slot1 * C4)]);
+  }
+  if constexpr (S > 1) {
+    sums[slice][lane] = s;
+    __syncthreads();
+    if (slice != 0) return;
+    s = Kv8Sum();
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const Kv8Sum& x = sums[k][lane];
+      s.l += x.l;
+      s.v.x += x.v.x;
+      s.v.y += x.v.y;
+      s.v.z += x.v.z;
+      s.v.w += x.v.w;
     }
   }
+  if (!mine) return;
+  const float L = s.l;
+  const float4 v = s.v;
   const float inv = L == 0.f ? 0.f : 1.0f / L;
   *reinterpret_cast<uint2*>(kv8_out_row(a, b, hk, r) + 4 * c4) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
 }
 
 template <int HD, int NT>
@@ -677,13 +710,20 @@ cudaError_t launch_kv8_attention_mma(const Kv8AttnArgs& a, cudaStream_t st) {
   return cudaErrorInvalidValue;
 }
 
+template <int HD>
+static cudaError_t run_merge(const Kv8AttnArgs& a, cudaStream_t st) {
+  const int64_t groups = (int64_t)a.B * a.units * (((int64_t)a.prows * (HD / 4) + 31) / 32);
+  if (a.rows == 256)
+    return launch_pdl(kv8_merge_kernel<HD, 1>, dim3(cdiv(groups, kMergeWarps)), dim3(32 * kMergeWarps), 0, st, a);
+  static_assert(kMergeSlices == kMergeWarps, "one group per CTA");
+  return launch_pdl(kv8_merge_kernel<HD, kMergeSlices>, dim3((unsigned)groups), dim3(32 * kMergeWarps), 0, st, a);
+}
+
 cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, cudaStream_t st) {
-  const int64_t per = ((int64_t)a.prows * (a.hd / 4) + 31) / 32;
-  const dim3 grid(cdiv((int64_t)a.B * a.units * per, 8)), block(256);
   switch (a.hd) {
-    case 32: return launch_pdl(kv8_merge_kernel<32>, grid, block, 0, st, a);
-    case 64: return launch_pdl(kv8_merge_kernel<64>, grid, block, 0, st, a);
-    case 128: return launch_pdl(kv8_merge_kernel<128>, grid, block, 0, st, a);
+    case 32: return run_merge<32>(a, st);
+    case 64: return run_merge<64>(a, st);
+    case 128: return run_merge<128>(a, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -115,8 +115,8 @@ struct Piece {
   DG_DEV int tiles() const { return t1 - t0; }
   DG_DEV bool fresh(int j) const { return t0 + j >= ntc; }  // tile j of the piece holds new tokens
 };
-DG_DEV Piece piece_at(const Kv8AttnArgs& a, int w, int w1) {
-  const Kv8Seq sq = kv8_locate(a, w);
+DG_DEV Piece piece_at(const Kv8AttnArgs& a, const Kv8Plan& plan, int w, int w1) {
+  const Kv8Seq sq = kv8_locate(a, plan, w);
   const int per = a.units / a.Hkv;
   const int unit = (w - sq.first) / sq.nt;
   Piece p;
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
-  const int total = kv8_total(a), share = kv8_share(a, total);
-  const int w0 = min(total, (int)blockIdx.x * share), w1 = min(total, w0 + share);
+  const Kv8Plan plan = kv8_plan(a);
+  const int w0 = min(plan.total, (int)blockIdx.x * plan.share), w1 = min(plan.total, w0 + plan.share);
   const int grp_rows = a.Hq / a.Hkv * a.C;
 
   if (warp < 4) {
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int kslot = 0, kpar = 1, J = 0, np = 0;  // slot counters run on through the pieces
       for (int w = w0; w < w1 && ok; ++np) {
-        const Piece p = piece_at(a, w, w1);
+        const Piece p = piece_at(a, plan, w, w1);
         if (lane == 0) {
           const int bh = p.b * a.Hkv + p.hk;
           ok = mbar_wait(qempty, (np & 1) ^ 1, status, abort);
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int kslot = 0, kpar = 0, J = 0, np = 0, step = 0;
       for (int w = w0; w < w1 && ok; ++np) {
-        const Piece p = piece_at(a, w, w1);
+        const Piece p = piece_at(a, plan, w, w1);
         const int n = p.tiles(), jfresh = p.ntc - p.t0;  // tiles from jfresh on hold new tokens
         int ka = 0, kb = 0;                              // K slots of tile j + 1
         auto wait_k = [&](int& k) -> bool {
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int J = 0;
     for (int w = w0; w < w1 && ok;) {
-      const Piece p = piece_at(a, w, w1);
+      const Piece p = piece_at(a, plan, w, w1);
       for (int j = 0; j < p.tiles(); ++j, ++J) {
         const int s = J % kNV, par = (J / kNV) & 1;
         if (!(ok = wait(&cfull[s], par, status, abort))) break;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int J = 0, np = 0;
     for (int w = w0; w < w1 && ok; ++np) {
-      const Piece p = piece_at(a, w, w1);
+      const Piece p = piece_at(a, plan, w, w1);
       const int n = p.tiles(), bh = p.b * a.Hkv + p.hk;
       const int ridx = p.row0 + 128 * t + r;
       const bool valid_row = ridx < grp_rows;
