@@ -223,6 +223,7 @@ dg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DG_OK : DG_ERR_CU
 int kv8_blocks(int cap) { return cdiv(cap, kKv8Block); }
 
 constexpr int kLocalTiles = 64;
+constexpr int kKv8Ovh = 3;  // measured: a unit's start and output take as long as some three tiles
 
 struct Kv8Ws {
   size_t part, ml, qterms, qexp, kterms, vf16, kexp, vexp, total;
@@ -274,7 +275,7 @@ dg_status check_kv8_attention(const dg_kv8_cache* c, int C, int Hq) {
   if (C > 1024 || (int64_t)c->B * C > (1 << 20) || (int64_t)c->B * Hq > 65535) return DG_ERR_SHAPE;
   // tiles, and CTAs of the merge, are counted in 32 bits
   const Kv8Ws w = kv8_ws(c, C, Hq);
-  const int64_t tiles = (int64_t)c->B * w.units * (cdiv(c->cap, w.tk) + cdiv(C, w.tk));
+  const int64_t tiles = (int64_t)c->B * w.units * (cdiv(c->cap, w.tk) + cdiv(C, w.tk) + kKv8Ovh);
   const int64_t ctas = (int64_t)c->B * w.units * cdiv((int64_t)w.prows * c->hd, 128);
   if (tiles > INT32_MAX - 65536 || ctas > INT32_MAX - 65536) return DG_ERR_SHAPE;
   return DG_OK;
@@ -367,6 +368,7 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   a.tk = w.tk;
   a.units = w.units;
   a.workers = w.workers;
+  a.ovh = kKv8Ovh;
   a.prows = w.prows;
   a.local = w.local;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

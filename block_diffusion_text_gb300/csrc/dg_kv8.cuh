@@ -34,21 +34,25 @@ struct Kv8AttnArgs {
   int causal;
   int rows, tk, units;       // rows per unit, keys per tile, units per sequence (Hkv * row tiles)
   int workers;               // warps or CTAs that the tiles are dealt to
+  int ovh;                   // what beginning a unit costs a worker, in tiles
   int prows;                 // rows of a part: min(rows, G C)
   int local;                 // warp-MMA kernel: one CTA per unit, its warps' parts merged in shared memory
 };
 
-// All tiles of a call, in the order (sequence, unit, tile), are dealt to the
+// All work of a call, in the order (sequence, unit, tile), is dealt to the
 // workers in equal contiguous shares, whatever the sequences' lengths: the
 // device computes the division from the lengths, so the host never reads them
-// and a captured graph follows a growing cache.  A unit cut by a share's
-// border is left in parts, merged by the merge kernel: a worker's part that
-// begins inside a unit goes to its slot 0 (there is one at most), the part of
-// a unit that it begins and does not finish to its slot 1.
-struct Kv8Seq {
+// and a captured graph follows a growing cache.  A unit counts its tiles and
+// `ovh` more, for the queries, the pipeline's start and the output (without
+// them workers with several short units ran twice as long as the others).  A
+// unit cut by a share's border is left in parts, merged by the merge kernel: a
+// worker's part that begins inside a unit goes to its slot 0 (there is one at
+// most), the part of a unit that it begins and does not finish to its slot 1.
+struct Kv8Piece {
   int b, len;                // sequence and its cached rows
-  int nt;                    // tiles of each of its units
-  int first;                 // first tile (in the call's order) of its first unit
+  int nt, unit;              // tiles of each of its units; the unit
+  int t0, t1;                // the piece's tiles (none where it ends before the unit's first)
+  int cost;                  // share that the piece takes
 };
 
 DG_DEV int kv8_len(const Kv8AttnArgs& a, int b) {
@@ -64,33 +68,35 @@ DG_DEV int kv8_tiles(const Kv8AttnArgs& a, int len) {
 DG_DEV float4* kv8_part(const Kv8AttnArgs& a, size_t slot, int c4, int r) {
   return reinterpret_cast<float4*>(a.part) + (slot * (a.hd / 4) + c4) * a.prows + r;
 }
+DG_DEV int kv8_cost(const Kv8AttnArgs& a, int nt) { return nt > 0 ? nt + a.ovh : 0; }
 // What a warp knows of the call's division: the lengths of the first 32
 // sequences, one in each lane (most calls have no more, and read them once).
 struct Kv8Plan {
   int len;                   // of sequence `lane`
-  int total, share;          // tiles of the call (below 2^31 - 2^16 by the entry point's check), and of a worker
+  int total, share;          // cost of the call (below 2^31 - 2^16 by the entry point's check), and of a worker
 };
 DG_DEV Kv8Plan kv8_plan(const Kv8AttnArgs& a) {
   const int lane = threadIdx.x & 31;
   Kv8Plan p;
   p.len = lane < a.B ? kv8_len(a, lane) : 0;
-  int n = lane < a.B ? kv8_tiles(a, p.len) * a.units : 0;
-  for (int b = lane + 32; b < a.B; b += 32) n += kv8_tiles(a, kv8_len(a, b)) * a.units;
+  int n = lane < a.B ? kv8_cost(a, kv8_tiles(a, p.len)) * a.units : 0;
+  for (int b = lane + 32; b < a.B; b += 32) n += kv8_cost(a, kv8_tiles(a, kv8_len(a, b))) * a.units;
   p.total = __reduce_add_sync(0xffffffffu, n);
   p.share = max((p.total + a.workers - 1) / a.workers, 1);
   return p;
 }
-// The sequence that tile w of the call belongs to (w below the total; every
-// lane of the calling warp gets the answer).
-DG_DEV Kv8Seq kv8_locate(const Kv8AttnArgs& a, const Kv8Plan& plan, int w) {
+// The piece that begins at w in a share that ends at w1 (w < w1 <= the total;
+// every lane of the calling warp gets the answer).
+DG_DEV Kv8Piece kv8_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int w, int w1) {
   const int lane = threadIdx.x & 31;
   int base = 0;
-  Kv8Seq p{0, 0, 1, 0};
+  Kv8Piece p{0, 0, 0, 0, 0, 0, w1 - w};
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
     const int len = b0 == 0 ? plan.len : b < a.B ? kv8_len(a, b) : 0;
     const int nt = b < a.B ? kv8_tiles(a, len) : 0;
-    int incl = nt * a.units;
+    const int mine = kv8_cost(a, nt) * a.units;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -102,7 +108,12 @@ DG_DEV Kv8Seq kv8_locate(const Kv8AttnArgs& a, const Kv8Plan& plan, int w) {
       p.b = b0 + src;
       p.len = __shfl_sync(0xffffffffu, len, src);
       p.nt = __shfl_sync(0xffffffffu, nt, src);
-      p.first = __shfl_sync(0xffffffffu, base + incl - nt * a.units, src);
+      const int off = w - __shfl_sync(0xffffffffu, base + incl - mine, src), cost = p.nt + a.ovh;
+      p.unit = off / cost;
+      const int o0 = off - p.unit * cost, o1 = min(cost, o0 + (w1 - w));
+      p.t0 = max(o0 - a.ovh, 0);
+      p.t1 = max(o1 - a.ovh, 0);
+      p.cost = o1 - o0;
       return p;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);

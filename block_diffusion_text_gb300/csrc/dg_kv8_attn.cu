@@ -235,26 +235,25 @@ __global__ void __launch_bounds__(32 * W, 1)
   bool ok = true;
 
   while (w < w1 && ok) {
-    Kv8Seq sq;
-    int unit, t0, t1;
+    Kv8Piece p;
     if (a.local) {
-      sq.b = w / a.units;
-      sq.len = kv8_len(a, sq.b);
-      sq.nt = kv8_tiles(a, sq.len);
-      unit = w - sq.b * a.units;
-      const int chunk = (sq.nt + W - 1) / W;
-      t0 = min(warp * chunk, sq.nt);
-      t1 = min(t0 + chunk, sq.nt);
+      p.b = w / a.units;
+      p.len = kv8_len(a, p.b);
+      p.nt = kv8_tiles(a, p.len);
+      p.unit = w - p.b * a.units;
+      const int chunk = (p.nt + W - 1) / W;
+      p.t0 = min(warp * chunk, p.nt);
+      p.t1 = min(p.t0 + chunk, p.nt);
     } else {
-      sq = kv8_locate(a, plan, w);
-      unit = (w - sq.first) / sq.nt;
-      t0 = w - sq.first - unit * sq.nt;
-      t1 = min(sq.nt, t0 + (w1 - w));
+      p = kv8_piece(a, plan, w, w1);
+      w += p.cost;
+      if (p.t1 <= p.t0) continue;
     }
-    const int hk = unit / row_tiles, row0 = unit % row_tiles * (8 * NT);
-    const int ntc = (sq.len + kKv8Block - 1) / kKv8Block;
+    const int t0 = p.t0, t1 = p.t1;
+    const int hk = p.unit / row_tiles, row0 = p.unit % row_tiles * (8 * NT);
+    const int ntc = (p.len + kKv8Block - 1) / kKv8Block;
     const int tc1 = min(t1, ntc);  // cached tiles of the piece end here
-    const size_t bh = (size_t)sq.b * a.Hkv + hk;
+    const size_t bh = (size_t)p.b * a.Hkv + hk;
     const uint8_t* Ke = a.Ke + bh * a.nblk;
     const uint8_t* Ve = a.Ve + bh * a.nblk;
     const int nsteps = max(tc1 - t0, 0) * (kKv8Block / kStep);
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(32 * W, 1)
         }
       }
       if (!(ok = wait(&full[slot], par, a.status, abort))) break;
-      const int valid = sq.len - (t0 * kKv8Block + i * kStep);
+      const int valid = p.len - (t0 * kKv8Block + i * kStep);
       if (valid > 0) {
         const uint8_t* sk = ring + slot * R::kStage;
         const uint8_t* sv = sk + R::kHalf;
@@ -554,13 +553,13 @@ __global__ void __launch_bounds__(32 * W, 1)
           v.w += s.v.w;
         }
         const float inv = L == 0.f ? 0.f : 1.0f / L;
-        *reinterpret_cast<uint2*>(kv8_out_row(a, sq.b, hk, row0 + r) + 4 * c4) =
+        *reinterpret_cast<uint2*>(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4) =
             make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
       }
       break;
     }
     if (!ok) break;
-    const bool whole = t0 == 0 && t1 == sq.nt;
+    const bool whole = t0 == 0 && t1 == p.nt;
     const size_t part = (size_t)worker * 2 + (t0 > 0 ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -571,7 +570,7 @@ __global__ void __launch_bounds__(32 * W, 1)
         const float l = acc.l[nt][e];
         if (whole) {
           const float inv = l == 0.f ? 0.f : 1.0f / l;
-          uint2* dst = reinterpret_cast<uint2*>(kv8_out_row(a, sq.b, hk, row0 + r) + g * NV);
+          uint2* dst = reinterpret_cast<uint2*>(kv8_out_row(a, p.b, hk, row0 + r) + g * NV);
 #pragma unroll
           for (int k = 0; k < NV / 4; ++k) {
             const float4 v = out4(nt, e, k);
@@ -584,7 +583,6 @@ __global__ void __launch_bounds__(32 * W, 1)
         }
       }
     }
-    w += t1 - t0;
   }
   if (*abort) {  // copies in flight land before the CTA's shared memory goes
     const uint64_t start = globaltimer();
@@ -622,8 +620,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv8_merge_kernel(Kv8AttnArgs
   const int nt = kv8_tiles(a, kv8_len(a, b));
   const Kv8Plan plan = kv8_plan(a);
   int first = 0;
-  for (int i = lane; i < b; i += 32) first += kv8_tiles(a, i < 32 ? plan.len : kv8_len(a, i)) * a.units;
-  first = __reduce_add_sync(0xffffffffu, first) + unit * nt;
+  for (int i = lane; i < b; i += 32) first += kv8_cost(a, kv8_tiles(a, i < 32 ? plan.len : kv8_len(a, i))) * a.units;
+  first = __reduce_add_sync(0xffffffffu, first) + unit * (nt + a.ovh) + a.ovh;  // the unit's first tile
   const int c0 = first / plan.share, n = (first + max(nt, 1) - 1) / plan.share - c0;
   pdl_wait();
   if (nt > 0 && n == 0) return;  // uniform over the warps that meet below

@@ -115,20 +115,17 @@ struct Piece {
   DG_DEV int tiles() const { return t1 - t0; }
   DG_DEV bool fresh(int j) const { return t0 + j >= ntc; }  // tile j of the piece holds new tokens
 };
-DG_DEV Piece piece_at(const Kv8AttnArgs& a, const Kv8Plan& plan, int w, int w1) {
-  const Kv8Seq sq = kv8_locate(a, plan, w);
-  const int per = a.units / a.Hkv;
-  const int unit = (w - sq.first) / sq.nt;
-  Piece p;
-  p.b = sq.b;
-  p.hk = unit / per;
-  p.row0 = unit % per * 256;
-  p.len = sq.len;
-  p.t0 = w - sq.first - unit * sq.nt;
-  p.t1 = min(sq.nt, p.t0 + (w1 - w));
-  p.nt = sq.nt;
-  p.ntc = (sq.len + kTK - 1) / kTK;
-  return p;
+// The next piece with tiles at or after w, or false.
+DG_DEV bool next_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int& w, int w1, Piece& p) {
+  while (w < w1) {
+    const Kv8Piece k = kv8_piece(a, plan, w, w1);
+    w += k.cost;
+    if (k.t1 <= k.t0) continue;
+    const int per = a.units / a.Hkv;
+    p = Piece{k.b, k.unit / per, k.unit % per * 256, k.len, k.t0, k.t1, k.nt, (k.len + kTK - 1) / kTK};
+    return true;
+  }
+  return false;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -209,8 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bool ok = true;
       int kslot = 0, kpar = 1, J = 0, np = 0;  // slot counters run on through the pieces
-      for (int w = w0; w < w1 && ok; ++np) {
-        const Piece p = piece_at(a, plan, w, w1);
+      Piece p;
+      for (int w = w0; ok && next_piece(a, plan, w, w1, p); ++np) {
         if (lane == 0) {
           const int bh = p.b * a.Hkv + p.hk;
           ok = mbar_wait(qempty, (np & 1) ^ 1, status, abort);
@@ -252,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        w += p.tiles();
       }
     } else if (warp < 3) {
       const int t = warp - 1;
@@ -263,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tS = tmem + 128 * t, tO = tmem + kColO + 128 * t;
       bool ok = true;
       int kslot = 0, kpar = 0, J = 0, np = 0, step = 0;
-      for (int w = w0; w < w1 && ok; ++np) {
-        const Piece p = piece_at(a, plan, w, w1);
+      Piece p;
+      for (int w = w0; ok && next_piece(a, plan, w, w1, p); ++np) {
         const int n = p.tiles(), jfresh = p.ntc - p.t0;  // tiles from jfresh on hold new tokens
         int ka = 0, kb = 0;                              // K slots of tile j + 1
         auto wait_k = [&](int& k) -> bool {
@@ -321,15 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         J += n;
-        w += n;
       }
     }
   } else if (warp < 8) {
     const int tid = threadIdx.x - 128;
     bool ok = true;
     int J = 0;
-    for (int w = w0; w < w1 && ok;) {
-      const Piece p = piece_at(a, plan, w, w1);
+    Piece p;
+    for (int w = w0; ok && next_piece(a, plan, w, w1, p);) {
       for (int j = 0; j < p.tiles(); ++j, ++J) {
         const int s = J % kNV, par = (J / kNV) & 1;
         if (!(ok = wait(&cfull[s], par, status, abort))) break;
@@ -359,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&vfull[s]);
         }
       }
-      w += p.tiles();
     }
   } else {
     const int t = (warp - 8) / 4, q4 = warp & 3;
@@ -368,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + kColO + 128 * t;
     bool ok = true;
     int J = 0, np = 0;
-    for (int w = w0; w < w1 && ok; ++np) {
-      const Piece p = piece_at(a, plan, w, w1);
+    Piece p;
+    for (int w = w0; ok && next_piece(a, plan, w, w1, p); ++np) {
       const int n = p.tiles(), bh = p.b * a.Hkv + p.hk;
       const int ridx = p.row0 + 128 * t + r;
       const bool valid_row = ridx < grp_rows;
@@ -511,7 +505,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       J += n;
-      w += n;
     }
   }
   __syncthreads();
