@@ -156,17 +156,42 @@ DG_DEV void softmax_step(float (&s)[kMT][NT][4], const float (&c)[NT][2], float 
   }
 }
 
-// Parts of four output columns and the row sum, on the maximum M of all parts.
+// Parts of 4 N output columns and the row sum, on the maximum M of all parts.
+template <int N>
 struct Kv8Sum {
   float l = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  DG_DEV void add(const float2& ml, float M, const float4& x) {
+  float4 v[N] = {};
+  // x: the part's columns, the next four `step` further
+  DG_DEV void add(const float2& ml, float M, const float4* x, size_t step) {
+    float4 p[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = x[i * step];
     const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
     l = fmaf(w, ml.y, l);
-    v.x = fmaf(w, x.x, v.x);
-    v.y = fmaf(w, x.y, v.y);
-    v.z = fmaf(w, x.z, v.z);
-    v.w = fmaf(w, x.w, v.w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i].x = fmaf(w, p[i].x, v[i].x);
+      v[i].y = fmaf(w, p[i].y, v[i].y);
+      v[i].z = fmaf(w, p[i].z, v[i].z);
+      v[i].w = fmaf(w, p[i].w, v[i].w);
+    }
+  }
+  DG_DEV void add(const Kv8Sum& s) {
+    l += s.l;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i].x += s.v[i].x;
+      v[i].y += s.v[i].y;
+      v[i].z += s.v[i].z;
+      v[i].w += s.v[i].w;
+    }
+  }
+  DG_DEV void store(__nv_bfloat16* dst) const {
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      *reinterpret_cast<uint2*>(dst + 4 * i) =
+          make_uint2(pack_bf16(v[i].x * inv, v[i].y * inv), pack_bf16(v[i].z * inv, v[i].w * inv));
   }
 };
 
@@ -536,25 +561,19 @@ __global__ void __launch_bounds__(32 * W, 1)
       for (int i = threadIdx.x; i < a.prows * (HD / 4); i += 32 * W) {
         const int r = i / (HD / 4), c4 = i % (HD / 4);
         if (row0 + r >= grp_rows) break;
-        float M = -INFINITY, L = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float M = -INFINITY;
 #pragma unroll
         for (int k = 0; k < W; ++k) M = fmaxf(M, ml[k * 32 + r].x);
+        Kv8Sum<1> sum;
 #pragma unroll
         for (int sl = 0; sl < kMergeSlices; ++sl) {  // the merge kernel's order of additions
-          Kv8Sum s;
+          Kv8Sum<1> s;
 #pragma unroll
           for (int k = sl; k < W; k += kMergeSlices)
-            s.add(ml[k * 32 + r], M, *reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4));
-          L += s.l;
-          v.x += s.v.x;
-          v.y += s.v.y;
-          v.z += s.v.z;
-          v.w += s.v.w;
+            s.add(ml[k * 32 + r], M, reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4), 0);
+          sum.add(s);
         }
-        const float inv = L == 0.f ? 0.f : 1.0f / L;
-        *reinterpret_cast<uint2*>(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4) =
-            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+        sum.store(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4);
       }
       break;
     }
@@ -590,49 +609,59 @@ __global__ void __launch_bounds__(32 * W, 1)
   }
 }
 
-// Merge of the parts.  32 consecutive float4 of a unit's output, lane by lane,
-// are made by S warps that share the parts: S = 8 for single tokens, whose units
-// have some 50 parts of few rows (one warp alone would wait for them round by
-// round: 15 us for 4 sequences of 131072 rows), S = 1 for the 256-row units of
-// the tensor-core kernel, which have few parts and items enough.  The shares'
-// borders are recomputed; a unit that one worker finished is already written,
-// and one without any key (an empty sequence without new tokens) gets zeros.
-// What it reads before pdl_wait, the lengths, no kernel of the call writes, and
-// the attention kernel lets this one start only once it has itself waited for
-// its predecessors; they are read past the first-level cache.
+// Merge of the parts.  A thread makes 4 N columns of an output row, a warp those
+// of 32 consecutive rows (of fewer rows and more columns where a part has
+// fewer), a CTA of 8 warps those of one unit.  Single tokens' units have some
+// 50 parts of few rows: the eight warps share them (S = 8; one warp alone would
+// wait for them round by round, 15 us for 4 sequences of 131072 rows).  The
+// 256-row units of the tensor-core kernel have fewer parts and rows enough for
+// a warp each (S = 1).  One warp works out where the shares' borders cut the
+// unit (done by every warp it took longer than the parts: 16 us for 8 prompt
+// pieces); a unit that one worker finished is already written, and one without
+// any key (an empty sequence without new tokens) gets zeros.  What is read
+// before pdl_wait, the lengths, no kernel of the call writes, and the
+// attention kernel lets this one start only once it has itself waited for its
+// predecessors; they are read past the first-level cache.
 constexpr int kMergeWarps = 8;
 
-template <int HD, int S>
-__global__ void __launch_bounds__(32 * kMergeWarps) kv8_merge_kernel(Kv8AttnArgs a) {
-  constexpr int C4 = HD / 4;
+template <int HD, int S, int N>
+__global__ void __launch_bounds__(32 * kMergeWarps) kv8_merge_kernel(Kv8AttnArgs a, int ctas) {
+  constexpr int CN = HD / (4 * N);
+  __shared__ int cut[3];
   __shared__ float top[S][32];
-  __shared__ Kv8Sum sums[S][32];
+  __shared__ Kv8Sum<N> sums[S > 1 ? S : 1][S > 1 ? 32 : 1];
   const int lane = threadIdx.x % 32, slice = threadIdx.x / 32 % S;
   const int grp_rows = a.Hq / a.Hkv * a.C;
-  const unsigned group = blockIdx.x * (kMergeWarps / S) + threadIdx.x / (32 * S);
-  const unsigned per = (a.prows * C4 + 31) / 32, all = group / per;  // groups of 32 per unit; the unit
+  const unsigned all = blockIdx.x / (unsigned)ctas;  // `ctas` CTAs a unit
   const int b = (int)(all / a.units), unit = (int)(all - (unsigned)b * a.units);
-  if (b >= a.B) return;
-  const int item = (int)(group - all * per) * 32 + lane;
+  if (threadIdx.x < 32) {
+    const Kv8Plan plan = kv8_plan(a);
+    const int nt = kv8_tiles(a, b < 32 ? __shfl_sync(0xffffffffu, plan.len, b & 31) : kv8_len(a, b));
+    int first = 0;
+    for (int i = lane; i < b; i += 32) first += kv8_cost(a, kv8_tiles(a, i < 32 ? plan.len : kv8_len(a, i))) * a.units;
+    first = __reduce_add_sync(0xffffffffu, first) + unit * (nt + a.ovh) + a.ovh;  // the unit's first tile
+    if (lane == 0) {
+      cut[0] = first / plan.share;
+      cut[1] = (first + max(nt, 1) - 1) / plan.share;
+      cut[2] = nt;
+    }
+  }
+  const int item = ((int)(blockIdx.x - all * ctas) * (kMergeWarps / S) + threadIdx.x / (32 * S)) * 32 + lane;
   const int row_tiles = a.units / a.Hkv, hk = unit / row_tiles;
-  const int c4 = item / a.prows, rr = item - c4 * a.prows, r = unit % row_tiles * a.rows + rr;
-  const bool mine = c4 < C4 && r < grp_rows;
-  const int nt = kv8_tiles(a, kv8_len(a, b));
-  const Kv8Plan plan = kv8_plan(a);
-  int first = 0;
-  for (int i = lane; i < b; i += 32) first += kv8_cost(a, kv8_tiles(a, i < 32 ? plan.len : kv8_len(a, i))) * a.units;
-  first = __reduce_add_sync(0xffffffffu, first) + unit * (nt + a.ovh) + a.ovh;  // the unit's first tile
-  const int c0 = first / plan.share, n = (first + max(nt, 1) - 1) / plan.share - c0;
+  const int cn = item / a.prows, rr = item - cn * a.prows, r = unit % row_tiles * a.rows + rr;
+  const bool mine = cn < CN && r < grp_rows;
+  __syncthreads();
+  const int c0 = cut[0], n = cut[1] - c0, nt = cut[2];
   pdl_wait();
-  if (nt > 0 && n == 0) return;  // uniform over the warps that meet below
+  if (nt > 0 && n == 0) return;  // uniform over the CTA
   // part 0 is the unit's beginning (slot 1 of its worker), the others slots 0
-  const size_t mstep = 2 * (size_t)a.prows, pstep = mstep * C4;
+  const size_t mstep = 2 * (size_t)a.prows, pstep = mstep * (HD / 4);
   const float2* ml = a.ml + c0 * mstep + (mine ? rr : 0);
-  const float4* src = kv8_part(a, (size_t)c0 * 2, mine ? c4 : 0, mine ? rr : 0);
+  const float4* src = kv8_part(a, (size_t)c0 * 2, mine ? cn * N : 0, mine ? rr : 0);
   const size_t slot1 = a.prows;
   float M = -INFINITY;
   if (nt > 0) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = slice; i <= n; i += S) M = fmaxf(M, ml[i * mstep + (i ? 0 : slot1)].x);
   }
   if constexpr (S > 1) {
@@ -641,33 +670,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv8_merge_kernel(Kv8AttnArgs
 #pragma unroll
     for (int k = 0; k < S; ++k) M = fmaxf(M, top[k][lane]);
   }
-  Kv8Sum s;
+  Kv8Sum<N> s;
   if (nt > 0) {
 #pragma unroll 4
     for (int i = slice; i <= n; i += S)
-      s.add(ml[i * mstep + (i ? 0 : slot1)], M, src[i * pstep + (i ? 0 : slot1 * C4)]);
+      s.add(ml[i * mstep + (i ? 0 : slot1)], M, src + i * pstep + (i ? 0 : slot1 * (HD / 4)), a.prows);
   }
   if constexpr (S > 1) {
     sums[slice][lane] = s;
     __syncthreads();
     if (slice != 0) return;
-    s = Kv8Sum();
+    s = Kv8Sum<N>();
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      const Kv8Sum& x = sums[k][lane];
-      s.l += x.l;
-      s.v.x += x.v.x;
-      s.v.y += x.v.y;
-      s.v.z += x.v.z;
-      s.v.w += x.v.w;
-    }
+    for (int k = 0; k < S; ++k) s.add(sums[k][lane]);
   }
-  if (!mine) return;
-  const float L = s.l;
-  const float4 v = s.v;
-  const float inv = L == 0.f ? 0.f : 1.0f / L;
-  *reinterpret_cast<uint2*>(kv8_out_row(a, b, hk, r) + 4 * c4) =
-      make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+  if (mine) s.store(kv8_out_row(a, b, hk, r) + 4 * N * cn);
 }
 
 template <int HD, int NT>
@@ -708,20 +725,23 @@ cudaError_t launch_kv8_attention_mma(const Kv8AttnArgs& a, cudaStream_t st) {
   return cudaErrorInvalidValue;
 }
 
-template <int HD>
+template <int HD, int S, int N>
 static cudaError_t run_merge(const Kv8AttnArgs& a, cudaStream_t st) {
-  const int64_t groups = (int64_t)a.B * a.units * (((int64_t)a.prows * (HD / 4) + 31) / 32);
-  if (a.rows == 256)
-    return launch_pdl(kv8_merge_kernel<HD, 1>, dim3(cdiv(groups, kMergeWarps)), dim3(32 * kMergeWarps), 0, st, a);
-  static_assert(kMergeSlices == kMergeWarps, "one group per CTA");
-  return launch_pdl(kv8_merge_kernel<HD, kMergeSlices>, dim3((unsigned)groups), dim3(32 * kMergeWarps), 0, st, a);
+  const int ctas = cdiv((int64_t)a.prows * (HD / (4 * N)), 32 * (kMergeWarps / S));
+  return launch_pdl(kv8_merge_kernel<HD, S, N>, dim3((unsigned)(a.B * a.units * ctas)), dim3(32 * kMergeWarps), 0, st, a,
+                    ctas);
 }
 
 cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, cudaStream_t st) {
   switch (a.hd) {
-    case 32: return run_merge<32>(a, st);
-    case 64: return run_merge<64>(a, st);
-    case 128: return run_merge<128>(a, st);
+    case 32: return run_merge<32, kMergeSlices, 1>(a, st);
+    case 64: return run_merge<64, kMergeSlices, 1>(a, st);
+    case 128:
+      if (a.rows < 256) return run_merge<128, kMergeSlices, 1>(a, st);
+      // Many parts a unit: short loops over them in many warps (canvas over 8192
+      // rows: 31.5 us against 36.0 with 16 columns a thread); few: fewer warps
+      // (8 prompt pieces: 40.9 us against 46.3 with four).
+      return a.workers >= 4 * a.B * a.units ? run_merge<128, 1, 1>(a, st) : run_merge<128, 1, 4>(a, st);
   }
   return cudaErrorInvalidValue;
 }

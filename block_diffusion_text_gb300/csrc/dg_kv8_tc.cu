@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  pdl_trigger();  // the merge, which needs no TMEM, may take the SMs that this kernel leaves
 
   const Kv8Plan plan = kv8_plan(a);
   const int w0 = min(plan.total, (int)blockIdx.x * plan.share), w1 = min(plan.total, w0 + plan.share);
