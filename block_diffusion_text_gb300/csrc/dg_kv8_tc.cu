@@ -340,8 +340,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 v = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
             if (row >= valid) v = make_uint4(0, 0, 0, 0);  // what lies behind the sequence never enters an MMA
             uint4 h[2];
-            h[0] = make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16));
-            h[1] = make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w), e4m3x2_f16x2(v.w >> 16));
+            e4m3x4_f16x4(v.x, h[0].x, h[0].y);
+            e4m3x4_f16x4(v.y, h[0].z, h[0].w);
+            e4m3x4_f16x4(v.z, h[1].x, h[1].y);
+            e4m3x4_f16x4(v.w, h[1].z, h[1].w);
             uint8_t* d = dst + (c / 4) * Smem::kBox + row * 128;
             const int ch = (c % 4) * 2, f = c / 4;  // the two boxes' lanes store their halves in opposite order: no bank conflicts
             *reinterpret_cast<uint4*>(d + (((ch + f) ^ (row & 7)) << 4)) = f ? h[1] : h[0];
