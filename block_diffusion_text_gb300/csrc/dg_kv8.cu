@@ -227,7 +227,7 @@ constexpr int kKv8Ovh = 3;  // measured: a unit's start and output take as long 
 
 struct Kv8Ws {
   size_t part, ml, qterms, qexp, kterms, vf16, kexp, vexp, total;
-  int rows, tk, units, workers, prows, Cp;
+  int rows, tk, units, workers, prows, subs, Cp;
   bool tc, local;
 };
 
@@ -236,7 +236,8 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   Kv8Ws w{};
   const int64_t R = (int64_t)(Hq / c->Hkv) * C;
   w.tc = c->hd == 128 && R > 16;
-  w.rows = w.tc ? 256 : kv8_mma_rows(c->hd, R);
+  w.subs = w.tc && R <= 128 ? 2 : 1;  // one row tile is enough: the two take every other key tile
+  w.rows = w.tc ? 256 / w.subs : kv8_mma_rows(c->hd, R);
   w.tk = w.tc ? 128 : kKv8Block;
   w.workers = w.tc ? kKv8Ctas : kKv8Ctas * kv8_mma_warps(c->hd, w.rows);
   w.units = (int)(c->Hkv * ((R + w.rows - 1) / w.rows));  // at most 65535 * 64 by the checks before
@@ -251,8 +252,8 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   // merge kernel.
   w.local = !w.tc && cdiv(c->cap, w.tk) + cdiv(C, w.tk) <= kLocalTiles;
   if (w.local) return w;
-  w.part = take((size_t)2 * w.workers * w.prows * c->hd * 4);
-  w.ml = take((size_t)2 * w.workers * w.prows * 8);
+  w.part = take((size_t)2 * w.workers * w.subs * w.prows * c->hd * 4);
+  w.ml = take((size_t)2 * w.workers * w.subs * w.prows * 8);
   if (w.tc) {
     w.Cp = cdiv(C, 128) * 128;
     const size_t qrows = (size_t)c->B * Hq * C, krows = (size_t)c->B * c->Hkv * w.Cp;
@@ -369,6 +370,7 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   a.units = w.units;
   a.workers = w.workers;
   a.ovh = kKv8Ovh;
+  a.subs = w.subs;
   a.prows = w.prows;
   a.local = w.local;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -27,13 +27,14 @@ struct Kv8AttnArgs {
   const int* len;            // [B]
   const void *kn, *vn;       // bf16 [B][Hkv][C][hd] or null
   void* o;                   // bf16 [B*C][Hq*hd]
-  float* part;               // fp32 [2 * workers][hd / 4][prows][4]
-  float2* ml;                // [2 * workers][prows]: maximum (log2 units) and sum
+  float* part;               // fp32 [2 * workers * subs][hd / 4][prows][4]
+  float2* ml;                // [2 * workers * subs][prows]: maximum (log2 units) and sum
   int* status;
   int B, C, Hq, Hkv, hd, cap, nblk;
   int causal;
   int rows, tk, units;       // rows per unit, keys per tile, units per sequence (Hkv * row tiles)
   int workers;               // warps or CTAs that the tiles are dealt to
+  int subs;                  // parts of a piece: 2 where the tensor-core kernel's two row tiles share the rows
   int ovh;                   // what beginning a unit costs a worker, in tiles
   int prows;                 // rows of a part: min(rows, G C)
   int local;                 // warp-MMA kernel: one CTA per unit, its warps' parts merged in shared memory

@@ -624,13 +624,13 @@ __global__ void __launch_bounds__(32 * W, 1)
 // predecessors; they are read past the first-level cache.
 constexpr int kMergeWarps = 8;
 
-template <int HD, int S, int N>
+template <int HD, int S, int N, int SUBS>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv8_merge_kernel(Kv8AttnArgs a, int ctas) {
   constexpr int CN = HD / (4 * N);
   __shared__ int cut[3];
-  __shared__ float top[S][32];
-  __shared__ Kv8Sum<N> sums[S > 1 ? S : 1][S > 1 ? 32 : 1];
-  const int lane = threadIdx.x % 32, slice = threadIdx.x / 32 % S;
+  __shared__ float top[kMergeWarps / S][S][32];
+  __shared__ Kv8Sum<N> sums[kMergeWarps / S][S > 1 ? S : 1][S > 1 ? 32 : 1];
+  const int lane = threadIdx.x % 32, slice = threadIdx.x / 32 % S, sub = threadIdx.x / (32 * S);
   const int grp_rows = a.Hq / a.Hkv * a.C;
   const unsigned all = blockIdx.x / (unsigned)ctas;  // `ctas` CTAs a unit
   const int b = (int)(all / a.units), unit = (int)(all - (unsigned)b * a.units);
@@ -646,43 +646,74 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv8_merge_kernel(Kv8AttnArgs
       cut[2] = nt;
     }
   }
-  const int item = ((int)(blockIdx.x - all * ctas) * (kMergeWarps / S) + threadIdx.x / (32 * S)) * 32 + lane;
+  const int item = ((int)(blockIdx.x - all * ctas) * (kMergeWarps / S) + sub) * 32 + lane;
   const int row_tiles = a.units / a.Hkv, hk = unit / row_tiles;
   const int cn = item / a.prows, rr = item - cn * a.prows, r = unit % row_tiles * a.rows + rr;
   const bool mine = cn < CN && r < grp_rows;
   __syncthreads();
   const int c0 = cut[0], n = cut[1] - c0, nt = cut[2];
   pdl_wait();
-  if (nt > 0 && n == 0) return;  // uniform over the CTA
-  // part 0 is the unit's beginning (slot 1 of its worker), the others slots 0
-  const size_t mstep = 2 * (size_t)a.prows, pstep = mstep * (HD / 4);
-  const float2* ml = a.ml + c0 * mstep + (mine ? rr : 0);
-  const float4* src = kv8_part(a, (size_t)c0 * 2, mine ? cn * N : 0, mine ? rr : 0);
-  const size_t slot1 = a.prows;
+  if (nt > 0 && n == 0 && SUBS == 1) return;  // uniform over the CTA
+  // Part 0 (with its sub-parts) is the unit's beginning, slot 1 of its worker; the
+  // others are slots 0.  The slots' loads go out in groups, whole ones: what a
+  // group lacks is read as an empty part, so that no remainder waits on its own.
+  const size_t mstep = a.prows, pstep = mstep * (HD / 4);
+  const float2* ml = a.ml + (size_t)c0 * 2 * SUBS * mstep + (mine ? rr : 0);
+  const float4* src = kv8_part(a, (size_t)c0 * 2 * SUBS, mine ? cn * N : 0, mine ? rr : 0);
+  const int last = nt > 0 ? n : -1;
+  auto at = [](int i, int u) { return (size_t)(i * 2 * SUBS + (i == 0 ? SUBS : 0) + u); };
+  constexpr int kGroup = 8 / SUBS;
   float M = -INFINITY;
-  if (nt > 0) {
-#pragma unroll 8
-    for (int i = slice; i <= n; i += S) M = fmaxf(M, ml[i * mstep + (i ? 0 : slot1)].x);
+#pragma unroll 1
+  for (int i0 = slice; i0 <= last; i0 += kGroup * S) {
+    float m[kGroup][SUBS];
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) m[k][u] = i0 + k * S <= last ? ml[at(i0 + k * S, u) * mstep].x : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) M = fmaxf(M, m[k][u]);
   }
   if constexpr (S > 1) {
-    top[slice][lane] = M;
+    top[sub][slice][lane] = M;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < S; ++k) M = fmaxf(M, top[k][lane]);
+    for (int k = 0; k < S; ++k) M = fmaxf(M, top[sub][k][lane]);
   }
   Kv8Sum<N> s;
-  if (nt > 0) {
-#pragma unroll 4
-    for (int i = slice; i <= n; i += S)
-      s.add(ml[i * mstep + (i ? 0 : slot1)], M, src + i * pstep + (i ? 0 : slot1 * (HD / 4)), a.prows);
+  constexpr int kGroup2 = N * SUBS >= 4 ? 2 : 8 / (N * SUBS);
+#pragma unroll 1
+  for (int i0 = slice; i0 <= last; i0 += kGroup2 * S) {
+    float2 m[kGroup2][SUBS];
+    float4 x[kGroup2][SUBS][N];
+#pragma unroll
+    for (int k = 0; k < kGroup2; ++k) {
+      const int i = i0 + k * S;
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) {
+        m[k][u] = make_float2(-INFINITY, 0.f);
+        if (i <= last) m[k][u] = ml[at(i, u) * mstep];
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          x[k][u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i <= last) x[k][u][c] = src[at(i, u) * pstep + c * mstep];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kGroup2; ++k)
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) s.add(m[k][u], M, x[k][u], 1);
   }
   if constexpr (S > 1) {
-    sums[slice][lane] = s;
+    sums[sub][slice][lane] = s;
     __syncthreads();
     if (slice != 0) return;
     s = Kv8Sum<N>();
 #pragma unroll
-    for (int k = 0; k < S; ++k) s.add(sums[k][lane]);
+    for (int k = 0; k < S; ++k) s.add(sums[sub][k][lane]);
   }
   if (mine) s.store(kv8_out_row(a, b, hk, r) + 4 * N * cn);
 }
@@ -725,10 +756,10 @@ cudaError_t launch_kv8_attention_mma(const Kv8AttnArgs& a, cudaStream_t st) {
   return cudaErrorInvalidValue;
 }
 
-template <int HD, int S, int N>
+template <int HD, int S, int N, int SUBS = 1>
 static cudaError_t run_merge(const Kv8AttnArgs& a, cudaStream_t st) {
   const int ctas = cdiv((int64_t)a.prows * (HD / (4 * N)), 32 * (kMergeWarps / S));
-  return launch_pdl(kv8_merge_kernel<HD, S, N>, dim3((unsigned)(a.B * a.units * ctas)), dim3(32 * kMergeWarps), 0, st, a,
+  return launch_pdl(kv8_merge_kernel<HD, S, N, SUBS>, dim3((unsigned)(a.B * a.units * ctas)), dim3(32 * kMergeWarps), 0, st, a,
                     ctas);
 }
 
@@ -736,12 +767,17 @@ cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, cudaStream_t st) {
   switch (a.hd) {
     case 32: return run_merge<32, kMergeSlices, 1>(a, st);
     case 64: return run_merge<64, kMergeSlices, 1>(a, st);
-    case 128:
-      if (a.rows < 256) return run_merge<128, kMergeSlices, 1>(a, st);
-      // Many parts a unit: short loops over them in many warps (canvas over 8192
-      // rows: 31.5 us against 36.0 with 16 columns a thread); few: fewer warps
-      // (8 prompt pieces: 40.9 us against 46.3 with four).
-      return a.workers >= 4 * a.B * a.units ? run_merge<128, 1, 1>(a, st) : run_merge<128, 1, 4>(a, st);
+    case 128: {
+      if (a.rows < 128) return run_merge<128, kMergeSlices, 1>(a, st);
+      // By the parts that a unit has (19 of them, a canvas over 131072 rows: 115.8
+      // us, against 128.9 with a warp for all parts and 120.5 with two; 9, over
+      // 8192 rows: 32.6 with two, against 37.9 and 33.8 with four; 2, prompt
+      // pieces: 41.7 with one, against 45.6 with two).
+      const int64_t units = (int64_t)a.B * a.units;
+      if (a.subs == 2) return a.workers >= 8 * units ? run_merge<128, 8, 1, 2>(a, st) : run_merge<128, 2, 2, 2>(a, st);
+      if (a.workers >= 16 * units) return run_merge<128, 4, 2>(a, st);
+      return a.workers >= 4 * units ? run_merge<128, 2, 2>(a, st) : run_merge<128, 1, 4>(a, st);
+    }
   }
   return cudaErrorInvalidValue;
 }

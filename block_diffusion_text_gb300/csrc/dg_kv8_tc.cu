@@ -122,12 +122,15 @@ DG_DEV bool next_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int& w, int w1
     w += k.cost;
     if (k.t1 <= k.t0) continue;
     const int per = a.units / a.Hkv;
-    p = Piece{k.b, k.unit / per, k.unit % per * 256, k.len, k.t0, k.t1, k.nt, (k.len + kTK - 1) / kTK};
+    p = Piece{k.b, k.unit / per, k.unit % per * a.rows, k.len, k.t0, k.t1, k.nt, (k.len + kTK - 1) / kTK};
     return true;
   }
   return false;
 }
 
+// DUP: up to 128 query rows.  Both row tiles hold the same rows and row tile t
+// takes key tiles t, t + 2, ..; their outputs are two parts.
+template <bool DUP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                        const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mKn,
@@ -158,16 +161,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     mbar_init(qfull, 1);
+    constexpr int readers = DUP ? 1 : 2;  // MMA warps that read a tile
     mbar_init(qempty, 2);
     for (int s = 0; s < kNK; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 2);
+      mbar_init(&kempty[s], readers);
     }
     for (int s = 0; s < kNV; ++s) {
       mbar_init(&cfull[s], 1);
       mbar_init(&cempty[s], 4);
       mbar_init(&vfull[s], 4);
-      mbar_init(&vempty[s], 2);
+      mbar_init(&vempty[s], readers);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int term = 0; term < 2; ++term)
-                tma_load_2d(smem + (2 * t + term) * Smem::kQ, &mQ, qfull, 0, term * pp.qrows + qrow + 128 * t);
+                tma_load_2d(smem + (2 * t + term) * Smem::kQ, &mQ, qfull, 0, term * pp.qrows + qrow + (DUP ? 0 : 128 * t));
           }
           for (int j = 0; j < p.tiles() && ok; ++j, ++J) {
             const bool fresh = p.fresh(j);
@@ -259,65 +263,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lo_v = desc_lo(smem_u32(smem + Smem::oVf), Smem::kBox);
       const uint32_t tS = tmem + 128 * t, tO = tmem + kColO + 128 * t;
       bool ok = true;
-      int kslot = 0, kpar = 0, J = 0, np = 0, step = 0;
+      static_assert((kNK & (kNK - 1)) == 0 && kNV == 2, "slots from running counts");
+      int K = 0, J = 0, Jt = 0, np = 0, turns = t ^ 1;  // K slots, tiles, own tiles, pieces so far; parity of the turn
+      const int stride = DUP ? 2 : 1, begin = DUP ? t : 0;
       Piece p;
       for (int w = w0; ok && next_piece(a, plan, w, w1, p); ++np) {
-        const int n = p.tiles(), jfresh = p.ntc - p.t0;  // tiles from jfresh on hold new tokens
-        int ka = 0, kb = 0;                              // K slots of tile j + 1
-        auto wait_k = [&](int& k) -> bool {
-          k = kslot;
-          const bool r = wait(&kfull[kslot], kpar, status, abort);
-          if (++kslot == kNK) {
-            kslot = 0;
-            kpar ^= 1;
-          }
-          return r;
-        };
+        const int n = p.tiles(), jfresh = max(p.ntc - p.t0, 0);  // tiles from jfresh on hold new tokens
+        const int own = DUP ? (n + 1 - t) >> 1 : n, steps = DUP ? (n + 1) >> 1 : n;
+        int j = begin - stride;                           // own key tile k of the piece
+        int kc = K + (begin > 0 ? (jfresh > 0 ? 1 : 2) : 0);  // K slot of tile j + stride
         ok = wait(qfull, np & 1, status, abort);
-        // Step j: P_t V of key tile j, then S_t of tile j + 1.  The two warps take
-        // turns, step by step, which keeps the row tiles' softmax phases apart
+        // Step k: P_t V of own key tile k, then S_t of own tile k + 1.  The two warps
+        // take turns, step by step, which keeps the row tiles' softmax phases apart
         // (left alone they fall into step, and the tensor core idles while both
         // wait); each does its waiting and committing during the other's turn.
-        // A commit covers all MMAs of its thread before it, so S_t of tile j + 1
-        // also says that P_t V of tile j is done.
+        // A commit covers all MMAs of its thread before it, so S_t of tile k + 1
+        // also says that P_t V of tile k is done.
 #pragma unroll 1
-        for (int j = -1; j < n && ok; ++j, ++step) {
-          const int s = (J + j) & 1;
-          const bool next = j + 1 < n, fresh = j + 1 >= jfresh;
-          if (next && !(ok = wait_k(ka) && (!fresh || wait_k(kb)))) break;
-          if (j >= 0) {
-            if (!(ok = wait(&vfull[s], ((J + j) / kNV) & 1, status, abort))) break;
-            if (j == 0 && np > 0 && !(ok = wait(&ofree[t], (np - 1) & 1, status, abort))) break;
-            if (!(ok = wait(&pready[2 * t], (J + j) & 1, status, abort))) break;
+        for (int k = -1; k < steps && ok; ++k) {
+          const int s = (J + j) & 1, jn = j + stride;
+          const bool next = k + 1 < own, fresh = jn >= jfresh;
+          const int ka = kc & (kNK - 1), kb = (kc + 1) & (kNK - 1);
+          if (next) {
+            if (!(ok = wait(&kfull[ka], (kc / kNK) & 1, status, abort))) break;
+            if (fresh && !(ok = wait(&kfull[kb], ((kc + 1) / kNK) & 1, status, abort))) break;
           }
-          if (!(ok = wait(&turn[t], (step & 1) ^ 1 ^ t, status, abort))) break;
-          tc_fence_after();
-          if (j >= 0) {
+          if (k >= 0 && k < own) {
+            if (!(ok = wait(&vfull[s], ((J + j) >> 1) & 1, status, abort))) break;
+            if (k == 0 && np > 0 && !(ok = wait(&ofree[t], (np - 1) & 1, status, abort))) break;
+            if (!(ok = wait(&pready[2 * t], (Jt + k) & 1, status, abort))) break;
+            if (!(ok = wait(&turn[t], turns, status, abort))) break;
+            tc_fence_after();
             const uint32_t v = lo_v + s * (Smem::kF16 >> 4);
 #pragma unroll
             for (int k4 = 0; k4 < kTK / 32; ++k4)
-              mma_pv(tO, tS + 8 * k4, desc64(v + k4 * (2048 >> 4)), idPV, (j | k4) ? 1u : 0u);
-            if (!(ok = wait(&pready[2 * t + 1], (J + j) & 1, status, abort))) break;
+              mma_pv(tO, tS + 8 * k4, desc64(v + k4 * (2048 >> 4)), idPV, (k | k4) ? 1u : 0u);
+            if (!(ok = wait(&pready[2 * t + 1], (Jt + k) & 1, status, abort))) break;
             tc_fence_after();
 #pragma unroll
             for (int k4 = kTK / 32; k4 < kTK / 16; ++k4)
               mma_pv(tO, tS + 8 * k4, desc64(v + k4 * (2048 >> 4)), idPV, 1u);
+          } else {
+            if (!(ok = wait(&turn[t], turns, status, abort))) break;
+            tc_fence_after();
           }
+          turns ^= 1;
           if (next) {
-            uint32_t k = lo_k + ka * (Smem::kK >> 4);
+            uint32_t kd = lo_k + ka * (Smem::kK >> 4);
 #pragma unroll 1
-            for (int term = 0; term <= (fresh ? 1 : 0); ++term, k = lo_k + kb * (Smem::kK >> 4)) s_terms(tS, lo_q, k, idS, term);
+            for (int term = 0; term <= (fresh ? 1 : 0); ++term, kd = lo_k + kb * (Smem::kK >> 4))
+              s_terms(tS, lo_q, kd, idS, term);
           }
           if (lane == 0) mbar_arrive(&turn[t ^ 1]);
-          commit(next ? &sfull[t] : &pvdone[t]);
-          if (j >= 0) commit(&vempty[s]);
+          if (next) commit(&sfull[t]);
+          else if (k >= 0 && k + 1 == own) commit(&pvdone[t]);
+          if (k >= 0 && k < own) commit(&vempty[s]);
           if (next) {
             commit(&kempty[ka]);
             if (fresh) commit(&kempty[kb]);
-            if (j + 2 == n) commit(qempty);
+            kc += fresh ? 2 : 1;
+            if (DUP) kc += jn + 1 >= jfresh ? 2 : 1;
           }
+          if (k + 2 == own || (own == 0 && k < 0)) commit(qempty);  // no later S reads Q
+          j = jn;
         }
         J += n;
+        Jt += own;
+        K += n + max(n - jfresh, 0);
       }
     }
   } else if (warp < 8) {
@@ -364,11 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + kColO + 128 * t;
     bool ok = true;
-    int J = 0, np = 0;
+    int Jt = 0, np = 0;  // own tiles, and pieces that had some
     Piece p;
-    for (int w = w0; ok && next_piece(a, plan, w, w1, p); ++np) {
-      const int n = p.tiles(), bh = p.b * a.Hkv + p.hk;
-      const int ridx = p.row0 + 128 * t + r;
+    for (int w = w0; ok && next_piece(a, plan, w, w1, p);) {
+      const int n = DUP ? (p.tiles() + 1 - t) / 2 : p.tiles(), bh = p.b * a.Hkv + p.hk;
+      const int rpart = DUP ? r : 128 * t + r, ridx = p.row0 + rpart;
+      auto tile = [&](int k) { return DUP ? 2 * k + t : k; };  // own tile k
       const bool valid_row = ridx < grp_rows;
       const int qx = valid_row ? pp.qexp[(size_t)bh * grp_rows + ridx] : 0;
       const int qi = valid_row ? ridx % a.C : 0;
@@ -384,14 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         e[2] = ve[i];
         e[3] = ve[i1];
       };
-      int ex[4], en[4];
-      exps(0, en);
+      int ex[4], en[4] = {};
+      if (n > 0) exps(tile(0), en);
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < n; ++j) {
+      for (int own = 0; own < n; ++own) {
+        const int j = tile(own);
 #pragma unroll
         for (int k = 0; k < 4; ++k) ex[k] = en[k] - kKv8Bias;
-        if (j + 1 < n) exps(j + 1, en);
-        if (!(ok = wait(&sfull[t], (J + j) & 1, status, abort))) break;
+        if (own + 1 < n) exps(tile(own + 1), en);
+        if (!(ok = wait(&sfull[t], (Jt + own) & 1, status, abort))) break;
         tc_fence_after();
         const bool fresh = p.fresh(j);
         const int key0 = (p.t0 + j - (fresh ? p.ntc : 0)) * kTK;
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ke = b ? ex[1] : ex[0], ve = b ? ex[3] : ex[2];
           mx = fmaxf(mx, fmaf(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), scale_log2 * pow2i(qx + ke), (float)ve));
         }
-        if (j == 0) {
+        if (own == 0) {
           m_run = mx;
         } else {
           const bool need = mx > m_run + kLazy;
@@ -477,16 +491,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run = fmaf(x0 + x1, pow2i(-ve), l_run);
         }
       }
-      if (!ok || !(ok = wait(&pvdone[t], np & 1, status, abort))) break;
+      if (!ok || (n > 0 && !(ok = wait(&pvdone[t], np & 1, status, abort)))) break;
       tc_fence_after();
-      const bool whole = p.t0 == 0 && p.t1 == p.nt;
-      const size_t slot = (size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1);
+      const bool whole = !DUP && p.t0 == 0 && p.t1 == p.nt;
+      const size_t slot = ((size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1)) * (DUP ? 2 : 1) + (DUP ? t : 0);
       const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
       __nv_bfloat16* orow = valid_row ? kv8_out_row(a, p.b, p.hk, ridx) : nullptr;
 #pragma unroll 1
       for (int c = 0; c < kHD / 32; ++c) {
         float o[32];
         tmem_ld32(tO + 32 * c, o);
+        if (n == 0) {  // no tile for this row tile: TMEM holds another piece's output
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
         if (c == kHD / 32 - 1) {
           tc_fence_before();
           __syncwarp();
@@ -502,12 +520,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            *kv8_part(a, slot, 8 * c + q, 128 * t + r) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            *kv8_part(a, slot, 8 * c + q, rpart) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           if (c == 0)
-            a.ml[slot * a.prows + 128 * t + r] = make_float2(m_run, l_run);
+            a.ml[slot * a.prows + rpart] = make_float2(m_run, l_run);
         }
       }
-      J += n;
+      Jt += n;
+      np += n > 0;
     }
   }
   __syncthreads();
@@ -598,13 +617,13 @@ cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cud
   if (a.kn && (!make_tmap_2d(&mKn, pp.kterms, kHD, 2 * (uint64_t)pp.krows, kHD, kHD, kTK, true) ||
                !make_tmap_2d(&mVn, pp.vf16, kHD, (uint64_t)pp.krows, kHD * 2, 64, kTK)))
     return cudaErrorInvalidValue;
-  cudaError_t e = set_smem_once<kv8_attn_tc_kernel>(Smem::kTotal);
+  cudaError_t e = a.subs == 2 ? set_smem_once<kv8_attn_tc_kernel<true>>(Smem::kTotal) : set_smem_once<kv8_attn_tc_kernel<false>>(Smem::kTotal);
   if (e != cudaSuccess) return e;
   const int kv_ctas = a.kn ? 2 * a.B * a.Hkv * (pp.Cp / kKv8Block) : 0;
   e = launch_pdl(kv8_prep_kernel, dim3(kv_ctas + cdiv(pp.qrows, 16)), dim3(256), 0, st, a, pp, kv_ctas);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_attn_tc_kernel, dim3(kKv8Ctas), dim3(kThreads), Smem::kTotal, st, mQ, mK, mV, mKn, mVn, a, pp,
-                    1.4426950408889634f / sqrtf((float)kHD));
+  return launch_pdl(a.subs == 2 ? kv8_attn_tc_kernel<true> : kv8_attn_tc_kernel<false>, dim3(kKv8Ctas), dim3(kThreads),
+                    Smem::kTotal, st, mQ, mK, mV, mKn, mVn, a, pp, 1.4426950408889634f / sqrtf((float)kHD));
 }
 
 }  // namespace dg

@@ -223,6 +223,19 @@ CASES = [
     (2, 17, 2, 1, 32, [4500, 100], False, True),
     (4, 1, 4, 4, 128, [6000, 1, 0, 3333], False, False),
     (2, 9, 2, 2, 64, [4097, 4096], True, True),
+    # up to 128 rows on the tensor cores: the row tiles share the rows, each every other key tile
+    (1, 17, 1, 1, 128, [0], False, True),
+    (3, 20, 4, 2, 128, [0, 129, 1], True, True),
+    (2, 32, 4, 1, 128, [3000, 255], False, True),
+    (2, 128, 1, 1, 128, [256, 0], False, False),
+    (5, 25, 10, 2, 128, [64, 640, 0, 127, 1111], True, True),
+    # more sequences than lanes, most of them empty or short
+    (70, 1, 4, 2, 128, [0, 5, 0, 64, 65] * 14, False, False),
+    (40, 3, 2, 1, 32, [1, 0, 0, 0, 99, 4200, 7, 31] * 5, True, True),
+    (36, 40, 2, 2, 128, [0, 200, 1] * 12, False, True),
+    # several row tiles to a kv head
+    (2, 300, 8, 2, 128, [100, 700], True, True),
+    (1, 1024, 2, 1, 64, [70], True, True),
 ]
 
 
