@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();  // the merge, which needs no TMEM, may take the SMs that this kernel leaves
 
   const Kv8Plan plan = kv8_plan(a);
-  const int w0 = min(plan.total, (int)blockIdx.x * plan.share), w1 = min(plan.total, w0 + plan.share);
+  const int w0 = (int)min((long long)plan.total, (long long)blockIdx.x * plan.share);
+  const int w1 = (int)min((long long)plan.total, (long long)w0 + plan.share);
   const int grp_rows = a.Hq / a.Hkv * a.C;
 
   if (warp < 4) {

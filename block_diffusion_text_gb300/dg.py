@@ -496,12 +496,24 @@ class Kv8Cache:
         for t in (K, V, K_exp, V_exp, len, status):
             _need(t.is_cuda and t.device == K.device and t.is_contiguous(),
                   "the cache's tensors are contiguous and on one CUDA device")
-        self.K, self.V, self.K_exp, self.V_exp, self.len, self.status_word = K, V, K_exp, V_exp, len, status
+        self.K, self.V, self.K_exp, self.V_exp, self._len, self.status_word = K, V, K_exp, V_exp, len, status
         self.B, self.Hkv, self.cap, self.hd = B, Hkv, cap, hd
         self.device = K.device
         self.s = dg_kv8_cache(*[t.data_ptr() for t in (K, V, K_exp, V_exp, len, status)], B, Hkv, cap, hd)
         self._ref = ct.byref(self.s)
+        self._lib = load()
         self._ws_bytes, self._ws = {}, {}
+
+    @property
+    def len(self) -> torch.Tensor:
+        """The device lengths that every call reads: int32 [B]."""
+        return self._len
+
+    @len.setter
+    def len(self, value):
+        # the calls hold the tensor's address: an assignment writes into it
+        if value is not self._len:
+            self._len.copy_(value)
 
     @classmethod
     def empty(cls, B, Hkv, cap, hd, device="cuda"):
@@ -523,7 +535,7 @@ class Kv8Cache:
         n = self._ws_bytes.get((C, Hq))
         if n is None:
             z = ct.c_size_t()
-            _check(load().dg_kv8_attention_workspace(self._ref, C, Hq, ct.byref(z)), "dg_kv8_attention_workspace")
+            _check(self._lib.dg_kv8_attention_workspace(self._ref, C, Hq, ct.byref(z)), "dg_kv8_attention_workspace")
             n = self._ws_bytes[(C, Hq)] = z.value
         return n
 
@@ -553,9 +565,10 @@ class Kv8Cache:
 
     def _launch_stream(self, stream):
         """The raw stream of a launch: the library launches on the current device, so that must be the cache's."""
-        if torch.cuda.current_device() != self.device.index:
+        index = self.device.index
+        if torch._C._cuda_getDevice() != index:
             raise ValueError(f"the cache lies on {self.device}, the current device is another")
-        return torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None,
@@ -566,14 +579,16 @@ def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, counts: torch.
     n = k.shape[2] if k.dim() == 4 else -1
     cache._rows(k, cache.Hkv, n, "k")
     cache._rows(v, cache.Hkv, n, "v")
+    cp = None
     if counts is not None:
         _need(counts.shape == (cache.B,) and counts.dtype == torch.int32 and counts.device == cache.device
               and counts.is_contiguous(), f"counts: int32 [{cache.B}] on {cache.device}")
+        cp = counts.data_ptr()
     if n == 0:
         return
-    _check(load().dg_kv8_append(cache._ref, k.data_ptr(), v.data_ptr(), n,
-                                None if counts is None else counts.data_ptr(), cache._launch_stream(stream)),
-           "dg_kv8_append")
+    rc = cache._lib.dg_kv8_append(cache._ref, k.data_ptr(), v.data_ptr(), n, cp, cache._launch_stream(stream))
+    if rc:
+        raise DgError(rc, "dg_kv8_append")
 
 
 def kv8_read(cache: Kv8Cache, row0: int, n: int, out=None, stream=None):
@@ -593,7 +608,9 @@ def kv8_read(cache: Kv8Cache, row0: int, n: int, out=None, stream=None):
         cache._rows(V, cache.Hkv, pitch, "out[1]")
     if n == 0:
         return K, V
-    _check(load().dg_kv8_read(cache._ref, row0, n, K.data_ptr(), V.data_ptr(), K.shape[2], st), "dg_kv8_read")
+    rc = cache._lib.dg_kv8_read(cache._ref, row0, n, K.data_ptr(), V.data_ptr(), K.shape[2], st)
+    if rc:
+        raise DgError(rc, "dg_kv8_read")
     return K, V
 
 
@@ -609,12 +626,13 @@ def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = Non
         raise ValueError("q: bf16 [B, Hq, C, hd]")
     _, Hq, C, _ = q.shape
     cache._rows(q, Hq, C, "q")
-    _need((k is None) == (v is None), "k and v come together")
     kp = vp = None
-    if k is not None:
+    if k is not None and v is not None:
         cache._rows(k, cache.Hkv, C, "k")
         cache._rows(v, cache.Hkv, C, "v")
         kp, vp = k.data_ptr(), v.data_ptr()
+    elif k is not v:
+        raise ValueError("k and v come together")
     st = cache._launch_stream(stream)
     if ws is None:
         wp, wn = cache._workspace(C, Hq, st, stream)
@@ -628,8 +646,10 @@ def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = Non
     elif stream is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
     else:
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(stream):  # memory of the launching stream
             out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    _check(load().dg_kv8_attention(cache._ref, q.data_ptr(), kp, vp, out.data_ptr(), C, Hq, 1 if causal else 0, wp, wn, st),
-           "dg_kv8_attention")
+    rc = cache._lib.dg_kv8_attention(cache._ref, q.data_ptr(), kp, vp, out.data_ptr(), C, Hq, 1 if causal else 0, wp, wn,
+                                     st)
+    if rc:
+        raise DgError(rc, "dg_kv8_attention")
     return out

@@ -424,6 +424,20 @@ def test_captured_decoding_follows_the_growing_cache():
         assert a.status() == b.status() == 0
 
 
+def test_assigned_lengths_reach_the_calls():
+    """cache.len = .. writes into the tensor whose address the calls hold."""
+    g = torch.Generator().manual_seed(34)
+    c = filled(g, 2, 1, 200, 64, [150, 70])
+    q = rows(g, 2, 1, 1, 64)
+    c.len = c.len - 50
+    assert c.len.tolist() == [100, 20]
+    check_attention(c, q, None, None, False)
+    c.len = torch.tensor([3, 150], dtype=torch.int32)
+    assert c.s.len == c.len.data_ptr()
+    K, V = dg.kv8_read(c, 0, 200)
+    assert torch.count_nonzero(K[0, :, 3:]).item() == 0
+
+
 def test_two_graphs_in_a_row_share_a_workspace():
     g = torch.Generator().manual_seed(33)
     c1, c2 = filled(g, 2, 2, 900, 128, [900, 3]), filled(g, 2, 2, 500, 128, [0, 499])
