@@ -222,7 +222,7 @@ dg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DG_OK : DG_ERR_CU
 
 int kv8_blocks(int cap) { return cdiv(cap, kKv8Block); }
 
-constexpr int kLocalTiles = 64;
+constexpr int kLocalTiles = 64, kSmallTiles = 24;
 constexpr int kKv8Ovh = 3;  // measured: a unit's start and output take as long as some three tiles
 
 struct Kv8Ws {
@@ -235,7 +235,13 @@ struct Kv8Ws {
 Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   Kv8Ws w{};
   const int64_t R = (int64_t)(Hq / c->Hkv) * C;
-  w.tc = c->hd == 128 && R > 16;
+  const int tiles = cdiv(c->cap, kKv8Block) + cdiv(C, kKv8Block);
+  // The tensor-core kernel takes more than 16 rows, but for calls that the warps
+  // finish in one launch and one wave of short CTAs: 8 sequences of 1000 rows, 128
+  // query rows to a head, 13 us against 26; longer caches go the other way (2000
+  // rows, 40 query rows: 17.7 us of kernel time against 13.0).
+  const bool small = tiles <= kSmallTiles && (int64_t)c->B * c->Hkv * cdiv(R, 16) <= kKv8Ctas;
+  w.tc = c->hd == 128 && R > 16 && !small;
   w.subs = w.tc && R <= 128 ? 2 : 1;  // one row tile is enough: the two take every other key tile
   w.rows = w.tc ? 256 / w.subs : kv8_mma_rows(c->hd, R);
   w.tk = w.tc ? 128 : kKv8Block;
@@ -250,7 +256,7 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   };
   // A short cache's units are finished by one CTA each: no parts in memory, no
   // merge kernel.
-  w.local = !w.tc && cdiv(c->cap, w.tk) + cdiv(C, w.tk) <= kLocalTiles;
+  w.local = !w.tc && tiles <= kLocalTiles;
   if (w.local) return w;
   w.part = take((size_t)2 * w.workers * w.subs * w.prows * c->hd * 4);
   w.ml = take((size_t)2 * w.workers * w.subs * w.prows * 8);

@@ -241,43 +241,46 @@ CASES = [
 
 @pytest.mark.parametrize("case", CASES, ids=[f"b{c[0]}c{c[1]}q{c[2]}k{c[3]}h{c[4]}l{max(c[5])}{'c' * c[6]}{'n' * c[7]}"
                                              for c in CASES])
-def test_attention(case):
+@pytest.mark.parametrize("room", [3, 1600])
+def test_attention(case, room):
+    """Each case in a cache with hardly any room left and in one with more, which takes other kernels."""
     B, C, Hq, Hkv, hd, lens, causal, new = case
     g = torch.Generator().manual_seed(sum(lens) + C)
-    c = filled(g, B, Hkv, max(lens) + 3, hd, lens)
+    c = filled(g, B, Hkv, max(lens) + room, hd, lens)
     q = rows(g, B, Hq, C, hd)
     k, v = (rows(g, B, Hkv, C, hd), rows(g, B, Hkv, C, hd)) if new else (None, None)
     check_attention(c, q, k, v, causal)
 
 
-@pytest.mark.parametrize("C,hd", [(1, 128), (8, 64), (256, 128)])
-def test_attention_follows_scales_of_many_octaves(C, hd):
+@pytest.mark.parametrize("C,hd,cap", [(1, 128, 640), (8, 64, 640), (256, 128, 640), (256, 128, 5000), (30, 128, 5000),
+                                      (1, 128, 5000)])
+def test_attention_follows_scales_of_many_octaves(C, hd, cap):
     """Key and value scales that differ by many octaves from block to block, with small queries: the value scale is
     part of the running maximum, the key scale of each block's softmax factor."""
     g = torch.Generator().manual_seed(21)
     lens = [640, 333]
-    c = filled(g, 2, 2, 640, hd, lens)
+    c = filled(g, 2, 2, cap, hd, lens)
     c.V_exp[:] = torch.randint(100, 150, tuple(c.V_exp.shape), generator=g).to(torch.uint8).cuda()
     c.K_exp[:] = torch.randint(105, 121, tuple(c.K_exp.shape), generator=g).to(torch.uint8).cuda()
     q = rows(g, 2, 4, C, hd)
     check_attention(c, q, rows(g, 2, 2, C, hd) , rows(g, 2, 2, C, hd), False)
 
 
-@pytest.mark.parametrize("C,hd", [(1, 128), (1, 32), (256, 128)])
-def test_attention_of_peaked_rows(C, hd):
+@pytest.mark.parametrize("C,hd,cap", [(1, 128, 500), (1, 32, 500), (256, 128, 500), (256, 128, 3000), (40, 128, 3000)])
+def test_attention_of_peaked_rows(C, hd, cap):
     """Scores of some hundreds: almost all weight on one key, first in one row and last in another."""
     g = torch.Generator().manual_seed(22)
-    c = filled(g, 1, 1, 500, hd, [451])
+    c = filled(g, 1, 1, cap, hd, [451])
     q = rows(g, 1, 2, C, hd) * 20
     check_attention(c, q.to(torch.bfloat16), rows(g, 1, 1, C, hd), rows(g, 1, 1, C, hd), False)
 
 
-@pytest.mark.parametrize("C,hd", [(2, 128), (2, 64), (200, 128)])
-def test_attention_scales_queries_exactly(C, hd):
+@pytest.mark.parametrize("C,hd,cap", [(2, 128, 200), (2, 64, 200), (200, 128, 200), (200, 128, 3000), (30, 128, 3000)])
+def test_attention_scales_queries_exactly(C, hd, cap):
     """Queries of 2^-40 and 2^30, zero rows among them, and one element 2^12 times the others: the power-of-two
     scaling of a row keeps what its scores need."""
     g = torch.Generator().manual_seed(23)
-    c = filled(g, 1, 2, 200, hd, [190])
+    c = filled(g, 1, 2, cap, hd, [190])
     for f in (2.0 ** -40, 1.0):
         q = rows(g, 1, 4, C, hd) * f
         q[0, 1, 0] = 0
@@ -290,8 +293,8 @@ def test_attention_scales_queries_exactly(C, hd):
 
 def test_attention_without_any_key_is_zero():
     g = torch.Generator().manual_seed(24)
-    for C, hd in ((1, 128), (5, 32), (200, 128)):
-        c = filled(g, 2, 1, 64, hd, [0, 0])
+    for C, hd, cap in ((1, 128, 64), (5, 32, 64), (200, 128, 64), (200, 128, 3000), (20, 128, 3000), (1, 64, 5000)):
+        c = filled(g, 2, 1, cap, hd, [0, 0])
         out = torch.full((2 * C, 2 * hd), 9.0, dtype=torch.bfloat16, device="cuda")
         dg.kv8_attention(c, rows(g, 2, 2, C, hd).cuda(), out=out)
         assert torch.count_nonzero(out).item() == 0
@@ -300,8 +303,8 @@ def test_attention_without_any_key_is_zero():
 def test_attention_writes_its_output_alone():
     """Bytes around the output and behind the workspace keep their values; the cache is read only."""
     g = torch.Generator().manual_seed(25)
-    for C in (1, 70):
-        c = filled(g, 2, 2, 400, 128, [399, 17])
+    for C, cap in ((1, 400), (70, 400), (1, 5000), (70, 5000), (20, 5000)):
+        c = filled(g, 2, 2, cap, 128, [399, 17])
         before = state(c)
         q, k, v = rows(g, 2, 4, C, 128).cuda(), rows(g, 2, 2, C, 128).cuda(), rows(g, 2, 2, C, 128).cuda()
         need = c.workspace_bytes(C, 4)
@@ -316,8 +319,8 @@ def test_attention_writes_its_output_alone():
 
 def test_results_repeat_bit_for_bit():
     g = torch.Generator().manual_seed(26)
-    for C in (1, 256):
-        c = filled(g, 5, 2, 3000, 128, [3000, 1, 0, 1555, 64])
+    for C, cap in ((1, 3000), (256, 3000), (16, 3000), (1, 5000)):
+        c = filled(g, 5, 2, cap, 128, [3000, 1, 0, 1555, 64])
         q, k, v = rows(g, 5, 8, C, 128).cuda(), rows(g, 5, 2, C, 128).cuda(), rows(g, 5, 2, C, 128).cuda()
         first = dg.kv8_attention(c, q, k, v)
         for _ in range(5):
