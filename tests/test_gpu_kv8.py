@@ -154,6 +154,31 @@ def test_read_is_exact_and_keeps_other_rows(hd, row0, n, pitch):
     assert c.status() == 0
 
 
+@pytest.mark.parametrize("hd", [32, 128])
+def test_outputs_aligned_to_16_bytes_only(hd):
+    """Outputs, queries and new rows that begin 16 bytes into an allocation."""
+    g = torch.Generator().manual_seed(12)
+    c = filled(g, 2, 1, 100, hd, [100, 50])
+
+    def shifted(t):
+        flat = torch.zeros(t.numel() + 8, dtype=t.dtype, device="cuda")
+        flat[8:] = t.flatten().cuda()
+        return flat[8:].view(t.shape)
+    out = [shifted(torch.full((2, 1, 90, hd), 7.0).to(torch.bfloat16)) for _ in range(2)]
+    assert out[0].data_ptr() % 32 == 16
+    for a, b in zip(dg.kv8_read(c, 10, 90, out=out), dg.kv8_read(c, 10, 90)):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1, :, :40], b[1, :, :40]) and (a[1, :, 40:] == 7).all()
+    q, k, v = rows(g, 2, 2, 3, hd), rows(g, 2, 1, 3, hd), rows(g, 2, 1, 3, hd)
+    o = shifted(torch.zeros(6, 2 * hd, dtype=torch.bfloat16))
+    assert torch.equal(dg.kv8_attention(c, shifted(q), shifted(k), shifted(v), out=o),
+                       dg.kv8_attention(c, q.cuda(), k.cuda(), v.cuda()))
+    c.len -= 10
+    one, two = [dg.Kv8Cache(*[t.clone() for t in (c.K, c.V, c.K_exp, c.V_exp, c.len)]) for _ in range(2)]
+    dg.kv8_append(one, shifted(k), shifted(v))
+    dg.kv8_append(two, k.cuda(), v.cuda())
+    assert torch.equal(one.K, two.K) and torch.equal(one.V, two.V)
+
+
 def test_read_covers_every_code_and_extreme_scales():
     for e in (63, 64, 120, 127, 200, 245):
         codes = torch.arange(256, dtype=torch.uint8).reshape(1, 1, 4, 64)
