@@ -35,7 +35,9 @@ DG_DEV int kv8_exponent(unsigned bits) {
 // One CTA per (block of 64 cached rows, kv head and sequence, K or V): the new
 // rows that fall into the block stay in registers between the reduction of
 // their maximum and the rounding, so every input is read once.  16 values per
-// thread and chunk: two 16-byte loads, one 16-byte store.  Bound by memory.
+// thread and chunk: two 16-byte loads, one 16-byte store.  Bound by memory: 4
+// sequences of 16384 rows and 8 heads 59.0 us (floor at the measured copy rate
+// 59.2); one row each of 32 sequences 2.5 us, a launch.
 template <int HD>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(Kv8AppendArgs a) {
   pdl_wait();

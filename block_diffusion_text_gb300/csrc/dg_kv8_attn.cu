@@ -29,6 +29,9 @@
 //    an eighth of the rounding of the bf16 output.
 // New tokens' bf16 keys and values keep their exponent range: bf16 MMAs, P
 // split into two bf16 parts (2^-17).
+// Measured: one token of 4 sequences over 131072 rows of 8 heads 167 us (6.4 TB/s,
+// 94 % of the measured copy rate), of 32 sequences of 0 to 8192 rows 48 us (5.2
+// TB/s; the start and the merge take some 8 us), of one over 2048 rows 11 us.
 #include <cfloat>
 
 #include "dg_kv8.cuh"

@@ -394,8 +394,8 @@ DG_API dg_status dg_attention_noalloc_status(int32_t* status, void* stream);
  * they describe no cache format, this one is the library's own).
  *   K, V    uint8 [B][Hkv][cap][hd] device: E4M3 codes, 16-byte aligned, keys
  *           already rotated by RoPE
- *   K_exp, V_exp  uint8 [B][Hkv][ceil(cap / 64)] device: one exponent byte x per
- *           block of 64 rows and head; a cached value is code * 2^(x - 127)
+ *   K_exp, V_exp  uint8 [B][Hkv][ceil(cap / 64)] device: one exponent byte x, 63 to
+ *           245, per block of 64 rows and head; a cached value is code * 2^(x - 127)
  *   len     int32 [B] device: rows 0..len[b]-1 of sequence b are valid.  The
  *           sequences' lengths are the device's: the calls below read them when
  *           they run, so a captured graph follows a growing cache.  No call
@@ -451,11 +451,14 @@ DG_API dg_status dg_kv8_read(const dg_kv8_cache* cache, int32_t row0, int32_t n,
  * step); causal = 1: token i sees new tokens 0..i (a prompt piece).  C = 1 is the
  * single-token form.  Sequences of any lengths share a call (0 included; the
  * work is divided by keys, not by sequences); a row without any key is zero.
- * k and v must be finite, the ones a causal mask hides included; what lies
- * behind len is never used.  Bounds as dg_attention_noalloc: C <= 1024,
- * B * C <= 2^20, B * Hq <= 65535.  ws: dg_kv8_attention_workspace bytes (0 for a
- * short cache: ws may be NULL then), 256-byte aligned, contents of no matter;
- * calls (and graphs) that may overlap on the GPU need one each.              */
+ * q, k and v must be finite, the new ones a causal mask hides included, and o
+ * must not overlap an input; what lies behind len is never used.  Probabilities
+ * enter the product as f16 on the scale of the row's largest, block by block:
+ * a contribution below 2^-33 of the largest is lost.  Bounds as
+ * dg_attention_noalloc: C <= 1024, B * C <= 2^20, B * Hq <= 65535.  ws:
+ * dg_kv8_attention_workspace bytes (0 for a short cache: ws may be NULL then),
+ * 256-byte aligned, contents of no matter; calls (and graphs) that may overlap
+ * on the GPU need one each.                                                   */
 DG_API dg_status dg_kv8_attention_workspace(const dg_kv8_cache* cache, int32_t C, int32_t Hq, size_t* bytes);
 DG_API dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, const void* k, const void* v, void* o,
                                   int32_t C, int32_t Hq, int32_t causal, void* ws, size_t ws_bytes, void* stream);
