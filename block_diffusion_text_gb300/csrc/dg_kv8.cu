@@ -25,13 +25,6 @@ struct Kv8AppendArgs {
 
 constexpr int kAppendThreads = 256;
 
-// Smallest e with absmax <= 448 2^e, from absmax's bf16 bits: 448 = 1.75 2^8.
-DG_DEV int kv8_exponent(unsigned bits) {
-  const int E = (int)(bits >> 7), m = (int)(bits & 127u);
-  const int e = E - 127 - 8 + (m > 96 ? 1 : 0);
-  return E == 0 ? kKv8Emin : min(max(e, kKv8Emin), kKv8Emax);
-}
-
 // One CTA per (block of 64 cached rows, kv head and sequence, K or V): the new
 // rows that fall into the block stay in registers between the reduction of
 // their maximum and the rounding, so every input is read once.  16 values per
@@ -73,11 +66,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(Kv8AppendArg
       x[p][1] = __ldcs(s + 1);
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 w = x[p][h];
-      top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
-                                   __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-    }
+    for (int h = 0; h < 2; ++h) top = __vmaxu2(top, abs_top(x[p][h]));
   }
   auto block_max = [&](unsigned t) {
     t = max(t & 0xffffu, t >> 16);
@@ -109,7 +98,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(Kv8AppendArg
     __syncthreads();  // red is read above
     amax = block_max(top);
   }
-  int e = kv8_exponent(amax);
+  int e = top_exponent(amax);
   if (lo > 0) {
     // Earlier rows share the block: its scale never shrinks, and where it
     // grows their codes move to it.

@@ -10,6 +10,11 @@ namespace dg {
 constexpr int kKv8Block = 64;             // cached tokens per scale
 constexpr int kKv8Bias = 127;             // exponent byte x: scale 2^(x - 127)
 constexpr int kKv8Emin = -64, kKv8Emax = 118;
+// Largest value scale attention takes.  A probability carries its block's value
+// scale, p' = 2^(s + e - m + 8) with m the largest s + e; on blocks 2^104 below
+// the largest scale it still has 2^30 above the smallest fp32, and the row's sum
+// gets it back exactly; further down the sum would lose it.
+constexpr int kKv8EmaxAttn = 40;
 constexpr int kKv8Ctas = kTargetCtas;     // CTAs of an attention launch (one per SM)
 // Warps (workers) per CTA of the warp-MMA kernel for units of `rows` rows: as
 // many as their registers allow.
@@ -181,7 +186,7 @@ DG_DEV void unpack8(const uint4& w, float f, float (&x)[8]) {
 DG_DEV unsigned abs_top(const uint4& w) {
   return __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
 }
-// Exponent that brings a largest magnitude (bf16 bits) into (224, 448].
+// Smallest e with a largest magnitude <= 448 2^e, from its bf16 bits: 448 = 1.75 2^8.
 DG_DEV int top_exponent(unsigned bits) {
   const int E = (int)(bits >> 7), m = (int)(bits & 127u);
   return E == 0 ? kKv8Emin : min(max(E - 127 - 8 + (m > 96 ? 1 : 0), kKv8Emin), kKv8Emax);

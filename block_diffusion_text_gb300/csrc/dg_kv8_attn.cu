@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(32 * W, 1)
         for (int k = 0; k < 4; ++k) acc.o[nt][i][k] = 0.f;
     }
 
-    int ke_next = 0, ve_next = 0, ke = 0, ve = 0;
+    int ke_next = 0, ve_next = 0, ke = 0, ve = 0, ve_top = kKv8Emin;
     if (nsteps > 0) {
       ke_next = Ke[t0];
       ve_next = Ve[t0];
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(32 * W, 1)
       if (i % (kKv8Block / kStep) == 0) {
         ke = ke_next - kKv8Bias;
         ve = ve_next - kKv8Bias;
+        ve_top = max(ve_top, ve);
         const int nx = t0 + i / (kKv8Block / kStep) + 1;
         if (nx < tc1) {
           ke_next = Ke[nx];
@@ -463,6 +464,7 @@ __global__ void __launch_bounds__(32 * W, 1)
     // them where this kernel is used.
     const __nv_bfloat16* kn = reinterpret_cast<const __nv_bfloat16*>(a.kn) + bh * a.C * HD;
     const __nv_bfloat16* vn = reinterpret_cast<const __nv_bfloat16*>(a.vn) + bh * a.C * HD;
+    unsigned vn_top = 0;
 #pragma unroll 1
     for (int key0 = (max(t0, ntc) - ntc) * kKv8Block, end = min((t1 - ntc) * kKv8Block, a.C); key0 < end;
          key0 += kStep) {
@@ -522,7 +524,10 @@ __global__ void __launch_bounds__(32 * W, 1)
         for (int i = 0; i < KS; ++i) {
           uint32_t vw[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) vw[q] = vr[q] ? *reinterpret_cast<const uint32_t*>(vr[q] + 2 * i) : 0u;
+          for (int q = 0; q < 4; ++q) {
+            vw[q] = vr[q] ? *reinterpret_cast<const uint32_t*>(vr[q] + 2 * i) : 0u;
+            vn_top = __vmaxu2(vn_top, vw[q] & 0x7fff7fffu);
+          }
           const uint32_t va[4] = {__byte_perm(vw[0], vw[1], 0x5410u), __byte_perm(vw[0], vw[1], 0x7632u),
                                   __byte_perm(vw[2], vw[3], 0x5410u), __byte_perm(vw[2], vw[3], 0x7632u)};
 #pragma unroll
@@ -533,6 +538,7 @@ __global__ void __launch_bounds__(32 * W, 1)
         }
       }
     }
+    if (max(ve_top, top_exponent(max(vn_top & 0xffffu, vn_top >> 16))) > kKv8EmaxAttn) atomicExch(a.status, kStatusValue);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -403,7 +403,8 @@ DG_API dg_status dg_attention_noalloc_status(int32_t* status, void* stream);
  *   status  int32 device word, zeroed by the caller before its first use; kernels
  *           set DG_ERR_CAPACITY (a length outside [0, cap], or an append past
  *           cap), DG_ERR_ARG (an append count outside [0, n]) or DG_ERR_VALUE (a
- *           non-finite value appended); read it with dg_read_status
+ *           non-finite value appended, or a value that attention does not take: its
+ *           entry below); read it with dg_read_status
  *   hd is 32, 64 or 128; B * Hkv <= 65535; B * Hkv * cap < 2^31 - 2^16.  The caches
  *   of several layers are as many dg_kv8_cache structs sharing len and status.
  * 2^(x - 127) is a power of two, so code * scale is exact in bf16 and a code is the
@@ -451,14 +452,16 @@ DG_API dg_status dg_kv8_read(const dg_kv8_cache* cache, int32_t row0, int32_t n,
  * step); causal = 1: token i sees new tokens 0..i (a prompt piece).  C = 1 is the
  * single-token form.  Sequences of any lengths share a call (0 included; the
  * work is divided by keys, not by sequences); a row without any key is zero.
- * q, k and v must be finite, the new ones a causal mask hides included, and o
- * must not overlap an input; what lies behind len is never used.  Probabilities
- * enter the product as f16 on the scale of the row's largest, block by block:
- * a contribution below 2^-33 of the largest is lost.  Bounds as
- * dg_attention_noalloc: C <= 1024, B * C <= 2^20, B * Hq <= 65535.  ws:
- * dg_kv8_attention_workspace bytes (0 for a short cache: ws may be NULL then),
- * 256-byte aligned, contents of no matter; calls (and graphs) that may overlap
- * on the GPU need one each.                                                   */
+ * q, k and v must be finite, the new ones a causal mask hides included, as must
+ * the scores be in fp32; o must not overlap an input; what lies behind len is
+ * never used.  Values go up to 448 * 2^40 in magnitude (V_exp bytes up to 167):
+ * where a larger one is met the status word gets DG_ERR_VALUE, and the output is
+ * not to be used.  Probabilities enter the product as f16 on the scale of the
+ * row's largest, block by block: a contribution below 2^-33 of the largest is
+ * lost.  Bounds as dg_attention_noalloc: C <= 1024, B * C <= 2^20,
+ * B * Hq <= 65535.  ws: dg_kv8_attention_workspace bytes (0 for a short cache: ws
+ * may be NULL then), 256-byte aligned, contents of no matter; calls (and graphs)
+ * that may overlap on the GPU need one each.                                  */
 DG_API dg_status dg_kv8_attention_workspace(const dg_kv8_cache* cache, int32_t C, int32_t Hq, size_t* bytes);
 DG_API dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, const void* k, const void* v, void* o,
                                   int32_t C, int32_t Hq, int32_t causal, void* ws, size_t ws_bytes, void* stream);

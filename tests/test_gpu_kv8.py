@@ -316,6 +316,43 @@ def test_attention_scales_queries_exactly(C, hd, cap):
     check_attention(c, q, None, None, False)
 
 
+WIDE = [(1, 128, 400), (1, 128, 5000), (20, 32, 400), (9, 64, 5000), (40, 128, 5000), (256, 128, 5000)]
+
+
+@pytest.mark.parametrize("C,hd,cap", WIDE)
+def test_attention_over_blocks_of_zeros_and_large_values(C, hd, cap):
+    """Values of 2^48 beside blocks of zeros, whose scale is the smallest: 2^104 between the scales, and equal
+    weights.  The zeros' probabilities count in full in the row's sum."""
+    g = torch.Generator().manual_seed(35)
+    c = filled(g, 1, 2, cap, hd, [390])
+    for blk in (0, 2, 3, 5):
+        c.V[:, :, 64 * blk:min(64 * blk + 64, 390)] = 0
+        c.V_exp[:, :, blk] = 63
+    for blk in (1, 4):
+        c.V_exp[:, :, blk] = 167
+    c.V_exp[:, 1, 6] = 63
+    q = rows(g, 1, 4, C, hd) * 0.1
+    check_attention(c, q, rows(g, 1, 2, C, hd), rows(g, 1, 2, C, hd), False)
+
+
+@pytest.mark.parametrize("C,hd,cap", WIDE)
+def test_attention_reports_values_it_does_not_take(C, hd, cap):
+    g = torch.Generator().manual_seed(36)
+    q, k, v = rows(g, 1, 4, C, hd).cuda(), rows(g, 1, 2, C, hd).cuda(), rows(g, 1, 2, C, hd).cuda()
+    c = filled(g, 1, 2, cap, hd, [390])
+    c.V_exp[0, 1, 3] = 168
+    dg.kv8_attention(c, q, k, v)
+    assert c.status() == dg.DG_ERR_VALUE
+    c = filled(g, 1, 2, cap, hd, [390])
+    big = v.clone()
+    big[0, 1, C - 1, 5] = 448 * 2.0 ** 40
+    dg.kv8_attention(c, q, k, big)
+    assert c.status() == dg.DG_OK
+    big[0, 1, C - 1, 5] = 450 * 2.0 ** 40
+    dg.kv8_attention(c, q, k, big)
+    assert c.status() == dg.DG_ERR_VALUE
+
+
 def test_attention_without_any_key_is_zero():
     g = torch.Generator().manual_seed(24)
     for C, hd, cap in ((1, 128, 64), (5, 32, 64), (200, 128, 64), (200, 128, 3000), (20, 128, 3000), (1, 64, 5000)):
