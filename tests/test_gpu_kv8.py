@@ -277,6 +277,28 @@ def test_attention(case, room):
     check_attention(c, q, k, v, causal)
 
 
+EDGES = [
+    # B, C, Hq, Hkv, hd, lens, cap, causal: the smallest call, many sequences, many heads to one kv head, the longest
+    # pieces, and caches filled to the last row
+    (1, 1, 1, 1, 32, [1], 1, True),
+    (2500, 1, 1, 1, 32, [0, 1] * 1250, 1, False),
+    (200, 2, 2, 1, 32, [0, 4200, 1, 64, 100] * 40, 4200, True),
+    (1, 1, 2048, 1, 128, [300], 300, False),
+    (1, 1, 2048, 1, 64, [300], 5000, False),
+    (1, 1024, 1, 1, 32, [0], 5000, True),
+    (2, 1024, 2, 1, 128, [64, 65], 65, True),
+    (1, 1, 65535, 1, 32, [3], 3, False),
+]
+
+
+@pytest.mark.parametrize("case", EDGES, ids=[f"b{c[0]}c{c[1]}q{c[2]}h{c[4]}cap{c[6]}" for c in EDGES])
+def test_attention_at_the_ends_of_its_range(case):
+    B, C, Hq, Hkv, hd, lens, cap, causal = case
+    g = torch.Generator().manual_seed(cap + C)
+    c = filled(g, B, Hkv, cap, hd, lens)
+    check_attention(c, rows(g, B, Hq, C, hd), rows(g, B, Hkv, C, hd), rows(g, B, Hkv, C, hd), causal)
+
+
 @pytest.mark.parametrize("C,hd,cap", [(1, 128, 640), (8, 64, 640), (256, 128, 640), (256, 128, 5000), (30, 128, 5000),
                                       (1, 128, 5000)])
 def test_attention_follows_scales_of_many_octaves(C, hd, cap):
@@ -435,6 +457,41 @@ def test_on_another_stream():
     assert torch.equal(got, want)
     K2, V2 = dg.kv8_read(c, 0, 300)
     assert torch.equal(K, K2) and torch.equal(V, V2)
+
+
+def test_calls_on_two_streams_at_once():
+    """The workspaces that the cache keeps by itself are a stream's own: calls of one cache that overlap on the GPU,
+    of sizes that grow the workspace in between, give what they give alone."""
+    g = torch.Generator().manual_seed(37)
+    c = filled(g, 4, 2, 9000, 128, [9000, 1, 4000, 8111])
+    sizes = (1, 40, 3, 256)
+    x = {C: [rows(g, 4, h, C, 128).cuda() for h in (8, 2, 2)] for C in sizes}
+    want = {C: dg.kv8_attention(c, *x[C]) for C in sizes}
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(10):
+        for j, st in enumerate(streams):
+            C = sizes[(i + 2 * j) % 4]
+            got.append((C, dg.kv8_attention(c, *x[C], stream=st)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[C]) for C, o in got)
+    # two graphs, each with a workspace from its own pool, replayed side by side
+    graphs = []
+    for C in (40, 1):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            o = dg.kv8_attention(c, *x[C])
+        graphs.append((C, gr, o))
+    for _ in range(5):
+        for _, _, o in graphs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for st, (_, gr, _) in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want[C]) for C, _, o in graphs)
 
 
 def test_captured_decoding_follows_the_growing_cache():
