@@ -38,7 +38,11 @@
 // softmax 2100 to 2300 cycles, P V and the next S 1250) bounds it: without the
 // exponentials it runs 107 us, without all softmax work 83.  Tried and slower:
 // two threads a row (24 warps of 80 registers, 123 us; 20 of 96, 168 us), the
-// scores read once block by block (123 to 129), MMA warps without turns (143).
+// scores read once block by block (123 to 129), the probabilities made on the old
+// maximum in one pass and again where it grew (135), loads 32 columns ahead (129),
+// scores of 64 keys at a time, two of them in flight to a row tile (126 to 129:
+// the softmax no longer waits, but an MMA of 64 columns takes as long as one of
+// 128 and the MMA warps have twice the turns), MMA warps without turns (143).
 #include <cfloat>
 
 #include "dg_kv8.cuh"
