@@ -210,13 +210,29 @@ dg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DG_OK : DG_ERR_CU
 
 int kv8_blocks(int cap) { return cdiv(cap, kKv8Block); }
 
-constexpr int kLocalTiles = 64, kSmallTiles = 24;
+// Key tiles to a CTA of a cluster, above which shares balance better than they
+// cost: 8 ragged sequences of up to 8000 rows, 8 heads, 15.2 us in shares, 19.5 with
+// two CTAs a unit; up to 4000 rows 13.2 against 12.6.
+constexpr int kClusterTiles = 64;
 constexpr int kKv8Ovh = 3;  // measured: a unit's start and output take as long as some three tiles
+
+// CTAs that share a unit of `tiles` key tiles, of `units` in the call: as many
+// as give every warp half a tile, while all clusters run at once (what
+// cudaOccupancyMaxActiveClusters answers for clusters of 2 to 8 CTAs of the
+// warp-MMA kernel, one to an SM; a second wave costs more: 16 units of 4000 rows
+// 14.2 us with 8 CTAs each, 8.3 with 6), one where its own warps suffice.
+int kv8_cluster(int64_t units, int tiles, int warps) {
+  constexpr int kFit[kMaxCluster + 1] = {0, 0, 76, 46, 36, 28, 23, 15, 15};
+  int n = 1;
+  if (tiles > warps)
+    while (n < kMaxCluster && n * warps < 2 * tiles && units <= kFit[n + 1]) ++n;
+  return n;
+}
 
 struct Kv8Ws {
   size_t part, ml, qterms, qexp, kterms, vf16, kexp, vexp, total;
-  int rows, tk, units, workers, prows, subs, Cp;
-  bool tc, local;
+  int rows, tk, units, workers, prows, subs, cluster, Cp;
+  bool tc;
 };
 
 // The kernel, its rows per unit, and the workspace of an attention call.
@@ -225,11 +241,15 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   const int64_t R = (int64_t)(Hq / c->Hkv) * C;
   const int tiles = cdiv(c->cap, kKv8Block) + cdiv(C, kKv8Block);
   // The tensor-core kernel takes more than 16 rows, but for calls that the warps
-  // finish in one launch and one wave of short CTAs: 8 sequences of 1000 rows, 128
-  // query rows to a head, 13 us against 26; longer caches go the other way (2000
-  // rows, 40 query rows: 17.7 us of kernel time against 13.0).
-  const bool small = tiles <= kSmallTiles && (int64_t)c->B * c->Hkv * cdiv(R, 16) <= kKv8Ctas;
-  w.tc = c->hd == 128 && R > 16 && !small;
+  // finish in one launch and one wave with a few tiles each (new tokens' tiles
+  // take a warp twice as long): 64 query rows to a head, 4000 rows, 8 heads 13.0 us
+  // against 15.7; 256 rows, 1500 rows, 2 heads 12.0 against 14.5; with more tiles
+  // to a warp it turns: 64 rows, 8000 rows, 16 heads 32.4 against 25.7, 256 rows,
+  // 2000 rows, 4 heads 15.7 against 15.4.
+  const int64_t all16 = (int64_t)c->B * c->Hkv * ((R + 15) / 16);
+  const int warps16 = kv8_mma_warps(128, 16) * kv8_cluster(all16, tiles, kv8_mma_warps(128, 16));
+  const bool few = all16 <= kKv8Ctas && tiles <= (C <= kKv8Block ? 4 : 1) * warps16;
+  w.tc = c->hd == 128 && R > 16 && !few;
   w.subs = w.tc && R <= 128 ? 2 : 1;  // one row tile is enough: the two take every other key tile
   w.rows = w.tc ? 256 / w.subs : kv8_mma_rows(c->hd, R);
   w.tk = w.tc ? 128 : kKv8Block;
@@ -242,10 +262,17 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
     off = align_up(off + bytes, 256);
     return o;
   };
-  // A short cache's units are finished by one CTA each: no parts in memory, no
-  // merge kernel.
-  w.local = !w.tc && tiles <= kLocalTiles;
-  if (w.local) return w;
+  if (!w.tc) {
+    // A short cache's units are finished by a cluster of CTAs each, without parts
+    // in memory and a merge kernel.  One token of one sequence, 2 kv heads, with
+    // and without: 4000 rows 7.5 and 9.4 us, 8000 9.6 and 12.1, 32000 20.0 and
+    // 28.4; 8 heads 32000 rows 20.0 and 21.1.
+    const int n = kv8_cluster((int64_t)c->B * w.units, tiles, kv8_mma_warps(c->hd, w.rows));
+    if (tiles <= kClusterTiles * n) {
+      w.cluster = n;
+      return w;
+    }
+  }
   w.part = take((size_t)2 * w.workers * w.subs * w.prows * c->hd * 4);
   w.ml = take((size_t)2 * w.workers * w.subs * w.prows * 8);
   if (w.tc) {
@@ -367,7 +394,7 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   a.ovh = kKv8Ovh;
   a.subs = w.subs;
   a.prows = w.prows;
-  a.local = w.local;
+  a.cluster = w.cluster;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (w.tc) {
@@ -377,6 +404,6 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   } else {
     e = launch_kv8_attention_mma(a, st);
   }
-  if (e == cudaSuccess && !w.local) e = launch_kv8_merge(a, st);
+  if (e == cudaSuccess && !w.cluster) e = launch_kv8_merge(a, st);
   return from_cuda(e);
 }

@@ -19,6 +19,7 @@ constexpr int kKv8Ctas = kTargetCtas;     // CTAs of an attention launch (one pe
 // Warps (workers) per CTA of the warp-MMA kernel for units of `rows` rows: as
 // many as their registers allow.
 constexpr int kv8_mma_warps(int hd, int rows) { return rows * hd <= 1024 ? 12 : 8; }
+constexpr int kMaxCluster = 8;            // CTAs that finish a unit of a short cache together
 constexpr int kStatusArg = 1, kStatusCapacity = 3;  // DG_ERR_ARG, DG_ERR_CAPACITY
 
 // One attention call.  A unit is one row tile of one (sequence, kv head): the
@@ -42,7 +43,7 @@ struct Kv8AttnArgs {
   int subs;                  // parts of a piece: 2 where the tensor-core kernel's two row tiles share the rows
   int ovh;                   // what beginning a unit costs a worker, in tiles
   int prows;                 // rows of a part: min(rows, G C)
-  int local;                 // warp-MMA kernel: one CTA per unit, its warps' parts merged in shared memory
+  int cluster;               // warp-MMA kernel: CTAs per unit, their warps' parts merged in shared memory (0: shares)
 };
 
 // All work of a call, in the order (sequence, unit, tile), is dealt to the

@@ -29,9 +29,10 @@
 //    an eighth of the rounding of the bf16 output.
 // New tokens' bf16 keys and values keep their exponent range: bf16 MMAs, P
 // split into two bf16 parts (2^-17).
-// Measured: one token of 4 sequences over 131072 rows of 8 heads 167 us (6.4 TB/s,
-// 94 % of the measured copy rate), of 32 sequences of 0 to 8192 rows 48 us (5.2
-// TB/s; the start and the merge take some 8 us), of one over 2048 rows 11 us.
+// Measured: one token of 4 sequences over 131072 rows of 8 heads 166 us (6.5 TB/s,
+// 95 % of the measured copy rate), of 32 sequences of 0 to 8192 rows 48 us (5.2
+// TB/s; the start and the merge take some 8 us), of one over 2048 rows 7.2 us (11
+// with one CTA to a kv head; a launch takes 2).
 #include <cfloat>
 
 #include "dg_kv8.cuh"
@@ -53,7 +54,10 @@ struct Ring {
   static constexpr int kWarp = kStages * kStage;
   static constexpr int oMl = W * kWarp;           // float2 [warps][32 rows]
   static constexpr int oBar = oMl + W * 32 * 8;   // mbarriers [warps][stages]
-  static constexpr int kSmem = oBar + W * kStages * 8 + 16;
+  static constexpr int oJoin = oBar + W * kStages * 8 + 16;  // the CTA's merged parts: float [rows][HD],
+  static constexpr int kJoin = (W == 8 ? 2048 : 1024) * 4;   // as many as kv8_mma_warps allows rows,
+  static constexpr int kSmem = oJoin + kJoin + 32 * 8;       // and float2 [32 rows]
+  static_assert(oJoin % 16 == 0 && kSmem <= 232448, "shared memory of one CTA");
 };
 
 // 16-byte chunk c of row r of a step lies at chunk c ^ swz(r), the swizzle of
@@ -198,6 +202,21 @@ struct Kv8Sum {
   }
 };
 
+// Loads from the shared memory of a CTA of the cluster.
+DG_DEV float2 ld_cluster_v2(uint32_t caddr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(caddr) : "memory");
+  return v;
+}
+DG_DEV float4 ld_cluster_v4(uint32_t caddr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(caddr)
+               : "memory");
+  return v;
+}
+
 // NB bytes of a fragment slice from shared memory.
 template <int NB>
 DG_DEV void lds(uint32_t* w, const uint8_t* p) {
@@ -251,9 +270,10 @@ __global__ void __launch_bounds__(32 * W, 1)
     for (int b = lane; b < a.B; b += 32)
       if (a.len[b] < 0 || a.len[b] > a.cap) atomicExch(a.status, kStatusCapacity);
   }
-  int w = blockIdx.x, w1 = w + 1;  // local: the CTA's unit
+  const int rank = a.cluster ? (int)blockIdx.x % a.cluster : 0;
+  int w = a.cluster ? (int)blockIdx.x / a.cluster : 0, w1 = w + 1;  // a cluster's unit
   Kv8Plan plan{};
-  if (!a.local) {
+  if (!a.cluster) {
     plan = kv8_plan(a);
     w1 = (int)min((long long)plan.total, (worker + 1ll) * plan.share);
     w = (int)min((long long)w1, (long long)worker * plan.share);
@@ -264,13 +284,13 @@ __global__ void __launch_bounds__(32 * W, 1)
 
   while (w < w1 && ok) {
     Kv8Piece p;
-    if (a.local) {
+    if (a.cluster) {
       p.b = w / a.units;
       p.len = kv8_len(a, p.b);
       p.nt = kv8_tiles(a, p.len);
       p.unit = w - p.b * a.units;
-      const int chunk = (p.nt + W - 1) / W;
-      p.t0 = min(warp * chunk, p.nt);
+      const int chunk = (p.nt + W * a.cluster - 1) / (W * a.cluster);
+      p.t0 = min((warp * a.cluster + rank) * chunk, p.nt);
       p.t1 = min(p.t0 + chunk, p.nt);
     } else {
       p = kv8_piece(a, plan, w, w1);
@@ -550,9 +570,10 @@ __global__ void __launch_bounds__(32 * W, 1)
     auto out4 = [&](int nt, int e, int k) {
       return make_float4(acc.o[nt][2 * k][e], acc.o[nt][2 * k][2 + e], acc.o[nt][2 * k + 1][e], acc.o[nt][2 * k + 1][2 + e]);
     };
-    if (a.local) {
+    if (a.cluster) {
       // every warp's output and (maximum, sum) to shared memory, the output to
-      // its own ring; then all threads merge, four columns of a row each
+      // its own ring; then the CTA's threads merge, four columns of a row each, and
+      // where a unit has several CTAs, the threads of all merge what these made
       float* mine = reinterpret_cast<float*>(ring);
       float2* ml = reinterpret_cast<float2*>(smem + R::oMl);
 #pragma unroll
@@ -566,8 +587,10 @@ __global__ void __launch_bounds__(32 * W, 1)
         }
       }
       __syncthreads();
-      if (*abort) break;
-      for (int i = threadIdx.x; i < a.prows * (HD / 4); i += 32 * W) {
+      float4* joined = reinterpret_cast<float4*>(smem + R::oJoin);
+      float2* joined_ml = reinterpret_cast<float2*>(smem + R::oJoin + R::kJoin);
+      const int items = *abort ? 0 : a.prows * (HD / 4);
+      for (int i = threadIdx.x; i < items; i += 32 * W) {
         const int r = i / (HD / 4), c4 = i % (HD / 4);
         if (row0 + r >= grp_rows) break;
         float M = -INFINITY;
@@ -582,8 +605,40 @@ __global__ void __launch_bounds__(32 * W, 1)
             s.add(ml[k * 32 + r], M, reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4), 0);
           sum.add(s);
         }
+        if (a.cluster == 1) {
+          sum.store(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4);
+        } else {
+          joined[i] = sum.v[0];
+          if (c4 == 0) joined_ml[r] = make_float2(M, sum.l);
+        }
+      }
+      if (a.cluster == 1) break;
+      __syncwarp();
+      cluster_sync();
+      for (int i = threadIdx.x * a.cluster + rank; i < items; i += 32 * W * a.cluster) {
+        const int r = i / (HD / 4), c4 = i % (HD / 4);
+        if (row0 + r >= grp_rows) break;
+        float2 y[kMaxCluster];
+        float4 x[kMaxCluster];
+        float M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+          y[k] = make_float2(-INFINITY, 0.f);
+          x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < a.cluster) {
+            y[k] = ld_cluster_v2(cluster_addr(joined_ml + r, k));
+            x[k] = ld_cluster_v4(cluster_addr(joined + i, k));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, y[k].x);
+        Kv8Sum<1> sum;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) sum.add(y[k], M, &x[k], 0);
         sum.store(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4);
       }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while a peer may still read its shared memory
       break;
     }
     if (!ok) break;
@@ -738,8 +793,20 @@ cudaError_t run_mma(const Kv8AttnArgs& a, cudaStream_t st) {
   if (!make_tmap_2d(&mK, a.K, HD, rows, HD, HD, kStep, true, HD) ||
       !make_tmap_2d(&mV, a.V, HD, rows, HD, HD, kStep, true, HD))
     return cudaErrorInvalidValue;
-  return launch_pdl(kv8_attn_kernel<HD, NT, W>, dim3(a.local ? a.B * a.units : kKv8Ctas), dim3(32 * W), R::kSmem, st, mK,
-                    mV, a, 1.4426950408889634f / sqrtf((float)HD));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.cluster ? a.B * a.units * a.cluster : kKv8Ctas);
+  cfg.blockDim = dim3(32 * W);
+  cfg.dynamicSmemBytes = R::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kv8_attn_kernel<HD, NT, W>, mK, mV, a, 1.4426950408889634f / sqrtf((float)HD));
 }
 
 template <int HD>

@@ -299,6 +299,31 @@ def test_attention_at_the_ends_of_its_range(case):
     check_attention(c, rows(g, B, Hq, C, hd), rows(g, B, Hkv, C, hd), rows(g, B, Hkv, C, hd), causal)
 
 
+LONG = [
+    # B, C, Hq, Hkv, hd, lens, cap, causal: caches too long for a cluster of CTAs to a unit, sequences of any length
+    (1, 1, 8, 2, 128, [69999], 70000, True),
+    (2, 3, 4, 1, 128, [40000, 5], 70000, True),
+    (1, 2, 2, 1, 64, [70000], 70000, False),
+    (3, 5, 2, 1, 32, [0, 33000, 64], 70000, True),
+    (1, 9, 2, 1, 128, [66000], 66003, True),
+    # and caches that clusters of two to eight finish, several tiles to a warp
+    (1, 1, 8, 2, 128, [32000], 32000, True),
+    (2, 1, 8, 8, 128, [23000, 1], 23000, True),
+    (5, 1, 4, 4, 64, [0, 9000, 65, 12000, 1], 12000, True),
+    (9, 2, 8, 4, 32, [9000, 0, 1, 4000, 64, 63, 5, 8999, 700], 9000, True),
+    (15, 1, 8, 4, 128, [5000, 0, 1, 4000, 64] * 3, 5000, True),
+    (2, 40, 4, 2, 128, [6000, 129], 6000, True),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=[f"b{c[0]}c{c[1]}q{c[2]}h{c[4]}cap{c[6]}" for c in LONG])
+def test_attention_over_long_caches(case):
+    B, C, Hq, Hkv, hd, lens, cap, causal = case
+    g = torch.Generator().manual_seed(cap + C)
+    c = filled(g, B, Hkv, cap, hd, lens)
+    check_attention(c, rows(g, B, Hq, C, hd), rows(g, B, Hkv, C, hd), rows(g, B, Hkv, C, hd), causal)
+
+
 @pytest.mark.parametrize("C,hd,cap", [(1, 128, 640), (8, 64, 640), (256, 128, 640), (256, 128, 5000), (30, 128, 5000),
                                       (1, 128, 5000)])
 def test_attention_follows_scales_of_many_octaves(C, hd, cap):
@@ -387,7 +412,7 @@ def test_attention_without_any_key_is_zero():
 def test_attention_writes_its_output_alone():
     """Bytes around the output and behind the workspace keep their values; the cache is read only."""
     g = torch.Generator().manual_seed(25)
-    for C, cap in ((1, 400), (70, 400), (1, 5000), (70, 5000), (20, 5000)):
+    for C, cap in ((1, 400), (70, 400), (1, 5000), (70, 5000), (20, 5000), (1, 40000)):
         c = filled(g, 2, 2, cap, 128, [399, 17])
         before = state(c)
         q, k, v = rows(g, 2, 4, C, 128).cuda(), rows(g, 2, 2, C, 128).cuda(), rows(g, 2, 2, C, 128).cuda()
@@ -403,7 +428,7 @@ def test_attention_writes_its_output_alone():
 
 def test_results_repeat_bit_for_bit():
     g = torch.Generator().manual_seed(26)
-    for C, cap in ((1, 3000), (256, 3000), (16, 3000), (1, 5000)):
+    for C, cap in ((1, 3000), (256, 3000), (16, 3000), (1, 5000), (1, 40000)):
         c = filled(g, 5, 2, cap, 128, [3000, 1, 0, 1555, 64])
         q, k, v = rows(g, 5, 8, C, 128).cuda(), rows(g, 5, 2, C, 128).cuda(), rows(g, 5, 2, C, 128).cuda()
         first = dg.kv8_attention(c, q, k, v)
@@ -463,7 +488,7 @@ def test_calls_on_two_streams_at_once():
     """The workspaces that the cache keeps by itself are a stream's own: calls of one cache that overlap on the GPU,
     of sizes that grow the workspace in between, give what they give alone."""
     g = torch.Generator().manual_seed(37)
-    c = filled(g, 4, 2, 9000, 128, [9000, 1, 4000, 8111])
+    c = filled(g, 4, 2, 40000, 128, [9000, 1, 4000, 8111])
     sizes = (1, 40, 3, 256)
     x = {C: [rows(g, 4, h, C, 128).cuda() for h in (8, 2, 2)] for C in sizes}
     want = {C: dg.kv8_attention(c, *x[C]) for C in sizes}
@@ -562,7 +587,8 @@ def test_assigned_lengths_reach_the_calls():
 
 def test_two_graphs_in_a_row_share_a_workspace():
     g = torch.Generator().manual_seed(33)
-    c1, c2 = filled(g, 2, 2, 900, 128, [900, 3]), filled(g, 2, 2, 500, 128, [0, 499])
+    c1, c2 = filled(g, 2, 2, 40000, 128, [900, 3]), filled(g, 2, 2, 9000, 128, [0, 499])
+    assert c1.workspace_bytes(1, 8) > 0 and c2.workspace_bytes(64, 8) > 0
     q = [rows(g, 2, 8, C, 128).cuda() for C in (1, 64)]
     ws = torch.empty(max(c1.workspace_bytes(1, 8), c2.workspace_bytes(64, 8)), dtype=torch.uint8, device="cuda")
     want = [dg.kv8_attention(c1, q[0]), dg.kv8_attention(c2, q[1])]

@@ -71,7 +71,7 @@ def test_attention_refusals(dg):
     L, f, z = dg.load(), FAKE, ct.c_size_t()
     # a short cache is finished in one launch, without a workspace; a long one needs one
     assert L.dg_kv8_attention_workspace(ct.byref(_cache(dg)), 16, 8, ct.byref(z)) == dg.DG_OK and z.value == 0
-    c = ct.byref(_cache(dg, cap=8192))
+    c = ct.byref(_cache(dg, cap=65536))
     assert L.dg_kv8_attention_workspace(c, 16, 8, ct.byref(z)) == dg.DG_OK and z.value > 0
     assert L.dg_kv8_attention_workspace(c, 16, 8, None) == dg.DG_ERR_ARG
     ok = dict(c=c, q=f, k=f, v=f, o=f, C=16, Hq=8, causal=0, ws=f, n=z.value)
