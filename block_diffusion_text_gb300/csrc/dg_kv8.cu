@@ -245,15 +245,18 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   // take a warp twice as long): 64 query rows to a head, 4000 rows, 8 heads 13.0 us
   // against 15.7; 256 rows, 1500 rows, 2 heads 12.0 against 14.5; with more tiles
   // to a warp it turns: 64 rows, 8000 rows, 16 heads 32.4 against 25.7, 256 rows,
-  // 2000 rows, 4 heads 15.7 against 15.4.
-  const int64_t all16 = (int64_t)c->B * c->Hkv * ((R + 15) / 16);
-  const int warps16 = kv8_mma_warps(128, 16) * kv8_cluster(all16, tiles, kv8_mma_warps(128, 16));
-  const bool few = all16 <= kKv8Ctas && tiles <= (C <= kKv8Block ? 4 : 1) * warps16;
-  w.tc = c->hd == 128 && R > 16 && !few;
+  // 2000 rows, 4 heads 15.7 against 15.4 (head dim 128; with 64 it turns nearby: 128
+  // rows, 6000 rows, 4 heads 13.9 and 13.9).  Head dim 32, half a row of a swizzled
+  // tile and no workload's but the smallest, stays with the warps.
+  const int rows = kv8_mma_rows(c->hd, R), warps = kv8_mma_warps(c->hd, rows);
+  const int64_t all = (int64_t)c->B * c->Hkv * ((R + rows - 1) / rows);
+  const int cluster = kv8_cluster(all, tiles, warps);
+  const bool few = all <= kKv8Ctas && tiles <= (C <= kKv8Block ? 4 : 1) * cluster * warps;
+  w.tc = c->hd >= 64 && R > 16 && !few;
   w.subs = w.tc && R <= 128 ? 2 : 1;  // one row tile is enough: the two take every other key tile
-  w.rows = w.tc ? 256 / w.subs : kv8_mma_rows(c->hd, R);
+  w.rows = w.tc ? 256 / w.subs : rows;
   w.tk = w.tc ? 128 : kKv8Block;
-  w.workers = w.tc ? kKv8Ctas : kKv8Ctas * kv8_mma_warps(c->hd, w.rows);
+  w.workers = w.tc ? kKv8Ctas : kKv8Ctas * warps;
   w.units = (int)(c->Hkv * ((R + w.rows - 1) / w.rows));  // at most 65535 * 64 by the checks before
   w.prows = (int)(R < w.rows ? R : w.rows);
   size_t off = 0;
@@ -267,9 +270,8 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
     // in memory and a merge kernel.  One token of one sequence, 2 kv heads, with
     // and without: 4000 rows 7.5 and 9.4 us, 8000 9.6 and 12.1, 32000 20.0 and
     // 28.4; 8 heads 32000 rows 20.0 and 21.1.
-    const int n = kv8_cluster((int64_t)c->B * w.units, tiles, kv8_mma_warps(c->hd, w.rows));
-    if (tiles <= kClusterTiles * n) {
-      w.cluster = n;
+    if (tiles <= kClusterTiles * cluster) {
+      w.cluster = cluster;
       return w;
     }
   }
@@ -278,10 +280,10 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   if (w.tc) {
     w.Cp = cdiv(C, 128) * 128;
     const size_t qrows = (size_t)c->B * Hq * C, krows = (size_t)c->B * c->Hkv * w.Cp;
-    w.qterms = take(2 * qrows * 128);
+    w.qterms = take(2 * qrows * c->hd);
     w.qexp = take(4 * qrows);
-    w.kterms = take(2 * krows * 128);
-    w.vf16 = take(2 * krows * 128);
+    w.kterms = take(2 * krows * c->hd);
+    w.vf16 = take(2 * krows * c->hd);
     w.kexp = take(krows / kKv8Block);
     w.vexp = take(krows / kKv8Block);
   }

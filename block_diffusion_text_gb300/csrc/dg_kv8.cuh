@@ -134,6 +134,14 @@ DG_DEV __nv_bfloat16* kv8_out_row(const Kv8AttnArgs& a, int b, int g, int r) {
   return reinterpret_cast<__nv_bfloat16*>(a.o) + (((size_t)b * a.C + i) * a.Hq + h) * a.hd;
 }
 
+// 16-byte chunk c of row r of a box of codes lies at chunk c ^ swz(r), the swizzle of
+// the TMA copies over hd bytes: the fragment reads of eight lanes then fall
+// into eight different bank groups (hd 128).
+template <int HD>
+DG_DEV int swz(int r) {
+  return HD == 128 ? (r & 7) : HD == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+}
+
 // 2^e as a float, e clamped to the normal range.
 DG_DEV float pow2i(int e) { return __uint_as_float((unsigned)(min(max(e, -126), 127) + 127) << 23); }
 DG_DEV float ex2_approx(float x) {
@@ -196,10 +204,10 @@ DG_DEV int top_exponent(unsigned bits) {
 // The forms of queries and new tokens that the tensor-core kernel reads, made
 // by its first launch in the call's workspace.
 struct Kv8Prep {
-  uint8_t* qterms;           // E4M3 [2 terms][qrows][128]
+  uint8_t* qterms;           // E4M3 [2 terms][qrows][hd]
   int* qexp;                 // [qrows] exponent of a row's scale
-  uint8_t* kterms;           // E4M3 [2 terms][krows][128], krows = B Hkv Cp
-  uint8_t* vf16;             // f16 [krows][128]
+  uint8_t* kterms;           // E4M3 [2 terms][krows][hd], krows = B Hkv Cp
+  uint8_t* vf16;             // f16 [krows][hd]
   uint8_t *kexp, *vexp;      // exponent bytes [B][Hkv][Cp / 64]
   int qrows, krows, Cp;      // Cp: new tokens padded to whole tiles
 };

@@ -1,5 +1,5 @@
 // Attention over the 8-bit prefix cache for few query rows per kv head (single
-// tokens, short canvases, head dims 32 and 64), and the merge of the parts.
+// tokens, calls of few tiles, head dim 32), and the merge of the parts.
 //
 // A warp is a worker: it streams its share of key tiles through a ring of its
 // own in shared memory (TMA, no barrier shared with other warps) and keeps
@@ -59,14 +59,6 @@ struct Ring {
   static constexpr int kSmem = oJoin + kJoin + 32 * 8;       // and float2 [32 rows]
   static_assert(oJoin % 16 == 0 && kSmem <= 232448, "shared memory of one CTA");
 };
-
-// 16-byte chunk c of row r of a step lies at chunk c ^ swz(r), the swizzle of
-// the TMA copies over hd bytes: the fragment reads of eight lanes then fall
-// into eight different bank groups (hd 128).
-template <int HD>
-DG_DEV int swz(int r) {
-  return HD == 128 ? (r & 7) : HD == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
-}
 
 // The MMAs without the order that volatile asm keeps: the scheduler may move
 // conversions and independent products between dependent ones.
@@ -839,21 +831,24 @@ static cudaError_t run_merge(const Kv8AttnArgs& a, cudaStream_t st) {
                     ctas);
 }
 
+template <int HD>
+static cudaError_t run_merge_rows(const Kv8AttnArgs& a, cudaStream_t st) {
+  if (a.rows < 128) return run_merge<HD, kMergeSlices, 1>(a, st);
+  // By the parts that a unit has (hd 128; 19 of them, a canvas over 131072 rows:
+  // 115.8 us, against 128.9 with a warp for all parts and 120.5 with two; 9, over
+  // 8192 rows: 32.6 with two, against 37.9 and 33.8 with four; 2, prompt pieces:
+  // 41.7 with one, against 45.6 with two).
+  const int64_t units = (int64_t)a.B * a.units;
+  if (a.subs == 2) return a.workers >= 8 * units ? run_merge<HD, 8, 1, 2>(a, st) : run_merge<HD, 2, 2, 2>(a, st);
+  if (a.workers >= 16 * units) return run_merge<HD, 4, 2>(a, st);
+  return a.workers >= 4 * units ? run_merge<HD, 2, 2>(a, st) : run_merge<HD, 1, 4>(a, st);
+}
+
 cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, cudaStream_t st) {
   switch (a.hd) {
     case 32: return run_merge<32, kMergeSlices, 1>(a, st);
-    case 64: return run_merge<64, kMergeSlices, 1>(a, st);
-    case 128: {
-      if (a.rows < 128) return run_merge<128, kMergeSlices, 1>(a, st);
-      // By the parts that a unit has (19 of them, a canvas over 131072 rows: 115.8
-      // us, against 128.9 with a warp for all parts and 120.5 with two; 9, over
-      // 8192 rows: 32.6 with two, against 37.9 and 33.8 with four; 2, prompt
-      // pieces: 41.7 with one, against 45.6 with two).
-      const int64_t units = (int64_t)a.B * a.units;
-      if (a.subs == 2) return a.workers >= 8 * units ? run_merge<128, 8, 1, 2>(a, st) : run_merge<128, 2, 2, 2>(a, st);
-      if (a.workers >= 16 * units) return run_merge<128, 4, 2>(a, st);
-      return a.workers >= 4 * units ? run_merge<128, 2, 2>(a, st) : run_merge<128, 1, 4>(a, st);
-    }
+    case 64: return run_merge_rows<64>(a, st);
+    case 128: return run_merge_rows<128>(a, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -1,5 +1,5 @@
 // Tensor-core (tcgen05 + TMA) attention over the 8-bit prefix cache for many
-// query rows per kv head (canvases and prompt pieces), head dim 128.
+// query rows per kv head (canvases and prompt pieces), head dims 64 and 128.
 //
 // A CTA owns 256 query rows (two tiles of 128) of one (sequence, kv head) and a
 // run of 128-key tiles; the tiles of a call are dealt to the CTAs in equal
@@ -23,8 +23,8 @@
 // largest).
 //
 // Warp roles (16 warps, one CTA per SM):
-//   warp 0       TMA: Q terms per piece, K tiles into a ring of 16 KB slots (a
-//                new tile takes two), V codes into their own ring (new tiles:
+//   warp 0       TMA: Q terms per piece, K tiles into a ring of slots (a new tile
+//                takes two), V codes into their own ring (new tiles:
 //                f16, straight to the MMA's buffer)
 //   warps 1, 2   MMA, one for each row tile, taking turns: P_t V of key tile j, then
 //                S_t of tile j + 1, so that one row tile's softmax and waits run
@@ -43,6 +43,8 @@
 // scores of 64 keys at a time, two of them in flight to a row tile (126 to 129:
 // the softmax no longer waits, but an MMA of 64 columns takes as long as one of
 // 128 and the MMA warps have twice the turns), MMA warps without turns (143).
+// Head dim 64 has half the MMAs and the same softmax: 256 rows over 32768 rows of
+// 8 heads 35.3 us (head dim 128: 42.6; the warp-MMA kernel 91.7).
 #include <cfloat>
 
 #include "dg_kv8.cuh"
@@ -50,25 +52,25 @@
 namespace dg {
 namespace {
 
-constexpr int kHD = 128;
 constexpr int kTK = 128;                   // keys per tile
 constexpr int kThreads = 512;
 constexpr int kNK = 4, kNV = 2;            // ring depths: K slots, V code and f16 slots
 constexpr float kHeadroom = 8.0f;          // p' of a row's maximum is 2^8 ..
 constexpr float kLazy = 6.0f;              // .. to 2^14: O is rescaled when the maximum grew by more than 2^6
 
+template <int HD>
 struct Smem {
-  static constexpr int kQ = 128 * kHD;               // one term of one row tile
-  static constexpr int kK = kTK * kHD;               // one tile of codes
+  static constexpr int kQ = 128 * HD;                // one term of one row tile
+  static constexpr int kK = kTK * HD;                // one tile of codes
   static constexpr int kBox = kTK * 128;             // 64 f16 columns of a tile
-  static constexpr int kF16 = 2 * kBox;
+  static constexpr int kF16 = HD / 64 * kBox;
   static constexpr int oK = 4 * kQ;
   static constexpr int oVc = oK + kNK * kK;
   static constexpr int oVf = oVc + kNV * kK;
   static constexpr int oBar = oVf + kNV * kF16;
   static constexpr int kTotal = oBar + 512;
+  static_assert(kTotal <= 232448, "shared memory of one CTA");
 };
-static_assert(Smem::kTotal <= 232448, "shared memory of one CTA");
 
 // TMEM: S_t at 128 t (P_t over its first 64 columns), O_t at 256 + 128 t.
 constexpr int kColO = 256;
@@ -97,22 +99,24 @@ DG_DEV void commit(uint64_t* bar) {
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
-// Shared-memory descriptors (128-byte swizzle, 1024 bytes between 8-row groups)
-// as a low word, address and leading offset, and a high word they all share.
+// Shared-memory descriptors (swizzle over rows of SW bytes, 128 or 64, 8 SW bytes
+// between 8-row groups) as a low word, address and leading offset, and a high word.
 DG_DEV uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | (lbo >> 4 << 16); }
+template <int SW>
 DG_DEV uint64_t desc64(uint32_t lo) {
-  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  constexpr uint32_t hi = (8u * SW >> 4) | (1u << 14) | ((SW == 128 ? 2u : 4u) << 29);
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "n"(hi));
   return d;
 }
 // D (+)= (Q_hi + Q_lo) K^T: the two terms of a query tile lie behind one another.
+template <int HD>
 DG_DEV void s_terms(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc, uint32_t accum) {
 #pragma unroll
   for (int term = 0; term < 2; ++term)
 #pragma unroll
-    for (int kk = 0; kk < kHD / 32; ++kk)
-      mma_s(d, desc64(q + term * (Smem::kQ >> 4) + 2 * kk), desc64(k + 2 * kk), idesc, (term | kk) ? 1u : accum);
+    for (int kk = 0; kk < HD / 32; ++kk)
+      mma_s(d, desc64<HD>(q + term * (Smem<HD>::kQ >> 4) + 2 * kk), desc64<HD>(k + 2 * kk), idesc, (term | kk) ? 1u : accum);
 }
 // Bounded wait of a whole warp whose usual case, the phase is complete, costs
 // one try (63 cycles against 171 for mbar_wait_warp's loops, measured alone).
@@ -143,11 +147,12 @@ DG_DEV bool next_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int& w, int w1
 
 // DUP: up to 128 query rows.  Both row tiles hold the same rows and row tile t
 // takes key tiles t, t + 2, ..; their outputs are two parts.
-template <bool DUP>
+template <int HD, bool DUP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                        const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mKn,
                        const __grid_constant__ CUtensorMap mVn, Kv8AttnArgs a, Kv8Prep pp, float scale_log2) {
+  using Smem = Smem<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // uniform over the CTA: return before any barrier
     if (threadIdx.x == 0) atomicExch(a.status, kStatusTimeout);
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint8_t* dst = smem + Smem::oVf + s * Smem::kF16;
               mbar_arrive_expect_tx(&cfull[s], Smem::kF16);
               tma_load_2d(dst, &mVn, &cfull[s], 0, bh * pp.Cp + key);
-              tma_load_2d(dst + Smem::kBox, &mVn, &cfull[s], 64, bh * pp.Cp + key);
+              if (HD == 128) tma_load_2d(dst + Smem::kBox, &mVn, &cfull[s], 64, bh * pp.Cp + key);
             } else {
               mbar_arrive_expect_tx(&cfull[s], Smem::kK);
               tma_load_2d(smem + Smem::oVc + s * Smem::kK, &mV, &cfull[s], 0, bh * a.cap + key);
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 3) {
       const int t = warp - 1;
       constexpr uint32_t idS = idesc_e4m3(128, kTK);
-      constexpr uint32_t idPV = idesc_f16(128, kHD, true);
+      constexpr uint32_t idPV = idesc_f16(128, HD, true);
       const uint32_t lo_q = desc_lo(smem_u32(smem + 2 * t * Smem::kQ), 16), lo_k = desc_lo(smem_u32(smem + Smem::oK), 16);
       const uint32_t lo_v = desc_lo(smem_u32(smem + Smem::oVf), Smem::kBox);
       const uint32_t tS = tmem + 128 * t, tO = tmem + kColO + 128 * t;
@@ -311,12 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t v = lo_v + s * (Smem::kF16 >> 4);
 #pragma unroll
             for (int k4 = 0; k4 < kTK / 32; ++k4)
-              mma_pv(tO, tS + 8 * k4, desc64(v + k4 * (2048 >> 4)), idPV, (k | k4) ? 1u : 0u);
+              mma_pv(tO, tS + 8 * k4, desc64<128>(v + k4 * (2048 >> 4)), idPV, (k | k4) ? 1u : 0u);
             if (!(ok = wait(&pready[2 * t + 1], (Jt + k) & 1, status, abort))) break;
             tc_fence_after();
 #pragma unroll
             for (int k4 = kTK / 32; k4 < kTK / 16; ++k4)
-              mma_pv(tO, tS + 8 * k4, desc64(v + k4 * (2048 >> 4)), idPV, 1u);
+              mma_pv(tO, tS + 8 * k4, desc64<128>(v + k4 * (2048 >> 4)), idPV, 1u);
           } else {
             if (!(ok = wait(&turn[t], turns, status, abort))) break;
             tc_fence_after();
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t kd = lo_k + ka * (Smem::kK >> 4);
 #pragma unroll 1
             for (int term = 0; term <= (fresh ? 1 : 0); ++term, kd = lo_k + kb * (Smem::kK >> 4))
-              s_terms(tS, lo_q, kd, idS, term);
+              s_terms<HD>(tS, lo_q, kd, idS, term);
           }
           if (lane == 0) mbar_arrive(&turn[t ^ 1]);
           if (next) commit(&sfull[t]);
@@ -361,9 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* dst = smem + Smem::oVf + s * Smem::kF16;
           const int valid = p.len - (p.t0 + j) * kTK;
 #pragma unroll
-          for (int it = 0; it < kTK * 8 / 128; ++it) {
-            const int id = it * 128 + tid, row = id / 8, c = id % 8;
-            uint4 v = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
+          for (int it = 0; it < HD / 16; ++it) {
+            const int id = it * 128 + tid, row = id / (HD / 16), c = id % (HD / 16);
+            uint4 v = *reinterpret_cast<const uint4*>(src + row * HD + ((c ^ swz<HD>(row)) << 4));
             if (row >= valid) v = make_uint4(0, 0, 0, 0);  // what lies behind the sequence never enters an MMA
             uint4 h[2];
             e4m3x4_f16x4(v.x, h[0].x, h[0].y);
@@ -463,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, need)) {
             const float corr = need ? ex2_approx(m_run - mx) : 1.0f;
 #pragma unroll 1
-            for (int c = 0; c < kHD / 16; ++c) {
+            for (int c = 0; c < HD / 16; ++c) {
               uint32_t o[16];
               tmem_ld16(tO + 16 * c, o);
 #pragma unroll
@@ -515,14 +520,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
       __nv_bfloat16* orow = valid_row ? kv8_out_row(a, p.b, p.hk, ridx) : nullptr;
 #pragma unroll 1
-      for (int c = 0; c < kHD / 32; ++c) {
+      for (int c = 0; c < HD / 32; ++c) {
         float o[32];
         tmem_ld32(tO + 32 * c, o);
         if (n == 0) {  // no tile for this row tile: TMEM holds another piece's output
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (c == kHD / 32 - 1) {
+        if (c == HD / 32 - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ofree[t]);
@@ -558,43 +563,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------- prep --
-// q to two E4M3 terms and a scale per row (16 lanes a row, 8 elements a lane);
+// q to two E4M3 terms and a scale per row (8 elements a lane);
 // new keys to two E4M3 terms and new values to f16, with a scale per 64 tokens
 // (one CTA per block, zeros behind the last token).
+template <int HD>
 __global__ void __launch_bounds__(256) kv8_prep_kernel(Kv8AttnArgs a, Kv8Prep pp, int kv_ctas) {
+  constexpr int LPR = HD / 8, RPC = 256 / LPR;  // lanes per row, rows per CTA
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
   if ((int)blockIdx.x >= kv_ctas) {
-    const long long row = (long long)(blockIdx.x - kv_ctas) * 16 + tid / 16;
+    const long long row = (long long)(blockIdx.x - kv_ctas) * RPC + tid / LPR;
     const bool there = row < pp.qrows;
-    const uint4 w = there ? *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + row * kHD +
-                                                            (tid % 16) * 8)
+    const uint4 w = there ? *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + row * HD +
+                                                            (tid % LPR) * 8)
                           : make_uint4(0, 0, 0, 0);
     unsigned top = abs_top(w);
     top = max(top & 0xffffu, top >> 16);
 #pragma unroll
-    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = LPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int e = top_exponent(top);
     float x[8];
     unpack8(w, pow2i(-e), x);
     uint2 hi, lo;
     split8(x, hi, lo);
     if (!there) return;
-    *reinterpret_cast<uint2*>(pp.qterms + row * kHD + (tid % 16) * 8) = hi;
-    *reinterpret_cast<uint2*>(pp.qterms + ((size_t)pp.qrows + row) * kHD + (tid % 16) * 8) = lo;
-    if (tid % 16 == 0) pp.qexp[row] = e;
+    *reinterpret_cast<uint2*>(pp.qterms + row * HD + (tid % LPR) * 8) = hi;
+    *reinterpret_cast<uint2*>(pp.qterms + ((size_t)pp.qrows + row) * HD + (tid % LPR) * 8) = lo;
+    if (tid % LPR == 0) pp.qexp[row] = e;
     return;
   }
   __shared__ unsigned red[8];
   const int nb = pp.Cp / kKv8Block, isv = blockIdx.x & 1, blk = (blockIdx.x >> 1) % nb, bh = (blockIdx.x >> 1) / nb;
-  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(isv ? a.vn : a.kn) + (size_t)bh * a.C * kHD;
-  uint4 w[4];
+  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(isv ? a.vn : a.kn) + (size_t)bh * a.C * HD;
+  uint4 w[kKv8Block / RPC];
   unsigned top = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = blk * kKv8Block + i * 16 + tid / 16;
-    w[i] = row < a.C ? *reinterpret_cast<const uint4*>(src + (size_t)row * kHD + (tid % 16) * 8) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < kKv8Block / RPC; ++i) {
+    const int row = blk * kKv8Block + i * RPC + tid / LPR;
+    w[i] = row < a.C ? *reinterpret_cast<const uint4*>(src + (size_t)row * HD + (tid % LPR) * 8) : make_uint4(0, 0, 0, 0);
     top = __vmaxu2(top, abs_top(w[i]));
   }
   top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
@@ -604,43 +611,51 @@ __global__ void __launch_bounds__(256) kv8_prep_kernel(Kv8AttnArgs a, Kv8Prep pp
   const int e = top_exponent(top);
   if (tid == 0) (isv ? pp.vexp : pp.kexp)[(size_t)bh * nb + blk] = (uint8_t)(e + kKv8Bias);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const size_t row = (size_t)bh * pp.Cp + blk * kKv8Block + i * 16 + tid / 16;
+  for (int i = 0; i < kKv8Block / RPC; ++i) {
+    const size_t row = (size_t)bh * pp.Cp + blk * kKv8Block + i * RPC + tid / LPR;
     float x[8];
     unpack8(w[i], pow2i(-e), x);
     if (isv) {
-      *reinterpret_cast<uint4*>(pp.vf16 + row * kHD * 2 + (tid % 16) * 16) =
+      *reinterpret_cast<uint4*>(pp.vf16 + row * HD * 2 + (tid % LPR) * 16) =
           make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]), pack_f16(x[6], x[7]));
     } else {
       uint2 hi, lo;
       split8(x, hi, lo);
-      *reinterpret_cast<uint2*>(pp.kterms + row * kHD + (tid % 16) * 8) = hi;
-      *reinterpret_cast<uint2*>(pp.kterms + ((size_t)pp.krows + row) * kHD + (tid % 16) * 8) = lo;
+      *reinterpret_cast<uint2*>(pp.kterms + row * HD + (tid % LPR) * 8) = hi;
+      *reinterpret_cast<uint2*>(pp.kterms + ((size_t)pp.krows + row) * HD + (tid % LPR) * 8) = lo;
     }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cudaStream_t st) {
+template <int HD, bool DUP>
+static cudaError_t run_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cudaStream_t st) {
+  constexpr auto kern = kv8_attn_tc_kernel<HD, DUP>;
   const uint64_t cached = (uint64_t)a.B * a.Hkv * a.cap;
   CUtensorMap mQ, mK, mV, mKn, mVn;
-  if (!make_tmap_2d(&mQ, pp.qterms, kHD, 2 * (uint64_t)pp.qrows, kHD, kHD, 128, true) ||
-      !make_tmap_2d(&mK, a.K, kHD, cached, kHD, kHD, kTK, true) ||
-      !make_tmap_2d(&mV, a.V, kHD, cached, kHD, kHD, kTK, true))
+  if (!make_tmap_2d(&mQ, pp.qterms, HD, 2 * (uint64_t)pp.qrows, HD, HD, 128, true, HD) ||
+      !make_tmap_2d(&mK, a.K, HD, cached, HD, HD, kTK, true, HD) ||
+      !make_tmap_2d(&mV, a.V, HD, cached, HD, HD, kTK, true, HD))
     return cudaErrorInvalidValue;
   mKn = mK;  // without new tokens neither is used
   mVn = mV;
-  if (a.kn && (!make_tmap_2d(&mKn, pp.kterms, kHD, 2 * (uint64_t)pp.krows, kHD, kHD, kTK, true) ||
-               !make_tmap_2d(&mVn, pp.vf16, kHD, (uint64_t)pp.krows, kHD * 2, 64, kTK)))
+  if (a.kn && (!make_tmap_2d(&mKn, pp.kterms, HD, 2 * (uint64_t)pp.krows, HD, HD, kTK, true, HD) ||
+               !make_tmap_2d(&mVn, pp.vf16, HD, (uint64_t)pp.krows, HD * 2, 64, kTK)))
     return cudaErrorInvalidValue;
-  cudaError_t e = a.subs == 2 ? set_smem_once<kv8_attn_tc_kernel<true>>(Smem::kTotal) : set_smem_once<kv8_attn_tc_kernel<false>>(Smem::kTotal);
+  cudaError_t e = set_smem_once<kern>(Smem<HD>::kTotal);
   if (e != cudaSuccess) return e;
   const int kv_ctas = a.kn ? 2 * a.B * a.Hkv * (pp.Cp / kKv8Block) : 0;
-  e = launch_pdl(kv8_prep_kernel, dim3(kv_ctas + cdiv(pp.qrows, 16)), dim3(256), 0, st, a, pp, kv_ctas);
+  e = launch_pdl(kv8_prep_kernel<HD>, dim3(kv_ctas + cdiv(pp.qrows, 256 / (HD / 8))), dim3(256), 0, st, a, pp, kv_ctas);
   if (e != cudaSuccess) return e;
-  return launch_pdl(a.subs == 2 ? kv8_attn_tc_kernel<true> : kv8_attn_tc_kernel<false>, dim3(kKv8Ctas), dim3(kThreads),
-                    Smem::kTotal, st, mQ, mK, mV, mKn, mVn, a, pp, 1.4426950408889634f / sqrtf((float)kHD));
+  return launch_pdl(kern, dim3(kKv8Ctas), dim3(kThreads), Smem<HD>::kTotal, st, mQ, mK, mV, mKn, mVn, a, pp,
+                    1.4426950408889634f / sqrtf((float)HD));
+}
+
+cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cudaStream_t st) {
+  if (a.hd == 64) return a.subs == 2 ? run_tc<64, true>(a, pp, st) : run_tc<64, false>(a, pp, st);
+  if (a.hd == 128) return a.subs == 2 ? run_tc<128, true>(a, pp, st) : run_tc<128, false>(a, pp, st);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace dg

@@ -313,6 +313,13 @@ LONG = [
     (9, 2, 8, 4, 32, [9000, 0, 1, 4000, 64, 63, 5, 8999, 700], 9000, True),
     (15, 1, 8, 4, 128, [5000, 0, 1, 4000, 64] * 3, 5000, True),
     (2, 40, 4, 2, 128, [6000, 129], 6000, True),
+    # head dim 64 on the tensor cores
+    (2, 40, 4, 2, 64, [20000, 129], 20000, True),
+    (1, 256, 8, 2, 64, [5000], 9000, True),
+    (2, 256, 2, 2, 64, [640, 1], 4000, False),
+    (3, 64, 2, 1, 64, [0, 33000, 64], 40000, False),
+    (2, 300, 8, 2, 64, [100, 700], 1000, True),
+    (40, 70, 2, 1, 64, [1, 0, 64, 2000, 129] * 8, 2003, True),
 ]
 
 
@@ -324,7 +331,7 @@ def test_attention_over_long_caches(case):
     check_attention(c, rows(g, B, Hq, C, hd), rows(g, B, Hkv, C, hd), rows(g, B, Hkv, C, hd), causal)
 
 
-@pytest.mark.parametrize("C,hd,cap", [(1, 128, 640), (8, 64, 640), (256, 128, 640), (256, 128, 5000), (30, 128, 5000),
+@pytest.mark.parametrize("C,hd,cap", [(1, 128, 640), (8, 64, 640), (256, 128, 640), (256, 128, 5000), (30, 128, 5000), (256, 64, 5000),
                                       (1, 128, 5000)])
 def test_attention_follows_scales_of_many_octaves(C, hd, cap):
     """Key and value scales that differ by many octaves from block to block, with small queries: the value scale is
@@ -338,7 +345,8 @@ def test_attention_follows_scales_of_many_octaves(C, hd, cap):
     check_attention(c, q, rows(g, 2, 2, C, hd) , rows(g, 2, 2, C, hd), False)
 
 
-@pytest.mark.parametrize("C,hd,cap", [(1, 128, 500), (1, 32, 500), (256, 128, 500), (256, 128, 3000), (40, 128, 3000)])
+@pytest.mark.parametrize("C,hd,cap", [(1, 128, 500), (1, 32, 500), (256, 128, 500), (256, 128, 3000), (40, 128, 3000),
+                                      (256, 64, 3000)])
 def test_attention_of_peaked_rows(C, hd, cap):
     """Scores of some hundreds: almost all weight on one key, first in one row and last in another."""
     g = torch.Generator().manual_seed(22)
@@ -347,7 +355,8 @@ def test_attention_of_peaked_rows(C, hd, cap):
     check_attention(c, q.to(torch.bfloat16), rows(g, 1, 1, C, hd), rows(g, 1, 1, C, hd), False)
 
 
-@pytest.mark.parametrize("C,hd,cap", [(2, 128, 200), (2, 64, 200), (200, 128, 200), (200, 128, 3000), (30, 128, 3000)])
+@pytest.mark.parametrize("C,hd,cap", [(2, 128, 200), (2, 64, 200), (200, 128, 200), (200, 128, 3000), (30, 128, 3000),
+                                      (200, 64, 3000)])
 def test_attention_scales_queries_exactly(C, hd, cap):
     """Queries of 2^-40 and 2^30, zero rows among them, and one element 2^12 times the others: the power-of-two
     scaling of a row keeps what its scores need."""
@@ -363,7 +372,7 @@ def test_attention_scales_queries_exactly(C, hd, cap):
     check_attention(c, q, None, None, False)
 
 
-WIDE = [(1, 128, 400), (1, 128, 5000), (20, 32, 400), (9, 64, 5000), (40, 128, 5000), (256, 128, 5000)]
+WIDE = [(1, 128, 400), (1, 128, 5000), (20, 32, 400), (9, 64, 5000), (40, 128, 5000), (256, 128, 5000), (256, 64, 5000)]
 
 
 @pytest.mark.parametrize("C,hd,cap", WIDE)
