@@ -456,6 +456,44 @@ def test_lengths_outside_the_cache_are_reported():
     assert c.status() == dg.DG_ERR_CAPACITY
 
 
+def test_calls_that_the_binding_refuses():
+    """Wrong types, shapes, strides and workspaces raise before any launch, and write nothing."""
+    g = torch.Generator().manual_seed(38)
+    c = filled(g, 2, 2, 40000, 64, [100, 7])
+    q, k, v = rows(g, 2, 4, 3, 64).cuda(), rows(g, 2, 2, 3, 64).cuda(), rows(g, 2, 2, 3, 64).cuda()
+    before = state(c)
+    out = torch.full((6, 256), 5.0, dtype=torch.bfloat16, device="cuda")
+    need = c.workspace_bytes(3, 4)
+    assert need > 0
+    ws = torch.zeros(need + 256, dtype=torch.uint8, device="cuda")
+    wrong = [dict(q=q.half()), dict(q=q.float()), dict(q=q.transpose(1, 2)), dict(q=q[:, :, :2]), dict(q=q[0]),
+             dict(q=q[..., :32]), dict(q=q.cpu()), dict(k=None), dict(v=None), dict(k=k[:1], v=v[:1]),
+             dict(k=k.transpose(2, 3).contiguous()), dict(v=v[:, :, :2].contiguous()), dict(out=out[:5]),
+             dict(out=out.float()), dict(out=out.cpu()), dict(ws=ws.cpu()), dict(ws=ws[::2])]
+    for kw in wrong:
+        with pytest.raises(ValueError):
+            dg.kv8_attention(c, **dict(dict(q=q, k=k, v=v, out=out), **kw))
+    for kw in (dict(ws=ws[:need - 1]), dict(ws=ws[128:128 + need]), dict(q=q[:, :3].contiguous(), out=out[:, :192].contiguous()),
+               dict(q=q[:, :, :0], k=k[:, :, :0], v=v[:, :, :0], out=out[:0])):
+        with pytest.raises(dg.DgError):
+            dg.kv8_attention(c, **dict(dict(q=q, k=k, v=v, out=out), **kw))
+    for kw in (dict(k=k.half()), dict(v=v[:, :1]), dict(k=k[..., :32].contiguous()), dict(counts=torch.ones(2).cuda()),
+               dict(counts=torch.ones(2, dtype=torch.int32)), dict(counts=torch.ones(3, dtype=torch.int32).cuda())):
+        with pytest.raises(ValueError):
+            dg.kv8_append(c, **dict(dict(k=k, v=v), **kw))
+    big = torch.zeros(2, 2, 9, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(dg.DgError):
+        dg.kv8_read(c, 0, 10, out=(big, big.clone()))
+    with pytest.raises(dg.DgError):
+        dg.kv8_read(c, -1, 5)
+    with pytest.raises(ValueError):
+        dg.kv8_read(c, 0, 5, out=(big, big.half()))
+    dg.kv8_append(c, k[:, :, :0], v[:, :, :0])
+    assert dg.kv8_read(c, 5, 0)[0].shape == (2, 2, 0, 64)
+    torch.cuda.synchronize()
+    assert (out == 5).all() and c.status() == 0 and all(torch.equal(x, y) for x, y in zip(before, state(c)))
+
+
 def test_offsets_past_32_bits():
     """A cache of 4.7 GB of codes each for K and V, its last head past 2^32 bytes."""
     g = torch.Generator().manual_seed(28)
