@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv8_merge_kernel(Kv8AttnArgs
   __syncthreads();
   const int c0 = cut[0], n = cut[1] - c0, nt = cut[2];
   pdl_wait();
-  if (nt > 0 && n == 0 && SUBS == 1) return;  // uniform over the CTA
+  if (nt > 0 && n == 0) return;  // uniform over the CTA
   // Part 0 (with its sub-parts) is the unit's beginning, slot 1 of its worker; the
   // others are slots 0.  The slots' loads go out in groups, whole ones: what a
   // group lacks is read as an empty part, so that no remainder waits on its own.

@@ -68,7 +68,8 @@ struct Smem {
   static constexpr int oVc = oK + kNK * kK;
   static constexpr int oVf = oVc + kNV * kK;
   static constexpr int oBar = oVf + kNV * kF16;
-  static constexpr int kTotal = oBar + 512;
+  static constexpr int oMl = oBar + 512;             // float2 [2 row tiles][128]: maximum and sum
+  static constexpr int kTotal = oMl + 2 * 128 * 8;
   static_assert(kTotal <= 232448, "shared memory of one CTA");
 };
 
@@ -146,7 +147,8 @@ DG_DEV bool next_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int& w, int w1
 }
 
 // DUP: up to 128 query rows.  Both row tiles hold the same rows and row tile t
-// takes key tiles t, t + 2, ..; their outputs are two parts.
+// takes key tiles t, t + 2, ..; their outputs are two parts, which the softmax
+// warps join themselves where the CTA has all of the unit's tiles.
 template <int HD, bool DUP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
@@ -170,9 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* sfull = vempty + kNV;    // [2]
   uint64_t* pready = sfull + 2;      // [2 tiles][2 halves]
   uint64_t* pvdone = pready + 4;     // [2]
-  uint64_t* ofree = pvdone + 2;      // [2] the piece's output has been read from TMEM
-  uint64_t* turn = ofree + 2;        // [2] row tile t's MMA warp may issue
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
+  uint64_t* turn = pvdone + 2;       // [2] row tile t's MMA warp may issue
+  uint64_t* meet = turn + 2;         // the softmax warps of both row tiles
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meet + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* status = a.status;
 
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(qfull, 1);
     constexpr int readers = DUP ? 1 : 2;  // MMA warps that read a tile
     mbar_init(qempty, 2);
+    mbar_init(meet, 8);
     for (int s = 0; s < kNK; ++s) {
       mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], readers);
@@ -197,7 +200,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&pready[2 * t + 1], 4);
       mbar_init(&pvdone[t], 1);
       mbar_init(&turn[t], 1);
-      mbar_init(&ofree[t], 4);
     }
     *abort = 0;
     fence_mbar_init();
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (k >= 0 && k < own) {
             if (!(ok = wait(&vfull[s], ((J + j) >> 1) & 1, status, abort))) break;
-            if (k == 0 && np > 0 && !(ok = wait(&ofree[t], (np - 1) & 1, status, abort))) break;
+            // (the first P of a piece also says that the last one's output has been read)
             if (!(ok = wait(&pready[2 * t], (Jt + k) & 1, status, abort))) break;
             if (!(ok = wait(&turn[t], turns, status, abort))) break;
             tc_fence_after();
@@ -395,7 +397,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + kColO + 128 * t;
     bool ok = true;
-    int Jt = 0, np = 0;  // own tiles, and pieces that had some
+    int Jt = 0, np = 0, met = 0;  // own tiles, pieces that had some, phases of meet
+    float2* ml = reinterpret_cast<float2*>(smem + Smem::oMl);
+    auto join = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(meet);
+      const bool all = wait(meet, met++ & 1, status, abort);
+      tc_fence_after();
+      return all;
+    };
     Piece p;
     for (int w = w0; ok && next_piece(a, plan, w, w1, p);) {
       const int n = DUP ? (p.tiles() + 1 - t) / 2 : p.tiles(), bh = p.b * a.Hkv + p.hk;
@@ -515,10 +526,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || (n > 0 && !(ok = wait(&pvdone[t], np & 1, status, abort)))) break;
       tc_fence_after();
       if (ve_top > kKv8EmaxAttn) atomicExch(status, kStatusValue);
-      const bool whole = !DUP && p.t0 == 0 && p.t1 == p.nt;
+      const bool whole = p.t0 == 0 && p.t1 == p.nt;
       const size_t slot = ((size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1)) * (DUP ? 2 : 1) + (DUP ? t : 0);
       const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
       __nv_bfloat16* orow = valid_row ? kv8_out_row(a, p.b, p.hk, ridx) : nullptr;
+      if (DUP && whole) {
+        // half of the columns each, from both row tiles' outputs
+        ml[128 * t + r] = make_float2(m_run, l_run);
+        if (!(ok = join())) break;
+        const float2 m0 = ml[r], m1 = ml[128 + r];
+        const float M = fmaxf(m0.x, m1.x);
+        float w0 = m0.x == -INFINITY ? 0.f : exp2f(m0.x - M), w1 = m1.x == -INFINITY ? 0.f : exp2f(m1.x - M);
+        const float l = fmaf(w0, m0.y, w1 * m1.y), scale = l == 0.f ? 0.f : 1.0f / l;
+        w0 *= scale;
+        w1 *= scale;
+#pragma unroll 1
+        for (int c = HD / 64 * t; c < HD / 64 * (t + 1); ++c) {
+          float o[32], o1[32];
+          tmem_ld32(tmem + lane_base + kColO + 32 * c, o);
+          tmem_ld32(tmem + lane_base + kColO + 128 + 32 * c, o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)  // with one tile TMEM holds another piece's output in the second place
+            o[e] = p.tiles() > 1 ? fmaf(w0, o[e], w1 * o1[e]) : w0 * o[e];
+          if (!valid_row) continue;
+          uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[q] = make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]), pack_bf16(o[8 * q + 2], o[8 * q + 3]),
+                                pack_bf16(o[8 * q + 4], o[8 * q + 5]), pack_bf16(o[8 * q + 6], o[8 * q + 7]));
+        }
+        if (!(ok = join())) break;  // both have read the outputs, and ml
+        Jt += n;
+        np += n > 0;
+        continue;
+      }
 #pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         float o[32];
@@ -527,13 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (c == HD / 32 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ofree[t]);
-        }
         if (!valid_row) continue;
-        if (whole) {
+        if (!DUP && whole) {
           uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
 #pragma unroll
           for (int q = 0; q < 4; ++q)

@@ -320,6 +320,12 @@ LONG = [
     (3, 64, 2, 1, 64, [0, 33000, 64], 40000, False),
     (2, 300, 8, 2, 64, [100, 700], 1000, True),
     (40, 70, 2, 1, 64, [1, 0, 64, 2000, 129] * 8, 2003, True),
+    # several whole units to a CTA
+    (33, 4, 64, 8, 64, [128, 0, 170, 192, 5, 288, 271, 62, 204, 149, 190] * 3, 305, True),
+    (33, 6, 6, 2, 128, [0, 2791, 64, 1088, 1408, 1, 200, 130, 129, 128, 384] * 3, 2821, True),
+    (40, 20, 8, 4, 128, [0, 1, 127, 128, 129, 300, 5, 0] * 5, 700, False),
+    (64, 64, 8, 4, 64, [5, 0, 128, 127] * 16, 2000, False),
+    (30, 100, 12, 4, 128, [0, 1, 255, 256, 257, 600] * 5, 2000, True),
 ]
 
 
