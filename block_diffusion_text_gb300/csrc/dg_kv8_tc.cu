@@ -450,12 +450,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32_async(tS + 64 * b, *reinterpret_cast<float(*)[32]>(s));
           tmem_ld32_async(tS + 64 * b + 32, *reinterpret_cast<float(*)[32]>(s + 32));
           tmem_wait_ld();
-          if (__any_sync(0xffffffffu, lim < 64 * b + 64)) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (64 * b + c >= lim) s[c] = -INFINITY;
-          }
         };
+        if (__any_sync(0xffffffffu, lim < kTK)) {
+          // a sequence's last tile, or a causal one: masked in TMEM, so that the
+          // passes' loops hold no code for it (prompt pieces 41.6 -> 39.8 us)
+#pragma unroll 1
+          for (int c = 0; c < kTK; c += 16) {
+            uint32_t s[16];
+            tmem_ld16(tS + c, s);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c + e >= lim) s[e] = __float_as_uint(-INFINITY);
+            tmem_st16(tS + c, s);
+          }
+          tmem_wait_st();
+        }
         float mx = -INFINITY;
 #pragma unroll 1
         for (int b = 0; b < 2; ++b) {
