@@ -502,7 +502,8 @@ class Kv8Cache:
         self.s = dg_kv8_cache(*[t.data_ptr() for t in (K, V, K_exp, V_exp, len, status)], B, Hkv, cap, hd)
         self._ref = ct.byref(self.s)
         self._lib = load()
-        self._ws_bytes, self._ws = {}, {}
+        self._index = K.device.index
+        self._ws_bytes, self._ws, self._shapes = {}, {}, {}
 
     @property
     def len(self) -> torch.Tensor:
@@ -539,36 +540,43 @@ class Kv8Cache:
             n = self._ws_bytes[(C, Hq)] = z.value
         return n
 
-    def _workspace(self, C, Hq, st, stream):
-        """(pointer, bytes) of a workspace for a call on the stream with handle st.
+    def _workspace(self, n, st, stream):
+        """Pointer of a workspace of n bytes for a call on the stream with handle st.
 
         One per stream, kept: the calls of a stream run one after another.  Under graph capture one from the
         graph's own pool, so that graphs that overlap share none."""
-        n = self.workspace_bytes(C, Hq)
-        if n == 0:
-            return None, 0
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self._workspace(C, Hq, st, None)
+                return self._workspace(n, st, None)
         if torch.cuda.is_current_stream_capturing():
-            return torch.empty(n, dtype=torch.uint8, device=self.device).data_ptr(), n
+            return torch.empty(n, dtype=torch.uint8, device=self.device).data_ptr()
         t = self._ws.get(st)
         if t is None or t.numel() < n:
             t = self._ws[st] = torch.empty(n, dtype=torch.uint8, device=self.device)
-        return t.data_ptr(), n
+        return t.data_ptr()
 
-    def _rows(self, t, heads, n, what):
-        if t.dtype != torch.bfloat16 or t.shape != (self.B, heads, n, self.hd) or t.device != self.device \
-                or not t.is_contiguous():
-            raise ValueError(f"{what}: contiguous bf16 [{self.B}, {heads}, {n}, {self.hd}] on {self.device}, "
+    def _attention_shapes(self, q):
+        """(C, Hq, shape of k and v, shape of the output, bytes of workspace) of queries shaped like q."""
+        if q.dim() != 4 or q.shape[0] != self.B or q.shape[3] != self.hd:
+            raise ValueError(f"q: contiguous bf16 [{self.B}, Hq, C, {self.hd}], got {tuple(q.shape)}")
+        self._bf16(q, q.shape, "q")
+        _, Hq, C, _ = q.shape
+        r = self._shapes[q.shape] = (C, Hq, torch.Size((self.B, self.Hkv, C, self.hd)),
+                                     torch.Size((self.B * C, Hq * self.hd)), self.workspace_bytes(C, Hq))
+        return r
+
+    def _bf16(self, t, shape, what):
+        """The address of a contiguous bf16 tensor of that shape on the cache's device."""
+        if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError(f"{what}: contiguous bf16 {list(shape)} on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
 
     def _launch_stream(self, stream):
         """The raw stream of a launch: the library launches on the current device, so that must be the cache's."""
-        index = self.device.index
-        if torch._C._cuda_getDevice() != index:
+        if torch._C._cuda_getDevice() != self._index:
             raise ValueError(f"the cache lies on {self.device}, the current device is another")
-        return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
 
 
 def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None,
@@ -577,16 +585,16 @@ def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, counts: torch.
 
     counts: optional int32 [B], rows of each sequence (the rest is padding).  len is not advanced."""
     n = k.shape[2] if k.dim() == 4 else -1
-    cache._rows(k, cache.Hkv, n, "k")
-    cache._rows(v, cache.Hkv, n, "v")
-    cp = None
+    shape = (cache.B, cache.Hkv, n, cache.hd)
+    kp, vp, cp = cache._bf16(k, shape, "k"), cache._bf16(v, shape, "v"), None
     if counts is not None:
-        _need(counts.shape == (cache.B,) and counts.dtype == torch.int32 and counts.device == cache.device
-              and counts.is_contiguous(), f"counts: int32 [{cache.B}] on {cache.device}")
+        if counts.shape != (cache.B,) or counts.dtype is not torch.int32 or counts.get_device() != cache._index \
+                or not counts.is_contiguous():
+            raise ValueError(f"counts: contiguous int32 [{cache.B}] on {cache.device}")
         cp = counts.data_ptr()
     if n == 0:
         return
-    rc = cache._lib.dg_kv8_append(cache._ref, k.data_ptr(), v.data_ptr(), n, cp, cache._launch_stream(stream))
+    rc = cache._lib.dg_kv8_append(cache._ref, kp, vp, n, cp, cache._launch_stream(stream))
     if rc:
         raise DgError(rc, "dg_kv8_append")
 
@@ -604,8 +612,9 @@ def kv8_read(cache: Kv8Cache, row0: int, n: int, out=None, stream=None):
     else:
         K, V = out
         pitch = K.shape[2] if K.dim() == 4 else -1
-        cache._rows(K, cache.Hkv, pitch, "out[0]")
-        cache._rows(V, cache.Hkv, pitch, "out[1]")
+        shape = (cache.B, cache.Hkv, pitch, cache.hd)
+        cache._bf16(K, shape, "out[0]")
+        cache._bf16(V, shape, "out[1]")
     if n == 0:
         return K, V
     rc = cache._lib.dg_kv8_read(cache._ref, row0, n, K.data_ptr(), V.data_ptr(), K.shape[2], st)
@@ -622,34 +631,28 @@ def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = Non
     q: bf16 [B, Hq, C, hd]; k, v: bf16 [B, Hkv, C, hd], or None for the cached rows alone.  ws: optional uint8
     workspace of cache.workspace_bytes(C, Hq) bytes, not shared by calls that may overlap; by default the cache keeps
     one for each stream, and a captured call takes one from the graph's pool."""
-    if q.dim() != 4:
-        raise ValueError("q: bf16 [B, Hq, C, hd]")
-    _, Hq, C, _ = q.shape
-    cache._rows(q, Hq, C, "q")
-    kp = vp = None
+    C, Hq, new, shape, wn = cache._shapes.get(q.shape) or cache._attention_shapes(q)
+    qp, kp, vp, wp = cache._bf16(q, q.shape, "q"), None, None, None
     if k is not None and v is not None:
-        cache._rows(k, cache.Hkv, C, "k")
-        cache._rows(v, cache.Hkv, C, "v")
-        kp, vp = k.data_ptr(), v.data_ptr()
+        kp, vp = cache._bf16(k, new, "k"), cache._bf16(v, new, "v")
     elif k is not v:
         raise ValueError("k and v come together")
     st = cache._launch_stream(stream)
-    if ws is None:
-        wp, wn = cache._workspace(C, Hq, st, stream)
-    else:
+    if ws is not None:
         _need(ws.device == cache.device and ws.is_contiguous(), "ws: contiguous, on the cache's device")
         wp, wn = ws.data_ptr(), ws.numel() * ws.element_size()
-    shape = (cache.B * C, Hq * cache.hd)
+    elif wn:
+        wp = cache._workspace(wn, st, stream)
     if out is not None:
-        _need(out.dtype == torch.bfloat16 and out.shape == shape and out.is_contiguous() and out.device == cache.device,
-              f"out: contiguous bf16 {list(shape)}")
-    elif stream is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        op = cache._bf16(out, shape, "out")
     else:
-        with torch.cuda.stream(stream):  # memory of the launching stream
+        if stream is None:
             out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    rc = cache._lib.dg_kv8_attention(cache._ref, q.data_ptr(), kp, vp, out.data_ptr(), C, Hq, 1 if causal else 0, wp, wn,
-                                     st)
+        else:
+            with torch.cuda.stream(stream):  # memory of the launching stream
+                out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        op = out.data_ptr()
+    rc = cache._lib.dg_kv8_attention(cache._ref, qp, kp, vp, op, C, Hq, 1 if causal else 0, wp, wn, st)
     if rc:
         raise DgError(rc, "dg_kv8_attention")
     return out
