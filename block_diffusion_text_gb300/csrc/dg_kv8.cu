@@ -210,10 +210,10 @@ dg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DG_OK : DG_ERR_CU
 
 int kv8_blocks(int cap) { return cdiv(cap, kKv8Block); }
 
-// Key tiles to a CTA of a cluster, above which shares balance better than they
+// Key tiles to a CTA (and to a warp of its groups), above which shares balance better than they
 // cost: 8 ragged sequences of up to 8000 rows, 8 heads, 15.2 us in shares, 19.5 with
 // two CTAs a unit; up to 4000 rows 13.2 against 12.6.
-constexpr int kClusterTiles = 64;
+constexpr int kClusterTiles = 64, kGroupTiles = 16;
 constexpr int kKv8Ovh = 3;  // measured: a unit's start and output take as long as some three tiles
 
 // CTAs that share a unit of `tiles` key tiles, of `units` in the call: as many
@@ -231,7 +231,7 @@ int kv8_cluster(int64_t units, int tiles, int warps) {
 
 struct Kv8Ws {
   size_t part, ml, qterms, qexp, kterms, vf16, kexp, vexp, total;
-  int rows, tk, units, workers, prows, subs, cluster, Cp;
+  int rows, tk, units, workers, prows, subs, cluster, group, Cp;
   bool tc;
 };
 
@@ -270,8 +270,17 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
     // in memory and a merge kernel.  One token of one sequence, 2 kv heads, with
     // and without: 4000 rows 7.5 and 9.4 us, 8000 9.6 and 12.1, 32000 20.0 and
     // 28.4; 8 heads 32000 rows 20.0 and 21.1.
-    if (tiles <= kClusterTiles * cluster) {
+    // More units than SMs share CTAs, each a group of the warps: 64 sequences of
+    // up to 500 rows, 8 heads, 10 us, one CTA to each 19; 500 sequences of up to 250
+    // rows 55 us, 152 with a CTA to each, 140 in shares.
+    int group = warps;
+    if (cluster == 1)
+      while (group > 1 && cdiv(all, warps / group) > kKv8Ctas)
+        do --group;
+        while (warps % group);
+    if (tiles <= (group == warps ? kClusterTiles * cluster : 2 * group == warps ? 40 : kGroupTiles * group)) {
       w.cluster = cluster;
+      w.group = group;
       return w;
     }
   }
@@ -397,6 +406,7 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   a.subs = w.subs;
   a.prows = w.prows;
   a.cluster = w.cluster;
+  a.group = w.group;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (w.tc) {

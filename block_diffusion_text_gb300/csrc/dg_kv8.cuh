@@ -44,6 +44,7 @@ struct Kv8AttnArgs {
   int ovh;                   // what beginning a unit costs a worker, in tiles
   int prows;                 // rows of a part: min(rows, G C)
   int cluster;               // warp-MMA kernel: CTAs per unit, their warps' parts merged in shared memory (0: shares)
+  int group;                 // then the warps of a CTA that share a unit: all, or with one CTA to a unit a divisor
 };
 
 // All work of a call, in the order (sequence, unit, tile), is dealt to the

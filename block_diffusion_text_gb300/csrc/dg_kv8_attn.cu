@@ -34,6 +34,7 @@
 // TB/s; the start and the merge take some 8 us), of one over 2048 rows 7.2 us (11
 // with one CTA to a kv head; a launch takes 2).
 #include <cfloat>
+#include <type_traits>
 
 #include "dg_kv8.cuh"
 
@@ -263,7 +264,13 @@ __global__ void __launch_bounds__(32 * W, 1)
       if (a.len[b] < 0 || a.len[b] > a.cap) atomicExch(a.status, kStatusCapacity);
   }
   const int rank = a.cluster ? (int)blockIdx.x % a.cluster : 0;
-  int w = a.cluster ? (int)blockIdx.x / a.cluster : 0, w1 = w + 1;  // a cluster's unit
+  int lead = 0;  // first warp of the warp's group
+  int w = a.cluster ? (int)blockIdx.x / a.cluster : 0;  // a cluster's unit, or a group's
+  if (a.cluster && a.group < W) {
+    lead = warp / a.group * a.group;
+    w = w * (W / a.group) + lead / a.group;  // behind the last unit for groups without any
+  }
+  int w1 = w + 1;
   Kv8Plan plan{};
   if (!a.cluster) {
     plan = kv8_plan(a);
@@ -278,11 +285,11 @@ __global__ void __launch_bounds__(32 * W, 1)
     Kv8Piece p;
     if (a.cluster) {
       p.b = w / a.units;
-      p.len = kv8_len(a, p.b);
-      p.nt = kv8_tiles(a, p.len);
+      p.len = p.b < a.B ? kv8_len(a, p.b) : 0;
+      p.nt = p.b < a.B ? kv8_tiles(a, p.len) : 0;
       p.unit = w - p.b * a.units;
-      const int chunk = (p.nt + W * a.cluster - 1) / (W * a.cluster);
-      p.t0 = min((warp * a.cluster + rank) * chunk, p.nt);
+      const int n = a.group * a.cluster, chunk = (p.nt + n - 1) / n;
+      p.t0 = min(((warp - lead) * a.cluster + rank) * chunk, p.nt);
       p.t1 = min(p.t0 + chunk, p.nt);
     } else {
       p = kv8_piece(a, plan, w, w1);
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(32 * W, 1)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + nt * 8 + g;
-      const bool there = r < grp_rows;
+      const bool there = r < grp_rows && p.b < a.B;
       qrow[nt] = there ? reinterpret_cast<const __nv_bfloat16*>(a.q) + (bh * grp_rows + r) * HD + t * SL : nullptr;
       uint2 raw[KS];
       unsigned top = 0;
@@ -564,7 +571,7 @@ __global__ void __launch_bounds__(32 * W, 1)
     };
     if (a.cluster) {
       // every warp's output and (maximum, sum) to shared memory, the output to
-      // its own ring; then the CTA's threads merge, four columns of a row each, and
+      // its own ring; then the unit's threads merge, four columns of a row each, and
       // where a unit has several CTAs, the threads of all merge what these made
       float* mine = reinterpret_cast<float*>(ring);
       float2* ml = reinterpret_cast<float2*>(smem + R::oMl);
@@ -581,29 +588,39 @@ __global__ void __launch_bounds__(32 * W, 1)
       __syncthreads();
       float4* joined = reinterpret_cast<float4*>(smem + R::oJoin);
       float2* joined_ml = reinterpret_cast<float2*>(smem + R::oJoin + R::kJoin);
-      const int items = *abort ? 0 : a.prows * (HD / 4);
-      for (int i = threadIdx.x; i < items; i += 32 * W) {
-        const int r = i / (HD / 4), c4 = i % (HD / 4);
-        if (row0 + r >= grp_rows) break;
-        float M = -INFINITY;
+      const int items = *abort || p.b >= a.B ? 0 : a.prows * (HD / 4);
+      auto merge = [&](auto all, int n) {  // all: the unit has the CTA's warps, n of them otherwise
+        const uint8_t* rings = smem + lead * R::kWarp;
+        const float2* parts = ml + lead * 32;
+        for (int i = threadIdx.x - 32 * lead; i < items; i += 32 * n) {
+          const int r = i / (HD / 4), c4 = i % (HD / 4);
+          if (row0 + r >= grp_rows) break;
+          float M = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < W; ++k) M = fmaxf(M, ml[k * 32 + r].x);
-        Kv8Sum<1> sum;
+          for (int k = 0; k < W; ++k)
+            if (all || k < n) M = fmaxf(M, parts[k * 32 + r].x);
+          Kv8Sum<1> sum;
 #pragma unroll
-        for (int sl = 0; sl < kMergeSlices; ++sl) {  // the merge kernel's order of additions
-          Kv8Sum<1> s;
+          for (int sl = 0; sl < kMergeSlices; ++sl) {  // the merge kernel's order of additions
+            Kv8Sum<1> s;
 #pragma unroll
-          for (int k = sl; k < W; k += kMergeSlices)
-            s.add(ml[k * 32 + r], M, reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4), 0);
-          sum.add(s);
+            for (int k = sl; k < W; k += kMergeSlices)
+              if (all || k < n)
+                s.add(parts[k * 32 + r], M, reinterpret_cast<const float4*>(rings + k * R::kWarp + (r * HD + 4 * c4) * 4), 0);
+            sum.add(s);
+          }
+          if (a.cluster == 1) {
+            sum.store(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4);
+          } else {
+            joined[i] = sum.v[0];
+            if (c4 == 0) joined_ml[r] = make_float2(M, sum.l);
+          }
         }
-        if (a.cluster == 1) {
-          sum.store(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4);
-        } else {
-          joined[i] = sum.v[0];
-          if (c4 == 0) joined_ml[r] = make_float2(M, sum.l);
-        }
-      }
+      };
+      if (a.group == W)
+        merge(std::true_type{}, W);
+      else
+        merge(std::false_type{}, a.group);
       if (a.cluster == 1) break;
       __syncwarp();
       cluster_sync();
@@ -673,7 +690,8 @@ __global__ void __launch_bounds__(32 * W, 1)
 // 256-row units of the tensor-core kernel have fewer parts and rows enough for
 // a warp each (S = 1).  One warp works out where the shares' borders cut the
 // unit (done by every warp it took longer than the parts: 16 us for 8 prompt
-// pieces); a unit that one worker finished is already written, and one without
+// pieces), all of them where there are many sequences (256: 28 us by one, 18 by
+// all); a unit that one worker finished is already written, and one without
 // any key (an empty sequence without new tokens) gets zeros.  What is read
 // before pdl_wait, the lengths, no kernel of the call writes, and the
 // attention kernel lets this one start only once it has itself waited for its
@@ -683,23 +701,44 @@ constexpr int kMergeWarps = 8;
 template <int HD, int S, int N, int SUBS>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv8_merge_kernel(Kv8AttnArgs a, int ctas) {
   constexpr int CN = HD / (4 * N);
-  __shared__ int cut[3];
+  __shared__ int costs[kMergeWarps][3], cut[3];
   __shared__ float top[kMergeWarps / S][S][32];
   __shared__ Kv8Sum<N> sums[kMergeWarps / S][S > 1 ? S : 1][S > 1 ? 32 : 1];
   const int lane = threadIdx.x % 32, slice = threadIdx.x / 32 % S, sub = threadIdx.x / (32 * S);
   const int grp_rows = a.Hq / a.Hkv * a.C;
   const unsigned all = blockIdx.x / (unsigned)ctas;  // `ctas` CTAs a unit
   const int b = (int)(all / a.units), unit = (int)(all - (unsigned)b * a.units);
-  if (threadIdx.x < 32) {
-    const Kv8Plan plan = kv8_plan(a);
-    const int nt = kv8_tiles(a, b < 32 ? __shfl_sync(0xffffffffu, plan.len, b & 31) : kv8_len(a, b));
-    int first = 0;
-    for (int i = lane; i < b; i += 32) first += kv8_cost(a, kv8_tiles(a, i < 32 ? plan.len : kv8_len(a, i))) * a.units;
-    first = __reduce_add_sync(0xffffffffu, first) + unit * (nt + a.ovh) + a.ovh;  // the unit's first tile
+  // Cost of the call, and of the sequences before b, by the first warp, or where
+  // it would have to go round by all.
+  const bool many = a.B > 32;
+  if (many || threadIdx.x < 32) {
+    int total = 0, before = 0, own = 0;
+    for (int i = threadIdx.x; i < a.B; i += many ? 32 * kMergeWarps : 32) {
+      const int nt = kv8_tiles(a, kv8_len(a, i)), cost = kv8_cost(a, nt) * a.units;
+      total += cost;
+      if (i < b) before += cost;
+      if (i == b) own = nt;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    before = __reduce_add_sync(0xffffffffu, before);
+    own = __reduce_add_sync(0xffffffffu, own);
     if (lane == 0) {
-      cut[0] = first / plan.share;
-      cut[1] = (first + max(nt, 1) - 1) / plan.share;
-      cut[2] = nt;
+      costs[threadIdx.x / 32][0] = total;
+      costs[threadIdx.x / 32][1] = before;
+      costs[threadIdx.x / 32][2] = own;
+    }
+    if (many) __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; many && i < kMergeWarps; ++i) {
+        total += costs[i][0];
+        before += costs[i][1];
+        own += costs[i][2];
+      }
+      const int share = max((total + a.workers - 1) / a.workers, 1);
+      const int first = before + unit * (own + a.ovh) + a.ovh;  // the unit's first tile
+      cut[0] = first / share;
+      cut[1] = (first + max(own, 1) - 1) / share;
+      cut[2] = own;
     }
   }
   const int item = ((int)(blockIdx.x - all * ctas) * (kMergeWarps / S) + sub) * 32 + lane;
@@ -786,7 +825,7 @@ cudaError_t run_mma(const Kv8AttnArgs& a, cudaStream_t st) {
       !make_tmap_2d(&mV, a.V, HD, rows, HD, HD, kStep, true, HD))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.cluster ? a.B * a.units * a.cluster : kKv8Ctas);
+  cfg.gridDim = dim3(a.cluster ? cdiv((int64_t)a.B * a.units, W / a.group) * a.cluster : kKv8Ctas);
   cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = R::kSmem;
   cfg.stream = st;
