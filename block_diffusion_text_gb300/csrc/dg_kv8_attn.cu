@@ -34,7 +34,6 @@
 // TB/s; the start and the merge take some 8 us), of one over 2048 rows 7.2 us (11
 // with one CTA to a kv head; a launch takes 2).
 #include <cfloat>
-#include <type_traits>
 
 #include "dg_kv8.cuh"
 
@@ -589,38 +588,48 @@ __global__ void __launch_bounds__(32 * W, 1)
       float4* joined = reinterpret_cast<float4*>(smem + R::oJoin);
       float2* joined_ml = reinterpret_cast<float2*>(smem + R::oJoin + R::kJoin);
       const int items = *abort || p.b >= a.B ? 0 : a.prows * (HD / 4);
-      auto merge = [&](auto all, int n) {  // all: the unit has the CTA's warps, n of them otherwise
-        const uint8_t* rings = smem + lead * R::kWarp;
-        const float2* parts = ml + lead * 32;
-        for (int i = threadIdx.x - 32 * lead; i < items; i += 32 * n) {
+      if (a.group < W) {  // rolled: the usual calls' code stays short
+        for (int i = threadIdx.x - 32 * lead; i < items; i += 32 * a.group) {
           const int r = i / (HD / 4), c4 = i % (HD / 4);
           if (row0 + r >= grp_rows) break;
           float M = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < W; ++k)
-            if (all || k < n) M = fmaxf(M, parts[k * 32 + r].x);
+#pragma unroll 1
+          for (int k = lead; k < lead + a.group; ++k) M = fmaxf(M, ml[k * 32 + r].x);
           Kv8Sum<1> sum;
-#pragma unroll
-          for (int sl = 0; sl < kMergeSlices; ++sl) {  // the merge kernel's order of additions
+#pragma unroll 1
+          for (int sl = 0; sl < min(kMergeSlices, a.group); ++sl) {
             Kv8Sum<1> s;
-#pragma unroll
-            for (int k = sl; k < W; k += kMergeSlices)
-              if (all || k < n)
-                s.add(parts[k * 32 + r], M, reinterpret_cast<const float4*>(rings + k * R::kWarp + (r * HD + 4 * c4) * 4), 0);
+#pragma unroll 1
+            for (int k = lead + sl; k < lead + a.group; k += kMergeSlices)
+              s.add(ml[k * 32 + r], M, reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4), 0);
             sum.add(s);
           }
-          if (a.cluster == 1) {
-            sum.store(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4);
-          } else {
-            joined[i] = sum.v[0];
-            if (c4 == 0) joined_ml[r] = make_float2(M, sum.l);
-          }
+          sum.store(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4);
         }
-      };
-      if (a.group == W)
-        merge(std::true_type{}, W);
-      else
-        merge(std::false_type{}, a.group);
+        break;
+      }
+      for (int i = threadIdx.x; i < items; i += 32 * W) {
+        const int r = i / (HD / 4), c4 = i % (HD / 4);
+        if (row0 + r >= grp_rows) break;
+        float M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < W; ++k) M = fmaxf(M, ml[k * 32 + r].x);
+        Kv8Sum<1> sum;
+#pragma unroll
+        for (int sl = 0; sl < kMergeSlices; ++sl) {  // the merge kernel's order of additions
+          Kv8Sum<1> s;
+#pragma unroll
+          for (int k = sl; k < W; k += kMergeSlices)
+            s.add(ml[k * 32 + r], M, reinterpret_cast<const float4*>(smem + k * R::kWarp + (r * HD + 4 * c4) * 4), 0);
+          sum.add(s);
+        }
+        if (a.cluster == 1) {
+          sum.store(kv8_out_row(a, p.b, hk, row0 + r) + 4 * c4);
+        } else {
+          joined[i] = sum.v[0];
+          if (c4 == 0) joined_ml[r] = make_float2(M, sum.l);
+        }
+      }
       if (a.cluster == 1) break;
       __syncwarp();
       cluster_sync();

@@ -320,6 +320,12 @@ LONG = [
     (3, 64, 2, 1, 64, [0, 33000, 64], 40000, False),
     (2, 300, 8, 2, 64, [100, 700], 1000, True),
     (40, 70, 2, 1, 64, [1, 0, 64, 2000, 129] * 8, 2003, True),
+    # more units than SMs: CTAs shared by groups of warps, down to one warp a unit, the last CTA not full
+    (25, 1, 16, 8, 128, [0, 1, 64, 129, 700] * 5, 1000, True),
+    (61, 1, 8, 8, 32, [5, 0, 64, 260] * 15 + [300], 300, False),
+    (101, 16, 4, 4, 128, [0, 65, 200, 31, 1] * 20 + [199], 200, True),
+    (201, 1, 4, 4, 128, [130, 0, 64, 1, 65, 7] * 33 + [2, 3, 4], 130, True),
+    (301, 2, 8, 8, 64, [100, 0, 64] * 100 + [1], 127, True),
     # several whole units to a CTA
     (33, 4, 64, 8, 64, [128, 0, 170, 192, 5, 288, 271, 62, 204, 149, 190] * 3, 305, True),
     (33, 6, 6, 2, 128, [0, 2791, 64, 1088, 1408, 1, 200, 130, 129, 128, 384] * 3, 2821, True),
