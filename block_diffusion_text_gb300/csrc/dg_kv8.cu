@@ -251,7 +251,11 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   const int rows = kv8_mma_rows(c->hd, R), warps = kv8_mma_warps(c->hd, rows);
   const int64_t all = (int64_t)c->B * c->Hkv * ((R + rows - 1) / rows);
   const int cluster = kv8_cluster(all, tiles, warps);
-  const bool few = all <= kKv8Ctas && tiles <= (C <= kKv8Block ? 4 : 1) * cluster * warps;
+  // With more units than SMs the tensor-core kernel, which begins and ends a CTA's
+  // units one after another, loses on short ones: 500 heads of 64 rows over up to 250
+  // rows 62 us against 47, over up to 1000 80 against 187 (24 rows, 500 rows: 59, 33).
+  const bool few = all <= kKv8Ctas ? tiles <= (C <= kKv8Block ? 4 : 1) * cluster * warps
+                                   : C <= kKv8Block && tiles * ((R + rows - 1) / rows) < 32;
   w.tc = c->hd >= 64 && R > 16 && !few;
   w.subs = w.tc && R <= 128 ? 2 : 1;  // one row tile is enough: the two take every other key tile
   w.rows = w.tc ? 256 / w.subs : rows;

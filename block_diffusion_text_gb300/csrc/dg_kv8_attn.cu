@@ -31,7 +31,7 @@
 // split into two bf16 parts (2^-17).
 // Measured: one token of 4 sequences over 131072 rows of 8 heads 166 us (6.5 TB/s,
 // 95 % of the measured copy rate), of 32 sequences of 0 to 8192 rows 48 us (5.2
-// TB/s; the start and the merge take some 8 us), of one over 2048 rows 7.2 us (11
+// TB/s; the start and the merge take some 8 us), of one over 2048 rows 7.4 us (11
 // with one CTA to a kv head; a launch takes 2).
 #include <cfloat>
 

@@ -328,6 +328,7 @@ LONG = [
     (301, 2, 8, 8, 64, [100, 0, 64] * 100 + [1], 127, True),
     # several whole units to a CTA
     (33, 4, 64, 8, 64, [128, 0, 170, 192, 5, 288, 271, 62, 204, 149, 190] * 3, 305, True),
+    (33, 4, 64, 8, 64, [128, 0, 170, 192, 5, 288, 271, 62, 204, 149, 190] * 3, 2305, True),
     (33, 6, 6, 2, 128, [0, 2791, 64, 1088, 1408, 1, 200, 130, 129, 128, 384] * 3, 2821, True),
     (40, 20, 8, 4, 128, [0, 1, 127, 128, 129, 300, 5, 0] * 5, 700, False),
     (64, 64, 8, 4, 64, [5, 0, 128, 127] * 16, 2000, False),
