@@ -93,13 +93,16 @@ DG_DEV Kv8Plan kv8_plan(const Kv8AttnArgs& a) {
   p.share = max((p.total + a.workers - 1) / a.workers, 1);
   return p;
 }
-// The piece that begins at w in a share that ends at w1 (w < w1 <= the total;
-// every lane of the calling warp gets the answer).
-DG_DEV Kv8Piece kv8_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int w, int w1) {
+// The piece that begins at w in a share that ends at w1 (w < w1 <= the total; every
+// lane of the calling warp gets the answer).  from: where the search begins, a
+// sequence and the cost before it; zeros at first, then what the last call left
+// there (375 sequences, 4 heads of 24 rows over up to 2000 rows: 298 us without
+// it, 235 with).
+DG_DEV Kv8Piece kv8_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, int w, int w1) {
   const int lane = threadIdx.x & 31;
-  int base = 0;
+  int base = from.y;
   Kv8Piece p{0, 0, 0, 0, 0, 0, w1 - w};
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
+  for (int b0 = from.x; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
     const int len = b0 == 0 ? plan.len : b < a.B ? kv8_len(a, b) : 0;
     const int nt = b < a.B ? kv8_tiles(a, len) : 0;
@@ -122,6 +125,7 @@ DG_DEV Kv8Piece kv8_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int w, int 
       p.t0 = max(o0 - a.ovh, 0);
       p.t1 = max(o1 - a.ovh, 0);
       p.cost = o1 - o0;
+      from = make_int2(b0, base);
       return p;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);

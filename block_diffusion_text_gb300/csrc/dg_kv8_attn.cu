@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(32 * W, 1)
   }
   int w1 = w + 1;
   Kv8Plan plan{};
+  int2 from = make_int2(0, 0);
   if (!a.cluster) {
     plan = kv8_plan(a);
     w1 = (int)min((long long)plan.total, (worker + 1ll) * plan.share);
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(32 * W, 1)
       p.t0 = min(((warp - lead) * a.cluster + rank) * chunk, p.nt);
       p.t1 = min(p.t0 + chunk, p.nt);
     } else {
-      p = kv8_piece(a, plan, w, w1);
+      p = kv8_piece(a, plan, from, w, w1);
       w += p.cost;
       if (p.t1 <= p.t0) continue;
     }

@@ -69,7 +69,8 @@ struct Smem {
   static constexpr int oVf = oVc + kNV * kK;
   static constexpr int oBar = oVf + kNV * kF16;
   static constexpr int oMl = oBar + 512;             // float2 [2 row tiles][128]: maximum and sum
-  static constexpr int kTotal = oMl + 2 * 128 * 8;
+  static constexpr int oFrom = oMl + 2 * 128 * 8;    // int2 [warps]: kv8_piece's `from`
+  static constexpr int kTotal = oFrom + kThreads / 32 * 8;
   static_assert(kTotal <= 232448, "shared memory of one CTA");
 };
 
@@ -134,9 +135,9 @@ struct Piece {
   DG_DEV bool fresh(int j) const { return t0 + j >= ntc; }  // tile j of the piece holds new tokens
 };
 // The next piece with tiles at or after w, or false.
-DG_DEV bool next_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int& w, int w1, Piece& p) {
+DG_DEV bool next_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, int& w, int w1, Piece& p) {
   while (w < w1) {
-    const Kv8Piece k = kv8_piece(a, plan, w, w1);
+    const Kv8Piece k = kv8_piece(a, plan, from, w, w1);
     w += k.cost;
     if (k.t1 <= k.t0) continue;
     const int per = a.units / a.Hkv;
@@ -216,6 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();  // the merge, which needs no TMEM, may take the SMs that this kernel leaves
 
   const Kv8Plan plan = kv8_plan(a);
+  int2& from = reinterpret_cast<int2*>(smem + Smem::oFrom)[warp];  // in memory: registers are short
+  from = make_int2(0, 0);
+  __syncwarp();
   const int w0 = (int)min((long long)plan.total, (long long)blockIdx.x * plan.share);
   const int w1 = (int)min((long long)plan.total, (long long)w0 + plan.share);
   const int grp_rows = a.Hq / a.Hkv * a.C;
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int kslot = 0, kpar = 1, J = 0, np = 0;  // slot counters run on through the pieces
       Piece p;
-      for (int w = w0; ok && next_piece(a, plan, w, w1, p); ++np) {
+      for (int w = w0; ok && next_piece(a, plan, from, w, w1, p); ++np) {
         if (lane == 0) {
           const int bh = p.b * a.Hkv + p.hk;
           ok = mbar_wait(qempty, (np & 1) ^ 1, status, abort);
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int K = 0, J = 0, Jt = 0, np = 0, turns = t ^ 1;  // K slots, tiles, own tiles, pieces so far; parity of the turn
       const int stride = DUP ? 2 : 1, begin = DUP ? t : 0;
       Piece p;
-      for (int w = w0; ok && next_piece(a, plan, w, w1, p); ++np) {
+      for (int w = w0; ok && next_piece(a, plan, from, w, w1, p); ++np) {
         const int n = p.tiles(), jfresh = max(p.ntc - p.t0, 0);  // tiles from jfresh on hold new tokens
         const int own = DUP ? (n + 1 - t) >> 1 : n, steps = DUP ? (n + 1) >> 1 : n;
         int j = begin - stride;                           // own key tile k of the piece
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int J = 0;
     Piece p;
-    for (int w = w0; ok && next_piece(a, plan, w, w1, p);) {
+    for (int w = w0; ok && next_piece(a, plan, from, w, w1, p);) {
       for (int j = 0; j < p.tiles(); ++j, ++J) {
         const int s = J % kNV, par = (J / kNV) & 1;
         if (!(ok = wait(&cfull[s], par, status, abort))) break;
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return all;
     };
     Piece p;
-    for (int w = w0; ok && next_piece(a, plan, w, w1, p);) {
+    for (int w = w0; ok && next_piece(a, plan, from, w, w1, p);) {
       const int n = DUP ? (p.tiles() + 1 - t) / 2 : p.tiles(), bh = p.b * a.Hkv + p.hk;
       const int rpart = DUP ? r : 128 * t + r, ridx = p.row0 + rpart;
       auto tile = [&](int k) { return DUP ? 2 * k + t : k; };  // own tile k
