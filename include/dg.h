@@ -450,8 +450,9 @@ DG_API dg_status dg_kv8_read(const dg_kv8_cache* cache, int32_t row0, int32_t n,
  *   h / (Hq / Hkv).
  * causal = 0: every new token sees every new token (the canvas of a denoising
  * step); causal = 1: token i sees new tokens 0..i (a prompt piece).  C = 1 is the
- * single-token form.  Sequences of any lengths share a call (0 included; the
- * work is divided by keys, not by sequences); a row without any key is zero.
+ * single-token form.  Sequences of any lengths share a call (0 included; in long
+ * caches the work is divided by keys, not by sequences); a row without any key is
+ * zero.
  * q, k and v must be finite, the new ones a causal mask hides included, as must
  * the scores be in fp32; o must not overlap an input; what lies behind len is
  * never used.  Values go up to 448 * 2^40 in magnitude (V_exp bytes up to 167):
