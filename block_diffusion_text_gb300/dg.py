@@ -541,19 +541,20 @@ class Kv8Cache:
         return n
 
     def _workspace(self, n, st, stream):
-        """Pointer of a workspace of n bytes for a call on the stream with handle st.
+        """A workspace of n bytes for a call on the stream with handle st, to be held until the call is enqueued.
 
         One per stream, kept: the calls of a stream run one after another.  Under graph capture one from the
-        graph's own pool, so that graphs that overlap share none."""
+        graph's own pool, so that graphs that overlap share none; the pool gives its memory to the next tensor
+        (the call's own output, too) as soon as it is let go."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self._workspace(n, st, None)
         if torch.cuda.is_current_stream_capturing():
-            return torch.empty(n, dtype=torch.uint8, device=self.device).data_ptr()
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
         t = self._ws.get(st)
         if t is None or t.numel() < n:
             t = self._ws[st] = torch.empty(n, dtype=torch.uint8, device=self.device)
-        return t.data_ptr()
+        return t
 
     def _attention_shapes(self, q):
         """(C, Hq, shape of k and v, shape of the output, bytes of workspace) of queries shaped like q."""
@@ -642,7 +643,8 @@ def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = Non
         _need(ws.device == cache.device and ws.is_contiguous(), "ws: contiguous, on the cache's device")
         wp, wn = ws.data_ptr(), ws.numel() * ws.element_size()
     elif wn:
-        wp = cache._workspace(wn, st, stream)
+        ws = cache._workspace(wn, st, stream)
+        wp = ws.data_ptr()
     if out is not None:
         op = cache._bf16(out, shape, "out")
     else:
