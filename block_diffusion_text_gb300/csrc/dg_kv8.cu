@@ -230,8 +230,8 @@ int kv8_cluster(int64_t units, int tiles, int warps) {
 }
 
 struct Kv8Ws {
-  size_t part, ml, qterms, qexp, kterms, vf16, kexp, vexp, total;
-  int rows, tk, units, workers, prows, subs, cluster, group, Cp;
+  size_t part, ml, total;
+  int rows, tk, units, workers, prows, subs, cluster, group;
   bool tc;
 };
 
@@ -290,16 +290,6 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   }
   w.part = take((size_t)2 * w.workers * w.subs * w.prows * c->hd * 4);
   w.ml = take((size_t)2 * w.workers * w.subs * w.prows * 8);
-  if (w.tc) {
-    w.Cp = cdiv(C, 128) * 128;
-    const size_t qrows = (size_t)c->B * Hq * C, krows = (size_t)c->B * c->Hkv * w.Cp;
-    w.qterms = take(2 * qrows * c->hd);
-    w.qexp = take(4 * qrows);
-    w.kterms = take(2 * krows * c->hd);
-    w.vf16 = take(2 * krows * c->hd);
-    w.kexp = take(krows / kKv8Block);
-    w.vexp = take(krows / kKv8Block);
-  }
   w.total = off;
   return w;
 }
@@ -412,14 +402,7 @@ extern "C" dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, 
   a.cluster = w.cluster;
   a.group = w.group;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (w.tc) {
-    Kv8Prep pp{base + w.qterms, reinterpret_cast<int*>(base + w.qexp), base + w.kterms, base + w.vf16, base + w.kexp,
-               base + w.vexp, cache->B * Hq * C, cache->B * cache->Hkv * w.Cp, w.Cp};
-    e = launch_kv8_attention_tc(a, pp, st);
-  } else {
-    e = launch_kv8_attention_mma(a, st);
-  }
+  cudaError_t e = w.tc ? launch_kv8_attention_tc(a, st) : launch_kv8_attention_mma(a, st);
   if (e == cudaSuccess && !w.cluster) e = launch_kv8_merge(a, st);
   return from_cuda(e);
 }

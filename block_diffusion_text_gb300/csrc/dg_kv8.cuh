@@ -173,30 +173,6 @@ DG_DEV uint32_t pack_e4m3(float lo, float hi) {
   return r;
 }
 
-// Two E4M3 terms of eight scaled values.
-DG_DEV void split8(const float (&x)[8], uint2& hi, uint2& lo) {
-  uint32_t h[2], l[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t c0 = pack_e4m3(x[4 * i], x[4 * i + 1]), c1 = pack_e4m3(x[4 * i + 2], x[4 * i + 3]);
-    const uint32_t w0 = e4m3x2_f16x2(c0), w1 = e4m3x2_f16x2(c1);
-    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w0));
-    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w1));
-    h[i] = c0 | (c1 << 16);
-    l[i] = pack_e4m3(x[4 * i] - f0.x, x[4 * i + 1] - f0.y) |
-           (pack_e4m3(x[4 * i + 2] - f1.x, x[4 * i + 3] - f1.y) << 16);
-  }
-  hi = make_uint2(h[0], h[1]);
-  lo = make_uint2(l[0], l[1]);
-}
-DG_DEV void unpack8(const uint4& w, float f, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16) * f;
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * f;
-  }
-}
 DG_DEV unsigned abs_top(const uint4& w) {
   return __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
 }
@@ -206,17 +182,6 @@ DG_DEV int top_exponent(unsigned bits) {
   return E == 0 ? kKv8Emin : min(max(E - 127 - 8 + (m > 96 ? 1 : 0), kKv8Emin), kKv8Emax);
 }
 
-// The forms of queries and new tokens that the tensor-core kernel reads, made
-// by its first launch in the call's workspace.
-struct Kv8Prep {
-  uint8_t* qterms;           // E4M3 [2 terms][qrows][hd]
-  int* qexp;                 // [qrows] exponent of a row's scale
-  uint8_t* kterms;           // E4M3 [2 terms][krows][hd], krows = B Hkv Cp
-  uint8_t* vf16;             // f16 [krows][hd]
-  uint8_t *kexp, *vexp;      // exponent bytes [B][Hkv][Cp / 64]
-  int qrows, krows, Cp;      // Cp: new tokens padded to whole tiles
-};
-
 // Rows per unit of the warp-MMA kernel for R query rows per kv head.
 int kv8_mma_rows(int hd, int64_t R);
 // Parts i = s mod kMergeSlices of a unit are summed by slice s of the merge, the
@@ -224,7 +189,7 @@ int kv8_mma_rows(int hd, int64_t R);
 constexpr int kMergeSlices = 8;
 
 cudaError_t launch_kv8_attention_mma(const Kv8AttnArgs& a, cudaStream_t st);
-cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cudaStream_t st);
+cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, cudaStream_t st);
 cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, cudaStream_t st);
 
 }  // namespace dg

@@ -5,46 +5,50 @@
 // run of 128-key tiles; the tiles of a call are dealt to the CTAs in equal
 // shares (dg_kv8.cuh), parts are merged by kv8_merge_kernel.  What the 8-bit
 // cache changes against the bf16 kernel (dg_attn_tc.cu):
-//  - S = Q K^T runs on kind::f8f6f4, so the key codes go from TMA into the MMA
-//    as they lie in memory.  A query row is split into two E4M3 terms, q 2^-x =
-//    hi + lo: a bf16 has 8 significant bits and each term holds 4, so the split
-//    is exact for elements down to 2^-10 of the row's largest and off by
-//    2^-10 / 224 of the largest below (its own bf16 rounding is 2^-9 of each).
-//    Two products at twice the 16-bit rate cost what one 16-bit product costs.
-//  - P V runs in f16: p' is rounded to f16 (2^-12), once, where bf16 would need
-//    two terms; the value codes become f16 (exact) in shared memory, by four
-//    warps that do nothing else.
-//  - Block scales never touch the codes: 2^ke joins the softmax factor of its 64
-//    columns and 2^ve the exponent of the probability (the running maximum is
-//    that of s + ve), whose share of the row sum is taken back.
-// The new tokens' bf16 keys and values are brought into the same forms by
-// kv8_prep_kernel: keys as two E4M3 terms on a scale per 64 tokens (four
-// products), values as f16 on such a scale (exact to 2^-22 of the block's
-// largest).
+//  - Eight warps expand the codes on their way to shared memory, keys with their
+//    block's scale to bf16 and values to f16, both exactly.  Queries and the new
+//    tokens' keys enter as the bf16 they are, so a score is the fp32 sum of exact
+//    products, whatever else is in its row, its block or behind its mask.  (Queries
+//    and new keys as two E4M3 terms each, against the codes as they lie, spared the
+//    expansion: 117 us where this takes 128.  But they took 2^-18 of the largest element
+//    of the row, or of 64 tokens, from every other: one padded token's key could
+//    cost the others all their bits.)
+//  - P V of cached tiles runs in f16: p' is rounded to f16 (2^-11), once, where
+//    bf16 would need two terms.  New tokens' values keep their exponent range:
+//    bf16 products, p' split into two bf16 (2^-17), the second over the other half
+//    of the scores' columns.
+//  - Value scales never touch the codes: 2^ve joins the exponent of the probability
+//    (the running maximum is that of s + ve), whose share of the row sum is taken
+//    back.
 //
-// Warp roles (16 warps, one CTA per SM):
-//   warp 0       TMA: Q terms per piece, K tiles into a ring of slots (a new tile
-//                takes two), V codes into their own ring (new tiles:
-//                f16, straight to the MMA's buffer)
+// Warp roles (20 warps, one CTA per SM):
+//   warp 0       TMA: queries per piece
 //   warps 1, 2   MMA, one for each row tile, taking turns: P_t V of key tile j, then
 //                S_t of tile j + 1, so that one row tile's softmax and waits run
 //                under the other's products
-//   warps 4-7    V codes to f16
+//   warps 4-7    values: codes to f16, new rows copied
 //   warps 8-15   softmax, one thread per row; P over S in TMEM
+//   warps 16-19  keys: codes to bf16, new rows copied
 //
-// Measured: a canvas of 256 rows over 131072 rows of 8 heads 116 us (the two
-// products at the measured bf16 rate: 72), 1.18 PFLOP/s; a key tile takes 3640
+// Measured: a canvas of 256 rows over 131072 rows of 8 heads 128 us (the two
+// products at the measured bf16 rate: 72), 1.07 PFLOP/s; a key tile takes some 3900
 // cycles, 2048 of them MMAs.  A row tile's chain (scores ready, two passes of
-// softmax 2100 to 2300 cycles, P V and the next S 1250) bounds it: without the
-// exponentials it runs 107 us, without all softmax work 83.  Tried and slower:
-// two threads a row (24 warps of 80 registers, 123 us; 20 of 96, 168 us), the
+// softmax 2100 to 2400 cycles, P V and the next S 1500 to 1800) bounds it, lengthened
+// by what the expansion takes of the issue slots and of shared memory (MMA
+// operands, expanded tiles and loads: some 2500 cycles a tile): with the keys' tiles
+// written but neither loaded nor expanded it runs 113 us, with loads that hit 120.
+// So the codes come through registers: rings of code tiles in shared memory, filled
+// by TMA, took 161 us (both) and 143 (one), expansion of half a tile at a time 131,
+// prefetches into L2 132 to 137, eight warps to each tile 142, four in all 162.
+// Tried and slower while the codes entered the MMA as they lie (117 us then): two
+// threads a row (24 warps of 80 registers, 123 us; 20 of 96, 168 us), the
 // scores read once block by block (123 to 129), the probabilities made on the old
 // maximum in one pass and again where it grew (135), loads 32 columns ahead (129),
 // scores of 64 keys at a time, two of them in flight to a row tile (126 to 129:
 // the softmax no longer waits, but an MMA of 64 columns takes as long as one of
 // 128 and the MMA warps have twice the turns), MMA warps without turns (143).
 // Head dim 64 has half the MMAs and the same softmax: 256 rows over 32768 rows of
-// 8 heads 35.3 us (head dim 128: 42.6; the warp-MMA kernel 91.7).
+// 8 heads 37 us (the warp-MMA kernel 91.7).
 #include <cfloat>
 
 #include "dg_kv8.cuh"
@@ -53,21 +57,23 @@ namespace dg {
 namespace {
 
 constexpr int kTK = 128;                   // keys per tile
-constexpr int kThreads = 512;
-constexpr int kNK = 4, kNV = 2;            // ring depths: K slots, V code and f16 slots
+constexpr int kThreads = 640;
+// Registers: the block is launched with 96 a thread; the softmax warps take 120,
+// the others keep 80.  The shares add up to no more than the launch's, or a
+// setmaxnreg would wait for ever.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 120, kOtherRegs = 80;
+static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "registers of one block");
+constexpr int kNS = 2;                     // slots of expanded keys, and of values
 constexpr float kHeadroom = 8.0f;          // p' of a row's maximum is 2^8 ..
 constexpr float kLazy = 6.0f;              // .. to 2^14: O is rescaled when the maximum grew by more than 2^6
 
 template <int HD>
 struct Smem {
-  static constexpr int kQ = 128 * HD;                // one term of one row tile
-  static constexpr int kK = kTK * HD;                // one tile of codes
-  static constexpr int kBox = kTK * 128;             // 64 f16 columns of a tile
-  static constexpr int kF16 = HD / 64 * kBox;
-  static constexpr int oK = 4 * kQ;
-  static constexpr int oVc = oK + kNK * kK;
-  static constexpr int oVf = oVc + kNV * kK;
-  static constexpr int oBar = oVf + kNV * kF16;
+  static constexpr int kBox = kTK * 128;             // 64 16-bit columns of a tile
+  static constexpr int kTile = HD / 64 * kBox;       // a tile of 128 rows in 16 bits
+  static constexpr int oK = 2 * kTile;               // behind the queries of both row tiles
+  static constexpr int oV = oK + kNS * kTile;
+  static constexpr int oBar = oV + kNS * kTile;
   static constexpr int oMl = oBar + 512;             // float2 [2 row tiles][128]: maximum and sum
   static constexpr int oFrom = oMl + 2 * 128 * 8;    // int2 [warps]: kv8_piece's `from`
   static constexpr int kTotal = oFrom + kThreads / 32 * 8;
@@ -84,7 +90,7 @@ constexpr int kColO = 256;
 DG_DEV void mma_s(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
   asm volatile(
       "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum)
       : "memory");
 }
@@ -101,24 +107,14 @@ DG_DEV void commit(uint64_t* bar) {
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
-// Shared-memory descriptors (swizzle over rows of SW bytes, 128 or 64, 8 SW bytes
-// between 8-row groups) as a low word, address and leading offset, and a high word.
+// Shared-memory descriptors (swizzle over rows of 128 bytes, 1024 between 8-row
+// groups) as a low word, address and leading offset, and a high word.
 DG_DEV uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | (lbo >> 4 << 16); }
-template <int SW>
 DG_DEV uint64_t desc64(uint32_t lo) {
-  constexpr uint32_t hi = (8u * SW >> 4) | (1u << 14) | ((SW == 128 ? 2u : 4u) << 29);
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "n"(hi));
   return d;
-}
-// D (+)= (Q_hi + Q_lo) K^T: the two terms of a query tile lie behind one another.
-template <int HD>
-DG_DEV void s_terms(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc, uint32_t accum) {
-#pragma unroll
-  for (int term = 0; term < 2; ++term)
-#pragma unroll
-    for (int kk = 0; kk < HD / 32; ++kk)
-      mma_s(d, desc64<HD>(q + term * (Smem<HD>::kQ >> 4) + 2 * kk), desc64<HD>(k + 2 * kk), idesc, (term | kk) ? 1u : accum);
 }
 // Bounded wait of a whole warp whose usual case, the phase is complete, costs
 // one try (63 cycles against 171 for mbar_wait_warp's loops, measured alone).
@@ -147,14 +143,136 @@ DG_DEV bool next_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, in
   return false;
 }
 
+DG_DEV uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+DG_DEV uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 16 codes to 16-bit words: keys times f as bf16, values as f16 (exact).
+DG_DEV void expand_keys(const uint4& w, float f, uint4 (&h)[2]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8];
+  const uint64_t f2 = f2_pack(f, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t x[2];
+    e4m3x4_f16x4(u[j], x[0], x[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&x[k]));
+      float y0, y1;
+      f2_unpack(f2_mul(f2_pack(t.x, t.y), f2), y0, y1);
+      o[2 * j + k] = pack_bf16(y0, y1);
+    }
+  }
+  h[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  h[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+DG_DEV void expand_values(const uint4& w, uint4 (&h)[2]) {
+  e4m3x4_f16x4(w.x, h[0].x, h[0].y);
+  e4m3x4_f16x4(w.y, h[0].z, h[0].w);
+  e4m3x4_f16x4(w.z, h[1].x, h[1].y);
+  e4m3x4_f16x4(w.w, h[1].z, h[1].w);
+}
+
+// The part of four warps: the tiles of all of the CTA's pieces, keys or values, to
+// the MMA's buffer of kNS slots.  A thread takes 16-byte chunks of codes and loads
+// the next tile's while it expands this one's.
+template <int HD, bool KEYS>
+DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, int w0, int w1, uint8_t* buf, uint64_t* full,
+                         uint64_t* empty, volatile int* abort) {
+  using Smem = Smem<HD>;
+  constexpr int IT = HD / 16, RS = 128 / IT;  // chunks of a row, and of a thread, whose rows are RS apart
+  static_assert(RS % 8 == 0, "one swizzle a thread");
+  // A row's chunk c of 16 elements is chunks 2 c and 2 c + 1 of its 16-bit row in box
+  // c / 4.  Eight consecutive lanes take four chunks of one box of two rows, whose
+  // swizzles make up the other four 16-byte banks.
+  const int tid = threadIdx.x & 127, lane = tid & 31;
+  const int r0 = HD == 128 ? tid / 32 * 4 + lane / 16 * 2 + (lane >> 2 & 1) : tid / 4;
+  const int c = HD == 128 ? (lane & 3) + (lane >> 3 & 1) * 4 : tid % 4;
+  const int o0 = c / 4 * Smem::kBox + r0 * 128 + ((c % 4 * 2 ^ (r0 & 7)) << 4), o1 = o0 ^ 16;
+  const uint8_t *codes = KEYS ? a.K : a.V, *rows = reinterpret_cast<const uint8_t*>(KEYS ? a.kn : a.vn);
+  bool ok = true;
+  int J = 0;
+  Piece p;
+  for (int w = w0; ok && next_piece(a, plan, from, w, w1, p);) {
+    const int n = p.tiles();
+    const size_t bh = (size_t)p.b * a.Hkv + p.hk;
+    uint4 x[IT];
+    const uint8_t *src = codes + (bh * a.cap + (size_t)p.t0 * kTK + r0) * HD + c * 16, *Ke = a.Ke + bh * a.nblk;
+    int left = p.len - p.t0 * kTK - r0, blk = p.t0 * 2, ke0 = 0, ke1 = 0;
+    // chunk `it` of the tile at src; what lies behind the sequence is not read
+    auto load = [&](int it) { x[it] = it * RS < left ? load16(src + it * RS * HD) : make_uint4(0, 0, 0, 0); };
+    auto scales = [&]() {
+      ke0 = Ke[blk];
+      ke1 = Ke[min(blk + 1, a.nblk - 1)];
+    };
+    if (!p.fresh(0)) {
+      if (KEYS) scales();
+#pragma unroll
+      for (int it = 0; it < IT; ++it) load(it);
+    }
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const int s = (J + j) & 1, par = ((J + j) >> 1) & 1;
+      if (!(ok = wait(&empty[s], par ^ 1, a.status, abort))) break;
+      uint8_t* dst = buf + s * Smem::kTile;
+      auto store = [&](int it, const uint4 (&h)[2]) {
+        *reinterpret_cast<uint4*>(dst + o0 + it * RS * 128) = h[0];
+        *reinterpret_cast<uint4*>(dst + o1 + it * RS * 128) = h[1];
+      };
+      if (!p.fresh(j)) {
+        const bool more = j + 1 < n && !p.fresh(j + 1);
+        const float f0 = pow2i(ke0 - kKv8Bias), f1 = pow2i(ke1 - kKv8Bias);
+        blk += 2;
+        if (KEYS && more) scales();
+        src += kTK * HD;
+        left -= kTK;
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {  // the first half of the chunks are the tile's first block
+          uint4 h[2];
+          if (KEYS) expand_keys(x[it], it < IT / 2 ? f0 : f1, h);
+          else expand_values(x[it], h);
+          if (more) load(it);
+          store(it, h);
+        }
+      } else {
+        // new rows as they are, zeros behind the last; the values' magnitudes are looked at
+        const int key0 = (p.t0 + j - p.ntc) * kTK;
+        const uint8_t* nr = rows + ((bh * a.C + key0 + r0) * HD + c * 16) * 2;
+        const int nleft = a.C - key0 - r0;
+        unsigned top = 0;
+#pragma unroll 4
+        for (int it = 0; it < IT; ++it) {
+          uint4 h[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+          if (it * RS < nleft) {
+            h[0] = load16(nr + it * RS * HD * 2);
+            h[1] = load16(nr + it * RS * HD * 2 + 16);
+          }
+          if (!KEYS) top = __vmaxu2(top, __vmaxu2(abs_top(h[0]), abs_top(h[1])));
+          store(it, h);
+        }
+        if (!KEYS && top_exponent(max(top & 0xffffu, top >> 16)) > kKv8EmaxAttn) atomicExch(a.status, kStatusValue);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+    }
+    J += n;
+  }
+}
+
 // DUP: up to 128 query rows.  Both row tiles hold the same rows and row tile t
 // takes key tiles t, t + 2, ..; their outputs are two parts, which the softmax
 // warps join themselves where the CTA has all of the unit's tiles.
 template <int HD, bool DUP>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
-                       const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mKn,
-                       const __grid_constant__ CUtensorMap mVn, Kv8AttnArgs a, Kv8Prep pp, float scale_log2) {
+    kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, Kv8AttnArgs a, float scale_log2) {
   using Smem = Smem<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // uniform over the CTA: return before any barrier
@@ -164,13 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::oBar);
   uint64_t* qfull = bars;
   uint64_t* qempty = qfull + 1;
-  uint64_t* kfull = qempty + 1;      // [kNK]
-  uint64_t* kempty = kfull + kNK;    // [kNK]
-  uint64_t* cfull = kempty + kNK;    // [kNV] V codes (or new f16 values) have landed
-  uint64_t* cempty = cfull + kNV;    // [kNV] V codes have been read
-  uint64_t* vfull = cempty + kNV;    // [kNV] f16 values ready for the MMA
-  uint64_t* vempty = vfull + kNV;    // [kNV]
-  uint64_t* sfull = vempty + kNV;    // [2]
+  uint64_t* kfull = qempty + 1;      // [kNS] keys ready for the MMA
+  uint64_t* kempty = kfull + kNS;    // [kNS]
+  uint64_t* vfull = kempty + kNS;    // [kNS] values
+  uint64_t* vempty = vfull + kNS;    // [kNS]
+  uint64_t* sfull = vempty + kNS;    // [2]
   uint64_t* pready = sfull + 2;      // [2 tiles][2 halves]
   uint64_t* pvdone = pready + 4;     // [2]
   uint64_t* turn = pvdone + 2;       // [2] row tile t's MMA warp may issue
@@ -185,13 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int readers = DUP ? 1 : 2;  // MMA warps that read a tile
     mbar_init(qempty, 2);
     mbar_init(meet, 8);
-    for (int s = 0; s < kNK; ++s) {
-      mbar_init(&kfull[s], 1);
+    for (int s = 0; s < kNS; ++s) {
+      mbar_init(&kfull[s], 4);
       mbar_init(&kempty[s], readers);
-    }
-    for (int s = 0; s < kNV; ++s) {
-      mbar_init(&cfull[s], 1);
-      mbar_init(&cempty[s], 4);
       mbar_init(&vfull[s], 4);
       mbar_init(&vempty[s], readers);
     }
@@ -225,78 +337,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int grp_rows = a.Hq / a.Hkv * a.C;
 
   if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 0) {
       if (blockIdx.x == 0)
         for (int b = lane; b < a.B; b += 32)
           if (a.len[b] < 0 || a.len[b] > a.cap) atomicExch(status, kStatusCapacity);
-      if (lane == 0) {
-        tma_prefetch(&mQ);
-        tma_prefetch(&mK);
-        tma_prefetch(&mV);
-      }
+      if (lane == 0) tma_prefetch(&mQ);
       bool ok = true;
-      int kslot = 0, kpar = 1, J = 0, np = 0;  // slot counters run on through the pieces
+      int np = 0;
       Piece p;
       for (int w = w0; ok && next_piece(a, plan, from, w, w1, p); ++np) {
         if (lane == 0) {
-          const int bh = p.b * a.Hkv + p.hk;
           ok = mbar_wait(qempty, (np & 1) ^ 1, status, abort);
           if (ok) {
-            const int qrow = bh * grp_rows + p.row0;
-            mbar_arrive_expect_tx(qfull, 4 * Smem::kQ);
+            const int qrow = (p.b * a.Hkv + p.hk) * grp_rows + p.row0;
+            mbar_arrive_expect_tx(qfull, 2 * Smem::kTile);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-              for (int term = 0; term < 2; ++term)
-                tma_load_2d(smem + (2 * t + term) * Smem::kQ, &mQ, qfull, 0, term * pp.qrows + qrow + (DUP ? 0 : 128 * t));
-          }
-          for (int j = 0; j < p.tiles() && ok; ++j, ++J) {
-            const bool fresh = p.fresh(j);
-            const int key = (p.t0 + j - (fresh ? p.ntc : 0)) * kTK;
-            for (int term = 0; term < (fresh ? 2 : 1) && ok; ++term) {
-              if (!(ok = mbar_wait(&kempty[kslot], kpar, status, abort))) break;
-              mbar_arrive_expect_tx(&kfull[kslot], Smem::kK);
-              tma_load_2d(smem + Smem::oK + kslot * Smem::kK, fresh ? &mKn : &mK, &kfull[kslot], 0,
-                          fresh ? term * pp.krows + bh * pp.Cp + key : bh * a.cap + key);
-              if (++kslot == kNK) {
-                kslot = 0;
-                kpar ^= 1;
-              }
-            }
-            if (!ok) break;
-            const int s = J % kNV, par = ((J / kNV) & 1) ^ 1;
-            if (!(ok = mbar_wait(&cempty[s], par, status, abort))) break;
-            if (fresh) {
-              if (!(ok = mbar_wait(&vempty[s], par, status, abort))) break;
-              uint8_t* dst = smem + Smem::oVf + s * Smem::kF16;
-              mbar_arrive_expect_tx(&cfull[s], Smem::kF16);
-              tma_load_2d(dst, &mVn, &cfull[s], 0, bh * pp.Cp + key);
-              if (HD == 128) tma_load_2d(dst + Smem::kBox, &mVn, &cfull[s], 64, bh * pp.Cp + key);
-            } else {
-              mbar_arrive_expect_tx(&cfull[s], Smem::kK);
-              tma_load_2d(smem + Smem::oVc + s * Smem::kK, &mV, &cfull[s], 0, bh * a.cap + key);
-            }
+              for (int x = 0; x < HD / 64; ++x)
+                tma_load_2d(smem + t * Smem::kTile + x * Smem::kBox, &mQ, qfull, 64 * x, qrow + (DUP ? 0 : 128 * t));
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
     } else if (warp < 3) {
       const int t = warp - 1;
-      constexpr uint32_t idS = idesc_e4m3(128, kTK);
-      constexpr uint32_t idPV = idesc_f16(128, HD, true);
-      const uint32_t lo_q = desc_lo(smem_u32(smem + 2 * t * Smem::kQ), 16), lo_k = desc_lo(smem_u32(smem + Smem::oK), 16);
-      const uint32_t lo_v = desc_lo(smem_u32(smem + Smem::oVf), Smem::kBox);
+      constexpr uint32_t idS = idesc_bf16(128, kTK, false);
+      constexpr uint32_t idPV = idesc_f16(128, HD, true), idPVn = idesc_bf16(128, HD, true);
+      const uint32_t lo_q = desc_lo(smem_u32(smem + t * Smem::kTile), 16), lo_k = desc_lo(smem_u32(smem + Smem::oK), 16);
+      const uint32_t lo_v = desc_lo(smem_u32(smem + Smem::oV), Smem::kBox);
       const uint32_t tS = tmem + 128 * t, tO = tmem + kColO + 128 * t;
       bool ok = true;
-      static_assert((kNK & (kNK - 1)) == 0 && kNV == 2, "slots from running counts");
-      int K = 0, J = 0, Jt = 0, np = 0, turns = t ^ 1;  // K slots, tiles, own tiles, pieces so far; parity of the turn
+      static_assert(kNS == 2, "slots from running counts");
+      int J = 0, Jt = 0, np = 0, turns = t ^ 1;  // tiles, own tiles, pieces so far; parity of the turn
       const int stride = DUP ? 2 : 1, begin = DUP ? t : 0;
       Piece p;
       for (int w = w0; ok && next_piece(a, plan, from, w, w1, p); ++np) {
         const int n = p.tiles(), jfresh = max(p.ntc - p.t0, 0);  // tiles from jfresh on hold new tokens
         const int own = DUP ? (n + 1 - t) >> 1 : n, steps = DUP ? (n + 1) >> 1 : n;
         int j = begin - stride;                           // own key tile k of the piece
-        int kc = K + (begin > 0 ? (jfresh > 0 ? 1 : 2) : 0);  // K slot of tile j + stride
         ok = wait(qfull, np & 1, status, abort);
         // Step k: P_t V of own key tile k, then S_t of own tile k + 1.  The two warps
         // take turns, step by step, which keeps the row tiles' softmax phases apart
@@ -306,96 +386,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         // also says that P_t V of tile k is done.
 #pragma unroll 1
         for (int k = -1; k < steps && ok; ++k) {
-          const int s = (J + j) & 1, jn = j + stride;
-          const bool next = k + 1 < own, fresh = jn >= jfresh;
-          const int ka = kc & (kNK - 1), kb = (kc + 1) & (kNK - 1);
-          if (next) {
-            if (!(ok = wait(&kfull[ka], (kc / kNK) & 1, status, abort))) break;
-            if (fresh && !(ok = wait(&kfull[kb], ((kc + 1) / kNK) & 1, status, abort))) break;
-          }
+          const int s = (J + j) & 1, jn = j + stride, sn = (J + jn) & 1;
+          const bool next = k + 1 < own;
+          if (next && !(ok = wait(&kfull[sn], ((J + jn) >> 1) & 1, status, abort))) break;
           if (k >= 0 && k < own) {
             if (!(ok = wait(&vfull[s], ((J + j) >> 1) & 1, status, abort))) break;
             // (the first P of a piece also says that the last one's output has been read)
             if (!(ok = wait(&pready[2 * t], (Jt + k) & 1, status, abort))) break;
             if (!(ok = wait(&turn[t], turns, status, abort))) break;
             tc_fence_after();
-            const uint32_t v = lo_v + s * (Smem::kF16 >> 4);
+            const uint32_t v = lo_v + s * (Smem::kTile >> 4);
+            const bool fresh = j >= jfresh;
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+              if (b) {
+                if (!(ok = wait(&pready[2 * t + 1], (Jt + k) & 1, status, abort))) break;
+                tc_fence_after();
+              }
+              const uint32_t vb = v + b * (64 * 128 >> 4);
+              if (!fresh) {
 #pragma unroll
-            for (int k4 = 0; k4 < kTK / 32; ++k4)
-              mma_pv(tO, tS + 8 * k4, desc64<128>(v + k4 * (2048 >> 4)), idPV, (k | k4) ? 1u : 0u);
-            if (!(ok = wait(&pready[2 * t + 1], (Jt + k) & 1, status, abort))) break;
-            tc_fence_after();
+                for (int k4 = 0; k4 < 4; ++k4)
+                  mma_pv(tO, tS + 32 * b + 8 * k4, desc64(vb + k4 * (2048 >> 4)), idPV, (k | b | k4) ? 1u : 0u);
+              } else {  // both terms of P
 #pragma unroll
-            for (int k4 = kTK / 32; k4 < kTK / 16; ++k4)
-              mma_pv(tO, tS + 8 * k4, desc64<128>(v + k4 * (2048 >> 4)), idPV, 1u);
+                for (int k4 = 0; k4 < 8; ++k4)
+                  mma_pv(tO, tS + 64 * b + 8 * k4, desc64(vb + (k4 & 3) * (2048 >> 4)), idPVn, (k | b | k4) ? 1u : 0u);
+              }
+            }
+            if (!ok) break;
           } else {
             if (!(ok = wait(&turn[t], turns, status, abort))) break;
             tc_fence_after();
           }
           turns ^= 1;
           if (next) {
-            uint32_t kd = lo_k + ka * (Smem::kK >> 4);
-#pragma unroll 1
-            for (int term = 0; term <= (fresh ? 1 : 0); ++term, kd = lo_k + kb * (Smem::kK >> 4))
-              s_terms<HD>(tS, lo_q, kd, idS, term);
+            const uint32_t kd = lo_k + sn * (Smem::kTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+              const uint32_t o = (kk >> 2) * (Smem::kBox >> 4) + 2 * (kk & 3);
+              mma_s(tS, desc64(lo_q + o), desc64(kd + o), idS, kk ? 1u : 0u);
+            }
           }
           if (lane == 0) mbar_arrive(&turn[t ^ 1]);
           if (next) commit(&sfull[t]);
           else if (k >= 0 && k + 1 == own) commit(&pvdone[t]);
           if (k >= 0 && k < own) commit(&vempty[s]);
-          if (next) {
-            commit(&kempty[ka]);
-            if (fresh) commit(&kempty[kb]);
-            kc += fresh ? 2 : 1;
-            if (DUP) kc += jn + 1 >= jfresh ? 2 : 1;
-          }
+          if (next) commit(&kempty[sn]);
           if (k + 2 == own || (own == 0 && k < 0)) commit(qempty);  // no later S reads Q
           j = jn;
         }
         J += n;
         Jt += own;
-        K += n + max(n - jfresh, 0);
       }
     }
   } else if (warp < 8) {
-    const int tid = threadIdx.x - 128;
-    bool ok = true;
-    int J = 0;
-    Piece p;
-    for (int w = w0; ok && next_piece(a, plan, from, w, w1, p);) {
-      for (int j = 0; j < p.tiles(); ++j, ++J) {
-        const int s = J % kNV, par = (J / kNV) & 1;
-        if (!(ok = wait(&cfull[s], par, status, abort))) break;
-        if (!p.fresh(j)) {
-          if (!(ok = wait(&vempty[s], par ^ 1, status, abort))) break;
-          const uint8_t* src = smem + Smem::oVc + s * Smem::kK;
-          uint8_t* dst = smem + Smem::oVf + s * Smem::kF16;
-          const int valid = p.len - (p.t0 + j) * kTK;
-#pragma unroll
-          for (int it = 0; it < HD / 16; ++it) {
-            const int id = it * 128 + tid, row = id / (HD / 16), c = id % (HD / 16);
-            uint4 v = *reinterpret_cast<const uint4*>(src + row * HD + ((c ^ swz<HD>(row)) << 4));
-            if (row >= valid) v = make_uint4(0, 0, 0, 0);  // what lies behind the sequence never enters an MMA
-            uint4 h[2];
-            e4m3x4_f16x4(v.x, h[0].x, h[0].y);
-            e4m3x4_f16x4(v.y, h[0].z, h[0].w);
-            e4m3x4_f16x4(v.z, h[1].x, h[1].y);
-            e4m3x4_f16x4(v.w, h[1].z, h[1].w);
-            uint8_t* d = dst + (c / 4) * Smem::kBox + row * 128;
-            const int ch = (c % 4) * 2, f = c / 4;  // the two boxes' lanes store their halves in opposite order: no bank conflicts
-            *reinterpret_cast<uint4*>(d + (((ch + f) ^ (row & 7)) << 4)) = f ? h[1] : h[0];
-            *reinterpret_cast<uint4*>(d + (((ch + 1 - f) ^ (row & 7)) << 4)) = f ? h[0] : h[1];
-          }
-          fence_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&cempty[s]);
-          mbar_arrive(&vfull[s]);
-        }
-      }
-    }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    expand_tiles<HD, false>(a, plan, from, w0, w1, smem + Smem::oV, vfull, vempty, abort);
+  } else if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    expand_tiles<HD, true>(a, plan, from, w0, w1, smem + Smem::oK, kfull, kempty, abort);
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int t = (warp - 8) / 4, q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
@@ -417,35 +469,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rpart = DUP ? r : 128 * t + r, ridx = p.row0 + rpart;
       auto tile = [&](int k) { return DUP ? 2 * k + t : k; };  // own tile k
       const bool valid_row = ridx < grp_rows;
-      const int qx = valid_row ? pp.qexp[(size_t)bh * grp_rows + ridx] : 0;
       const int qi = valid_row ? ridx % a.C : 0;
-      // exponents of the tile's two blocks: key 0, key 1, value 0, value 1
-      auto exps = [&](int j, int (&e)[4]) {
-        const bool fresh = p.fresh(j);
-        const int i = (p.t0 + j - (fresh ? p.ntc : 0)) * 2, nb = fresh ? pp.Cp / kKv8Block : a.nblk;
-        const uint8_t* ke = (fresh ? pp.kexp : a.Ke) + (size_t)bh * nb;
-        const uint8_t* ve = (fresh ? pp.vexp : a.Ve) + (size_t)bh * nb;
-        const int i1 = min(i + 1, nb - 1);
-        e[0] = ke[i];
-        e[1] = ke[i1];
-        e[2] = ve[i];
-        e[3] = ve[i1];
+      // value exponents of the tile's two blocks; new tokens have none
+      const uint8_t* Ve = a.Ve + (size_t)bh * a.nblk;
+      auto exps = [&](int j, int (&e)[2]) {
+        e[0] = e[1] = kKv8Bias;
+        if (p.fresh(j)) return;
+        const int i = (p.t0 + j) * 2;
+        e[0] = Ve[i];
+        e[1] = Ve[min(i + 1, a.nblk - 1)];
       };
-      int ex[4], en[4] = {};
+      int ex[2], en[2] = {};
       if (n > 0) exps(tile(0), en);
       float m_run = -INFINITY, l_run = 0.f;
       int ve_top = kKv8Emin;  // checked here: by the four warps of the V codes it cost 3 % more
       for (int own = 0; own < n; ++own) {
         const int j = tile(own);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ex[k] = en[k] - kKv8Bias;
+        for (int k = 0; k < 2; ++k) ex[k] = en[k] - kKv8Bias;
         if (own + 1 < n) exps(tile(own + 1), en);
         if (!(ok = wait(&sfull[t], (Jt + own) & 1, status, abort))) break;
         tc_fence_after();
         const bool fresh = p.fresh(j);
         const int key0 = (p.t0 + j - (fresh ? p.ntc : 0)) * kTK;
         int lim = (fresh ? a.C : p.len) - key0;  // columns of the tile that this row sees
-        ve_top = max(ve_top, lim > kKv8Block ? max(ex[2], ex[3]) : ex[2]);
+        ve_top = max(ve_top, lim > kKv8Block ? max(ex[0], ex[1]) : ex[0]);
         if (fresh && a.causal) lim = min(lim, qi - key0 + 1);
         // Two passes over the scores, 64 columns (one block's scales) at a
         // time: kept in registers between them they would need twice the
@@ -482,8 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x2 = fmax3(x2, s[c + 4], s[c + 5]);
             x3 = fmax3(x3, s[c + 6], s[c + 7]);
           }
-          const int ke = b ? ex[1] : ex[0], ve = b ? ex[3] : ex[2];
-          mx = fmaxf(mx, fmaf(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), scale_log2 * pow2i(qx + ke), (float)ve));
+          mx = fmaxf(mx, fmaf(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), scale_log2, (float)(b ? ex[1] : ex[0])));
         }
         if (own == 0) {
           m_run = mx;
@@ -507,25 +554,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float mm = m_run == -INFINITY ? 0.f : m_run - kHeadroom;
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b) {  // 32 columns of P each
+        for (int b = 0; b < 2; ++b) {  // 32 columns of P each, or of both its terms over the block's own scores
           float s[64];
           load(b, s);
-          const int ke = b ? ex[1] : ex[0], ve = b ? ex[3] : ex[2];
-          const float c = scale_log2 * pow2i(qx + ke), off = (float)ve - mm;
-          const uint64_t c2 = f2_pack(c, c), off2 = f2_pack(off, off);
+          const int ve = b ? ex[1] : ex[0];
+          const float off = (float)ve - mm;
+          const uint64_t c2 = f2_pack(scale_log2, scale_log2), off2 = f2_pack(off, off);
           uint64_t rs[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t hw[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float t0, t1;
-              f2_unpack(f2_fma(f2_pack(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), c2, off2), t0, t1);
-              const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+              float &p0 = s[32 * h + 2 * e], &p1 = s[32 * h + 2 * e + 1];
+              f2_unpack(f2_fma(f2_pack(p0, p1), c2, off2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
               rs[e & 1] = f2_add(rs[e & 1], f2_pack(p0, p1));
-              hw[e] = pack_f16(p0, p1);
             }
-            tmem_st16(tS + 32 * b + 16 * h, hw);
+            if (!fresh) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) hw[e] = pack_f16(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]);
+              tmem_st16(tS + 32 * b + 16 * h, hw);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) hw[e] = pack_bf16(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]);
+              tmem_st16(tS + 64 * b + 16 * h, hw);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                hw[e] = pack_bf16(s[32 * h + 2 * e] - __uint_as_float(hw[e] << 16),
+                                  s[32 * h + 2 * e + 1] - __uint_as_float(hw[e] & 0xffff0000u));
+              tmem_st16(tS + 64 * b + 32 + 16 * h, hw);
+            }
           }
           tmem_wait_st();
           tc_fence_before();
@@ -611,99 +671,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------- prep --
-// q to two E4M3 terms and a scale per row (8 elements a lane);
-// new keys to two E4M3 terms and new values to f16, with a scale per 64 tokens
-// (one CTA per block, zeros behind the last token).
-template <int HD>
-__global__ void __launch_bounds__(256) kv8_prep_kernel(Kv8AttnArgs a, Kv8Prep pp, int kv_ctas) {
-  constexpr int LPR = HD / 8, RPC = 256 / LPR;  // lanes per row, rows per CTA
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= kv_ctas) {
-    const long long row = (long long)(blockIdx.x - kv_ctas) * RPC + tid / LPR;
-    const bool there = row < pp.qrows;
-    const uint4 w = there ? *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + row * HD +
-                                                            (tid % LPR) * 8)
-                          : make_uint4(0, 0, 0, 0);
-    unsigned top = abs_top(w);
-    top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-    for (int o = LPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = top_exponent(top);
-    float x[8];
-    unpack8(w, pow2i(-e), x);
-    uint2 hi, lo;
-    split8(x, hi, lo);
-    if (!there) return;
-    *reinterpret_cast<uint2*>(pp.qterms + row * HD + (tid % LPR) * 8) = hi;
-    *reinterpret_cast<uint2*>(pp.qterms + ((size_t)pp.qrows + row) * HD + (tid % LPR) * 8) = lo;
-    if (tid % LPR == 0) pp.qexp[row] = e;
-    return;
-  }
-  __shared__ unsigned red[8];
-  const int nb = pp.Cp / kKv8Block, isv = blockIdx.x & 1, blk = (blockIdx.x >> 1) % nb, bh = (blockIdx.x >> 1) / nb;
-  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(isv ? a.vn : a.kn) + (size_t)bh * a.C * HD;
-  uint4 w[kKv8Block / RPC];
-  unsigned top = 0;
-#pragma unroll
-  for (int i = 0; i < kKv8Block / RPC; ++i) {
-    const int row = blk * kKv8Block + i * RPC + tid / LPR;
-    w[i] = row < a.C ? *reinterpret_cast<const uint4*>(src + (size_t)row * HD + (tid % LPR) * 8) : make_uint4(0, 0, 0, 0);
-    top = __vmaxu2(top, abs_top(w[i]));
-  }
-  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-  if (tid % 32 == 0) red[tid / 32] = top;
-  __syncthreads();
-  top = __reduce_max_sync(0xffffffffu, red[tid % 8]);
-  const int e = top_exponent(top);
-  if (tid == 0) (isv ? pp.vexp : pp.kexp)[(size_t)bh * nb + blk] = (uint8_t)(e + kKv8Bias);
-#pragma unroll
-  for (int i = 0; i < kKv8Block / RPC; ++i) {
-    const size_t row = (size_t)bh * pp.Cp + blk * kKv8Block + i * RPC + tid / LPR;
-    float x[8];
-    unpack8(w[i], pow2i(-e), x);
-    if (isv) {
-      *reinterpret_cast<uint4*>(pp.vf16 + row * HD * 2 + (tid % LPR) * 16) =
-          make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]), pack_f16(x[6], x[7]));
-    } else {
-      uint2 hi, lo;
-      split8(x, hi, lo);
-      *reinterpret_cast<uint2*>(pp.kterms + row * HD + (tid % LPR) * 8) = hi;
-      *reinterpret_cast<uint2*>(pp.kterms + ((size_t)pp.krows + row) * HD + (tid % LPR) * 8) = lo;
-    }
-  }
-}
-
 }  // namespace
 
 template <int HD, bool DUP>
-static cudaError_t run_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cudaStream_t st) {
+static cudaError_t run_tc(const Kv8AttnArgs& a, cudaStream_t st) {
   constexpr auto kern = kv8_attn_tc_kernel<HD, DUP>;
-  const uint64_t cached = (uint64_t)a.B * a.Hkv * a.cap;
-  CUtensorMap mQ, mK, mV, mKn, mVn;
-  if (!make_tmap_2d(&mQ, pp.qterms, HD, 2 * (uint64_t)pp.qrows, HD, HD, 128, true, HD) ||
-      !make_tmap_2d(&mK, a.K, HD, cached, HD, HD, kTK, true, HD) ||
-      !make_tmap_2d(&mV, a.V, HD, cached, HD, HD, kTK, true, HD))
-    return cudaErrorInvalidValue;
-  mKn = mK;  // without new tokens neither is used
-  mVn = mV;
-  if (a.kn && (!make_tmap_2d(&mKn, pp.kterms, HD, 2 * (uint64_t)pp.krows, HD, HD, kTK, true, HD) ||
-               !make_tmap_2d(&mVn, pp.vf16, HD, (uint64_t)pp.krows, HD * 2, 64, kTK)))
-    return cudaErrorInvalidValue;
+  CUtensorMap mQ;
+  if (!make_tmap_2d(&mQ, a.q, HD, (uint64_t)a.B * a.Hq * a.C, HD * 2, 64, 128)) return cudaErrorInvalidValue;
+  static const cudaError_t regs = [] {  // what the register shares are reckoned from
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+    return e == cudaSuccess && fa.numRegs < kLaunchRegs ? cudaErrorLaunchOutOfResources : e;
+  }();
+  if (regs != cudaSuccess) return regs;
   cudaError_t e = set_smem_once<kern>(Smem<HD>::kTotal);
   if (e != cudaSuccess) return e;
-  const int kv_ctas = a.kn ? 2 * a.B * a.Hkv * (pp.Cp / kKv8Block) : 0;
-  e = launch_pdl(kv8_prep_kernel<HD>, dim3(kv_ctas + cdiv(pp.qrows, 256 / (HD / 8))), dim3(256), 0, st, a, pp, kv_ctas);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(kKv8Ctas), dim3(kThreads), Smem<HD>::kTotal, st, mQ, mK, mV, mKn, mVn, a, pp,
+  return launch_pdl(kern, dim3(kKv8Ctas), dim3(kThreads), Smem<HD>::kTotal, st, mQ, a,
                     1.4426950408889634f / sqrtf((float)HD));
 }
 
-cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, const Kv8Prep& pp, cudaStream_t st) {
-  if (a.hd == 64) return a.subs == 2 ? run_tc<64, true>(a, pp, st) : run_tc<64, false>(a, pp, st);
-  if (a.hd == 128) return a.subs == 2 ? run_tc<128, true>(a, pp, st) : run_tc<128, false>(a, pp, st);
+cudaError_t launch_kv8_attention_tc(const Kv8AttnArgs& a, cudaStream_t st) {
+  if (a.hd == 64) return a.subs == 2 ? run_tc<64, true>(a, st) : run_tc<64, false>(a, st);
+  if (a.hd == 128) return a.subs == 2 ? run_tc<128, true>(a, st) : run_tc<128, false>(a, st);
   return cudaErrorInvalidValue;
 }
 

@@ -457,9 +457,11 @@ DG_API dg_status dg_kv8_read(const dg_kv8_cache* cache, int32_t row0, int32_t n,
  * the scores be in fp32; o must not overlap an input; what lies behind len is
  * never used.  Values go up to 448 * 2^40 in magnitude (V_exp bytes up to 167):
  * where a larger one is met the status word gets DG_ERR_VALUE, and the output is
- * not to be used.  Probabilities enter the product as f16 on the scale of the
- * row's largest, block by block: a contribution below 2^-33 of the largest is
- * lost.  Bounds as dg_attention_noalloc: C <= 1024, B * C <= 2^20,
+ * not to be used.  Scores are fp32 sums of exact products (of a query row's
+ * elements what is above 2^-27 of its largest at least).  Cached keys'
+ * probabilities enter the product as f16 on the scale of the row's largest, block
+ * by block: a contribution below 2^-33 of the largest is lost; new tokens' as pairs
+ * of bf16.  Bounds as dg_attention_noalloc: C <= 1024, B * C <= 2^20,
  * B * Hq <= 65535.  ws: dg_kv8_attention_workspace bytes (0 for a short cache: ws
  * may be NULL then), 256-byte aligned, contents of no matter; calls (and graphs)
  * that may overlap on the GPU need one each.                                  */
