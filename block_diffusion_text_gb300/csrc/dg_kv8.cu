@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(Kv8ReadArgs a) {
   const bool isv = blockIdx.z != 0;
   const int len = a.len[b];
   if ((len < 0 || len > a.cap) && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.status, kStatusCapacity);
-  const int rows = min(a.n, min(len, a.cap) - a.row0);           // rows of this sequence in the range
+  const int rows = min(a.n, min(max(len, 0), a.cap) - a.row0);   // rows of this sequence in the range (no length overflows)
   const long long c = (long long)blockIdx.x * kReadThreads + threadIdx.x;
   const int row = (int)(c / CPR);
   if (row >= rows) return;
