@@ -468,6 +468,12 @@ def quantize_rows_e4m3(X: torch.Tensor, stream=None):
 
 KV8_BLOCK = 64  # cached tokens per scale of the 8-bit cache
 
+# Workspaces of kv8_attention, one for each (device, stream): the calls of a stream run one after another, so the caches
+# of a stack share it.  The lock is held until a call's launches are enqueued: those of two host threads on one stream
+# must not mix, and none may replace a workspace that another has not launched with yet.
+_kv8_workspaces = {}
+_kv8_lock = threading.Lock()
+
 
 def _need(ok, what):
     if not ok:
@@ -503,7 +509,7 @@ class Kv8Cache:
         self._ref = ct.byref(self.s)
         self._lib = load()
         self._index = K.device.index
-        self._ws_bytes, self._ws, self._shapes = {}, {}, {}
+        self._ws_bytes, self._shapes = {}, {}
 
     @property
     def len(self) -> torch.Tensor:
@@ -541,19 +547,11 @@ class Kv8Cache:
         return n
 
     def _workspace(self, n, st, stream):
-        """A workspace of n bytes for a call on the stream with handle st, to be held until the call is enqueued.
-
-        One per stream, kept: the calls of a stream run one after another.  Under graph capture one from the
-        graph's own pool, so that graphs that overlap share none; the pool gives its memory to the next tensor
-        (the call's own output, too) as soon as it is let go."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return self._workspace(n, st, None)
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(n, dtype=torch.uint8, device=self.device)
-        t = self._ws.get(st)
+        """The workspace of the stream with handle st, of n bytes at least; called with _kv8_lock held."""
+        t = _kv8_workspaces.get((self._index, st))
         if t is None or t.numel() < n:
-            t = self._ws[st] = torch.empty(n, dtype=torch.uint8, device=self.device)
+            with torch.cuda.stream(stream):  # memory of the launching stream
+                t = _kv8_workspaces[self._index, st] = torch.empty(n, dtype=torch.uint8, device=self.device)
         return t
 
     def _attention_shapes(self, q):
@@ -630,21 +628,15 @@ def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = Non
     """Attention of C new tokens over the cached rows and their own k, v (dg_kv8_attention); o [B*C, Hq*hd].
 
     q: bf16 [B, Hq, C, hd]; k, v: bf16 [B, Hkv, C, hd], or None for the cached rows alone.  ws: optional uint8
-    workspace of cache.workspace_bytes(C, Hq) bytes, not shared by calls that may overlap; by default the cache keeps
-    one for each stream, and a captured call takes one from the graph's pool."""
+    workspace of cache.workspace_bytes(C, Hq) bytes, not shared by calls that may overlap; by default the calls of a
+    stream share one, which is kept (kv8_release_workspaces), and a captured call takes one from the graph's pool."""
     C, Hq, new, shape, wn = cache._shapes.get(q.shape) or cache._attention_shapes(q)
-    qp, kp, vp, wp = cache._bf16(q, q.shape, "q"), None, None, None
+    qp, kp, vp = cache._bf16(q, q.shape, "q"), None, None
     if k is not None and v is not None:
         kp, vp = cache._bf16(k, new, "k"), cache._bf16(v, new, "v")
     elif k is not v:
         raise ValueError("k and v come together")
     st = cache._launch_stream(stream)
-    if ws is not None:
-        _need(ws.device == cache.device and ws.is_contiguous(), "ws: contiguous, on the cache's device")
-        wp, wn = ws.data_ptr(), ws.numel() * ws.element_size()
-    elif wn:
-        ws = cache._workspace(wn, st, stream)
-        wp = ws.data_ptr()
     if out is not None:
         op = cache._bf16(out, shape, "out")
     else:
@@ -654,7 +646,45 @@ def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = Non
             with torch.cuda.stream(stream):  # memory of the launching stream
                 out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
         op = out.data_ptr()
-    rc = cache._lib.dg_kv8_attention(cache._ref, qp, kp, vp, op, C, Hq, 1 if causal else 0, wp, wn, st)
+
+    wp, flag = None, 1 if causal else 0
+    if ws is not None:
+        _need(ws.device == cache.device and ws.is_contiguous(), "ws: contiguous, on the cache's device")
+        wp, wn = ws.data_ptr(), ws.numel() * ws.element_size()
+    elif wn:
+        if not _capturing(stream):
+            with _kv8_lock:
+                wp = cache._workspace(wn, st, stream).data_ptr()
+                rc = cache._lib.dg_kv8_attention(cache._ref, qp, kp, vp, op, C, Hq, flag, wp, wn, st)
+            if rc:
+                raise DgError(rc, "dg_kv8_attention")
+            return out
+        # from the graph's own pool, so that graphs that overlap share none; held until the launches are enqueued, since
+        # the pool gives the memory of a tensor to the next one as soon as it is let go
+        with torch.cuda.stream(stream):
+            ws = torch.empty(wn, dtype=torch.uint8, device=cache.device)
+        wp = ws.data_ptr()
+    rc = cache._lib.dg_kv8_attention(cache._ref, qp, kp, vp, op, C, Hq, flag, wp, wn, st)
     if rc:
         raise DgError(rc, "dg_kv8_attention")
     return out
+
+
+def _capturing(stream):
+    """Whether the stream (None: the current one) is being captured into a graph."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def kv8_release_workspaces(device=None) -> None:
+    """Let go of the workspaces that kv8_attention keeps for the streams of `device` (default: of every device).
+
+    Their memory goes back to PyTorch's allocator in the order of each stream; the next call takes a new one."""
+    index = None if device is None else torch.device(device).index
+    if device is not None and index is None:
+        index = torch.cuda.current_device()
+    with _kv8_lock:
+        for key in [k for k in _kv8_workspaces if index is None or k[0] == index]:
+            del _kv8_workspaces[key]
