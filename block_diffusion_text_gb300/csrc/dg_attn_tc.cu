@@ -306,8 +306,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int col = 32 * c;
         float o[32];
         tmem_ld32(tO + col, o);
-        if (!valid) continue;
-        if (nsplit == 1) {
+        if (valid && nsplit == 1) {
           const float inv = 1.0f / l_run;
           uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o) +
                                                 ((size_t)b * a.C + i) * ((size_t)a.Hq * kTcHD) +
@@ -321,13 +320,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             w.w = pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
             dst[q] = w;
           }
-        } else {
+        } else if (valid) {
           const size_t rowid = (((size_t)split * a.B + b) * a.Hq + h) * a.C + i;
           float4* dst = reinterpret_cast<float4*>(a.opart + rowid * kTcHD + col);
 #pragma unroll
           for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           if (c == 0) *reinterpret_cast<float2*>(a.ml + rowid * 2) = make_float2(m_run, l_run);
         }
+        __syncwarp();  // the next TMEM load is the whole warp's
       }
     }
   }

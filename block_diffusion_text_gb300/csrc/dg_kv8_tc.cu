@@ -621,12 +621,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e)  // with one tile TMEM holds another piece's output in the second place
             o[e] = p.tiles() > 1 ? fmaf(w0, o[e], w1 * o1[e]) : w0 * o[e];
-          if (!valid_row) continue;
-          uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
+          if (valid_row) {
+            uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[q] = make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]), pack_bf16(o[8 * q + 2], o[8 * q + 3]),
-                                pack_bf16(o[8 * q + 4], o[8 * q + 5]), pack_bf16(o[8 * q + 6], o[8 * q + 7]));
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]), pack_bf16(o[8 * q + 2], o[8 * q + 3]),
+                                  pack_bf16(o[8 * q + 4], o[8 * q + 5]), pack_bf16(o[8 * q + 6], o[8 * q + 7]));
+          }
+          __syncwarp();  // the next TMEM load is the whole warp's
         }
         if (!(ok = join())) break;  // both have read the outputs, and ml
         Jt += n;
@@ -641,20 +643,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (!valid_row) continue;
-        if (!DUP && whole) {
+        if (valid_row && !DUP && whole) {
           uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             dst[q] = make_uint4(pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv), pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
                                 pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv), pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
-        } else {
+        } else if (valid_row) {
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             *kv8_part(a, slot, 8 * c + q, rpart) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-          if (c == 0)
-            a.ml[slot * a.prows + rpart] = make_float2(m_run, l_run);
+          if (c == 0) a.ml[slot * a.prows + rpart] = make_float2(m_run, l_run);
         }
+        __syncwarp();
       }
       Jt += n;
       np += n > 0;
