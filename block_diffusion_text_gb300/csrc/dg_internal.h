@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/dg.h"
 
 namespace dg {
@@ -74,13 +76,20 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Opt a kernel in to more than 48 KB of dynamic shared memory, once per
-// kernel (the value is fixed per kernel), so that enqueueing a step makes no
-// attribute calls and can be captured into a CUDA graph.
+// Opt a kernel in to more than 48 KB of dynamic shared memory, once per kernel
+// and device (the value is fixed per kernel; the attribute is the device's), so that
+// enqueueing a step makes no attribute calls and can be captured into a CUDA graph.
 template <auto Kernel>
 cudaError_t set_smem_once(int bytes) {
-  static cudaError_t result = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return result;
+  static std::atomic<uint64_t> done{0};  // a bit for each of the first 64 devices
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (bf16, or
