@@ -15,6 +15,11 @@ constexpr int kKv8Emin = -64, kKv8Emax = 118;
 // the largest scale it still has 2^30 above the smallest fp32, and the row's sum
 // gets it back exactly; further down the sum would lose it.
 constexpr int kKv8EmaxAttn = 40;
+// Largest running maximum (log2 units; scores of 2^23).  A probability's argument is
+// one rounding, s c + (ve - m): the rest of m's own rounding grows with m, up to
+// 2 here, which the headroom below f16's largest holds.  Beyond, fp32 has not even
+// the scores' units.
+constexpr float kKv8Far = 16777216.0f;
 constexpr int kKv8Ctas = kTargetCtas;     // CTAs of an attention launch (one per SM)
 // Warps (workers) per CTA of the warp-MMA kernel for units of `rows` rows: as
 // many as their registers allow.
@@ -147,6 +152,8 @@ DG_DEV int swz(int r) {
   return HD == 128 ? (r & 7) : HD == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
 }
 
+// Whether a running maximum lies too far from zero (none yet: no).
+DG_DEV bool kv8_far(float m) { return fabsf(m) > kKv8Far && m != -INFINITY; }
 // 2^e as a float, e clamped to the normal range.
 DG_DEV float pow2i(int e) { return __uint_as_float((unsigned)(min(max(e, -126), 127) + 127) << 23); }
 DG_DEV float ex2_approx(float x) {

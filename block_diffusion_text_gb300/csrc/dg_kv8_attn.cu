@@ -557,7 +557,10 @@ __global__ void __launch_bounds__(32 * W, 1)
         }
       }
     }
-    if (max(ve_top, top_exponent(max(vn_top & 0xffffu, vn_top >> 16))) > kKv8EmaxAttn) atomicExch(a.status, kStatusValue);
+    bool beyond = max(ve_top, top_exponent(max(vn_top & 0xffffu, vn_top >> 16))) > kKv8EmaxAttn;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) beyond |= kv8_far(acc.m[nt][0]) || kv8_far(acc.m[nt][1]);
+    if (beyond) atomicExch(a.status, kStatusValue);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok || (n > 0 && !(ok = wait(&pvdone[t], np & 1, status, abort)))) break;
       tc_fence_after();
-      if (ve_top > kKv8EmaxAttn) atomicExch(status, kStatusValue);
+      if (ve_top > kKv8EmaxAttn || (valid_row && kv8_far(m_run))) atomicExch(status, kStatusValue);
       const bool whole = p.t0 == 0 && p.t1 == p.nt;
       const size_t slot = ((size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1)) * (DUP ? 2 : 1) + (DUP ? t : 0);
       const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;

@@ -453,11 +453,11 @@ DG_API dg_status dg_kv8_read(const dg_kv8_cache* cache, int32_t row0, int32_t n,
  * single-token form.  Sequences of any lengths share a call (0 included; in long
  * caches the work is divided by keys, not by sequences); a row without any key is
  * zero.
- * q, k and v must be finite, the new ones a causal mask hides included, as must
- * the scores be in fp32; o must not overlap an input; what lies behind len is
- * never used.  Values go up to 448 * 2^40 in magnitude (V_exp bytes up to 167):
- * where a larger one is met the status word gets DG_ERR_VALUE, and the output is
- * not to be used.  Scores are fp32 sums of exact products (of a query row's
+ * q, k and v must be finite, the new ones a causal mask hides included; o must not
+ * overlap an input; what lies behind len is never used.  Values go up to 448 * 2^40
+ * in magnitude (V_exp bytes up to 167), scores up to 2^23 (beyond, fp32 does not
+ * hold their units): where larger ones are met, scores as the largest of a run of
+ * keys, the status word gets DG_ERR_VALUE, and the output is not to be used.  Scores are fp32 sums of exact products (of a query row's
  * elements what is above 2^-27 of its largest at least).  Cached keys'
  * probabilities enter the product as f16 on the scale of the row's largest, block
  * by block: a contribution below 2^-33 of the largest is lost; new tokens' as pairs
