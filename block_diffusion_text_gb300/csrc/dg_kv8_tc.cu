@@ -27,7 +27,8 @@
 //                S_t of tile j + 1, so that one row tile's softmax and waits run
 //                under the other's products
 //   warps 4-7    values: codes to f16, new rows copied
-//   warps 8-15   softmax, one thread per row; P over S in TMEM
+//   warps 8-15   softmax, one thread per row, 64 columns at a time (up to 128 rows 32,
+//                for shorter code); P over S in TMEM
 //   warps 16-19  keys: codes to bf16, new rows copied
 //
 // Measured: a canvas of 256 rows over 131072 rows of 8 heads 128 us (the two
@@ -38,8 +39,9 @@
 // operands, expanded tiles and loads: some 2500 cycles a tile): with the keys' tiles
 // written but neither loaded nor expanded it runs 113 us, with loads that hit 120.
 // So the codes come through registers: rings of code tiles in shared memory, filled
-// by TMA, took 161 us (both) and 143 (one), expansion of half a tile at a time 131,
-// prefetches into L2 132 to 137, eight warps to each tile 142, four in all 162.
+// by TMA, took 161 us (both) and 143 (one), slots filled by cp.async 132, expansion
+// of half a tile at a time 131, prefetches into L2 132 to 137, eight warps to each
+// tile 142, four in all 162.
 // Tried and slower while the codes entered the MMA as they lie (117 us then): two
 // threads a row (24 warps of 80 registers, 123 us; 20 of 96, 168 us), the
 // scores read once block by block (123 to 129), the probabilities made on the old
@@ -67,13 +69,15 @@ constexpr int kNS = 2;                     // slots of expanded keys, and of val
 constexpr float kHeadroom = 8.0f;          // p' of a row's maximum is 2^8 ..
 constexpr float kLazy = 6.0f;              // .. to 2^14: O is rescaled when the maximum grew by more than 2^6
 
-template <int HD>
+template <int HD, bool DUP>
 struct Smem {
   static constexpr int kBox = kTK * 128;             // 64 16-bit columns of a tile
   static constexpr int kTile = HD / 64 * kBox;       // a tile of 128 rows in 16 bits
   static constexpr int oK = 2 * kTile;               // behind the queries of both row tiles
   static constexpr int oV = oK + kNS * kTile;
-  static constexpr int oBar = oV + kNS * kTile;
+  static constexpr int kCode = DUP ? kTK * HD : 0;   // codes on their way: a tile of keys, one of values
+  static constexpr int oC = oV + kNS * kTile;
+  static constexpr int oBar = oC + 2 * kCode;
   static constexpr int oMl = oBar + 512;             // float2 [2 row tiles][128]: maximum and sum
   static constexpr int oFrom = oMl + 2 * 128 * 8;    // int2 [warps]: kv8_piece's `from`
   static constexpr int kTotal = oFrom + kThreads / 32 * 8;
@@ -181,12 +185,18 @@ DG_DEV void expand_values(const uint4& w, uint4 (&h)[2]) {
 }
 
 // The part of four warps: the tiles of all of the CTA's pieces, keys or values, to
-// the MMA's buffer of kNS slots.  A thread takes 16-byte chunks of codes and loads
-// the next tile's while it expands this one's.
-template <int HD, bool KEYS>
+// the MMA's buffer of kNS slots.  A thread takes 16-byte chunks of codes and has the
+// next tile's on their way while it expands this one's: in registers, or (DUP) in
+// slots of its own in shared memory.  Up to 128 rows the MMAs and the softmax of a
+// tile are half as many, and the expansion bounds the call: it has to be a loop
+// whose code stays in the instruction cache (64 rows over 131072 rows of 8 heads 97 us
+// unrolled, 87 rolled; 375 ragged sequences of up to 2000 rows, 4 heads of 24 rows, 296
+// and 207), which registers do not allow.  With 256 rows shared memory is the
+// scarcer (128 us in registers, 132 in slots, 256 rows over 131072).
+template <int HD, bool DUP, bool KEYS>
 DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, int w0, int w1, uint8_t* buf, uint64_t* full,
-                         uint64_t* empty, volatile int* abort) {
-  using Smem = Smem<HD>;
+                         uint64_t* empty, uint8_t* slots, volatile int* abort) {
+  using Smem = Smem<HD, DUP>;
   constexpr int IT = HD / 16, RS = 128 / IT;  // chunks of a row, and of a thread, whose rows are RS apart
   static_assert(RS % 8 == 0, "one swizzle a thread");
   // A row's chunk c of 16 elements is chunks 2 c and 2 c + 1 of its 16-bit row in box
@@ -197,25 +207,31 @@ DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, 
   const int c = HD == 128 ? (lane & 3) + (lane >> 3 & 1) * 4 : tid % 4;
   const int o0 = c / 4 * Smem::kBox + r0 * 128 + ((c % 4 * 2 ^ (r0 & 7)) << 4), o1 = o0 ^ 16;
   const uint8_t *codes = KEYS ? a.K : a.V, *rows = reinterpret_cast<const uint8_t*>(KEYS ? a.kn : a.vn);
+  slots += tid * 16;  // chunk `it` of this thread at 2048 it
   bool ok = true;
   int J = 0;
   Piece p;
   for (int w = w0; ok && next_piece(a, plan, from, w, w1, p);) {
-    const int n = p.tiles();
+    const int n = p.tiles(), cached = min(p.t1, p.ntc) - p.t0;
     const size_t bh = (size_t)p.b * a.Hkv + p.hk;
-    uint4 x[IT];
     const uint8_t *src = codes + (bh * a.cap + (size_t)p.t0 * kTK + r0) * HD + c * 16, *Ke = a.Ke + bh * a.nblk;
     int left = p.len - p.t0 * kTK - r0, blk = p.t0 * 2, ke0 = 0, ke1 = 0;
-    // chunk `it` of the tile at src; what lies behind the sequence is not read
-    auto load = [&](int it) { x[it] = it * RS < left ? load16(src + it * RS * HD) : make_uint4(0, 0, 0, 0); };
+    uint4 x[DUP ? 1 : IT];
+    // chunk `it` of the tile at src on its way; what lies behind the sequence is not read
+    auto load = [&](int it) {
+      const bool there = it * RS < left;
+      if constexpr (DUP) cp_async16(slots + it * 2048, there ? src + it * RS * HD : codes, there);
+      else x[it] = there ? load16(src + it * RS * HD) : make_uint4(0, 0, 0, 0);
+    };
     auto scales = [&]() {
       ke0 = Ke[blk];
       ke1 = Ke[min(blk + 1, a.nblk - 1)];
     };
-    if (!p.fresh(0)) {
-      if (KEYS) scales();
+    if (KEYS && cached > 0) scales();
 #pragma unroll
-      for (int it = 0; it < IT; ++it) load(it);
+    for (int it = 0; it < IT; ++it) {
+      if (cached > 0) load(it);
+      if (DUP) cp_async_commit();  // a group for each chunk
     }
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
@@ -226,20 +242,37 @@ DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, 
         *reinterpret_cast<uint4*>(dst + o0 + it * RS * 128) = h[0];
         *reinterpret_cast<uint4*>(dst + o1 + it * RS * 128) = h[1];
       };
-      if (!p.fresh(j)) {
-        const bool more = j + 1 < n && !p.fresh(j + 1);
+      if (j < cached) {
+        const bool more = j + 1 < cached;
         const float f0 = pow2i(ke0 - kKv8Bias), f1 = pow2i(ke1 - kKv8Bias);
         blk += 2;
         if (KEYS && more) scales();
         src += kTK * HD;
         left -= kTK;
-#pragma unroll
-        for (int it = 0; it < IT; ++it) {  // the first half of the chunks are the tile's first block
+        auto expand = [&](int it, const uint4& y) {  // the first half of the chunks are the tile's first block
           uint4 h[2];
-          if (KEYS) expand_keys(x[it], it < IT / 2 ? f0 : f1, h);
-          else expand_values(x[it], h);
-          if (more) load(it);
+          if (KEYS) expand_keys(y, it < IT / 2 ? f0 : f1, h);
+          else expand_values(y, h);
           store(it, h);
+        };
+        if constexpr (DUP) {
+          cp_async_wait<IT - 1>();
+          x[0] = *reinterpret_cast<const uint4*>(slots);
+#pragma unroll 1
+          for (int it = 0; it < IT; ++it) {
+            const uint4 y = x[0];
+            cp_async_wait<IT - 2>();
+            x[0] = *reinterpret_cast<const uint4*>(slots + (it + 1 < IT ? it + 1 : 0) * 2048);
+            expand(it, y);
+            if (more) load(it);  // the chunk's slot again
+            cp_async_commit();
+          }
+        } else {
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            expand(it, x[it]);
+            if (more) load(it);
+          }
         }
       } else {
         // new rows as they are, zeros behind the last; the values' magnitudes are looked at
@@ -273,7 +306,7 @@ DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, 
 template <int HD, bool DUP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, Kv8AttnArgs a, float scale_log2) {
-  using Smem = Smem<HD>;
+  using Smem = Smem<HD, DUP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // uniform over the CTA: return before any barrier
     if (threadIdx.x == 0) atomicExch(a.status, kStatusTimeout);
@@ -410,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mma_pv(tO, tS + 32 * b + 8 * k4, desc64(vb + k4 * (2048 >> 4)), idPV, (k | b | k4) ? 1u : 0u);
               } else {  // both terms of P
 #pragma unroll
-                for (int k4 = 0; k4 < 8; ++k4)
-                  mma_pv(tO, tS + 64 * b + 8 * k4, desc64(vb + (k4 & 3) * (2048 >> 4)), idPVn, (k | b | k4) ? 1u : 0u);
+                for (int k4 = 0; k4 < 8; ++k4)  // of each 32 keys the first terms, then the second
+                  mma_pv(tO, tS + 64 * b + 8 * k4, desc64(vb + (k4 / 4 * 2 + (k4 & 1)) * (2048 >> 4)), idPVn, (k | b | k4) ? 1u : 0u);
               }
             }
             if (!ok) break;
@@ -442,16 +475,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    expand_tiles<HD, false>(a, plan, from, w0, w1, smem + Smem::oV, vfull, vempty, abort);
+    expand_tiles<HD, DUP, false>(a, plan, from, w0, w1, smem + Smem::oV, vfull, vempty, smem + Smem::oC + Smem::kCode, abort);
   } else if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    expand_tiles<HD, true>(a, plan, from, w0, w1, smem + Smem::oK, kfull, kempty, abort);
+    expand_tiles<HD, DUP, true>(a, plan, from, w0, w1, smem + Smem::oK, kfull, kempty, smem + Smem::oC, abort);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int t = (warp - 8) / 4, q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + kColO + 128 * t;
+    constexpr int NC = DUP ? 32 : 64;  // columns of scores at a time
     bool ok = true;
     int Jt = 0, np = 0, met = 0;  // own tiles, pieces that had some, phases of meet
     float2* ml = reinterpret_cast<float2*>(smem + Smem::oMl);
@@ -498,9 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Two passes over the scores, 64 columns (one block's scales) at a
         // time: kept in registers between them they would need twice the
         // registers and unrolled code that no instruction cache holds.
-        auto load = [&](int b, float (&s)[64]) {
-          tmem_ld32_async(tS + 64 * b, *reinterpret_cast<float(*)[32]>(s));
-          tmem_ld32_async(tS + 64 * b + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+        auto load = [&](int q, float (&s)[NC]) {
+#pragma unroll
+          for (int i = 0; i < NC / 32; ++i) tmem_ld32_async(tS + NC * q + 32 * i, *reinterpret_cast<float(*)[32]>(s + 32 * i));
           tmem_wait_ld();
         };
         if (__any_sync(0xffffffffu, lim < kTK)) {
@@ -519,18 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float mx = -INFINITY;
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-          float s[64];
-          load(b, s);
+        for (int q = 0; q < kTK / NC; ++q) {
+          float s[NC];
+          load(q, s);
           float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]), x2 = fmaxf(s[4], s[5]), x3 = fmaxf(s[6], s[7]);
 #pragma unroll
-          for (int c = 8; c < 64; c += 8) {
+          for (int c = 8; c < NC; c += 8) {
             x0 = fmax3(x0, s[c], s[c + 1]);
             x1 = fmax3(x1, s[c + 2], s[c + 3]);
             x2 = fmax3(x2, s[c + 4], s[c + 5]);
             x3 = fmax3(x3, s[c + 6], s[c + 7]);
           }
-          mx = fmaxf(mx, fmaf(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), scale_log2, (float)(b ? ex[1] : ex[0])));
+          mx = fmaxf(mx, fmaf(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), scale_log2, (float)(NC * q < kKv8Block ? ex[0] : ex[1])));
         }
         if (own == 0) {
           m_run = mx;
@@ -554,15 +588,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float mm = m_run == -INFINITY ? 0.f : m_run - kHeadroom;
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b) {  // 32 columns of P each, or of both its terms over the block's own scores
-          float s[64];
-          load(b, s);
-          const int ve = b ? ex[1] : ex[0];
+        for (int q = 0; q < kTK / NC; ++q) {  // half as many columns of P each, or of both its terms over its own scores
+          float s[NC];
+          load(q, s);
+          const int ve = NC * q < kKv8Block ? ex[0] : ex[1];
           const float off = (float)ve - mm;
           const uint64_t c2 = f2_pack(scale_log2, scale_log2), off2 = f2_pack(off, off);
           uint64_t rs[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < NC / 32; ++h) {
             uint32_t hw[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -575,22 +609,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!fresh) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) hw[e] = pack_f16(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]);
-              tmem_st16(tS + 32 * b + 16 * h, hw);
+              tmem_st16(tS + NC / 2 * q + 16 * h, hw);
             } else {
 #pragma unroll
               for (int e = 0; e < 16; ++e) hw[e] = pack_bf16(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]);
-              tmem_st16(tS + 64 * b + 16 * h, hw);
+              tmem_st16(tS + NC * q + 32 * h, hw);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 hw[e] = pack_bf16(s[32 * h + 2 * e] - __uint_as_float(hw[e] << 16),
                                   s[32 * h + 2 * e + 1] - __uint_as_float(hw[e] & 0xffff0000u));
-              tmem_st16(tS + 64 * b + 32 + 16 * h, hw);
+              tmem_st16(tS + NC * q + 32 * h + 16, hw);
             }
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&pready[2 * t + b]);
+          if (NC == 64 || (q & 1)) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pready[2 * t + NC * q / kKv8Block]);
+          }
           float x0, x1;
           f2_unpack(f2_add(rs[0], rs[1]), x0, x1);
           l_run = fmaf(x0 + x1, pow2i(-ve), l_run);
@@ -685,9 +721,9 @@ static cudaError_t run_tc(const Kv8AttnArgs& a, cudaStream_t st) {
     return e == cudaSuccess && fa.numRegs < kLaunchRegs ? cudaErrorLaunchOutOfResources : e;
   }();
   if (regs != cudaSuccess) return regs;
-  cudaError_t e = set_smem_once<kern>(Smem<HD>::kTotal);
+  cudaError_t e = set_smem_once<kern>(Smem<HD, DUP>::kTotal);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(kKv8Ctas), dim3(kThreads), Smem<HD>::kTotal, st, mQ, a,
+  return launch_pdl(kern, dim3(kKv8Ctas), dim3(kThreads), Smem<HD, DUP>::kTotal, st, mQ, a,
                     1.4426950408889634f / sqrtf((float)HD));
 }
 
