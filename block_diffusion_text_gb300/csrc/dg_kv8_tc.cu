@@ -10,13 +10,12 @@
 //    tokens' keys enter as the bf16 they are, so a score is the fp32 sum of exact
 //    products, whatever else is in its row, its block or behind its mask.  (Queries
 //    and new keys as two E4M3 terms each, against the codes as they lie, spared the
-//    expansion: 117 us where this takes 128.  But they took 2^-18 of the largest element
+//    expansion: 117 us where this takes 124.  But they took 2^-18 of the largest element
 //    of the row, or of 64 tokens, from every other: one padded token's key could
 //    cost the others all their bits.)
 //  - P V of cached tiles runs in f16: p' is rounded to f16 (2^-11), once, where
 //    bf16 would need two terms.  New tokens' values keep their exponent range:
-//    bf16 products, p' split into two bf16 (2^-17), the second over the other half
-//    of the scores' columns.
+//    bf16 products, p' split into two bf16 (2^-17), both over the 32 keys' own scores.
 //  - Value scales never touch the codes: 2^ve joins the exponent of the probability
 //    (the running maximum is that of s + ve), whose share of the row sum is taken
 //    back.
@@ -31,17 +30,17 @@
 //                for shorter code); P over S in TMEM
 //   warps 16-19  keys: codes to bf16, new rows copied
 //
-// Measured: a canvas of 256 rows over 131072 rows of 8 heads 128 us (the two
-// products at the measured bf16 rate: 72), 1.07 PFLOP/s; a key tile takes some 3900
+// Measured: a canvas of 256 rows over 131072 rows of 8 heads 124 us (the two
+// products at the measured bf16 rate: 72), 1.11 PFLOP/s; a key tile takes some 3700
 // cycles, 2048 of them MMAs.  A row tile's chain (scores ready, two passes of
-// softmax 2100 to 2400 cycles, P V and the next S 1500 to 1800) bounds it, lengthened
-// by what the expansion takes of the issue slots and of shared memory (MMA
-// operands, expanded tiles and loads: some 2500 cycles a tile): with the keys' tiles
-// written but neither loaded nor expanded it runs 113 us, with loads that hit 120.
-// So the codes come through registers: rings of code tiles in shared memory, filled
-// by TMA, took 161 us (both) and 143 (one), slots filled by cp.async 132, expansion
-// of half a tile at a time 131, prefetches into L2 132 to 137, eight warps to each
-// tile 142, four in all 162.
+// softmax 2100 to 2400 cycles, P V and the next S 1500) bounds it, lengthened by
+// what the expansion takes of the issue slots, of shared memory (MMA operands,
+// codes and expanded tiles: some 2500 cycles a tile) and of the instruction
+// cache, where what the warps run at a time has to fit: with the expansion unrolled,
+// and the loop over the probabilities choosing between cached and new tiles, it ran
+// 128 us, calls of many short units a third longer.  Tried and slower: rings of code
+// tiles filled by TMA, 161 us (with half tiles) and 143 (for keys or values alone),
+// prefetches into L2 132 to 137, eight warps to each tile 142, four in all 162.
 // Tried and slower while the codes entered the MMA as they lie (117 us then): two
 // threads a row (24 warps of 80 registers, 123 us; 20 of 96, 168 us), the
 // scores read once block by block (123 to 129), the probabilities made on the old
@@ -50,7 +49,7 @@
 // the softmax no longer waits, but an MMA of 64 columns takes as long as one of
 // 128 and the MMA warps have twice the turns), MMA warps without turns (143).
 // Head dim 64 has half the MMAs and the same softmax: 256 rows over 32768 rows of
-// 8 heads 37 us (the warp-MMA kernel 91.7).
+// 8 heads 35 us (the warp-MMA kernel 92.7).
 #include <cfloat>
 
 #include "dg_kv8.cuh"
@@ -69,13 +68,13 @@ constexpr int kNS = 2;                     // slots of expanded keys, and of val
 constexpr float kHeadroom = 8.0f;          // p' of a row's maximum is 2^8 ..
 constexpr float kLazy = 6.0f;              // .. to 2^14: O is rescaled when the maximum grew by more than 2^6
 
-template <int HD, bool DUP>
+template <int HD>
 struct Smem {
   static constexpr int kBox = kTK * 128;             // 64 16-bit columns of a tile
   static constexpr int kTile = HD / 64 * kBox;       // a tile of 128 rows in 16 bits
   static constexpr int oK = 2 * kTile;               // behind the queries of both row tiles
   static constexpr int oV = oK + kNS * kTile;
-  static constexpr int kCode = DUP ? kTK * HD : 0;   // codes on their way: a tile of keys, one of values
+  static constexpr int kCode = kTK * HD;             // codes on their way: a tile of keys, one of values
   static constexpr int oC = oV + kNS * kTile;
   static constexpr int oBar = oC + 2 * kCode;
   static constexpr int oMl = oBar + 512;             // float2 [2 row tiles][128]: maximum and sum
@@ -186,17 +185,15 @@ DG_DEV void expand_values(const uint4& w, uint4 (&h)[2]) {
 
 // The part of four warps: the tiles of all of the CTA's pieces, keys or values, to
 // the MMA's buffer of kNS slots.  A thread takes 16-byte chunks of codes and has the
-// next tile's on their way while it expands this one's: in registers, or (DUP) in
-// slots of its own in shared memory.  Up to 128 rows the MMAs and the softmax of a
-// tile are half as many, and the expansion bounds the call: it has to be a loop
-// whose code stays in the instruction cache (64 rows over 131072 rows of 8 heads 97 us
-// unrolled, 87 rolled; 375 ragged sequences of up to 2000 rows, 4 heads of 24 rows, 296
-// and 207), which registers do not allow.  With 256 rows shared memory is the
-// scarcer (128 us in registers, 132 in slots, 256 rows over 131072).
-template <int HD, bool DUP, bool KEYS>
+// next tile's on their way while it expands this one's, in slots of its own in shared
+// memory.  The loop is rolled: alone a key tile takes 528 cycles unrolled, but
+// beside the softmax's code no instruction cache held it, and it took 2700 (375
+// ragged sequences of up to 2000 rows, 4 heads of 24 rows: 296 us, with codes in
+// registers, as unrolled loops allow; 207 rolled).
+template <int HD, bool KEYS>
 DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, int w0, int w1, uint8_t* buf, uint64_t* full,
                          uint64_t* empty, uint8_t* slots, volatile int* abort) {
-  using Smem = Smem<HD, DUP>;
+  using Smem = Smem<HD>;
   constexpr int IT = HD / 16, RS = 128 / IT;  // chunks of a row, and of a thread, whose rows are RS apart
   static_assert(RS % 8 == 0, "one swizzle a thread");
   // A row's chunk c of 16 elements is chunks 2 c and 2 c + 1 of its 16-bit row in box
@@ -216,12 +213,10 @@ DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, 
     const size_t bh = (size_t)p.b * a.Hkv + p.hk;
     const uint8_t *src = codes + (bh * a.cap + (size_t)p.t0 * kTK + r0) * HD + c * 16, *Ke = a.Ke + bh * a.nblk;
     int left = p.len - p.t0 * kTK - r0, blk = p.t0 * 2, ke0 = 0, ke1 = 0;
-    uint4 x[DUP ? 1 : IT];
     // chunk `it` of the tile at src on its way; what lies behind the sequence is not read
     auto load = [&](int it) {
       const bool there = it * RS < left;
-      if constexpr (DUP) cp_async16(slots + it * 2048, there ? src + it * RS * HD : codes, there);
-      else x[it] = there ? load16(src + it * RS * HD) : make_uint4(0, 0, 0, 0);
+      cp_async16(slots + it * 2048, there ? src + it * RS * HD : codes, there);
     };
     auto scales = [&]() {
       ke0 = Ke[blk];
@@ -231,7 +226,7 @@ DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, 
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
       if (cached > 0) load(it);
-      if (DUP) cp_async_commit();  // a group for each chunk
+      cp_async_commit();  // a group for each chunk
     }
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
@@ -249,30 +244,19 @@ DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, 
         if (KEYS && more) scales();
         src += kTK * HD;
         left -= kTK;
-        auto expand = [&](int it, const uint4& y) {  // the first half of the chunks are the tile's first block
-          uint4 h[2];
-          if (KEYS) expand_keys(y, it < IT / 2 ? f0 : f1, h);
-          else expand_values(y, h);
-          store(it, h);
-        };
-        if constexpr (DUP) {
-          cp_async_wait<IT - 1>();
-          x[0] = *reinterpret_cast<const uint4*>(slots);
+        cp_async_wait<IT - 1>();
+        uint4 next = *reinterpret_cast<const uint4*>(slots);
 #pragma unroll 1
-          for (int it = 0; it < IT; ++it) {
-            const uint4 y = x[0];
-            cp_async_wait<IT - 2>();
-            x[0] = *reinterpret_cast<const uint4*>(slots + (it + 1 < IT ? it + 1 : 0) * 2048);
-            expand(it, y);
-            if (more) load(it);  // the chunk's slot again
-            cp_async_commit();
-          }
-        } else {
-#pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            expand(it, x[it]);
-            if (more) load(it);
-          }
+        for (int it = 0; it < IT; ++it) {  // the first half of the chunks are the tile's first block
+          const uint4 x = next;
+          cp_async_wait<IT - 2>();
+          next = *reinterpret_cast<const uint4*>(slots + (it + 1 < IT ? it + 1 : 0) * 2048);
+          uint4 h[2];
+          if (KEYS) expand_keys(x, it < IT / 2 ? f0 : f1, h);
+          else expand_values(x, h);
+          store(it, h);
+          if (more) load(it);  // the chunk's slot again: its values have been used
+          cp_async_commit();
         }
       } else {
         // new rows as they are, zeros behind the last; the values' magnitudes are looked at
@@ -306,7 +290,7 @@ DG_DEV void expand_tiles(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, 
 template <int HD, bool DUP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, Kv8AttnArgs a, float scale_log2) {
-  using Smem = Smem<HD, DUP>;
+  using Smem = Smem<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // uniform over the CTA: return before any barrier
     if (threadIdx.x == 0) atomicExch(a.status, kStatusTimeout);
@@ -475,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    expand_tiles<HD, DUP, false>(a, plan, from, w0, w1, smem + Smem::oV, vfull, vempty, smem + Smem::oC + Smem::kCode, abort);
+    expand_tiles<HD, false>(a, plan, from, w0, w1, smem + Smem::oV, vfull, vempty, smem + Smem::oC + Smem::kCode, abort);
   } else if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    expand_tiles<HD, DUP, true>(a, plan, from, w0, w1, smem + Smem::oK, kfull, kempty, smem + Smem::oC, abort);
+    expand_tiles<HD, true>(a, plan, from, w0, w1, smem + Smem::oK, kfull, kempty, smem + Smem::oC, abort);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int t = (warp - 8) / 4, q4 = warp & 3;
@@ -529,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int lim = (fresh ? a.C : p.len) - key0;  // columns of the tile that this row sees
         ve_top = max(ve_top, lim > kKv8Block ? max(ex[0], ex[1]) : ex[0]);
         if (fresh && a.causal) lim = min(lim, qi - key0 + 1);
-        // Two passes over the scores, 64 columns (one block's scales) at a
+        // Two passes over the scores, NC columns (of one block's scales) at a
         // time: kept in registers between them they would need twice the
         // registers and unrolled code that no instruction cache holds.
         auto load = [&](int q, float (&s)[NC]) {
@@ -587,49 +571,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float mm = m_run == -INFINITY ? 0.f : m_run - kHeadroom;
+        const uint64_t c2 = f2_pack(scale_log2, scale_log2);
+        auto ready = [&](int half) {  // this half of the tile's P is in TMEM
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pready[2 * t + half]);
+        };
+        // apart, so that the loop of the cached tiles is short
+        if (!fresh) {
 #pragma unroll 1
-        for (int q = 0; q < kTK / NC; ++q) {  // half as many columns of P each, or of both its terms over its own scores
-          float s[NC];
-          load(q, s);
-          const int ve = NC * q < kKv8Block ? ex[0] : ex[1];
-          const float off = (float)ve - mm;
-          const uint64_t c2 = f2_pack(scale_log2, scale_log2), off2 = f2_pack(off, off);
-          uint64_t rs[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+          for (int q = 0; q < kTK / NC; ++q) {  // half as many columns of P each
+            float s[NC];
+            load(q, s);
+            const int ve = NC * q < kKv8Block ? ex[0] : ex[1];
+            const float off = (float)ve - mm;
+            const uint64_t off2 = f2_pack(off, off);
+            uint64_t rs[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-          for (int h = 0; h < NC / 32; ++h) {
-            uint32_t hw[16];
+            for (int h = 0; h < NC / 32; ++h) {
+              uint32_t hw[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float t0, t1;
+                f2_unpack(f2_fma(f2_pack(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), c2, off2), t0, t1);
+                const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+                rs[e & 1] = f2_add(rs[e & 1], f2_pack(p0, p1));
+                hw[e] = pack_f16(p0, p1);
+              }
+              tmem_st16(tS + NC / 2 * q + 16 * h, hw);
+            }
+            if (NC == 64 || (q & 1)) ready(NC * q / kKv8Block);
+            float x0, x1;
+            f2_unpack(f2_add(rs[0], rs[1]), x0, x1);
+            l_run = fmaf(x0 + x1, pow2i(-ve), l_run);
+          }
+        } else {
+          const uint64_t off2 = f2_pack(-mm, -mm);
+#pragma unroll 1
+          for (int q = 0; q < kTK / 32; ++q) {  // both terms of P over its own scores
+            float s[32];
+            tmem_ld32(tS + 32 * q, s);
+            uint64_t rs[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+            uint32_t hi[16], lo[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float &p0 = s[32 * h + 2 * e], &p1 = s[32 * h + 2 * e + 1];
-              f2_unpack(f2_fma(f2_pack(p0, p1), c2, off2), p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
+              float t0, t1;
+              f2_unpack(f2_fma(f2_pack(s[2 * e], s[2 * e + 1]), c2, off2), t0, t1);
+              const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
               rs[e & 1] = f2_add(rs[e & 1], f2_pack(p0, p1));
+              hi[e] = pack_bf16(p0, p1);
+              lo[e] = pack_bf16(p0 - __uint_as_float(hi[e] << 16), p1 - __uint_as_float(hi[e] & 0xffff0000u));
             }
-            if (!fresh) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) hw[e] = pack_f16(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]);
-              tmem_st16(tS + NC / 2 * q + 16 * h, hw);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) hw[e] = pack_bf16(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]);
-              tmem_st16(tS + NC * q + 32 * h, hw);
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                hw[e] = pack_bf16(s[32 * h + 2 * e] - __uint_as_float(hw[e] << 16),
-                                  s[32 * h + 2 * e + 1] - __uint_as_float(hw[e] & 0xffff0000u));
-              tmem_st16(tS + NC * q + 32 * h + 16, hw);
-            }
+            tmem_st16(tS + 32 * q, hi);
+            tmem_st16(tS + 32 * q + 16, lo);
+            if (q & 1) ready(q >> 1);
+            float x0, x1;
+            f2_unpack(f2_add(rs[0], rs[1]), x0, x1);
+            l_run += x0 + x1;
           }
-          if (NC == 64 || (q & 1)) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pready[2 * t + NC * q / kKv8Block]);
-          }
-          float x0, x1;
-          f2_unpack(f2_add(rs[0], rs[1]), x0, x1);
-          l_run = fmaf(x0 + x1, pow2i(-ve), l_run);
         }
       }
       if (!ok || (n > 0 && !(ok = wait(&pvdone[t], np & 1, status, abort)))) break;
@@ -721,9 +721,9 @@ static cudaError_t run_tc(const Kv8AttnArgs& a, cudaStream_t st) {
     return e == cudaSuccess && fa.numRegs < kLaunchRegs ? cudaErrorLaunchOutOfResources : e;
   }();
   if (regs != cudaSuccess) return regs;
-  cudaError_t e = set_smem_once<kern>(Smem<HD, DUP>::kTotal);
+  cudaError_t e = set_smem_once<kern>(Smem<HD>::kTotal);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(kKv8Ctas), dim3(kThreads), Smem<HD, DUP>::kTotal, st, mQ, a,
+  return launch_pdl(kern, dim3(kKv8Ctas), dim3(kThreads), Smem<HD>::kTotal, st, mQ, a,
                     1.4426950408889634f / sqrtf((float)HD));
 }
 
