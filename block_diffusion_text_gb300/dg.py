@@ -546,14 +546,6 @@ class Kv8Cache:
             n = self._ws_bytes[(C, Hq)] = z.value
         return n
 
-    def _workspace(self, n, st, stream):
-        """The workspace of the stream with handle st, of n bytes at least; called with _kv8_lock held."""
-        t = _kv8_workspaces.get((self._index, st))
-        if t is None or t.numel() < n:
-            with torch.cuda.stream(stream):  # memory of the launching stream
-                t = _kv8_workspaces[self._index, st] = torch.empty(n, dtype=torch.uint8, device=self.device)
-        return t
-
     def _attention_shapes(self, q):
         """(C, Hq, shape of k and v, shape of the output, bytes of workspace) of queries shaped like q."""
         if q.dim() != 4 or q.shape[0] != self.B or q.shape[3] != self.hd:
@@ -654,7 +646,12 @@ def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = Non
     elif wn:
         if not _capturing(stream):
             with _kv8_lock:
-                wp = cache._workspace(wn, st, stream).data_ptr()
+                t = _kv8_workspaces.get((cache._index, st))
+                if t is None or t.numel() < wn:
+                    with torch.cuda.stream(stream):  # memory of the launching stream
+                        t = torch.empty(wn, dtype=torch.uint8, device=cache.device)
+                    _kv8_workspaces[cache._index, st] = t
+                wp = t.data_ptr()
                 rc = cache._lib.dg_kv8_attention(cache._ref, qp, kp, vp, op, C, Hq, flag, wp, wn, st)
             if rc:
                 raise DgError(rc, "dg_kv8_attention")
@@ -673,7 +670,7 @@ def kv8_attention(cache: Kv8Cache, q: torch.Tensor, k: torch.Tensor | None = Non
 def _capturing(stream):
     """Whether the stream (None: the current one) is being captured into a graph."""
     if stream is None:
-        return torch.cuda.is_current_stream_capturing()
+        return torch._C._cuda_isCurrentStreamCapturing()
     with torch.cuda.stream(stream):
         return torch.cuda.is_current_stream_capturing()
 
@@ -681,7 +678,8 @@ def _capturing(stream):
 def kv8_release_workspaces(device=None) -> None:
     """Let go of the workspaces that kv8_attention keeps for the streams of `device` (default: of every device).
 
-    Their memory goes back to PyTorch's allocator in the order of each stream; the next call takes a new one."""
+    Their memory goes back to PyTorch's allocator in the order of each stream; the next call takes a new one.  To be
+    called before a stream that PyTorch does not own is destroyed: another may come to have its handle."""
     index = None if device is None else torch.device(device).index
     if device is not None and index is None:
         index = torch.cuda.current_device()
