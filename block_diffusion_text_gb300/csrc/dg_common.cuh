@@ -45,7 +45,9 @@ DG_DEV uint64_t globaltimer() {
 // cluster synchronisation), which reads nothing the kernel before wrote, so
 // that the prologue of a GEMM launched early overlaps the short kernel
 // before it.  No kernel that holds TMEM triggers early, so such a prologue
-// never waits on TMEM held by a kernel still running.
+// never waits on TMEM held by a kernel still running; but for the 8-bit cache's
+// attention, whose dependent is always its own merge, which uses none and does
+// not trigger.
 DG_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 DG_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

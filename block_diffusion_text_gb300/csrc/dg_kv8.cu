@@ -242,18 +242,21 @@ Kv8Ws kv8_ws(const dg_kv8_cache* c, int C, int Hq) {
   const int tiles = cdiv(c->cap, kKv8Block) + cdiv(C, kKv8Block);
   // The tensor-core kernel takes more than 16 rows, but for calls that the warps
   // finish in one launch and one wave with a few tiles each (new tokens' tiles
-  // take a warp twice as long): 64 query rows to a head, 4000 rows, 8 heads 13.0 us
-  // against 15.7; 256 rows, 1500 rows, 2 heads 12.0 against 14.5; with more tiles
-  // to a warp it turns: 64 rows, 8000 rows, 16 heads 32.4 against 25.7, 256 rows,
-  // 2000 rows, 4 heads 15.7 against 15.4 (head dim 128; with 64 it turns nearby: 128
-  // rows, 6000 rows, 4 heads 13.9 and 13.9).  Head dim 32, half a row of a swizzled
-  // tile and no workload's but the smallest, stays with the warps.
+  // take a warp twice as long): 64 query rows to a head, 4000 rows, 8 heads 14.1 us
+  // against 14.4; 256 rows, 1500 rows, 2 heads 12.3 against 14.6; with more tiles
+  // to a warp it turns: 64 rows, 8000 rows, 16 heads 27.1 against 25.3, 256 rows,
+  // 2000 rows, 4 heads 19.9 against 16.0 (head dim 128; with 64, 128 rows, 6000 rows,
+  // 4 heads 15.7 and 13.3).  Head dim 32, half a row of a swizzled tile and no
+  // workload's but the smallest, stays with the warps.  All of this goes by the
+  // capacity: the lengths are the device's.
   const int rows = kv8_mma_rows(c->hd, R), warps = kv8_mma_warps(c->hd, rows);
   const int64_t all = (int64_t)c->B * c->Hkv * ((R + rows - 1) / rows);
   const int cluster = kv8_cluster(all, tiles, warps);
   // With more units than SMs the tensor-core kernel, which begins and ends a CTA's
-  // units one after another, loses on short ones: 500 heads of 64 rows over up to 250
-  // rows 62 us against 47, over up to 1000 80 against 187 (24 rows, 500 rows: 59, 33).
+  // units one after another, loses on short ones: 400 heads of 24 rows over up to 500
+  // rows 41.1 us against 34.6, over up to 1000 49.5 against 87.0; of 64 rows, 8 tokens of
+  // 8 heads, over up to 250 rows 44.7 against 40.7, over up to 500 47.7 against 52.2.
+  // (Of 64 tokens it turns earlier, 250 rows 45.5 against 51.9: still the warps'.)
   const bool few = all <= kKv8Ctas ? tiles <= (C <= kKv8Block ? 4 : 1) * cluster * warps
                                    : C <= kKv8Block && tiles * ((R + rows - 1) / rows) < 32;
   w.tc = c->hd >= 64 && R > 16 && !few;

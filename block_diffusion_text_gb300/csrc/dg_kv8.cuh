@@ -101,8 +101,8 @@ DG_DEV Kv8Plan kv8_plan(const Kv8AttnArgs& a) {
 // The piece that begins at w in a share that ends at w1 (w < w1 <= the total; every
 // lane of the calling warp gets the answer).  from: where the search begins, a
 // sequence and the cost before it; zeros at first, then what the last call left
-// there (375 sequences, 4 heads of 24 rows over up to 2000 rows: 298 us without
-// it, 235 with).
+// there (375 sequences, 4 heads of 24 rows over up to 2000 rows: 275 us without
+// it, 207 with).
 DG_DEV Kv8Piece kv8_piece(const Kv8AttnArgs& a, const Kv8Plan& plan, int2& from, int w, int w1) {
   const int lane = threadIdx.x & 31;
   int base = from.y;

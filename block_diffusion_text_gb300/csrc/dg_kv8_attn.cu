@@ -24,13 +24,13 @@
 //    p' = 2^(s + e - m), so that P' V sums codes, with m the running maximum of
 //    s + e; the row sum takes p' 2^-e back.
 //  - Queries enter as f16 scaled by a power of two per row (exact for elements
-//    down to 2^-27 of the row's largest).  p' is rounded to f16 (2^-12 of its
+//    down to 2^-27 of the row's largest).  p' is rounded to f16 (2^-11 of its
 //    value; 2^-33 of the largest at least, with the headroom of 2^8 below):
 //    an eighth of the rounding of the bf16 output.
 // New tokens' bf16 keys and values keep their exponent range: bf16 MMAs, P
 // split into two bf16 parts (2^-17).
-// Measured: one token of 4 sequences over 131072 rows of 8 heads 166 us (6.5 TB/s,
-// 95 % of the measured copy rate), of 32 sequences of 0 to 8192 rows 48 us (5.2
+// Measured: one token of 4 sequences over 131072 rows of 8 heads 166 to 169 us (6.4
+// TB/s, 94 % of the measured copy rate), of 32 sequences of 0 to 8192 rows 48 us (5.2
 // TB/s; the start and the merge take some 8 us), of one over 2048 rows 7.4 us (11
 // with one CTA to a kv head; a launch takes 2).
 #include <cfloat>
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(32 * W, 1)
   }
   __syncthreads();
   pdl_wait();
-  pdl_trigger();  // the merge waits for this kernel's completion all the same
+  pdl_trigger();  // the next kernel (the merge, or with clusters any) waits for this one's completion all the same
 
   if (worker == 0) {
     for (int b = lane; b < a.B; b += 32)
@@ -887,9 +887,9 @@ template <int HD>
 static cudaError_t run_merge_rows(const Kv8AttnArgs& a, cudaStream_t st) {
   if (a.rows < 128) return run_merge<HD, kMergeSlices, 1>(a, st);
   // By the parts that a unit has (hd 128; 19 of them, a canvas over 131072 rows:
-  // 115.8 us, against 128.9 with a warp for all parts and 120.5 with two; 9, over
-  // 8192 rows: 32.6 with two, against 37.9 and 33.8 with four; 2, prompt pieces:
-  // 41.7 with one, against 45.6 with two).
+  // 124.1 us, against 140.1 with a warp for all parts and 126.5 with two; 9, over
+  // 8192 rows: 29.9 with two, against 37.9 with one and 32.0 with four; 2, prompt
+  // pieces: 40.7 with one, against 44.3 with two).
   const int64_t units = (int64_t)a.B * a.units;
   if (a.subs == 2) return a.workers >= 8 * units ? run_merge<HD, 8, 1, 2>(a, st) : run_merge<HD, 2, 2, 2>(a, st);
   if (a.workers >= 16 * units) return run_merge<HD, 4, 2>(a, st);
