@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(32 * W, 1)
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int x = top < 128 ? 0 : max((int)(top >> 7) - 127 - 13, -100);
+      const int x = top == 0 ? 0 : max((int)(top >> 7) - 127 - 13, -127);
       const float f = pow2i(-x);
 #pragma unroll
       for (int j = 0; j < KS; ++j) {

@@ -114,7 +114,7 @@ def test_tokens_that_get_no_weight(C, hd, cap, power):
     check(c, q, k, v, False)
 
 
-@pytest.mark.parametrize("power", [-40, -90, -100, 50])
+@pytest.mark.parametrize("power", [-40, -90, -100, -120, 50])
 @pytest.mark.parametrize("C,hd,cap", SIZES, ids=ids)
 def test_small_queries_over_large_keys(C, hd, cap, power):
     """Queries of 2^power over keys 2^-power times larger: ordinary scores."""
