@@ -457,14 +457,15 @@ DG_API dg_status dg_kv8_read(const dg_kv8_cache* cache, int32_t row0, int32_t n,
  * overlap an input; what lies behind len is never used.  Values go up to 448 * 2^40
  * in magnitude (V_exp bytes up to 167), scores up to 2^23 (beyond, fp32 does not
  * hold their units): where larger ones are met, scores as the largest of a run of
- * keys, the status word gets DG_ERR_VALUE, and the output is not to be used.  Scores are fp32 sums of exact products (of a query row's
- * elements what is above 2^-27 of its largest at least).  Cached keys'
- * probabilities enter the product as f16 on the scale of the row's largest, block
- * by block: a contribution below 2^-33 of the largest is lost; new tokens' as pairs
- * of bf16.  Bounds as dg_attention_noalloc: C <= 1024, B * C <= 2^20,
- * B * Hq <= 65535.  ws: dg_kv8_attention_workspace bytes (0 for a short cache: ws
- * may be NULL then), 256-byte aligned, contents of no matter; calls (and graphs)
- * that may overlap on the GPU need one each.                                  */
+ * keys, the status word gets DG_ERR_VALUE, and the output is not to be used.
+ * Scores are fp32 sums of exact products (of a query row's elements what is above
+ * 2^-27 of its largest at least).  Cached keys' probabilities enter the product as
+ * f16 on the scale of the row's largest, block by block: a contribution below 2^-33
+ * of the largest is lost; new tokens' as pairs of bf16.  Bounds as
+ * dg_attention_noalloc: C <= 1024, B * C <= 2^20, B * Hq <= 65535.
+ * ws: dg_kv8_attention_workspace bytes (0 for a short cache: ws may be NULL
+ * then), 256-byte aligned, contents of no matter; calls (and graphs) that may
+ * overlap on the GPU need one each.                                           */
 DG_API dg_status dg_kv8_attention_workspace(const dg_kv8_cache* cache, int32_t C, int32_t Hq, size_t* bytes);
 DG_API dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, const void* k, const void* v, void* o,
                                   int32_t C, int32_t Hq, int32_t causal, void* ws, size_t ws_bytes, void* stream);
