@@ -1,0 +1,336 @@
+// Matrices of 4-bit weights with a scale per group, times a few rows.
+//
+//   y[m][n] = coef alpha[m] sum_k x[m][k] s[n][k / group] (c[n][k] - 8) + resid[m][n]
+//
+// The weights' bytes bound it (2 M flops a weight, 32 rows at most), so the
+// codes lie in memory as the tensor cores take them: a tile of 16 rows by 64
+// columns is 512 consecutive bytes, 16 for each lane of the warp that
+// multiplies it.  Lane 4 g + t holds rows g and g + 8 at columns 32 p + 8 t + i,
+// p = 0, 1, i = 0..7.  Word j of its four is the A operand of one m16n8k16
+// product: of the columns i = 4 (j % 2) + 0..3 of half p = j / 2, nibble r + 2 u
+// (+ 4) is row g + 8 r at column i = 4 (j % 2) + 2 u (+ 1).  The order of a
+// product's inner index is free as long as both operands follow it, so x is read
+// in 16-byte pieces of a row.  Scales: bf16, [tile][group][8][2], rows g and g + 8
+// side by side.
+#include <cfloat>
+#include <climits>
+
+#include "dg_common.cuh"
+#include "dg_internal.h"
+
+namespace dg {
+namespace {
+
+constexpr int kW4Rows = 16, kW4Cols = 64;  // a tile
+constexpr int kW4MaxM = 32;
+
+// Column of the tile at which the lane's word j begins.
+DG_DEV int w4_col(int j, int t) { return 32 * (j / 2) + 8 * t + 4 * (j % 2); }
+
+DG_DEV uint32_t f32_to_bf16_bits(float f) { return pack_bf16(f, 0.f) & 0xffffu; }
+
+// ---------------------------------------------------- quantise, pack, read --
+struct W4StoreArgs {
+  const void* W;       // bf16 [N][ld], or codes uint8 [N][ld]
+  const uint16_t* s;   // codes' scales [N][K / group]
+  uint32_t* codes;
+  uint32_t* scales;    // a pair of bf16 each
+  int* status;
+  int N, K, group, ld;
+};
+
+// A warp writes the tiles of one group of columns (two tiles where the group is
+// 128): rows rt * 16 .., bound by reading the matrix once.
+constexpr int kStoreWarps = 8;
+
+template <bool kQuantize>
+__global__ void __launch_bounds__(kStoreWarps * 32) w4_store_kernel(W4StoreArgs a) {
+  pdl_wait();
+  const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int KB = a.K / kW4Cols, span = a.group > kW4Cols ? 2 : 1, spans = KB / span;
+  const int64_t id = (int64_t)blockIdx.x * kStoreWarps + threadIdx.x / 32;
+  const int rt = (int)(id / spans), kb0 = (int)(id % spans) * span;
+  if (rt >= (a.N + kW4Rows - 1) / kW4Rows) return;
+  for (int half = 0; half < (a.group < kW4Cols ? 2 : 1); ++half) {
+    // the group's columns: both halves of its tiles, or with groups of 32 one half
+    const int p0 = a.group < kW4Cols ? half : 0, p1 = a.group < kW4Cols ? half + 1 : 2;
+    uint32_t sc[2];
+    if (kQuantize) {
+      const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.W);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int n = rt * kW4Rows + g + 8 * r;
+        float top = 0.f;
+        bool bad = false;
+        if (n < a.N)
+          for (int kb = kb0; kb < kb0 + span; ++kb)
+            for (int p = p0; p < p1; ++p)
+              for (int i = 0; i < 8; ++i) {
+                const float v = fabsf(__bfloat162float(W[(size_t)n * a.ld + kb * kW4Cols + 32 * p + 8 * t + i]));
+                if (v <= FLT_MAX) top = fmaxf(top, v);
+                else bad = true;
+              }
+        if (bad) atomicExch(a.status, kStatusValue);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        sc[r] = f32_to_bf16_bits(top / 7.0f);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int n = rt * kW4Rows + g + 8 * r;
+        sc[r] = n < a.N ? a.s[(size_t)n * (a.K / a.group) + (kb0 * kW4Cols + 32 * p0) / a.group] : 0u;
+      }
+    }
+    if (t == 0)
+      a.scales[((size_t)rt * (a.K / a.group) + (kb0 * kW4Cols + 32 * p0) / a.group) * 8 + g] = sc[0] | (sc[1] << 16);
+    for (int kb = kb0; kb < kb0 + span; ++kb)
+      for (int j = 2 * p0; j < 2 * p1; ++j) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int n = rt * kW4Rows + g + 8 * r;
+          const float s = __uint_as_float(sc[r] << 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t c = 8;
+            if (n < a.N) {
+              const size_t at = (size_t)n * a.ld + kb * kW4Cols + w4_col(j, t) + i;
+              if (kQuantize) {
+                const float v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.W)[at]);
+                // a group of zeros has scale 0; NaN is stored as zero
+                const float q = s > 0.f && v == v ? fminf(fmaxf(rintf(v / s), -7.f), 7.f) : 0.f;
+                c = (uint32_t)((int)q + 8);
+              } else {
+                c = static_cast<const uint8_t*>(a.W)[at] & 15u;
+              }
+            }
+            word |= c << (4 * (r + 2 * (i / 2) + 4 * (i % 2)));
+          }
+        }
+        a.codes[(((size_t)rt * KB + kb) * 32 + lane) * 4 + j] = word;
+      }
+  }
+}
+
+struct W4ReadArgs {
+  const uint32_t* codes;
+  const uint32_t* scales;
+  float* out;
+  int N, K, group;
+  int64_t ld;
+};
+
+__global__ void __launch_bounds__(256) w4_read_kernel(W4ReadArgs a) {
+  pdl_wait();
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;  // one word: two rows, four columns
+  const int KB = a.K / kW4Cols;
+  const int j = (int)(id % 4), lane = (int)(id / 4 % 32), g = lane / 4, t = lane % 4;
+  const int64_t tile = id / 128;
+  const int rt = (int)(tile / KB), kb = (int)(tile % KB);
+  if (rt >= (a.N + kW4Rows - 1) / kW4Rows) return;
+  const uint32_t word = a.codes[id];
+  const int k = kb * kW4Cols + w4_col(j, t);
+  const uint32_t sc = a.scales[((size_t)rt * (a.K / a.group) + k / a.group) * 8 + g];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int n = rt * kW4Rows + g + 8 * r;
+    if (n >= a.N) continue;
+    const float s = __uint_as_float(r ? sc & 0xffff0000u : sc << 16);
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = s * (float)((int)((word >> (4 * (r + 2 * (i / 2) + 4 * (i % 2)))) & 15u) - 8);
+    float* dst = a.out + (size_t)n * a.ld + k;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = v[i];
+  }
+}
+
+// ---------------------------------------------------------------- products --
+struct W4Args {
+  const uint4* codes;
+  const uint32_t* scales;
+  const __nv_bfloat16* x;
+  const float* alpha;          // [M] or null
+  const __nv_bfloat16* resid;  // [M][ldr] or null
+  void* y;                     // [M][ldy]
+  float coef;
+  int N, K, group, M;
+  int64_t ldx, ldr, ldy;
+  int f32;
+  int wk;                      // warps that share a row tile's columns
+};
+
+constexpr int kW4Warps = 8;
+
+// Four codes' pairs as bf16: the nibble in the low bits of 128 (the mantissa's
+// unit there is 1), less 136.  Both are exact.
+DG_DEV uint32_t w4_pair(uint32_t word, int i) {
+  const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __nv_bfloat162(136.f, 136.f));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kW4Warps * 32) w4_matvec_kernel(W4Args a) {
+  pdl_wait();
+  __shared__ float part[kW4Warps][NT * 4][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int KB = a.K / kW4Cols, tiles = (a.N + kW4Rows - 1) / kW4Rows;
+  const int per = kW4Warps / a.wk;            // row tiles of a CTA at a time
+  const int sub = warp % a.wk, rt = blockIdx.x * per + warp / a.wk;
+  const int gpt = a.group < kW4Cols ? 2 : 1;  // groups in a tile
+  float y[NT][4] = {};
+  if (rt < tiles) {
+    const uint4* c = a.codes + (size_t)rt * KB * 32 + lane;
+    const uint32_t* sp = a.scales + (size_t)rt * (a.K / a.group) * 8 + g;
+    for (int kb = sub; kb < KB; kb += a.wk) {
+      const uint4 cw = __ldcs(c + (size_t)kb * 32);
+      uint32_t s[2];
+      s[0] = __ldg(sp + (size_t)(kb * kW4Cols / a.group) * 8);
+      s[1] = gpt == 2 ? __ldg(sp + (size_t)(kb * 2 + 1) * 8) : s[0];
+      uint4 b[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          b[n][p] = make_uint4(0, 0, 0, 0);
+          if (8 * n + g < a.M)
+            b[n][p] = __ldg(reinterpret_cast<const uint4*>(a.x + (8 * n + g) * a.ldx + kb * kW4Cols + 32 * p + 8 * t));
+        }
+      const uint32_t words[4] = {cw.x, cw.y, cw.z, cw.w};
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        float acc[NT][4] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t A[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) A[i] = w4_pair(words[2 * p + h], i);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma_bf16_16816(acc[n], A, h ? b[n][p].z : b[n][p].x, h ? b[n][p].w : b[n][p].y);
+        }
+        const float s0 = __uint_as_float(s[p] << 16), s1 = __uint_as_float(s[p] & 0xffff0000u);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          y[n][0] += s0 * acc[n][0];
+          y[n][1] += s0 * acc[n][1];
+          y[n][2] += s1 * acc[n][2];
+          y[n][3] += s1 * acc[n][3];
+        }
+      }
+    }
+  }
+  if (a.wk > 1) {  // the warps' sums in order
+    if (sub > 0) {
+#pragma unroll
+      for (int i = 0; i < NT * 4; ++i) part[warp][i][lane] = y[i / 4][i % 4];
+    }
+    __syncthreads();
+    if (sub > 0) return;
+    for (int w = 1; w < a.wk; ++w) {
+#pragma unroll
+      for (int i = 0; i < NT * 4; ++i) y[i / 4][i % 4] += part[warp + w][i][lane];
+    }
+  }
+  if (rt >= tiles) return;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = 8 * n + 2 * t + i % 2, col = rt * kW4Rows + g + 8 * (i / 2);
+      if (m >= a.M || col >= a.N) continue;
+      float v = y[n][i] * (a.alpha ? a.coef * a.alpha[m] : a.coef);
+      if (a.resid) v += __bfloat162float(a.resid[m * a.ldr + col]);
+      if (a.f32) static_cast<float*>(a.y)[m * a.ldy + col] = v;
+      else static_cast<__nv_bfloat16*>(a.y)[m * a.ldy + col] = __float2bfloat16_rn(v);
+    }
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+dg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DG_OK : DG_ERR_CUDA; }
+
+dg_status check_w4_sizes(int32_t N, int32_t K, int32_t group) {
+  if (N <= 0 || K <= 0 || group <= 0) return DG_ERR_ARG;
+  if (group != 32 && group != 64 && group != 128) return DG_ERR_SHAPE;
+  if (K % kW4Cols || K % group || K > 65536 || N > (1 << 24)) return DG_ERR_SHAPE;
+  return DG_OK;
+}
+
+dg_status check_w4(const dg_w4* w) {
+  if (!w || !w->codes || !w->scales) return DG_ERR_ARG;
+  if (!aligned16(w->codes) || !aligned16(w->scales)) return DG_ERR_ARG;
+  return check_w4_sizes(w->N, w->K, w->group);
+}
+
+template <bool kQuantize>
+dg_status store(const dg_w4* w, const void* W, int32_t ld, const void* s, int32_t* status, void* stream) {
+  W4StoreArgs a{W, static_cast<const uint16_t*>(s), static_cast<uint32_t*>(w->codes), static_cast<uint32_t*>(w->scales),
+                status, w->N, w->K, w->group, ld};
+  const int64_t spans = (int64_t)cdiv(w->N, kW4Rows) * (w->K / (w->group > kW4Cols ? w->group : kW4Cols));
+  const int64_t ctas = (spans + kStoreWarps - 1) / kStoreWarps;
+  if (ctas > INT_MAX) return DG_ERR_SHAPE;
+  return from_cuda(launch_pdl(w4_store_kernel<kQuantize>, dim3((unsigned)ctas), dim3(kStoreWarps * 32), 0,
+                              reinterpret_cast<cudaStream_t>(stream), a));
+}
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" dg_status dg_w4_bytes(int32_t N, int32_t K, int32_t group, size_t* codes, size_t* scales) {
+  if (!codes || !scales) return DG_ERR_ARG;
+  dg_status e = check_w4_sizes(N, K, group);
+  if (e) return e;
+  const size_t rows = (size_t)cdiv(N, kW4Rows) * kW4Rows;
+  *codes = rows * K / 2;
+  *scales = rows * (K / group) * 2;
+  return DG_OK;
+}
+
+extern "C" dg_status dg_w4_quantize(const dg_w4* w, const void* W, int32_t ldw, int32_t* status, void* stream) {
+  dg_status e = check_w4(w);
+  if (e) return e;
+  if (!W || !status || ldw < w->K || reinterpret_cast<uintptr_t>(W) % 2 || reinterpret_cast<uintptr_t>(status) % 4)
+    return DG_ERR_ARG;
+  return store<true>(w, W, ldw, nullptr, status, stream);
+}
+
+extern "C" dg_status dg_w4_pack(const dg_w4* w, const void* codes, const void* scales, void* stream) {
+  dg_status e = check_w4(w);
+  if (e) return e;
+  if (!codes || !scales || reinterpret_cast<uintptr_t>(scales) % 2) return DG_ERR_ARG;
+  return store<false>(w, codes, w->K, scales, nullptr, stream);
+}
+
+extern "C" dg_status dg_w4_read(const dg_w4* w, float* out, int32_t ldo, void* stream) {
+  dg_status e = check_w4(w);
+  if (e) return e;
+  if (!out || ldo < w->K || reinterpret_cast<uintptr_t>(out) % 4) return DG_ERR_ARG;
+  W4ReadArgs a{static_cast<const uint32_t*>(w->codes), static_cast<const uint32_t*>(w->scales), out, w->N, w->K, w->group, ldo};
+  const int64_t words = (int64_t)cdiv(w->N, kW4Rows) * (w->K / kW4Cols) * 128;
+  if (words / 256 > INT_MAX - 1) return DG_ERR_SHAPE;
+  return from_cuda(launch_pdl(w4_read_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0,
+                              reinterpret_cast<cudaStream_t>(stream), a));
+}
+
+extern "C" dg_status dg_w4_matvec(const dg_w4* w, const void* x, int32_t ldx, int32_t M, const float* alpha, float coef,
+                                  const void* resid, int32_t ldr, void* y, int32_t ldy, int32_t y_f32, void* stream) {
+  dg_status e = check_w4(w);
+  if (e) return e;
+  if (!x || !y || M <= 0 || ldx < w->K || ldy < w->N || (resid && ldr < w->N)) return DG_ERR_ARG;
+  if (!aligned16(x) || ldx % 8 || reinterpret_cast<uintptr_t>(y) % (y_f32 ? 4 : 2) ||
+      reinterpret_cast<uintptr_t>(resid) % 2 || reinterpret_cast<uintptr_t>(alpha) % 4)
+    return DG_ERR_ARG;
+  if (M > kW4MaxM) return DG_ERR_SHAPE;
+  W4Args a{static_cast<const uint4*>(w->codes), static_cast<const uint32_t*>(w->scales),
+           static_cast<const __nv_bfloat16*>(x), alpha, static_cast<const __nv_bfloat16*>(resid), y, coef, w->N, w->K,
+           w->group, M, ldx, ldr, ldy, y_f32 != 0, 8};
+  const dim3 grid(cdiv(w->N, kW4Rows * (kW4Warps / a.wk))), block(kW4Warps * 32);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (M <= 8) return from_cuda(launch_pdl(w4_matvec_kernel<1>, grid, block, 0, st, a));
+  if (M <= 16) return from_cuda(launch_pdl(w4_matvec_kernel<2>, grid, block, 0, st, a));
+  return from_cuda(launch_pdl(w4_matvec_kernel<4>, grid, block, 0, st, a));
+}

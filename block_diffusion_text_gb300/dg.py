@@ -29,7 +29,7 @@ EXPORTS = ("dg_status_string", "dg_workspace_size", "dg_read_status", "dg_tau", 
            "dg_attention_noalloc", "dg_attention_noalloc_status", "dg_debug_wait_timeout",
            "dg_canvas_init_masked", "dg_denoise_step_masked", "dg_denoise_canvas_masked", "dg_prefill",
            "dg_quantize_rows_e4m3", "dg_kv8_append", "dg_kv8_read", "dg_kv8_attention_workspace",
-           "dg_kv8_attention")
+           "dg_kv8_attention", "dg_w4_bytes", "dg_w4_quantize", "dg_w4_pack", "dg_w4_read", "dg_w4_matvec")
 
 
 class DgError(RuntimeError):
@@ -72,6 +72,11 @@ class dg_step_out(ct.Structure):
 class dg_kv8_cache(ct.Structure):
     _fields_ = [(n, ct.c_void_p) for n in ("K", "V", "K_exp", "V_exp", "len", "status")] + [
         (n, ct.c_int32) for n in ("B", "Hkv", "cap", "hd")]
+
+
+class dg_w4(ct.Structure):
+    _fields_ = [("codes", ct.c_void_p), ("scales", ct.c_void_p), ("N", ct.c_int32), ("K", ct.c_int32),
+                ("group", ct.c_int32)]
 
 
 # Kernel slots of one step (dg_step_out.events), in launch order.
@@ -142,6 +147,12 @@ def load():
             L.dg_kv8_attention.argtypes = [ct.c_void_p, ct.c_void_p, ct.c_void_p, ct.c_void_p, ct.c_void_p,
                                            ct.c_int32, ct.c_int32, ct.c_int32, ct.c_void_p, ct.c_size_t,
                                            ct.c_void_p]
+            i32, vp = ct.c_int32, ct.c_void_p
+            L.dg_w4_bytes.argtypes = [i32, i32, i32, ct.POINTER(ct.c_size_t), ct.POINTER(ct.c_size_t)]
+            L.dg_w4_quantize.argtypes = [vp, vp, i32, vp, vp]
+            L.dg_w4_pack.argtypes = [vp, vp, vp, vp]
+            L.dg_w4_read.argtypes = [vp, vp, i32, vp]
+            L.dg_w4_matvec.argtypes = [vp, vp, i32, i32, vp, ct.c_float, vp, i32, vp, i32, i32, vp]
             _lib = L
     return _lib
 
@@ -686,3 +697,139 @@ def kv8_release_workspaces(device=None) -> None:
     with _kv8_lock:
         for key in [k for k in _kv8_workspaces if index is None or k[0] == index]:
             del _kv8_workspaces[key]
+
+
+# ------------------------------------------------- operators of a decoded token
+def _on(t, dtype, what, index):
+    """Checks a tensor's type and device (a CUDA device's index); returns the tensor."""
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{what}: {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
+    return t
+
+
+def _index_of(t, what):
+    """The index of the tensor's CUDA device."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{what}: a CUDA tensor, got one on {t.device}")
+    return i
+
+
+def _raw_stream(index, stream):
+    """The raw stream of a launch: the library launches on the current device, so that must be the tensors'."""
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError(f"the tensors lie on cuda:{index}, the current device is another")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _empty(shape, dtype, index, stream):
+    """Memory of the launching stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=index)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=index)
+
+
+def _rows_of(t, dtype, width, what, index):
+    """(rows, pitch) of a 2-D tensor whose rows of `width` elements are contiguous."""
+    _on(t, dtype, what, index)
+    if t.dim() != 2 or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: [rows, {width}] with contiguous rows, got {tuple(t.shape)}, strides {t.stride()}")
+    rows = t.shape[0]
+    return rows, (t.stride(0) if rows > 1 else max(width, t.stride(0)))
+
+
+class W4Matrix:
+    """A matrix [N, K] of 4-bit weights with a bf16 scale for each row and `group` columns (dg_w4), laid out for
+    w4_matvec.  Made by w4_quantize or W4Matrix.from_codes; read() gives the weights back."""
+
+    def __init__(self, N, K, group, device="cuda"):
+        self._lib = load()
+        nc, ns = ct.c_size_t(), ct.c_size_t()
+        _check(self._lib.dg_w4_bytes(N, K, group, ct.byref(nc), ct.byref(ns)), "dg_w4_bytes")
+        self.codes = torch.empty(nc.value, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(ns.value // 2, dtype=torch.bfloat16, device=device)
+        self.N, self.K, self.group = N, K, group
+        self._index = _index_of(self.codes, "device")
+        self.s = dg_w4(self.codes.data_ptr(), self.scales.data_ptr(), N, K, group)
+        self._ref = ct.byref(self.s)
+
+    @classmethod
+    def from_codes(cls, codes, scales, stream=None):
+        """Lay out codes (uint8 [N, K], 0 to 15, weight s * (c - 8)) and scales (bf16 [N, K / group]) (dg_w4_pack)."""
+        i = _index_of(codes, "codes")
+        _on(codes, torch.uint8, "codes", i)
+        _on(scales, torch.bfloat16, "scales", i)
+        _need(codes.dim() == 2 and scales.dim() == 2 and scales.shape[0] == codes.shape[0] and scales.shape[1] > 0
+              and codes.shape[1] % scales.shape[1] == 0, "codes [N, K], scales [N, K / group]")
+        _need(codes.is_contiguous() and scales.is_contiguous(), "codes and scales: contiguous")
+        st = _raw_stream(i, stream)
+        with torch.cuda.stream(stream):
+            w = cls(codes.shape[0], codes.shape[1], codes.shape[1] // scales.shape[1], codes.device)
+        _check(w._lib.dg_w4_pack(w._ref, codes.data_ptr(), scales.data_ptr(), st), "dg_w4_pack")
+        return w
+
+    def read(self, stream=None) -> torch.Tensor:
+        """The weights as float32 [N, K], exactly (dg_w4_read)."""
+        st = _raw_stream(self._index, stream)
+        out = _empty((self.N, self.K), torch.float32, self._index, stream)
+        _check(self._lib.dg_w4_read(self._ref, out.data_ptr(), self.K, st), "dg_w4_read")
+        return out
+
+
+def w4_quantize(W: torch.Tensor, group: int = 64, status: torch.Tensor | None = None, stream=None) -> W4Matrix:
+    """4-bit weights of a bf16 matrix [N, K] (dg_w4_quantize).
+
+    status: optional int32 [1] device word, set to DG_ERR_VALUE where W holds infinities or NaN; without it the
+    call waits for the stream and raises DgError in that case."""
+    i = _index_of(W, "W")
+    _on(W, torch.bfloat16, "W", i)
+    _need(W.dim() == 2, "W: [N, K]")
+    _, ld = _rows_of(W, torch.bfloat16, W.shape[1], "W", i)
+    st = _raw_stream(i, stream)
+    with torch.cuda.stream(stream):
+        w = W4Matrix(W.shape[0], W.shape[1], group, W.device)
+        word = torch.zeros(1, dtype=torch.int32, device=W.device) if status is None else status
+    _need(_on(word, torch.int32, "status", i).shape == (1,), "status: int32 [1]")
+    _check(w._lib.dg_w4_quantize(w._ref, W.data_ptr(), ld, word.data_ptr(), st), "dg_w4_quantize")
+    if status is None:
+        code = ct.c_int32()
+        _check(w._lib.dg_read_status(word.data_ptr(), ct.byref(code), st), "dg_read_status")
+        _check(code.value, "dg_w4_quantize: the matrix")
+    return w
+
+
+def w4_matvec(w: W4Matrix, x: torch.Tensor, alpha: torch.Tensor | None = None, coef: float = 1.0,
+              resid: torch.Tensor | None = None, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """coef * alpha[m] * (x w^T) + resid for 1 to 32 rows x (bf16 [M, K]) (dg_w4_matvec); bf16 or float32 [M, N].
+
+    alpha: optional float32 [M]; resid: optional bf16 [M, N], which may also be `out`."""
+    i = w._index
+    M, ldx = _rows_of(x, torch.bfloat16, w.K, "x", i)
+    ap = rp = None
+    ldr = 0
+    if alpha is not None:
+        if _on(alpha, torch.float32, "alpha", i).shape != (M,) or not alpha.is_contiguous():
+            raise ValueError(f"alpha: contiguous float32 [{M}]")
+        ap = alpha.data_ptr()
+    if resid is not None:
+        rr, ldr = _rows_of(resid, torch.bfloat16, w.N, "resid", i)
+        _need(rr == M, f"resid: [{M}, {w.N}]")
+        rp = resid.data_ptr()
+    st = _raw_stream(i, stream)
+    if out is None:
+        out, ldy = _empty((M, w.N), dtype, i, stream), w.N
+    else:
+        rr, ldy = _rows_of(out, out.dtype, w.N, "out", i)
+        _need(rr == M, f"out: [{M}, {w.N}]")
+    if out.dtype is torch.float32:
+        f32 = 1
+    elif out.dtype is torch.bfloat16:
+        f32 = 0
+    else:
+        raise ValueError(f"the product is bfloat16 or float32, not {out.dtype}")
+    rc = w._lib.dg_w4_matvec(w._ref, x.data_ptr(), ldx, M, ap, coef, rp, ldr, out.data_ptr(), ldy, f32, st)
+    if rc:
+        raise DgError(rc, "dg_w4_matvec")
+    return out

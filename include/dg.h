@@ -470,6 +470,44 @@ DG_API dg_status dg_kv8_attention_workspace(const dg_kv8_cache* cache, int32_t C
 DG_API dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, const void* k, const void* v, void* o,
                                   int32_t C, int32_t Hq, int32_t causal, void* ws, size_t ws_bytes, void* stream);
 
+/* Products with 4-bit weights, for a few rows: the projections and the LM head of a
+ * decoded token, which the weights' bytes bound.  (The pages quote quantised
+ * deployments, [SURV] §11; they describe no format, this one is the library's own.)
+ *   a weight is s * (c - 8): a code c of 4 bits and a bf16 scale s for each row and
+ *   `group` (32, 64 or 128) consecutive columns
+ *   codes, scales   device, 16-byte aligned, of dg_w4_bytes bytes, in the layout that
+ *           the products read (tiles of 16 rows and 64 columns; the rows behind the
+ *           last one of the last tile are zeros): written by dg_w4_quantize or
+ *           dg_w4_pack, read back by dg_w4_read
+ *   N       rows (1 .. 2^24); K  columns, a multiple of 64 and of group, <= 65536   */
+typedef struct dg_w4 {
+  void *codes, *scales;
+  int32_t N, K, group;
+} dg_w4;
+
+DG_API dg_status dg_w4_bytes(int32_t N, int32_t K, int32_t group, size_t* codes, size_t* scales);
+
+/* Quantises a bf16 matrix W [N][ldw], ldw >= K: s = max |w| of the group / 7 rounded to
+ * bf16, c = 8 + (w / s rounded to nearest even, within +-7); a group whose s is zero
+ * has codes 8.  Infinities are stored as +-7 and NaN as 0 on the scale of the finite
+ * values, with DG_ERR_VALUE in *status (device word, zeroed by the caller).         */
+DG_API dg_status dg_w4_quantize(const dg_w4* w, const void* W, int32_t ldw, int32_t* status, void* stream);
+
+/* Lays out given codes (uint8 [N][K], one to a byte, the low four bits count) and
+ * scales (bf16 [N][K / group]).                                                  */
+DG_API dg_status dg_w4_pack(const dg_w4* w, const void* codes, const void* scales, void* stream);
+
+/* The weights as float32 [N][ldo], ldo >= K (exact).                              */
+DG_API dg_status dg_w4_read(const dg_w4* w, float* out, int32_t ldo, void* stream);
+
+/* y[m][n] = coef * alpha[m] * sum_k x[m][k] w[n][k] + resid[m][n] for M rows, 1 <= M
+ * <= 32.  x bf16 [M][ldx], 16-byte aligned, ldx a multiple of 8; alpha float32 [M] or
+ * NULL for ones; resid bf16 [M][ldr] or NULL; y [M][ldy], bf16, or float32 where
+ * y_f32 is set (the LM head's logits).  y may be resid itself (same pitch); it must not
+ * overlap anything else.  Products are exact, sums fp32, rounded once.             */
+DG_API dg_status dg_w4_matvec(const dg_w4* w, const void* x, int32_t ldx, int32_t M, const float* alpha, float coef,
+                              const void* resid, int32_t ldr, void* y, int32_t ldy, int32_t y_f32, void* stream);
+
 /* Diagnostics of the bounded device waits (not a step of the method): runs
  * one kernel whose mbarrier wait is never satisfied.  The wait gives up after
  * its limit (2 s), records DG_ERR_TIMEOUT in a library status word, and the
