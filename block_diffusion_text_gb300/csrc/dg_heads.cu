@@ -1,0 +1,149 @@
+// RMSNorm of the query and key heads with the position rotation, from the packed
+// projection of a token, [q heads | k heads | v heads], into the layouts that
+// attention and the cache's append take:
+//
+//   t = x g / sqrt(mean(x^2) + eps),  (a, b) -> (a cos - b sin, a sin + b cos)
+//
+// with a the first and b the second half of the head and the angle pos base^(-2 j / hd)
+// for pair j; v heads are moved.  Bound by memory: every value is read once and
+// written once.
+#include <climits>
+#include <cmath>
+
+#include "dg_common.cuh"
+#include "dg_internal.h"
+
+namespace dg {
+namespace {
+
+constexpr int kHeadThreads = 256;
+
+// theta_j / (2 pi) as a 64-bit binary fraction of a turn.  The integer product
+// with a position, modulo 2^64, is the angle in turns modulo one: no far position
+// loses bits (an angle is off by pos 2^-54 theta / 2 pi at most, as a double's
+// rounding of theta is).
+struct HeadTurns {
+  uint64_t t[64];
+};
+
+struct HeadArgs {
+  const __nv_bfloat16* x;        // [B][C][W], strides sb, st
+  const int* pos;                // [B]
+  const __nv_bfloat16 *qg, *kg;  // [hd] or null
+  __nv_bfloat16 *q, *k, *v;      // [B][H][C][hd]
+  int64_t sb, st;
+  int tokens;                    // B * C
+  int C, Hq, Hkv;
+  float eps;
+};
+
+// A thread holds eight pairs of one head: 16 bytes of its first half and 16 of
+// its second.  A CTA takes as many tokens as fill its threads (at least one);
+// the tokens' sines and cosines are worked out once, in shared memory, while the
+// heads' values are on their way.
+template <int HD>
+__global__ void __launch_bounds__(kHeadThreads) qk_norm_rope_kernel(HeadArgs a, HeadTurns turns, int per) {
+  pdl_wait();
+  constexpr int L = HD / 16;  // threads per head
+  extern __shared__ float2 cs[];  // [per][HD / 2]
+  const int H = a.Hq + 2 * a.Hkv;
+  const int tok0 = blockIdx.x * per;
+  const int here = min(per, a.tokens - tok0);
+  for (int i = threadIdx.x; i < here * (HD / 2); i += kHeadThreads) {
+    const int tok = tok0 + i / (HD / 2);
+    const uint64_t at = (uint64_t)((int64_t)a.pos[tok / a.C] + tok % a.C);
+    const int32_t turn = (int32_t)(uint32_t)((at * turns.t[i % (HD / 2)]) >> 32);  // signed: half a turn is 2^31
+    float sn, c;
+    sincospif((float)turn * 4.656612873077393e-10f, &sn, &c);  // 2^-31
+    cs[i] = make_float2(c, sn);
+  }
+  __syncthreads();
+  for (int it = threadIdx.x; it < here * H * L; it += kHeadThreads) {
+    const int l = it % L, head = it / L % H, ti = it / (L * H);
+    const int tok = tok0 + ti;
+    const int64_t b = tok / a.C, i = tok % a.C;
+    const uint4* src = reinterpret_cast<const uint4*>(a.x + b * a.sb + i * a.st + head * HD) + l;
+    const uint4 lo = __ldcs(src), hi = __ldcs(src + L);
+    const bool isq = head < a.Hq, isv = head >= a.Hq + a.Hkv;
+    const int hh = isq ? head : head - a.Hq - (isv ? a.Hkv : 0);
+    __nv_bfloat16* dst = isq ? a.q + ((b * a.Hq + hh) * a.C + i) * HD : (isv ? a.v : a.k) + ((b * a.Hkv + hh) * a.C + i) * HD;
+    uint4* d4 = reinterpret_cast<uint4*>(dst) + l;
+    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+    float x[8], y[8], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = __uint_as_float(j % 2 ? wl[j / 2] & 0xffff0000u : wl[j / 2] << 16);
+      y[j] = __uint_as_float(j % 2 ? wh[j / 2] & 0xffff0000u : wh[j / 2] << 16);
+      sum += x[j] * x[j] + y[j] * y[j];
+    }
+    // a head's lanes are neighbours and come together: the items are a multiple of L
+    const unsigned mask = ((1u << L) - 1) << (threadIdx.x % 32 / L * L);
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
+    if (isv) {
+      d4[0] = lo;
+      d4[L] = hi;
+      continue;
+    }
+    const float inv = 1.0f / sqrtf(sum * (1.0f / HD) + a.eps);
+    const __nv_bfloat16* gain = isq ? a.qg : a.kg;
+    uint32_t ol[4], oh[4];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      float u[2], w[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float p = x[j + e] * inv, r = y[j + e] * inv;
+        if (gain) {
+          p *= __bfloat162float(gain[8 * l + j + e]);
+          r *= __bfloat162float(gain[HD / 2 + 8 * l + j + e]);
+        }
+        const float2 c = cs[ti * (HD / 2) + 8 * l + j + e];
+        u[e] = p * c.x - r * c.y;
+        w[e] = p * c.y + r * c.x;
+      }
+      ol[j / 2] = pack_bf16(u[0], u[1]);
+      oh[j / 2] = pack_bf16(w[0], w[1]);
+    }
+    d4[0] = make_uint4(ol[0], ol[1], ol[2], ol[3]);
+    d4[L] = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+  }
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int64_t token_stride, const int32_t* pos,
+                                     const void* q_gain, const void* k_gain, void* q, void* k, void* v, int32_t B,
+                                     int32_t C, int32_t Hq, int32_t Hkv, int32_t hd, float rope_base, float rms_eps,
+                                     void* stream) {
+  if (!qkv || !pos || !q || !k || !v || B <= 0 || C <= 0 || Hq <= 0 || Hkv <= 0) return DG_ERR_ARG;
+  if (!(rope_base >= 1.f) || !std::isfinite(rope_base) || !(rms_eps >= 0.f)) return DG_ERR_ARG;
+  if (hd != 32 && hd != 64 && hd != 128) return DG_ERR_SHAPE;
+  if (Hq > 1024 || Hkv > 1024 || (int64_t)B * C > (1 << 26)) return DG_ERR_SHAPE;
+  const int64_t W = (int64_t)(Hq + 2 * Hkv) * hd;
+  if ((C > 1 && token_stride < W) || token_stride % 8 || batch_stride % 8 || (B > 1 && batch_stride < W)) return DG_ERR_ARG;
+  if (!aligned16(qkv) || !aligned16(q) || !aligned16(k) || !aligned16(v) || reinterpret_cast<uintptr_t>(pos) % 4 ||
+      reinterpret_cast<uintptr_t>(q_gain) % 2 || reinterpret_cast<uintptr_t>(k_gain) % 2)
+    return DG_ERR_ARG;
+  HeadTurns turns{};
+  for (int j = 0; j < hd / 2; ++j) {
+    turns.t[j] = (uint64_t)std::ldexp(std::pow((double)rope_base, -2.0 * j / hd) * 0.15915494309189535, 64);  // 1 / 2 pi
+  }
+  HeadArgs a{static_cast<const __nv_bfloat16*>(qkv), pos, static_cast<const __nv_bfloat16*>(q_gain),
+             static_cast<const __nv_bfloat16*>(k_gain), static_cast<__nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(k),
+             static_cast<__nv_bfloat16*>(v), batch_stride, token_stride, B * C, C, Hq, Hkv, rms_eps};
+  const int items = (Hq + 2 * Hkv) * (hd / 16);
+  const int per = items >= kHeadThreads ? 1 : kHeadThreads / items;
+  const dim3 grid(cdiv(a.tokens, per)), block(kHeadThreads);
+  const size_t smem = sizeof(float2) * per * (hd / 2);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = hd == 32   ? launch_pdl(qk_norm_rope_kernel<32>, grid, block, smem, st, a, turns, per)
+                  : hd == 64 ? launch_pdl(qk_norm_rope_kernel<64>, grid, block, smem, st, a, turns, per)
+                             : launch_pdl(qk_norm_rope_kernel<128>, grid, block, smem, st, a, turns, per);
+  return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}

@@ -29,7 +29,8 @@ EXPORTS = ("dg_status_string", "dg_workspace_size", "dg_read_status", "dg_tau", 
            "dg_attention_noalloc", "dg_attention_noalloc_status", "dg_debug_wait_timeout",
            "dg_canvas_init_masked", "dg_denoise_step_masked", "dg_denoise_canvas_masked", "dg_prefill",
            "dg_quantize_rows_e4m3", "dg_kv8_append", "dg_kv8_read", "dg_kv8_attention_workspace",
-           "dg_kv8_attention", "dg_w4_bytes", "dg_w4_quantize", "dg_w4_pack", "dg_w4_read", "dg_w4_matvec")
+           "dg_kv8_attention", "dg_w4_bytes", "dg_w4_quantize", "dg_w4_pack", "dg_w4_read", "dg_w4_matvec",
+           "dg_qk_norm_rope")
 
 
 class DgError(RuntimeError):
@@ -153,6 +154,7 @@ def load():
             L.dg_w4_pack.argtypes = [vp, vp, vp, vp]
             L.dg_w4_read.argtypes = [vp, vp, i32, vp]
             L.dg_w4_matvec.argtypes = [vp, vp, i32, i32, vp, ct.c_float, vp, i32, vp, i32, i32, vp]
+            L.dg_qk_norm_rope.argtypes = [vp, ct.c_int64, ct.c_int64] + [vp] * 6 + [i32] * 5 + [ct.c_float] * 2 + [vp]
             _lib = L
     return _lib
 
@@ -833,3 +835,45 @@ def w4_matvec(w: W4Matrix, x: torch.Tensor, alpha: torch.Tensor | None = None, c
     if rc:
         raise DgError(rc, "dg_w4_matvec")
     return out
+
+
+def qk_norm_rope(qkv: torch.Tensor, pos: torch.Tensor, Hq: int, Hkv: int, q_gain: torch.Tensor | None = None,
+                 k_gain: torch.Tensor | None = None, rms_eps: float = 1e-6, rope_base: float = 10000.0, out=None,
+                 stream=None):
+    """RMSNorm and rotation of the q and k heads of packed projections (dg_qk_norm_rope): (q, k, v).
+
+    qkv: bf16 [B, C, (Hq + 2 Hkv) hd]; pos: int32 [B], position of each sequence's first token (e.g. cache.len);
+    q_gain, k_gain: optional bf16 [hd].  q [B, Hq, C, hd], k, v [B, Hkv, C, hd], as kv8_append and kv8_attention take
+    them; out: optional (q, k, v) to write."""
+    i = _index_of(qkv, "qkv")
+    H = Hq + 2 * Hkv
+    if qkv.dtype is not torch.bfloat16 or qkv.dim() != 3 or Hq < 1 or Hkv < 1 or qkv.shape[2] % H \
+            or (qkv.shape[2] > 1 and qkv.stride(2) != 1):
+        raise ValueError(f"qkv: bf16 [B, C, {H} hd] with contiguous tokens, got {qkv.dtype} {tuple(qkv.shape)}")
+    B, C, W = qkv.shape
+    hd = W // H
+    sb, sc, _ = qkv.stride()
+    if _on(pos, torch.int32, "pos", i).shape != (B,) or not pos.is_contiguous():
+        raise ValueError(f"pos: contiguous int32 [{B}]")
+    gains = []
+    for t, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+        if t is not None and (_on(t, torch.bfloat16, what, i).shape != (hd,) or not t.is_contiguous()):
+            raise ValueError(f"{what}: contiguous bf16 [{hd}]")
+        gains.append(None if t is None else t.data_ptr())
+    st = _raw_stream(i, stream)
+    sq, sk = (B, Hq, C, hd), (B, Hkv, C, hd)
+    if out is None:
+        q, k, v = (_empty(s, torch.bfloat16, i, stream) for s in (sq, sk, sk))
+    else:
+        q, k, v = out
+        for t, s, what in ((q, sq, "q"), (k, sk, "k"), (v, sk, "v")):
+            if _on(t, torch.bfloat16, what, i).shape != s or not t.is_contiguous():
+                raise ValueError(f"{what}: contiguous bf16 {list(s)}")
+    if B * C == 0:
+        return q, k, v
+    rc = load().dg_qk_norm_rope(qkv.data_ptr(), sb if B > 1 else C * max(sc, W), sc if C > 1 else W, pos.data_ptr(),
+                                gains[0], gains[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), B, C, Hq, Hkv, hd,
+                                rope_base, rms_eps, st)
+    if rc:
+        raise DgError(rc, "dg_qk_norm_rope")
+    return q, k, v

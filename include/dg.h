@@ -508,6 +508,26 @@ DG_API dg_status dg_w4_read(const dg_w4* w, float* out, int32_t ldo, void* strea
 DG_API dg_status dg_w4_matvec(const dg_w4* w, const void* x, int32_t ldx, int32_t M, const float* alpha, float coef,
                               const void* resid, int32_t ldr, void* y, int32_t ldy, int32_t y_f32, void* stream);
 
+/* Norms of the query and key heads with the position rotation, from the packed
+ * projections of the tokens (e.g. of dg_w4_matvec with Wq, Wk, Wv stacked) into the
+ * layouts that dg_kv8_append and the attention calls take.
+ *   qkv  bf16 [B][C][(Hq + 2 Hkv) hd], a token's q heads, k heads, v heads; elements
+ *        from one sequence and token to the next: batch_stride, token_stride (multiples
+ *        of 8); 16-byte aligned
+ *   pos  int32 [B] device: token i of sequence b stands at position pos[b] + i (a
+ *        cache's len: a captured graph follows it)
+ *   q [B][Hq][C][hd], k, v [B][Hkv][C][hd]: bf16, written, 16-byte aligned; they must
+ *        not overlap each other or an input
+ * Each q and k head: t = x * gain / sqrt(mean(x^2) + rms_eps) (q_gain, k_gain bf16 [hd]
+ * or NULL for ones), then pair (t_j, t_{j + hd/2}) turned by the angle
+ * pos * rope_base^(-2 j / hd), in fp32, rounded once; v heads are moved.  Angles are
+ * exact to some 2^-24 of a turn at any position.  hd 32, 64 or 128; Hq, Hkv 1..1024;
+ * B * C <= 2^26; rope_base >= 1; squares are summed in fp32 (values up to 2^60).     */
+DG_API dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int64_t token_stride, const int32_t* pos,
+                                 const void* q_gain, const void* k_gain, void* q, void* k, void* v, int32_t B,
+                                 int32_t C, int32_t Hq, int32_t Hkv, int32_t hd, float rope_base, float rms_eps,
+                                 void* stream);
+
 /* Diagnostics of the bounded device waits (not a step of the method): runs
  * one kernel whose mbarrier wait is never satisfied.  The wait gives up after
  * its limit (2 s), records DG_ERR_TIMEOUT in a library status word, and the
