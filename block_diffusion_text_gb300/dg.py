@@ -30,7 +30,7 @@ EXPORTS = ("dg_status_string", "dg_workspace_size", "dg_read_status", "dg_tau", 
            "dg_canvas_init_masked", "dg_denoise_step_masked", "dg_denoise_canvas_masked", "dg_prefill",
            "dg_quantize_rows_e4m3", "dg_kv8_append", "dg_kv8_read", "dg_kv8_attention_workspace",
            "dg_kv8_attention", "dg_w4_bytes", "dg_w4_quantize", "dg_w4_pack", "dg_w4_read", "dg_w4_matvec",
-           "dg_qk_norm_rope")
+           "dg_qk_norm_rope", "dg_moe_tokens_workspace", "dg_moe_tokens")
 
 
 class DgError(RuntimeError):
@@ -155,6 +155,8 @@ def load():
             L.dg_w4_read.argtypes = [vp, vp, i32, vp]
             L.dg_w4_matvec.argtypes = [vp, vp, i32, i32, vp, ct.c_float, vp, i32, vp, i32, i32, vp]
             L.dg_qk_norm_rope.argtypes = [vp, ct.c_int64, ct.c_int64] + [vp] * 6 + [i32] * 5 + [ct.c_float] * 2 + [vp]
+            L.dg_moe_tokens_workspace.argtypes = [vp, i32, ct.POINTER(ct.c_size_t)]
+            L.dg_moe_tokens.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp, ct.c_size_t, vp]
             _lib = L
     return _lib
 
@@ -877,3 +879,113 @@ def qk_norm_rope(qkv: torch.Tensor, pos: torch.Tensor, Hq: int, Hkv: int, q_gain
     if rc:
         raise DgError(rc, "dg_qk_norm_rope")
     return q, k, v
+
+
+# Workspaces of moe_tokens, one for each (device, stream), zeroed when made; the lock as _kv8_lock's.
+_moe_workspaces = {}
+_moe_lock = threading.Lock()
+
+
+class MoeFfn:
+    """The mixture-of-experts block of one layer for moe_tokens: router Wr [n_exp, d], expert matrices We1
+    [n_exp + 1, Fe, d] and We2 [n_exp + 1, d, Fe] (index n_exp: the shared expert), bf16, contiguous."""
+
+    def __init__(self, Wr, We1, We2, top_k, rms_eps=1e-6):
+        i = self._index = _index_of(Wr, "Wr")
+        _need(Wr.dim() == 2 and We1.dim() == 3, "Wr [n_exp, d], We1 [n_exp + 1, Fe, d], We2 [n_exp + 1, d, Fe]")
+        n, d = Wr.shape
+        Fe = We1.shape[1]
+        for t, shape, what in ((Wr, (n, d), "Wr"), (We1, (n + 1, Fe, d), "We1"), (We2, (n + 1, d, Fe), "We2")):
+            _need(_on(t, torch.bfloat16, what, i).shape == shape and t.is_contiguous(), f"{what}: contiguous bf16 {list(shape)}")
+        self.Wr, self.We1, self.We2 = Wr, We1, We2
+        self.d, self.n_exp, self.top_k, self.Fe, self.rms_eps = d, n, int(top_k), Fe, float(rms_eps)
+        self.s = dg_model()
+        self.s.dims = dg_dims(d=d, n_exp=n, top_k=self.top_k, Fe=Fe, rms_eps=self.rms_eps, L=1)
+        self.s.Wr, self.s.We1, self.s.We2 = Wr.data_ptr(), We1.data_ptr(), We2.data_ptr()
+        self._ref = ct.byref(self.s)
+        self._lib = load()
+        self._ws_bytes = {}
+        self.workspace_bytes(1)
+
+    @classmethod
+    def of(cls, model: Model, layer: int = 0):
+        """The block of a layer of a Model with experts."""
+        _need(model.dims.n_exp > 0 and 0 <= layer < model.dims.L, "a layer of a model with experts")
+        w = [model.w[k] if model.dims.L == 1 else model.w[k][layer] for k in ("Wr", "We1", "We2")]
+        return cls(*w, top_k=model.dims.top_k, rms_eps=model.dims.rms_eps)
+
+    def workspace_bytes(self, M: int) -> int:
+        """Bytes of workspace of moe_tokens with M tokens."""
+        n = self._ws_bytes.get(M)
+        if n is None:
+            z = ct.c_size_t()
+            _check(self._lib.dg_moe_tokens_workspace(self._ref, M, ct.byref(z)), "dg_moe_tokens_workspace")
+            n = self._ws_bytes[M] = z.value
+        return n
+
+
+def moe_tokens(ffn: MoeFfn, h: torch.Tensor, out: torch.Tensor | None = None, routing=None, ws: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """The whole mixture-of-experts block, residual included, for 1 to 32 tokens h (bf16 [M, d]) (dg_moe_tokens).
+
+    out: optional bf16 [M, d], which may be h.  routing: optional (int32 [M, top_k], float32 [M, top_k]) to receive
+    the experts and their gates.  ws: optional uint8 workspace of ffn.workspace_bytes(M) bytes, zeroed before its
+    first use and not shared by calls that may overlap; by default the calls of a stream share one, which is kept
+    (moe_tokens_status, moe_release_workspaces), and a captured call takes one from the graph's pool."""
+    i = ffn._index
+    M = h.shape[0] if h.dim() == 2 else 0
+    for t, what in ((h, "h"), (out, "out")):
+        if t is not None and (_on(t, torch.bfloat16, what, i).shape != (M, ffn.d) or not t.is_contiguous()):
+            raise ValueError(f"{what}: contiguous bf16 [M, {ffn.d}], got {tuple(t.shape)}")
+    ip = gp = None
+    if routing is not None:
+        for t, dt in zip(routing, (torch.int32, torch.float32)):
+            if _on(t, dt, "routing", i).shape != (M, ffn.top_k) or not t.is_contiguous():
+                raise ValueError(f"routing: contiguous int32 and float32 [{M}, {ffn.top_k}]")
+        ip, gp = routing[0].data_ptr(), routing[1].data_ptr()
+    st = _raw_stream(i, stream)
+    wn = ffn.workspace_bytes(M)
+    if out is None:
+        out = _empty((M, ffn.d), torch.bfloat16, i, stream)
+    call, hp, op = ffn._lib.dg_moe_tokens, h.data_ptr(), out.data_ptr()
+    if ws is not None:
+        _need(ws.get_device() == i and ws.is_contiguous(), "ws: contiguous, on the block's device")
+        rc = call(ffn._ref, 0, hp, op, M, ip, gp, ws.data_ptr(), ws.numel() * ws.element_size(), st)
+    elif _capturing(stream):
+        # from the graph's own pool, zeroed by the graph, held until the launch is enqueued
+        with torch.cuda.stream(stream):
+            ws = torch.zeros(wn, dtype=torch.uint8, device=i)
+        rc = call(ffn._ref, 0, hp, op, M, ip, gp, ws.data_ptr(), wn, st)
+    else:
+        with _moe_lock:
+            t = _moe_workspaces.get((i, st))
+            if t is None or t.numel() < wn:
+                with torch.cuda.stream(stream):
+                    t = torch.zeros(wn, dtype=torch.uint8, device=i)
+                _moe_workspaces[i, st] = t
+            rc = call(ffn._ref, 0, hp, op, M, ip, gp, t.data_ptr(), wn, st)
+    if rc:
+        raise DgError(rc, "dg_moe_tokens")
+    return out
+
+
+def moe_tokens_status(device=None, stream=None) -> int:
+    """The status word of the workspace that moe_tokens keeps for the stream (synchronises it): DG_OK, or what the
+    calls since it was made have met."""
+    i = torch.cuda.current_device() if device is None else torch.device(device).index
+    t = _moe_workspaces.get((i, _raw_stream(i, stream)))
+    if t is None:
+        return DG_OK
+    code = ct.c_int32()
+    _check(load().dg_read_status(t.data_ptr(), ct.byref(code), _raw_stream(i, stream)), "dg_read_status")
+    return code.value
+
+
+def moe_release_workspaces(device=None) -> None:
+    """Let go of the workspaces that moe_tokens keeps, as kv8_release_workspaces does of its own."""
+    index = None if device is None else torch.device(device).index
+    if device is not None and index is None:
+        index = torch.cuda.current_device()
+    with _moe_lock:
+        for key in [k for k in _moe_workspaces if index is None or k[0] == index]:
+            del _moe_workspaces[key]

@@ -528,6 +528,30 @@ DG_API dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int64_t 
                                  int32_t C, int32_t Hq, int32_t Hkv, int32_t hd, float rope_base, float rms_eps,
                                  void* stream);
 
+/* A layer's whole mixture-of-experts block ([SURV] §11, §13; the block that a step takes
+ * with n_exp > 0, dg_dims) for 1 to 32 tokens, in one launch: at these sizes the chosen
+ * experts' weights bound it, and each is read once.
+ *   model   of which dims.d, n_exp, top_k, Fe, rms_eps and L and the weights Wr, We1,
+ *           We2 are read (limits as dg_dims, d and Fe up to 16384; weights finite and
+ *           16-byte aligned); layer in [0, L)
+ *   h       bf16 [M][d]; out bf16 [M][d], written: h + sum_j g_j FFN_ej(x) +
+ *           FFN_shared(x); may be h itself; both 16-byte aligned
+ *   idx     int32 [M][top_k] the experts in rank order, gate float32 [M][top_k]: written;
+ *           either may be NULL
+ *   ws      dg_moe_tokens_workspace bytes, 256-byte aligned, zeroed before its first use
+ *           (and after DG_ERR_TIMEOUT); the first 4 bytes are the status word
+ *           (dg_read_status): DG_ERR_VALUE for router logits that are not finite (the
+ *           token's output is not to be used), DG_ERR_TIMEOUT.  Calls (and graphs) that
+ *           may overlap on the GPU need one each.
+ * x, the router's logits and the hidden values are not rounded to bf16 as a step rounds
+ * them: fp32 sums of exact products, hidden values good to 2^-17.  A token's sums run
+ * over the experts that any token of the call chose (zeros where it did not), so their
+ * last bits go with the other tokens.  The launch is cooperative: it begins when all SMs
+ * have room for it.                                                                */
+DG_API dg_status dg_moe_tokens_workspace(const dg_model* model, int32_t M, size_t* bytes);
+DG_API dg_status dg_moe_tokens(const dg_model* model, int32_t layer, const void* h, void* out, int32_t M, int32_t* idx,
+                               float* gate, void* ws, size_t ws_bytes, void* stream);
+
 /* Diagnostics of the bounded device waits (not a step of the method): runs
  * one kernel whose mbarrier wait is never satisfied.  The wait gives up after
  * its limit (2 s), records DG_ERR_TIMEOUT in a library status word, and the
