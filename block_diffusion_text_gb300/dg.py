@@ -30,7 +30,7 @@ EXPORTS = ("dg_status_string", "dg_workspace_size", "dg_read_status", "dg_tau", 
            "dg_canvas_init_masked", "dg_denoise_step_masked", "dg_denoise_canvas_masked", "dg_prefill",
            "dg_quantize_rows_e4m3", "dg_kv8_append", "dg_kv8_read", "dg_kv8_attention_workspace",
            "dg_kv8_attention", "dg_w4_bytes", "dg_w4_quantize", "dg_w4_pack", "dg_w4_read", "dg_w4_matvec",
-           "dg_qk_norm_rope", "dg_moe_tokens_workspace", "dg_moe_tokens")
+           "dg_qk_norm_rope", "dg_moe_tokens_workspace", "dg_moe_tokens", "dg_sample")
 
 
 class DgError(RuntimeError):
@@ -78,6 +78,11 @@ class dg_kv8_cache(ct.Structure):
 class dg_w4(ct.Structure):
     _fields_ = [("codes", ct.c_void_p), ("scales", ct.c_void_p), ("N", ct.c_int32), ("K", ct.c_int32),
                 ("group", ct.c_int32)]
+
+
+class dg_sampling(ct.Structure):
+    _fields_ = [(n, ct.c_void_p) for n in ("temperature", "top_p", "min_p", "top_k")] + [
+        (n, ct.c_float) for n in ("temperature_all", "top_p_all", "min_p_all")] + [("top_k_all", ct.c_int32)]
 
 
 # Kernel slots of one step (dg_step_out.events), in launch order.
@@ -157,6 +162,7 @@ def load():
             L.dg_qk_norm_rope.argtypes = [vp, ct.c_int64, ct.c_int64] + [vp] * 6 + [i32] * 5 + [ct.c_float] * 2 + [vp]
             L.dg_moe_tokens_workspace.argtypes = [vp, i32, ct.POINTER(ct.c_size_t)]
             L.dg_moe_tokens.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp, ct.c_size_t, vp]
+            L.dg_sample.argtypes = [vp, i32, ct.c_int64, i32, i32, vp, vp, vp, vp, vp, vp]
             _lib = L
     return _lib
 
@@ -989,3 +995,45 @@ def moe_release_workspaces(device=None) -> None:
     with _moe_lock:
         for key in [k for k in _moe_workspaces if index is None or k[0] == index]:
             del _moe_workspaces[key]
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, stream=None):
+    """A token for each row of logits (float32 or bf16 [R, V]) by the random numbers u (float32 [R], in [0, 1)), with
+    temperature, top-k, top-p and min-p (dg_sample): (token int32, logprob float32, kept int32), each [R].
+
+    The settings are numbers, or tensors [R] with one for each row (float32; top_k int32): 0 / 0 / 1 / 0 are greedy and
+    no cut.  A row that cannot be drawn from (NaN, +inf, no finite logit, a setting or u outside its range) gets token
+    -1.  out: optional (token, logprob, kept) to write."""
+    i = _index_of(logits, "logits")
+    dt = logits.dtype
+    if dt is not torch.float32 and dt is not torch.bfloat16:
+        raise ValueError(f"logits: float32 or bfloat16, got {dt}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits: [R, V], got {tuple(logits.shape)}")
+    R, ld = _rows_of(logits, dt, logits.shape[1], "logits", i)
+    V = logits.shape[1]
+    if _on(u, torch.float32, "u", i).shape != (R,) or not u.is_contiguous():
+        raise ValueError(f"u: contiguous float32 [{R}]")
+    how = dg_sampling()
+    for name, v, want in (("temperature", temperature, torch.float32), ("top_p", top_p, torch.float32),
+                          ("min_p", min_p, torch.float32), ("top_k", top_k, torch.int32)):
+        if isinstance(v, torch.Tensor):
+            if _on(v, want, name, i).shape != (R,) or not v.is_contiguous():
+                raise ValueError(f"{name}: contiguous {want} [{R}], or a number")
+            setattr(how, name, v.data_ptr())
+        else:
+            setattr(how, name + "_all", v)
+    st = _raw_stream(i, stream)
+    if out is None:
+        out = tuple(_empty((R,), t, i, stream) for t in (torch.int32, torch.float32, torch.int32))
+    else:
+        for t, want, what in zip(out, (torch.int32, torch.float32, torch.int32), ("token", "logprob", "kept")):
+            if _on(t, want, what, i).shape != (R,) or not t.is_contiguous():
+                raise ValueError(f"{what}: contiguous {want} [{R}]")
+    if R == 0:
+        return out
+    rc = load().dg_sample(logits.data_ptr(), 1 if dt is torch.bfloat16 else 0, ld, R, V, ct.byref(how), u.data_ptr(),
+                          out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), st)
+    if rc:
+        raise DgError(rc, "dg_sample")
+    return out

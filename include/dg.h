@@ -552,6 +552,40 @@ DG_API dg_status dg_moe_tokens_workspace(const dg_model* model, int32_t M, size_
 DG_API dg_status dg_moe_tokens(const dg_model* model, int32_t layer, const void* h, void* out, int32_t M, int32_t* idx,
                                float* gate, void* ws, size_t ws_bytes, void* stream);
 
+/* Tokens from logits, by given random numbers (the sampler of a decoded token, next to
+ * the denoising step's entropy-bounded one).  A row's tokens are ordered by value, the
+ * lower index first where two are equal, and weigh w = exp((l - max) / temperature).
+ * Kept is the leading run of that order that is left by, in turn,
+ *   top_k   the first top_k (0: all)
+ *   top_p   of those, the smallest run whose weights sum to top_p of theirs at least
+ *           (>= 1: all; one token at least)
+ *   min_p   of those, the ones with w >= min_p (0: all)
+ * and the token is the first by index at which the sum of the kept weights, in index
+ * order, passes u times their total.  temperature 0 (below 2^-64) or top_k 1: the
+ * lowest index of the largest value.
+ * Per row (device arrays [R], or NULL for the value `_all`): temperature >= 0, top_k >=
+ * 0, 0 <= top_p, 0 <= min_p <= 1.                                                  */
+typedef struct dg_sampling {
+  const float *temperature, *top_p, *min_p;
+  const int32_t* top_k;
+  float temperature_all, top_p_all, min_p_all;
+  int32_t top_k_all;
+} dg_sampling;
+
+/* One token for each of R rows.
+ *   logits   float32, or bf16 where bf16 is set, [R][ld], ld >= V; V <= 2^20.  -inf (a
+ *            banned token) is never kept
+ *   u        float32 [R], 0 <= u < 1
+ *   token    int32 [R]; logprob float32 [R] or NULL, ln of the token's share of the kept
+ *            weights; kept int32 [R] or NULL, the number of tokens kept: written
+ * A row with NaN or +inf, without any finite logit, or with a setting or u outside its
+ * range gets token -1, logprob NaN and kept 0.
+ * Weights are whole numbers of 30 bits and an exponent, down to 2^-42 of the largest
+ * (smaller ones count as kept, but are not drawn), and their sums exact: the same bits
+ * every time.                                                                      */
+DG_API dg_status dg_sample(const void* logits, int32_t bf16, int64_t ld, int32_t R, int32_t V, const dg_sampling* how,
+                           const float* u, int32_t* token, float* logprob, int32_t* kept, void* stream);
+
 /* Diagnostics of the bounded device waits (not a step of the method): runs
  * one kernel whose mbarrier wait is never satisfied.  The wait gives up after
  * its limit (2 s), records DG_ERR_TIMEOUT in a library status word, and the
