@@ -4,14 +4,15 @@
 //
 // The weights' bytes bound it (2 M flops a weight, 32 rows at most), so the
 // codes lie in memory as the tensor cores take them: a tile of 16 rows by 64
-// columns is 512 consecutive bytes, 16 for each lane of the warp that
-// multiplies it.  Lane 4 g + t holds rows g and g + 8 at columns 32 p + 8 t + i,
-// p = 0, 1, i = 0..7.  Word j of its four is the A operand of one m16n8k16
+// columns is 512 consecutive bytes, 16 for each lane of the warp that multiplies
+// it, and the tiles of 64 rows lie side by side: [N / 64][K / 64][4 tiles][32
+// lanes][16 bytes].  Lane 4 g + t holds rows g and g + 8 of its tile at columns 32 p +
+// 8 t + i, p = 0, 1, i = 0..7.  Word j of its four is the A operand of one m16n8k16
 // product: of the columns i = 4 (j % 2) + 0..3 of half p = j / 2, nibble r + 2 u
 // (+ 4) is row g + 8 r at column i = 4 (j % 2) + 2 u (+ 1).  The order of a
 // product's inner index is free as long as both operands follow it, so x is read
-// in 16-byte pieces of a row.  Scales: bf16, [tile][group][8][2], rows g and g + 8
-// side by side.
+// in 16-byte pieces of a row.  Scales: bf16, [N / 64][K / group][8 g][4 tiles][rows g
+// and g + 8], 16 bytes for a lane.
 #include <cfloat>
 #include <climits>
 
@@ -22,7 +23,16 @@ namespace dg {
 namespace {
 
 constexpr int kW4Rows = 16, kW4Cols = 64;  // a tile
+constexpr int kW4Tiles = 4;                // tiles side by side
+constexpr int kW4Bytes = kW4Rows * kW4Cols / 2;
 constexpr int kW4MaxM = 32;
+
+// Tile (rt, kb) in the order of memory, and the place of a group's scales of the rows
+// g, g + 8 of row tile rt (in pairs).
+DG_DEV size_t w4_tile(int rt, int kb, int KB) { return ((size_t)(rt / kW4Tiles) * KB + kb) * kW4Tiles + rt % kW4Tiles; }
+DG_DEV size_t w4_scale(int rt, int group, int KG, int g) {
+  return (((size_t)(rt / kW4Tiles) * KG + group) * 8 + g) * kW4Tiles + rt % kW4Tiles;
+}
 
 // Column of the tile at which the lane's word j begins.
 DG_DEV int w4_col(int j, int t) { return 32 * (j / 2) + 8 * t + 4 * (j % 2); }
@@ -50,7 +60,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32) w4_store_kernel(W4StoreArgs 
   const int KB = a.K / kW4Cols, span = a.group > kW4Cols ? 2 : 1, spans = KB / span;
   const int64_t id = (int64_t)blockIdx.x * kStoreWarps + threadIdx.x / 32;
   const int rt = (int)(id / spans), kb0 = (int)(id % spans) * span;
-  if (rt >= (a.N + kW4Rows - 1) / kW4Rows) return;
+  if (rt >= (a.N + kW4Rows * kW4Tiles - 1) / (kW4Rows * kW4Tiles) * kW4Tiles) return;
   for (int half = 0; half < (a.group < kW4Cols ? 2 : 1); ++half) {
     // the group's columns: both halves of its tiles, or with groups of 32 one half
     const int p0 = a.group < kW4Cols ? half : 0, p1 = a.group < kW4Cols ? half + 1 : 2;
@@ -83,7 +93,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32) w4_store_kernel(W4StoreArgs 
       }
     }
     if (t == 0)
-      a.scales[((size_t)rt * (a.K / a.group) + (kb0 * kW4Cols + 32 * p0) / a.group) * 8 + g] = sc[0] | (sc[1] << 16);
+      a.scales[w4_scale(rt, (kb0 * kW4Cols + 32 * p0) / a.group, a.K / a.group, g)] = sc[0] | (sc[1] << 16);
     for (int kb = kb0; kb < kb0 + span; ++kb)
       for (int j = 2 * p0; j < 2 * p1; ++j) {
         uint32_t word = 0;
@@ -108,7 +118,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32) w4_store_kernel(W4StoreArgs 
             word |= c << (4 * (r + 2 * (i / 2) + 4 * (i % 2)));
           }
         }
-        a.codes[(((size_t)rt * KB + kb) * 32 + lane) * 4 + j] = word;
+        a.codes[(w4_tile(rt, kb, KB) * 32 + lane) * 4 + j] = word;
       }
   }
 }
@@ -124,14 +134,14 @@ struct W4ReadArgs {
 __global__ void __launch_bounds__(256) w4_read_kernel(W4ReadArgs a) {
   pdl_wait();
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;  // one word: two rows, four columns
-  const int KB = a.K / kW4Cols;
   const int j = (int)(id % 4), lane = (int)(id / 4 % 32), g = lane / 4, t = lane % 4;
   const int64_t tile = id / 128;
-  const int rt = (int)(tile / KB), kb = (int)(tile % KB);
+  const int KB = a.K / kW4Cols, kb = (int)(tile / kW4Tiles % KB);
+  const int rt = (int)(tile / kW4Tiles / KB) * kW4Tiles + (int)(tile % kW4Tiles);
   if (rt >= (a.N + kW4Rows - 1) / kW4Rows) return;
   const uint32_t word = a.codes[id];
   const int k = kb * kW4Cols + w4_col(j, t);
-  const uint32_t sc = a.scales[((size_t)rt * (a.K / a.group) + k / a.group) * 8 + g];
+  const uint32_t sc = a.scales[w4_scale(rt, k / a.group, a.K / a.group, g)];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int n = rt * kW4Rows + g + 8 * r;
@@ -162,90 +172,202 @@ struct W4Args {
 };
 
 constexpr int kW4Warps = 8;
+constexpr int kW4Stages = 4;
+
+DG_DEV void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+DG_DEV void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Warps that share a unit: as few as leave the waves of sets on an SM's `ctas`
+// CTAs within 5 % of full (fewer barriers), all eight otherwise.
+int w4_split(int units, int KB, int ctas) {
+  for (int wk = 1; wk < kW4Warps && wk < KB; wk *= 2) {
+    const int sets = cdiv(units, kW4Warps / wk), slots = ctas * kTargetCtas;
+    if (cdiv(sets, slots) * slots <= sets * 1.05) return wk;
+  }
+  return kW4Warps;
+}
 
 // Four codes' pairs as bf16: the nibble in the low bits of 128 (the mantissa's
 // unit there is 1), less 136.  Both are exact.
 DG_DEV uint32_t w4_pair(uint32_t word, int i) {
-  const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+  uint32_t v;  // (word >> 4 i) & mask | 128's bits, in one operation after the shift
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __nv_bfloat162(136.f, 136.f));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kW4Warps * 32) w4_matvec_kernel(W4Args a) {
-  pdl_wait();
-  __shared__ float part[kW4Warps][NT * 4][32];
+// D = A B, the sum's first product
+DG_DEV void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// A unit is R row tiles and all their columns, shared by wk warps (every wk-th
+// tile of 64 columns each); a CTA works on kW4Warps / wk units at a time, a set.  A
+// warp's codes and scales come through a ring of cp.async copies that runs on over
+// the borders of its units; a lane reads only what it copied itself, so it waits for
+// nothing but its own copies.
+template <int NT, int R, int SG>
+__global__ void __launch_bounds__(kW4Warps * 32, R * NT > 8 ? 1 : 2) w4_matvec_kernel(W4Args a) {
+  constexpr int S = kW4Stages, kStage = R * kW4Bytes + SG * 32 * 4 * R;  // a lane's scales: 4 bytes to a tile
+  extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int KB = a.K / kW4Cols, tiles = (a.N + kW4Rows - 1) / kW4Rows;
-  const int per = kW4Warps / a.wk;            // row tiles of a CTA at a time
-  const int sub = warp % a.wk, rt = blockIdx.x * per + warp / a.wk;
-  const int gpt = a.group < kW4Cols ? 2 : 1;  // groups in a tile
-  float y[NT][4] = {};
-  if (rt < tiles) {
-    const uint4* c = a.codes + (size_t)rt * KB * 32 + lane;
-    const uint32_t* sp = a.scales + (size_t)rt * (a.K / a.group) * 8 + g;
-    for (int kb = sub; kb < KB; kb += a.wk) {
-      const uint4 cw = __ldcs(c + (size_t)kb * 32);
-      uint32_t s[2];
-      s[0] = __ldg(sp + (size_t)(kb * kW4Cols / a.group) * 8);
-      s[1] = gpt == 2 ? __ldg(sp + (size_t)(kb * 2 + 1) * 8) : s[0];
+  char* ring = smem + warp * S * kStage;
+  float* part = reinterpret_cast<float*>(smem + kW4Warps * S * kStage);  // [2][warps][R * NT * 4][32]
+  const int KB = a.K / kW4Cols, KG = a.K / a.group, tiles = (a.N + kW4Rows - 1) / kW4Rows;
+  const int wk = a.wk, per = kW4Warps / wk, sub = warp % wk;
+  const int sets = (tiles + per * R - 1) / (per * R);
+  const int sg_shift = a.group == 2 * kW4Cols ? 1 : 0;  // tiles that share a group
+
+  int pset = blockIdx.x, pkb = sub, pslot = 0;  // what is copied next, and where it lies
+  bool more = sub < KB;                         // (else no columns for this warp)
+  const char *pc = nullptr, *ps = nullptr;
+  auto seek = [&]() {
+    const int rt0 = (pset * per + warp / wk) * R;
+    more = more && pset < sets && rt0 < tiles;
+    pc = reinterpret_cast<const char*>(a.codes) + w4_tile(rt0, sub, KB) * kW4Bytes + lane * 16;
+    ps = reinterpret_cast<const char*>(a.scales + w4_scale(rt0, 0, KG, g));
+  };
+  auto issue = [&]() {
+    if (more) {
+      char* slot = ring + pslot;
+#pragma unroll
+      for (int r = 0; r < R; ++r) cp_async16(slot + r * kW4Bytes + lane * 16, pc + r * kW4Bytes);
+#pragma unroll
+      for (int q = 0; q < SG; ++q) {
+        const char* s = ps + ((pkb * SG >> sg_shift) + q) * 128;
+        if (R == kW4Tiles) cp_async16(slot + R * kW4Bytes + q * 512 + lane * 16, s);
+        else cp_async4(slot + R * kW4Bytes + q * 128 + lane * 4, s);
+      }
+      pkb += wk;
+      pc += wk * kW4Tiles * kW4Bytes;
+      if (pkb >= KB) {
+        pkb = sub;
+        pset += gridDim.x;
+        seek();
+      }
+    }
+    cp_async_commit();
+    pslot = pslot + kStage == S * kStage ? 0 : pslot + kStage;
+  };
+  seek();
+  pdl_wait();
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue();
+
+  // columns past the last row of x repeat it: their sums are not stored
+  const __nv_bfloat16* xp[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xp[n] = a.x + min(8 * n + g, a.M - 1) * a.ldx + 8 * t;
+  int slot_at = 0, buf = 0;
+  for (int set = blockIdx.x; set < sets; set += gridDim.x) {
+    float y[R][NT][4] = {};
+#pragma unroll 1
+    for (int kb = sub; kb < KB; kb += wk) {
       uint4 b[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
+        for (int p = 0; p < 2; ++p) b[n][p] = __ldg(reinterpret_cast<const uint4*>(xp[n] + kb * kW4Cols + 32 * p));
+      issue();
+      cp_async_wait<S - 1>();
+      const char* slot = ring + slot_at;
+      slot_at = slot_at + kStage == S * kStage ? 0 : slot_at + kStage;
+      uint32_t sw[SG][R];
+#pragma unroll
+      for (int q = 0; q < SG; ++q) {
+        const char* from = slot + R * kW4Bytes + q * 128 * R + lane * 4 * R;
+        if (R == kW4Tiles) *reinterpret_cast<uint4*>(sw[q]) = *reinterpret_cast<const uint4*>(from);
+        else sw[q][0] = *reinterpret_cast<const uint32_t*>(from);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint4 cw = *reinterpret_cast<const uint4*>(slot + r * kW4Bytes + lane * 16);
+        const uint32_t words[4] = {cw.x, cw.y, cw.z, cw.w};
+        float acc[NT][4];
+#pragma unroll
         for (int p = 0; p < 2; ++p) {
-          b[n][p] = make_uint4(0, 0, 0, 0);
-          if (8 * n + g < a.M)
-            b[n][p] = __ldg(reinterpret_cast<const uint4*>(a.x + (8 * n + g) * a.ldx + kb * kW4Cols + 32 * p + 8 * t));
-        }
-      const uint32_t words[4] = {cw.x, cw.y, cw.z, cw.w};
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        float acc[NT][4] = {};
+          for (int h = 0; h < 2; ++h) {
+            uint32_t A[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t A[4];
+            for (int i = 0; i < 4; ++i) A[i] = w4_pair(words[2 * p + h], i);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) A[i] = w4_pair(words[2 * p + h], i);
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t b0 = h ? b[n][p].z : b[n][p].x, b1 = h ? b[n][p].w : b[n][p].y;
+              if (h == 0 && (SG == 2 || p == 0)) mma_bf16_first(acc[n], A, b0, b1);
+              else mma_bf16_16816(acc[n], A, b0, b1);
+            }
+          }
+          if (SG == 2 || p == 1) {
+            const uint32_t s = sw[SG == 2 ? p : 0][r];
+            const float s0 = __uint_as_float(s << 16), s1 = __uint_as_float(s & 0xffff0000u);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma_bf16_16816(acc[n], A, h ? b[n][p].z : b[n][p].x, h ? b[n][p].w : b[n][p].y);
-        }
-        const float s0 = __uint_as_float(s[p] << 16), s1 = __uint_as_float(s[p] & 0xffff0000u);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          y[n][0] += s0 * acc[n][0];
-          y[n][1] += s0 * acc[n][1];
-          y[n][2] += s1 * acc[n][2];
-          y[n][3] += s1 * acc[n][3];
+            for (int n = 0; n < NT; ++n) {
+              y[r][n][0] += s0 * acc[n][0];
+              y[r][n][1] += s0 * acc[n][1];
+              y[r][n][2] += s1 * acc[n][2];
+              y[r][n][3] += s1 * acc[n][3];
+            }
+          }
         }
       }
     }
-  }
-  if (a.wk > 1) {  // the warps' sums in order
-    if (sub > 0) {
-#pragma unroll
-      for (int i = 0; i < NT * 4; ++i) part[warp][i][lane] = y[i / 4][i % 4];
-    }
-    __syncthreads();
-    if (sub > 0) return;
-    for (int w = 1; w < a.wk; ++w) {
-#pragma unroll
-      for (int i = 0; i < NT * 4; ++i) y[i / 4][i % 4] += part[warp + w][i][lane];
-    }
-  }
-  if (rt >= tiles) return;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = 8 * n + 2 * t + i % 2, col = rt * kW4Rows + g + 8 * (i / 2);
-      if (m >= a.M || col >= a.N) continue;
-      float v = y[n][i] * (a.alpha ? a.coef * a.alpha[m] : a.coef);
+    const int rt0 = (set * per + warp / wk) * R;
+    auto store = [&](int r, int i, float v) {
+      const int m = 8 * (i / 4) + 2 * t + i % 2, col = (rt0 + r) * kW4Rows + g + 8 * (i % 4 / 2);
+      if (m >= a.M || col >= a.N) return;
+      v *= a.alpha ? a.coef * a.alpha[m] : a.coef;
       if (a.resid) v += __bfloat162float(a.resid[m * a.ldr + col]);
       if (a.f32) static_cast<float*>(a.y)[m * a.ldy + col] = v;
       else static_cast<__nv_bfloat16*>(a.y)[m * a.ldy + col] = __float2bfloat16_rn(v);
+    };
+    if (wk > 1) {
+      // the warps' sums, in order, each warp some of the unit's values; the other half
+      // of `part` is free at the next unit's barrier
+      float* unit = part + (buf * kW4Warps + warp - sub) * R * NT * 128 + lane;
+#pragma unroll
+      for (int i = 0; i < R * NT * 4; ++i) unit[(sub * R * NT * 4 + i) * 32] = y[i / (NT * 4)][i / 4 % NT][i % 4];
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wk), "r"(wk * 32) : "memory");
+      buf ^= 1;
+      for (int i = sub; i < R * NT * 4; i += wk) {
+        float v = 0.f;
+        for (int w = 0; w < wk; ++w) v += unit[(w * R * NT * 4 + i) * 32];
+        store(i / (NT * 4), i % (NT * 4), v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R * NT * 4; ++i) store(i / (NT * 4), i % (NT * 4), y[i / (NT * 4)][i / 4 % NT][i % 4]);
     }
+  }
+  cp_async_wait<0>();
+}
+
+template <int NT, int R, int SG>
+cudaError_t launch_w4(const W4Args& args, cudaStream_t st) {
+  W4Args a = args;
+  const int tiles = cdiv(a.N, kW4Rows), units = cdiv(tiles, R), KB = a.K / kW4Cols;
+  constexpr int ctas = R * NT > 8 ? 1 : 2;
+  a.wk = w4_split(units, KB, ctas);
+  const int ring = kW4Warps * kW4Stages * R * (kW4Bytes + SG * 128);
+  const int part = 2 * kW4Warps * R * NT * 128 * (int)sizeof(float);
+  const cudaError_t e = set_smem_once<w4_matvec_kernel<NT, R, SG>>(ring + part);
+  if (e != cudaSuccess) return e;
+  const int sets = cdiv(units, kW4Warps / a.wk);
+  return launch_pdl(w4_matvec_kernel<NT, R, SG>, dim3(sets < ctas * kTargetCtas ? sets : ctas * kTargetCtas), dim3(kW4Warps * 32),
+                    (size_t)(ring + (a.wk > 1 ? part : 0)), st, a);
+}
+
+template <int SG>
+cudaError_t launch_w4_rows(const W4Args& a, bool wide, cudaStream_t st) {
+  if (a.M <= 8) return wide ? launch_w4<1, kW4Tiles, SG>(a, st) : launch_w4<1, 1, SG>(a, st);
+  if (a.M <= 16) return wide ? launch_w4<2, kW4Tiles, SG>(a, st) : launch_w4<2, 1, SG>(a, st);
+  return wide ? launch_w4<4, kW4Tiles, SG>(a, st) : launch_w4<4, 1, SG>(a, st);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -268,7 +390,7 @@ template <bool kQuantize>
 dg_status store(const dg_w4* w, const void* W, int32_t ld, const void* s, int32_t* status, void* stream) {
   W4StoreArgs a{W, static_cast<const uint16_t*>(s), static_cast<uint32_t*>(w->codes), static_cast<uint32_t*>(w->scales),
                 status, w->N, w->K, w->group, ld};
-  const int64_t spans = (int64_t)cdiv(w->N, kW4Rows) * (w->K / (w->group > kW4Cols ? w->group : kW4Cols));
+  const int64_t spans = (int64_t)cdiv(w->N, kW4Rows * kW4Tiles) * kW4Tiles * (w->K / (w->group > kW4Cols ? w->group : kW4Cols));
   const int64_t ctas = (spans + kStoreWarps - 1) / kStoreWarps;
   if (ctas > INT_MAX) return DG_ERR_SHAPE;
   return from_cuda(launch_pdl(w4_store_kernel<kQuantize>, dim3((unsigned)ctas), dim3(kStoreWarps * 32), 0,
@@ -284,7 +406,7 @@ extern "C" dg_status dg_w4_bytes(int32_t N, int32_t K, int32_t group, size_t* co
   if (!codes || !scales) return DG_ERR_ARG;
   dg_status e = check_w4_sizes(N, K, group);
   if (e) return e;
-  const size_t rows = (size_t)cdiv(N, kW4Rows) * kW4Rows;
+  const size_t rows = (size_t)cdiv(N, kW4Rows * kW4Tiles) * kW4Rows * kW4Tiles;
   *codes = rows * K / 2;
   *scales = rows * (K / group) * 2;
   return DG_OK;
@@ -310,7 +432,7 @@ extern "C" dg_status dg_w4_read(const dg_w4* w, float* out, int32_t ldo, void* s
   if (e) return e;
   if (!out || ldo < w->K || reinterpret_cast<uintptr_t>(out) % 4) return DG_ERR_ARG;
   W4ReadArgs a{static_cast<const uint32_t*>(w->codes), static_cast<const uint32_t*>(w->scales), out, w->N, w->K, w->group, ldo};
-  const int64_t words = (int64_t)cdiv(w->N, kW4Rows) * (w->K / kW4Cols) * 128;
+  const int64_t words = (int64_t)cdiv(w->N, kW4Rows * kW4Tiles) * kW4Tiles * (w->K / kW4Cols) * 128;
   if (words / 256 > INT_MAX - 1) return DG_ERR_SHAPE;
   return from_cuda(launch_pdl(w4_read_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0,
                               reinterpret_cast<cudaStream_t>(stream), a));
@@ -327,10 +449,8 @@ extern "C" dg_status dg_w4_matvec(const dg_w4* w, const void* x, int32_t ldx, in
   if (M > kW4MaxM) return DG_ERR_SHAPE;
   W4Args a{static_cast<const uint4*>(w->codes), static_cast<const uint32_t*>(w->scales),
            static_cast<const __nv_bfloat16*>(x), alpha, static_cast<const __nv_bfloat16*>(resid), y, coef, w->N, w->K,
-           w->group, M, ldx, ldr, ldy, y_f32 != 0, 8};
-  const dim3 grid(cdiv(w->N, kW4Rows * (kW4Warps / a.wk))), block(kW4Warps * 32);
+           w->group, M, ldx, ldr, ldy, y_f32 != 0, 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (M <= 8) return from_cuda(launch_pdl(w4_matvec_kernel<1>, grid, block, 0, st, a));
-  if (M <= 16) return from_cuda(launch_pdl(w4_matvec_kernel<2>, grid, block, 0, st, a));
-  return from_cuda(launch_pdl(w4_matvec_kernel<4>, grid, block, 0, st, a));
+  const bool wide = cdiv(w->N, kW4Rows) >= 16 * kTargetCtas;
+  return from_cuda(w->group == 32 ? launch_w4_rows<2>(a, wide, st) : launch_w4_rows<1>(a, wide, st));
 }

@@ -476,7 +476,7 @@ DG_API dg_status dg_kv8_attention(const dg_kv8_cache* cache, const void* q, cons
  *   a weight is s * (c - 8): a code c of 4 bits and a bf16 scale s for each row and
  *   `group` (32, 64 or 128) consecutive columns
  *   codes, scales   device, 16-byte aligned, of dg_w4_bytes bytes, in the layout that
- *           the products read (tiles of 16 rows and 64 columns; the rows behind the
+ *           the products read (tiles of 64 rows and 64 columns; the rows behind the
  *           last one of the last tile are zeros): written by dg_w4_quantize or
  *           dg_w4_pack, read back by dg_w4_read
  *   N       rows (1 .. 2^24); K  columns, a multiple of 64 and of group, <= 65536   */

@@ -45,7 +45,7 @@ def test_bad_matrices_are_refused(dg, kw, code):
 def test_bytes(dg):
     L, a, b = dg.load(), ct.c_size_t(), ct.c_size_t()
     assert L.dg_w4_bytes(17, 128, 32, ct.byref(a), ct.byref(b)) == dg.DG_OK
-    assert (a.value, b.value) == (32 * 64, 32 * 4 * 2)
+    assert (a.value, b.value) == (64 * 64, 64 * 4 * 2)
     assert L.dg_w4_bytes(17, 128, 32, None, ct.byref(b)) == L.dg_w4_bytes(17, 128, 32, ct.byref(a), None) == dg.DG_ERR_ARG
     assert L.dg_w4_bytes(0, 128, 32, ct.byref(a), ct.byref(b)) == dg.DG_ERR_ARG
     assert L.dg_w4_bytes(17, 100, 32, ct.byref(a), ct.byref(b)) == dg.DG_ERR_SHAPE
