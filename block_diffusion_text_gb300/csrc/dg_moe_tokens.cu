@@ -22,6 +22,7 @@
 // but the lane's own copies.
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "dg_common.cuh"
 #include "dg_internal.h"
@@ -31,8 +32,10 @@ namespace {
 
 constexpr int kMtWarps = 16;
 constexpr int kMtThreads = kMtWarps * 32;
-constexpr int kMtStages = 4;
-constexpr int kMtStage = 2048;  // 16 rows of 64 columns
+constexpr int kMtStages = 2;
+constexpr int kMtRows = 32;     // rows of a unit: two MMA tiles
+constexpr int kMtStage = kMtRows * 128;  // 64 columns of them
+constexpr int kMtRed = 65536;   // shared memory for the warps' parts of units' sums
 constexpr int kMtMaxM = 32;
 constexpr int kMtMaxExp = 256, kMtMaxK = 16;
 
@@ -101,43 +104,126 @@ DG_DEV void cp_async16(void* dst, const void* src) {
 
 DG_DEV float gelu(float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f)); }
 
-// Stage of a ring: the lane's pieces of rows g and g + 8, halves 0 and 1 of the 64
-// columns.  Rows at or past `rows` are not copied: what their products hold is not used.
-DG_DEV void load_block(char* slot, const __nv_bfloat16* w, int64_t pitch, int rows, int lane) {
+// Stage of a ring: the lane's pieces of rows g, g + 8, g + 16 and g + 24, halves 0 and
+// 1 of the 64 columns.  Rows at or past `rows` are not copied: what their products
+// hold is not used.
+DG_DEV void load_block(char* slot, const __nv_bfloat16* w, int pitch, int rows, int lane) {
   const int g = lane / 4, t = lane % 4;
+  const __nv_bfloat16* src = w + g * pitch + 8 * t;
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int r = 0; r < kMtRows / 8; ++r)
     if (g + 8 * r < rows) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-        cp_async16(slot + ((r * 2 + p) * 32 + lane) * 16, w + (g + 8 * r) * pitch + 32 * p + 8 * t);
+      for (int p = 0; p < 2; ++p) cp_async16(slot + ((r * 2 + p) * 32 + lane) * 16, src + 8 * r * pitch + 32 * p);
     }
-}
-
-// The products of one block: acc[n] += (16 rows) x (8 tokens), b(n, p) the lane's
-// eight values of its token in half p.
-template <int NT, class B>
-DG_DEV void block_products(float (&acc)[NT][4], const char* slot, int lane, unsigned tiles, const B& b) {
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const uint4 u = *reinterpret_cast<const uint4*>(slot + (p * 32 + lane) * 16);
-    const uint4 v = *reinterpret_cast<const uint4*>(slot + ((2 + p) * 32 + lane) * 16);
-    const uint32_t A0[4] = {u.x, v.x, u.y, v.y}, A1[4] = {u.z, v.z, u.w, v.w};
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if (tiles >> n & 1) b(acc[n], n, p, A0, A1);
-  }
 }
 
 DG_DEV unsigned tiles_of(unsigned mask) {  // a bit for each eight tokens that hold one
   return (mask & 0xffu ? 1u : 0u) | (mask & 0xff00u ? 2u : 0u) | (mask & 0xff0000u ? 4u : 0u) | (mask & 0xff000000u ? 8u : 0u);
 }
 
+// Rows [r0, r1) cut into units of 32 rows at most, from r0 to the border rb (a
+// matrix's end) and from there on.  (Further matrices begin at multiples of 32 from
+// there: their rows are multiples of 128.)
+struct MtCut {
+  int r0, rb, r1, U0, U;
+  DG_DEV MtCut() {}
+  DG_DEV MtCut(int first, int end, int border) : r0(first), r1(end) {
+    rb = border > first && border < end ? border : end;
+    U0 = (rb - r0 + kMtRows - 1) / kMtRows;
+    U = U0 + (r1 - rb + kMtRows - 1) / kMtRows;
+  }
+  DG_DEV int row(int u) const { return u < U0 ? r0 + kMtRows * u : rb + kMtRows * (u - U0); }
+  DG_DEV int rows(int u) const { return min(kMtRows, (u < U0 ? rb : r1) - row(u)); }
+};
+
+// Cursors over the segments of a CTA's units: of the router and the shared expert,
+// of the chosen experts (both multiply the tokens themselves), and of the second
+// matrices.
+template <int NT>
+struct RowsOfH0 {
+  MtCut cut;
+  const __nv_bfloat16 *Wr, *Ws, *w;
+  int border, n_exp, d, u, rows;
+  unsigned mask;
+  int off[NT];
+  DG_DEV void start(int g, int t, int pitch) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) off[n] = (8 * n + g) * pitch + 8 * t;
+    u = -1;
+    next();
+  }
+  DG_DEV void next() {
+    if (++u >= cut.U) return;
+    const int r = cut.row(u);
+    rows = r < border ? min(cut.rows(u), n_exp - r) : cut.rows(u);
+    w = r < border ? Wr + (int64_t)r * d : Ws + (int64_t)(r - border) * d;
+  }
+};
+
+template <int NT>
+struct RowsOfH1 {
+  MtCut cut;
+  const __nv_bfloat16 *W1, *w;
+  const int* act;
+  const unsigned* masks;
+  int F, d, u, rows;
+  unsigned mask;
+  int off[NT];
+  DG_DEV void start(int g, int t, int pitch) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) off[n] = (8 * n + g) * pitch + 8 * t;
+    u = -1;
+    next();
+  }
+  DG_DEV void next() {
+    if (++u >= cut.U) return;
+    const int r = cut.row(u), x = r / F, e = act[x];
+    rows = cut.rows(u);
+    w = W1 + ((int64_t)e * F + r - x * F) * d;
+    mask = masks[e];
+  }
+};
+
+template <int NT, bool kTokens>
+struct RowsOfHidden {
+  MtCut cut;
+  const __nv_bfloat16 *W2, *w;
+  const MtShared* s;
+  int F, d, n_exp, nact, K1, g, t, u, x, rows;
+  unsigned all, mask;
+  int off[NT];
+  DG_DEV void start() {
+    u = 0;
+    x = -1;
+    next();
+  }
+  DG_DEV void next() {
+    if (++x > nact) {
+      x = 0;
+      ++u;
+    }
+    if (u >= cut.U) return;
+    const int e = x < nact ? s->act[x] : n_exp;
+    if (!kTokens) {
+      rows = cut.rows(u);
+      w = W2 + ((int64_t)e * d + cut.row(u)) * F;
+      return;
+    }
+    mask = x < nact ? s->mask[e] : all;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int m = 8 * n + g;
+      if (mask >> m & 1) off[n] = (m * K1 + (x < nact ? s->rank[e][m] : K1 - 1)) * F + 8 * t;
+    }
+  }
+};
+
 template <int NT>
 __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   extern __shared__ __align__(16) char smem[];
   char* ring = smem + (threadIdx.x / 32) * kMtStages * kMtStage;
-  float* red = reinterpret_cast<float*>(smem + kMtWarps * kMtStages * kMtStage);  // [warps][NT * 4][32]
+  float* red = reinterpret_cast<float*>(smem + kMtWarps * kMtStages * kMtStage);  // [units][warps][NT * 4][32]
   __shared__ MtShared s;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int K1 = a.top_k + 1, KB1 = a.d / 64, KB2 = a.Fe / 64;
@@ -164,79 +250,119 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   }
   __syncthreads();
 
-  // The sums of a unit over the CTA's warps, in order; thread i * 32 + lane gets the
-  // value of (row g + 8 (i % 4 / 2), token 8 (i / 4) + 2 t + i % 2).
-  auto unit_sum = [&](const float (&acc)[NT][4], const auto& put) {
-#pragma unroll
-    for (int i = 0; i < NT * 4; ++i) red[(warp * NT * 4 + i) * 32 + lane] = acc[i / 4][i % 4];
+  // A unit (32 rows at most) ends with each warp's part of its sums in `red`; the parts
+  // are added, in order, after kBatch units or the last.  Then thread i * 32 + lane of a
+  // unit's values has (row 16 r + g + 8 (i % 4 / 2), token 8 (i / 4 % NT) + 2 t + i % 2),
+  // r = i / (4 NT).
+  constexpr int kVals = 2 * NT * 4, kBatch = kMtRed / (kMtWarps * kVals * 128);
+  auto add_parts = [&](int u0, int u1, const auto& put) {
     __syncthreads();
-    if (tid < NT * 128) {
-      float v = 0.f;
+    for (int v = tid; v < (u1 - u0) * kVals * 32; v += kMtThreads) {
+      const int u = u0 + v / (kVals * 32), at = v % (kVals * 32), i = at / 32;
+      const float* from = red + (u % kBatch) * kMtWarps * kVals * 32 + at;
+      float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kMtWarps; ++w) v += red[w * NT * 128 + tid];
-      const int i = tid / 32;
-      put(g + 8 * (i % 4 / 2), 8 * (i / 4) + 2 * t + i % 2, v);
+      for (int w = 0; w < kMtWarps; ++w) sum += from[w * kVals * 32];
+      put(u, 16 * (i / (4 * NT)) + g + 8 * (i % 4 / 2), 8 * (i / 4 % NT) + 2 * t + i % 2, sum);
     }
     __syncthreads();
   };
 
-  // Products of h with rows [r0, r1) of a row space cut into tiles of 16: unit u is
-  // tile r0 / 16 + u.  src(tile) is the tile's first row in memory and the tokens that
-  // want it; put(row of the space, token, sum).
-  auto rows_of_h = [&](int r0, int r1, const auto& src, const auto& put) {
-    if (r1 <= r0) return;
-    const int T0 = r0 / 16, U = (r1 + 15) / 16 - T0;
-    const int total = U * KB1;
-    auto issue = [&](int i, int slot) {
-      if (i < total) {
-        const int u = i / KB1, kb = i % KB1, lo = max(r0, 16 * (T0 + u)), hi = min(r1, 16 * (T0 + u) + 16);
-        const __nv_bfloat16* w;
-        int rows;
-        unsigned mask;
-        src(T0 + u, &w, &rows, &mask);
-        const int skip = lo - 16 * (T0 + u);
-        rows = min(rows - skip, hi - lo);
-        load_block(ring + slot * kMtStage, w + (int64_t)skip * a.d + kb * 64, a.d, rows, lane);
+  // The engine of all phases.  A unit's sums run over segments (matrices of `pitch`
+  // columns, KB blocks of 64 each); a warp takes every 16th block, over the borders of
+  // segments and units.  It walks the segments with two cursors: one for the copies
+  // (kMtStages - 1 blocks ahead), one for the tokens' values (a block ahead, in
+  // registers, where they leave room).  A cursor gives the segment's first row w, rows,
+  // tokens (mask) and unit u, the lane's offsets of the tokens' values, and next().
+  // Columns of a token that does not want the segment's expert are zeros.
+  auto stream = [&](auto pc, auto bc, int KB, int pitch, int U, const __nv_bfloat16* bh, const __nv_bfloat16* bl, auto pair,
+                    const auto& put) {
+    constexpr bool kPair = decltype(pair)::value, kAhead = NT <= 2;
+    constexpr int kB = kPair ? 2 : 1;
+    int pk = warp, bk = warp, pslot = 0;
+    auto settle = [&](auto& c, int& k) {
+      while (k >= KB && c.u < U) {
+        k -= KB;
+        c.next();
+      }
+    };
+    auto issue = [&]() {
+      if (pc.u < U) {
+        load_block(ring + pslot, pc.w + pk * 64, pitch, pc.rows, lane);
+        pk += kMtWarps;
+        settle(pc, pk);
       }
       cp_async_commit();
+      pslot = pslot + kMtStage == kMtStages * kMtStage ? 0 : pslot + kMtStage;
     };
-    int i = warp, put_slot = 0, get_slot = 0;
+    uint4 b[NT][2][kB];
+    auto load_b = [&](unsigned mask, const int (&off)[NT], int k) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int q = 0; q < kB; ++q) {
+            b[n][p][q] = make_uint4(0, 0, 0, 0);
+            if (mask >> (8 * n + g) & 1) b[n][p][q] = *reinterpret_cast<const uint4*>((q ? bl : bh) + off[n] + k * 64 + 32 * p);
+          }
+    };
+    settle(pc, pk);
+    settle(bc, bk);
 #pragma unroll 1
-    for (int s0 = 0; s0 < kMtStages - 1; ++s0) {
-      issue(i + s0 * kMtWarps, put_slot);
-      put_slot = put_slot + 1 == kMtStages ? 0 : put_slot + 1;
-    }
+    for (int s0 = 0; s0 < kMtStages - 1; ++s0) issue();
+    float acc[2][NT][4] = {};
+    int u = 0, done = 0, slot = 0;
+    auto flush_to = [&](int to) {  // units u .. to - 1 have all that this warp adds to them
 #pragma unroll 1
-    for (int u = 0; u < U; ++u) {
-      float acc[NT][4] = {};
-      const __nv_bfloat16* w;
-      int rows;
-      unsigned mask;
-      src(T0 + u, &w, &rows, &mask);
-      const unsigned tiles = tiles_of(mask);
-#pragma unroll 1
-      for (; i < (u + 1) * KB1; i += kMtWarps) {
-        issue(i + (kMtStages - 1) * kMtWarps, put_slot);
-        put_slot = put_slot + 1 == kMtStages ? 0 : put_slot + 1;
-        cp_async_wait<kMtStages - 1>();
-        const __nv_bfloat16* x = a.h + (i - u * KB1) * 64 + 8 * t;
-        block_products<NT>(acc, ring + get_slot * kMtStage, lane, tiles,
-                           [&](float(&c)[4], int n, int p, const uint32_t(&A0)[4], const uint32_t(&A1)[4]) {
-                             uint4 b = make_uint4(0, 0, 0, 0);
-                             if (mask >> (8 * n + g) & 1)
-                               b = *reinterpret_cast<const uint4*>(x + (int64_t)(8 * n + g) * a.d + 32 * p);
-                             mma_bf16_16816(c, A0, b.x, b.y);
-                             mma_bf16_16816(c, A1, b.z, b.w);
-                           });
-        get_slot = get_slot + 1 == kMtStages ? 0 : get_slot + 1;
+      for (; u < to; ++u) {
+        float* part = red + ((u % kBatch) * kMtWarps + warp) * kVals * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) {
+          part[i * 32] = acc[i / (4 * NT)][i / 4 % NT][i % 4];
+          acc[i / (4 * NT)][i / 4 % NT][i % 4] = 0.f;
+        }
+        if (u + 1 == U || (u + 1) % kBatch == 0) {
+          add_parts(done, u + 1, put);
+          done = u + 1;
+        }
       }
-      const int lo = max(r0, 16 * (T0 + u)), hi = min(r1, 16 * (T0 + u) + 16);
-      unit_sum(acc, [&](int row, int m, float v) {
-        if (lo + row < hi && (mask >> m & 1)) put(lo + row, m, v * s.inv[m]);
-      });
+    };
+    flush_to(min(bc.u, U));
+    if (kAhead && bc.u < U) load_b(bc.mask, bc.off, bk);
+#pragma unroll 1
+    while (bc.u < U) {
+      issue();
+      cp_async_wait<kMtStages - 1>();
+      const unsigned mask = bc.mask, tiles = tiles_of(mask);
+      if (!kAhead) load_b(mask, bc.off, bk);
+      bk += kMtWarps;
+      settle(bc, bk);
+      const char* from = ring + slot + lane * 16;
+      slot = slot + kMtStage == kMtStages * kMtStage ? 0 : slot + kMtStage;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint4 v = *reinterpret_cast<const uint4*>(from + (4 * r + p) * 512);
+          const uint4 w = *reinterpret_cast<const uint4*>(from + (4 * r + 2 + p) * 512);
+          const uint32_t A0[4] = {v.x, w.x, v.y, w.y}, A1[4] = {v.z, w.z, v.w, w.w};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (tiles >> n & 1) {
+#pragma unroll
+              for (int q = 0; q < kB; ++q) {
+                mma_bf16_16816(acc[r][n], A0, b[n][p][q].x, b[n][p][q].y);
+                mma_bf16_16816(acc[r][n], A1, b[n][p][q].z, b[n][p][q].w);
+              }
+            }
+        }
+      if (kAhead && bc.u < U) load_b(bc.mask, bc.off, bk);
+      flush_to(min(bc.u, U));
     }
     cp_async_wait<0>();
   };
+
   auto range = [&](int rows, int c) { return (int)((int64_t)rows * c / ctas); };
   auto store_hidden = [&](int m, int j, int f, float v) {
     const size_t at = ((size_t)m * K1 + j) * a.Fe + f;
@@ -246,19 +372,25 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   };
 
   // ---- phase 0: the router's rows, then the shared expert's
-  const int n16 = (a.n_exp + 15) / 16 * 16;
-  rows_of_h(
-      range(n16 + a.Fe, cta), range(n16 + a.Fe, cta + 1),
-      [&](int tile, const __nv_bfloat16** w, int* rows, unsigned* mask) {
-        const bool router = 16 * tile < n16;
-        *w = router ? a.Wr + (int64_t)tile * 16 * a.d : a.W1 + ((int64_t)a.n_exp * a.Fe + 16 * tile - n16) * a.d;
-        *rows = router ? min(16, a.n_exp - 16 * tile) : 16;
-        *mask = all;
-      },
-      [&](int row, int m, float v) {
-        if (row < a.n_exp) a.logits[(size_t)m * a.n_exp + row] = v;
-        else if (row >= n16) store_hidden(m, a.top_k, row - n16, gelu(v));
-      });
+  {
+    const int n32 = (a.n_exp + kMtRows - 1) / kMtRows * kMtRows, R = n32 + a.Fe;
+    const MtCut cut(range(R, cta), range(R, cta + 1), n32);
+    RowsOfH0<NT> c;
+    c.cut = cut;
+    c.Wr = a.Wr;
+    c.Ws = a.W1 + (int64_t)a.n_exp * a.Fe * a.d;
+    c.border = n32;
+    c.n_exp = a.n_exp;
+    c.d = a.d;
+    c.mask = all;
+    c.start(g, t, a.d);
+    stream(c, c, KB1, a.d, cut.U, a.h, a.h, std::false_type{}, [&](int u, int row, int m, float v) {
+      if (row >= cut.rows(u) || m >= a.M) return;
+      row += cut.row(u);
+      if (row < a.n_exp) a.logits[(size_t)m * a.n_exp + row] = v * s.inv[m];
+      else if (row >= n32) store_hidden(m, a.top_k, row - n32, gelu(v * s.inv[m]));
+    });
+  }
   if (!grid_barrier(a.bar, a.status, &s.stop)) return;
 
   // ---- the routing: one warp for each token, a lane holding experts lane, lane + 32, ..
@@ -337,78 +469,54 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   const int nact = s.nact;
 
   // ---- phase 1: the chosen experts' hidden rows
-  const int R1 = nact * a.Fe;
-  rows_of_h(
-      range(R1, cta), range(R1, cta + 1),
-      [&](int tile, const __nv_bfloat16** w, int* rows, unsigned* mask) {
-        const int e = s.act[16 * tile / a.Fe];
-        *w = a.W1 + ((int64_t)e * a.Fe + 16 * tile % a.Fe) * a.d;
-        *rows = 16;
-        *mask = s.mask[e];
-      },
-      [&](int row, int m, float v) {
-        const int e = s.act[row / a.Fe], j = s.rank[e][m];
-        store_hidden(m, j, row % a.Fe, s.gate[m][j] * gelu(v));
-      });
+  {
+    const int R = nact * a.Fe, r0 = range(R, cta), r1 = range(R, cta + 1);
+    const MtCut cut(r0, r1, min(r1, r0 / a.Fe * a.Fe + a.Fe));
+    RowsOfH1<NT> c;
+    c.cut = cut;
+    c.W1 = a.W1;
+    c.act = s.act;
+    c.masks = s.mask;
+    c.F = a.Fe;
+    c.d = a.d;
+    c.start(g, t, a.d);
+    stream(c, c, KB1, a.d, cut.U, a.h, a.h, std::false_type{}, [&](int u, int row, int m, float v) {
+      if (row >= cut.rows(u)) return;
+      row += cut.row(u);
+      const int x = row / a.Fe, e = s.act[x];
+      if (!(s.mask[e] >> m & 1)) return;
+      const int j = s.rank[e][m];
+      store_hidden(m, j, row - x * a.Fe, s.gate[m][j] * gelu(v * s.inv[m]));
+    });
+  }
   if (!grid_barrier(a.bar, a.status, &s.stop)) return;
 
-  // ---- phase 2: output columns [r0, r1), their sums over the experts' hidden values
+  // ---- phase 2: output columns, their sums over the experts' hidden values
   {
     const int r0 = range(a.d, cta), r1 = range(a.d, cta + 1);
-    const int U = (r1 - r0 + 15) / 16, items = (nact + 1) * KB2;
-    const int64_t total = (int64_t)U * items;
-    auto issue = [&](int64_t i, int slot) {
-      if (i < total) {
-        const int u = (int)(i / items), at = (int)(i % items), x = at / KB2, kb = at % KB2;
-        const int e = x < nact ? s.act[x] : a.n_exp, row = r0 + 16 * u;
-        load_block(ring + slot * kMtStage, a.W2 + ((int64_t)e * a.d + row) * a.Fe + kb * 64, a.Fe, r1 - row, lane);
-      }
-      cp_async_commit();
+    const MtCut cut(r0, r1, r1);
+    auto cursor = [&](auto tokens) {
+      RowsOfHidden<NT, decltype(tokens)::value> c;
+      c.cut = cut;
+      c.W2 = a.W2;
+      c.s = &s;
+      c.F = a.Fe;
+      c.d = a.d;
+      c.n_exp = a.n_exp;
+      c.nact = nact;
+      c.K1 = K1;
+      c.all = all;
+      c.g = g;
+      c.t = t;
+      c.start();
+      return c;
     };
-    int64_t i = warp;
-    int put_slot = 0, get_slot = 0;
-#pragma unroll 1
-    for (int s0 = 0; s0 < kMtStages - 1; ++s0) {
-      issue(i + s0 * kMtWarps, put_slot);
-      put_slot = put_slot + 1 == kMtStages ? 0 : put_slot + 1;
-    }
-#pragma unroll 1
-    for (int u = 0; u < U; ++u) {
-      float acc[NT][4] = {};
-#pragma unroll 1
-      for (; i < (int64_t)(u + 1) * items; i += kMtWarps) {
-        issue(i + (kMtStages - 1) * kMtWarps, put_slot);
-        put_slot = put_slot + 1 == kMtStages ? 0 : put_slot + 1;
-        cp_async_wait<kMtStages - 1>();
-        const int at = (int)(i - (int64_t)u * items), x = at / KB2, kb = at % KB2;
-        const int e = x < nact ? s.act[x] : a.n_exp;
-        const unsigned mask = x < nact ? s.mask[e] : all;
-        block_products<NT>(acc, ring + get_slot * kMtStage, lane, tiles_of(mask),
-                           [&](float(&c)[4], int n, int p, const uint32_t(&A0)[4], const uint32_t(&A1)[4]) {
-                             uint4 b = make_uint4(0, 0, 0, 0), bl = b;
-                             const int m = 8 * n + g;
-                             if (mask >> m & 1) {
-                               const int j = x < nact ? s.rank[e][m] : a.top_k;
-                               const size_t off = ((size_t)m * K1 + j) * a.Fe + kb * 64 + 32 * p + 8 * t;
-                               b = *reinterpret_cast<const uint4*>(a.hi + off);
-                               bl = *reinterpret_cast<const uint4*>(a.lo + off);
-                             }
-                             mma_bf16_16816(c, A0, b.x, b.y);
-                             mma_bf16_16816(c, A1, b.z, b.w);
-                             mma_bf16_16816(c, A0, bl.x, bl.y);
-                             mma_bf16_16816(c, A1, bl.z, bl.w);
-                           });
-        get_slot = get_slot + 1 == kMtStages ? 0 : get_slot + 1;
-      }
-      const int row0 = r0 + 16 * u;
-      unit_sum(acc, [&](int row, int m, float v) {
-        if (row0 + row < r1 && m < a.M) {
-          const size_t at = (size_t)m * a.d + row0 + row;
-          a.out[at] = __float2bfloat16_rn(__bfloat162float(a.h[at]) + v);
-        }
-      });
-    }
-    cp_async_wait<0>();
+    stream(cursor(std::false_type{}), cursor(std::true_type{}), KB2, a.Fe, cut.U, a.hi, a.lo, std::true_type{},
+           [&](int u, int row, int m, float v) {
+             if (row >= cut.rows(u) || m >= a.M) return;
+             const int at = m * a.d + cut.row(u) + row;
+             a.out[at] = __float2bfloat16_rn(__bfloat162float(a.h[at]) + v);
+           });
   }
 }
 
@@ -441,7 +549,7 @@ dg_status check_sizes(const dg_model* m, int32_t M) {
 
 template <int NT>
 cudaError_t launch(const MtArgs& a, int sms, cudaStream_t st) {
-  const int smem = kMtWarps * kMtStages * kMtStage + kMtWarps * NT * 4 * 32 * (int)sizeof(float);
+  const int smem = kMtWarps * kMtStages * kMtStage + kMtRed;
   cudaError_t e = set_smem_once<moe_tokens_kernel<NT>>(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
