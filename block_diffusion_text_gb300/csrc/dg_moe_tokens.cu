@@ -44,7 +44,8 @@ struct MtArgs {
   __nv_bfloat16* out;                      // [M][d], may be h
   const __nv_bfloat16 *Wr, *W1, *W2;       // [n_exp][d], [n_exp + 1][Fe][d], [n_exp + 1][d][Fe]
   float* logits;                           // [M][n_exp]
-  __nv_bfloat16 *hi, *lo;                  // [M][top_k + 1][Fe]: gate GELU(x We1^T)
+  __nv_bfloat16* hid;                      // [M (top_k + 1) + 1][Fe / 32][2][32]: gate GELU(x We1^T), the values as
+                                           // bf16 and what that leaves; the last row is zeros
   int* idx;                                // [M][top_k] or null
   float* gate;                             // [M][top_k] or null
   int* status;
@@ -53,12 +54,18 @@ struct MtArgs {
   float eps;
 };
 
+struct MtExpert {
+  int e;
+  unsigned mask;                           // its tokens
+};
+
 struct MtShared {
   float inv[kMtMaxM];
   float gate[kMtMaxM][kMtMaxK];
-  unsigned mask[kMtMaxExp];                // tokens of an expert
-  uint8_t rank[kMtMaxExp][kMtMaxM];        // their place among the token's experts
-  int act[kMtMaxExp];                      // the experts with tokens, ascending
+  unsigned mask[kMtMaxExp];                // tokens of every expert
+  uint8_t place[kMtMaxExp][kMtMaxM];       // their place among the token's experts
+  MtExpert ex[kMtMaxExp + 1];              // the experts with tokens, ascending, and the shared one
+  uint8_t rank[kMtMaxExp + 1][kMtMaxM];    // and the place of each of their tokens
   int nact;
   int stop;
 };
@@ -145,11 +152,12 @@ struct RowsOfH0 {
   MtCut cut;
   const __nv_bfloat16 *Wr, *Ws, *w;
   int border, n_exp, d, u, rows;
-  unsigned mask;
+  unsigned tiles;
   int off[NT];
-  DG_DEV void start(int g, int t, int pitch) {
+  DG_DEV void start(int g, int t, int M) {
+    tiles = (1u << ((M + 7) / 8)) - 1;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) off[n] = (8 * n + g) * pitch + 8 * t;
+    for (int n = 0; n < NT; ++n) off[n] = min(8 * n + g, M - 1) * d + 8 * t;  // columns past the last token repeat it
     u = -1;
     next();
   }
@@ -161,37 +169,42 @@ struct RowsOfH0 {
   }
 };
 
+// A column whose token does not want the expert takes the values of one that does:
+// its sum is not stored.
 template <int NT>
 struct RowsOfH1 {
   MtCut cut;
   const __nv_bfloat16 *W1, *w;
-  const int* act;
-  const unsigned* masks;
-  int F, d, u, rows;
-  unsigned mask;
+  const MtExpert* ex;
+  int F, d, u, rows, g, t;
+  unsigned tiles;
   int off[NT];
-  DG_DEV void start(int g, int t, int pitch) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) off[n] = (8 * n + g) * pitch + 8 * t;
+  DG_DEV void start() {
     u = -1;
     next();
   }
   DG_DEV void next() {
     if (++u >= cut.U) return;
-    const int r = cut.row(u), x = r / F, e = act[x];
+    const int r = cut.row(u), x = r / F;
+    const MtExpert e = ex[x];
     rows = cut.rows(u);
-    w = W1 + ((int64_t)e * F + r - x * F) * d;
-    mask = masks[e];
+    w = W1 + ((int64_t)e.e * F + r - x * F) * d;
+    tiles = tiles_of(e.mask);
+    const int some = __ffs(e.mask) - 1;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) off[n] = (e.mask >> (8 * n + g) & 1 ? 8 * n + g : some) * d + 8 * t;
   }
 };
 
+// .. and here, where a column's sum runs over all experts, the row of zeros.
 template <int NT, bool kTokens>
 struct RowsOfHidden {
   MtCut cut;
   const __nv_bfloat16 *W2, *w;
   const MtShared* s;
-  int F, d, n_exp, nact, K1, g, t, u, x, rows;
-  unsigned all, mask;
+  int F, K1, g, t, u, x, rows, zeros;
+  int64_t dF;
+  unsigned tiles;
   int off[NT];
   DG_DEV void start() {
     u = 0;
@@ -199,22 +212,22 @@ struct RowsOfHidden {
     next();
   }
   DG_DEV void next() {
-    if (++x > nact) {
+    if (++x > s->nact) {
       x = 0;
       ++u;
     }
     if (u >= cut.U) return;
-    const int e = x < nact ? s->act[x] : n_exp;
+    const MtExpert e = s->ex[x];
     if (!kTokens) {
       rows = cut.rows(u);
-      w = W2 + ((int64_t)e * d + cut.row(u)) * F;
+      w = W2 + (e.e * dF + cut.row(u) * F);
       return;
     }
-    mask = x < nact ? s->mask[e] : all;
+    tiles = tiles_of(e.mask);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int m = 8 * n + g;
-      if (mask >> m & 1) off[n] = (m * K1 + (x < nact ? s->rank[e][m] : K1 - 1)) * F + 8 * t;
+      off[n] = (e.mask >> m & 1 ? m * K1 + s->rank[x][m] : zeros) * 2 * F + 8 * t;
     }
   }
 };
@@ -273,10 +286,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   // segments and units.  It walks the segments with two cursors: one for the copies
   // (kMtStages - 1 blocks ahead), one for the tokens' values (a block ahead, in
   // registers, where they leave room).  A cursor gives the segment's first row w, rows,
-  // tokens (mask) and unit u, the lane's offsets of the tokens' values, and next().
-  // Columns of a token that does not want the segment's expert are zeros.
-  auto stream = [&](auto pc, auto bc, int KB, int pitch, int U, const __nv_bfloat16* bh, const __nv_bfloat16* bl, auto pair,
-                    const auto& put) {
+  // unit u, the column tiles with tokens, the lane's offsets of the tokens' values, and
+  // next().
+  auto stream = [&](auto pc, auto bc, int KB, int pitch, int U, const __nv_bfloat16* values, auto pair, const auto& put) {
     constexpr bool kPair = decltype(pair)::value, kAhead = NT <= 2;
     constexpr int kB = kPair ? 2 : 1;
     int pk = warp, bk = warp, pslot = 0;
@@ -296,16 +308,16 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
       pslot = pslot + kMtStage == kMtStages * kMtStage ? 0 : pslot + kMtStage;
     };
     uint4 b[NT][2][kB];
-    auto load_b = [&](unsigned mask, const int (&off)[NT], int k) {
+    auto load_b = [&](unsigned tiles, const int (&off)[NT], int k) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
+        if (NT == 1 || (tiles >> n & 1)) {
+          const __nv_bfloat16* from = values + off[n] + k * 64 * kB;
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int q = 0; q < kB; ++q) {
-            b[n][p][q] = make_uint4(0, 0, 0, 0);
-            if (mask >> (8 * n + g) & 1) b[n][p][q] = *reinterpret_cast<const uint4*>((q ? bl : bh) + off[n] + k * 64 + 32 * p);
-          }
+            for (int q = 0; q < kB; ++q) b[n][p][q] = *reinterpret_cast<const uint4*>(from + (p * kB + q) * 32);
+        }
     };
     settle(pc, pk);
     settle(bc, bk);
@@ -329,13 +341,13 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
       }
     };
     flush_to(min(bc.u, U));
-    if (kAhead && bc.u < U) load_b(bc.mask, bc.off, bk);
+    if (kAhead && bc.u < U) load_b(bc.tiles, bc.off, bk);
 #pragma unroll 1
     while (bc.u < U) {
       issue();
       cp_async_wait<kMtStages - 1>();
-      const unsigned mask = bc.mask, tiles = tiles_of(mask);
-      if (!kAhead) load_b(mask, bc.off, bk);
+      const unsigned tiles = bc.tiles;
+      if (!kAhead) load_b(tiles, bc.off, bk);
       bk += kMtWarps;
       settle(bc, bk);
       const char* from = ring + slot + lane * 16;
@@ -349,7 +361,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
           const uint32_t A0[4] = {v.x, w.x, v.y, w.y}, A1[4] = {v.z, w.z, v.w, w.w};
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            if (tiles >> n & 1) {
+            if (NT == 1 || (tiles >> n & 1)) {
 #pragma unroll
               for (int q = 0; q < kB; ++q) {
                 mma_bf16_16816(acc[r][n], A0, b[n][p][q].x, b[n][p][q].y);
@@ -357,7 +369,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
               }
             }
         }
-      if (kAhead && bc.u < U) load_b(bc.mask, bc.off, bk);
+      if (kAhead && bc.u < U) load_b(bc.tiles, bc.off, bk);
       flush_to(min(bc.u, U));
     }
     cp_async_wait<0>();
@@ -365,11 +377,15 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
 
   auto range = [&](int rows, int c) { return (int)((int64_t)rows * c / ctas); };
   auto store_hidden = [&](int m, int j, int f, float v) {
-    const size_t at = ((size_t)m * K1 + j) * a.Fe + f;
+    const size_t at = ((size_t)m * K1 + j) * 2 * a.Fe + f / 32 * 64 + f % 32;
     const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-    a.hi[at] = hi;
-    a.lo[at] = __float2bfloat16_rn(v - __bfloat162float(hi));
+    a.hid[at] = hi;
+    a.hid[at + 32] = __float2bfloat16_rn(v - __bfloat162float(hi));
   };
+
+  if (cta == 0)
+    for (int i = tid; i < a.Fe / 4; i += kMtThreads)
+      reinterpret_cast<uint4*>(a.hid + (size_t)a.M * K1 * 2 * a.Fe)[i] = make_uint4(0, 0, 0, 0);
 
   // ---- phase 0: the router's rows, then the shared expert's
   {
@@ -382,9 +398,8 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     c.border = n32;
     c.n_exp = a.n_exp;
     c.d = a.d;
-    c.mask = all;
-    c.start(g, t, a.d);
-    stream(c, c, KB1, a.d, cut.U, a.h, a.h, std::false_type{}, [&](int u, int row, int m, float v) {
+    c.start(g, t, a.M);
+    stream(c, c, KB1, a.d, cut.U, a.h, std::false_type{}, [&](int u, int row, int m, float v) {
       if (row >= cut.rows(u) || m >= a.M) return;
       row += cut.row(u);
       if (row < a.n_exp) a.logits[(size_t)m * a.n_exp + row] = v * s.inv[m];
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     if (lane < a.top_k) {
       const float gt = expf(mine - top) / Z;
       s.gate[m][lane] = gt;
-      s.rank[mye][m] = (uint8_t)lane;
+      s.place[mye][m] = (uint8_t)lane;
       atomicOr(&s.mask[mye], 1u << m);
       if (cta == 0) {
         if (a.idx) a.idx[(size_t)m * a.top_k + lane] = mye;
@@ -460,13 +475,21 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     for (int e0 = 0; e0 < a.n_exp; e0 += 32) {
       const bool on = e0 + lane < a.n_exp && s.mask[e0 + lane] != 0;
       const unsigned b = __ballot_sync(0xffffffffu, on);
-      if (on) s.act[n + __popc(b & ((1u << lane) - 1))] = e0 + lane;
+      if (on) s.ex[n + __popc(b & ((1u << lane) - 1))] = MtExpert{e0 + lane, s.mask[e0 + lane]};
       n += __popc(b);
     }
-    if (lane == 0) s.nact = n;
+    if (lane == 0) {
+      s.nact = n;
+      s.ex[n] = MtExpert{a.n_exp, all};
+    }
   }
   __syncthreads();
   const int nact = s.nact;
+  for (int i = tid; i < (nact + 1) * kMtMaxM; i += kMtThreads) {
+    const int x = i / kMtMaxM, m = i % kMtMaxM;
+    s.rank[x][m] = x < nact ? s.place[s.ex[x].e][m] : (uint8_t)a.top_k;
+  }
+  __syncthreads();
 
   // ---- phase 1: the chosen experts' hidden rows
   {
@@ -475,17 +498,18 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     RowsOfH1<NT> c;
     c.cut = cut;
     c.W1 = a.W1;
-    c.act = s.act;
-    c.masks = s.mask;
+    c.ex = s.ex;
     c.F = a.Fe;
     c.d = a.d;
-    c.start(g, t, a.d);
-    stream(c, c, KB1, a.d, cut.U, a.h, a.h, std::false_type{}, [&](int u, int row, int m, float v) {
+    c.g = g;
+    c.t = t;
+    c.start();
+    stream(c, c, KB1, a.d, cut.U, a.h, std::false_type{}, [&](int u, int row, int m, float v) {
       if (row >= cut.rows(u)) return;
       row += cut.row(u);
-      const int x = row / a.Fe, e = s.act[x];
-      if (!(s.mask[e] >> m & 1)) return;
-      const int j = s.rank[e][m];
+      const int x = row / a.Fe;
+      if (!(s.ex[x].mask >> m & 1)) return;
+      const int j = s.rank[x][m];
       store_hidden(m, j, row - x * a.Fe, s.gate[m][j] * gelu(v * s.inv[m]));
     });
   }
@@ -501,17 +525,15 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
       c.W2 = a.W2;
       c.s = &s;
       c.F = a.Fe;
-      c.d = a.d;
-      c.n_exp = a.n_exp;
-      c.nact = nact;
+      c.dF = (int64_t)a.d * a.Fe;
       c.K1 = K1;
-      c.all = all;
+      c.zeros = a.M * K1;
       c.g = g;
       c.t = t;
       c.start();
       return c;
     };
-    stream(cursor(std::false_type{}), cursor(std::true_type{}), KB2, a.Fe, cut.U, a.hi, a.lo, std::true_type{},
+    stream(cursor(std::false_type{}), cursor(std::true_type{}), KB2, a.Fe, cut.U, a.hid, std::true_type{},
            [&](int u, int row, int m, float v) {
              if (row >= cut.rows(u) || m >= a.M) return;
              const int at = m * a.d + cut.row(u) + row;
@@ -521,7 +543,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
 }
 
 struct MtWs {
-  size_t logits, hi, lo, total;
+  size_t logits, hid, total;
 };
 
 MtWs mt_ws(int M, int n_exp, int top_k, int Fe) {
@@ -529,10 +551,8 @@ MtWs mt_ws(int M, int n_exp, int top_k, int Fe) {
   size_t o = 256;  // status word, the barrier's two words
   w.logits = o;
   o = align_up(o + sizeof(float) * M * n_exp, 256);
-  w.hi = o;
-  o = align_up(o + 2 * (size_t)M * (top_k + 1) * Fe, 256);
-  w.lo = o;
-  o = align_up(o + 2 * (size_t)M * (top_k + 1) * Fe, 256);
+  w.hid = o;
+  o = align_up(o + 4 * ((size_t)M * (top_k + 1) + 1) * Fe, 256);
   w.total = o;
   return w;
 }
@@ -600,8 +620,7 @@ extern "C" dg_status dg_moe_tokens(const dg_model* model, int32_t layer, const v
   a.W1 = static_cast<const __nv_bfloat16*>(model->We1) + layer * e1;
   a.W2 = static_cast<const __nv_bfloat16*>(model->We2) + layer * e1;
   a.logits = reinterpret_cast<float*>(base + w.logits);
-  a.hi = reinterpret_cast<__nv_bfloat16*>(base + w.hi);
-  a.lo = reinterpret_cast<__nv_bfloat16*>(base + w.lo);
+  a.hid = reinterpret_cast<__nv_bfloat16*>(base + w.hid);
   a.idx = idx;
   a.gate = gate;
   a.status = reinterpret_cast<int*>(base);
