@@ -35,7 +35,9 @@ constexpr int kMtThreads = kMtWarps * 32;
 constexpr int kMtStages = 2;
 constexpr int kMtRows = 32;     // rows of a unit: two MMA tiles
 constexpr int kMtStage = kMtRows * 128;  // 64 columns of them
-constexpr int kMtRed = 65536;   // shared memory for the warps' parts of units' sums
+// Units of a round: the warps' parts of their sums, 16 and one more for each, have to
+// fit beside the rings.
+constexpr int mt_units(int NT) { return NT == 4 ? 4 : 16; }
 constexpr int kMtMaxM = 32;
 constexpr int kMtMaxExp = 256, kMtMaxK = 16;
 
@@ -43,13 +45,13 @@ struct MtArgs {
   const __nv_bfloat16* h;                  // [M][d]
   __nv_bfloat16* out;                      // [M][d], may be h
   const __nv_bfloat16 *Wr, *W1, *W2;       // [n_exp][d], [n_exp + 1][Fe][d], [n_exp + 1][d][Fe]
-  float* logits;                           // [M][n_exp]
+  float* logits;                           // [M][n_exp], before the product with 1 / rms
   __nv_bfloat16* hid;                      // [M (top_k + 1) + 1][Fe / 32][2][32]: gate GELU(x We1^T), the values as
                                            // bf16 and what that leaves; the last row is zeros
   int* idx;                                // [M][top_k] or null
   float* gate;                             // [M][top_k] or null
   int* status;
-  unsigned* bar;                           // arrivals, rounds
+  unsigned *arrivals, *rounds;             // of the grid's barrier
   int M, d, Fe, n_exp, top_k;
   float eps;
 };
@@ -61,33 +63,37 @@ struct MtExpert {
 
 struct MtShared {
   float inv[kMtMaxM];
+  float squares[kMtMaxM][kMtWarps];
   float gate[kMtMaxM][kMtMaxK];
   unsigned mask[kMtMaxExp];                // tokens of every expert
-  uint8_t place[kMtMaxExp][kMtMaxM];       // their place among the token's experts
+  uint8_t sel[kMtMaxM][kMtMaxK];           // a token's experts in rank order
+  uint16_t pos[kMtMaxExp];                 // an expert's place in ex
   MtExpert ex[kMtMaxExp + 1];              // the experts with tokens, ascending, and the shared one
   uint8_t rank[kMtMaxExp + 1][kMtMaxM];    // and the place of each of their tokens
   int nact;
   int stop;
 };
 
-// All CTAs of the grid are here (the launch is cooperative).  Thread 0 arrives for
-// its CTA; the last one to arrive begins the next round.  Bounded: false, with the
-// status word set, if the others do not come.
-DG_DEV bool grid_barrier(unsigned* bar, int* status, int* stop) {
+// All CTAs of the grid are here (the launch is cooperative).  Thread 0 arrives for its
+// CTA; the last one to arrive begins the next round.  Arrivals and rounds lie in
+// memory lines of their own: a line that is polled while others write to it goes back
+// and forth between the dies (flags of the CTAs side by side took 6 us).  Bounded:
+// false, with the status word set, if the others do not come.
+DG_DEV bool grid_barrier(unsigned* arrivals, unsigned* rounds, int* status, int* stop) {
   __syncthreads();
   if (threadIdx.x == 0) {
     unsigned round;
-    asm volatile("ld.relaxed.gpu.u32 %0, [%1];" : "=r"(round) : "l"(bar + 1) : "memory");
+    asm volatile("ld.relaxed.gpu.u32 %0, [%1];" : "=r"(round) : "l"(rounds) : "memory");
     __threadfence();
-    if (atomicAdd(bar, 1u) == gridDim.x - 1) {
-      *reinterpret_cast<volatile unsigned*>(bar) = 0u;
+    if (atomicAdd(arrivals, 1u) == gridDim.x - 1) {
+      *reinterpret_cast<volatile unsigned*>(arrivals) = 0u;
       __threadfence();
-      atomicAdd(bar + 1, 1u);
+      asm volatile("st.relaxed.gpu.u32 [%0], %1;" ::"l"(rounds), "r"(round + 1) : "memory");
     } else {
       uint64_t t0 = 0;
       for (unsigned i = 0;; ++i) {
         unsigned now;
-        asm volatile("ld.relaxed.gpu.u32 %0, [%1];" : "=r"(now) : "l"(bar + 1) : "memory");
+        asm volatile("ld.relaxed.gpu.u32 %0, [%1];" : "=r"(now) : "l"(rounds) : "memory");
         if (now != round) break;
         if (i % 256 == 255) {
           if (!t0) t0 = globaltimer();
@@ -114,12 +120,10 @@ DG_DEV float gelu(float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678118654
 // Stage of a ring: the lane's pieces of rows g, g + 8, g + 16 and g + 24, halves 0 and
 // 1 of the 64 columns.  Rows at or past `rows` are not copied: what their products
 // hold is not used.
-DG_DEV void load_block(char* slot, const __nv_bfloat16* w, int pitch, int rows, int lane) {
-  const int g = lane / 4, t = lane % 4;
-  const __nv_bfloat16* src = w + g * pitch + 8 * t;
+DG_DEV void load_block(char* slot, const __nv_bfloat16* src, int pitch, int rows, int lane) {
 #pragma unroll
   for (int r = 0; r < kMtRows / 8; ++r)
-    if (g + 8 * r < rows) {
+    if (lane / 4 + 8 * r < rows) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) cp_async16(slot + ((r * 2 + p) * 32 + lane) * 16, src + 8 * r * pitch + 32 * p);
     }
@@ -144,99 +148,11 @@ struct MtCut {
   DG_DEV int rows(int u) const { return min(kMtRows, (u < U0 ? rb : r1) - row(u)); }
 };
 
-// Cursors over the segments of a CTA's units: of the router and the shared expert,
-// of the chosen experts (both multiply the tokens themselves), and of the second
-// matrices.
-template <int NT>
-struct RowsOfH0 {
-  MtCut cut;
-  const __nv_bfloat16 *Wr, *Ws, *w;
-  int border, n_exp, d, u, rows;
-  unsigned tiles;
-  int off[NT];
-  DG_DEV void start(int g, int t, int M) {
-    tiles = (1u << ((M + 7) / 8)) - 1;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) off[n] = min(8 * n + g, M - 1) * d + 8 * t;  // columns past the last token repeat it
-    u = -1;
-    next();
-  }
-  DG_DEV void next() {
-    if (++u >= cut.U) return;
-    const int r = cut.row(u);
-    rows = r < border ? min(cut.rows(u), n_exp - r) : cut.rows(u);
-    w = r < border ? Wr + (int64_t)r * d : Ws + (int64_t)(r - border) * d;
-  }
-};
-
-// A column whose token does not want the expert takes the values of one that does:
-// its sum is not stored.
-template <int NT>
-struct RowsOfH1 {
-  MtCut cut;
-  const __nv_bfloat16 *W1, *w;
-  const MtExpert* ex;
-  int F, d, u, rows, g, t;
-  unsigned tiles;
-  int off[NT];
-  DG_DEV void start() {
-    u = -1;
-    next();
-  }
-  DG_DEV void next() {
-    if (++u >= cut.U) return;
-    const int r = cut.row(u), x = r / F;
-    const MtExpert e = ex[x];
-    rows = cut.rows(u);
-    w = W1 + ((int64_t)e.e * F + r - x * F) * d;
-    tiles = tiles_of(e.mask);
-    const int some = __ffs(e.mask) - 1;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) off[n] = (e.mask >> (8 * n + g) & 1 ? 8 * n + g : some) * d + 8 * t;
-  }
-};
-
-// .. and here, where a column's sum runs over all experts, the row of zeros.
-template <int NT, bool kTokens>
-struct RowsOfHidden {
-  MtCut cut;
-  const __nv_bfloat16 *W2, *w;
-  const MtShared* s;
-  int F, K1, g, t, u, x, rows, zeros;
-  int64_t dF;
-  unsigned tiles;
-  int off[NT];
-  DG_DEV void start() {
-    u = 0;
-    x = -1;
-    next();
-  }
-  DG_DEV void next() {
-    if (++x > s->nact) {
-      x = 0;
-      ++u;
-    }
-    if (u >= cut.U) return;
-    const MtExpert e = s->ex[x];
-    if (!kTokens) {
-      rows = cut.rows(u);
-      w = W2 + (e.e * dF + cut.row(u) * F);
-      return;
-    }
-    tiles = tiles_of(e.mask);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int m = 8 * n + g;
-      off[n] = (e.mask >> m & 1 ? m * K1 + s->rank[x][m] : zeros) * 2 * F + 8 * t;
-    }
-  }
-};
-
 template <int NT>
 __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   extern __shared__ __align__(16) char smem[];
   char* ring = smem + (threadIdx.x / 32) * kMtStages * kMtStage;
-  float* red = reinterpret_cast<float*>(smem + kMtWarps * kMtStages * kMtStage);  // [units][warps][NT * 4][32]
+  float* red = reinterpret_cast<float*>(smem + kMtWarps * kMtStages * kMtStage);  // [warps + units - 1][kVals][32]
   __shared__ MtShared s;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int K1 = a.top_k + 1, KB1 = a.d / 64, KB2 = a.Fe / 64;
@@ -244,136 +160,177 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   const unsigned all = a.M == 32 ? 0xffffffffu : (1u << a.M) - 1;
   if (tid == 0) s.stop = 0;
 
-  // 1 / rms of every token, for this CTA's own use
-  for (int m = warp; m < a.M; m += kMtWarps) {
-    float sum = 0.f;
-    const uint4* src = reinterpret_cast<const uint4*>(a.h + (size_t)m * a.d);
-    for (int i = lane; i < a.d / 8; i += 32) {
-      const uint4 v = src[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = __uint_as_float(w[j] << 16), y = __uint_as_float(w[j] & 0xffff0000u);
-        sum += x * x + y * y;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s.inv[m] = 1.0f / sqrtf(sum / (float)a.d + a.eps);
-  }
-  __syncthreads();
-
-  // A unit (32 rows at most) ends with each warp's part of its sums in `red`; the parts
-  // are added, in order, after kBatch units or the last.  Then thread i * 32 + lane of a
-  // unit's values has (row 16 r + g + 8 (i % 4 / 2), token 8 (i / 4 % NT) + 2 t + i % 2),
-  // r = i / (4 NT).
-  constexpr int kVals = 2 * NT * 4, kBatch = kMtRed / (kMtWarps * kVals * 128);
-  auto add_parts = [&](int u0, int u1, const auto& put) {
-    __syncthreads();
-    for (int v = tid; v < (u1 - u0) * kVals * 32; v += kMtThreads) {
-      const int u = u0 + v / (kVals * 32), at = v % (kVals * 32), i = at / 32;
-      const float* from = red + (u % kBatch) * kMtWarps * kVals * 32 + at;
+  // 1 / rms of every token, for this CTA's own use: 16 / M warps to a token
+  auto norms = [&]() {
+    const int per = a.M >= kMtWarps ? 1 : kMtWarps / a.M, m0 = warp / per, part = warp % per, n8 = a.d / 8;
+    for (int m = m0; m < a.M; m += kMtWarps / per) {
       float sum = 0.f;
+      const uint4* src = reinterpret_cast<const uint4*>(a.h + (size_t)m * a.d);
+      for (int i0 = part * 32 + lane; i0 < n8; i0 += per * 128) {
+        uint4 v[4];
 #pragma unroll
-      for (int w = 0; w < kMtWarps; ++w) sum += from[w * kVals * 32];
-      put(u, 16 * (i / (4 * NT)) + g + 8 * (i % 4 / 2), 8 * (i / 4 % NT) + 2 * t + i % 2, sum);
+        for (int k = 0; k < 4; ++k) v[k] = i0 + k * per * 32 < n8 ? src[i0 + k * per * 32] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = __uint_as_float(w[j] << 16), y = __uint_as_float(w[j] & 0xffff0000u);
+            sum += x * x + y * y;
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) s.squares[m][part] = sum;
     }
     __syncthreads();
+    if (tid < a.M) {
+      float sum = 0.f;
+      for (int p = 0; p < per; ++p) sum += s.squares[tid][p];
+      s.inv[tid] = 1.0f / sqrtf(sum / (float)a.d + a.eps);
+    }
+    // (read after the barriers of the units' sums)
   };
 
-  // The engine of all phases.  A unit's sums run over segments (matrices of `pitch`
-  // columns, KB blocks of 64 each); a warp takes every 16th block, over the borders of
-  // segments and units.  It walks the segments with two cursors: one for the copies
-  // (kMtStages - 1 blocks ahead), one for the tokens' values (a block ahead, in
-  // registers, where they leave room).  A cursor gives the segment's first row w, rows,
-  // unit u, the column tiles with tokens, the lane's offsets of the tokens' values, and
-  // next().
-  auto stream = [&](auto pc, auto bc, int KB, int pitch, int U, const __nv_bfloat16* values, auto pair, const auto& put) {
-    constexpr bool kPair = decltype(pair)::value, kAhead = NT <= 2;
+  // The engine of all phases.  Work comes in rounds of some segments, matrices of KB
+  // blocks of 64 columns and up to 32 rows; a round's blocks, in that order, are dealt to
+  // the warps in equal shares, so a warp has parts of one segment or of several: a task
+  // each.  Its sums stay in registers over the tasks of a unit (all of the round with
+  // kOne, else one segment) and go to `red` at its end; the parts of a unit are added
+  // up, in order, when the round ends, and given to put(round, unit, row, token, sum).
+  // The copies run ahead over all borders, the tokens' values only within a task (a block
+  // ahead, where the registers leave room).
+  constexpr int kVals = 2 * NT * 4;  // of a unit, in a lane
+  auto stream = [&](int F, const auto& segments, int KB, int pitch, auto one, const auto& seg_w, const auto& seg_b,
+                    const __nv_bfloat16* values, auto pair, const auto& begun, const auto& put) {
+    constexpr bool kOne = decltype(one)::value, kPair = decltype(pair)::value, kAhead = NT <= 2;
     constexpr int kB = kPair ? 2 : 1;
-    int pk = warp, bk = warp, pslot = 0;
-    auto settle = [&](auto& c, int& k) {
-      while (k >= KB && c.u < U) {
-        k -= KB;
-        c.next();
-      }
+    // of n blocks; where there are fewer blocks than warps, one each for the first warps
+    auto share = [&](int n, int* first, int* end) {
+      const int W = min(n, kMtWarps);
+      *first = warp < W ? n * warp / W : 0;
+      *end = warp < W ? n * (warp + 1) / W : 0;
     };
+    int pf = -1, pi = 0, pe = 0, pn = 0, prows = 0, pslot = 0;
+    const __nv_bfloat16* pw = nullptr;
     auto issue = [&]() {
-      if (pc.u < U) {
-        load_block(ring + pslot, pc.w + pk * 64, pitch, pc.rows, lane);
-        pk += kMtWarps;
-        settle(pc, pk);
+      while (pn == 0 && pf < F) {  // the next task
+        if (pi == pe) {
+          if (++pf == F) break;
+          const int total = segments(pf) * KB;
+          share(total, &pi, &pe);
+          continue;
+        }
+        const int seg = pi / KB, kb = pi - seg * KB;
+        seg_w(pf, seg, &pw, &prows);
+        pw += g * pitch + kb * 64 + 8 * t;
+        pn = min(KB - kb, pe - pi);
+        pi += pn;
+      }
+      if (pn > 0) {
+        load_block(ring + pslot, pw, pitch, prows, lane);
+        pw += 64;
+        --pn;
       }
       cp_async_commit();
       pslot = pslot + kMtStage == kMtStages * kMtStage ? 0 : pslot + kMtStage;
     };
-    uint4 b[NT][2][kB];
-    auto load_b = [&](unsigned tiles, const int (&off)[NT], int k) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (NT == 1 || (tiles >> n & 1)) {
-          const __nv_bfloat16* from = values + off[n] + k * 64 * kB;
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int q = 0; q < kB; ++q) b[n][p][q] = *reinterpret_cast<const uint4*>(from + (p * kB + q) * 32);
-        }
-    };
-    settle(pc, pk);
-    settle(bc, bk);
 #pragma unroll 1
     for (int s0 = 0; s0 < kMtStages - 1; ++s0) issue();
-    float acc[2][NT][4] = {};
-    int u = 0, done = 0, slot = 0;
-    auto flush_to = [&](int to) {  // units u .. to - 1 have all that this warp adds to them
+    begun();
+    int slot = 0;
 #pragma unroll 1
-      for (; u < to; ++u) {
-        float* part = red + ((u % kBatch) * kMtWarps + warp) * kVals * 32 + lane;
+    for (int f = 0; f < F; ++f) {
+      const int segs = segments(f), total = segs * KB;
+      float acc[2][NT][4] = {};
+      auto leave = [&](int unit) {
+        float* part = red + (warp + unit) * kVals * 32 + lane;
 #pragma unroll
         for (int i = 0; i < kVals; ++i) {
           part[i * 32] = acc[i / (4 * NT)][i / 4 % NT][i % 4];
           acc[i / (4 * NT)][i / 4 % NT][i % 4] = 0.f;
         }
-        if (u + 1 == U || (u + 1) % kBatch == 0) {
-          add_parts(done, u + 1, put);
-          done = u + 1;
-        }
-      }
-    };
-    flush_to(min(bc.u, U));
-    if (kAhead && bc.u < U) load_b(bc.tiles, bc.off, bk);
+      };
+      int i, end;
+      share(total, &i, &end);
 #pragma unroll 1
-    while (bc.u < U) {
-      issue();
-      cp_async_wait<kMtStages - 1>();
-      const unsigned tiles = bc.tiles;
-      if (!kAhead) load_b(tiles, bc.off, bk);
-      bk += kMtWarps;
-      settle(bc, bk);
-      const char* from = ring + slot + lane * 16;
-      slot = slot + kMtStage == kMtStages * kMtStage ? 0 : slot + kMtStage;
+      while (i < end) {
+        const int seg = i / KB, kb = i - seg * KB;
+        int off[NT], nb = min(KB - kb, end - i);
+        unsigned tiles;
+        i += nb;
+        seg_b(f, seg, off, &tiles);
+        const __nv_bfloat16* from[NT];
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint4 v = *reinterpret_cast<const uint4*>(from + (4 * r + p) * 512);
-          const uint4 w = *reinterpret_cast<const uint4*>(from + (4 * r + 2 + p) * 512);
-          const uint32_t A0[4] = {v.x, w.x, v.y, w.y}, A1[4] = {v.z, w.z, v.w, w.w};
+        for (int n = 0; n < NT; ++n) from[n] = values + off[n] + kb * 64 * kB;
+        uint4 b[NT][2][kB];
+        auto load_b = [&]() {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
             if (NT == 1 || (tiles >> n & 1)) {
 #pragma unroll
-              for (int q = 0; q < kB; ++q) {
-                mma_bf16_16816(acc[r][n], A0, b[n][p][q].x, b[n][p][q].y);
-                mma_bf16_16816(acc[r][n], A1, b[n][p][q].z, b[n][p][q].w);
-              }
+              for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int q = 0; q < kB; ++q) b[n][p][q] = *reinterpret_cast<const uint4*>(from[n] + (p * kB + q) * 32);
+              from[n] += 64 * kB;
             }
+        };
+        if (kAhead) load_b();
+#pragma unroll 1
+        for (; nb > 0; --nb) {
+          issue();
+          cp_async_wait<kMtStages - 1>();
+          if (!kAhead) load_b();
+          const char* at = ring + slot + lane * 16;
+          slot = slot + kMtStage == kMtStages * kMtStage ? 0 : slot + kMtStage;
+          uint32_t A[2][2][2][4];
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint4 v = *reinterpret_cast<const uint4*>(at + (4 * r + p) * 512);
+              const uint4 w = *reinterpret_cast<const uint4*>(at + (4 * r + 2 + p) * 512);
+              A[p][r][0][0] = v.x, A[p][r][0][1] = w.x, A[p][r][0][2] = v.y, A[p][r][0][3] = w.y;
+              A[p][r][1][0] = v.z, A[p][r][1][1] = w.z, A[p][r][1][2] = v.w, A[p][r][1][3] = w.w;
+            }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (NT == 1 || (tiles >> n & 1)) {
+#pragma unroll
+              for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int q = 0; q < kB; ++q)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r) {
+                    mma_bf16_16816(acc[r][n], A[p][r][0], b[n][p][q].x, b[n][p][q].y);
+                    mma_bf16_16816(acc[r][n], A[p][r][1], b[n][p][q].z, b[n][p][q].w);
+                  }
+            }
+          if (kAhead && nb > 1) load_b();
         }
-      if (kAhead && bc.u < U) load_b(bc.tiles, bc.off, bk);
-      flush_to(min(bc.u, U));
+        if (!kOne) leave(seg);
+      }
+      if (kOne) leave(0);
+      const int W = min(total, kMtWarps);
+      __syncthreads();
+      // thread i * 32 + lane of a unit's values has (row 16 r + g + 8 (i % 4 / 2), token
+      // 8 (i / 4 % NT) + 2 t + i % 2), r = i / (4 NT); its parts are those of the warps
+      // from the owner of its first block to that of its last
+      for (int v = tid; v < (kOne ? 1 : segs) * kVals * 32; v += kMtThreads) {
+        const int u = v / (kVals * 32), i = v / 32 % kVals;
+        const int w0 = kOne ? 0 : ((u * KB + 1) * W - 1) / total;
+        const int w1 = kOne ? W - 1 : ((u + 1) * KB * W - 1) / total;
+        const float* src = red + (u * kVals + i) * 32 + lane;
+        float sum = 0.f;
+        for (int w = w0; w <= w1; ++w) sum += src[w * kVals * 32];
+        put(f, u, 16 * (i / (4 * NT)) + g + 8 * (i % 4 / 2), 8 * (i / 4 % NT) + 2 * t + i % 2, sum);
+      }
+      __syncthreads();
     }
     cp_async_wait<0>();
   };
+  constexpr int kUnits = mt_units(NT);  // of a round
 
   auto range = [&](int rows, int c) { return (int)((int64_t)rows * c / ctas); };
   auto store_hidden = [&](int m, int j, int f, float v) {
@@ -391,22 +348,26 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   {
     const int n32 = (a.n_exp + kMtRows - 1) / kMtRows * kMtRows, R = n32 + a.Fe;
     const MtCut cut(range(R, cta), range(R, cta + 1), n32);
-    RowsOfH0<NT> c;
-    c.cut = cut;
-    c.Wr = a.Wr;
-    c.Ws = a.W1 + (int64_t)a.n_exp * a.Fe * a.d;
-    c.border = n32;
-    c.n_exp = a.n_exp;
-    c.d = a.d;
-    c.start(g, t, a.M);
-    stream(c, c, KB1, a.d, cut.U, a.h, std::false_type{}, [&](int u, int row, int m, float v) {
+    stream((cut.U + kUnits - 1) / kUnits, [&](int f) { return min(kUnits, cut.U - f * kUnits); }, KB1, a.d, std::false_type{},
+           [&](int f, int u, const __nv_bfloat16** w, int* rows) {
+             const int r = cut.row(u + f * kUnits);
+             *rows = r < n32 ? min(cut.rows(u + f * kUnits), a.n_exp - r) : cut.rows(u + f * kUnits);
+             *w = r < n32 ? a.Wr + (int64_t)r * a.d : a.W1 + ((int64_t)a.n_exp * a.Fe + r - n32) * a.d;
+           },
+           [&](int, int, int* off, unsigned* tiles) {
+             *tiles = (1u << ((a.M + 7) / 8)) - 1;
+#pragma unroll
+             for (int n = 0; n < NT; ++n) off[n] = min(8 * n + g, a.M - 1) * a.d + 8 * t;  // columns past the last token repeat it
+           },
+           a.h, std::false_type{}, norms, [&](int f, int u, int row, int m, float v) {
+      u += f * kUnits;
       if (row >= cut.rows(u) || m >= a.M) return;
       row += cut.row(u);
-      if (row < a.n_exp) a.logits[(size_t)m * a.n_exp + row] = v * s.inv[m];
+      if (row < a.n_exp) a.logits[(size_t)m * a.n_exp + row] = v;
       else if (row >= n32) store_hidden(m, a.top_k, row - n32, gelu(v * s.inv[m]));
     });
   }
-  if (!grid_barrier(a.bar, a.status, &s.stop)) return;
+  if (!grid_barrier(a.arrivals, a.rounds, a.status, &s.stop)) return;
 
   // ---- the routing: one warp for each token, a lane holding experts lane, lane + 32, ..
   for (int e = tid; e < kMtMaxExp; e += kMtThreads) s.mask[e] = 0;
@@ -415,42 +376,38 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     float l[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) l[j] = lane + 32 * j < a.n_exp ? __ldcg(a.logits + (size_t)m * a.n_exp + lane + 32 * j) : 0.f;
-    uint32_t taken = 0;
+    // keys in the order of the values; 0: no expert, taken, or NaN
+    unsigned key[8];
+    bool wrong = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      l[j] *= s.inv[m];
+      const bool there = lane + 32 * j < a.n_exp;
+      wrong |= there && !(fabsf(l[j]) <= FLT_MAX);
+      key[j] = there && l[j] == l[j] ? float_key(l[j] == 0.f ? 0.f : l[j]) : 0u;
+    }
+    if (__any_sync(0xffffffffu, wrong) && lane == 0 && cta == 0) atomicExch(a.status, kStatusValue);
     float top = 0.f, Z = 0.f, mine = 0.f;
     int mye = 0;
+    unsigned taken = 0;
 #pragma unroll 1
     for (int k = 0; k < a.top_k; ++k) {
-      float bv = -FLT_MAX;
-      int be = INT_MAX;
+      unsigned best = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = lane + 32 * j;
-        if (e < a.n_exp && !((taken >> j) & 1u) && (l[j] > bv || (l[j] == bv && e < be))) {
-          bv = l[j];
-          be = e;
-        }
-      }
+      for (int j = 0; j < 8; ++j) best = max(best, key[j]);
+      best = __reduce_max_sync(0xffffffffu, best);
+      int first = INT_MAX;  // the lowest one with that value (of value 0: not taken)
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-        const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-        if (ov > bv || (ov == bv && oe < be)) {
-          bv = ov;
-          be = oe;
-        }
-      }
-      if (be >= a.n_exp || !(bv <= FLT_MAX)) {  // non-finite logits: recorded
-        if (lane == 0 && cta == 0) atomicExch(a.status, kStatusValue);
-        if (be >= a.n_exp) {  // none is left that compares: the lowest one not taken
-          bv = -FLT_MAX;
-          int first = INT_MAX;
+      for (int j = 7; j >= 0; --j)
+        if (key[j] == best && !(taken >> j & 1) && lane + 32 * j < a.n_exp) first = lane + 32 * j;
+      const int be = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
+      if ((be & 31) == lane) {
+        taken |= 1u << (be >> 5);
 #pragma unroll
-          for (int j = 7; j >= 0; --j)
-            if (lane + 32 * j < a.n_exp && !((taken >> j) & 1u)) first = lane + 32 * j;
-          be = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
-        }
+        for (int j = 0; j < 8; ++j)
+          if (j == be >> 5) key[j] = 0u;
       }
-      if ((be & 31) == lane) taken |= 1u << (be >> 5);
+      const float bv = best ? key_float(best) : -FLT_MAX;
       if (k == 0) top = bv;
       Z += expf(bv - top);
       if (lane == k) {
@@ -461,7 +418,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     if (lane < a.top_k) {
       const float gt = expf(mine - top) / Z;
       s.gate[m][lane] = gt;
-      s.place[mye][m] = (uint8_t)lane;
+      s.sel[m][lane] = (uint8_t)mye;
       atomicOr(&s.mask[mye], 1u << m);
       if (cta == 0) {
         if (a.idx) a.idx[(size_t)m * a.top_k + lane] = mye;
@@ -475,7 +432,11 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     for (int e0 = 0; e0 < a.n_exp; e0 += 32) {
       const bool on = e0 + lane < a.n_exp && s.mask[e0 + lane] != 0;
       const unsigned b = __ballot_sync(0xffffffffu, on);
-      if (on) s.ex[n + __popc(b & ((1u << lane) - 1))] = MtExpert{e0 + lane, s.mask[e0 + lane]};
+      if (on) {
+        const int x = n + __popc(b & ((1u << lane) - 1));
+        s.ex[x] = MtExpert{e0 + lane, s.mask[e0 + lane]};
+        s.pos[e0 + lane] = (uint16_t)x;
+      }
       n += __popc(b);
     }
     if (lane == 0) {
@@ -485,9 +446,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   }
   __syncthreads();
   const int nact = s.nact;
-  for (int i = tid; i < (nact + 1) * kMtMaxM; i += kMtThreads) {
-    const int x = i / kMtMaxM, m = i % kMtMaxM;
-    s.rank[x][m] = x < nact ? s.place[s.ex[x].e][m] : (uint8_t)a.top_k;
+  for (int i = tid; i < a.M * K1; i += kMtThreads) {
+    const int m = i / K1, j = i - m * K1;
+    s.rank[j < a.top_k ? s.pos[s.sel[m][j]] : nact][m] = (uint8_t)j;
   }
   __syncthreads();
 
@@ -495,16 +456,22 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   {
     const int R = nact * a.Fe, r0 = range(R, cta), r1 = range(R, cta + 1);
     const MtCut cut(r0, r1, min(r1, r0 / a.Fe * a.Fe + a.Fe));
-    RowsOfH1<NT> c;
-    c.cut = cut;
-    c.W1 = a.W1;
-    c.ex = s.ex;
-    c.F = a.Fe;
-    c.d = a.d;
-    c.g = g;
-    c.t = t;
-    c.start();
-    stream(c, c, KB1, a.d, cut.U, a.h, std::false_type{}, [&](int u, int row, int m, float v) {
+    stream((cut.U + kUnits - 1) / kUnits, [&](int f) { return min(kUnits, cut.U - f * kUnits); }, KB1, a.d, std::false_type{},
+           [&](int f, int u, const __nv_bfloat16** w, int* rows) {
+             const int r = cut.row(u + f * kUnits), x = r / a.Fe;
+             *rows = cut.rows(u + f * kUnits);
+             *w = a.W1 + ((int64_t)s.ex[x].e * a.Fe + r - x * a.Fe) * a.d;
+           },
+           [&](int f, int u, int* off, unsigned* tiles) {
+             const unsigned mask = s.ex[cut.row(u + f * kUnits) / a.Fe].mask;
+             const int some = __ffs(mask) - 1;
+             *tiles = tiles_of(mask);
+#pragma unroll
+             for (int n = 0; n < NT; ++n)  // a token that does not want the expert: another's values, not stored
+               off[n] = (mask >> (8 * n + g) & 1 ? 8 * n + g : some) * a.d + 8 * t;
+           },
+           a.h, std::false_type{}, [] {}, [&](int f, int u, int row, int m, float v) {
+      u += f * kUnits;
       if (row >= cut.rows(u)) return;
       row += cut.row(u);
       const int x = row / a.Fe;
@@ -513,28 +480,28 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
       store_hidden(m, j, row - x * a.Fe, s.gate[m][j] * gelu(v * s.inv[m]));
     });
   }
-  if (!grid_barrier(a.bar, a.status, &s.stop)) return;
+  if (!grid_barrier(a.arrivals, a.rounds, a.status, &s.stop)) return;
 
   // ---- phase 2: output columns, their sums over the experts' hidden values
   {
     const int r0 = range(a.d, cta), r1 = range(a.d, cta + 1);
     const MtCut cut(r0, r1, r1);
-    auto cursor = [&](auto tokens) {
-      RowsOfHidden<NT, decltype(tokens)::value> c;
-      c.cut = cut;
-      c.W2 = a.W2;
-      c.s = &s;
-      c.F = a.Fe;
-      c.dF = (int64_t)a.d * a.Fe;
-      c.K1 = K1;
-      c.zeros = a.M * K1;
-      c.g = g;
-      c.t = t;
-      c.start();
-      return c;
-    };
-    stream(cursor(std::false_type{}), cursor(std::true_type{}), KB2, a.Fe, cut.U, a.hid, std::true_type{},
-           [&](int u, int row, int m, float v) {
+    stream(cut.U, [&](int) { return nact + 1; }, KB2, a.Fe, std::true_type{},
+           [&](int f, int x, const __nv_bfloat16** w, int* rows) {
+             *rows = cut.rows(f);
+             *w = a.W2 + ((int64_t)s.ex[x].e * a.d + cut.row(f)) * a.Fe;
+           },
+           [&](int, int x, int* off, unsigned* tiles) {
+             const unsigned mask = s.ex[x].mask;
+             *tiles = tiles_of(mask);
+#pragma unroll
+             for (int n = 0; n < NT; ++n) {  // a token that does not want the expert: the row of zeros
+               const int m = 8 * n + g;
+               off[n] = (mask >> m & 1 ? m * K1 + s.rank[x][m] : a.M * K1) * 2 * a.Fe + 8 * t;
+             }
+           },
+           a.hid, std::true_type{}, [] {},
+           [&](int u, int, int row, int m, float v) {
              if (row >= cut.rows(u) || m >= a.M) return;
              const int at = m * a.d + cut.row(u) + row;
              a.out[at] = __float2bfloat16_rn(__bfloat162float(a.h[at]) + v);
@@ -548,7 +515,7 @@ struct MtWs {
 
 MtWs mt_ws(int M, int n_exp, int top_k, int Fe) {
   MtWs w;
-  size_t o = 256;  // status word, the barrier's two words
+  size_t o = 768;  // status word, the barrier's two lines
   w.logits = o;
   o = align_up(o + sizeof(float) * M * n_exp, 256);
   w.hid = o;
@@ -569,7 +536,7 @@ dg_status check_sizes(const dg_model* m, int32_t M) {
 
 template <int NT>
 cudaError_t launch(const MtArgs& a, int sms, cudaStream_t st) {
-  const int smem = kMtWarps * kMtStages * kMtStage + kMtRed;
+  const int smem = kMtWarps * kMtStages * kMtStage + (kMtWarps + mt_units(NT) - 1) * 2 * NT * 4 * 32 * (int)sizeof(float);
   cudaError_t e = set_smem_once<moe_tokens_kernel<NT>>(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -624,7 +591,8 @@ extern "C" dg_status dg_moe_tokens(const dg_model* model, int32_t layer, const v
   a.idx = idx;
   a.gate = gate;
   a.status = reinterpret_cast<int*>(base);
-  a.bar = reinterpret_cast<unsigned*>(base + 64);
+  a.arrivals = reinterpret_cast<unsigned*>(base + 256);
+  a.rounds = reinterpret_cast<unsigned*>(base + 512);
   a.M = M;
   a.d = D.d;
   a.Fe = D.Fe;
