@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
       for (int p = 0; p < per; ++p) sum += s.squares[tid][p];
       s.inv[tid] = 1.0f / sqrtf(sum / (float)a.d + a.eps);
     }
-    // (read after the barriers of the units' sums)
+    // (read after the barrier before the units' sums)
   };
 
   // The engine of all phases.  Work comes in rounds of some segments, matrices of KB
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   // ahead, where the registers leave room).
   constexpr int kVals = 2 * NT * 4;  // of a unit, in a lane
   auto stream = [&](int F, const auto& segments, int KB, int pitch, auto one, const auto& seg_w, const auto& seg_b,
-                    const __nv_bfloat16* values, auto pair, const auto& begun, const auto& put) {
+                    const __nv_bfloat16* values, auto pair, const auto& meanwhile, const auto& put) {
     constexpr bool kOne = decltype(one)::value, kPair = decltype(pair)::value, kAhead = NT <= 2;
     constexpr int kB = kPair ? 2 : 1;
     // of n blocks; where there are fewer blocks than warps, one each for the first warps
@@ -237,8 +237,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
       pslot = pslot + kMtStage == kMtStages * kMtStage ? 0 : pslot + kMtStage;
     };
 #pragma unroll 1
-    for (int s0 = 0; s0 < kMtStages - 1; ++s0) issue();
-    begun();
+    for (int s0 = 0; s0 < kMtStages; ++s0) issue();
     int slot = 0;
 #pragma unroll 1
     for (int f = 0; f < F; ++f) {
@@ -279,7 +278,6 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
         if (kAhead) load_b();
 #pragma unroll 1
         for (; nb > 0; --nb) {
-          issue();
           cp_async_wait<kMtStages - 1>();
           if (!kAhead) load_b();
           const char* at = ring + slot + lane * 16;
@@ -294,6 +292,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
               A[p][r][0][0] = v.x, A[p][r][0][1] = w.x, A[p][r][0][2] = v.y, A[p][r][0][3] = w.y;
               A[p][r][1][0] = v.z, A[p][r][1][1] = w.z, A[p][r][1][2] = v.w, A[p][r][1][3] = w.w;
             }
+          issue();  // into the slot just read
 #pragma unroll
           for (int n = 0; n < NT; ++n)
             if (NT == 1 || (tiles >> n & 1)) {
@@ -312,6 +311,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
         if (!kOne) leave(seg);
       }
       if (kOne) leave(0);
+      if (f == 0) meanwhile();
       const int W = min(total, kMtWarps);
       __syncthreads();
       // thread i * 32 + lane of a unit's values has (row 16 r + g + 8 (i % 4 / 2), token
@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
       }
       __syncthreads();
     }
+    if (F == 0) meanwhile();
     cp_async_wait<0>();
   };
   constexpr int kUnits = mt_units(NT);  // of a round
