@@ -13,20 +13,23 @@
 // them in, and a border between tokens is where the exact arithmetic has it but for
 // the weights' own 2^-28.
 //
-// A cluster of CTAs takes a row: each holds a slice in shared memory, read once from
-// global memory (what bounds the call), and the passes over it are on chip.  A cut is
-// searched in three steps:
-//   a sample of the slices, in a histogram linear in the value below the maximum, gives
-//     a bracket of values in which the border most likely lies
-//   one pass over all values: what lies above the bracket is summed in registers, what
-//     lies in it goes into 2048 bins of a second histogram (atomics for a few per cent
-//     of the values; all of them through atomics took three times as long)
-//   the values of the bin that holds the border, a few, are compared with one another
-// Where the border is not in the bracket, or too many different values share its bin,
-// histograms of all values, refined over the bits of the values, find it instead.
+// A cluster of CTAs takes a row, a slice each; a warp a run of its CTA's slice.  What
+// bounds the call is reading the logits; they are small enough, for the rows under way,
+// to be read again from L2.  The passes:
+//   the largest value
+//   where a cut is asked for, a sample: its histogram, linear in the value below the
+//     maximum, gives a bracket of values in which the border most likely lies
+//   all values, with their weights: what lies above the bracket is summed in registers,
+//     what lies in it (some thousand values) goes into lists in index order
+// Then one CTA, the leader, has the lists and the runs' sums in its shared memory and
+// finishes alone: it finds the border among the listed values, adds up what is kept of
+// each run, and goes through the run in which the token lies.
+// Where the border is not in the bracket, the exact sums say how far off the sample was
+// and the pass is taken again; where that fails too, or too many values lie in the
+// bracket, histograms of all values, refined over the bits of the values, find it.
+#include <atomic>
 #include <cfloat>
 #include <climits>
-#include <atomic>
 #include <cmath>
 
 #include "dg_common.cuh"
@@ -39,14 +42,17 @@ constexpr int kSpThreads = 512;
 constexpr int kSpWarps = kSpThreads / 32;
 constexpr int kSpBins = 2048;
 constexpr int kSpMaxV = 1 << 20;
-constexpr int kSpList = 512;                  // keys of a bin that are compared with one another
+constexpr int kSpKeys = 512;                  // keys of a bin that are compared with one another
+constexpr int kSpSample = 8192;               // longer vocabularies are sampled first
 constexpr int kSpSide = 512;                  // sampled values on either side of a bracket
+constexpr int kSpTries = 3;
 constexpr int kSpMaxCluster = 16;
+constexpr int kSpRuns = kSpMaxCluster * kSpWarps;
+constexpr int kSpCap = 640;                   // listed values of a run, over the CTAs of a row
 constexpr int kSpTable = 128;                 // 2^(j / 128)
 constexpr int kSpTop = 43;                    // a weight of the row's scale is 2^43: 2^20 of them stay below 2^63
 constexpr float kSpUnit = 32.0f;              // bins of the first histogram to a factor of two in weight
-constexpr int kSpSample = 16384;              // longer vocabularies are sampled first
-constexpr int kSpHeld = 43008;                // most values of a slice held in shared memory
+constexpr float kNone = -INFINITY;            // behind the end, or banned
 
 struct SpArgs {
   const void* logits;  // fp32 or bf16 [R][ld]
@@ -55,7 +61,7 @@ struct SpArgs {
   int32_t *token, *kept;
   float* logprob;
   int64_t ld;
-  int R, V, slice, held, bf16;
+  int R, V, slice, run4, step, bf16;
   float temperature_all, top_p_all, min_p_all;
   int top_k_all;
 };
@@ -79,24 +85,36 @@ struct SpScale {
   int nref;        // weights are relative to 2^nref, above the largest
 };
 
-struct SpShared {
+// The cut of a leading run: values above `key` are in, and of those equal to it the
+// first `ties` by index.
+struct SpCut {
+  unsigned key;
+  unsigned long long ties;
+};
+
+struct alignas(16) SpShared {
   unsigned count[kSpBins];
   unsigned lo[kSpBins], hi[kSpBins];      // masses, 64 bits in two words
-  unsigned long long sum[kSpBins];        // the bins, summed over the cluster; then the cluster's list, below
+  unsigned long long sum[kSpBins];        // the bins, summed over the cluster
   uint2 pow2[kSpTable];                   // the table entry as an integer and as a float
-  SpBoard board[5];
+  SpBoard board[4];
   unsigned long long warp_a[kSpWarps], warp_b[kSpWarps];
-  unsigned list[kSpList];                 // this CTA's keys in the border's bin
-  unsigned long long found_total;
-  unsigned listed;
-  unsigned long long found_above;
+  // the leader's: of every run of the row, the mass and the number of values above the
+  // bracket (or of all that is kept), how many are equal to the cut, how many listed
+  unsigned long long run_mass[kSpRuns];
+  unsigned run_count[kSpRuns], run_equal[kSpRuns], run_listed[kSpRuns];
+  unsigned keys[kSpKeys];                 // the border's bin
+  unsigned nkeys, key_lo, key_hi;
+  unsigned long long found_above, found_total;
   int found_bin;
-  unsigned cut_key;
-  unsigned long long cut_ties;
+  SpCut cut;
   float bracket_hi, bracket_lo;
   SpScale scale;
   unsigned floor_key;
 };
+
+static_assert(sizeof(SpShared) % 16 == 0, "the lists lie behind it");
+constexpr int kSpSmem = (int)sizeof(SpShared) + kSpWarps * kSpCap * 6;
 
 DG_DEV unsigned ld_cluster_u32(uint32_t a) {
   unsigned v;
@@ -105,6 +123,9 @@ DG_DEV unsigned ld_cluster_u32(uint32_t a) {
 }
 DG_DEV void st_cluster_u32(uint32_t a, unsigned v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+DG_DEV void st_cluster_u16(uint32_t a, uint16_t v) {
+  asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory");
 }
 DG_DEV void st_cluster_u64(uint32_t a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
@@ -171,23 +192,18 @@ DG_DEV unsigned long long fraction(float f) { return (unsigned long long)(f * 18
 // The order of values; -0 and 0 are equal.
 DG_DEV unsigned key_of(float v) { return float_key(v == 0.f ? 0.f : v); }
 
-// The cut of a leading run: values above `key` are in, and of those equal to it the
-// first `ties` by index.
-struct SpCut {
-  unsigned key;
-  unsigned long long ties;
-};
-
 __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTables tables) {
-  extern __shared__ __align__(16) float held[];
-  __shared__ SpShared s;
+  extern __shared__ __align__(16) char smem[];
+  SpShared& s = *reinterpret_cast<SpShared*>(smem);
+  // [run][cap] listed values, then their places in their runs: of the CTA's own runs,
+  // in the leader of all
+  float* list_v = reinterpret_cast<float*>(smem + sizeof(SpShared));
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const uint32_t ctas = gridDim.y, rank = cluster_ctarank();
   const int row = blockIdx.x;
+  const int cap = kSpCap / (int)ctas, runs = (int)ctas * kSpWarps;
+  uint16_t* list_at = reinterpret_cast<uint16_t*>(list_v + kSpWarps * kSpCap);
   const char* src = static_cast<const char*>(a.logits) + (size_t)row * a.ld * (a.bf16 ? 2 : 4);
-  const int base = (int)rank * a.slice;
-  const int n = max(0, min(a.slice, a.V - base));  // this CTA's values
-  const int n4 = (n + 3) / 4;
   pdl_wait();
   for (int i = tid; i < kSpTable; i += kSpThreads) s.pow2[i] = make_uint2(tables.t[i], __float_as_uint((float)tables.t[i]));
 
@@ -197,69 +213,74 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   const float u = a.u[row];
   bool bad = !(T >= 0.f && T <= FLT_MAX) || !(top_p >= 0.f) || !(min_p >= 0.f && min_p <= 1.f) || top_k < 0 || !(u >= 0.f && u < 1.f);
 
-  const float kNone = __uint_as_float(0xff800000u);  // -inf: behind the end, or banned
-  auto load1 = [&](int i) {
-    if (i >= n) return kNone;
-    return a.bf16 ? __uint_as_float((unsigned)reinterpret_cast<const uint16_t*>(src)[base + i] << 16)
-                  : __ldcs(reinterpret_cast<const float*>(src) + base + i);
-  };
-  // four values from i = 4 j on, from global memory
-  const bool vec = (reinterpret_cast<uintptr_t>(src) + (size_t)base * (a.bf16 ? 2 : 4)) % (a.bf16 ? 8 : 16) == 0;
-  auto load4 = [&](int j) {
-    if (vec && 4 * j + 4 <= n) {
-      if (!a.bf16) return __ldcs(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(src) + base) + j);
-      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(src) + base) + j);
+  // four values from i on (a multiple of 4), -inf from `end` on
+  const bool vec = reinterpret_cast<uintptr_t>(src) % (a.bf16 ? 8 : 16) == 0;
+  auto load4 = [&](int i, int end) {
+    if (vec && i + 4 <= end) {
+      if (!a.bf16) return __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(src) + i));
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(src) + i));
       return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                          __uint_as_float(w.y & 0xffff0000u));
     }
-    return make_float4(load1(4 * j), load1(4 * j + 1), load1(4 * j + 2), load1(4 * j + 3));
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = i + e >= end ? kNone
+             : a.bf16     ? __uint_as_float((unsigned)__ldg(reinterpret_cast<const uint16_t*>(src) + i + e) << 16)
+                          : __ldg(reinterpret_cast<const float*>(src) + i + e);
+    return make_float4(v[0], v[1], v[2], v[3]);
   };
-  const int held4 = a.held / 4;
-  auto value4 = [&](int j) { return j < held4 ? reinterpret_cast<const float4*>(held)[j] : load4(j); };
+  // this warp's run: values [first, last)
+  auto run_first = [&](int r) { return min(a.V, r / kSpWarps * a.slice + r % kSpWarps * a.run4 * 4); };
+  auto run_last = [&](int r) { return min(min(a.V, (r / kSpWarps + 1) * a.slice), run_first(r) + a.run4 * 4); };
+  const int mine = (int)rank * kSpWarps + warp, first = run_first(mine), last = run_last(mine);
 
-  // ---- the slice, its largest value, its finite ones
-  float top = kNone, low = __uint_as_float(0x7f800000u);
+  // ---- the largest value, the lowest, the number of finite ones
+  float top = kNone, low = INFINITY;
   bool fine = true;
   unsigned fin = 0;
 #pragma unroll 4
-  for (int j = tid; j < n4; j += kSpThreads) {
-    const float4 v = load4(j);
-    if (j < held4) reinterpret_cast<float4*>(held)[j] = v;
+  for (int i = first + 4 * lane; i < last; i += 128) {
+    const float4 v = load4(i, last);
     const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       top = fmaxf(top, w[e]);
-      if (w[e] >= -FLT_MAX) low = fminf(low, w[e]);
       fine = fine && w[e] <= FLT_MAX;
-      fin += w[e] >= -FLT_MAX;
+      if (w[e] >= -FLT_MAX) {
+        low = fminf(low, w[e]);
+        ++fin;
+      }
     }
   }
   unsigned mkey = __reduce_max_sync(0xffffffffu, top >= -FLT_MAX ? key_of(top) : 0u);
+  unsigned lowest = __reduce_min_sync(0xffffffffu, low <= FLT_MAX ? key_of(low) : 0xffffffffu);
   const unsigned wrong = __any_sync(0xffffffffu, !fine) ? 1u : 0u;
   fin = __reduce_add_sync(0xffffffffu, fin);
-  unsigned lowest = __reduce_min_sync(0xffffffffu, low <= FLT_MAX ? key_of(low) : 0xffffffffu);
   if (lane == 0) {
     s.warp_a[warp] = ((unsigned long long)wrong << 32) | mkey;
     s.warp_b[warp] = ((unsigned long long)lowest << 32) | fin;
   }
   cluster_sync();  // (every CTA of the cluster runs before another writes to it)
-  unsigned long long mw = 0, fin_here = 0;
+  unsigned long long mw = 0, finite = 0;
   for (int w = 0; w < kSpWarps; ++w) {
     const unsigned long long x = s.warp_a[w];
     mw = ((mw | x) >> 32 << 32) | max((unsigned)mw, (unsigned)x);
-    fin_here += (unsigned)s.warp_b[w];
+    finite += (unsigned)s.warp_b[w];
     lowest = min(lowest, (unsigned)(s.warp_b[w] >> 32));
   }
-  exchange(s, 0, mw, ((unsigned long long)lowest << 32) | fin_here, rank, ctas);
-  unsigned long long finite = 0;
-  mkey = 0;
-  for (uint32_t c = 0; c < ctas; ++c) {
-    mkey = max(mkey, (unsigned)s.board[0].a[c]);
-    bad |= (s.board[0].a[c] >> 32) != 0;
-    finite += (unsigned)s.board[0].b[c];
-    lowest = min(lowest, (unsigned)(s.board[0].b[c] >> 32));
+  if (ctas > 1) {
+    exchange(s, 0, mw, ((unsigned long long)lowest << 32) | finite, rank, ctas);
+    finite = mw = 0;
+    for (uint32_t c = 0; c < ctas; ++c) {
+      const unsigned long long x = s.board[0].a[c];
+      mw = ((mw | x) >> 32 << 32) | max((unsigned)mw, (unsigned)x);
+      finite += (unsigned)s.board[0].b[c];
+      lowest = min(lowest, (unsigned)(s.board[0].b[c] >> 32));
+    }
   }
-  bad |= finite == 0;
+  mkey = (unsigned)mw;
+  bad |= (mw >> 32) != 0 || finite == 0;
   if (bad) {
     if (rank == 0 && tid == 0) {
       a.token[row] = -1;
@@ -271,8 +292,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   const float m = key_float(mkey);
 
   // Everything from here on is the same in all CTAs of the cluster but for their
-  // slices, so that they come to every exchange together.
-  SpCut cut{0u, ~0ull};       // all
+  // slices, so that they come to every exchange together, until the leader goes on alone.
   const bool greedy = T < 5.421010862427522e-20f || top_k == 1;  // 2^-64
   if (tid == 0) {  // in 64 bits, which few units compute
     unsigned fk = 1u;
@@ -298,7 +318,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   const unsigned floor_key = s.floor_key;  // min_p's: values at least this
   auto weight = [&](float v) { return greedy ? 1ull : weight_of(v, sc, s.pow2); };
 
-  // ------------------------------------------------ histograms over the cluster
+  // ---------------------------------------------------------------- histograms
   auto clear = [&](bool mass) {
     for (int i = tid; i < kSpBins; i += kSpThreads) {
       s.count[i] = 0u;
@@ -307,7 +327,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     if (tid == 0) {
       s.found_bin = -1;
       s.found_above = 0;
-      s.listed = 0;
+      s.nkeys = 0;
+      s.key_lo = 0xffffffffu;
+      s.key_hi = 0;
     }
     __syncthreads();
   };
@@ -317,9 +339,16 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     const unsigned wh = (unsigned)(w >> 32) + (old + wl < old ? 1u : 0u);
     if (wh) atomicAdd(&s.hi[bin], wh);
   };
-  // s.sum: the bins' masses (what = 1) or counts (0), or with what = 2 the counts above
-  // the 32 bits of `lo`, over the cluster: each CTA adds up some bins and tells all.
+  // s.sum: the bins' masses (what = 1), counts (0), or counts above the 32 bits of `lo`
+  // (2), over the cluster: each CTA adds up some bins and tells all.
   auto combine = [&](int what) {
+    if (ctas == 1) {
+      __syncthreads();
+      for (int i = tid; i < kSpBins; i += kSpThreads)
+        s.sum[i] = what == 0 ? s.count[i] : s.lo[i] + ((unsigned long long)(what == 1 ? s.hi[i] : s.count[i]) << 32);
+      __syncthreads();
+      return;
+    }
     cluster_sync();
     const int per = kSpBins / (int)ctas, b0 = (int)rank * per;
     for (int i = b0 + tid; i < b0 + per; i += kSpThreads) {
@@ -327,8 +356,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
 #pragma unroll 4
       for (uint32_t c = 0; c < ctas; ++c) {
         unsigned long long x;
-        if (what == 0) x = ld_cluster_u32(cluster_addr(&s.count[i], c));
-        else {
+        if (what == 0) {
+          x = ld_cluster_u32(cluster_addr(&s.count[i], c));
+        } else {
           x = ld_cluster_u32(cluster_addr(&s.lo[i], c));
           x += (unsigned long long)ld_cluster_u32(cluster_addr(what == 1 ? &s.hi[i] : &s.count[i], c)) << 32;
         }
@@ -358,14 +388,14 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     for (int e = 0; e < 4; ++e) run[e] += before;
     __syncthreads();
   };
-  // The first bin at which above + the running sum reaches the target: s.found_bin, and
-  // what lies above it, s.found_above.
-  auto find_bin = [&](unsigned long long above, unsigned long long target) {
+  // The first bin at which above + the running sum of `of` reaches the target:
+  // s.found_bin, what lies above it: s.found_above, and all: s.found_total.
+  auto find_bin = [&](unsigned long long above, unsigned long long target, auto&& of) {
     unsigned long long run[4];
-    scan_bins(run, [&](int i) { return s.sum[i]; });
+    scan_bins(run, of);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const unsigned long long v = s.sum[4 * tid + e];
+      const unsigned long long v = of(4 * tid + e);
       if (above + run[e] >= target && above + run[e] - v < target) {
         s.found_bin = 4 * tid + e;
         s.found_above = above + run[e] - v;
@@ -376,9 +406,20 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   };
   // bins of the first histogram: linear below the maximum
   auto bin1 = [&](float v) { return (int)fminf((m - v) * (sc.c * kSpUnit), (float)(kSpBins - 1)); };
+  const float unit = 1.0f / (sc.c * kSpUnit);
+  // the bounds of two keys over the CTA's threads, in s.key_lo and s.key_hi
+  auto bounds = [&](unsigned lo, unsigned hi) {
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      atomicMin(&s.key_lo, lo);
+      atomicMax(&s.key_hi, hi);
+    }
+    __syncthreads();
+  };
 
-  // One cut: the smallest leading run of the values above key `in` whose count or mass
-  // reaches `target`; the run is there.  Histograms of all values, refined.
+  // One cut over all values, where the short ways failed: the smallest leading run of the
+  // values above key `in` whose count or mass reaches `target` (it does).
   auto find_slowly = [&](bool mass, unsigned long long target, unsigned in) {
     unsigned khi = mkey, klo = 0;
     int shift = -1, want = -1;         // first level: linear in the value
@@ -386,11 +427,10 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     SpCut out{0u, ~0ull};
     for (int level = 0; level < 6; ++level) {
       clear(mass);
-      unsigned lo_key = 0xffffffffu, hi_key = 0u;
-      for (int j = tid; j < n4; j += kSpThreads) {
-        const float4 v4 = value4(j);
+      for (int i = first + 4 * lane; i < last; i += 128) {
+        const float4 v4 = load4(i, last);
         const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < 4; ++e) {
           const float v = vs[e];
           if (!(v >= -FLT_MAX)) continue;
@@ -407,7 +447,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         }
       }
       combine(mass ? 1 : 0);
-      find_bin(above, target);
+      find_bin(above, target, [&](int i) { return s.sum[i]; });
       const int bin = s.found_bin;
       above = s.found_above;
       if (bin < 0) return out;
@@ -416,42 +456,31 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         const unsigned long long w = mass ? weight(key_float(khi - (unsigned)bin)) : 1ull;
         out.key = khi - (unsigned)bin;
         out.ties = w ? (target - above + w - 1) / w : 1;
-        cluster_sync();
         return out;
       }
       if (level == 0) {
         want = bin;
-        // the bounds of the bin's keys over the cluster
-        for (int j = tid; j < n4; j += kSpThreads) {
-          const float4 v4 = value4(j);
+        unsigned lo_key = 0xffffffffu, hi_key = 0u;  // the bounds of the bin's keys
+        for (int i = first + 4 * lane; i < last; i += 128) {
+          const float4 v4 = load4(i, last);
           const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
+#pragma unroll 1
           for (int e = 0; e < 4; ++e) {
-            const float v = vs[e];
-            const unsigned k = key_of(v);
-            if (!(v >= -FLT_MAX) || k <= in || bin1(v) != want) continue;
+            const unsigned k = key_of(vs[e]);
+            if (!(vs[e] >= -FLT_MAX) || k <= in || bin1(vs[e]) != want) continue;
             lo_key = min(lo_key, k);
             hi_key = max(hi_key, k);
           }
         }
-        lo_key = __reduce_min_sync(0xffffffffu, lo_key);
-        hi_key = __reduce_max_sync(0xffffffffu, hi_key);
-        __syncthreads();
-        if (lane == 0) {
-          s.warp_a[warp] = lo_key;
-          s.warp_b[warp] = hi_key;
-        }
-        __syncthreads();
-        for (int w = 0; w < kSpWarps; ++w) {
-          lo_key = min(lo_key, (unsigned)s.warp_a[w]);
-          hi_key = max(hi_key, (unsigned)s.warp_b[w]);
-        }
-        exchange(s, 1, lo_key, hi_key, rank, ctas);
-        klo = 0xffffffffu;
-        khi = 0;
-        for (uint32_t c = 0; c < ctas; ++c) {
-          klo = min(klo, (unsigned)s.board[1].a[c]);
-          khi = max(khi, (unsigned)s.board[1].b[c]);
+        bounds(lo_key, hi_key);
+        klo = s.key_lo;
+        khi = s.key_hi;
+        if (ctas > 1) {
+          exchange(s, 1, klo, khi, rank, ctas);
+          for (uint32_t c = 0; c < ctas; ++c) {
+            klo = min(klo, (unsigned)s.board[1].a[c]);
+            khi = max(khi, (unsigned)s.board[1].b[c]);
+          }
         }
       } else {
         const unsigned t = khi - ((unsigned)bin << shift), span = (1u << shift) - 1;
@@ -464,392 +493,491 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     return out;
   };
 
-  // A bracket of values around the border, from a sample of the slices: about kSpSide
-  // sampled values on either side.  share: the border's share of the sample's mass, or
-  // rank its place among all values.
-  auto sample_bracket = [&](bool mass, float share, unsigned long long place) {
-    clear(true);
-    const int bits = 28 - (32 - __clz(a.slice / 8));  // so that the whole sample's sum fits 32
-    for (int j = tid; j < n4; j += 2 * kSpThreads) {
-      const float v = value4(j).x;  // every eighth value
-      if (!(v >= -FLT_MAX)) continue;
-      const int b = bin1(v);
-      atomicAdd(&s.count[b], 1u);
-      if (mass) atomicAdd(&s.lo[b], (unsigned)(weight(v) >> (kSpTop - bits)));
-    }
-    combine(2);
-    unsigned long long run[4], count[4];
-    scan_bins(run, [&](int i) { return s.sum[i] & 0xffffffffull; });
-    scan_bins(count, [&](int i) { return s.sum[i] >> 32; });
-    // the estimated bin: where the running mass (or eight times the count) reaches the border
-    if (tid == kSpThreads - 1) s.warp_b[0] = run[3];
-    if (tid == 0) {
-      s.bracket_hi = m;
-      s.bracket_lo = kNone;
-      s.found_above = ~0ull;  // the estimated place in the sample
-    }
-    __syncthreads();
-    const float goal = fmaxf(mass ? share * (float)s.warp_b[0] : (float)place * 0.125f, 1e-30f);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const unsigned long long x = s.sum[4 * tid + e];
-      const float now = mass ? (float)run[e] : (float)count[e];
-      const float was = mass ? (float)(run[e] - (x & 0xffffffffull)) : (float)(count[e] - (x >> 32));
-      if (was < goal && now >= goal) s.found_above = count[e];
-    }
-    __syncthreads();
-    const unsigned long long at = s.found_above;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int b = 4 * tid + e;
-      const unsigned long long prev = count[e] - (s.sum[b] >> 32);
-      const float unit = 1.0f / (sc.c * kSpUnit);
-      // the last bin that ends kSpSide before, the first that ends kSpSide behind
-      if (at != ~0ull && count[e] + kSpSide <= at && b + 1 < kSpBins && count[e] + kSpSide + (s.sum[b + 1] >> 32) > at)
-        s.bracket_hi = m - (float)(b + 1) * unit;
-      if (at != ~0ull && count[e] >= at + kSpSide && prev < at + kSpSide && b < kSpBins - 1) s.bracket_lo = m - (float)(b + 1) * unit;
-    }
-    __syncthreads();
-  };
-
-  // the cluster's keys of the border's bin and their weights, where the sums were
-  unsigned* list_all = reinterpret_cast<unsigned*>(s.sum);
-  unsigned long long* list_weight = s.sum + kSpList / 2;
-
-  // What is kept of this slice, where a search has added it up already
-  bool saved = false;
-  unsigned long long mass_here = 0, count_here = 0, equal_here = 0;
-
-  // One cut, by a bracket [lo, hi] of values: the smallest leading run of the values
-  // above key `in` (0: all) whose count, or mass with p times their sum (and `more`, the
-  // weight of values equal to `in` that count too), reaches the target.  floored: what
-  // lies below the bracket is of no matter.
-  auto find_cut = [&](bool mass, unsigned long long target, unsigned long long p, unsigned in, unsigned long long more, float lo,
-                      float hi, bool floored, SpCut& out) {
-    const float scale = fminf((float)(kSpBins - 1) / (hi - lo), FLT_MAX);
-    auto bin2 = [&](float v) { return (int)fminf((hi - v) * scale, (float)(kSpBins - 1)); };
-    clear(mass);
-    unsigned long long above = 0, all = 0;
-    unsigned nabove = 0;
-    auto put = [&](float v) {
-      if (!(v >= lo)) return;
-      const unsigned k = key_of(v);
-      if (k <= in) return;
-      if (v > hi) {
-        ++nabove;
-        return;
-      }
-      atomicAdd(&s.count[bin2(v)], 1u);
-    };
-    auto put_mass = [&](float v) {
-      if (in && key_of(v) <= in) return;
-      const unsigned long long w = weight(v);
-      all += w;
-      if (v > hi) {
-        above += w;
-        ++nabove;
-      } else if (v >= lo) {
-        const int b = bin2(v);
-        atomicAdd(&s.count[b], 1u);
-        add_mass(b, w);
-      }
-    };
-    if (mass) {
-      const bool few = in != 0;
-      const float least = few ? key_float(in) : kNone;
-      for (int j = tid; j < n4; j += kSpThreads) {
-        const float4 v = value4(j);
-        if (few && fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) < least) continue;
-        put_mass(v.x);
-        put_mass(v.y);
-        put_mass(v.z);
-        put_mass(v.w);
-      }
-    } else {
-      for (int j = tid; j < n4; j += kSpThreads) {
-        const float4 v = value4(j);
-        if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) < lo) continue;
-        put(v.x);
-        put(v.y);
-        put(v.z);
-        put(v.w);
-      }
-    }
-    unsigned long long na = nabove, none = 0;
-    cta_sum(s, above, all);
-    cta_sum(s, na, none);
-    const unsigned long long above_here = mass ? above : na;
-    // the masses of the bins (or their counts), what lies above, the sum of all
-    if (tid < ctas) {
-      st_cluster_u64(cluster_addr(&s.board[2].a[rank], tid), above_here);
-      st_cluster_u64(cluster_addr(&s.board[2].b[rank], tid), all);
-    }
-    combine(mass ? 1 : 0);
-    above = all = 0;
-    for (uint32_t c = 0; c < ctas; ++c) {
-      above += s.board[2].a[c];
-      all += s.board[2].b[c];
-    }
-    if (mass) {
-      all += more;
-      target = max(1ull, __umul64hi(all, p) + (all * p != 0 ? 1 : 0));
-    }
-    find_bin(above, target);
-    const int bin = s.found_bin;
-    if (bin < 0) {
-      const unsigned long long t = s.found_total;
-      if (t < target && in) {
-        // within the values equal to `in`, which are not in the histogram
-        const unsigned long long w = weight(key_float(in));
-        out.key = in;
-        out.ties = w ? (target - t + w - 1) / w : 1;
-        return;
-      }
-      if (t < target && floored) return;  // min_p's floor cuts first
-      out = find_slowly(mass, target, in);
-      return;
-    }
-    const unsigned long long before = s.found_above;
-    // the bin's keys: their bounds, their number, and as many as fit in the list
-    unsigned lo_key = 0xffffffffu, hi_key = 0u;
-    for (int j = tid; j < n4; j += kSpThreads) {
-      const float4 v4 = value4(j);
-      if (fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) < lo) continue;
-      const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = vs[e];
-        if (!(v >= lo) || v > hi || bin2(v) != bin) continue;
-        const unsigned k = key_of(v);
-        if (k <= in) continue;
-        lo_key = min(lo_key, k);
-        hi_key = max(hi_key, k);
-        const unsigned at = atomicAdd(&s.listed, 1u);
-        if (at < kSpList) s.list[at] = k;
-      }
-    }
-    lo_key = __reduce_min_sync(0xffffffffu, lo_key);
-    hi_key = __reduce_max_sync(0xffffffffu, hi_key);
-    __syncthreads();
-    if (lane == 0) {
-      s.warp_a[warp] = lo_key;
-      s.warp_b[warp] = hi_key;
-    }
-    __syncthreads();
-    for (int w = 0; w < kSpWarps; ++w) {
-      lo_key = min(lo_key, (unsigned)s.warp_a[w]);
-      hi_key = max(hi_key, (unsigned)s.warp_b[w]);
-    }
-    const unsigned here = s.listed;
-    exchange(s, 3, ((unsigned long long)hi_key << 32) | lo_key, here, rank, ctas);
-    lo_key = 0xffffffffu;
-    hi_key = 0;
-    unsigned first = 0, number = 0;
-    for (uint32_t c = 0; c < ctas; ++c) {
-      lo_key = min(lo_key, (unsigned)s.board[3].a[c]);
-      hi_key = max(hi_key, (unsigned)(s.board[3].a[c] >> 32));
-      if (c < rank) first += (unsigned)s.board[3].b[c];
-      number += (unsigned)s.board[3].b[c];
-    }
-    if (lo_key != hi_key && number > kSpList) {
-      out = find_slowly(mass, target, in);
-      return;
-    }
-    if (lo_key == hi_key) {
-      const unsigned long long w = mass ? weight(key_float(lo_key)) : 1ull;
-      out.key = lo_key;
-      out.ties = (target - before + w - 1) / w;
-      cluster_sync();  // (the boards and lists are free again)
-    } else {
-      for (unsigned i = tid; i < here; i += kSpThreads)
-        for (uint32_t c = 0; c < ctas; ++c) st_cluster_u32(cluster_addr(&list_all[first + i], c), s.list[i]);
-      cluster_sync();
-      if (tid < number) list_weight[tid] = mass ? weight(key_float(list_all[tid])) : 1ull;
-      __syncthreads();
-      if (tid < number) {
-        const unsigned k = list_all[tid];
-        unsigned long long over = before, same = 0;
-        for (unsigned i = 0; i < number; ++i) {
-          const unsigned o = list_all[i];
-          if (o > k) over += list_weight[i];
-          same += o == k;
-        }
-        if (over < target && over + same * list_weight[tid] >= target) {  // (every equal one says the same)
-          s.cut_key = k;
-          s.cut_ties = (target - over + list_weight[tid] - 1) / list_weight[tid];
-        }
-      }
-      __syncthreads();
-      out.key = s.cut_key;
-      out.ties = s.cut_ties;
-    }
-    if (mass && !in) {
-      // this slice's kept mass: above the bracket, in the bins before, and of the list
-      unsigned long long w = 0, c = 0;
-      for (int i = tid; i < bin; i += kSpThreads) {
-        w += s.lo[i] + ((unsigned long long)s.hi[i] << 32);
-        c += s.count[i];
-      }
-      unsigned long long eq = 0, zero = 0;
-      if (lo_key == hi_key) {
-        if (tid == 0) eq = here;
-      } else {
-        for (unsigned i = tid; i < here; i += kSpThreads) {
-          if (s.list[i] > out.key) {
-            w += weight(key_float(s.list[i]));
-            ++c;
-          }
-          eq += s.list[i] == out.key;
-        }
-      }
-      cta_sum(s, w, c);
-      cta_sum(s, eq, zero);
-      mass_here = above_here + w;
-      count_here = na + c;
-      equal_here = eq;
-      saved = true;
-    }
-  };
-
-  if (greedy) {
-    cut.key = mkey;
-    cut.ties = 1;
-  } else {
-    // without a bracket: down to the lowest value, or to where nothing weighs
-    const float lowest_v = fmaxf(key_float(lowest), m - (float)kSpBins / (sc.c * kSpUnit));
-    if (top_k > 0 && (unsigned long long)top_k < finite) {
-      float lo = lowest_v, hi = m;
-      if (a.V > kSpSample) {
-        sample_bracket(false, 0.f, (unsigned long long)top_k);
-        lo = fmaxf(lo, s.bracket_lo);
-        hi = s.bracket_hi;
-      }
-      find_cut(false, (unsigned long long)top_k, 0, 0u, 0, lo, hi, false, cut);
-    }
-    if (top_p < 1.f) {
-      const unsigned long long p = fraction(top_p);
-      SpCut c{0u, ~0ull};
-      if (cut.key) {
-        const unsigned long long w = weight(key_float(cut.key));
-        find_cut(true, 0, p, cut.key, cut.ties * w, key_float(cut.key), m, false, c);
-      } else {
-        float lo = lowest_v, hi = m;
-        if (floor_key > 1u) lo = key_float(floor_key);  // what lies below is not kept anyway
-        else if (a.V > kSpSample) {
-          sample_bracket(true, top_p, 0);
-          lo = fmaxf(lo, s.bracket_lo);
-          hi = s.bracket_hi;
-        }
-        find_cut(true, 0, p, 0u, 0, lo, hi, floor_key > 1u, c);
-      }
-      if (c.key) cut = c;
-    }
-  }
-  // min_p's floor, where it is tighter
-  const bool tied = cut.key && cut.ties != ~0ull && cut.key >= floor_key;
-  const unsigned least = max(cut.key, floor_key);  // above it (tied), or from it on
-  auto in_run = [&](unsigned k) { return tied ? k > cut.key : k >= least; };
-  const float least_v = key_float(max(least, 0x00800000u));  // no finite value is below
-
-  // ---- this slice's kept mass and count
-  if (!(saved && tied)) {
-    unsigned long long w = 0, c = 0, eq = 0, zero = 0;
-    for (int j = tid; j < n4; j += kSpThreads) {
-      const float4 v4 = value4(j);
+  // ------------------------------------------------------ what is kept, run by run
+  // The mass and the number of this run's values above the cut (with `from`: from it on),
+  // and the number of those equal to it.
+  auto sum_run = [&](unsigned least, bool from, int i0, int i1, unsigned long long& w, unsigned& c, unsigned& eq) {
+    const float least_v = key_float(max(least, 0x00800000u));  // no finite value is below
+    w = 0;
+    c = eq = 0;
+    for (int i = i0 + 4 * lane; i < i1; i += 128) {
+      const float4 v4 = load4(i, i1);
       if (!(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= least_v)) continue;
       const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float v = vs[e];
-        if (!(v >= -FLT_MAX)) continue;
-        const unsigned k = key_of(v);
-        if (in_run(k)) {
-          ++c;
-          w += weight(v);
-        }
-        eq += tied && k == cut.key;
+        const unsigned k = vs[e] >= -FLT_MAX ? key_of(vs[e]) : 0u;
+        const bool in = k > least || (from && k == least);
+        const unsigned long long x = weight(vs[e]);
+        w += in ? x : 0ull;
+        c += in;
+        eq += k == least;
       }
     }
-    cta_sum(s, w, c);
-    cta_sum(s, eq, zero);
-    mass_here = w;
-    count_here = c;
-    equal_here = eq;
-  }
-  const unsigned long long w_tie = tied ? weight(key_float(cut.key)) : 0ull;
-  // equal ones are taken in the order of the slices
-  if (tid < ctas) st_cluster_u64(cluster_addr(&s.board[4].a[rank], tid), mass_here);
-  if (tid < ctas) st_cluster_u64(cluster_addr(&s.board[4].b[rank], tid), (count_here << 32) | equal_here);
-  cluster_sync();
-  unsigned long long total = 0, kept = 0, before = 0, mine = 0, left = tied ? cut.ties : 0, left_here = 0;
-  for (uint32_t c = 0; c < ctas; ++c) {
-    const unsigned long long eq = s.board[4].b[c] & 0xffffffffull, take = min(left, eq);
-    const unsigned long long x = s.board[4].a[c] + take * w_tie;
-    if (c < rank) before += x;
-    if (c == rank) {
-      mine = x;
-      left_here = take;
+    w = warp_sum(w);
+    c = __reduce_add_sync(0xffffffffu, c);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+  };
+  // .. told to the leader
+  auto tell_run = [&](unsigned long long w, unsigned c, unsigned eq, unsigned listed) {
+    if (lane == 0) {
+      st_cluster_u64(cluster_addr(&s.run_mass[mine], 0), w);
+      st_cluster_u32(cluster_addr(&s.run_count[mine], 0), c);
+      st_cluster_u32(cluster_addr(&s.run_equal[mine], 0), eq);
+      st_cluster_u32(cluster_addr(&s.run_listed[mine], 0), listed);
     }
-    left -= take;
-    total += x;
-    kept += (s.board[4].b[c] >> 32) + take;
-  }
-  const unsigned long long target = __umul64hi(total, fraction(u));  // the first running sum above it
-  if (target < before || target >= before + mine) return;  // drawn from another slice
+  };
 
-  // ---- the token: a warp takes a run of the slice; the run that holds the border is
-  // gone through by its warp
-  const int run4 = ((n4 + kSpWarps - 1) / kSpWarps + 31) / 32 * 32, j0 = warp * run4, j1 = min(n4, j0 + run4);
-  unsigned long long w = 0, eq = 0;
-  for (int j = j0 + lane; j < j1; j += 32) {
-    const float4 v4 = value4(j);
-    if (!(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= least_v)) continue;
-    const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
+  SpCut cut{0u, ~0ull};  // all
+  bool listed = false;   // whether the border's neighbourhood is in lists
+  unsigned long long above = 0, all = 0, target = 0;
+  float lo = 0.f, hi = m;
+  const bool by_k = top_k > 0 && (unsigned long long)top_k < finite, by_p = top_p < 1.f, floored = floor_key > 1u;
+  const unsigned long long p = by_p ? fraction(top_p) : 0ull;
+  auto share = [&](unsigned long long x) { return max(1ull, __umul64hi(x, p) + (x * p != 0 ? 1 : 0)); };  // ceil(p x)
+  if (greedy) {
+    cut.key = mkey;
+    cut.ties = 1;
+  } else if (by_k || by_p) {
+    // ---- a bracket.  Without a sample: down to the lowest value, or where nothing weighs
+    lo = fmaxf(key_float(lowest), m - (float)kSpBins * unit);
+    // of the sample: the running sum and count at a thread's bins
+    unsigned long long run[4], count[4];
+    const int bits = 28 - (32 - __clz(a.slice / a.step));  // a weight's, so that the whole sample's sum fits 32
+    const bool sampled = a.V > kSpSample && (by_k || !floored);
+    // The bracket about the bin at which the sample's mass (or count) reaches `goal`: the
+    // values that lie kSpSide sampled ones before and behind.
+    auto bracket = [&](float goal) {
+      if (tid == 0) {
+        s.bracket_hi = m;
+        s.bracket_lo = kNone;
+        s.found_above = ~0ull;  // its place in the sample
+      }
+      __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v = vs[e];
-      if (!(v >= -FLT_MAX)) continue;
-      const unsigned k = key_of(v);
-      if (in_run(k)) w += weight(v);
-      eq += tied && k == cut.key;
+      for (int e = 0; e < 4; ++e) {
+        const unsigned long long x = s.sum[4 * tid + e];
+        const float now = by_k ? (float)count[e] : (float)run[e];
+        const float was = by_k ? (float)(count[e] - (x >> 32)) : (float)(run[e] - (x & 0xffffffffull));
+        if (was < goal && now >= goal) s.found_above = count[e];
+      }
+      __syncthreads();
+      const unsigned long long at = s.found_above;
+      if (at != ~0ull) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int b = 4 * tid + e;
+          const unsigned long long prev = count[e] - (s.sum[b] >> 32);
+          // the last bin that ends kSpSide before, the first that ends kSpSide behind
+          if (b + 1 < kSpBins && count[e] + kSpSide <= at && count[e] + kSpSide + (s.sum[b + 1] >> 32) > at)
+            s.bracket_hi = m - (float)(b + 1) * unit;
+          if (b + 1 < kSpBins && count[e] >= at + kSpSide && prev < at + kSpSide) s.bracket_lo = m - (float)(b + 1) * unit;
+        }
+      }
+      __syncthreads();
+      hi = by_k ? m : s.bracket_hi;  // (the first k are all listed)
+      lo = fmaxf(fmaxf(key_float(lowest), m - (float)kSpBins * unit), s.bracket_lo);
+    };
+    if (sampled) {
+      clear(true);
+      // every a.step-th 128 values of a run
+      for (int i = first + 4 * lane; i < last; i += 128 * a.step) {
+        const float4 v4 = load4(i, last);
+        const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!(vs[e] >= -FLT_MAX)) continue;
+          const int b = bin1(vs[e]);
+          atomicAdd(&s.count[b], 1u);
+          if (!by_k) {
+            const unsigned w = (unsigned)(weight(vs[e]) >> (kSpTop - bits));
+            if (w) atomicAdd(&s.lo[b], w);
+          }
+        }
+      }
+      combine(2);
+      scan_bins(run, [&](int i) { return s.sum[i] & 0xffffffffull; });
+      scan_bins(count, [&](int i) { return s.sum[i] >> 32; });
+      if (tid == kSpThreads - 1) s.warp_b[0] = run[3];
+      __syncthreads();
+      bracket(fmaxf(by_k ? (float)top_k / (float)a.step : top_p * (float)s.warp_b[0], 1e-30f));
+    } else if (floored && !by_k) {
+      lo = key_float(floor_key);  // what lies below is not kept anyway
+    }
+
+    // ---- all values: their sum, what lies above the bracket, and the lists
+    for (int round = 0; round < kSpTries; ++round) {
+      unsigned long long w_all = 0, w_above = 0, w_list = 0;
+      unsigned c_above = 0, n_list = 0;
+      float* my_v = list_v + warp * cap;
+      uint16_t* my_at = list_at + warp * cap;
+      for (int i = first + 4 * lane; i - 4 * lane < last; i += 128) {
+        const float4 v4 = i < last ? load4(i, last) : make_float4(kNone, kNone, kNone, kNone);
+        const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
+        unsigned inside = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool ge = vs[e] >= lo, gt = vs[e] > hi;
+          if (!by_k) {
+            const unsigned long long x = weight(vs[e]);
+            w_all += x;
+            w_above += gt ? x : 0ull;
+            w_list += ge && !gt ? x : 0ull;
+            c_above += gt;
+          }
+          inside |= (ge && !gt ? 1u : 0u) << e;
+        }
+        if (__any_sync(0xffffffffu, inside)) {
+          unsigned upto = __popc(inside);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+          }
+          unsigned at = n_list + upto - __popc(inside);
+          n_list += __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (inside >> e & 1) {
+              if (at < (unsigned)cap) {
+                my_v[at] = vs[e];
+                my_at[at] = (uint16_t)(i + e - first);
+              }
+              ++at;
+            }
+        }
+      }
+      w_all = warp_sum(w_all);
+      w_above = warp_sum(w_above);
+      w_list = warp_sum(w_list);
+      c_above = __reduce_add_sync(0xffffffffu, c_above);
+      // the row's sums (a list that ran over is told by a count beyond any)
+      const unsigned long long n_told = n_list > (unsigned)cap ? 1ull << 40 : n_list;
+      unsigned long long t_all = w_all, t_above = w_above, t_list = w_list, t_n = n_told;
+      __syncthreads();
+      if (lane == 0) {
+        s.warp_a[warp] = w_all;
+        s.warp_b[warp] = w_above;
+      }
+      __syncthreads();
+      t_all = t_above = 0;
+      for (int w = 0; w < kSpWarps; ++w) {
+        t_all += s.warp_a[w];
+        t_above += s.warp_b[w];
+      }
+      __syncthreads();
+      if (lane == 0) {
+        s.warp_a[warp] = w_list;
+        s.warp_b[warp] = n_told;
+      }
+      __syncthreads();
+      t_list = t_n = 0;
+      for (int w = 0; w < kSpWarps; ++w) {
+        t_list += s.warp_a[w];
+        t_n += s.warp_b[w];
+      }
+      if (ctas > 1) {
+        const int x = round % 2 ? 0 : 2;  // boards in turns: the others may still read the last ones
+        if (tid < (int)ctas) {
+          st_cluster_u64(cluster_addr(&s.board[x].a[rank], tid), t_all);
+          st_cluster_u64(cluster_addr(&s.board[x].b[rank], tid), t_above);
+          st_cluster_u64(cluster_addr(&s.board[x + 1].a[rank], tid), t_list);
+          st_cluster_u64(cluster_addr(&s.board[x + 1].b[rank], tid), t_n);
+        }
+        cluster_sync();
+        t_all = t_above = t_list = t_n = 0;
+        for (uint32_t c = 0; c < ctas; ++c) {
+          t_all += s.board[x].a[c];
+          t_above += s.board[x].b[c];
+          t_list += s.board[x + 1].a[c];
+          t_n += s.board[x + 1].b[c];
+        }
+      }
+      above = t_above;
+      all = t_all;
+      if (by_k) {
+        listed = t_n < (1ull << 40) && t_n >= (unsigned long long)top_k;
+      } else {
+        target = share(all);
+        const bool border = above < target && (above + t_list >= target || floored);
+        listed = border && t_n < (1ull << 40);
+        if (!border && sampled && round + 1 < kSpTries) {
+          // the sample's own sums from the nearer end of the bracket on
+          const bool before = above >= target;
+          const float edge = before ? hi : lo;
+          const int b = min(kSpBins - 1, max(0, (int)rintf((m - edge) / unit)));  // the first bin behind the edge
+          if (b / 4 == tid) s.found_total = run[b % 4] - (s.sum[b] & 0xffffffffull);
+          __syncthreads();
+          const float at_edge = (float)s.found_total;
+          const float off = before ? -(float)(above - target) : (float)(target - above - t_list);
+          __syncthreads();
+          bracket(fmaxf(at_edge + off * exp2f((float)(bits - kSpTop)) / (float)a.step, 1e-30f));
+          continue;
+        }
+      }
+      if (listed) {
+        tell_run(w_above, c_above, 0u, n_list);
+        if (rank > 0) {
+          const uint32_t to_v = cluster_addr(list_v + mine * cap, 0), to_at = cluster_addr(list_at + mine * cap, 0);
+          for (unsigned i = lane; i < n_list; i += 32) {
+            st_cluster_u32(to_v + 4 * i, __float_as_uint(my_v[i]));
+            st_cluster_u16(to_at + 2 * i, my_at[i]);
+          }
+        }
+      }
+      break;
+    }
+    if (!listed) {
+      // ---- the long way
+      if (by_k) cut = find_slowly(false, (unsigned long long)top_k, 0u);
+      if (by_p) {
+        SpCut c{0u, ~0ull};
+        unsigned long long sum = all, eq_w = 0;
+        if (by_k) {
+          unsigned long long w;
+          unsigned n, eq;
+          sum_run(cut.key, false, first, last, w, n, eq);
+          unsigned long long t = lane == 0 ? w : 0, none = 0;
+          cta_sum(s, t, none);
+          if (ctas > 1) {
+            cluster_sync();
+            exchange(s, 3, t, 0, rank, ctas);
+            t = 0;
+            for (uint32_t x = 0; x < ctas; ++x) t += s.board[3].a[x];
+          }
+          eq_w = weight(key_float(cut.key));
+          sum = t + cut.ties * eq_w;
+          target = share(sum);
+          if (t < target) {
+            c.key = cut.key;
+            c.ties = eq_w ? (target - t + eq_w - 1) / eq_w : 1;
+          }
+        }
+        if (!c.key) c = find_slowly(true, target, cut.key);
+        if (c.key) cut = c;
+      }
     }
   }
-  w = warp_sum(w);
-  eq = warp_sum(eq);
+
+  if (!listed) {
+    const bool tied = cut.key && cut.ties != ~0ull && cut.key >= floor_key;
+    unsigned long long w;
+    unsigned c, eq;
+    sum_run(tied ? cut.key : max(cut.key, floor_key), !tied, first, last, w, c, eq);
+    tell_run(w, c, tied ? eq : 0u, 0u);
+  }
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+  if (rank > 0) return;
+
+  // ================================================================= the leader
+  const int slots = runs * cap;
+  auto each_listed = [&](auto&& f) {
+    for (int i = tid; i < slots; i += kSpThreads) {
+      const int r = i / cap;
+      if (i - r * cap < (int)s.run_listed[r]) f(i, r);
+    }
+  };
+  if (listed) {
+    // One cut among the listed values above key `in`: bins linear in the value, and where
+    // a bin holds too many different ones, over the bits of their keys.
+    auto find_listed = [&](bool mass, unsigned long long goal, unsigned long long over, unsigned in, SpCut& out) {
+      const float scale = fminf((float)(kSpBins - 1) / (hi - lo), FLT_MAX);
+      unsigned khi = 0, klo = 0;
+      int shift = -1;
+      auto bin_of = [&](float v, unsigned k) {
+        if (shift < 0) return (int)fminf((hi - v) * scale, (float)(kSpBins - 1));
+        return k > khi || k < klo ? -1 : (int)((khi - k) >> shift);
+      };
+      for (int level = 0; level < 6; ++level) {
+        clear(mass);
+        each_listed([&](int i, int) {
+          const float v = list_v[i];
+          const unsigned k = key_of(v);
+          if (k <= in) return;
+          const int b = bin_of(v, k);
+          if (b < 0) return;
+          if (mass) add_mass(b, weight(v));
+          else atomicAdd(&s.count[b], 1u);
+        });
+        __syncthreads();
+        find_bin(over, goal, [&](int i) { return mass ? s.lo[i] + ((unsigned long long)s.hi[i] << 32) : (unsigned long long)s.count[i]; });
+        const int bin = s.found_bin;
+        if (bin < 0) return;
+        over = s.found_above;
+        unsigned lo_key = 0xffffffffu, hi_key = 0u;
+        each_listed([&](int i, int) {
+          const float v = list_v[i];
+          const unsigned k = key_of(v);
+          if (k <= in || bin_of(v, k) != bin) return;
+          lo_key = min(lo_key, k);
+          hi_key = max(hi_key, k);
+          const unsigned at = atomicAdd(&s.nkeys, 1u);
+          if (at < kSpKeys) s.keys[at] = k;
+        });
+        bounds(lo_key, hi_key);
+        klo = s.key_lo;
+        khi = s.key_hi;
+        const unsigned n = s.nkeys;
+        if (klo == khi) {
+          const unsigned long long w = mass ? weight(key_float(klo)) : 1ull;
+          out.key = klo;
+          out.ties = (goal - over + w - 1) / w;
+          __syncthreads();
+          return;
+        }
+        if (n <= kSpKeys) {
+          // compared with one another; the weights lie where the cluster's sums were
+          if (tid < (int)n) s.sum[tid] = mass ? weight(key_float(s.keys[tid])) : 1ull;
+          __syncthreads();
+          if (tid < (int)n) {
+            const unsigned k = s.keys[tid];
+            unsigned long long before = over, same = 0;
+            for (unsigned i = 0; i < n; ++i) {
+              const unsigned o = s.keys[i];
+              if (o > k) before += s.sum[i];
+              same += o == k;
+            }
+            const unsigned long long w = s.sum[tid];
+            if (before < goal && before + same * w >= goal) s.cut = SpCut{k, (goal - before + w - 1) / w};  // (equal ones agree)
+          }
+          __syncthreads();
+          out = s.cut;
+          return;
+        }
+        shift = 0;
+        while (((khi - klo) >> shift) >= kSpBins) ++shift;
+        __syncthreads();
+      }
+    };
+    if (by_k) {
+      find_listed(false, (unsigned long long)top_k, 0, 0u, cut);
+      if (by_p) {
+        unsigned long long w = 0, none = 0;
+        each_listed([&](int i, int) {
+          if (key_of(list_v[i]) > cut.key) w += weight(list_v[i]);
+        });
+        cta_sum(s, w, none);
+        const unsigned long long w_tie = weight(key_float(cut.key)), goal = share(w + cut.ties * w_tie);
+        if (w >= goal) find_listed(true, goal, 0, cut.key, cut);
+        else cut.ties = w_tie ? (goal - w + w_tie - 1) / w_tie : 1;
+      }
+    } else {
+      find_listed(true, target, above, 0u, cut);
+    }
+  }
+  const bool tied = cut.key && cut.ties != ~0ull && cut.key >= floor_key;
+  const unsigned least = tied ? cut.key : max(cut.key, floor_key);
+  if (listed) {
+    // the lists' part of what is kept of each run
+    __syncthreads();
+    for (int r = warp; r < runs; r += kSpWarps) {
+      const unsigned n = s.run_listed[r];
+      unsigned long long w = 0;
+      unsigned c = 0, eq = 0;
+      for (unsigned i = lane; i < n; i += 32) {
+        const float v = list_v[r * cap + i];
+        const unsigned k = key_of(v);
+        if (k > least || (!tied && k == least)) {
+          w += weight(v);
+          ++c;
+        }
+        eq += k == least;
+      }
+      w = warp_sum(w);
+      c = __reduce_add_sync(0xffffffffu, c);
+      eq = __reduce_add_sync(0xffffffffu, eq);
+      if (lane == 0) {
+        s.run_mass[r] += w;
+        s.run_count[r] += c;
+        s.run_equal[r] = tied ? eq : 0u;
+      }
+    }
+  }
   __syncthreads();
+  // ---- the run that holds the border (equal values are taken in the order of the runs)
+  const unsigned long long w_tie = tied ? weight(key_float(cut.key)) : 0ull;
+  if (warp == 0) {
+    unsigned long long left = tied ? cut.ties : 0, total = 0, kept = 0;
+    for (int r0 = 0; r0 < runs; r0 += 32) {
+      unsigned long long eq = r0 + lane < runs ? s.run_equal[r0 + lane] : 0, upto = eq;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const unsigned long long had = min(left, upto - eq), take = min(left, upto) - had;
+      if (r0 + lane < runs) {
+        s.run_equal[r0 + lane] = (unsigned)take;  // from here on: how many of them are kept
+        s.run_mass[r0 + lane] += take * w_tie;
+        total += s.run_mass[r0 + lane];
+        kept += s.run_count[r0 + lane] + take;
+      }
+      left -= min(left, __shfl_sync(0xffffffffu, upto, 31));
+    }
+    total = warp_sum(total);
+    kept = warp_sum(kept);
+    const unsigned long long goal = __umul64hi(total, fraction(u));  // the first running sum above it
+    unsigned long long run = 0;
+    for (int r0 = 0; r0 < runs; r0 += 32) {
+      const unsigned long long w = r0 + lane < runs ? s.run_mass[r0 + lane] : 0;
+      unsigned long long upto = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (goal >= run + upto - w && goal < run + upto) {
+        s.found_bin = r0 + lane;
+        s.found_above = run + upto - w;
+      }
+      run += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) {
+      s.found_total = total;
+      s.board[0].a[0] = goal;
+      if (a.kept) a.kept[row] = (int)min(kept, (unsigned long long)INT_MAX);
+    }
+  }
+  __syncthreads();
+  const int r = s.found_bin, f = run_first(r), l = run_last(r);
+  const unsigned long long goal = s.board[0].a[0], total = s.found_total;
+  unsigned long long now = s.found_above, left = s.run_equal[r];
+  // ---- a piece of it for each warp, and the piece that holds the border by its warp
+  const int piece = ((l - f + kSpWarps - 1) / kSpWarps + 127) / 128 * 128, i0 = min(l, f + warp * piece), i1 = min(l, i0 + piece);
+  unsigned long long w;
+  unsigned c, eq;
+  sum_run(least, !tied, i0, i1, w, c, eq);
   if (lane == 0) {
     s.warp_a[warp] = w;
-    s.warp_b[warp] = eq;
+    s.warp_b[warp] = tied ? eq : 0u;
   }
   __syncthreads();
-  unsigned long long run = before;
-  left = left_here;
   for (int x = 0; x < warp; ++x) {
     const unsigned long long take = min(left, s.warp_b[x]);
-    run += s.warp_a[x] + take * w_tie;
+    now += s.warp_a[x] + take * w_tie;
     left -= take;
   }
-  if (target < run || target >= run + s.warp_a[warp] + min(left, s.warp_b[warp]) * w_tie) return;
-  for (int j = j0 + lane; j - lane < j1; j += 32) {
-    const float4 v4 = j < j1 ? value4(j) : make_float4(kNone, kNone, kNone, kNone);
+  if (goal < now || goal >= now + w + min(left, s.warp_b[warp]) * w_tie) return;
+  for (int i = i0 + 4 * lane; i - 4 * lane < i1; i += 128) {
+    const float4 v4 = i < i1 ? load4(i, i1) : make_float4(kNone, kNone, kNone, kNone);
     const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
     unsigned long long ws[4], sum = 0;
     unsigned equal = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const unsigned k = key_of(vs[e]);
-      const bool there = vs[e] >= -FLT_MAX;
-      ws[e] = there && in_run(k) ? weight(vs[e]) : 0ull;
-      equal |= (there && tied && k == cut.key ? 1u : 0u) << e;
+      const unsigned k = vs[e] >= -FLT_MAX ? key_of(vs[e]) : 0u;
+      ws[e] = k > least || (!tied && k == least) ? weight(vs[e]) : 0ull;
+      equal |= (tied && k == least ? 1u : 0u) << e;
     }
     // the equal ones' places
-    unsigned places = __popc(equal), upto = places;
+    unsigned upto = __popc(equal);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
     }
-    unsigned long long place = upto - places;
+    unsigned long long place = upto - __popc(equal);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (equal >> e & 1) {
@@ -864,31 +992,29 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += x;
     }
-    unsigned long long now = run + inc - sum;
+    unsigned long long at = now + inc - sum;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (ws[e] && target >= now && target < now + ws[e]) {
-        const float v = vs[e];
-        a.token[row] = base + 4 * j + e;
-        if (a.kept) a.kept[row] = (int)min(kept, (unsigned long long)INT_MAX);
+      if (ws[e] && goal >= at && goal < at + ws[e]) {
+        a.token[row] = i + e;
         if (a.logprob)
-          a.logprob[row] = greedy ? 0.f : (float)(((double)v - (double)sc.base) / (double)T -
+          a.logprob[row] = greedy ? 0.f : (float)(((double)vs[e] - (double)sc.base) / (double)T -
                                                   log((double)total) + 0.69314718055994530942 * (kSpTop - sc.nref));
       }
-      now += ws[e];
+      at += ws[e];
     }
-    const unsigned total_eq = __shfl_sync(0xffffffffu, upto, 31);
-    left -= min(left, (unsigned long long)total_eq);
-    run += __shfl_sync(0xffffffffu, inc, 31);
-    if (run > target) return;
+    left -= min(left, (unsigned long long)__shfl_sync(0xffffffffu, upto, 31));
+    now += __shfl_sync(0xffffffffu, inc, 31);
+    if (now > goal) return;
   }
 }
 
-// CTAs of a row's cluster: slices of up to 16384 values, so that two CTAs share an SM
-// and one row's values come while another's are worked on.
-int sample_ctas(int V) {
+// CTAs of a row's cluster: slices of 65536 values at most (so many rows under way fit
+// L2), shorter ones as long as there are SMs for them and 2048 values for each.
+int sample_ctas(int R, int V) {
   int c = 1;
-  while (c < kSpMaxCluster && (int64_t)c * 16384 < V) c *= 2;
+  while (c < kSpMaxCluster && (int64_t)c * 65536 < V) c *= 2;
+  while (c < kSpMaxCluster && (int64_t)R * c * 2 <= 2 * kTargetCtas && V >= 2 * c * 2048) c *= 2;
   return c;
 }
 
@@ -924,7 +1050,7 @@ extern "C" dg_status dg_sample(const void* logits, int32_t bf16, int64_t ld, int
     for (int j = 0; j < kSpTable; ++j) t.t[j] = (uint32_t)std::llround(std::ldexp(std::exp2(j / (double)kSpTable), 29));
     return t;
   }();
-  const int ctas = sample_ctas(V);
+  const int ctas = sample_ctas(R, V);
   SpArgs a{};
   a.logits = logits;
   a.u = u;
@@ -938,20 +1064,21 @@ extern "C" dg_status dg_sample(const void* logits, int32_t bf16, int64_t ld, int
   a.ld = ld;
   a.R = R;
   a.V = V;
-  a.slice = cdiv(cdiv(V, ctas), 8) * 8;
-  a.held = a.slice < kSpHeld ? a.slice : kSpHeld;
+  a.run4 = cdiv(cdiv(V, ctas * kSpWarps * 4), 32) * 32;
+  a.slice = a.run4 * 4 * kSpWarps;
+  a.step = a.slice >= 32768 ? 8 : a.slice >= 16384 ? 4 : a.slice >= 8192 ? 2 : 1;
   a.bf16 = bf16 != 0;
   a.temperature_all = how->temperature_all;
   a.top_p_all = how->top_p_all;
   a.min_p_all = how->min_p_all;
   a.top_k_all = how->top_k_all;
-  cudaError_t e = set_smem_once<sample_kernel>(kSpHeld * (int)sizeof(float));
+  cudaError_t e = set_smem_once<sample_kernel>(kSpSmem);
   if (e == cudaSuccess) e = allow_large_clusters();
   if (e != cudaSuccess) return DG_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(R, ctas);
   cfg.blockDim = dim3(kSpThreads);
-  cfg.dynamicSmemBytes = sizeof(float) * a.held;
+  cfg.dynamicSmemBytes = kSpSmem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
