@@ -44,14 +44,14 @@ constexpr int kSpBins = 2048;
 constexpr int kSpMaxV = 1 << 20;
 constexpr int kSpKeys = 512;                  // keys of a bin that are compared with one another
 constexpr int kSpSample = 8192;               // longer vocabularies are sampled first
-constexpr int kSpSide = 512;                  // sampled values on either side of a bracket
+constexpr int kSpSide = 384;                  // sampled values on either side of a bracket
 constexpr int kSpTries = 3;
 constexpr int kSpMaxCluster = 16;
 constexpr int kSpRuns = kSpMaxCluster * kSpWarps;
 constexpr int kSpCap = 640;                   // listed values of a run, over the CTAs of a row
 constexpr int kSpTable = 128;                 // 2^(j / 128)
 constexpr int kSpTop = 43;                    // a weight of the row's scale is 2^43: 2^20 of them stay below 2^63
-constexpr float kSpUnit = 32.0f;              // bins of the first histogram to a factor of two in weight
+constexpr float kSpFar = 64.0f;               // factors of two below the largest weight at which nothing weighs
 constexpr float kNone = -INFINITY;            // behind the end, or banned
 
 struct SpArgs {
@@ -404,9 +404,11 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     if (tid == kSpThreads - 1) s.found_total = above + run[3];
     __syncthreads();
   };
-  // bins of the first histogram: linear below the maximum
-  auto bin1 = [&](float v) { return (int)fminf((m - v) * (sc.c * kSpUnit), (float)(kSpBins - 1)); };
-  const float unit = 1.0f / (sc.c * kSpUnit);
+  // bins of the first histogram: linear from the maximum down to the lowest value, or
+  // to where nothing weighs
+  const float bottom = fmaxf(key_float(lowest), m - kSpFar / sc.c);
+  const float unit = (m - bottom) / (float)kSpBins, per_unit = fminf((float)kSpBins / (m - bottom), FLT_MAX);
+  auto bin1 = [&](float v) { return (int)fminf((m - v) * per_unit, (float)(kSpBins - 1)); };
   // the bounds of two keys over the CTA's threads, in s.key_lo and s.key_hi
   auto bounds = [&](unsigned lo, unsigned hi) {
     lo = __reduce_min_sync(0xffffffffu, lo);
@@ -539,12 +541,23 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     cut.key = mkey;
     cut.ties = 1;
   } else if (by_k || by_p) {
-    // ---- a bracket.  Without a sample: down to the lowest value, or where nothing weighs
-    lo = fmaxf(key_float(lowest), m - (float)kSpBins * unit);
+    // ---- a bracket: without a sample, all values
+    lo = bottom;
     // of the sample: the running sum and count at a thread's bins
     unsigned long long run[4], count[4];
     const int bits = 28 - (32 - __clz(a.slice / a.step));  // a weight's, so that the whole sample's sum fits 32
-    const bool sampled = a.V > kSpSample && (by_k || !floored);
+    const bool sampled = a.V > kSpSample;
+    const float floor_v = key_float(max(floor_key, 0x00800000u));
+    // What min_p leaves out needs no list: a bracket that ends below its floor begins
+    // there, and one that lies below it is empty, with all from the floor on above it.
+    auto at_floor = [&]() {
+      if (by_k || !floored || lo >= floor_v) return;
+      lo = floor_v;
+      if (hi < floor_v) {
+        hi = key_float(floor_key - 1u);
+        lo = INFINITY;
+      }
+    };
     // The bracket about the bin at which the sample's mass (or count) reaches `goal`: the
     // values that lie kSpSide sampled ones before and behind.
     auto bracket = [&](float goal) {
@@ -576,7 +589,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       }
       __syncthreads();
       hi = by_k ? m : s.bracket_hi;  // (the first k are all listed)
-      lo = fmaxf(fmaxf(key_float(lowest), m - (float)kSpBins * unit), s.bracket_lo);
+      lo = fmaxf(bottom, s.bracket_lo);
     };
     if (sampled) {
       clear(true);
@@ -601,12 +614,13 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       if (tid == kSpThreads - 1) s.warp_b[0] = run[3];
       __syncthreads();
       bracket(fmaxf(by_k ? (float)top_k / (float)a.step : top_p * (float)s.warp_b[0], 1e-30f));
-    } else if (floored && !by_k) {
-      lo = key_float(floor_key);  // what lies below is not kept anyway
     }
+    const float sample_sum = sampled ? (float)s.warp_b[0] : 0.f;
+    __syncthreads();
 
     // ---- all values: their sum, what lies above the bracket, and the lists
     for (int round = 0; round < kSpTries; ++round) {
+      at_floor();
       unsigned long long w_all = 0, w_above = 0, w_list = 0;
       unsigned c_above = 0, n_list = 0;
       float* my_v = list_v + warp * cap;
@@ -699,19 +713,20 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         listed = t_n < (1ull << 40) && t_n >= (unsigned long long)top_k;
       } else {
         target = share(all);
-        const bool border = above < target && (above + t_list >= target || floored);
+        // (the border lies in the bracket, or below the floor, where it is of no matter)
+        const bool border = above < target && (above + t_list >= target || (floored && lo >= floor_v));
         listed = border && t_n < (1ull << 40);
         if (!border && sampled && round + 1 < kSpTries) {
           // the sample's own sums from the nearer end of the bracket on
           const bool before = above >= target;
-          const float edge = before ? hi : lo;
+          const float edge = before ? hi : fminf(lo, hi);
           const int b = min(kSpBins - 1, max(0, (int)rintf((m - edge) / unit)));  // the first bin behind the edge
           if (b / 4 == tid) s.found_total = run[b % 4] - (s.sum[b] & 0xffffffffull);
           __syncthreads();
           const float at_edge = (float)s.found_total;
           const float off = before ? -(float)(above - target) : (float)(target - above - t_list);
           __syncthreads();
-          bracket(fmaxf(at_edge + off * exp2f((float)(bits - kSpTop)) / (float)a.step, 1e-30f));
+          bracket(fminf(fmaxf(at_edge + off * exp2f((float)(bits - kSpTop)) / (float)a.step, 1e-30f), sample_sum));
           continue;
         }
       }
