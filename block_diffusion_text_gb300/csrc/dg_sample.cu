@@ -131,17 +131,19 @@ DG_DEV void st_cluster_u64(uint32_t a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
-// The weight of a value, 2^(x - nref + 43) rounded down to a whole number.  x = l c is
-// taken as a sum of two floats, so that r = x - k / 128 keeps all its bits; 2^(k / 128)
-// comes from the table and 2^r - 1 from three terms of its series (the fourth is
-// below 2^-38); their product is added in units of 2^-29 of the table's scale.
-DG_DEV unsigned long long weight_of(float v, const SpScale& s, const uint2* pow2) {
+// The weight of a value, 2^(x - nref + 43) rounded down to a whole number, as m << e.
+// x = l c is taken as a sum of two floats, so that r = x - k / 128 keeps all its bits;
+// 2^(k / 128) comes from the table and 2^r - 1 from three terms of its series (the
+// fourth is below 2^-38); their product is added in units of 2^-29 of the table's scale.
+struct SpWeight {
+  unsigned m, p;  // m p
+  DG_DEV void add_to(unsigned long long& sum) const { sum += (unsigned long long)m * p; }
+};
+DG_DEV SpWeight weight_parts(float v, const SpScale& s, const uint2* pow2) {
   const float l = v - s.base;
   const float x = l * s.c;
   float e = fmaf(l, s.c, -x);
   e = fmaf(l, s.clo, e);
-  // values far below the largest weigh nothing (and x may be -inf)
-  if (!(x > (float)(s.nref - 64))) return 0ull;
   // 128 x, rounded: the sum with 1.5 2^23 holds it in its low bits (|x| is below 2^15)
   const float y = fmaf(x, 128.0f, 12582912.0f);
   const int k = __float_as_int(y) - 0x4b400000;
@@ -149,8 +151,15 @@ DG_DEV unsigned long long weight_of(float v, const SpScale& s, const uint2* pow2
   const float q = r * fmaf(r, fmaf(r, 0.05550410866f, 0.2402265070f), 0.6931471806f);
   const uint2 t = pow2[k & (kSpTable - 1)];
   // t q, rounded, the same way (below 2^22)
-  const unsigned m = t.x + (__float_as_uint(fmaf(__uint_as_float(t.y), q, 12582912.0f)) - 0x4b400000u);
-  return ((unsigned long long)m << 32) >> min(32 + 29 - kSpTop + s.nref - (k >> 7), 63);  // by 19 and more
+  unsigned m = t.x + (__float_as_uint(fmaf(__uint_as_float(t.y), q, 12582912.0f)) - 0x4b400000u);
+  // values far below the largest weigh nothing (and x may be -inf)
+  if (!(x > (float)(s.nref - 64))) m = 0u;
+  const int up = kSpTop - 29 - s.nref + (k >> 7), shift = min(max(up, 0), 31);
+  return SpWeight{m >> min(shift - up, 31), 1u << shift};
+}
+DG_DEV unsigned long long weight_of(float v, const SpScale& s, const uint2* pow2) {
+  const SpWeight w = weight_parts(v, s, pow2);
+  return (unsigned long long)w.m * w.p;
 }
 
 DG_DEV unsigned long long warp_sum(unsigned long long v) {
@@ -350,11 +359,12 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       return;
     }
     cluster_sync();
-    const int per = kSpBins / (int)ctas, b0 = (int)rank * per;
-    for (int i = b0 + tid; i < b0 + per; i += kSpThreads) {
+    // the CTA's kSpBins / ctas bins, `team` neighbouring threads to each
+    const int per = kSpBins / (int)ctas, b0 = (int)rank * per, team = max(1, kSpThreads / per), mate = tid % team;
+    for (int i = b0 + tid / team; i < b0 + per; i += kSpThreads / team) {
       unsigned long long t = 0;
 #pragma unroll 4
-      for (uint32_t c = 0; c < ctas; ++c) {
+      for (uint32_t c = mate; c < ctas; c += team) {
         unsigned long long x;
         if (what == 0) {
           x = ld_cluster_u32(cluster_addr(&s.count[i], c));
@@ -364,7 +374,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         }
         t += x;
       }
-      for (uint32_t c = 0; c < ctas; ++c) st_cluster_u64(cluster_addr(&s.sum[i], c), t);
+      for (int o = 1; o < team; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      for (uint32_t c = mate; c < ctas; c += team) st_cluster_u64(cluster_addr(&s.sum[i], c), t);
     }
     cluster_sync();
   };
@@ -510,9 +521,11 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       for (int e = 0; e < 4; ++e) {
         const unsigned k = vs[e] >= -FLT_MAX ? key_of(vs[e]) : 0u;
         const bool in = k > least || (from && k == least);
-        const unsigned long long x = weight(vs[e]);
-        w += in ? x : 0ull;
-        c += in;
+        const SpWeight x = weight_parts(vs[e], sc, s.pow2);
+        if (in) {
+          x.add_to(w);
+          ++c;
+        }
         eq += k == least;
       }
     }
@@ -621,47 +634,59 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     // ---- all values: their sum, what lies above the bracket, and the lists
     for (int round = 0; round < kSpTries; ++round) {
       at_floor();
-      unsigned long long w_all = 0, w_above = 0, w_list = 0;
+      unsigned long long w_below = 0, w_above = 0, w_list = 0;
       unsigned c_above = 0, n_list = 0;
       float* my_v = list_v + warp * cap;
       uint16_t* my_at = list_at + warp * cap;
-      for (int i = first + 4 * lane; i - 4 * lane < last; i += 128) {
-        const float4 v4 = i < last ? load4(i, last) : make_float4(kNone, kNone, kNone, kNone);
+      auto listed_of = [&](const float4& v4, int i) {  // the four values that lie in the bracket
         const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
         unsigned inside = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool ge = vs[e] >= lo, gt = vs[e] > hi;
-          if (!by_k) {
-            const unsigned long long x = weight(vs[e]);
-            w_all += x;
-            w_above += gt ? x : 0ull;
-            w_list += ge && !gt ? x : 0ull;
-            c_above += gt;
-          }
-          inside |= (ge && !gt ? 1u : 0u) << e;
+        for (int e = 0; e < 4; ++e) inside |= (vs[e] >= lo && vs[e] <= hi ? 1u : 0u) << e;
+        if (!__any_sync(0xffffffffu, inside)) return;
+        unsigned upto = __popc(inside);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
         }
-        if (__any_sync(0xffffffffu, inside)) {
-          unsigned upto = __popc(inside);
+        unsigned at = n_list + upto - __popc(inside);
+        n_list += __shfl_sync(0xffffffffu, upto, 31);
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
-          }
-          unsigned at = n_list + upto - __popc(inside);
-          n_list += __shfl_sync(0xffffffffu, upto, 31);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (inside >> e & 1) {
-              if (at < (unsigned)cap) {
-                my_v[at] = vs[e];
-                my_at[at] = (uint16_t)(i + e - first);
-              }
-              ++at;
+        for (int e = 0; e < 4; ++e)
+          if (inside >> e & 1) {
+            if (at < (unsigned)cap) {
+              my_v[at] = vs[e];
+              my_at[at] = (uint16_t)(i + e - first);
             }
+            ++at;
+          }
+      };
+      if (by_k) {
+#pragma unroll 2
+        for (int i = first + 4 * lane; i - 4 * lane < last; i += 128)
+          listed_of(i < last ? load4(i, last) : make_float4(kNone, kNone, kNone, kNone), i);
+      } else {
+#pragma unroll 1
+        for (int i = first + 4 * lane; i - 4 * lane < last; i += 128) {
+          const float4 v4 = i < last ? load4(i, last) : make_float4(kNone, kNone, kNone, kNone);
+          const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const SpWeight x = weight_parts(vs[e], sc, s.pow2);
+            if (vs[e] > hi) {
+              x.add_to(w_above);
+              ++c_above;
+            } else {
+              x.add_to(w_below);
+            }
+          }
+          listed_of(v4, i);
         }
+        __syncwarp();
+        for (unsigned i = lane; i < min(n_list, (unsigned)cap); i += 32) w_list += weight(my_v[i]);
       }
-      w_all = warp_sum(w_all);
+      unsigned long long w_all = warp_sum(w_below + w_above);
       w_above = warp_sum(w_above);
       w_list = warp_sum(w_list);
       c_above = __reduce_add_sync(0xffffffffu, c_above);
@@ -713,7 +738,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         listed = t_n < (1ull << 40) && t_n >= (unsigned long long)top_k;
       } else {
         target = share(all);
-        // (the border lies in the bracket, or below the floor, where it is of no matter)
+        // (the border lies in the bracket, or below the floor, where it is of no matter; a
+        // list that ran over is not added up)
         const bool border = above < target && (above + t_list >= target || (floored && lo >= floor_v));
         listed = border && t_n < (1ull << 40);
         if (!border && sampled && round + 1 < kSpTries) {
@@ -786,28 +812,48 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   if (rank > 0) return;
 
   // ================================================================= the leader
-  const int slots = runs * cap;
+  // a team of threads for every run's list (a warp at most: there are 16 runs at least)
+  const int team = kSpThreads / runs, my_run = tid / team, mate = tid % team;
   auto each_listed = [&](auto&& f) {
-    for (int i = tid; i < slots; i += kSpThreads) {
-      const int r = i / cap;
-      if (i - r * cap < (int)s.run_listed[r]) f(i, r);
+    const int n = (int)s.run_listed[my_run];
+    for (int i = mate; i < n; i += team) f(list_v[my_run * cap + i]);
+  };
+  // The inclusive running sum over the CTA's threads
+  auto scan = [&](unsigned long long x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    __syncthreads();
+    if (lane == 31) s.warp_a[warp] = x;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) x += s.warp_a[w];
+    return x;
   };
   if (listed) {
     // One cut among the listed values above key `in`: bins linear in the value, and where
     // a bin holds too many different ones, over the bits of their keys.
     auto find_listed = [&](bool mass, unsigned long long goal, unsigned long long over, unsigned in, SpCut& out) {
-      const float scale = fminf((float)(kSpBins - 1) / (hi - lo), FLT_MAX);
+      constexpr int kBins = kSpThreads;  // a thread's each
+      const float scale = fminf((float)kBins / (hi - lo), FLT_MAX);
       unsigned khi = 0, klo = 0;
       int shift = -1;
       auto bin_of = [&](float v, unsigned k) {
-        if (shift < 0) return (int)fminf((hi - v) * scale, (float)(kSpBins - 1));
+        if (shift < 0) return (int)fminf((hi - v) * scale, (float)(kBins - 1));
         return k > khi || k < klo ? -1 : (int)((khi - k) >> shift);
       };
       for (int level = 0; level < 6; ++level) {
-        clear(mass);
-        each_listed([&](int i, int) {
-          const float v = list_v[i];
+        __syncthreads();
+        s.count[tid] = s.lo[tid] = s.hi[tid] = 0u;
+        if (tid == 0) {
+          s.found_bin = -1;
+          s.nkeys = 0;
+          s.key_lo = 0xffffffffu;
+          s.key_hi = 0;
+        }
+        __syncthreads();
+        each_listed([&](float v) {
           const unsigned k = key_of(v);
           if (k <= in) return;
           const int b = bin_of(v, k);
@@ -816,21 +862,25 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           else atomicAdd(&s.count[b], 1u);
         });
         __syncthreads();
-        find_bin(over, goal, [&](int i) { return mass ? s.lo[i] + ((unsigned long long)s.hi[i] << 32) : (unsigned long long)s.count[i]; });
+        const unsigned long long mine_w = mass ? s.lo[tid] + ((unsigned long long)s.hi[tid] << 32) : (unsigned long long)s.count[tid];
+        const unsigned long long upto = over + scan(mine_w);
+        if (upto >= goal && upto - mine_w < goal) {
+          s.found_bin = tid;
+          s.found_above = upto - mine_w;
+        }
+        __syncthreads();
         const int bin = s.found_bin;
         if (bin < 0) return;
         over = s.found_above;
-        unsigned lo_key = 0xffffffffu, hi_key = 0u;
-        each_listed([&](int i, int) {
-          const float v = list_v[i];
+        each_listed([&](float v) {
           const unsigned k = key_of(v);
           if (k <= in || bin_of(v, k) != bin) return;
-          lo_key = min(lo_key, k);
-          hi_key = max(hi_key, k);
           const unsigned at = atomicAdd(&s.nkeys, 1u);
+          atomicMin(&s.key_lo, k);
+          atomicMax(&s.key_hi, k);
           if (at < kSpKeys) s.keys[at] = k;
         });
-        bounds(lo_key, hi_key);
+        __syncthreads();
         klo = s.key_lo;
         khi = s.key_hi;
         const unsigned n = s.nkeys;
@@ -838,7 +888,6 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           const unsigned long long w = mass ? weight(key_float(klo)) : 1ull;
           out.key = klo;
           out.ties = (goal - over + w - 1) / w;
-          __syncthreads();
           return;
         }
         if (n <= kSpKeys) {
@@ -861,16 +910,15 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           return;
         }
         shift = 0;
-        while (((khi - klo) >> shift) >= kSpBins) ++shift;
-        __syncthreads();
+        while (((khi - klo) >> shift) >= kBins) ++shift;
       }
     };
     if (by_k) {
       find_listed(false, (unsigned long long)top_k, 0, 0u, cut);
       if (by_p) {
         unsigned long long w = 0, none = 0;
-        each_listed([&](int i, int) {
-          if (key_of(list_v[i]) > cut.key) w += weight(list_v[i]);
+        each_listed([&](float v) {
+          if (key_of(v) > cut.key) w += weight(v);
         });
         cta_sum(s, w, none);
         const unsigned long long w_tie = weight(key_float(cut.key)), goal = share(w + cut.ties * w_tie);
@@ -883,80 +931,50 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   }
   const bool tied = cut.key && cut.ties != ~0ull && cut.key >= floor_key;
   const unsigned least = tied ? cut.key : max(cut.key, floor_key);
-  if (listed) {
-    // the lists' part of what is kept of each run
-    __syncthreads();
-    for (int r = warp; r < runs; r += kSpWarps) {
-      const unsigned n = s.run_listed[r];
-      unsigned long long w = 0;
-      unsigned c = 0, eq = 0;
-      for (unsigned i = lane; i < n; i += 32) {
-        const float v = list_v[r * cap + i];
-        const unsigned k = key_of(v);
-        if (k > least || (!tied && k == least)) {
-          w += weight(v);
-          ++c;
-        }
-        eq += k == least;
-      }
-      w = warp_sum(w);
-      c = __reduce_add_sync(0xffffffffu, c);
-      eq = __reduce_add_sync(0xffffffffu, eq);
-      if (lane == 0) {
-        s.run_mass[r] += w;
-        s.run_count[r] += c;
-        s.run_equal[r] = tied ? eq : 0u;
-      }
-    }
-  }
-  __syncthreads();
-  // ---- the run that holds the border (equal values are taken in the order of the runs)
+  // ---- what is kept of each run (in its team's first thread), and the run that holds
+  // the border; equal values are taken in the order of the runs
   const unsigned long long w_tie = tied ? weight(key_float(cut.key)) : 0ull;
-  if (warp == 0) {
-    unsigned long long left = tied ? cut.ties : 0, total = 0, kept = 0;
-    for (int r0 = 0; r0 < runs; r0 += 32) {
-      unsigned long long eq = r0 + lane < runs ? s.run_equal[r0 + lane] : 0, upto = eq;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
+  unsigned long long run_w = 0, run_c = 0, run_eq = 0;
+  if (listed) {
+    each_listed([&](float v) {
+      const unsigned k = key_of(v);
+      if (k > least || (!tied && k == least)) {
+        run_w += weight(v);
+        ++run_c;
       }
-      const unsigned long long had = min(left, upto - eq), take = min(left, upto) - had;
-      if (r0 + lane < runs) {
-        s.run_equal[r0 + lane] = (unsigned)take;  // from here on: how many of them are kept
-        s.run_mass[r0 + lane] += take * w_tie;
-        total += s.run_mass[r0 + lane];
-        kept += s.run_count[r0 + lane] + take;
-      }
-      left -= min(left, __shfl_sync(0xffffffffu, upto, 31));
+      run_eq += tied && k == least;
+    });
+    for (int o = 1; o < team; o <<= 1) {
+      run_w += __shfl_xor_sync(0xffffffffu, run_w, o);
+      run_c += __shfl_xor_sync(0xffffffffu, run_c, o);
+      run_eq += __shfl_xor_sync(0xffffffffu, run_eq, o);
     }
-    total = warp_sum(total);
-    kept = warp_sum(kept);
-    const unsigned long long goal = __umul64hi(total, fraction(u));  // the first running sum above it
-    unsigned long long run = 0;
-    for (int r0 = 0; r0 < runs; r0 += 32) {
-      const unsigned long long w = r0 + lane < runs ? s.run_mass[r0 + lane] : 0;
-      unsigned long long upto = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-      }
-      if (goal >= run + upto - w && goal < run + upto) {
-        s.found_bin = r0 + lane;
-        s.found_above = run + upto - w;
-      }
-      run += __shfl_sync(0xffffffffu, upto, 31);
+  } else {
+    run_eq = s.run_equal[my_run];
+  }
+  run_w = mate == 0 ? run_w + s.run_mass[my_run] : 0;
+  run_c = mate == 0 ? run_c + s.run_count[my_run] : 0;
+  run_eq = mate == 0 ? run_eq : 0;
+  {
+    const unsigned long long ties = tied ? cut.ties : 0, upto = scan(run_eq), had = min(ties, upto - run_eq);
+    run_eq = min(ties, upto) - had;  // from here on: how many of them are kept
+    run_w += run_eq * w_tie;
+    const unsigned long long w_upto = scan(run_w), c_upto = scan(run_c + run_eq);
+    if (tid == kSpThreads - 1) {
+      s.found_total = w_upto;
+      if (a.kept) a.kept[row] = (int)min(c_upto, (unsigned long long)INT_MAX);
     }
-    if (lane == 0) {
-      s.found_total = total;
-      s.board[0].a[0] = goal;
-      if (a.kept) a.kept[row] = (int)min(kept, (unsigned long long)INT_MAX);
+    __syncthreads();
+    const unsigned long long goal = __umul64hi(s.found_total, fraction(u));  // the first running sum above it
+    if (goal >= w_upto - run_w && goal < w_upto) {
+      s.found_bin = my_run;
+      s.found_above = w_upto - run_w;
+      s.run_equal[my_run] = (unsigned)run_eq;
     }
   }
   __syncthreads();
   const int r = s.found_bin, f = run_first(r), l = run_last(r);
-  const unsigned long long goal = s.board[0].a[0], total = s.found_total;
+  const unsigned long long total = s.found_total, goal = __umul64hi(total, fraction(u));
   unsigned long long now = s.found_above, left = s.run_equal[r];
   // ---- a piece of it for each warp, and the piece that holds the border by its warp
   const int piece = ((l - f + kSpWarps - 1) / kSpWarps + 127) / 128 * 128, i0 = min(l, f + warp * piece), i1 = min(l, i0 + piece);
