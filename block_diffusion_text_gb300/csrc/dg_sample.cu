@@ -98,7 +98,7 @@ struct alignas(16) SpShared {
   unsigned long long sum[kSpBins];        // the bins, summed over the cluster
   uint2 pow2[kSpTable];                   // the table entry as an integer and as a float
   SpBoard board[4];
-  unsigned long long warp_a[kSpWarps], warp_b[kSpWarps];
+  unsigned long long warp_a[kSpWarps], warp_b[kSpWarps], part[4][kSpWarps];
   // the leader's: of every run of the row, the mass and the number of values above the
   // bracket (or of all that is kept), how many are equal to the cut, how many listed
   unsigned long long run_mass[kSpRuns];
@@ -114,7 +114,7 @@ struct alignas(16) SpShared {
 };
 
 static_assert(sizeof(SpShared) % 16 == 0, "the lists lie behind it");
-constexpr int kSpSmem = (int)sizeof(SpShared) + kSpWarps * kSpCap * 6;
+constexpr int kSpSmem = (int)sizeof(SpShared) + kSpWarps * kSpCap * 4;
 
 DG_DEV unsigned ld_cluster_u32(uint32_t a) {
   unsigned v;
@@ -123,9 +123,6 @@ DG_DEV unsigned ld_cluster_u32(uint32_t a) {
 }
 DG_DEV void st_cluster_u32(uint32_t a, unsigned v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-DG_DEV void st_cluster_u16(uint32_t a, uint16_t v) {
-  asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory");
 }
 DG_DEV void st_cluster_u64(uint32_t a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
@@ -204,15 +201,15 @@ DG_DEV unsigned key_of(float v) { return float_key(v == 0.f ? 0.f : v); }
 __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTables tables) {
   extern __shared__ __align__(16) char smem[];
   SpShared& s = *reinterpret_cast<SpShared*>(smem);
-  // [run][cap] listed values, then their places in their runs: of the CTA's own runs,
-  // in the leader of all
+  // [run][cap] listed values, in any order: of the CTA's own runs, in the leader of all
   float* list_v = reinterpret_cast<float*>(smem + sizeof(SpShared));
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const uint32_t ctas = gridDim.y, rank = cluster_ctarank();
   const int row = blockIdx.x;
   const int cap = kSpCap / (int)ctas, runs = (int)ctas * kSpWarps;
-  uint16_t* list_at = reinterpret_cast<uint16_t*>(list_v + kSpWarps * kSpCap);
   const char* src = static_cast<const char*>(a.logits) + (size_t)row * a.ld * (a.bf16 ? 2 : 4);
+  // every CTA of the cluster runs before another writes to it: waited for below
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   for (int i = tid; i < kSpTable; i += kSpThreads) s.pow2[i] = make_uint2(tables.t[i], __float_as_uint((float)tables.t[i]));
 
@@ -270,7 +267,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     s.warp_a[warp] = ((unsigned long long)wrong << 32) | mkey;
     s.warp_b[warp] = ((unsigned long long)lowest << 32) | fin;
   }
-  cluster_sync();  // (every CTA of the cluster runs before another writes to it)
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __syncthreads();
   unsigned long long mw = 0, finite = 0;
   for (int w = 0; w < kSpWarps; ++w) {
     const unsigned long long x = s.warp_a[w];
@@ -556,8 +554,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   } else if (by_k || by_p) {
     // ---- a bracket: without a sample, all values
     lo = bottom;
-    // of the sample: the running sum and count at a thread's bins
-    unsigned long long run[4], count[4];
+    // of the sample: the running sum (low word) and count (high word) at a thread's bins
+    unsigned long long run[4];
     const int bits = 28 - (32 - __clz(a.slice / a.step));  // a weight's, so that the whole sample's sum fits 32
     const bool sampled = a.V > kSpSample;
     const float floor_v = key_float(max(floor_key, 0x00800000u));
@@ -583,9 +581,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const unsigned long long x = s.sum[4 * tid + e];
-        const float now = by_k ? (float)count[e] : (float)run[e];
-        const float was = by_k ? (float)(count[e] - (x >> 32)) : (float)(run[e] - (x & 0xffffffffull));
-        if (was < goal && now >= goal) s.found_above = count[e];
+        const float now = by_k ? (float)(run[e] >> 32) : (float)(unsigned)run[e];
+        const float was = by_k ? (float)((run[e] - x) >> 32) : (float)(unsigned)(run[e] - x);
+        if (was < goal && now >= goal) s.found_above = run[e] >> 32;
       }
       __syncthreads();
       const unsigned long long at = s.found_above;
@@ -593,11 +591,11 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int b = 4 * tid + e;
-          const unsigned long long prev = count[e] - (s.sum[b] >> 32);
+          const unsigned long long here = run[e] >> 32, prev = (run[e] - s.sum[b]) >> 32;
           // the last bin that ends kSpSide before, the first that ends kSpSide behind
-          if (b + 1 < kSpBins && count[e] + kSpSide <= at && count[e] + kSpSide + (s.sum[b + 1] >> 32) > at)
+          if (b + 1 < kSpBins && here + kSpSide <= at && here + kSpSide + (s.sum[b + 1] >> 32) > at)
             s.bracket_hi = m - (float)(b + 1) * unit;
-          if (b + 1 < kSpBins && count[e] >= at + kSpSide && prev < at + kSpSide) s.bracket_lo = m - (float)(b + 1) * unit;
+          if (b + 1 < kSpBins && here >= at + kSpSide && prev < at + kSpSide) s.bracket_lo = m - (float)(b + 1) * unit;
         }
       }
       __syncthreads();
@@ -622,9 +620,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         }
       }
       combine(2);
-      scan_bins(run, [&](int i) { return s.sum[i] & 0xffffffffull; });
-      scan_bins(count, [&](int i) { return s.sum[i] >> 32; });
-      if (tid == kSpThreads - 1) s.warp_b[0] = run[3];
+      scan_bins(run, [&](int i) { return s.sum[i]; });
+      if (tid == kSpThreads - 1) s.warp_b[0] = (unsigned)run[3];
       __syncthreads();
       bracket(fmaxf(by_k ? (float)top_k / (float)a.step : top_p * (float)s.warp_b[0], 1e-30f));
     }
@@ -637,39 +634,30 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       unsigned long long w_below = 0, w_above = 0, w_list = 0;
       unsigned c_above = 0, n_list = 0;
       float* my_v = list_v + warp * cap;
-      uint16_t* my_at = list_at + warp * cap;
-      auto listed_of = [&](const float4& v4, int i) {  // the four values that lie in the bracket
-        const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
-        unsigned inside = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) inside |= (vs[e] >= lo && vs[e] <= hi ? 1u : 0u) << e;
-        if (!__any_sync(0xffffffffu, inside)) return;
-        unsigned upto = __popc(inside);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += x;
-        }
-        unsigned at = n_list + upto - __popc(inside);
-        n_list += __shfl_sync(0xffffffffu, upto, 31);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (inside >> e & 1) {
-            if (at < (unsigned)cap) {
-              my_v[at] = vs[e];
-              my_at[at] = (uint16_t)(i + e - first);
-            }
-            ++at;
-          }
+      auto list = [&](float v) {  // if it lies in the bracket
+        const bool in = v >= lo && v <= hi;
+        const unsigned b = __ballot_sync(0xffffffffu, in), at = n_list + __popc(b & ((1u << lane) - 1));
+        if (in && at < (unsigned)cap) my_v[at] = v;
+        n_list += __popc(b);
       };
+      auto four = [&](int i) { return i < last ? load4(i, last) : make_float4(kNone, kNone, kNone, kNone); };
+      float4 next = four(first + 4 * lane);
       if (by_k) {
-#pragma unroll 2
-        for (int i = first + 4 * lane; i - 4 * lane < last; i += 128)
-          listed_of(i < last ? load4(i, last) : make_float4(kNone, kNone, kNone, kNone), i);
+#pragma unroll 1
+        for (int i = first + 4 * lane; i - 4 * lane < last; i += 128) {
+          const float4 v4 = next;
+          next = four(i + 128);
+          if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= lo)) continue;
+          list(v4.x);
+          list(v4.y);
+          list(v4.z);
+          list(v4.w);
+        }
       } else {
 #pragma unroll 1
         for (int i = first + 4 * lane; i - 4 * lane < last; i += 128) {
-          const float4 v4 = i < last ? load4(i, last) : make_float4(kNone, kNone, kNone, kNone);
+          const float4 v4 = next;
+          next = four(i + 128);
           const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -680,8 +668,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
             } else {
               x.add_to(w_below);
             }
+            list(vs[e]);
           }
-          listed_of(v4, i);
         }
         __syncwarp();
         for (unsigned i = lane; i < min(n_list, (unsigned)cap); i += 32) w_list += weight(my_v[i]);
@@ -692,46 +680,33 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       c_above = __reduce_add_sync(0xffffffffu, c_above);
       // the row's sums (a list that ran over is told by a count beyond any)
       const unsigned long long n_told = n_list > (unsigned)cap ? 1ull << 40 : n_list;
-      unsigned long long t_all = w_all, t_above = w_above, t_list = w_list, t_n = n_told;
-      __syncthreads();
       if (lane == 0) {
-        s.warp_a[warp] = w_all;
-        s.warp_b[warp] = w_above;
+        s.part[0][warp] = w_all;
+        s.part[1][warp] = w_above;
+        s.part[2][warp] = w_list;
+        s.part[3][warp] = n_told;
       }
       __syncthreads();
-      t_all = t_above = 0;
-      for (int w = 0; w < kSpWarps; ++w) {
-        t_all += s.warp_a[w];
-        t_above += s.warp_b[w];
-      }
-      __syncthreads();
-      if (lane == 0) {
-        s.warp_a[warp] = w_list;
-        s.warp_b[warp] = n_told;
-      }
-      __syncthreads();
-      t_list = t_n = 0;
-      for (int w = 0; w < kSpWarps; ++w) {
-        t_list += s.warp_a[w];
-        t_n += s.warp_b[w];
-      }
-      if (ctas > 1) {
-        const int x = round % 2 ? 0 : 2;  // boards in turns: the others may still read the last ones
-        if (tid < (int)ctas) {
-          st_cluster_u64(cluster_addr(&s.board[x].a[rank], tid), t_all);
-          st_cluster_u64(cluster_addr(&s.board[x].b[rank], tid), t_above);
-          st_cluster_u64(cluster_addr(&s.board[x + 1].a[rank], tid), t_list);
-          st_cluster_u64(cluster_addr(&s.board[x + 1].b[rank], tid), t_n);
-        }
-        cluster_sync();
-        t_all = t_above = t_list = t_n = 0;
-        for (uint32_t c = 0; c < ctas; ++c) {
-          t_all += s.board[x].a[c];
-          t_above += s.board[x].b[c];
-          t_list += s.board[x + 1].a[c];
-          t_n += s.board[x + 1].b[c];
+      unsigned long long t[4];
+      const int x = round % 2 ? 0 : 2;  // boards in turns: the others may still read the last ones
+      if (warp == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          t[q] = warp_sum(lane < kSpWarps ? s.part[q][lane] : 0ull);
+          if (lane < (int)ctas) st_cluster_u64(cluster_addr(q % 2 ? &s.board[x + q / 2].b[rank] : &s.board[x + q / 2].a[rank], lane), t[q]);
         }
       }
+      if (ctas > 1) cluster_sync();
+      else __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) t[q] = 0;
+      for (uint32_t c = 0; c < ctas; ++c) {
+        t[0] += s.board[x].a[c];
+        t[1] += s.board[x].b[c];
+        t[2] += s.board[x + 1].a[c];
+        t[3] += s.board[x + 1].b[c];
+      }
+      const unsigned long long t_all = t[0], t_above = t[1], t_list = t[2], t_n = t[3];
       above = t_above;
       all = t_all;
       if (by_k) {
@@ -747,7 +722,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           const bool before = above >= target;
           const float edge = before ? hi : fminf(lo, hi);
           const int b = min(kSpBins - 1, max(0, (int)rintf((m - edge) / unit)));  // the first bin behind the edge
-          if (b / 4 == tid) s.found_total = run[b % 4] - (s.sum[b] & 0xffffffffull);
+          if (b / 4 == tid) s.found_total = (unsigned)(run[b % 4] - s.sum[b]);
           __syncthreads();
           const float at_edge = (float)s.found_total;
           const float off = before ? -(float)(above - target) : (float)(target - above - t_list);
@@ -759,11 +734,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       if (listed) {
         tell_run(w_above, c_above, 0u, n_list);
         if (rank > 0) {
-          const uint32_t to_v = cluster_addr(list_v + mine * cap, 0), to_at = cluster_addr(list_at + mine * cap, 0);
-          for (unsigned i = lane; i < n_list; i += 32) {
-            st_cluster_u32(to_v + 4 * i, __float_as_uint(my_v[i]));
-            st_cluster_u16(to_at + 2 * i, my_at[i]);
-          }
+          const uint32_t to = cluster_addr(list_v + mine * cap, 0);
+          for (unsigned i = lane; i < n_list; i += 32) st_cluster_u32(to + 4 * i, __float_as_uint(my_v[i]));
         }
       }
       break;
@@ -959,12 +931,15 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     const unsigned long long ties = tied ? cut.ties : 0, upto = scan(run_eq), had = min(ties, upto - run_eq);
     run_eq = min(ties, upto) - had;  // from here on: how many of them are kept
     run_w += run_eq * w_tie;
-    const unsigned long long w_upto = scan(run_w), c_upto = scan(run_c + run_eq);
-    if (tid == kSpThreads - 1) {
-      s.found_total = w_upto;
-      if (a.kept) a.kept[row] = (int)min(c_upto, (unsigned long long)INT_MAX);
-    }
+    const unsigned long long w_upto = scan(run_w);
+    const unsigned c = __reduce_add_sync(0xffffffffu, (unsigned)(run_c + run_eq));
+    if (lane == 0) s.part[0][warp] = c;
+    if (tid == kSpThreads - 1) s.found_total = w_upto;
     __syncthreads();
+    if (warp == 0 && a.kept) {
+      const unsigned all_c = __reduce_add_sync(0xffffffffu, lane < kSpWarps ? (unsigned)s.part[0][lane] : 0u);
+      if (lane == 0) a.kept[row] = (int)all_c;
+    }
     const unsigned long long goal = __umul64hi(s.found_total, fraction(u));  // the first running sum above it
     if (goal >= w_upto - run_w && goal < w_upto) {
       s.found_bin = my_run;
