@@ -110,6 +110,22 @@ __global__ void __launch_bounds__(kHeadThreads) qk_norm_rope_kernel(HeadArgs a, 
   }
 }
 
+// The table of a base and head dim; a host thread keeps the last one (64 powers take as
+// long as the launch).
+const HeadTurns& turns_of(float base, int hd) {
+  thread_local HeadTurns t;
+  thread_local float of_base = 0.f;
+  thread_local int of_hd = 0;
+  if (of_base != base || of_hd != hd) {
+    t = HeadTurns{};
+    for (int j = 0; j < hd / 2; ++j)
+      t.t[j] = (uint64_t)std::ldexp(std::pow((double)base, -2.0 * j / hd) * 0.15915494309189535, 64);  // 1 / 2 pi
+    of_base = base;
+    of_hd = hd;
+  }
+  return t;
+}
+
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
@@ -130,10 +146,7 @@ extern "C" dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int6
   if (!aligned16(qkv) || !aligned16(q) || !aligned16(k) || !aligned16(v) || reinterpret_cast<uintptr_t>(pos) % 4 ||
       reinterpret_cast<uintptr_t>(q_gain) % 2 || reinterpret_cast<uintptr_t>(k_gain) % 2)
     return DG_ERR_ARG;
-  HeadTurns turns{};
-  for (int j = 0; j < hd / 2; ++j) {
-    turns.t[j] = (uint64_t)std::ldexp(std::pow((double)rope_base, -2.0 * j / hd) * 0.15915494309189535, 64);  // 1 / 2 pi
-  }
+  const HeadTurns& turns = turns_of(rope_base, hd);
   HeadArgs a{static_cast<const __nv_bfloat16*>(qkv), pos, static_cast<const __nv_bfloat16*>(q_gain),
              static_cast<const __nv_bfloat16*>(k_gain), static_cast<__nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(k),
              static_cast<__nv_bfloat16*>(v), batch_stride, token_stride, B * C, C, Hq, Hkv, rms_eps};

@@ -710,6 +710,10 @@ def kv8_release_workspaces(device=None) -> None:
 
 
 # ------------------------------------------------- operators of a decoded token
+# Their device time is a few microseconds for small calls, so the checks of the usual case are few and made in place.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
 def _on(t, dtype, what, index):
     """Checks a tensor's type and device (a CUDA device's index); returns the tensor."""
     if t.dtype is not dtype or t.get_device() != index:
@@ -732,12 +736,12 @@ def _raw_stream(index, stream):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _empty(shape, dtype, index, stream):
+def _empty(shape, dtype, device, stream):
     """Memory of the launching stream."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=index)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=index)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _rows_of(t, dtype, width, what, index):
@@ -761,6 +765,8 @@ class W4Matrix:
         self.scales = torch.empty(ns.value // 2, dtype=torch.bfloat16, device=device)
         self.N, self.K, self.group = N, K, group
         self._index = _index_of(self.codes, "device")
+        self._device = torch.device("cuda", self._index)
+        self._call = self._lib.dg_w4_matvec
         self.s = dg_w4(self.codes.data_ptr(), self.scales.data_ptr(), N, K, group)
         self._ref = ct.byref(self.s)
 
@@ -782,7 +788,7 @@ class W4Matrix:
     def read(self, stream=None) -> torch.Tensor:
         """The weights as float32 [N, K], exactly (dg_w4_read)."""
         st = _raw_stream(self._index, stream)
-        out = _empty((self.N, self.K), torch.float32, self._index, stream)
+        out = _empty((self.N, self.K), torch.float32, self._device, stream)
         _check(self._lib.dg_w4_read(self._ref, out.data_ptr(), self.K, st), "dg_w4_read")
         return out
 
@@ -815,34 +821,55 @@ def w4_matvec(w: W4Matrix, x: torch.Tensor, alpha: torch.Tensor | None = None, c
     """coef * alpha[m] * (x w^T) + resid for 1 to 32 rows x (bf16 [M, K]) (dg_w4_matvec); bf16 or float32 [M, N].
 
     alpha: optional float32 [M]; resid: optional bf16 [M, N], which may also be `out`."""
-    i = w._index
-    M, ldx = _rows_of(x, torch.bfloat16, w.K, "x", i)
-    ap = rp = None
-    ldr = 0
+    i, N, ap, rp, ldr = w._index, w.N, None, None, 0
+    if x.dtype is _BF16 and x.get_device() == i and x.dim() == 2 and x.is_contiguous() and x.shape[1] == w.K:
+        M, ldx = x.shape[0], w.K
+    else:
+        M, ldx = _rows_of(x, _BF16, w.K, "x", i)
     if alpha is not None:
-        if _on(alpha, torch.float32, "alpha", i).shape != (M,) or not alpha.is_contiguous():
-            raise ValueError(f"alpha: contiguous float32 [{M}]")
+        if alpha.dtype is not _F32 or alpha.get_device() != i or alpha.shape != (M,) or not alpha.is_contiguous():
+            raise ValueError(f"alpha: contiguous float32 [{M}] on cuda:{i}")
         ap = alpha.data_ptr()
     if resid is not None:
-        rr, ldr = _rows_of(resid, torch.bfloat16, w.N, "resid", i)
-        _need(rr == M, f"resid: [{M}, {w.N}]")
+        rr, ldr = _rows_of(resid, _BF16, N, "resid", i)
+        _need(rr == M, f"resid: [{M}, {N}]")
         rp = resid.data_ptr()
     st = _raw_stream(i, stream)
     if out is None:
-        out, ldy = _empty((M, w.N), dtype, i, stream), w.N
+        out, ldy = _empty((M, N), dtype, w._device, stream), N
     else:
-        rr, ldy = _rows_of(out, out.dtype, w.N, "out", i)
-        _need(rr == M, f"out: [{M}, {w.N}]")
-    if out.dtype is torch.float32:
-        f32 = 1
-    elif out.dtype is torch.bfloat16:
-        f32 = 0
-    else:
-        raise ValueError(f"the product is bfloat16 or float32, not {out.dtype}")
-    rc = w._lib.dg_w4_matvec(w._ref, x.data_ptr(), ldx, M, ap, coef, rp, ldr, out.data_ptr(), ldy, f32, st)
+        dtype = out.dtype
+        rr, ldy = _rows_of(out, dtype, N, "out", i)
+        _need(rr == M, f"out: [{M}, {N}]")
+    if dtype is not _F32 and dtype is not _BF16:
+        raise ValueError(f"the product is bfloat16 or float32, not {dtype}")
+    rc = w._call(w._ref, x.data_ptr(), ldx, M, ap, coef, rp, ldr, out.data_ptr(), ldy, 1 if dtype is _F32 else 0, st)
     if rc:
         raise DgError(rc, "dg_w4_matvec")
     return out
+
+
+_qk_plans = {}  # shapes, strides and heads of qkv -> (B, C, hd, strides, output shapes)
+
+
+def _qk_plan(qkv, Hq, Hkv):
+    H = Hq + 2 * Hkv
+    if qkv.dim() != 3 or Hq < 1 or Hkv < 1 or qkv.shape[2] % H or (qkv.shape[2] > 1 and qkv.stride(2) != 1):
+        raise ValueError(f"qkv: bf16 [B, C, {H} hd] with contiguous tokens, got {tuple(qkv.shape)}")
+    B, C, W = qkv.shape
+    sb, sc, _ = qkv.stride()
+    sc = sc if C > 1 else W
+    plan = (B, C, W // H, sb if B > 1 else C * max(sc, W), sc, (B, Hq, C, W // H), (B, Hkv, C, W // H))
+    if len(_qk_plans) >= 256:
+        _qk_plans.clear()
+    _qk_plans[(qkv.shape, qkv.stride(), Hq, Hkv)] = plan
+    return plan
+
+
+def _gain(t, hd, what, index):
+    if t.dtype is not _BF16 or t.get_device() != index or t.shape != (hd,) or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous bf16 [{hd}] on cuda:{index}")
+    return t.data_ptr()
 
 
 def qk_norm_rope(qkv: torch.Tensor, pos: torch.Tensor, Hq: int, Hkv: int, q_gain: torch.Tensor | None = None,
@@ -853,35 +880,31 @@ def qk_norm_rope(qkv: torch.Tensor, pos: torch.Tensor, Hq: int, Hkv: int, q_gain
     qkv: bf16 [B, C, (Hq + 2 Hkv) hd]; pos: int32 [B], position of each sequence's first token (e.g. cache.len);
     q_gain, k_gain: optional bf16 [hd].  q [B, Hq, C, hd], k, v [B, Hkv, C, hd], as kv8_append and kv8_attention take
     them; out: optional (q, k, v) to write."""
-    i = _index_of(qkv, "qkv")
-    H = Hq + 2 * Hkv
-    if qkv.dtype is not torch.bfloat16 or qkv.dim() != 3 or Hq < 1 or Hkv < 1 or qkv.shape[2] % H \
-            or (qkv.shape[2] > 1 and qkv.stride(2) != 1):
-        raise ValueError(f"qkv: bf16 [B, C, {H} hd] with contiguous tokens, got {qkv.dtype} {tuple(qkv.shape)}")
-    B, C, W = qkv.shape
-    hd = W // H
-    sb, sc, _ = qkv.stride()
-    if _on(pos, torch.int32, "pos", i).shape != (B,) or not pos.is_contiguous():
-        raise ValueError(f"pos: contiguous int32 [{B}]")
-    gains = []
-    for t, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
-        if t is not None and (_on(t, torch.bfloat16, what, i).shape != (hd,) or not t.is_contiguous()):
-            raise ValueError(f"{what}: contiguous bf16 [{hd}]")
-        gains.append(None if t is None else t.data_ptr())
+    plan = _qk_plans.get((qkv.shape, qkv.stride(), Hq, Hkv)) or _qk_plan(qkv, Hq, Hkv)
+    B, C, hd, sb, sc, sq, sk = plan
+    i = qkv.get_device()
+    if i < 0 or qkv.dtype is not _BF16:
+        raise ValueError(f"qkv: a bf16 CUDA tensor, got {qkv.dtype} on {qkv.device}")
+    if pos.dtype is not _I32 or pos.get_device() != i or pos.shape != (B,) or not pos.is_contiguous():
+        raise ValueError(f"pos: contiguous int32 [{B}] on cuda:{i}")
+    qg = kg = None
+    if q_gain is not None:
+        qg = _gain(q_gain, hd, "q_gain", i)
+    if k_gain is not None:
+        kg = _gain(k_gain, hd, "k_gain", i)
     st = _raw_stream(i, stream)
-    sq, sk = (B, Hq, C, hd), (B, Hkv, C, hd)
     if out is None:
-        q, k, v = (_empty(s, torch.bfloat16, i, stream) for s in (sq, sk, sk))
+        dev = qkv.device
+        q, k, v = _empty(sq, _BF16, dev, stream), _empty(sk, _BF16, dev, stream), _empty(sk, _BF16, dev, stream)
     else:
         q, k, v = out
         for t, s, what in ((q, sq, "q"), (k, sk, "k"), (v, sk, "v")):
-            if _on(t, torch.bfloat16, what, i).shape != s or not t.is_contiguous():
+            if _on(t, _BF16, what, i).shape != s or not t.is_contiguous():
                 raise ValueError(f"{what}: contiguous bf16 {list(s)}")
     if B * C == 0:
         return q, k, v
-    rc = load().dg_qk_norm_rope(qkv.data_ptr(), sb if B > 1 else C * max(sc, W), sc if C > 1 else W, pos.data_ptr(),
-                                gains[0], gains[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), B, C, Hq, Hkv, hd,
-                                rope_base, rms_eps, st)
+    rc = (_lib or load()).dg_qk_norm_rope(qkv.data_ptr(), sb, sc, pos.data_ptr(), qg, kg, q.data_ptr(), k.data_ptr(),
+                                          v.data_ptr(), B, C, Hq, Hkv, hd, rope_base, rms_eps, st)
     if rc:
         raise DgError(rc, "dg_qk_norm_rope")
     return q, k, v
@@ -910,6 +933,7 @@ class MoeFfn:
         self.s.Wr, self.s.We1, self.s.We2 = Wr.data_ptr(), We1.data_ptr(), We2.data_ptr()
         self._ref = ct.byref(self.s)
         self._lib = load()
+        self._device = torch.device("cuda", i)
         self._ws_bytes = {}
         self.workspace_bytes(1)
 
@@ -938,11 +962,12 @@ def moe_tokens(ffn: MoeFfn, h: torch.Tensor, out: torch.Tensor | None = None, ro
     the experts and their gates.  ws: optional uint8 workspace of ffn.workspace_bytes(M) bytes, zeroed before its
     first use and not shared by calls that may overlap; by default the calls of a stream share one, which is kept
     (moe_tokens_status, moe_release_workspaces), and a captured call takes one from the graph's pool."""
-    i = ffn._index
+    i, d = ffn._index, ffn.d
     M = h.shape[0] if h.dim() == 2 else 0
-    for t, what in ((h, "h"), (out, "out")):
-        if t is not None and (_on(t, torch.bfloat16, what, i).shape != (M, ffn.d) or not t.is_contiguous()):
-            raise ValueError(f"{what}: contiguous bf16 [M, {ffn.d}], got {tuple(t.shape)}")
+    if h.dtype is not _BF16 or h.get_device() != i or h.shape != (M, d) or not h.is_contiguous():
+        raise ValueError(f"h: contiguous bf16 [M, {d}] on cuda:{i}, got {h.dtype} {tuple(h.shape)} on {h.device}")
+    if out is not None and (_on(out, _BF16, "out", i).shape != (M, d) or not out.is_contiguous()):
+        raise ValueError(f"out: contiguous bf16 [{M}, {d}], got {tuple(out.shape)}")
     ip = gp = None
     if routing is not None:
         for t, dt in zip(routing, (torch.int32, torch.float32)):
@@ -950,9 +975,9 @@ def moe_tokens(ffn: MoeFfn, h: torch.Tensor, out: torch.Tensor | None = None, ro
                 raise ValueError(f"routing: contiguous int32 and float32 [{M}, {ffn.top_k}]")
         ip, gp = routing[0].data_ptr(), routing[1].data_ptr()
     st = _raw_stream(i, stream)
-    wn = ffn.workspace_bytes(M)
+    wn = ffn._ws_bytes.get(M) or ffn.workspace_bytes(M)
     if out is None:
-        out = _empty((M, ffn.d), torch.bfloat16, i, stream)
+        out = _empty((M, d), _BF16, ffn._device, stream)
     call, hp, op = ffn._lib.dg_moe_tokens, h.data_ptr(), out.data_ptr()
     if ws is not None:
         _need(ws.get_device() == i and ws.is_contiguous(), "ws: contiguous, on the block's device")
@@ -997,6 +1022,12 @@ def moe_release_workspaces(device=None) -> None:
             del _moe_workspaces[key]
 
 
+def _setting(t, dtype, R, what, index):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (R,) or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous {dtype} [{R}] on cuda:{index}, or a number")
+    return t.data_ptr()
+
+
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, stream=None):
     """A token for each row of logits (float32 or bf16 [R, V]) by the random numbers u (float32 [R], in [0, 1)), with
     temperature, top-k, top-p and min-p (dg_sample): (token int32, logprob float32, kept int32), each [R].
@@ -1004,36 +1035,43 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     The settings are numbers, or tensors [R] with one for each row (float32; top_k int32): 0 / 0 / 1 / 0 are greedy and
     no cut.  A row that cannot be drawn from (NaN, +inf, no finite logit, a setting or u outside its range) gets token
     -1.  out: optional (token, logprob, kept) to write."""
-    i = _index_of(logits, "logits")
+    i = logits.get_device()
     dt = logits.dtype
-    if dt is not torch.float32 and dt is not torch.bfloat16:
-        raise ValueError(f"logits: float32 or bfloat16, got {dt}")
-    if logits.dim() != 2:
-        raise ValueError(f"logits: [R, V], got {tuple(logits.shape)}")
-    R, ld = _rows_of(logits, dt, logits.shape[1], "logits", i)
-    V = logits.shape[1]
-    if _on(u, torch.float32, "u", i).shape != (R,) or not u.is_contiguous():
-        raise ValueError(f"u: contiguous float32 [{R}]")
+    if i < 0 or (dt is not _F32 and dt is not _BF16) or logits.dim() != 2:
+        raise ValueError(f"logits: float32 or bfloat16 [R, V] on a CUDA device, got {dt} {tuple(logits.shape)} on {logits.device}")
+    R, V = logits.shape
+    ld = V if logits.is_contiguous() else _rows_of(logits, dt, V, "logits", i)[1]
+    if u.dtype is not _F32 or u.get_device() != i or u.shape != (R,) or not u.is_contiguous():
+        raise ValueError(f"u: contiguous float32 [{R}] on cuda:{i}")
     how = dg_sampling()
-    for name, v, want in (("temperature", temperature, torch.float32), ("top_p", top_p, torch.float32),
-                          ("min_p", min_p, torch.float32), ("top_k", top_k, torch.int32)):
-        if isinstance(v, torch.Tensor):
-            if _on(v, want, name, i).shape != (R,) or not v.is_contiguous():
-                raise ValueError(f"{name}: contiguous {want} [{R}], or a number")
-            setattr(how, name, v.data_ptr())
-        else:
-            setattr(how, name + "_all", v)
+    if isinstance(temperature, torch.Tensor):
+        how.temperature = _setting(temperature, _F32, R, "temperature", i)
+    else:
+        how.temperature_all = temperature
+    if isinstance(top_p, torch.Tensor):
+        how.top_p = _setting(top_p, _F32, R, "top_p", i)
+    else:
+        how.top_p_all = top_p
+    if isinstance(min_p, torch.Tensor):
+        how.min_p = _setting(min_p, _F32, R, "min_p", i)
+    else:
+        how.min_p_all = min_p
+    if isinstance(top_k, torch.Tensor):
+        how.top_k = _setting(top_k, _I32, R, "top_k", i)
+    else:
+        how.top_k_all = top_k
     st = _raw_stream(i, stream)
     if out is None:
-        out = tuple(_empty((R,), t, i, stream) for t in (torch.int32, torch.float32, torch.int32))
+        dev, shape = logits.device, (R,)
+        out = (_empty(shape, _I32, dev, stream), _empty(shape, _F32, dev, stream), _empty(shape, _I32, dev, stream))
     else:
-        for t, want, what in zip(out, (torch.int32, torch.float32, torch.int32), ("token", "logprob", "kept")):
+        for t, want, what in zip(out, (_I32, _F32, _I32), ("token", "logprob", "kept")):
             if _on(t, want, what, i).shape != (R,) or not t.is_contiguous():
                 raise ValueError(f"{what}: contiguous {want} [{R}]")
     if R == 0:
         return out
-    rc = load().dg_sample(logits.data_ptr(), 1 if dt is torch.bfloat16 else 0, ld, R, V, ct.byref(how), u.data_ptr(),
-                          out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), st)
+    rc = (_lib or load()).dg_sample(logits.data_ptr(), 1 if dt is _BF16 else 0, ld, R, V, ct.byref(how), u.data_ptr(),
+                                    out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), st)
     if rc:
         raise DgError(rc, "dg_sample")
     return out
