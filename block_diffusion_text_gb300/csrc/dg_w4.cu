@@ -207,13 +207,21 @@ DG_DEV void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+DG_DEV void w4_store(const W4Args& a, int m, int col, float v) {
+  if (m >= a.M || col >= a.N) return;
+  v *= a.alpha ? a.coef * a.alpha[m] : a.coef;
+  if (a.resid) v += __bfloat162float(a.resid[m * a.ldr + col]);
+  if (a.f32) static_cast<float*>(a.y)[m * a.ldy + col] = v;
+  else static_cast<__nv_bfloat16*>(a.y)[m * a.ldy + col] = __float2bfloat16_rn(v);
+}
+
 // A unit is R row tiles and all their columns, shared by wk warps (every wk-th
 // tile of 64 columns each); a CTA works on kW4Warps / wk units at a time, a set.  A
 // warp's codes and scales come through a ring of cp.async copies that runs on over
 // the borders of its units; a lane reads only what it copied itself, so it waits for
 // nothing but its own copies.
 template <int NT, int R, int SG>
-__global__ void __launch_bounds__(kW4Warps * 32, R * NT > 8 ? 1 : 2) w4_matvec_kernel(W4Args a) {
+__global__ void __launch_bounds__(kW4Warps * 32, 2) w4_matvec_kernel(W4Args a) {
   constexpr int S = kW4Stages, kStage = R * kW4Bytes + SG * 32 * 4 * R;  // a lane's scales: 4 bytes to a tile
   extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -320,12 +328,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, R * NT > 8 ? 1 : 2) w4_matvec_k
     }
     const int rt0 = (set * per + warp / wk) * R;
     auto store = [&](int r, int i, float v) {
-      const int m = 8 * (i / 4) + 2 * t + i % 2, col = (rt0 + r) * kW4Rows + g + 8 * (i % 4 / 2);
-      if (m >= a.M || col >= a.N) return;
-      v *= a.alpha ? a.coef * a.alpha[m] : a.coef;
-      if (a.resid) v += __bfloat162float(a.resid[m * a.ldr + col]);
-      if (a.f32) static_cast<float*>(a.y)[m * a.ldy + col] = v;
-      else static_cast<__nv_bfloat16*>(a.y)[m * a.ldy + col] = __float2bfloat16_rn(v);
+      w4_store(a, 8 * (i / 4) + 2 * t + i % 2, (rt0 + r) * kW4Rows + g + 8 * (i % 4 / 2), v);
     };
     if (wk > 1) {
       // the warps' sums, in order, each warp some of the unit's values; the other half
@@ -352,7 +355,7 @@ template <int NT, int R, int SG>
 cudaError_t launch_w4(const W4Args& args, cudaStream_t st) {
   W4Args a = args;
   const int tiles = cdiv(a.N, kW4Rows), units = cdiv(tiles, R), KB = a.K / kW4Cols;
-  constexpr int ctas = R * NT > 8 ? 1 : 2;
+  constexpr int ctas = 2;
   a.wk = w4_split(units, KB, ctas);
   const int ring = kW4Warps * kW4Stages * R * (kW4Bytes + SG * 128);
   const int part = 2 * kW4Warps * R * NT * 128 * (int)sizeof(float);
@@ -363,11 +366,163 @@ cudaError_t launch_w4(const W4Args& args, cudaStream_t st) {
                     (size_t)(ring + (a.wk > 1 ? part : 0)), st, a);
 }
 
+// More than eight rows over many row tiles: x no longer stays in L1 beside the rings
+// (it would come from L2 twice as often as the codes from HBM), so all warps of a CTA
+// work on the same columns at the same time, on row tiles of their own, and x lies in
+// shared memory for kChunk tiles of columns at a time, in the order of the products'
+// operands.  A CTA has an equal share of all row tiles, 32 at a time, two to a warp.
+constexpr int kW4WideWarps = 16;
+constexpr int kW4Chunk = 4;
+
+template <int NT, int SG>
+__global__ void __launch_bounds__(kW4WideWarps * 32, 1) w4_wide_kernel(W4Args a) {
+  constexpr int R = 2, S = kW4Stages, kStage = R * (kW4Bytes + SG * 128), kX = NT * 1024;  // x of a tile of columns
+  extern __shared__ __align__(16) char smem[];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  char* ring = smem + warp * S * kStage;
+  char* xs = smem + kW4WideWarps * S * kStage;  // [2][kW4Chunk][NT][2 halves][32 lanes][16 bytes]
+  const int KB = a.K / kW4Cols, KG = a.K / a.group, tiles = (a.N + kW4Rows - 1) / kW4Rows;
+  const int sg_shift = a.group == 2 * kW4Cols ? 1 : 0;
+  const int t0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), t1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+  const int passes = (t1 - t0 + R * kW4WideWarps - 1) / (R * kW4WideWarps);
+  auto tile_of = [&](int pass, int r) { return t0 + (pass * R + r) * kW4WideWarps + warp; };
+
+  int ppass = 0, pkb = 0, pslot = 0;  // what is copied next
+  auto issue = [&]() {
+    if (ppass < passes) {
+      char* slot = ring + pslot;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int rt = tile_of(ppass, r);
+        if (rt < t1) {
+          cp_async16(slot + r * kW4Bytes + lane * 16,
+                     reinterpret_cast<const char*>(a.codes) + w4_tile(rt, pkb, KB) * kW4Bytes + lane * 16);
+#pragma unroll
+          for (int q = 0; q < SG; ++q)
+            cp_async4(slot + R * kW4Bytes + (r * SG + q) * 128 + lane * 4,
+                      a.scales + w4_scale(rt, (pkb * SG >> sg_shift) + q, KG, g));
+        }
+      }
+      if (++pkb == KB) {
+        pkb = 0;
+        ++ppass;
+      }
+    }
+    cp_async_commit();
+    pslot = pslot + kStage == S * kStage ? 0 : pslot + kStage;
+  };
+  // x of the tiles of columns from kb on, 16 bytes (a lane's of one operand) at a time;
+  // rows past the last one repeat it: their sums are not stored
+  auto load_x = [&](int kb, int buf) {
+    const int n = min(kW4Chunk, KB - kb) * NT * 64;
+    for (int i = tid; i < n; i += kW4WideWarps * 32) {
+      const int l = i % 32, p = i / 32 % 2, nt = i / 64 % NT, k = i / (64 * NT);
+      const int m = min(8 * nt + l / 4, a.M - 1);
+      cp_async16(xs + buf * kW4Chunk * kX + i * 16, a.x + m * a.ldx + (kb + k) * kW4Cols + 32 * p + 8 * (l % 4));
+    }
+  };
+  pdl_wait();
+  load_x(0, 0);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue();
+  int slot_at = 0, buf = 0;
+  bool settled = false;  // whether four groups were begun since the chunk's x
+  for (int pass = 0; pass < passes; ++pass) {
+    float y[R][NT][4] = {};
+    const bool one = tile_of(pass, 0) < t1, two = tile_of(pass, 1) < t1;
+    for (int kb0 = 0; kb0 < KB; kb0 += kW4Chunk) {
+      const int nk = min(kW4Chunk, KB - kb0);
+#pragma unroll 1
+      for (int k = 0; k < nk; ++k) {
+        issue();
+        if (k == 0) {
+          if (settled) cp_async_wait<S - 1>();
+          else cp_async_wait<0>();
+          __syncthreads();  // this chunk's x is there, and the one before is done with
+          const int next = kb0 + kW4Chunk < KB ? kb0 + kW4Chunk : 0;
+          if (next > 0 || pass + 1 < passes) load_x(next, buf ^ 1);  // (in the next step's group)
+          settled = nk == kW4Chunk;
+        } else {
+          cp_async_wait<S - 1>();
+        }
+        const char* slot = ring + slot_at;
+        slot_at = slot_at + kStage == S * kStage ? 0 : slot_at + kStage;
+        if (!one) continue;
+        const uint4* xb = reinterpret_cast<const uint4*>(xs + (buf * kW4Chunk + k) * kX) + lane;
+        uint4 cw[R];
+        uint32_t sw[R][SG];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          cw[r] = *reinterpret_cast<const uint4*>(slot + r * kW4Bytes + lane * 16);
+#pragma unroll
+          for (int q = 0; q < SG; ++q)
+            sw[r][q] = *reinterpret_cast<const uint32_t*>(slot + R * kW4Bytes + (r * SG + q) * 128 + lane * 4);
+        }
+        float acc[R][NT][4];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint4 b[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) b[n] = xb[(n * 2 + p) * 32];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (r == 1 && !two) break;
+            const uint32_t words[4] = {cw[r].x, cw[r].y, cw[r].z, cw[r].w};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t A[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) A[i] = w4_pair(words[2 * p + h], i);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint32_t b0 = h ? b[n].z : b[n].x, b1 = h ? b[n].w : b[n].y;
+                if (h == 0 && (SG == 2 || p == 0)) mma_bf16_first(acc[r][n], A, b0, b1);
+                else mma_bf16_16816(acc[r][n], A, b0, b1);
+              }
+            }
+            if (SG == 2 || p == 1) {
+              const uint32_t s = sw[r][SG == 2 ? p : 0];
+              const float s0 = __uint_as_float(s << 16), s1 = __uint_as_float(s & 0xffff0000u);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                y[r][n][0] += s0 * acc[r][n][0];
+                y[r][n][1] += s0 * acc[r][n][1];
+                y[r][n][2] += s1 * acc[r][n][2];
+                y[r][n][3] += s1 * acc[r][n][3];
+              }
+            }
+          }
+        }
+      }
+      buf ^= 1;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int rt = tile_of(pass, r);
+      if (rt >= t1) break;
+#pragma unroll
+      for (int i = 0; i < NT * 4; ++i) {
+        const int m = 8 * (i / 4) + 2 * t + i % 2, col = rt * kW4Rows + g + 8 * (i % 4 / 2);
+        w4_store(a, m, col, y[r][i / 4][i % 4]);
+      }
+    }
+  }
+  cp_async_wait<0>();
+}
+
+template <int NT, int SG>
+cudaError_t launch_w4_wide(const W4Args& a, cudaStream_t st) {
+  const int smem = kW4WideWarps * kW4Stages * 2 * (kW4Bytes + SG * 128) + 2 * kW4Chunk * NT * 1024;
+  const cudaError_t e = set_smem_once<w4_wide_kernel<NT, SG>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(w4_wide_kernel<NT, SG>, dim3(kTargetCtas), dim3(kW4WideWarps * 32), (size_t)smem, st, a);
+}
+
 template <int SG>
 cudaError_t launch_w4_rows(const W4Args& a, bool wide, cudaStream_t st) {
   if (a.M <= 8) return wide ? launch_w4<1, kW4Tiles, SG>(a, st) : launch_w4<1, 1, SG>(a, st);
-  if (a.M <= 16) return wide ? launch_w4<2, kW4Tiles, SG>(a, st) : launch_w4<2, 1, SG>(a, st);
-  return wide ? launch_w4<4, kW4Tiles, SG>(a, st) : launch_w4<4, 1, SG>(a, st);
+  if (a.M <= 16) return wide ? launch_w4_wide<2, SG>(a, st) : launch_w4<2, 1, SG>(a, st);
+  return wide ? launch_w4_wide<4, SG>(a, st) : launch_w4<4, 1, SG>(a, st);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }

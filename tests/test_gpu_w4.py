@@ -169,3 +169,15 @@ def test_binding_refusals():
         dg.W4Matrix.from_codes(c.cuda(), s[:, :1].contiguous().cuda().repeat(1, 8))
     with pytest.raises(ValueError):
         dg.W4Matrix.from_codes(c.cuda()[:, ::2], s.cuda())
+
+
+@pytest.mark.parametrize("M", [9, 16, 17, 32])
+@pytest.mark.parametrize("N,K,group", [(38912, 64, 64), (40007, 192, 32), (45000, 640, 128), (60000, 320, 64), (39000, 1088, 32)])
+def test_products_of_many_rows(M, N, K, group):
+    """The kernel that keeps x in shared memory: row tiles that do not divide, columns that end inside a chunk."""
+    g = torch.Generator().manual_seed(M + N)
+    c, s = drawn(g, N, K, group)
+    w = dg.W4Matrix.from_codes(c.cuda(), s.cuda())
+    x = torch.randn(M, K, generator=g).to(BF)
+    check(w, c, s, x, dtype=torch.float32, alpha=torch.rand(M, generator=g) + 0.5)
+    check(w, c, s, x, resid=torch.randn(M, N, generator=g).to(BF))
