@@ -181,6 +181,13 @@ DG_DEV void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
+DG_DEV void cp_async16_s(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+DG_DEV void cp_async4_s(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Warps that share a unit: as few as leave the waves of sets on an SM's `ctas`
 // CTAs within 5 % of full (fewer barriers), all eight otherwise.
 int w4_split(int units, int KB, int ctas) {
@@ -213,6 +220,13 @@ DG_DEV void w4_store(const W4Args& a, int m, int col, float v) {
   if (a.resid) v += __bfloat162float(a.resid[m * a.ldr + col]);
   if (a.f32) static_cast<float*>(a.y)[m * a.ldy + col] = v;
   else static_cast<__nv_bfloat16*>(a.y)[m * a.ldy + col] = __float2bfloat16_rn(v);
+}
+
+// D += A B
+DG_DEV void mma_bf16_more(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // A unit is R row tiles and all their columns, shared by wk warps (every wk-th
@@ -309,7 +323,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 2) w4_matvec_kernel(W4Args a) {
             for (int n = 0; n < NT; ++n) {
               const uint32_t b0 = h ? b[n][p].z : b[n][p].x, b1 = h ? b[n][p].w : b[n][p].y;
               if (h == 0 && (SG == 2 || p == 0)) mma_bf16_first(acc[n], A, b0, b1);
-              else mma_bf16_16816(acc[n], A, b0, b1);
+              else mma_bf16_more(acc[n], A, b0, b1);
             }
           }
           if (SG == 2 || p == 1) {
@@ -387,26 +401,34 @@ __global__ void __launch_bounds__(kW4WideWarps * 32, 1) w4_wide_kernel(W4Args a)
   const int passes = (t1 - t0 + R * kW4WideWarps - 1) / (R * kW4WideWarps);
   auto tile_of = [&](int pass, int r) { return t0 + (pass * R + r) * kW4WideWarps + warp; };
 
-  int ppass = 0, pkb = 0, pslot = 0;  // what is copied next
+  int ppass = 0, pkb = 0, pslot = 0;  // what is copied next, and where it lies
+  const char *pc[R] = {}, *ps[R] = {};
+  bool there[R];
+  auto seek = [&]() {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int rt = tile_of(ppass, r);
+      there[r] = ppass < passes && rt < t1;
+      pc[r] = reinterpret_cast<const char*>(a.codes) + w4_tile(rt, 0, KB) * kW4Bytes + lane * 16;
+      ps[r] = reinterpret_cast<const char*>(a.scales + w4_scale(rt, 0, KG, g));
+    }
+  };
+  seek();
   auto issue = [&]() {
-    if (ppass < passes) {
-      char* slot = ring + pslot;
+    const uint32_t slot = smem_u32(ring) + pslot + lane * 16;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int rt = tile_of(ppass, r);
-        if (rt < t1) {
-          cp_async16(slot + r * kW4Bytes + lane * 16,
-                     reinterpret_cast<const char*>(a.codes) + w4_tile(rt, pkb, KB) * kW4Bytes + lane * 16);
+    for (int r = 0; r < R; ++r)
+      if (there[r]) {
+        cp_async16_s(slot + r * kW4Bytes, pc[r]);
 #pragma unroll
-          for (int q = 0; q < SG; ++q)
-            cp_async4(slot + R * kW4Bytes + (r * SG + q) * 128 + lane * 4,
-                      a.scales + w4_scale(rt, (pkb * SG >> sg_shift) + q, KG, g));
-        }
+        for (int q = 0; q < SG; ++q) cp_async4_s(slot - lane * 12 + R * kW4Bytes + (r * SG + q) * 128, ps[r] + q * 128);
+        pc[r] += kW4Tiles * kW4Bytes;
+        if (sg_shift == 0 || pkb % 2) ps[r] += SG * 128;
       }
-      if (++pkb == KB) {
-        pkb = 0;
-        ++ppass;
-      }
+    if (++pkb == KB) {
+      pkb = 0;
+      ++ppass;
+      seek();
     }
     cp_async_commit();
     pslot = pslot + kStage == S * kStage ? 0 : pslot + kStage;
@@ -477,7 +499,7 @@ __global__ void __launch_bounds__(kW4WideWarps * 32, 1) w4_wide_kernel(W4Args a)
               for (int n = 0; n < NT; ++n) {
                 const uint32_t b0 = h ? b[n].z : b[n].x, b1 = h ? b[n].w : b[n].y;
                 if (h == 0 && (SG == 2 || p == 0)) mma_bf16_first(acc[r][n], A, b0, b1);
-                else mma_bf16_16816(acc[r][n], A, b0, b1);
+                else mma_bf16_more(acc[r][n], A, b0, b1);
               }
             }
             if (SG == 2 || p == 1) {
