@@ -38,37 +38,69 @@ struct HeadArgs {
 };
 
 // A thread holds eight pairs of one head: 16 bytes of its first half and 16 of
-// its second.  A CTA takes as many tokens as fill its threads (at least one);
-// the tokens' sines and cosines are worked out once, in shared memory, while the
-// heads' values are on their way.
+// its second.  A CTA takes `per` tokens, enough to fill its threads, and where there are
+// many so many that each thread works out one sine and cosine, for all heads, while
+// the first values are on their way; the next values are loaded before the last ones
+// are worked on.  In shared memory the operands of neighbouring threads are neighbours,
+// 16 bytes each: [quarter of the eight pairs][thread of the head].
 template <int HD>
 __global__ void __launch_bounds__(kHeadThreads) qk_norm_rope_kernel(HeadArgs a, HeadTurns turns, int per) {
   pdl_wait();
   constexpr int L = HD / 16;  // threads per head
-  extern __shared__ float2 cs[];  // [per][HD / 2]
-  const int H = a.Hq + 2 * a.Hkv;
-  const int tok0 = blockIdx.x * per;
-  const int here = min(per, a.tokens - tok0);
-  for (int i = threadIdx.x; i < here * (HD / 2); i += kHeadThreads) {
-    const int tok = tok0 + i / (HD / 2);
+  extern __shared__ __align__(16) float4 cs[];  // [per][4][L]: cosine and sine of two pairs
+  __shared__ __align__(16) float4 gains[2][2][2][L];  // of q, k: [half of the head][half of the eight]
+  const int H = a.Hq + 2 * a.Hkv, tid = threadIdx.x, items = H * L;
+  const int tok0 = blockIdx.x * per, here = min(per, a.tokens - tok0);
+  // where the thread stands: token of the CTA, its sequence and place, item of the token
+  int ti = tid / items, item = tid - ti * items;
+  int b = (tok0 + ti) / a.C, i = tok0 + ti - b * a.C;
+  auto advance = [&]() {
+    item += kHeadThreads;
+    while (item >= items) {
+      item -= items;
+      ++ti;
+      if (++i == a.C) {
+        i = 0;
+        ++b;
+      }
+    }
+  };
+  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+  auto load = [&]() {
+    const uint4* src = reinterpret_cast<const uint4*>(a.x + b * a.sb + i * a.st + item / L * HD) + item % L;
+    lo = __ldcs(src);
+    hi = __ldcs(src + L);
+  };
+  if (ti < here) load();
+  for (int e = tid; e < 2 * HD; e += kHeadThreads) {
+    const __nv_bfloat16* from = e < HD ? a.qg : a.kg;
+    const int j = e % (HD / 2);  // of the half: pair j is pair j % 8 of thread j / 8
+    reinterpret_cast<float*>(&gains[e / HD][e / (HD / 2) % 2][j % 8 / 4][j / 8])[j % 4] = from ? __bfloat162float(from[e % HD]) : 1.0f;
+  }
+  for (int e = tid; e < here * (HD / 2); e += kHeadThreads) {
+    const int tok = tok0 + e / (HD / 2), j = e % (HD / 2);
     const uint64_t at = (uint64_t)((int64_t)a.pos[tok / a.C] + tok % a.C);
-    const int32_t turn = (int32_t)(uint32_t)((at * turns.t[i % (HD / 2)]) >> 32);  // signed: half a turn is 2^31
+    const int32_t turn = (int32_t)(uint32_t)((at * turns.t[j]) >> 32);  // signed: half a turn is 2^31
     float sn, c;
     sincospif((float)turn * 4.656612873077393e-10f, &sn, &c);  // 2^-31
-    cs[i] = make_float2(c, sn);
+    reinterpret_cast<float2*>(cs + (e / (HD / 2) * 4 + j % 8 / 2) * L + j / 8)[j % 2] = make_float2(c, sn);
   }
   __syncthreads();
-  for (int it = threadIdx.x; it < here * H * L; it += kHeadThreads) {
-    const int l = it % L, head = it / L % H, ti = it / (L * H);
-    const int tok = tok0 + ti;
-    const int64_t b = tok / a.C, i = tok % a.C;
-    const uint4* src = reinterpret_cast<const uint4*>(a.x + b * a.sb + i * a.st + head * HD) + l;
-    const uint4 lo = __ldcs(src), hi = __ldcs(src + L);
+  while (ti < here) {
+    const int head = item / L, l = item % L, at = ti;
     const bool isq = head < a.Hq, isv = head >= a.Hq + a.Hkv;
     const int hh = isq ? head : head - a.Hq - (isv ? a.Hkv : 0);
-    __nv_bfloat16* dst = isq ? a.q + ((b * a.Hq + hh) * a.C + i) * HD : (isv ? a.v : a.k) + ((b * a.Hkv + hh) * a.C + i) * HD;
+    __nv_bfloat16* dst = isq ? a.q + (((int64_t)b * a.Hq + hh) * a.C + i) * HD : (isv ? a.v : a.k) + (((int64_t)b * a.Hkv + hh) * a.C + i) * HD;
     uint4* d4 = reinterpret_cast<uint4*>(dst) + l;
-    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+    const uint4 vl = lo, vh = hi;
+    advance();
+    if (ti < here) load();
+    if (isv) {
+      __stcs(d4, vl);
+      __stcs(d4 + L, vh);
+      continue;
+    }
+    const uint32_t wl[4] = {vl.x, vl.y, vl.z, vl.w}, wh[4] = {vh.x, vh.y, vh.z, vh.w};
     float x[8], y[8], sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -77,36 +109,31 @@ __global__ void __launch_bounds__(kHeadThreads) qk_norm_rope_kernel(HeadArgs a, 
       sum += x[j] * x[j] + y[j] * y[j];
     }
     // a head's lanes are neighbours and come together: the items are a multiple of L
-    const unsigned mask = ((1u << L) - 1) << (threadIdx.x % 32 / L * L);
+    const unsigned mask = ((1u << L) - 1) << (tid % 32 / L * L);
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
-    if (isv) {
-      d4[0] = lo;
-      d4[L] = hi;
-      continue;
-    }
     const float inv = 1.0f / sqrtf(sum * (1.0f / HD) + a.eps);
-    const __nv_bfloat16* gain = isq ? a.qg : a.kg;
+    const float4(&gain)[2][2][L] = gains[isq ? 0 : 1];
     uint32_t ol[4], oh[4];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      float u[2], w[2];
+    for (int q = 0; q < 2; ++q) {
+      const float4 g0 = gain[0][q][l], g1 = gain[1][q][l], c0 = cs[(at * 4 + 2 * q) * L + l], c1 = cs[(at * 4 + 2 * q + 1) * L + l];
+      const float ga[4] = {g0.x, g0.y, g0.z, g0.w}, gb[4] = {g1.x, g1.y, g1.z, g1.w};
+      const float cc[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
+      float u[4], w[4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float p = x[j + e] * inv, r = y[j + e] * inv;
-        if (gain) {
-          p *= __bfloat162float(gain[8 * l + j + e]);
-          r *= __bfloat162float(gain[HD / 2 + 8 * l + j + e]);
-        }
-        const float2 c = cs[ti * (HD / 2) + 8 * l + j + e];
-        u[e] = p * c.x - r * c.y;
-        w[e] = p * c.y + r * c.x;
+      for (int e = 0; e < 4; ++e) {
+        const float p = x[4 * q + e] * inv * ga[e], r = y[4 * q + e] * inv * gb[e];
+        u[e] = p * cc[e] - r * sn[e];
+        w[e] = p * sn[e] + r * cc[e];
       }
-      ol[j / 2] = pack_bf16(u[0], u[1]);
-      oh[j / 2] = pack_bf16(w[0], w[1]);
+      ol[2 * q] = pack_bf16(u[0], u[1]);
+      ol[2 * q + 1] = pack_bf16(u[2], u[3]);
+      oh[2 * q] = pack_bf16(w[0], w[1]);
+      oh[2 * q + 1] = pack_bf16(w[2], w[3]);
     }
-    d4[0] = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-    d4[L] = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+    __stcs(d4, make_uint4(ol[0], ol[1], ol[2], ol[3]));
+    __stcs(d4 + L, make_uint4(oh[0], oh[1], oh[2], oh[3]));
   }
 }
 
@@ -151,7 +178,10 @@ extern "C" dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int6
              static_cast<const __nv_bfloat16*>(k_gain), static_cast<__nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(k),
              static_cast<__nv_bfloat16*>(v), batch_stride, token_stride, B * C, C, Hq, Hkv, rms_eps};
   const int items = (Hq + 2 * Hkv) * (hd / 16);
-  const int per = items >= kHeadThreads ? 1 : kHeadThreads / items;
+  int per = items >= kHeadThreads ? 1 : kHeadThreads / items;
+  // with many tokens, a sine and cosine for every thread
+  const int fill = kHeadThreads / (hd / 2);
+  if (per < fill && a.tokens >= 8 * kTargetCtas * fill) per = fill;
   const dim3 grid(cdiv(a.tokens, per)), block(kHeadThreads);
   const size_t smem = sizeof(float2) * per * (hd / 2);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
