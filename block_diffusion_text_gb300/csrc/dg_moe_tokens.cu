@@ -6,8 +6,9 @@
 // The chosen experts' weights bound it: each matrix is read once, whatever the
 // number of tokens that chose it.  One persistent CTA per SM works through three
 // phases with a barrier of the grid between them, as the data demands:
-//   0  router logits, and the shared expert's hidden rows (they need no routing)
-//   1  every CTA works the routing out for itself; the chosen experts' hidden rows
+//   0  the router's logits
+//   1  every CTA works the routing out for itself; the hidden rows of the chosen experts
+//      and of the shared one
 //   2  the output columns
 // In each phase the rows of the weights that it needs are cut into equal ranges,
 // one for each CTA, row by row, so that all SMs read the same number of bytes.
@@ -199,11 +200,12 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   // each.  Its sums stay in registers over the tasks of a unit (all of the round with
   // kOne, else one segment) and go to `red` at its end; the parts of a unit are added
   // up, in order, when the round ends, and given to put(round, unit, row, token, sum).
-  // The copies run ahead over all borders, the tokens' values only within a task (a block
+  // The first copies are on their way before gate() is passed (the weights wait for
+  // nobody).  They run ahead over all borders, the tokens' values only within a task (a block
   // ahead, where the registers leave room).
   constexpr int kVals = 2 * NT * 4;  // of a unit, in a lane
   auto stream = [&](int F, const auto& segments, int KB, int pitch, auto one, const auto& seg_w, const auto& seg_b,
-                    const __nv_bfloat16* values, auto pair, const auto& meanwhile, const auto& put) {
+                    const __nv_bfloat16* values, auto pair, const auto& gate, const auto& meanwhile, const auto& put) {
     constexpr bool kOne = decltype(one)::value, kPair = decltype(pair)::value, kAhead = NT <= 2;
     constexpr int kB = kPair ? 2 : 1;
     // of n blocks; where there are fewer blocks than warps, one each for the first warps
@@ -238,6 +240,10 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     };
 #pragma unroll 1
     for (int s0 = 0; s0 < kMtStages; ++s0) issue();
+    if (!gate()) {
+      cp_async_wait<0>();
+      return false;
+    }
     int slot = 0;
 #pragma unroll 1
     for (int f = 0; f < F; ++f) {
@@ -330,7 +336,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     }
     if (F == 0) meanwhile();
     cp_async_wait<0>();
+    return true;
   };
+  auto go = [] { return true; };
   constexpr int kUnits = mt_units(NT);  // of a round
 
   auto range = [&](int rows, int c) { return (int)((int64_t)rows * c / ctas); };
@@ -345,34 +353,30 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     for (int i = tid; i < a.Fe / 4; i += kMtThreads)
       reinterpret_cast<uint4*>(a.hid + (size_t)a.M * K1 * 2 * a.Fe)[i] = make_uint4(0, 0, 0, 0);
 
-  // ---- phase 0: the router's rows, then the shared expert's
+  for (int e = tid; e < kMtMaxExp; e += kMtThreads) s.mask[e] = 0;
+
+  // ---- phase 0: the router's rows
   {
-    const int n32 = (a.n_exp + kMtRows - 1) / kMtRows * kMtRows, R = n32 + a.Fe;
-    const MtCut cut(range(R, cta), range(R, cta + 1), n32);
+    const int r0 = range(a.n_exp, cta), r1 = range(a.n_exp, cta + 1);
+    const MtCut cut(r0, r1, r1);
     stream((cut.U + kUnits - 1) / kUnits, [&](int f) { return min(kUnits, cut.U - f * kUnits); }, KB1, a.d, std::false_type{},
            [&](int f, int u, const __nv_bfloat16** w, int* rows) {
-             const int r = cut.row(u + f * kUnits);
-             *rows = r < n32 ? min(cut.rows(u + f * kUnits), a.n_exp - r) : cut.rows(u + f * kUnits);
-             *w = r < n32 ? a.Wr + (int64_t)r * a.d : a.W1 + ((int64_t)a.n_exp * a.Fe + r - n32) * a.d;
+             *rows = cut.rows(u + f * kUnits);
+             *w = a.Wr + (int64_t)cut.row(u + f * kUnits) * a.d;
            },
            [&](int, int, int* off, unsigned* tiles) {
              *tiles = (1u << ((a.M + 7) / 8)) - 1;
 #pragma unroll
              for (int n = 0; n < NT; ++n) off[n] = min(8 * n + g, a.M - 1) * a.d + 8 * t;  // columns past the last token repeat it
            },
-           a.h, std::false_type{}, norms, [&](int f, int u, int row, int m, float v) {
-      u += f * kUnits;
-      if (row >= cut.rows(u) || m >= a.M) return;
-      row += cut.row(u);
-      if (row < a.n_exp) a.logits[(size_t)m * a.n_exp + row] = v;
-      else if (row >= n32) store_hidden(m, a.top_k, row - n32, gelu(v * s.inv[m]));
-    });
+           a.h, std::false_type{}, go, norms, [&](int f, int u, int row, int m, float v) {
+             u += f * kUnits;
+             if (row < cut.rows(u) && m < a.M) a.logits[(size_t)m * a.n_exp + cut.row(u) + row] = v;
+           });
   }
   if (!grid_barrier(a.arrivals, a.rounds, a.status, &s.stop)) return;
 
   // ---- the routing: one warp for each token, a lane holding experts lane, lane + 32, ..
-  for (int e = tid; e < kMtMaxExp; e += kMtThreads) s.mask[e] = 0;
-  __syncthreads();
   for (int m = warp; m < a.M; m += kMtWarps) {
     float l[8];
 #pragma unroll
@@ -453,9 +457,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   }
   __syncthreads();
 
-  // ---- phase 1: the chosen experts' hidden rows
+  // ---- phase 1: the hidden rows of the chosen experts, then of the shared one
   {
-    const int R = nact * a.Fe, r0 = range(R, cta), r1 = range(R, cta + 1);
+    const int R = (nact + 1) * a.Fe, r0 = range(R, cta), r1 = range(R, cta + 1);
     const MtCut cut(r0, r1, min(r1, r0 / a.Fe * a.Fe + a.Fe));
     stream((cut.U + kUnits - 1) / kUnits, [&](int f) { return min(kUnits, cut.U - f * kUnits); }, KB1, a.d, std::false_type{},
            [&](int f, int u, const __nv_bfloat16** w, int* rows) {
@@ -471,17 +475,16 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
              for (int n = 0; n < NT; ++n)  // a token that does not want the expert: another's values, not stored
                off[n] = (mask >> (8 * n + g) & 1 ? 8 * n + g : some) * a.d + 8 * t;
            },
-           a.h, std::false_type{}, [] {}, [&](int f, int u, int row, int m, float v) {
+           a.h, std::false_type{}, go, [] {}, [&](int f, int u, int row, int m, float v) {
       u += f * kUnits;
       if (row >= cut.rows(u)) return;
       row += cut.row(u);
       const int x = row / a.Fe;
       if (!(s.ex[x].mask >> m & 1)) return;
       const int j = s.rank[x][m];
-      store_hidden(m, j, row - x * a.Fe, s.gate[m][j] * gelu(v * s.inv[m]));
+      store_hidden(m, j, row - x * a.Fe, (j < a.top_k ? s.gate[m][j] : 1.0f) * gelu(v * s.inv[m]));
     });
   }
-  if (!grid_barrier(a.arrivals, a.rounds, a.status, &s.stop)) return;
 
   // ---- phase 2: output columns, their sums over the experts' hidden values
   {
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
                off[n] = (mask >> m & 1 ? m * K1 + s.rank[x][m] : a.M * K1) * 2 * a.Fe + 8 * t;
              }
            },
-           a.hid, std::true_type{}, [] {},
+           a.hid, std::true_type{}, [&] { return grid_barrier(a.arrivals, a.rounds, a.status, &s.stop); }, [] {},
            [&](int u, int, int row, int m, float v) {
              if (row >= cut.rows(u) || m >= a.M) return;
              const int at = m * a.d + cut.row(u) + row;
