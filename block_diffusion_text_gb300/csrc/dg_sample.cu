@@ -31,6 +31,7 @@
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "dg_common.cuh"
 #include "dg_internal.h"
@@ -236,6 +237,29 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
                           : __ldg(reinterpret_cast<const float*>(src) + i + e);
     return make_float4(v[0], v[1], v[2], v[3]);
   };
+  // f(four values, their place) for all of [i0, i1), 128 values of a warp at a time (-inf
+  // behind the end, where the warp's other lanes still have some); the loads are D steps
+  // ahead.
+  auto each4 = [&](auto depth, int i0, int i1, auto&& f) {
+    constexpr int D = decltype(depth)::value;
+    auto next = [&](int i) { return i < i1 ? load4(i, i1) : make_float4(kNone, kNone, kNone, kNone); };
+    float4 v[D];
+    int i = i0 + 4 * lane;
+#pragma unroll
+    for (int j = 0; j < D; ++j) v[j] = next(i + 128 * j);
+#pragma unroll 1
+    while (i - 4 * lane < i1) {
+#pragma unroll
+      for (int j = 0; j < D; ++j) {
+        const float4 now = v[j];
+        v[j] = next(i + 128 * D);
+        if (i - 4 * lane < i1) f(now, i);
+        i += 128;
+      }
+    }
+  };
+  using Ahead1 = std::integral_constant<int, 1>;
+  using Ahead4 = std::integral_constant<int, 4>;
   // this warp's run: values [first, last)
   auto run_first = [&](int r) { return min(a.V, r / kSpWarps * a.slice + r % kSpWarps * a.run4 * 4); };
   auto run_last = [&](int r) { return min(min(a.V, (r / kSpWarps + 1) * a.slice), run_first(r) + a.run4 * 4); };
@@ -245,9 +269,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   float top = kNone, low = INFINITY;
   bool fine = true;
   unsigned fin = 0;
-#pragma unroll 4
-  for (int i = first + 4 * lane; i < last; i += 128) {
-    const float4 v = load4(i, last);
+  each4(Ahead4{}, first, last, [&](const float4& v, int i) {
     const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -258,7 +280,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         ++fin;
       }
     }
-  }
+  });
   unsigned mkey = __reduce_max_sync(0xffffffffu, top >= -FLT_MAX ? key_of(top) : 0u);
   unsigned lowest = __reduce_min_sync(0xffffffffu, low <= FLT_MAX ? key_of(low) : 0xffffffffu);
   const unsigned wrong = __any_sync(0xffffffffu, !fine) ? 1u : 0u;
@@ -511,22 +533,22 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     const float least_v = key_float(max(least, 0x00800000u));  // no finite value is below
     w = 0;
     c = eq = 0;
-    for (int i = i0 + 4 * lane; i < i1; i += 128) {
-      const float4 v4 = load4(i, i1);
-      if (!(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= least_v)) continue;
+    each4(Ahead1{}, i0, i1, [&](const float4& v4, int) {
+      if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= least_v)) return;
       const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const unsigned k = vs[e] >= -FLT_MAX ? key_of(vs[e]) : 0u;
         const bool in = k > least || (from && k == least);
-        const SpWeight x = weight_parts(vs[e], sc, s.pow2);
+        SpWeight x = weight_parts(vs[e], sc, s.pow2);
+        if (greedy) x = SpWeight{1u, 1u};
         if (in) {
           x.add_to(w);
           ++c;
         }
         eq += k == least;
       }
-    }
+    });
     w = warp_sum(w);
     c = __reduce_add_sync(0xffffffffu, c);
     eq = __reduce_add_sync(0xffffffffu, eq);
@@ -640,24 +662,16 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         if (in && at < (unsigned)cap) my_v[at] = v;
         n_list += __popc(b);
       };
-      auto four = [&](int i) { return i < last ? load4(i, last) : make_float4(kNone, kNone, kNone, kNone); };
-      float4 next = four(first + 4 * lane);
       if (by_k) {
-#pragma unroll 1
-        for (int i = first + 4 * lane; i - 4 * lane < last; i += 128) {
-          const float4 v4 = next;
-          next = four(i + 128);
-          if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= lo)) continue;
+        each4(Ahead4{}, first, last, [&](const float4& v4, int) {
+          if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= lo)) return;
           list(v4.x);
           list(v4.y);
           list(v4.z);
           list(v4.w);
-        }
+        });
       } else {
-#pragma unroll 1
-        for (int i = first + 4 * lane; i - 4 * lane < last; i += 128) {
-          const float4 v4 = next;
-          next = four(i + 128);
+        each4(Ahead1{}, first, last, [&](const float4& v4, int) {
           const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -670,7 +684,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
             }
             list(vs[e]);
           }
-        }
+        });
         __syncwarp();
         for (unsigned i = lane; i < min(n_list, (unsigned)cap); i += 32) w_list += weight(my_v[i]);
       }
