@@ -376,59 +376,100 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   }
   if (!grid_barrier(a.arrivals, a.rounds, a.status, &s.stop)) return;
 
-  // ---- the routing: one warp for each token, a lane holding experts lane, lane + 32, ..
-  for (int m = warp; m < a.M; m += kMtWarps) {
-    float l[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) l[j] = lane + 32 * j < a.n_exp ? __ldcg(a.logits + (size_t)m * a.n_exp + lane + 32 * j) : 0.f;
-    // keys in the order of the values; 0: no expert, taken, or NaN
-    unsigned key[8];
-    bool wrong = false;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      l[j] *= s.inv[m];
-      const bool there = lane + 32 * j < a.n_exp;
-      wrong |= there && !(fabsf(l[j]) <= FLT_MAX);
-      key[j] = there && l[j] == l[j] ? float_key(l[j] == 0.f ? 0.f : l[j]) : 0u;
+  // ---- the routing.  Keys in the order of the logits, 0 for NaN; equal ones by index.
+  auto key_of = [&](float l) { return l == l ? float_key(l == 0.f ? 0.f : l) : 0u; };
+  auto chosen = [&](int m, int k, int e, float gt) {
+    s.gate[m][k] = gt;
+    s.sel[m][k] = (uint8_t)e;
+    atomicOr(&s.mask[e], 1u << m);
+    if (cta == 0) {
+      if (a.idx) a.idx[(size_t)m * a.top_k + k] = e;
+      if (a.gate) a.gate[(size_t)m * a.top_k + k] = gt;
     }
-    if (__any_sync(0xffffffffu, wrong) && lane == 0 && cta == 0) atomicExch(a.status, kStatusValue);
-    float top = 0.f, Z = 0.f, mine = 0.f;
-    int mye = 0;
-    unsigned taken = 0;
+  };
+  if (a.M * a.n_exp <= kMtThreads) {
+    // few logits: each is ranked by a team of threads that compares it with all others
+    // (0.9 us; a warp that picks the largest one after the other takes 2.6)
+    unsigned* keys = reinterpret_cast<unsigned*>(red);  // [M][n_exp]
+    const int pairs = a.M * a.n_exp;
+    float mine = 0.f;
+    if (tid < pairs) {
+      const int m = tid / a.n_exp;
+      mine = __ldcg(a.logits + tid) * s.inv[m];
+      if (!(fabsf(mine) <= FLT_MAX) && cta == 0) atomicExch(a.status, kStatusValue);
+      keys[tid] = key_of(mine);
+      red[kMtThreads + tid] = mine;
+    }
+    __syncthreads();
+    int team = 1;
+    while (team < 32 && pairs * team * 2 <= kMtThreads) team *= 2;
+    const int pair = tid / team, m = pair / a.n_exp, e = pair - m * a.n_exp, mate = tid % team;
+    int rank = 0;
+    if (pair < pairs) {
+      const unsigned* of = keys + m * a.n_exp;
+      const unsigned key = of[e];
+      for (int o = mate; o < a.n_exp; o += team) rank += of[o] > key || (of[o] == key && o < e);
+    }
+    for (int o = 1; o < team; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    float* top = red + 2 * kMtThreads;  // [M][top_k] logits in rank order
+    if (pair < pairs && mate == 0 && rank < a.top_k) {
+      top[m * a.top_k + rank] = keys[pair] ? red[kMtThreads + pair] : -FLT_MAX;
+      s.sel[m][rank] = (uint8_t)e;
+    }
+    __syncthreads();
+    if (tid < a.M * a.top_k) {
+      const int row = tid / a.top_k, k = tid - row * a.top_k;
+      const float* v = top + row * a.top_k;
+      float Z = 0.f;
+      for (int j = 0; j < a.top_k; ++j) Z += expf(v[j] - v[0]);
+      chosen(row, k, s.sel[row][k], expf(v[k] - v[0]) / Z);
+    }
+  } else {
+    // one warp for each token, a lane holding experts lane, lane + 32, ..
+    for (int m = warp; m < a.M; m += kMtWarps) {
+      float l[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) l[j] = lane + 32 * j < a.n_exp ? __ldcg(a.logits + (size_t)m * a.n_exp + lane + 32 * j) : 0.f;
+      // keys in the order of the values; 0: no expert, taken, or NaN
+      unsigned key[8];
+      bool wrong = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        l[j] *= s.inv[m];
+        const bool there = lane + 32 * j < a.n_exp;
+        wrong |= there && !(fabsf(l[j]) <= FLT_MAX);
+        key[j] = there ? key_of(l[j]) : 0u;
+      }
+      if (__any_sync(0xffffffffu, wrong) && lane == 0 && cta == 0) atomicExch(a.status, kStatusValue);
+      float top = 0.f, Z = 0.f, mine = 0.f;
+      int mye = 0;
+      unsigned taken = 0;
 #pragma unroll 1
-    for (int k = 0; k < a.top_k; ++k) {
-      unsigned best = 0;
+      for (int k = 0; k < a.top_k; ++k) {
+        unsigned best = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) best = max(best, key[j]);
-      best = __reduce_max_sync(0xffffffffu, best);
-      int first = INT_MAX;  // the lowest one with that value (of value 0: not taken)
+        for (int j = 0; j < 8; ++j) best = max(best, key[j]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        int first = INT_MAX;  // the lowest one with that value (of value 0: not taken)
 #pragma unroll
-      for (int j = 7; j >= 0; --j)
-        if (key[j] == best && !(taken >> j & 1) && lane + 32 * j < a.n_exp) first = lane + 32 * j;
-      const int be = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
-      if ((be & 31) == lane) {
-        taken |= 1u << (be >> 5);
+        for (int j = 7; j >= 0; --j)
+          if (key[j] == best && !(taken >> j & 1) && lane + 32 * j < a.n_exp) first = lane + 32 * j;
+        const int be = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
+        if ((be & 31) == lane) {
+          taken |= 1u << (be >> 5);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j == be >> 5) key[j] = 0u;
+          for (int j = 0; j < 8; ++j)
+            if (j == be >> 5) key[j] = 0u;
+        }
+        const float bv = best ? key_float(best) : -FLT_MAX;
+        if (k == 0) top = bv;
+        Z += expf(bv - top);
+        if (lane == k) {
+          mine = bv;
+          mye = be;
+        }
       }
-      const float bv = best ? key_float(best) : -FLT_MAX;
-      if (k == 0) top = bv;
-      Z += expf(bv - top);
-      if (lane == k) {
-        mine = bv;
-        mye = be;
-      }
-    }
-    if (lane < a.top_k) {
-      const float gt = expf(mine - top) / Z;
-      s.gate[m][lane] = gt;
-      s.sel[m][lane] = (uint8_t)mye;
-      atomicOr(&s.mask[mye], 1u << m);
-      if (cta == 0) {
-        if (a.idx) a.idx[(size_t)m * a.top_k + lane] = mye;
-        if (a.gate) a.gate[(size_t)m * a.top_k + lane] = gt;
-      }
+      if (lane < a.top_k) chosen(m, lane, mye, expf(mine - top) / Z);
     }
   }
   __syncthreads();

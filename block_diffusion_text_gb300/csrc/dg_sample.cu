@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       }
     }
   };
-  using Ahead1 = std::integral_constant<int, 1>;
+  using Ahead2 = std::integral_constant<int, 2>;
   using Ahead4 = std::integral_constant<int, 4>;
   // this warp's run: values [first, last)
   auto run_first = [&](int r) { return min(a.V, r / kSpWarps * a.slice + r % kSpWarps * a.run4 * 4); };
@@ -323,14 +323,15 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   // Everything from here on is the same in all CTAs of the cluster but for their
   // slices, so that they come to every exchange together, until the leader goes on alone.
   const bool greedy = T < 5.421010862427522e-20f || top_k == 1;  // 2^-64
-  if (tid == 0) {  // in 64 bits, which few units compute
+  if (tid == 0) {
     unsigned fk = 1u;
     if (!greedy) {
-      const double c = 1.4426950408889634074 / (double)T, xm = (double)m * c;
-      const float base_v = fabs(xm) > 16384.0 ? m : 0.f;
-      s.scale = SpScale{(float)c, (float)(c - (double)(float)c), base_v, (int)ceil(base_v != 0.f ? 0.0 : xm) + 1};
+      // log2(e) / T in two floats: the quotient, and what it leaves of log2(e) (exact) over T
+      const float c = 1.44269502162933349609f / T, clo = (fmaf(-c, T, 1.44269502162933349609f) + 1.92596299112661e-8f) / T;
+      const float base_v = fabsf(m * c) > 16384.0f ? m : 0.f;
+      s.scale = SpScale{c, clo, base_v, base_v != 0.f ? 1 : (int)ceilf(m * c) + 1};
       if (min_p > 0.f) {
-        // w >= min_p where l >= max + T ln(min_p): the first float at or above that border
+        // w >= min_p where l >= max + T ln(min_p): the first float at or above that border, worked out in 64 bits
         const double border = (double)m + (double)T * log((double)min_p);
         if (border >= -(double)FLT_MAX) {
           const float f = (float)border;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     const float least_v = key_float(max(least, 0x00800000u));  // no finite value is below
     w = 0;
     c = eq = 0;
-    each4(Ahead1{}, i0, i1, [&](const float4& v4, int) {
+    each4(Ahead2{}, i0, i1, [&](const float4& v4, int) {
       if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= least_v)) return;
       const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
@@ -671,7 +672,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           list(v4.w);
         });
       } else {
-        each4(Ahead1{}, first, last, [&](const float4& v4, int) {
+        each4(Ahead2{}, first, last, [&](const float4& v4, int) {
           const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
