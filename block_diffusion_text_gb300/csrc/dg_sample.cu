@@ -584,8 +584,11 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     const float floor_v = key_float(max(floor_key, 0x00800000u));
     // What min_p leaves out needs no list: a bracket that ends below its floor begins
     // there, and one that lies below it is empty, with all from the floor on above it.
+    // Nothing that may be kept lies below it then.
+    bool to_floor = false;
     auto at_floor = [&]() {
-      if (by_k || !floored || lo >= floor_v) return;
+      to_floor = !by_k && floored && lo <= floor_v;
+      if (!to_floor) return;
       lo = floor_v;
       if (hi < floor_v) {
         hi = key_float(floor_key - 1u);
@@ -730,7 +733,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         target = share(all);
         // (the border lies in the bracket, or below the floor, where it is of no matter; a
         // list that ran over is not added up)
-        const bool border = above < target && (above + t_list >= target || (floored && lo >= floor_v));
+        const bool border = above < target && (above + t_list >= target || to_floor);
         listed = border && t_n < (1ull << 40);
         if (!border && sampled && round + 1 < kSpTries) {
           // the sample's own sums from the nearer end of the bracket on

@@ -151,6 +151,32 @@ def test_pitch_out_and_optional_outputs():
     assert rc == 0 and torch.equal(tok.cpu(), want[0])
 
 
+@pytest.mark.parametrize("R,period", [(1, 4), (3, 4), (40, 8)])
+@pytest.mark.parametrize("high", [0, 1])
+def test_logits_whose_sample_misleads(R, period, high):
+    """Every period-th 128 values are higher: the ones that a sample of every period-th sees, or ones that it does not.
+    The cuts lie among either, above and below min_p's floor."""
+    g = torch.Generator().manual_seed(10 * R + high)
+    V = 262144
+    x = 0.3 * torch.randn(R, V, generator=g) + 4.0 * (torch.arange(V) // 128 % period == high)
+    u = torch.rand(R, generator=g)
+    p = 0.3 + 0.69 * torch.arange(R).float() / R if R > 3 else torch.tensor([0.95, 0.6, 0.3])[:R]
+    floors = torch.tensor([0.0, 2.0 ** -9, 0.01, 0.1, 0.5])
+    for n in range(5 if R <= 3 else 2):
+        mp = floors[(torch.arange(R) + n) % 5]
+        check(x, u, p=p, mp=mp)
+    check(x.to(torch.bfloat16), u, p=p, mp=2.0 ** -9)
+
+
+def test_many_long_rows():
+    """More rows than run at once, from flat to sharp, cut by top_p and min_p."""
+    g = torch.Generator().manual_seed(5)
+    R, V = 80, 262144
+    x = torch.randn(R, V, generator=g) * torch.exp(2.4 * torch.rand(R, 1, generator=g) - 0.7)
+    check(x, torch.rand(R, generator=g), p=0.5 + 0.499 * torch.rand(R, generator=g),
+          mp=torch.where(torch.arange(R) % 2 == 0, 0.0, 0.05 * torch.rand(R, generator=g) ** 2))
+
+
 def test_longest_vocabulary():
     g = torch.Generator().manual_seed(5)
     x = torch.randn(3, 1 << 20, generator=g)
