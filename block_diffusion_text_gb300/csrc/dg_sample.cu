@@ -640,7 +640,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           const int b = bin1(vs[e]);
           atomicAdd(&s.count[b], 1u);
           if (!by_k) {
-            const unsigned w = (unsigned)(weight(vs[e]) >> (kSpTop - bits));
+            // rounded up or down by the value's place, so that many small weights lose nothing on the whole
+            const unsigned long long dither = (unsigned)(i + e) * 0x9e3779b1u & ((1u << (kSpTop - bits)) - 1u);
+            const unsigned w = (unsigned)((weight(vs[e]) + dither) >> (kSpTop - bits));
             if (w) atomicAdd(&s.lo[b], w);
           }
         }
