@@ -15,6 +15,7 @@
 // and g + 8], 16 bytes for a lane.
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "dg_common.cuh"
 #include "dg_internal.h"
@@ -383,161 +384,204 @@ cudaError_t launch_w4(const W4Args& args, cudaStream_t st) {
 // More than eight rows over many row tiles: x no longer stays in L1 beside the rings
 // (it would come from L2 twice as often as the codes from HBM), so all warps of a CTA
 // work on the same columns at the same time, on row tiles of their own, and x lies in
-// shared memory for kChunk tiles of columns at a time, in the order of the products'
-// operands.  A CTA has an equal share of all row tiles, 32 at a time, two to a warp.
+// shared memory for kW4Chunk tiles of columns at a time, in the order of the products'
+// operands.  A warp has a pair of neighbouring row tiles, whose codes of a tile of
+// columns are one piece of memory: one lane copies a chunk's (cp.async.bulk, two chunks
+// to a warp), so that little but the codes' own work is left to the others.  A CTA has
+// an equal share of all pairs, 16 at a time; a rest of eight or fewer goes tile by tile.
 constexpr int kW4WideWarps = 16;
 constexpr int kW4Chunk = 4;
 
+__device__ int g_w4_status;
+
+DG_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// y += s a for two sums at once
+DG_DEV void fma_two(float& y0, float& y1, float s, float a0, float a1) {
+  asm("{\n .reg .b64 y, s, a;\n mov.b64 y, {%0, %1};\n mov.b64 s, {%2, %2};\n mov.b64 a, {%3, %4};\n"
+      " fma.rn.f32x2 y, s, a, y;\n mov.b64 {%0, %1}, y;\n}\n"
+      : "+f"(y0), "+f"(y1)
+      : "f"(s), "f"(a0), "f"(a1));
+}
+
+template <int NT, int SG>
+struct W4Wide {
+  static constexpr int kX = NT * 1024;  // x of a tile of columns
+  static constexpr int kCodes = kW4Chunk * 2 * kW4Bytes, kSlot = kCodes + kW4Chunk * SG * 128;
+  static constexpr int kSmem = kW4WideWarps * 2 * kSlot + 2 * kW4Chunk * kX;
+};
+
 template <int NT, int SG>
 __global__ void __launch_bounds__(kW4WideWarps * 32, 1) w4_wide_kernel(W4Args a) {
-  constexpr int R = 2, S = kW4Stages, kStage = R * (kW4Bytes + SG * 128), kX = NT * 1024;  // x of a tile of columns
-  extern __shared__ __align__(16) char smem[];
+  using L = W4Wide<NT, SG>;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ uint64_t full[kW4WideWarps][2];
+  __shared__ int gave_up;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
-  char* ring = smem + warp * S * kStage;
-  char* xs = smem + kW4WideWarps * S * kStage;  // [2][kW4Chunk][NT][2 halves][32 lanes][16 bytes]
-  const int KB = a.K / kW4Cols, KG = a.K / a.group, tiles = (a.N + kW4Rows - 1) / kW4Rows;
-  const int sg_shift = a.group == 2 * kW4Cols ? 1 : 0;
-  const int t0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), t1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
-  const int passes = (t1 - t0 + R * kW4WideWarps - 1) / (R * kW4WideWarps);
-  auto tile_of = [&](int pass, int r) { return t0 + (pass * R + r) * kW4WideWarps + warp; };
+  char* ring = smem + warp * 2 * L::kSlot;
+  char* xs = smem + kW4WideWarps * 2 * L::kSlot;  // [2][kW4Chunk][NT][2 halves][32 lanes][16 bytes]
+  const int KB = a.K / kW4Cols, KG = a.K / a.group, chunks = (KB + kW4Chunk - 1) / kW4Chunk;
+  const int sg_shift = a.group == 2 * kW4Cols ? 1 : 0;  // tiles of columns that share a group
+  const int pairs = (a.N + 2 * kW4Rows - 1) / (2 * kW4Rows);
+  const int p0 = (int)((int64_t)pairs * blockIdx.x / gridDim.x), p1 = (int)((int64_t)pairs * (blockIdx.x + 1) / gridDim.x);
+  const int whole = (p1 - p0) / kW4WideWarps, rest = (p1 - p0) % kW4WideWarps, passes = whole + (rest > 0);
+  // the first row tile of a pass, and how many
+  auto tile_of = [&](int pass, int& n) {
+    const int p = p0 + pass * kW4WideWarps;
+    if (pass == whole && 2 * rest <= kW4WideWarps) {
+      n = warp < 2 * rest ? 1 : 0;
+      return 2 * p + warp;
+    }
+    n = pass < whole || warp < rest ? 2 : 0;
+    return 2 * (p + warp);
+  };
 
-  int ppass = 0, pkb = 0, pslot = 0;  // what is copied next, and where it lies
-  const char *pc[R] = {}, *ps[R] = {};
-  bool there[R];
-  auto seek = [&]() {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int rt = tile_of(ppass, r);
-      there[r] = ppass < passes && rt < t1;
-      pc[r] = reinterpret_cast<const char*>(a.codes) + w4_tile(rt, 0, KB) * kW4Bytes + lane * 16;
-      ps[r] = reinterpret_cast<const char*>(a.scales + w4_scale(rt, 0, KG, g));
-    }
-  };
-  seek();
+  if (tid == 0) {
+    for (int i = 0; i < 2 * kW4WideWarps; ++i) mbar_init(&full[i / 2][i % 2], 1);
+    gave_up = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+
+  int ppass = 0, pchunk = 0, pslot = 0;  // what is copied next, and where it lies
   auto issue = [&]() {
-    const uint32_t slot = smem_u32(ring) + pslot + lane * 16;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (there[r]) {
-        cp_async16_s(slot + r * kW4Bytes, pc[r]);
-#pragma unroll
-        for (int q = 0; q < SG; ++q) cp_async4_s(slot - lane * 12 + R * kW4Bytes + (r * SG + q) * 128, ps[r] + q * 128);
-        pc[r] += kW4Tiles * kW4Bytes;
-        if (sg_shift == 0 || pkb % 2) ps[r] += SG * 128;
-      }
-    if (++pkb == KB) {
-      pkb = 0;
-      ++ppass;
-      seek();
+    if (ppass >= passes) return;
+    int n;
+    const int rt = tile_of(ppass, n);
+    if (lane == 0 && n > 0) {
+      const int kb = pchunk * kW4Chunk, nk = min(kW4Chunk, KB - kb);
+      const int g0 = SG == 2 ? 2 * kb : kb >> sg_shift, ng = SG == 2 ? 2 * nk : nk >> sg_shift;
+      uint64_t* bar = &full[warp][pslot];
+      const uint32_t slot = smem_u32(ring) + pslot * L::kSlot;
+      mbar_arrive_expect_tx(bar, nk * n * kW4Bytes + ng * 128);
+      const char* codes = reinterpret_cast<const char*>(a.codes) + w4_tile(rt, kb, KB) * kW4Bytes;
+      for (int k = 0; k < nk; ++k)
+        bulk_load(slot + k * 2 * kW4Bytes, codes + k * kW4Tiles * kW4Bytes, n * kW4Bytes, bar);
+      bulk_load(slot + L::kCodes, a.scales + w4_scale(rt / kW4Tiles * kW4Tiles, g0, KG, 0), ng * 128, bar);
     }
-    cp_async_commit();
-    pslot = pslot + kStage == S * kStage ? 0 : pslot + kStage;
+    pslot ^= 1;
+    if (++pchunk == chunks) {
+      pchunk = 0;
+      ++ppass;
+    }
   };
-  // x of the tiles of columns from kb on, 16 bytes (a lane's of one operand) at a time;
-  // rows past the last one repeat it: their sums are not stored
-  auto load_x = [&](int kb, int buf) {
-    const int n = min(kW4Chunk, KB - kb) * NT * 64;
+  // x of a chunk, 16 bytes (a lane's of one operand) at a time; rows past the last one
+  // repeat it: their sums are not stored
+  auto load_x = [&](int chunk, int buf) {
+    const int kb = chunk * kW4Chunk, n = min(kW4Chunk, KB - kb) * NT * 64;
     for (int i = tid; i < n; i += kW4WideWarps * 32) {
       const int l = i % 32, p = i / 32 % 2, nt = i / 64 % NT, k = i / (64 * NT);
       const int m = min(8 * nt + l / 4, a.M - 1);
-      cp_async16(xs + buf * kW4Chunk * kX + i * 16, a.x + m * a.ldx + (kb + k) * kW4Cols + 32 * p + 8 * (l % 4));
+      cp_async16(xs + buf * kW4Chunk * L::kX + i * 16, a.x + m * a.ldx + (kb + k) * kW4Cols + 32 * p + 8 * (l % 4));
     }
+    cp_async_commit();
   };
-  pdl_wait();
   load_x(0, 0);
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue();
-  int slot_at = 0, buf = 0;
-  bool settled = false;  // whether four groups were begun since the chunk's x
-  for (int pass = 0; pass < passes; ++pass) {
+  issue();
+  issue();
+  unsigned it = 0;  // chunks gone through
+  bool ok = true;
+  auto next_x = [&](int pass, int chunk) {
+    cp_async_wait<0>();
+    __syncthreads();  // this chunk's x is there, and the one before is done with
+    if (chunk + 1 < chunks) load_x(chunk + 1, (it + 1) & 1);
+    else if (pass + 1 < passes) load_x(0, (it + 1) & 1);
+  };
+  auto go = [&](auto tiles, int pass, int rt) {
+    constexpr int R = decltype(tiles)::value;
     float y[R][NT][4] = {};
-    const bool one = tile_of(pass, 0) < t1, two = tile_of(pass, 1) < t1;
-    for (int kb0 = 0; kb0 < KB; kb0 += kW4Chunk) {
-      const int nk = min(kW4Chunk, KB - kb0);
+    const int at_scale = L::kCodes + g * 16 + rt % kW4Tiles * 4;
 #pragma unroll 1
-      for (int k = 0; k < nk; ++k) {
-        issue();
-        if (k == 0) {
-          if (settled) cp_async_wait<S - 1>();
-          else cp_async_wait<0>();
-          __syncthreads();  // this chunk's x is there, and the one before is done with
-          const int next = kb0 + kW4Chunk < KB ? kb0 + kW4Chunk : 0;
-          if (next > 0 || pass + 1 < passes) load_x(next, buf ^ 1);  // (in the next step's group)
-          settled = nk == kW4Chunk;
-        } else {
-          cp_async_wait<S - 1>();
-        }
-        const char* slot = ring + slot_at;
-        slot_at = slot_at + kStage == S * kStage ? 0 : slot_at + kStage;
-        if (!one) continue;
-        const uint4* xb = reinterpret_cast<const uint4*>(xs + (buf * kW4Chunk + k) * kX) + lane;
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      next_x(pass, chunk);
+      ok &= mbar_wait_warp(&full[warp][it & 1], it >> 1 & 1, &g_w4_status, &gave_up);
+      const char* slot = ring + (it & 1) * L::kSlot;
+      const uint4* xb = reinterpret_cast<const uint4*>(xs + (it & 1) * kW4Chunk * L::kX) + lane;
+      const int nk = min(kW4Chunk, KB - chunk * kW4Chunk);
+#pragma unroll
+      for (int k = 0; k < kW4Chunk; ++k) {
+        if (k >= nk) break;
         uint4 cw[R];
-        uint32_t sw[R][SG];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          cw[r] = *reinterpret_cast<const uint4*>(slot + r * kW4Bytes + lane * 16);
-#pragma unroll
-          for (int q = 0; q < SG; ++q)
-            sw[r][q] = *reinterpret_cast<const uint32_t*>(slot + R * kW4Bytes + (r * SG + q) * 128 + lane * 4);
-        }
+        for (int r = 0; r < R; ++r) cw[r] = *reinterpret_cast<const uint4*>(slot + (k * 2 + r) * kW4Bytes + lane * 16);
         float acc[R][NT][4];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           uint4 b[NT];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) b[n] = xb[(n * 2 + p) * 32];
+          for (int n = 0; n < NT; ++n) b[n] = xb[k * NT * 64 + (n * 2 + p) * 32];
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (r == 1 && !two) break;
-            const uint32_t words[4] = {cw[r].x, cw[r].y, cw[r].z, cw[r].w};
+          for (int h = 0; h < 2; ++h) {
+            uint32_t A[R][4];  // of all row tiles first: their products are independent
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t A[4];
+            for (int r = 0; r < R; ++r) {
+              const uint32_t word = p ? (h ? cw[r].w : cw[r].z) : (h ? cw[r].y : cw[r].x);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) A[i] = w4_pair(words[2 * p + h], i);
+              for (int i = 0; i < 4; ++i) A[r][i] = w4_pair(word, i);
+            }
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                const uint32_t b0 = h ? b[n].z : b[n].x, b1 = h ? b[n].w : b[n].y;
-                if (h == 0 && (SG == 2 || p == 0)) mma_bf16_first(acc[r][n], A, b0, b1);
-                else mma_bf16_more(acc[r][n], A, b0, b1);
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t b0 = h ? b[n].z : b[n].x, b1 = h ? b[n].w : b[n].y;
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                if (h == 0 && (SG == 2 || p == 0)) mma_bf16_first(acc[r][n], A[r], b0, b1);
+                else mma_bf16_more(acc[r][n], A[r], b0, b1);
               }
             }
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
             if (SG == 2 || p == 1) {
-              const uint32_t s = sw[r][SG == 2 ? p : 0];
+              const int group = SG == 2 ? 2 * k + p : k >> sg_shift;
+              const uint32_t s = *reinterpret_cast<const uint32_t*>(slot + at_scale + group * 128 + r * 4);
               const float s0 = __uint_as_float(s << 16), s1 = __uint_as_float(s & 0xffff0000u);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                y[r][n][0] += s0 * acc[r][n][0];
-                y[r][n][1] += s0 * acc[r][n][1];
-                y[r][n][2] += s1 * acc[r][n][2];
-                y[r][n][3] += s1 * acc[r][n][3];
+                fma_two(y[r][n][0], y[r][n][1], s0, acc[r][n][0], acc[r][n][1]);
+                fma_two(y[r][n][2], y[r][n][3], s1, acc[r][n][2], acc[r][n][3]);
               }
             }
           }
         }
       }
-      buf ^= 1;
+      __syncwarp();  // the slot is free
+      issue();
+      ++it;
     }
+    if (!ok) return;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int rt = tile_of(pass, r);
-      if (rt >= t1) break;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < NT * 4; ++i) {
-        const int m = 8 * (i / 4) + 2 * t + i % 2, col = rt * kW4Rows + g + 8 * (i % 4 / 2);
+        const int m = 8 * (i / 4) + 2 * t + i % 2, col = (rt + r) * kW4Rows + g + 8 * (i % 4 / 2);
         w4_store(a, m, col, y[r][i / 4][i % 4]);
       }
+  };
+#pragma unroll 1
+  for (int pass = 0; pass < passes; ++pass) {
+    int n;
+    const int rt = tile_of(pass, n);
+    if (n == 2) {
+      go(std::integral_constant<int, 2>{}, pass, rt);
+    } else if (n == 1) {
+      go(std::integral_constant<int, 1>{}, pass, rt);
+    } else {
+      for (int chunk = 0; chunk < chunks; ++chunk, ++it) next_x(pass, chunk);
     }
   }
-  cp_async_wait<0>();
 }
 
 template <int NT, int SG>
 cudaError_t launch_w4_wide(const W4Args& a, cudaStream_t st) {
-  const int smem = kW4WideWarps * kW4Stages * 2 * (kW4Bytes + SG * 128) + 2 * kW4Chunk * NT * 1024;
-  const cudaError_t e = set_smem_once<w4_wide_kernel<NT, SG>>(smem);
+  using L = W4Wide<NT, SG>;
+  const cudaError_t e = set_smem_once<w4_wide_kernel<NT, SG>>(L::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(w4_wide_kernel<NT, SG>, dim3(kTargetCtas), dim3(kW4WideWarps * 32), (size_t)smem, st, a);
+  return launch_pdl(w4_wide_kernel<NT, SG>, dim3(kTargetCtas), dim3(kW4WideWarps * 32), (size_t)L::kSmem, st, a);
 }
 
 template <int SG>
@@ -630,4 +674,11 @@ extern "C" dg_status dg_w4_matvec(const dg_w4* w, const void* x, int32_t ldx, in
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool wide = cdiv(w->N, kW4Rows) >= 16 * kTargetCtas;
   return from_cuda(w->group == 32 ? launch_w4_rows<2>(a, wide, st) : launch_w4_rows<1>(a, wide, st));
+}
+
+extern "C" dg_status dg_w4_status(int32_t* status, void* stream) {
+  if (!status) return DG_ERR_ARG;
+  void* word = nullptr;
+  if (cudaGetSymbolAddress(&word, g_w4_status) != cudaSuccess) return DG_ERR_CUDA;
+  return dg_read_status(word, status, stream);
 }

@@ -29,7 +29,7 @@ EXPORTS = ("dg_status_string", "dg_workspace_size", "dg_read_status", "dg_tau", 
            "dg_attention_noalloc", "dg_attention_noalloc_status", "dg_debug_wait_timeout",
            "dg_canvas_init_masked", "dg_denoise_step_masked", "dg_denoise_canvas_masked", "dg_prefill",
            "dg_quantize_rows_e4m3", "dg_kv8_append", "dg_kv8_read", "dg_kv8_attention_workspace",
-           "dg_kv8_attention", "dg_w4_bytes", "dg_w4_quantize", "dg_w4_pack", "dg_w4_read", "dg_w4_matvec",
+           "dg_kv8_attention", "dg_w4_bytes", "dg_w4_quantize", "dg_w4_pack", "dg_w4_read", "dg_w4_matvec", "dg_w4_status",
            "dg_qk_norm_rope", "dg_moe_tokens_workspace", "dg_moe_tokens", "dg_sample")
 
 
@@ -159,6 +159,7 @@ def load():
             L.dg_w4_pack.argtypes = [vp, vp, vp, vp]
             L.dg_w4_read.argtypes = [vp, vp, i32, vp]
             L.dg_w4_matvec.argtypes = [vp, vp, i32, i32, vp, ct.c_float, vp, i32, vp, i32, i32, vp]
+            L.dg_w4_status.argtypes = [ct.POINTER(i32), vp]
             L.dg_qk_norm_rope.argtypes = [vp, ct.c_int64, ct.c_int64] + [vp] * 6 + [i32] * 5 + [ct.c_float] * 2 + [vp]
             L.dg_moe_tokens_workspace.argtypes = [vp, i32, ct.POINTER(ct.c_size_t)]
             L.dg_moe_tokens.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp, ct.c_size_t, vp]
@@ -847,6 +848,13 @@ def w4_matvec(w: W4Matrix, x: torch.Tensor, alpha: torch.Tensor | None = None, c
     if rc:
         raise DgError(rc, "dg_w4_matvec")
     return out
+
+
+def w4_status(stream=None) -> int:
+    """Status word of the 4-bit products on the current device (dg_w4_status; synchronises the stream)."""
+    st = ct.c_int32()
+    _check(load().dg_w4_status(ct.byref(st), _stream(stream)), "dg_w4_status")
+    return st.value
 
 
 _qk_plans = {}  # shapes, strides and heads of qkv -> (B, C, hd, strides, output shapes)

@@ -508,6 +508,10 @@ DG_API dg_status dg_w4_read(const dg_w4* w, float* out, int32_t ldo, void* strea
 DG_API dg_status dg_w4_matvec(const dg_w4* w, const void* x, int32_t ldx, int32_t M, const float* alpha, float coef,
                               const void* resid, int32_t ldr, void* y, int32_t ldy, int32_t y_f32, void* stream);
 
+/* Status word of the products on the current device (dg_read_status): DG_ERR_TIMEOUT once
+ * a bounded wait of one of them ran out (its rows were not written), else DG_OK.     */
+DG_API dg_status dg_w4_status(int32_t* status, void* stream);
+
 /* Norms of the query and key heads with the position rotation, from the packed
  * projections of the tokens (e.g. of dg_w4_matvec with Wq, Wk, Wv stacked) into the
  * layouts that dg_kv8_append and the attention calls take.

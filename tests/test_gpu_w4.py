@@ -181,3 +181,28 @@ def test_products_of_many_rows(M, N, K, group):
     x = torch.randn(M, K, generator=g).to(BF)
     check(w, c, s, x, dtype=torch.float32, alpha=torch.rand(M, generator=g) + 0.5)
     check(w, c, s, x, resid=torch.randn(M, N, generator=g).to(BF))
+
+
+@pytest.mark.parametrize("M,group", [(8, 64), (12, 64), (32, 128), (32, 32)])
+def test_long_products_side_by_side(M, group):
+    """Two streams and a captured product at once over the same long matrix: the same bits as alone."""
+    g = torch.Generator().manual_seed(M + group)
+    N, K = 39001, 384
+    c, s = drawn(g, N, K, group)
+    w = dg.W4Matrix.from_codes(c.cuda(), s.cuda())
+    xs = [torch.randn(M, K, generator=g).to(BF).cuda() for _ in range(3)]
+    want = [check(w, c, s, x, dtype=torch.float32) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    out = [torch.zeros(M, N, device="cuda") for _ in xs]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=streams[2]):
+        dg.w4_matvec(w, xs[2], out=out[2], dtype=torch.float32)
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                dg.w4_matvec(w, xs[i], out=out[i], dtype=torch.float32)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert dg.w4_status() == 0

@@ -85,3 +85,7 @@ def test_quantised_weights_are_within_half_a_step(group):
     # the scale is rounded by 2^-9 at most: the largest weight, 7 steps before, is off by 7 * 2^-9 of a step more
     assert bool((err <= step * (0.5 + 7 * 2.0 ** -8)).all())
     assert c.min() >= 1 and c.max() <= 15
+
+
+def test_status_refuses_null(dg):
+    assert dg.load().dg_w4_status(None, None) == 1
