@@ -1025,9 +1025,13 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     for (int e = 0; e < 4; ++e) {
       if (ws[e] && goal >= at && goal < at + ws[e]) {
         a.token[row] = i + e;
-        if (a.logprob)
-          a.logprob[row] = greedy ? 0.f : (float)(((double)vs[e] - (double)sc.base) / (double)T -
-                                                  log((double)total) + 0.69314718055994530942 * (kSpTop - sc.nref));
+        if (a.logprob) {
+          // a likely token's is taken from what the others weigh, so that it is exact near 0 too
+          const unsigned long long rest = total - ws[e];
+          a.logprob[row] = rest < ws[e] ? (float)(log1p(-(double)rest / (double)total) + 0.0)
+                                        : (float)(((double)vs[e] - (double)sc.base) / (double)T - log((double)total) +
+                                                  0.69314718055994530942 * (kSpTop - sc.nref));
+        }
       }
       at += ws[e];
     }
@@ -1037,12 +1041,18 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   }
 }
 
-// CTAs of a row's cluster: slices of 65536 values at most (so many rows under way fit
-// L2), shorter ones as long as there are SMs for them and 2048 values for each.
+// CTAs of a row's cluster: slices of 65536 values at most (256 rows of 262144: 4 CTAs
+// 290 us, 8 353, 1 461), shorter ones of 2048 values at least while that gives every SM
+// no more than one CTA (8 rows of 262144: 16 CTAs 43 us, 4 63), and of 16384 up to two
+// (64 rows of 151936: 4 CTAs 68 us, 2 75; 32 of 50257 in 8 CTAs 40, in 4 36).
 int sample_ctas(int R, int V) {
   int c = 1;
   while (c < kSpMaxCluster && (int64_t)c * 65536 < V) c *= 2;
-  while (c < kSpMaxCluster && (int64_t)R * c * 2 <= 2 * kTargetCtas && V >= 2 * c * 2048) c *= 2;
+  while (c < kSpMaxCluster) {
+    const int64_t all = (int64_t)R * c * 2, least = all <= kTargetCtas ? 2048 : 16384;
+    if (all > 2 * kTargetCtas || V < 2 * c * least) break;
+    c *= 2;
+  }
   return c;
 }
 

@@ -197,6 +197,23 @@ def test_shares_follow_the_weights():
     assert bool((tok[1:] >= tok[:-1]).all())
 
 
+@pytest.mark.parametrize("T", [1.0, 0.37])
+def test_logprob_of_nearly_certain_tokens(T):
+    """Relative to itself: the others' weights are off by 2^-28 and a unit, 2^-41 of the largest at most, each; the result
+    by 2^-24."""
+    d = torch.tensor([0.0, 1.0, 3.0, 6.0, 9.0, 12.0, 40.0])
+    x = torch.full((len(d), 7), -1e4)
+    x[:, 3], x[:, 5], x[:, 6] = 20.0, 20.0 - d, 19.5 - d
+    tok, lp, kept = (t.cpu() for t in dg.sample(x.cuda(), torch.full((len(d),), 1e-6, device="cuda"), temperature=T))
+    tk = float(torch.tensor(T, dtype=torch.float32))
+    rest = torch.exp((x[:, 5:].double() - 20.0) / tk).sum(1)
+    want = -torch.log1p(rest)
+    assert tok.tolist() == [3] * len(d)
+    assert bool(((lp.double() - want).abs() <= -want * (2.0 ** -24 + 2.0 ** -27) + 2 * 2.0 ** -41).all()), (lp, want)
+    tok, lp, kept = (t.cpu() for t in dg.sample(x.cuda(), torch.full((len(d),), 0.3, device="cuda"), temperature=T, top_p=1e-3))
+    assert kept.tolist() == [1] * len(d) and tok.tolist() == [3] * len(d) and bool((lp == 0).all())
+
+
 def test_streams_graphs_and_the_same_bits():
     g = torch.Generator().manual_seed(6)
     x = torch.randn(40, 70000, generator=g).cuda()
