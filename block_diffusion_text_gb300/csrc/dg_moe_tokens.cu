@@ -3,9 +3,9 @@
 //   x = RMSNorm(h), r = x Wr^T, e_j = the top_k experts of r, g = softmax of their r
 //   out = h + sum_j g_j We2_ej GELU(We1_ej x) + We2_s GELU(We1_s x)
 //
-// The chosen experts' weights bound it: each matrix is read once, whatever the
-// number of tokens that chose it.  One persistent CTA per SM works through three
-// phases with a barrier of the grid between them, as the data demands:
+// The chosen experts' weights bound it: each matrix is read once for each eight of the
+// tokens that chose it (from L2 after the first).  One persistent CTA per SM works
+// through three phases with a barrier of the grid between them, as the data demands:
 //   0  the router's logits
 //   1  every CTA works the routing out for itself; the hidden rows of the chosen experts
 //      and of the shared one
@@ -13,11 +13,13 @@
 // In each phase the rows of the weights that it needs are cut into equal ranges,
 // one for each CTA, row by row, so that all SMs read the same number of bytes.
 //
-// Warp MMAs, the weights as the 16-row operand, the tokens as the columns; a row of
-// 32 tokens is four column tiles, and those without a token of the expert are
-// skipped.  x W^T is taken as (h W^T) / rms, so the tokens enter as the bf16 they
-// are; the hidden values, which carry their gate (the second product is linear), as
-// pairs of bf16 (16 bits or more).  A warp's share of the products' inner dimension
+// Warp MMAs, the weights as the 16-row operand, up to eight of the expert's own tokens as
+// the columns: an expert with more of them comes several times.  (With a column for
+// every token of the call, tiles of eight of them where one had chosen the expert,
+// 32 tokens took 355 us at 128 experts of 768 x 2816.)
+// x W^T is taken as (h W^T) / rms, so the tokens enter as the bf16 they are; the hidden
+// values, which carry their gate (the second product is linear), as pairs of bf16 (16
+// bits or more).  A warp's share of the products' inner dimension
 // is a block of 64 columns in turn; its own weights come through a ring of cp.async
 // copies that only the lane that issued them reads, so nothing has to be waited for
 // but the lane's own copies.
@@ -36,19 +38,20 @@ constexpr int kMtThreads = kMtWarps * 32;
 constexpr int kMtStages = 2;
 constexpr int kMtRows = 32;     // rows of a unit: two MMA tiles
 constexpr int kMtStage = kMtRows * 128;  // 64 columns of them
-// Units of a round: the warps' parts of their sums, 16 and one more for each, have to
-// fit beside the rings.
-constexpr int mt_units(int NT) { return NT == 4 ? 4 : 16; }
+constexpr int kMtUnits = 16;    // units of a round
+constexpr int kMtVals = 8;      // sums of a unit in a lane
+constexpr int kMtPitch = kMtRows + 1;    // of a token's sums of an output unit
 constexpr int kMtMaxM = 32;
 constexpr int kMtMaxExp = 256, kMtMaxK = 16;
+constexpr int kMtMaxSegs = kMtMaxExp + (kMtMaxM * kMtMaxK + kMtMaxM) / 8;
 
 struct MtArgs {
   const __nv_bfloat16* h;                  // [M][d]
   __nv_bfloat16* out;                      // [M][d], may be h
   const __nv_bfloat16 *Wr, *W1, *W2;       // [n_exp][d], [n_exp + 1][Fe][d], [n_exp + 1][d][Fe]
   float* logits;                           // [M][n_exp], before the product with 1 / rms
-  __nv_bfloat16* hid;                      // [M (top_k + 1) + 1][Fe / 32][2][32]: gate GELU(x We1^T), the values as
-                                           // bf16 and what that leaves; the last row is zeros
+  __nv_bfloat16* hid;                      // [M (top_k + 1)][Fe / 32][2][32]: gate GELU(x We1^T), the values as
+                                           // bf16 and what that leaves
   int* idx;                                // [M][top_k] or null
   float* gate;                             // [M][top_k] or null
   int* status;
@@ -57,21 +60,21 @@ struct MtArgs {
   float eps;
 };
 
-struct MtExpert {
-  int e;
-  unsigned mask;                           // its tokens
+// An expert with up to eight of its tokens
+struct MtSeg {
+  int e, n;
+  uint8_t tok[8], rank[8];                 // the tokens, and the expert's place among theirs
 };
 
 struct MtShared {
   float inv[kMtMaxM];
   float squares[kMtMaxM][kMtWarps];
   float gate[kMtMaxM][kMtMaxK];
-  unsigned mask[kMtMaxExp];                // tokens of every expert
+  unsigned mask[kMtMaxExp + 32];           // tokens of every expert, all for the shared one, and zeros
   uint8_t sel[kMtMaxM][kMtMaxK];           // a token's experts in rank order
-  uint16_t pos[kMtMaxExp];                 // an expert's place in ex
-  MtExpert ex[kMtMaxExp + 1];              // the experts with tokens, ascending, and the shared one
-  uint8_t rank[kMtMaxExp + 1][kMtMaxM];    // and the place of each of their tokens
-  int nact;
+  uint16_t pos[kMtMaxExp + 1];             // an expert's first place in seg
+  MtSeg seg[kMtMaxSegs];                   // of the experts with tokens, ascending, and the shared one's
+  int nseg;
   int stop;
 };
 
@@ -130,16 +133,11 @@ DG_DEV void load_block(char* slot, const __nv_bfloat16* src, int pitch, int rows
     }
 }
 
-DG_DEV unsigned tiles_of(unsigned mask) {  // a bit for each eight tokens that hold one
-  return (mask & 0xffu ? 1u : 0u) | (mask & 0xff00u ? 2u : 0u) | (mask & 0xff0000u ? 4u : 0u) | (mask & 0xff000000u ? 8u : 0u);
-}
-
 // Rows [r0, r1) cut into units of 32 rows at most, from r0 to the border rb (a
 // matrix's end) and from there on.  (Further matrices begin at multiples of 32 from
 // there: their rows are multiples of 128.)
 struct MtCut {
   int r0, rb, r1, U0, U;
-  DG_DEV MtCut() {}
   DG_DEV MtCut(int first, int end, int border) : r0(first), r1(end) {
     rb = border > first && border < end ? border : end;
     U0 = (rb - r0 + kMtRows - 1) / kMtRows;
@@ -149,16 +147,15 @@ struct MtCut {
   DG_DEV int rows(int u) const { return min(kMtRows, (u < U0 ? rb : r1) - row(u)); }
 };
 
-template <int NT>
 __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   extern __shared__ __align__(16) char smem[];
   char* ring = smem + (threadIdx.x / 32) * kMtStages * kMtStage;
-  float* red = reinterpret_cast<float*>(smem + kMtWarps * kMtStages * kMtStage);  // [warps + units - 1][kVals][32]
+  // sums: [warps + units - 1][kMtVals][32], or [warps][M][kMtPitch] of an output unit
+  float* red = reinterpret_cast<float*>(smem + kMtWarps * kMtStages * kMtStage);
   __shared__ MtShared s;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int K1 = a.top_k + 1, KB1 = a.d / 64, KB2 = a.Fe / 64;
   const int cta = blockIdx.x, ctas = gridDim.x;
-  const unsigned all = a.M == 32 ? 0xffffffffu : (1u << a.M) - 1;
   if (tid == 0) s.stop = 0;
 
   // 1 / rms of every token, for this CTA's own use: 16 / M warps to a token
@@ -197,17 +194,17 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   // The engine of all phases.  Work comes in rounds of some segments, matrices of KB
   // blocks of 64 columns and up to 32 rows; a round's blocks, in that order, are dealt to
   // the warps in equal shares, so a warp has parts of one segment or of several: a task
-  // each.  Its sums stay in registers over the tasks of a unit (all of the round with
-  // kOne, else one segment) and go to `red` at its end; the parts of a unit are added
-  // up, in order, when the round ends, and given to put(round, unit, row, token, sum).
+  // each.  The parts of a segment's sums are added up, in order, when the round ends,
+  // and given to put(round, segment, row, column, sum); with kOne the round is one unit of
+  // output rows, to which all segments add: a warp adds its parts up for their tokens,
+  // and put gets (round, 0, row, token, sum).
   // The first copies are on their way before gate() is passed (the weights wait for
-  // nobody).  They run ahead over all borders, the tokens' values only within a task (a block
-  // ahead, where the registers leave room).
-  constexpr int kVals = 2 * NT * 4;  // of a unit, in a lane
+  // nobody).  They run ahead over all borders, the tokens' values a block ahead within a
+  // task.
   auto stream = [&](int F, const auto& segments, int KB, int pitch, auto one, const auto& seg_w, const auto& seg_b,
                     const __nv_bfloat16* values, auto pair, const auto& gate, const auto& meanwhile, const auto& put) {
-    constexpr bool kOne = decltype(one)::value, kPair = decltype(pair)::value, kAhead = NT <= 2;
-    constexpr int kB = kPair ? 2 : 1;
+    constexpr bool kOne = decltype(one)::value;
+    constexpr int kB = decltype(pair)::value ? 2 : 1;
     // of n blocks; where there are fewer blocks than warps, one each for the first warps
     auto share = [&](int n, int* first, int* end) {
       const int W = min(n, kMtWarps);
@@ -240,6 +237,12 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     };
 #pragma unroll 1
     for (int s0 = 0; s0 < kMtStages; ++s0) issue();
+    float* own = red + warp * a.M * kMtPitch;
+    auto clear = [&]() {
+      for (int i = lane; i < a.M * kMtPitch; i += 32) own[i] = 0.f;
+      __syncwarp();
+    };
+    if (kOne) clear();
     if (!gate()) {
       cp_async_wait<0>();
       return false;
@@ -248,44 +251,27 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
 #pragma unroll 1
     for (int f = 0; f < F; ++f) {
       const int segs = segments(f), total = segs * KB;
-      float acc[2][NT][4] = {};
-      auto leave = [&](int unit) {
-        float* part = red + (warp + unit) * kVals * 32 + lane;
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) {
-          part[i * 32] = acc[i / (4 * NT)][i / 4 % NT][i % 4];
-          acc[i / (4 * NT)][i / 4 % NT][i % 4] = 0.f;
-        }
-      };
       int i, end;
       share(total, &i, &end);
 #pragma unroll 1
       while (i < end) {
         const int seg = i / KB, kb = i - seg * KB;
-        int off[NT], nb = min(KB - kb, end - i);
-        unsigned tiles;
+        int nb = min(KB - kb, end - i);
         i += nb;
-        seg_b(f, seg, off, &tiles);
-        const __nv_bfloat16* from[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) from[n] = values + off[n] + kb * 64 * kB;
-        uint4 b[NT][2][kB];
+        const __nv_bfloat16* from = values + seg_b(f, seg) + kb * 64 * kB;
+        float acc[2][4] = {};
+        uint4 b[2][kB];
         auto load_b = [&]() {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (NT == 1 || (tiles >> n & 1)) {
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-              for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int q = 0; q < kB; ++q) b[n][p][q] = *reinterpret_cast<const uint4*>(from[n] + (p * kB + q) * 32);
-              from[n] += 64 * kB;
-            }
+            for (int q = 0; q < kB; ++q) b[p][q] = *reinterpret_cast<const uint4*>(from + (p * kB + q) * 32);
+          from += 64 * kB;
         };
-        if (kAhead) load_b();
+        load_b();
 #pragma unroll 1
         for (; nb > 0; --nb) {
           cp_async_wait<kMtStages - 1>();
-          if (!kAhead) load_b();
           const char* at = ring + slot + lane * 16;
           slot = slot + kMtStage == kMtStages * kMtStage ? 0 : slot + kMtStage;
           uint32_t A[2][2][2][4];
@@ -300,47 +286,65 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
             }
           issue();  // into the slot just read
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (NT == 1 || (tiles >> n & 1)) {
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-              for (int p = 0; p < 2; ++p)
+            for (int q = 0; q < kB; ++q)
 #pragma unroll
-                for (int q = 0; q < kB; ++q)
-#pragma unroll
-                  for (int r = 0; r < 2; ++r) {
-                    mma_bf16_16816(acc[r][n], A[p][r][0], b[n][p][q].x, b[n][p][q].y);
-                    mma_bf16_16816(acc[r][n], A[p][r][1], b[n][p][q].z, b[n][p][q].w);
-                  }
-            }
-          if (kAhead && nb > 1) load_b();
+              for (int r = 0; r < 2; ++r) {
+                mma_bf16_16816(acc[r], A[p][r][0], b[p][q].x, b[p][q].y);
+                mma_bf16_16816(acc[r], A[p][r][1], b[p][q].z, b[p][q].w);
+              }
+          if (nb > 1) load_b();
         }
-        if (!kOne) leave(seg);
+        // a lane's value v: row 16 (v / 4) + g + 8 (v % 4 / 2), column 2 t + v % 2
+        if (kOne) {
+          const MtSeg& x = s.seg[seg];
+#pragma unroll
+          for (int v = 0; v < kMtVals; ++v) {
+            const int col = 2 * t + v % 2;
+            if (col < x.n) own[x.tok[col] * kMtPitch + 16 * (v / 4) + g + 8 * (v % 4 / 2)] += acc[v / 4][v % 4];
+          }
+          __syncwarp();
+        } else {
+          float* part = red + (warp + seg) * kMtVals * 32 + lane;
+#pragma unroll
+          for (int v = 0; v < kMtVals; ++v) part[v * 32] = acc[v / 4][v % 4];
+        }
       }
-      if (kOne) leave(0);
       if (f == 0) meanwhile();
-      const int W = min(total, kMtWarps);
       __syncthreads();
-      // thread i * 32 + lane of a unit's values has (row 16 r + g + 8 (i % 4 / 2), token
-      // 8 (i / 4 % NT) + 2 t + i % 2), r = i / (4 NT); its parts are those of the warps
-      // from the owner of its first block to that of its last
-      for (int v = tid; v < (kOne ? 1 : segs) * kVals * 32; v += kMtThreads) {
-        const int u = v / (kVals * 32), i = v / 32 % kVals;
-        const int w0 = kOne ? 0 : ((u * KB + 1) * W - 1) / total;
-        const int w1 = kOne ? W - 1 : ((u + 1) * KB * W - 1) / total;
-        const float* src = red + (u * kVals + i) * 32 + lane;
-        float sum = 0.f;
-        for (int w = w0; w <= w1; ++w) sum += src[w * kVals * 32];
-        put(f, u, 16 * (i / (4 * NT)) + g + 8 * (i % 4 / 2), 8 * (i / 4 % NT) + 2 * t + i % 2, sum);
+      if (kOne) {
+        for (int v = tid; v < a.M * kMtRows; v += kMtThreads) {
+          const float* src = red + v / kMtRows * kMtPitch + v % kMtRows;
+          float sum = 0.f;
+#pragma unroll 4
+          for (int w = 0; w < kMtWarps; ++w) sum += src[w * a.M * kMtPitch];
+          put(f, 0, v % kMtRows, v / kMtRows, sum);
+        }
+      } else {
+        // the parts of a segment are those of the warps from the owner of its first block
+        // to that of its last
+        const int W = min(total, kMtWarps);
+        for (int v = tid; v < segs * kMtVals * 32; v += kMtThreads) {
+          const int u = v / (kMtVals * 32), i = v / 32 % kMtVals;
+          const int w0 = ((u * KB + 1) * W - 1) / total, w1 = ((u + 1) * KB * W - 1) / total;
+          const float* src = red + (u * kMtVals + i) * 32 + lane;
+          float sum = 0.f;
+#pragma unroll 4
+          for (int w = w0; w <= w1; ++w) sum += src[w * kMtVals * 32];
+          put(f, u, 16 * (i / 4) + g + 8 * (i % 4 / 2), 2 * t + i % 2, sum);
+        }
       }
       __syncthreads();
+      if (kOne) clear();
     }
     if (F == 0) meanwhile();
     cp_async_wait<0>();
     return true;
   };
   auto go = [] { return true; };
-  constexpr int kUnits = mt_units(NT);  // of a round
-
+  auto rounds = [](const MtCut& cut) { return (cut.U + kMtUnits - 1) / kMtUnits; };
+  auto units = [](const MtCut& cut, int f) { return min(kMtUnits, cut.U - f * kMtUnits); };
   auto range = [&](int rows, int c) { return (int)((int64_t)rows * c / ctas); };
   auto store_hidden = [&](int m, int j, int f, float v) {
     const size_t at = ((size_t)m * K1 + j) * 2 * a.Fe + f / 32 * 64 + f % 32;
@@ -349,29 +353,25 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     a.hid[at + 32] = __float2bfloat16_rn(v - __bfloat162float(hi));
   };
 
-  if (cta == 0)
-    for (int i = tid; i < a.Fe / 4; i += kMtThreads)
-      reinterpret_cast<uint4*>(a.hid + (size_t)a.M * K1 * 2 * a.Fe)[i] = make_uint4(0, 0, 0, 0);
+  for (int e = tid; e < kMtMaxExp + 32; e += kMtThreads) s.mask[e] = e == a.n_exp ? ~0u >> (32 - a.M) : 0u;
 
-  for (int e = tid; e < kMtMaxExp; e += kMtThreads) s.mask[e] = 0;
-
-  // ---- phase 0: the router's rows
+  // ---- phase 0: the router's rows, for each eight tokens (a range of rows is shorter than
+  // the matrix, so it meets no second border)
   {
-    const int r0 = range(a.n_exp, cta), r1 = range(a.n_exp, cta + 1);
-    const MtCut cut(r0, r1, r1);
-    stream((cut.U + kUnits - 1) / kUnits, [&](int f) { return min(kUnits, cut.U - f * kUnits); }, KB1, a.d, std::false_type{},
+    const int R = (a.M + 7) / 8 * a.n_exp, r0 = range(R, cta), r1 = range(R, cta + 1);
+    const MtCut cut(r0, r1, min(r1, r0 / a.n_exp * a.n_exp + a.n_exp));
+    stream(rounds(cut), [&](int f) { return units(cut, f); }, KB1, a.d, std::false_type{},
            [&](int f, int u, const __nv_bfloat16** w, int* rows) {
-             *rows = cut.rows(u + f * kUnits);
-             *w = a.Wr + (int64_t)cut.row(u + f * kUnits) * a.d;
+             u += f * kMtUnits;
+             *rows = cut.rows(u);
+             *w = a.Wr + (int64_t)(cut.row(u) % a.n_exp) * a.d;
            },
-           [&](int, int, int* off, unsigned* tiles) {
-             *tiles = (1u << ((a.M + 7) / 8)) - 1;
-#pragma unroll
-             for (int n = 0; n < NT; ++n) off[n] = min(8 * n + g, a.M - 1) * a.d + 8 * t;  // columns past the last token repeat it
-           },
-           a.h, std::false_type{}, go, norms, [&](int f, int u, int row, int m, float v) {
-             u += f * kUnits;
-             if (row < cut.rows(u) && m < a.M) a.logits[(size_t)m * a.n_exp + cut.row(u) + row] = v;
+           // columns past the last token repeat it
+           [&](int f, int u) { return min(cut.row(u + f * kMtUnits) / a.n_exp * 8 + g, a.M - 1) * a.d + 8 * t; },
+           a.h, std::false_type{}, go, norms, [&](int f, int u, int row, int col, float v) {
+             u += f * kMtUnits;
+             const int r = cut.row(u) + row, m = cut.row(u) / a.n_exp * 8 + col;
+             if (row < cut.rows(u) && m < a.M) a.logits[(size_t)m * a.n_exp + r % a.n_exp] = v;
            });
   }
   if (!grid_barrier(a.arrivals, a.rounds, a.status, &s.stop)) return;
@@ -475,79 +475,78 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
   __syncthreads();
   if (warp == 0) {
     int n = 0;
-    for (int e0 = 0; e0 < a.n_exp; e0 += 32) {
-      const bool on = e0 + lane < a.n_exp && s.mask[e0 + lane] != 0;
-      const unsigned b = __ballot_sync(0xffffffffu, on);
-      if (on) {
-        const int x = n + __popc(b & ((1u << lane) - 1));
-        s.ex[x] = MtExpert{e0 + lane, s.mask[e0 + lane]};
-        s.pos[e0 + lane] = (uint16_t)x;
+#pragma unroll 1
+    for (int e = lane; e - lane <= a.n_exp; e += 32) {
+      const int tokens = __popc(s.mask[e]);
+      int first = n;
+#pragma unroll 1
+      for (int j = 0; j < a.M; j += 8) {
+        const unsigned some = __ballot_sync(0xffffffffu, tokens > j);
+        first += __popc(some & ((1u << lane) - 1));
+        n += __popc(some);
       }
-      n += __popc(b);
+      if (tokens) s.pos[e] = (uint16_t)first;
+#pragma unroll 1
+      for (int j = 0; j < tokens; j += 8, ++first) {
+        s.seg[first].e = e;
+        s.seg[first].n = min(8, tokens - j);
+      }
     }
-    if (lane == 0) {
-      s.nact = n;
-      s.ex[n] = MtExpert{a.n_exp, all};
-    }
+    if (lane == 0) s.nseg = n;
   }
   __syncthreads();
-  const int nact = s.nact;
+  const int nseg = s.nseg;
   for (int i = tid; i < a.M * K1; i += kMtThreads) {
     const int m = i / K1, j = i - m * K1;
-    s.rank[j < a.top_k ? s.pos[s.sel[m][j]] : nact][m] = (uint8_t)j;
+    const int e = j < a.top_k ? s.sel[m][j] : a.n_exp, at = __popc(s.mask[e] & ((1u << m) - 1));
+    MtSeg& x = s.seg[s.pos[e] + at / 8];
+    x.tok[at % 8] = (uint8_t)m;
+    x.rank[at % 8] = (uint8_t)j;
   }
   __syncthreads();
 
   // ---- phase 1: the hidden rows of the chosen experts, then of the shared one
   {
-    const int R = (nact + 1) * a.Fe, r0 = range(R, cta), r1 = range(R, cta + 1);
+    const int R = nseg * a.Fe, r0 = range(R, cta), r1 = range(R, cta + 1);
     const MtCut cut(r0, r1, min(r1, r0 / a.Fe * a.Fe + a.Fe));
-    stream((cut.U + kUnits - 1) / kUnits, [&](int f) { return min(kUnits, cut.U - f * kUnits); }, KB1, a.d, std::false_type{},
+    stream(rounds(cut), [&](int f) { return units(cut, f); }, KB1, a.d, std::false_type{},
            [&](int f, int u, const __nv_bfloat16** w, int* rows) {
-             const int r = cut.row(u + f * kUnits), x = r / a.Fe;
-             *rows = cut.rows(u + f * kUnits);
-             *w = a.W1 + ((int64_t)s.ex[x].e * a.Fe + r - x * a.Fe) * a.d;
+             const int r = cut.row(u + f * kMtUnits), x = r / a.Fe;
+             *rows = cut.rows(u + f * kMtUnits);
+             *w = a.W1 + ((int64_t)s.seg[x].e * a.Fe + r - x * a.Fe) * a.d;
            },
-           [&](int f, int u, int* off, unsigned* tiles) {
-             const unsigned mask = s.ex[cut.row(u + f * kUnits) / a.Fe].mask;
-             const int some = __ffs(mask) - 1;
-             *tiles = tiles_of(mask);
-#pragma unroll
-             for (int n = 0; n < NT; ++n)  // a token that does not want the expert: another's values, not stored
-               off[n] = (mask >> (8 * n + g) & 1 ? 8 * n + g : some) * a.d + 8 * t;
+           [&](int f, int u) {  // (columns without a token repeat the first)
+             const MtSeg& x = s.seg[cut.row(u + f * kMtUnits) / a.Fe];
+             return x.tok[g < x.n ? g : 0] * a.d + 8 * t;
            },
-           a.h, std::false_type{}, go, [] {}, [&](int f, int u, int row, int m, float v) {
-      u += f * kUnits;
-      if (row >= cut.rows(u)) return;
-      row += cut.row(u);
-      const int x = row / a.Fe;
-      if (!(s.ex[x].mask >> m & 1)) return;
-      const int j = s.rank[x][m];
-      store_hidden(m, j, row - x * a.Fe, (j < a.top_k ? s.gate[m][j] : 1.0f) * gelu(v * s.inv[m]));
-    });
+           a.h, std::false_type{}, go, [] {}, [&](int f, int u, int row, int col, float v) {
+             u += f * kMtUnits;
+             if (row >= cut.rows(u)) return;
+             row += cut.row(u);
+             const MtSeg& x = s.seg[row / a.Fe];
+             if (col >= x.n) return;
+             const int m = x.tok[col], j = x.rank[col];
+             store_hidden(m, j, row % a.Fe, (j < a.top_k ? s.gate[m][j] : 1.0f) * gelu(v * s.inv[m]));
+           });
   }
 
   // ---- phase 2: output columns, their sums over the experts' hidden values
   {
     const int r0 = range(a.d, cta), r1 = range(a.d, cta + 1);
     const MtCut cut(r0, r1, r1);
-    stream(cut.U, [&](int) { return nact + 1; }, KB2, a.Fe, std::true_type{},
+    stream(cut.U, [&](int) { return nseg; }, KB2, a.Fe, std::true_type{},
            [&](int f, int x, const __nv_bfloat16** w, int* rows) {
              *rows = cut.rows(f);
-             *w = a.W2 + ((int64_t)s.ex[x].e * a.d + cut.row(f)) * a.Fe;
+             *w = a.W2 + ((int64_t)s.seg[x].e * a.d + cut.row(f)) * a.Fe;
            },
-           [&](int, int x, int* off, unsigned* tiles) {
-             const unsigned mask = s.ex[x].mask;
-             *tiles = tiles_of(mask);
-#pragma unroll
-             for (int n = 0; n < NT; ++n) {  // a token that does not want the expert: the row of zeros
-               const int m = 8 * n + g;
-               off[n] = (mask >> m & 1 ? m * K1 + s.rank[x][m] : a.M * K1) * 2 * a.Fe + 8 * t;
-             }
+           [&](int, int k) {
+             const MtSeg& x = s.seg[k];
+             const int col = g < x.n ? g : 0;
+             return (x.tok[col] * K1 + x.rank[col]) * 2 * a.Fe + 8 * t;
            },
            a.hid, std::true_type{}, [&] { return grid_barrier(a.arrivals, a.rounds, a.status, &s.stop); }, [] {},
            [&](int u, int, int row, int m, float v) {
-             if (row >= cut.rows(u) || m >= a.M) return;
+             if (row >= cut.rows(u)) return;
              const int at = m * a.d + cut.row(u) + row;
              a.out[at] = __float2bfloat16_rn(__bfloat162float(a.h[at]) + v);
            });
@@ -564,7 +563,7 @@ MtWs mt_ws(int M, int n_exp, int top_k, int Fe) {
   w.logits = o;
   o = align_up(o + sizeof(float) * M * n_exp, 256);
   w.hid = o;
-  o = align_up(o + 4 * ((size_t)M * (top_k + 1) + 1) * Fe, 256);
+  o = align_up(o + 4 * (size_t)M * (top_k + 1) * Fe, 256);
   w.total = o;
   return w;
 }
@@ -579,10 +578,11 @@ dg_status check_sizes(const dg_model* m, int32_t M) {
   return DG_OK;
 }
 
-template <int NT>
 cudaError_t launch(const MtArgs& a, int sms, cudaStream_t st) {
-  const int smem = kMtWarps * kMtStages * kMtStage + (kMtWarps + mt_units(NT) - 1) * 2 * NT * 4 * 32 * (int)sizeof(float);
-  cudaError_t e = set_smem_once<moe_tokens_kernel<NT>>(smem);
+  const int sums = (kMtWarps + kMtUnits - 1) * kMtVals * 32, tokens = kMtWarps * a.M * kMtPitch;
+  constexpr int most = kMtWarps * (kMtStages * kMtStage + kMtMaxM * kMtPitch * (int)sizeof(float));
+  const int smem = kMtWarps * kMtStages * kMtStage + (sums > tokens ? sums : tokens) * (int)sizeof(float);
+  cudaError_t e = set_smem_once<moe_tokens_kernel>(most);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms);
@@ -594,7 +594,7 @@ cudaError_t launch(const MtArgs& a, int sms, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_tokens_kernel<NT>, a);
+  return cudaLaunchKernelEx(&cfg, moe_tokens_kernel, a);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -648,6 +648,6 @@ extern "C" dg_status dg_moe_tokens(const dg_model* model, int32_t layer, const v
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DG_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = M <= 8 ? launch<1>(a, sms, st) : M <= 16 ? launch<2>(a, sms, st) : launch<4>(a, sms, st);
+  const cudaError_t e = launch(a, sms, st);
   return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }

@@ -54,6 +54,13 @@ def test_model_sizes(M, d, n, top_k, Fe):
     check(drawn(g, d, n, Fe), torch.randn(M, d, generator=g).to(BF), top_k)
 
 
+@pytest.mark.parametrize("M,d,n,top_k,Fe", [(32, 256, 256, 16, 128), (32, 128, 2, 2, 128), (25, 256, 3, 2, 1024), (32, 2816, 128, 8, 768)])
+def test_experts_with_many_tokens_and_many_experts(M, d, n, top_k, Fe):
+    """More than eight tokens to an expert, and as many parts as there can be."""
+    g = torch.Generator().manual_seed(M + d + n)
+    check(drawn(g, d, n, Fe), torch.randn(M, d, generator=g).to(BF), top_k)
+
+
 def test_all_tokens_on_one_expert_and_ties():
     """A router of zeros but one row: that expert, then the lowest of the equal ones, for every token."""
     g = torch.Generator().manual_seed(3)
