@@ -1067,7 +1067,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     if isinstance(top_k, torch.Tensor):
         how.top_k = _setting(top_k, _I32, R, "top_k", i)
     else:
-        how.top_k_all = top_k
+        how.top_k_all = max(-1, min(top_k, V))  # (V and more keep all; 32 bits go to the library)
     st = _raw_stream(i, stream)
     if out is None:
         dev, shape = logits.device, (R,)

@@ -534,7 +534,7 @@ DG_API dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int64_t 
 
 /* A layer's whole mixture-of-experts block ([SURV] §11, §13; the block that a step takes
  * with n_exp > 0, dg_dims) for 1 to 32 tokens, in one launch: at these sizes the chosen
- * experts' weights bound it, and each is read once.
+ * experts' weights bound it, and each is read once for each eight of its tokens.
  *   model   of which dims.d, n_exp, top_k, Fe, rms_eps and L and the weights Wr, We1,
  *           We2 are read (limits as dg_dims, d and Fe up to 16384; weights finite and
  *           16-byte aligned); layer in [0, L)
@@ -548,10 +548,10 @@ DG_API dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int64_t 
  *           token's output is not to be used), DG_ERR_TIMEOUT.  Calls (and graphs) that
  *           may overlap on the GPU need one each.
  * x, the router's logits and the hidden values are not rounded to bf16 as a step rounds
- * them: fp32 sums of exact products, hidden values good to 2^-17.  A token's sums run
- * over the experts that any token of the call chose (zeros where it did not), so their
- * last bits go with the other tokens.  The launch is cooperative: it begins when all SMs
- * have room for it.                                                                */
+ * them: fp32 sums of exact products, hidden values good to 2^-17.  How a token's sums
+ * are cut into parts goes with the number of experts that the call's tokens chose, so
+ * their last bits go with the other tokens.  The launch is cooperative: it begins when
+ * all SMs have room for it.                                                        */
 DG_API dg_status dg_moe_tokens_workspace(const dg_model* model, int32_t M, size_t* bytes);
 DG_API dg_status dg_moe_tokens(const dg_model* model, int32_t layer, const void* h, void* out, int32_t M, int32_t* idx,
                                float* gate, void* ws, size_t ws_bytes, void* stream);

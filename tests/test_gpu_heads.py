@@ -66,6 +66,23 @@ def test_strides_zero_heads_and_neighbours():
     assert torch.equal(q2, q) and torch.equal(k2, k) and torch.equal(v2, v)
 
 
+@pytest.mark.parametrize("B,C,Hq,Hkv,hd", [(3, 1701, 26, 3, 128), (1, 9733, 20, 2, 64), (5, 4001, 14, 1, 32)])
+def test_several_tokens_to_a_block(B, C, Hq, Hkv, hd):
+    g = torch.Generator().manual_seed(B + C)
+    pos = torch.randint(0, 100000, (B,), generator=g, dtype=torch.int32)
+    gains = [(1 + 0.3 * torch.randn(hd, generator=g)).to(BF) for _ in range(2)]
+    check(packed(g, B, C, Hq, Hkv, hd), pos, Hq, Hkv, gains)
+
+
+def test_sequences_past_32_bits_apart():
+    g = torch.Generator().manual_seed(9)
+    B, C, Hq, Hkv, hd = 2, 3, 2, 1, 64
+    x, W, sb = packed(g, B, C, Hq, Hkv, hd), (Hq + 2 * Hkv) * hd, 2 ** 31 + 8
+    wide = torch.empty(sb + C * W, dtype=BF, device="cuda").as_strided((B, C, W), (sb, W, 1))
+    wide.copy_(x)
+    check(x, torch.tensor([7, 4000], dtype=torch.int32), Hq, Hkv, cuda=wide)
+
+
 def test_out_stream_and_graph_follow_the_positions():
     g = torch.Generator().manual_seed(3)
     x = packed(g, 2, 3, 4, 2, 128)

@@ -186,6 +186,29 @@ def test_longest_vocabulary():
     check(x, u, k=100000, mp=1e-3)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_past_32_bits_apart(dtype):
+    g = torch.Generator().manual_seed(12)
+    R, V, ld = 3, 9001, 2 ** 31 + 8
+    x = (torch.randn(R, V, generator=g) * 2).to(dtype)
+    u = torch.rand(R, generator=g)
+    wide = torch.empty((R - 1) * ld + V, dtype=dtype, device="cuda").as_strided((R, V), (ld, 1))
+    wide.copy_(x)
+    for kw in (dict(top_p=0.9), dict(top_k=30), dict(min_p=0.01)):
+        got, want = dg.sample(wide, u.cuda(), **kw), dg.sample(x.cuda(), u.cuda(), **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_top_k_of_any_size_as_a_number():
+    g = torch.Generator().manual_seed(13)
+    x, u = torch.randn(4, 300, generator=g).cuda(), torch.rand(4, generator=g).cuda()
+    want = dg.sample(x, u)
+    for k in (300, 301, 2 ** 31, 2 ** 32 + 1, 10 ** 30):
+        assert all(torch.equal(a, b) for a, b in zip(dg.sample(x, u, top_k=k), want))
+    for k in (-1, -2 ** 32 + 1):
+        assert dg.sample(x, u, top_k=k)[0].tolist() == [-1] * 4
+
+
 def test_shares_follow_the_weights():
     """The whole range of u in equal steps draws each token as often as its weight says, to a step at either end."""
     x = torch.tensor([0.3, -1.0, 2.0, -INF, 0.9, 2.0])

@@ -206,3 +206,22 @@ def test_long_products_side_by_side(M, group):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
     assert dg.w4_status() == 0
+
+
+@pytest.mark.parametrize("M,group", [(3, 64), (20, 32), (32, 128)])
+def test_codes_past_32_bits(M, group):
+    """A matrix of more than 2^32 codes (2^31 bytes): its rows at both ends and about the border."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    N, K = 2 ** 19 + 40, 8320
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device="cuda")
+    codes = torch.stack((codes & 15, codes >> 4), dim=2).view(N, K)
+    scales = (torch.randn(N, K // group, generator=g, device="cuda") * 0.05).to(BF)
+    w = dg.W4Matrix.from_codes(codes, scales)
+    assert w.codes.numel() > 2 ** 31
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF)
+    y = dg.w4_matvec(w, x, dtype=torch.float32)
+    border = 2 ** 32 // K
+    rows = torch.cat([torch.arange(a, a + 40) for a in (0, border - 20, N - 40)])
+    want, tol = w4_ref.product(codes[rows.cuda()].cpu(), scales[rows.cuda()].cpu(), x.cpu(), None, 1.0, None, torch.float32)
+    err = (y[:, rows.cuda()].double().cpu() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
