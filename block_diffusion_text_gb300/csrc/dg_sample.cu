@@ -50,6 +50,7 @@ constexpr int kSpTries = 3;
 constexpr int kSpMaxCluster = 16;
 constexpr int kSpRuns = kSpMaxCluster * kSpWarps;
 constexpr int kSpCap = 640;                   // listed values of a run, over the CTAs of a row
+constexpr int kSpSampled = 4;                 // sampled blocks of 128 values of a run, at most
 constexpr int kSpTable = 128;                 // 2^(j / 128)
 constexpr int kSpTop = 43;                    // a weight of the row's scale is 2^43: 2^20 of them stay below 2^63
 constexpr float kSpFar = 64.0f;               // factors of two below the largest weight at which nothing weighs
@@ -62,7 +63,7 @@ struct SpArgs {
   int32_t *token, *kept;
   float* logprob;
   int64_t ld;
-  int R, V, slice, run4, step, bf16;
+  int R, V, slice, run4, step, bf16;  // step: a power of two
   float temperature_all, top_p_all, min_p_all;
   int top_k_all;
 };
@@ -115,6 +116,7 @@ struct alignas(16) SpShared {
 };
 
 static_assert(sizeof(SpShared) % 16 == 0, "the lists lie behind it");
+static_assert(kSpSampled * 128 <= kSpCap, "the samples lie where the lists will");
 constexpr int kSpSmem = (int)sizeof(SpShared) + kSpWarps * kSpCap * 4;
 
 DG_DEV unsigned ld_cluster_u32(uint32_t a) {
@@ -269,7 +271,13 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   float top = kNone, low = INFINITY;
   bool fine = true;
   unsigned fin = 0;
+  // every a.step-th 128 values are a run's sample, kept where its list will lie
+  const bool sampled = a.V > kSpSample;
+  const int step_log = 31 - __clz(a.step);
+  float4* sample = reinterpret_cast<float4*>(list_v) + warp * kSpSampled * 32 + lane;
   each4(Ahead4{}, first, last, [&](const float4& v, int i) {
+    const int block = (i - 4 * lane - first) >> 7;
+    if (sampled && (block & (a.step - 1)) == 0) sample[(block >> step_log) * 32] = v;
     const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -580,7 +588,6 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     // of the sample: the running sum (low word) and count (high word) at a thread's bins
     unsigned long long run[4];
     const int bits = 28 - (32 - __clz(a.slice / a.step));  // a weight's, so that the whole sample's sum fits 32
-    const bool sampled = a.V > kSpSample;
     const float floor_v = key_float(max(floor_key, 0x00800000u));
     // What min_p leaves out needs no list: a bracket that ends below its floor begins
     // there, and one that lies below it is empty, with all from the floor on above it.
@@ -630,9 +637,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     };
     if (sampled) {
       clear(true);
-      // every a.step-th 128 values of a run
-      for (int i = first + 4 * lane; i < last; i += 128 * a.step) {
-        const float4 v4 = load4(i, last);
+      for (int i = first + 4 * lane, b = 0; i < last; i += 128 * a.step, ++b) {
+        const float4 v4 = sample[b * 32];
         const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
