@@ -6,7 +6,7 @@
 //
 // with a the first and b the second half of the head and the angle pos base^(-2 j / hd)
 // for pair j; v heads are moved.  Bound by memory: every value is read once and
-// written once.
+// written once (16384 tokens of 32 heads of 128: 48.8 us, 5.5 TB/s; one token 2 us).
 #include <climits>
 #include <cmath>
 
@@ -179,9 +179,11 @@ extern "C" dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int6
              static_cast<__nv_bfloat16*>(v), batch_stride, token_stride, B * C, C, Hq, Hkv, rms_eps};
   const int items = (Hq + 2 * Hkv) * (hd / 16);
   int per = items >= kHeadThreads ? 1 : kHeadThreads / items;
-  // with many tokens, a sine and cosine for every thread
+  // with many tokens, a sine and cosine for every thread (16 / 8 heads of 128: 608 tokens
+  // 3.9 us against 3.2 without, 1216 5.0 against 5.2, 4096 12.4 against 16.7, 16384 48.8
+  // against 65.1)
   const int fill = kHeadThreads / (hd / 2);
-  if (per < fill && a.tokens >= 8 * kTargetCtas * fill) per = fill;
+  if (per < fill && a.tokens >= 2 * kTargetCtas * fill) per = fill;
   const dim3 grid(cdiv(a.tokens, per)), block(kHeadThreads);
   const size_t smem = sizeof(float2) * per * (hd / 2);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -13,16 +13,19 @@
 // In each phase the rows of the weights that it needs are cut into equal ranges,
 // one for each CTA, row by row, so that all SMs read the same number of bytes.
 //
+// Measured, 128 experts of 768 x 2816, top 8: one token 34 us (79 MB: 12 us at the copy
+// rate; the router takes 4, routing 3, each barrier 2), 16 tokens 165 (723 MB, 108), 32
+// tokens 223 (146).
+//
 // Warp MMAs, the weights as the 16-row operand, up to eight of the expert's own tokens as
 // the columns: an expert with more of them comes several times.  (With a column for
 // every token of the call, tiles of eight of them where one had chosen the expert,
 // 32 tokens took 355 us at 128 experts of 768 x 2816.)
 // x W^T is taken as (h W^T) / rms, so the tokens enter as the bf16 they are; the hidden
 // values, which carry their gate (the second product is linear), as pairs of bf16 (16
-// bits or more).  A warp's share of the products' inner dimension
-// is a block of 64 columns in turn; its own weights come through a ring of cp.async
-// copies that only the lane that issued them reads, so nothing has to be waited for
-// but the lane's own copies.
+// bits or more).  A warp's share of the products' inner dimension is a block of 64
+// columns in turn; its own weights come through a ring of cp.async copies that only the
+// lane that issued them reads, so nothing has to be waited for but the lane's own copies.
 #include <cfloat>
 #include <climits>
 #include <type_traits>

@@ -190,7 +190,9 @@ DG_DEV void cp_async4_s(uint32_t dst, const void* src) {
 }
 
 // Warps that share a unit: as few as leave the waves of sets on an SM's `ctas`
-// CTAs within 5 % of full (fewer barriers), all eight otherwise.
+// CTAs within 5 % of full (fewer barriers), all eight otherwise (one row, K = 2816:
+// 2816 rows with 8, 4, 2, 1 warps 3.9, 5.1, 8.4, 14.3 us; 9728 rows 6.3, 5.8, 8.7,
+// 14.5; 262144 rows 79.7, 76.0, 74.6, 79.8).
 int w4_split(int units, int KB, int ctas) {
   for (int wk = 1; wk < kW4Warps && wk < KB; wk *= 2) {
     const int sets = cdiv(units, kW4Warps / wk), slots = ctas * kTargetCtas;
@@ -234,7 +236,9 @@ DG_DEV void mma_bf16_more(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, ui
 // tile of 64 columns each); a CTA works on kW4Warps / wk units at a time, a set.  A
 // warp's codes and scales come through a ring of cp.async copies that runs on over
 // the borders of its units; a lane reads only what it copied itself, so it waits for
-// nothing but its own copies.
+// nothing but its own copies.  Bound by latency for short matrices (4096 x 2816, one
+// row: 3.9 us), by its instructions beside HBM for long ones (262144 x 2816: 76 us, 5.2
+// TB/s, 160 instructions of a warp for 2048 codes).
 template <int NT, int R, int SG>
 __global__ void __launch_bounds__(kW4Warps * 32, 2) w4_matvec_kernel(W4Args a) {
   constexpr int S = kW4Stages, kStage = R * kW4Bytes + SG * 32 * 4 * R;  // a lane's scales: 4 bytes to a tile
@@ -385,7 +389,8 @@ cudaError_t launch_w4(const W4Args& args, cudaStream_t st) {
 // (it would come from L2 twice as often as the codes from HBM), so all warps of a CTA
 // work on the same columns at the same time, on row tiles of their own, and x lies in
 // shared memory for kW4Chunk tiles of columns at a time, in the order of the products'
-// operands.  A warp has a pair of neighbouring row tiles, whose codes of a tile of
+// operands (32 rows over 262144 x 2816: 166 us, 203 MB of codes and scales in 89 us at
+// 131072; the MMAs alone are 8 cycles each of a quarter SM, 79 us of it).  A warp has a pair of neighbouring row tiles, whose codes of a tile of
 // columns are one piece of memory: one lane copies a chunk's (cp.async.bulk, two chunks
 // to a warp), so that little but the codes' own work is left to the others.  A CTA has
 // an equal share of all pairs, 16 at a time; a rest of eight or fewer goes tile by tile.
@@ -584,8 +589,15 @@ cudaError_t launch_w4_wide(const W4Args& a, cudaStream_t st) {
   return launch_pdl(w4_wide_kernel<NT, SG>, dim3(kTargetCtas), dim3(kW4WideWarps * 32), (size_t)L::kSmem, st, a);
 }
 
+// Four row tiles to a unit (x is read once for them, and their scales in one piece) where
+// there are units enough for all SMs (K = 2816, one row: 9728 rows 5.7 us both ways,
+// 19456 rows 7.9 against 10.9, 38912 rows 15.0 against 22.5; 4864 rows 5.5 against
+// 4.1).  Above eight rows the kernel that keeps x in shared memory, from six pairs of
+// row tiles to an SM on (32 rows of x: 29184 rows 27.3 us against 32.0, 19456 rows
+// 22.5 against 19.9; 16 rows: 19.4 against 21.9, 16.3 against 13.3).
 template <int SG>
-cudaError_t launch_w4_rows(const W4Args& a, bool wide, cudaStream_t st) {
+cudaError_t launch_w4_rows(const W4Args& a, cudaStream_t st) {
+  const bool wide = cdiv(a.N, kW4Rows) >= (a.M <= 8 ? 4 : 12) * kTargetCtas;
   if (a.M <= 8) return wide ? launch_w4<1, kW4Tiles, SG>(a, st) : launch_w4<1, 1, SG>(a, st);
   if (a.M <= 16) return wide ? launch_w4_wide<2, SG>(a, st) : launch_w4<2, 1, SG>(a, st);
   return wide ? launch_w4_wide<4, SG>(a, st) : launch_w4<4, 1, SG>(a, st);
@@ -672,8 +684,7 @@ extern "C" dg_status dg_w4_matvec(const dg_w4* w, const void* x, int32_t ldx, in
            static_cast<const __nv_bfloat16*>(x), alpha, static_cast<const __nv_bfloat16*>(resid), y, coef, w->N, w->K,
            w->group, M, ldx, ldr, ldy, y_f32 != 0, 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool wide = cdiv(w->N, kW4Rows) >= 16 * kTargetCtas;
-  return from_cuda(w->group == 32 ? launch_w4_rows<2>(a, wide, st) : launch_w4_rows<1>(a, wide, st));
+  return from_cuda(w->group == 32 ? launch_w4_rows<2>(a, st) : launch_w4_rows<1>(a, st));
 }
 
 extern "C" dg_status dg_w4_status(int32_t* status, void* stream) {

@@ -183,6 +183,16 @@ def test_products_of_many_rows(M, N, K, group):
     check(w, c, s, x, resid=torch.randn(M, N, generator=g).to(BF))
 
 
+@pytest.mark.parametrize("M", [1, 5, 8, 9, 32])
+@pytest.mark.parametrize("N,K,group", [(9712, 320, 64), (9713, 128, 128), (9729, 192, 32), (14600, 64, 64), (29168, 128, 64), (29169, 192, 32),
+                                       (29200, 384, 128)])
+def test_products_where_the_kernels_change(M, N, K, group):
+    g = torch.Generator().manual_seed(M + N)
+    c, s = drawn(g, N, K, group)
+    w = dg.W4Matrix.from_codes(c.cuda(), s.cuda())
+    check(w, c, s, torch.randn(M, K, generator=g).to(BF), dtype=torch.float32)
+
+
 @pytest.mark.parametrize("M,group", [(8, 64), (12, 64), (32, 128), (32, 32)])
 def test_long_products_side_by_side(M, group):
     """Two streams and a captured product at once over the same long matrix: the same bits as alone."""
