@@ -114,6 +114,7 @@ struct alignas(16) SpShared {
   SpCut cut;
   float bracket_hi, bracket_lo;
   SpScale scale;
+  double ln_min_p;                        // T ln(min_p), worked out while the logits are on their way
   unsigned floor_key;
 };
 
@@ -162,6 +163,17 @@ DG_DEV SpWeight weight_parts(float v, const SpScale& s, const uint2* pow2) {
 DG_DEV unsigned long long weight_of(float v, const SpScale& s, const uint2* pow2) {
   const SpWeight w = weight_parts(v, s, pow2);
   return (unsigned long long)w.m * w.p;
+}
+
+// log2 of a sum of weights, to 2^-28: the table entry below its leading bits, and three
+// terms of the series for the rest.  (A 64-bit log takes a microsecond here.)
+DG_DEV double log2_of(unsigned long long sum, const uint2* pow2) {
+  const int lead = __clzll(sum);
+  const unsigned top = (unsigned)((sum << lead) >> 32);  // 2^31 times the mantissa
+  const int j = min(kSpTable - 1, max(0, (int)(kSpTable * __log2f((float)top * 4.656612873077393e-10f))));
+  const unsigned t = pow2[j].x << 2;
+  const float r = (float)(int)(top - t) / (float)t;
+  return (63 - lead) + j * (1.0 / kSpTable) + (double)(1.442695041f * (r * fmaf(r, fmaf(r, 0.333333333f, -0.5f), 1.0f)));
 }
 
 DG_DEV unsigned long long warp_sum(unsigned long long v) {
@@ -224,6 +236,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   const float u = a.u[row];
   bool bad = !(T >= 0.f && T <= FLT_MAX) || !(top_p >= 0.f) || !(min_p >= 0.f && min_p <= 1.f) || top_k < 0 || !(u >= 0.f && u < 1.f);
 
+  if (tid == kSpThreads - 1 && min_p > 0.f) s.ln_min_p = (double)T * log((double)min_p);
   // four values from i on (a multiple of 4), -inf from `end` on
   const bool vec = reinterpret_cast<uintptr_t>(src) % (a.bf16 ? 8 : 16) == 0;
   auto load4 = [&](int i, int end) {
@@ -342,7 +355,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       s.scale = SpScale{c, clo, base_v, base_v != 0.f ? 1 : (int)ceilf(m * c) + 1};
       if (min_p > 0.f) {
         // w >= min_p where l >= max + T ln(min_p): the first float at or above that border, worked out in 64 bits
-        const double border = (double)m + (double)T * log((double)min_p);
+        const double border = (double)m + s.ln_min_p;
         if (border >= -(double)FLT_MAX) {
           const float f = (float)border;
           fk = min(key_of(f) + ((double)f < border ? 1u : 0u), mkey);
@@ -1037,8 +1050,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           // a likely token's is taken from what the others weigh, so that it is exact near 0 too
           const unsigned long long rest = total - ws[e];
           a.logprob[row] = rest < ws[e] ? (float)(log1p(-(double)rest / (double)total) + 0.0)
-                                        : (float)(((double)vs[e] - (double)sc.base) / (double)T - log((double)total) +
-                                                  0.69314718055994530942 * (kSpTop - sc.nref));
+                                        : (float)((((double)vs[e] - (double)sc.base) * ((double)sc.c + (double)sc.clo) -
+                                                   log2_of(total, s.pow2) + (kSpTop - sc.nref)) * 0.69314718055994530942);
         }
       }
       at += ws[e];
