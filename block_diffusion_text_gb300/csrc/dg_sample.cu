@@ -866,14 +866,26 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           s.key_hi = 0;
         }
         __syncthreads();
-        each_listed([&](float v) {
-          const unsigned k = key_of(v);
-          if (k <= in) return;
-          const int b = bin_of(v, k);
-          if (b < 0) return;
-          if (mass) add_mass(b, weight(v));
-          else atomicAdd(&s.count[b], 1u);
-        });
+        // two at a time: their weights side by side, then the atomics
+        const int listed_n = (int)s.run_listed[my_run];
+        for (int i = mate; i < listed_n; i += 2 * team) {
+          const float* at = list_v + my_run * cap + i;
+          const float v[2] = {at[0], i + team < listed_n ? at[team] : kNone};
+          unsigned long long w[2];
+          int b[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const unsigned k = v[e] >= -FLT_MAX ? key_of(v[e]) : 0u;
+            b[e] = k > in ? bin_of(v[e], k) : -1;
+            w[e] = mass ? weight(v[e]) : 0ull;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (b[e] < 0) continue;
+            if (mass) add_mass(b[e], w[e]);
+            else atomicAdd(&s.count[b[e]], 1u);
+          }
+        }
         __syncthreads();
         const unsigned long long mine_w = mass ? s.lo[tid] + ((unsigned long long)s.hi[tid] << 32) : (unsigned long long)s.count[tid];
         const unsigned long long upto = over + scan(mine_w);
@@ -910,6 +922,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           if (tid < (int)n) {
             const unsigned k = s.keys[tid];
             unsigned long long before = over, same = 0;
+#pragma unroll 4
             for (unsigned i = 0; i < n; ++i) {
               const unsigned o = s.keys[i];
               if (o > k) before += s.sum[i];
