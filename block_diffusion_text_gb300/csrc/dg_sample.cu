@@ -827,9 +827,14 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   // ================================================================= the leader
   // a team of threads for every run's list (a warp at most: there are 16 runs at least)
   const int team = kSpThreads / runs, my_run = tid / team, mate = tid % team;
+  // two values at a time, the second with key 0 where there is none
   auto each_listed = [&](auto&& f) {
     const int n = (int)s.run_listed[my_run];
-    for (int i = mate; i < n; i += team) f(list_v[my_run * cap + i]);
+    for (int i = mate; i < n; i += 2 * team) {
+      const float* at = list_v + my_run * cap + i;
+      const float v0 = at[0], v1 = i + team < n ? at[team] : kNone;
+      f(v0, v1, key_of(v0), v1 >= -FLT_MAX ? key_of(v1) : 0u);
+    }
   };
   // The inclusive running sum over the CTA's threads
   auto scan = [&](unsigned long long x) {
@@ -866,26 +871,18 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           s.key_hi = 0;
         }
         __syncthreads();
-        // two at a time: their weights side by side, then the atomics
-        const int listed_n = (int)s.run_listed[my_run];
-        for (int i = mate; i < listed_n; i += 2 * team) {
-          const float* at = list_v + my_run * cap + i;
-          const float v[2] = {at[0], i + team < listed_n ? at[team] : kNone};
-          unsigned long long w[2];
-          int b[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const unsigned k = v[e] >= -FLT_MAX ? key_of(v[e]) : 0u;
-            b[e] = k > in ? bin_of(v[e], k) : -1;
-            w[e] = mass ? weight(v[e]) : 0ull;
+        each_listed([&](float v0, float v1, unsigned k0, unsigned k1) {
+          const int b0 = k0 > in ? bin_of(v0, k0) : -1, b1 = k1 > in ? bin_of(v1, k1) : -1;
+          const unsigned long long w0 = mass ? weight(v0) : 0ull, w1 = mass ? weight(v1) : 0ull;
+          if (b0 >= 0) {
+            if (mass) add_mass(b0, w0);
+            else atomicAdd(&s.count[b0], 1u);
           }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (b[e] < 0) continue;
-            if (mass) add_mass(b[e], w[e]);
-            else atomicAdd(&s.count[b[e]], 1u);
+          if (b1 >= 0) {
+            if (mass) add_mass(b1, w1);
+            else atomicAdd(&s.count[b1], 1u);
           }
-        }
+        });
         __syncthreads();
         const unsigned long long mine_w = mass ? s.lo[tid] + ((unsigned long long)s.hi[tid] << 32) : (unsigned long long)s.count[tid];
         const unsigned long long upto = over + scan(mine_w);
@@ -897,13 +894,16 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         const int bin = s.found_bin;
         if (bin < 0) return;
         over = s.found_above;
-        each_listed([&](float v) {
-          const unsigned k = key_of(v);
+        auto take = [&](float v, unsigned k) {
           if (k <= in || bin_of(v, k) != bin) return;
           const unsigned at = atomicAdd(&s.nkeys, 1u);
           atomicMin(&s.key_lo, k);
           atomicMax(&s.key_hi, k);
           if (at < kSpKeys) s.keys[at] = k;
+        };
+        each_listed([&](float v0, float v1, unsigned k0, unsigned k1) {
+          take(v0, k0);
+          take(v1, k1);
         });
         __syncthreads();
         klo = s.key_lo;
@@ -943,8 +943,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       find_listed(false, (unsigned long long)top_k, 0, 0u, cut);
       if (by_p) {
         unsigned long long w = 0, none = 0;
-        each_listed([&](float v) {
-          if (key_of(v) > cut.key) w += weight(v);
+        each_listed([&](float v0, float v1, unsigned k0, unsigned k1) {
+          const unsigned long long w0 = weight(v0), w1 = weight(v1);
+          w += (k0 > cut.key ? w0 : 0ull) + (k1 > cut.key ? w1 : 0ull);
         });
         cta_sum(s, w, none);
         const unsigned long long w_tie = weight(key_float(cut.key)), goal = share(w + cut.ties * w_tie);
@@ -962,13 +963,12 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   const unsigned long long w_tie = tied ? weight(key_float(cut.key)) : 0ull;
   unsigned long long run_w = 0, run_c = 0, run_eq = 0;
   if (listed) {
-    each_listed([&](float v) {
-      const unsigned k = key_of(v);
-      if (k > least || (!tied && k == least)) {
-        run_w += weight(v);
-        ++run_c;
-      }
-      run_eq += tied && k == least;
+    const unsigned above_it = tied ? least : least - 1u;
+    each_listed([&](float v0, float v1, unsigned k0, unsigned k1) {
+      const unsigned long long w0 = weight(v0), w1 = weight(v1);
+      run_w += (k0 > above_it ? w0 : 0ull) + (k1 > above_it ? w1 : 0ull);
+      run_c += (k0 > above_it) + (k1 > above_it);
+      run_eq += (tied && k0 == least) + (tied && k1 == least);
     });
     for (int o = 1; o < team; o <<= 1) {
       run_w += __shfl_xor_sync(0xffffffffu, run_w, o);
