@@ -14,9 +14,9 @@
 // the weights' own 2^-28.
 //
 // A cluster of CTAs takes a row, a slice each; a warp a run of its CTA's slice.  What
-// bounds few rows is the chain of dependent steps (one row of 262144: 32 us, five
+// bounds few rows is the chain of dependent steps (one row of 262144: 31 us, five
 // exchanges of the cluster among them), many rows the instructions of an exact weight
-// (some 50 a value; 256 rows of 262144: 282 us, 268 MB read once from HBM; for the rows
+// (some 50 a value; 256 rows of 262144: 278 us, 268 MB read once from HBM; for the rows
 // under way they are read again from L2).  The passes:
 //   the largest value
 //   where a cut is asked for, a sample: its histogram, linear in the value below the
@@ -174,6 +174,18 @@ DG_DEV double log2_of(unsigned long long sum, const uint2* pow2) {
   const unsigned t = pow2[j].x << 2;
   const float r = (float)(int)(top - t) / (float)t;
   return (63 - lead) + j * (1.0 / kSpTable) + (double)(1.442695041f * (r * fmaf(r, fmaf(r, 0.333333333f, -0.5f), 1.0f)));
+}
+
+// ln(w / (w + rest)) for rest < w, to 2^-27 of itself: -2 atanh(z) with z = rest / (2 w +
+// rest), which is 1/3 at most, in two floats, and nine terms of the series.
+DG_DEV float ln_share(unsigned long long rest, unsigned long long w) {
+  const double den = (double)(rest + 2 * w);
+  const float z0 = (float)rest / (float)den, q = z0 * z0;
+  const double z = (double)z0 + (double)((float)fma(-(double)z0, den, (double)rest) / (float)den);
+  float t = 1.0f / 17;
+#pragma unroll
+  for (int n = 15; n >= 3; n -= 2) t = fmaf(t, q, 1.0f / n);
+  return (float)(-2.0 * z * (1.0 + (double)(t * q)) + 0.0);
 }
 
 DG_DEV unsigned long long warp_sum(unsigned long long v) {
@@ -1062,7 +1074,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         if (a.logprob) {
           // a likely token's is taken from what the others weigh, so that it is exact near 0 too
           const unsigned long long rest = total - ws[e];
-          a.logprob[row] = rest < ws[e] ? (float)(log1p(-(double)rest / (double)total) + 0.0)
+          a.logprob[row] = rest < ws[e] ? ln_share(rest, ws[e])
                                         : (float)((((double)vs[e] - (double)sc.base) * ((double)sc.c + (double)sc.clo) -
                                                    log2_of(total, s.pow2) + (kSpTop - sc.nref)) * 0.69314718055994530942);
         }
