@@ -832,8 +832,11 @@ def w4_matvec(w: W4Matrix, x: torch.Tensor, alpha: torch.Tensor | None = None, c
             raise ValueError(f"alpha: contiguous float32 [{M}] on cuda:{i}")
         ap = alpha.data_ptr()
     if resid is not None:
-        rr, ldr = _rows_of(resid, _BF16, N, "resid", i)
-        _need(rr == M, f"resid: [{M}, {N}]")
+        if resid.dtype is _BF16 and resid.get_device() == i and resid.shape == (M, N) and resid.is_contiguous():
+            ldr = N
+        else:
+            rr, ldr = _rows_of(resid, _BF16, N, "resid", i)
+            _need(rr == M, f"resid: [{M}, {N}]")
         rp = resid.data_ptr()
     st = _raw_stream(i, stream)
     if out is None:
