@@ -14,8 +14,8 @@
 // one for each CTA, row by row, so that all SMs read the same number of bytes.
 //
 // Measured, 128 experts of 768 x 2816, top 8: one token 34 us (79 MB: 12 us at the copy
-// rate; the router takes 4, routing 3, each barrier 2), 16 tokens 165 (723 MB, 108), 32
-// tokens 223 (146).
+// rate; the router takes 4, routing 3, each barrier 2), 16 tokens 152 (723 MB, 108), 32
+// tokens 211 (146).
 //
 // Warp MMAs, the weights as the 16-row operand, up to eight of the expert's own tokens as
 // the columns: an expert with more of them comes several times.  (With a column for
@@ -118,8 +118,11 @@ DG_DEV bool grid_barrier(unsigned* arrivals, unsigned* rounds, int* status, int*
   return *stop == 0;
 }
 
+// L2 takes 256 bytes about them: a row's next block is there when its turn comes, and a
+// page of the memory is opened half as often (16 tokens of 128 experts of 768 x 2816: 152
+// us, 166 without; blocks of 128 columns 159, prefetches of whole pieces of a row 174).
 DG_DEV void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 DG_DEV float gelu(float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f)); }

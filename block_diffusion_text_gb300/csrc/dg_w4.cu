@@ -182,13 +182,6 @@ DG_DEV void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-DG_DEV void cp_async16_s(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-DG_DEV void cp_async4_s(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // Warps that share a unit: as few as leave the waves of sets on an SM's `ctas`
 // CTAs within 5 % of full (fewer barriers), all eight otherwise (one row, K = 2816:
 // 2816 rows with 8, 4, 2, 1 warps 3.9, 5.1, 8.4, 14.3 us; 9728 rows 6.3, 5.8, 8.7,
