@@ -230,11 +230,12 @@ DG_DEV void mma_bf16_more(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, ui
 // warp's codes and scales come through a ring of cp.async copies that runs on over
 // the borders of its units; a lane reads only what it copied itself, so it waits for
 // nothing but its own copies.  Bound by latency for short matrices (4096 x 2816, one
-// row: 3.9 us), by its instructions beside HBM for long ones (262144 x 2816: 76 us, 5.2
-// TB/s, 160 instructions of a warp for 2048 codes).
+// row: 3.9 us), by HBM for long ones (262144 x 2816: 76 us, 5.2 TB/s, 160
+// instructions of a warp for 2048 codes).
 template <int NT, int R, int SG>
 __global__ void __launch_bounds__(kW4Warps * 32, 2) w4_matvec_kernel(W4Args a) {
   constexpr int S = kW4Stages, kStage = R * kW4Bytes + SG * 32 * 4 * R;  // a lane's scales: 4 bytes to a tile
+  constexpr int kSteps = R == kW4Tiles ? 2 : 1;  // tiles of columns at a time: eight rows over 262144 x 2816 95 -> 88 us; short matrices lose 5 %
   extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   char* ring = smem + warp * S * kStage;
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 2) w4_matvec_kernel(W4Args a) {
   int slot_at = 0, buf = 0;
   for (int set = blockIdx.x; set < sets; set += gridDim.x) {
     float y[R][NT][4] = {};
-#pragma unroll 1
+#pragma unroll kSteps
     for (int kb = sub; kb < KB; kb += wk) {
       uint4 b[NT][2];
 #pragma unroll
