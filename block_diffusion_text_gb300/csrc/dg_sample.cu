@@ -14,9 +14,9 @@
 // the weights' own 2^-28.
 //
 // A cluster of CTAs takes a row, a slice each; a warp a run of its CTA's slice.  What
-// bounds few rows is the chain of dependent steps (one row of 262144: 31 us, five
+// bounds few rows is the chain of dependent steps (one row of 262144: 29 us, five
 // exchanges of the cluster among them), many rows the instructions of an exact weight
-// (some 50 a value; 256 rows of 262144: 278 us, 268 MB read once from HBM; for the rows
+// (some 50 a value; 256 rows of 262144: 263 us, 268 MB read once from HBM; for the rows
 // under way they are read again from L2).  The passes:
 //   the largest value
 //   where a cut is asked for, a sample: its histogram, linear in the value below the
@@ -266,26 +266,43 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
                           : __ldg(reinterpret_cast<const float*>(src) + i + e);
     return make_float4(v[0], v[1], v[2], v[3]);
   };
-  // f(four values, their place) for all of [i0, i1), 128 values of a warp at a time (-inf
-  // behind the end, where the warp's other lanes still have some); the loads are D steps
-  // ahead.
+  // f(four values, their place, the block of 128) for all of [i0, i1), a block of a warp at
+  // a time (-inf behind the end, where the warp's other lanes still have some).  The loads
+  // of whole blocks are D blocks ahead and ask nothing of their places.
   auto each4 = [&](auto depth, int i0, int i1, auto&& f) {
     constexpr int D = decltype(depth)::value;
-    auto next = [&](int i) { return i < i1 ? load4(i, i1) : make_float4(kNone, kNone, kNone, kNone); };
+    const int whole = vec ? (i1 - i0) >> 7 : 0, step = a.bf16 ? 256 : 512;
+    const char* from = src + (size_t)(i0 + 4 * lane) * (a.bf16 ? 2 : 4);
+    auto next = [&](int j) {
+      const char* at = from + j * step;
+      if (!a.bf16) return __ldg(reinterpret_cast<const float4*>(at));
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
+      return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                         __uint_as_float(w.y & 0xffff0000u));
+    };
     float4 v[D];
-    int i = i0 + 4 * lane;
 #pragma unroll
-    for (int j = 0; j < D; ++j) v[j] = next(i + 128 * j);
+    for (int j = 0; j < D; ++j)
+      if (j < whole) v[j] = next(j);
+    int i = i0 + 4 * lane, block = 0;
 #pragma unroll 1
-    while (i - 4 * lane < i1) {
+    while (block < whole) {
 #pragma unroll
       for (int j = 0; j < D; ++j) {
+        if (block >= whole) break;
         const float4 now = v[j];
-        v[j] = next(i + 128 * D);
-        if (i - 4 * lane < i1) f(now, i);
+        if (block + D < whole) v[j] = next(D);
+        f(now, i, block);
+        from += step;
         i += 128;
+        ++block;
       }
     }
+    // the last block's part, or all of a row that does not lie on 16 (8) bytes (loads ahead
+    // of these gain nothing)
+#pragma unroll 1
+    for (; i - 4 * lane < i1; i += 128, ++block)
+      f(i < i1 ? load4(i, i1) : make_float4(kNone, kNone, kNone, kNone), i, block);
   };
   using Ahead2 = std::integral_constant<int, 2>;
   using Ahead4 = std::integral_constant<int, 4>;
@@ -296,26 +313,33 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
 
   // ---- the largest value, the lowest, the number of finite ones
   float top = kNone, low = INFINITY;
-  bool fine = true;
   unsigned fin = 0;
   // every a.step-th 128 values are a run's sample, kept where its list will lie
   const bool sampled = a.V > kSpSample;
   const int step_log = 31 - __clz(a.step);
   float4* sample = reinterpret_cast<float4*>(list_v) + warp * kSpSampled * 32 + lane;
-  each4(Ahead4{}, first, last, [&](const float4& v, int i) {
-    const int block = (i - 4 * lane - first) >> 7;
+  each4(Ahead4{}, first, last, [&](const float4& v, int, int block) {
     if (sampled && (block & (a.step - 1)) == 0) sample[(block >> step_log) * 32] = v;
-    const float w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      top = fmaxf(top, w[e]);
-      fine = fine && w[e] <= FLT_MAX;
-      if (w[e] >= -FLT_MAX) {
-        low = fminf(low, w[e]);
-        ++fin;
+    // NaN goes through to the largest
+    asm("max.NaN.f32 %0, %0, %1;\n max.NaN.f32 %0, %0, %2;\n max.NaN.f32 %0, %0, %3;\n max.NaN.f32 %0, %0, %4;"
+        : "+f"(top)
+        : "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w));
+    const float least = fminf(fminf(v.x, v.y), fminf(v.z, v.w));
+    if (least >= -FLT_MAX) {
+      low = fminf(low, least);
+      fin += 4;
+    } else {
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        const float x = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+        if (x >= -FLT_MAX) {
+          low = fminf(low, x);
+          ++fin;
+        }
       }
     }
   });
+  const bool fine = top <= FLT_MAX;
   unsigned mkey = __reduce_max_sync(0xffffffffu, top >= -FLT_MAX ? key_of(top) : 0u);
   unsigned lowest = __reduce_min_sync(0xffffffffu, low <= FLT_MAX ? key_of(low) : 0xffffffffu);
   const unsigned wrong = __any_sync(0xffffffffu, !fine) ? 1u : 0u;
@@ -569,7 +593,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     const float least_v = key_float(max(least, 0x00800000u));  // no finite value is below
     w = 0;
     c = eq = 0;
-    each4(Ahead2{}, i0, i1, [&](const float4& v4, int) {
+    each4(Ahead2{}, i0, i1, [&](const float4& v4, int, int) {
       if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= least_v)) return;
       const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
@@ -702,7 +726,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         n_list += __popc(b);
       };
       if (by_k) {
-        each4(Ahead4{}, first, last, [&](const float4& v4, int) {
+        each4(Ahead4{}, first, last, [&](const float4& v4, int, int) {
           if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)) >= lo)) return;
           list(v4.x);
           list(v4.y);
@@ -710,7 +734,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
           list(v4.w);
         });
       } else {
-        each4(Ahead2{}, first, last, [&](const float4& v4, int) {
+        each4(Ahead2{}, first, last, [&](const float4& v4, int, int) {
           const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
