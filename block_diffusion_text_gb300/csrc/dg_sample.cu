@@ -393,8 +393,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
         // w >= min_p where l >= max + T ln(min_p): the first float at or above that border, worked out in 64 bits
         const double border = (double)m + s.ln_min_p;
         if (border >= -(double)FLT_MAX) {
+          // (a key of a value: behind the negative value nearest to zero comes 0, not -0)
           const float f = (float)border;
-          fk = min(key_of(f) + ((double)f < border ? 1u : 0u), mkey);
+          fk = min((double)f < border ? key_of(key_float(key_of(f) + 1u)) : key_of(f), mkey);
         }
       }
     } else {
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
       if (!to_floor) return;
       lo = floor_v;
       if (hi < floor_v) {
-        hi = key_float(floor_key - 1u);
+        hi = key_float(floor_key - (floor_v == 0.f ? 2u : 1u));  // the first value below (0 is not above -0)
         lo = INFINITY;
       }
     };
@@ -1021,6 +1022,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     const unsigned long long ties = tied ? cut.ties : 0, upto = scan(run_eq), had = min(ties, upto - run_eq);
     run_eq = min(ties, upto) - had;  // from here on: how many of them are kept
     run_w += run_eq * w_tie;
+    if (tid == 0) s.found_bin = -1;
     const unsigned long long w_upto = scan(run_w);
     const unsigned c = __reduce_add_sync(0xffffffffu, (unsigned)(run_c + run_eq));
     if (lane == 0) s.part[0][warp] = c;
@@ -1038,7 +1040,16 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
     }
   }
   __syncthreads();
-  const int r = s.found_bin, f = run_first(r), l = run_last(r);
+  const int r = s.found_bin;
+  if (r < 0) {  // no run is indexed that the sums do not name: the row is told as one that cannot be drawn from
+    if (tid == 0) {
+      a.token[row] = -1;
+      if (a.logprob) a.logprob[row] = __uint_as_float(0x7fc00000u);
+      if (a.kept) a.kept[row] = 0;
+    }
+    return;
+  }
+  const int f = run_first(r), l = run_last(r);
   const unsigned long long total = s.found_total, goal = __umul64hi(total, fraction(u));
   unsigned long long now = s.found_above, left = s.run_equal[r];
   // ---- a piece of it for each warp, and the piece that holds the border by its warp
