@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
 
   // ---------------------------------------------------------------- histograms
   auto clear = [&](bool mass) {
+    __syncthreads();  // what the last search left has been read by all
     for (int i = tid; i < kSpBins; i += kSpThreads) {
       s.count[i] = 0u;
       if (mass) s.lo[i] = s.hi[i] = 0u;
