@@ -81,22 +81,28 @@ struct MtShared {
   int stop;
 };
 
+// One arrival at the grid's barrier; the last of a round begins the next.  The count wraps
+// to zero by itself.
+DG_DEV bool grid_arrive(unsigned* arrivals, unsigned* rounds) {
+  __threadfence();
+  if (atomicInc(arrivals, gridDim.x - 1) != gridDim.x - 1) return false;
+  __threadfence();
+  atomicAdd(rounds, 1u);
+  return true;
+}
+
 // All CTAs of the grid are here (the launch is cooperative).  Thread 0 arrives for its
-// CTA; the last one to arrive begins the next round.  Arrivals and rounds lie in
-// memory lines of their own: a line that is polled while others write to it goes back
-// and forth between the dies (flags of the CTAs side by side took 6 us).  Bounded:
-// false, with the status word set, if the others do not come.
+// CTA.  Arrivals and rounds lie in memory lines of their own: a line that is polled while
+// others write to it goes back and forth between the dies (flags of the CTAs side by side
+// took 6 us).  Bounded: false, with the status word set, if the others do not come.  A
+// CTA that gives up arrives all the same at the barriers that it will not come to: every
+// launch makes two rounds of arrivals, so the next one finds the count at zero.
 DG_DEV bool grid_barrier(unsigned* arrivals, unsigned* rounds, int* status, int* stop) {
   __syncthreads();
   if (threadIdx.x == 0) {
     unsigned round;
     asm volatile("ld.relaxed.gpu.u32 %0, [%1];" : "=r"(round) : "l"(rounds) : "memory");
-    __threadfence();
-    if (atomicAdd(arrivals, 1u) == gridDim.x - 1) {
-      *reinterpret_cast<volatile unsigned*>(arrivals) = 0u;
-      __threadfence();
-      asm volatile("st.relaxed.gpu.u32 [%0], %1;" ::"l"(rounds), "r"(round + 1) : "memory");
-    } else {
+    if (!grid_arrive(arrivals, rounds)) {
       uint64_t t0 = 0;
       for (unsigned i = 0;; ++i) {
         unsigned now;
@@ -380,7 +386,10 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
              if (row < cut.rows(u) && m < a.M) a.logits[(size_t)m * a.n_exp + r % a.n_exp] = v;
            });
   }
-  if (!grid_barrier(a.arrivals, a.rounds, a.status, &s.stop)) return;
+  if (!grid_barrier(a.arrivals, a.rounds, a.status, &s.stop)) {
+    if (tid == 0) grid_arrive(a.arrivals, a.rounds);  // for the second barrier
+    return;
+  }
 
   // ---- the routing.  Keys in the order of the logits, 0 for NaN; equal ones by index.
   auto key_of = [&](float l) { return l == l ? float_key(l == 0.f ? 0.f : l) : 0u; };
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     if (tid < pairs) {
       const int m = tid / a.n_exp;
       mine = __ldcg(a.logits + tid) * s.inv[m];
-      if (!(fabsf(mine) <= FLT_MAX) && cta == 0) atomicExch(a.status, kStatusValue);
+      if (!(fabsf(mine) <= FLT_MAX) && cta == 0) atomicCAS(a.status, 0, kStatusValue);
       keys[tid] = key_of(mine);
       red[kMtThreads + tid] = mine;
     }
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
         wrong |= there && !(fabsf(l[j]) <= FLT_MAX);
         key[j] = there ? key_of(l[j]) : 0u;
       }
-      if (__any_sync(0xffffffffu, wrong) && lane == 0 && cta == 0) atomicExch(a.status, kStatusValue);
+      if (__any_sync(0xffffffffu, wrong) && lane == 0 && cta == 0) atomicCAS(a.status, 0, kStatusValue);
       float top = 0.f, Z = 0.f, mine = 0.f;
       int mye = 0;
       unsigned taken = 0;

@@ -972,7 +972,8 @@ def moe_tokens(ffn: MoeFfn, h: torch.Tensor, out: torch.Tensor | None = None, ro
     out: optional bf16 [M, d], which may be h.  routing: optional (int32 [M, top_k], float32 [M, top_k]) to receive
     the experts and their gates.  ws: optional uint8 workspace of ffn.workspace_bytes(M) bytes, zeroed before its
     first use and not shared by calls that may overlap; by default the calls of a stream share one, which is kept
-    (moe_tokens_status, moe_release_workspaces), and a captured call takes one from the graph's pool."""
+    (moe_tokens_status, moe_release_workspaces), and a captured call takes one from the graph's pool, whose status
+    word nothing reads: a graph whose status matters is given a ws."""
     i, d = ffn._index, ffn.d
     M = h.shape[0] if h.dim() == 2 else 0
     if h.dtype is not _BF16 or h.get_device() != i or h.shape != (M, d) or not h.is_contiguous():
@@ -1013,13 +1014,19 @@ def moe_tokens(ffn: MoeFfn, h: torch.Tensor, out: torch.Tensor | None = None, ro
 
 def moe_tokens_status(device=None, stream=None) -> int:
     """The status word of the workspace that moe_tokens keeps for the stream (synchronises it): DG_OK, or what the
-    calls since it was made have met."""
+    calls since it was made have met.  After DG_ERR_TIMEOUT it is let go of, and the next call takes a new one."""
     i = torch.cuda.current_device() if device is None else torch.device(device).index
-    t = _moe_workspaces.get((i, _raw_stream(i, stream)))
+    key = (i, _raw_stream(i, stream))
+    with _moe_lock:
+        t = _moe_workspaces.get(key)
     if t is None:
         return DG_OK
     code = ct.c_int32()
-    _check(load().dg_read_status(t.data_ptr(), ct.byref(code), _raw_stream(i, stream)), "dg_read_status")
+    _check(load().dg_read_status(t.data_ptr(), ct.byref(code), key[1]), "dg_read_status")
+    if code.value == DG_ERR_TIMEOUT:
+        with _moe_lock:
+            if _moe_workspaces.get(key) is t:
+                del _moe_workspaces[key]
     return code.value
 
 

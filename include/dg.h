@@ -542,11 +542,12 @@ DG_API dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int64_t 
  *           FFN_shared(x); may be h itself; both 16-byte aligned
  *   idx     int32 [M][top_k] the experts in rank order, gate float32 [M][top_k]: written;
  *           either may be NULL
- *   ws      dg_moe_tokens_workspace bytes, 256-byte aligned, zeroed before its first use
- *           (and after DG_ERR_TIMEOUT); the first 4 bytes are the status word
- *           (dg_read_status): DG_ERR_VALUE for router logits that are not finite (the
- *           token's output is not to be used), DG_ERR_TIMEOUT.  Calls (and graphs) that
- *           may overlap on the GPU need one each.
+ *   ws      dg_moe_tokens_workspace bytes, 256-byte aligned, zeroed before its first use;
+ *           the first 4 bytes are the status word (dg_read_status): DG_ERR_VALUE for
+ *           router logits that are not finite (the token's output is not to be used),
+ *           DG_ERR_TIMEOUT if a bounded wait ran out (outputs not to be used; calls after
+ *           that one are right again, the word stays).  Calls (and graphs) that may overlap
+ *           on the GPU need one each.
  * x, the router's logits and the hidden values are not rounded to bf16 as a step rounds
  * them: fp32 sums of exact products, hidden values good to 2^-17.  How a token's sums
  * are cut into parts goes with the number of experts that the call's tokens chose, so
