@@ -47,7 +47,8 @@ struct W4StoreArgs {
   uint32_t* codes;
   uint32_t* scales;    // a pair of bf16 each
   int* status;
-  int N, K, group, ld;
+  int N, K, group;
+  int64_t ld;
 };
 
 // A warp writes the tiles of one group of columns (two tiles where the group is
@@ -614,7 +615,7 @@ dg_status check_w4(const dg_w4* w) {
 }
 
 template <bool kQuantize>
-dg_status store(const dg_w4* w, const void* W, int32_t ld, const void* s, int32_t* status, void* stream) {
+dg_status store(const dg_w4* w, const void* W, int64_t ld, const void* s, int32_t* status, void* stream) {
   W4StoreArgs a{W, static_cast<const uint16_t*>(s), static_cast<uint32_t*>(w->codes), static_cast<uint32_t*>(w->scales),
                 status, w->N, w->K, w->group, ld};
   const int64_t spans = (int64_t)cdiv(w->N, kW4Rows * kW4Tiles) * kW4Tiles * (w->K / (w->group > kW4Cols ? w->group : kW4Cols));
@@ -639,7 +640,7 @@ extern "C" dg_status dg_w4_bytes(int32_t N, int32_t K, int32_t group, size_t* co
   return DG_OK;
 }
 
-extern "C" dg_status dg_w4_quantize(const dg_w4* w, const void* W, int32_t ldw, int32_t* status, void* stream) {
+extern "C" dg_status dg_w4_quantize(const dg_w4* w, const void* W, int64_t ldw, int32_t* status, void* stream) {
   dg_status e = check_w4(w);
   if (e) return e;
   if (!W || !status || ldw < w->K || reinterpret_cast<uintptr_t>(W) % 2 || reinterpret_cast<uintptr_t>(status) % 4)
@@ -654,7 +655,7 @@ extern "C" dg_status dg_w4_pack(const dg_w4* w, const void* codes, const void* s
   return store<false>(w, codes, w->K, scales, nullptr, stream);
 }
 
-extern "C" dg_status dg_w4_read(const dg_w4* w, float* out, int32_t ldo, void* stream) {
+extern "C" dg_status dg_w4_read(const dg_w4* w, float* out, int64_t ldo, void* stream) {
   dg_status e = check_w4(w);
   if (e) return e;
   if (!out || ldo < w->K || reinterpret_cast<uintptr_t>(out) % 4) return DG_ERR_ARG;
@@ -665,8 +666,8 @@ extern "C" dg_status dg_w4_read(const dg_w4* w, float* out, int32_t ldo, void* s
                               reinterpret_cast<cudaStream_t>(stream), a));
 }
 
-extern "C" dg_status dg_w4_matvec(const dg_w4* w, const void* x, int32_t ldx, int32_t M, const float* alpha, float coef,
-                                  const void* resid, int32_t ldr, void* y, int32_t ldy, int32_t y_f32, void* stream) {
+extern "C" dg_status dg_w4_matvec(const dg_w4* w, const void* x, int64_t ldx, int32_t M, const float* alpha, float coef,
+                                  const void* resid, int64_t ldr, void* y, int64_t ldy, int32_t y_f32, void* stream) {
   dg_status e = check_w4(w);
   if (e) return e;
   if (!x || !y || M <= 0 || ldx < w->K || ldy < w->N || (resid && ldr < w->N)) return DG_ERR_ARG;

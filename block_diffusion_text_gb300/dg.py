@@ -153,17 +153,17 @@ def load():
             L.dg_kv8_attention.argtypes = [ct.c_void_p, ct.c_void_p, ct.c_void_p, ct.c_void_p, ct.c_void_p,
                                            ct.c_int32, ct.c_int32, ct.c_int32, ct.c_void_p, ct.c_size_t,
                                            ct.c_void_p]
-            i32, vp = ct.c_int32, ct.c_void_p
+            i32, i64, vp = ct.c_int32, ct.c_int64, ct.c_void_p
             L.dg_w4_bytes.argtypes = [i32, i32, i32, ct.POINTER(ct.c_size_t), ct.POINTER(ct.c_size_t)]
-            L.dg_w4_quantize.argtypes = [vp, vp, i32, vp, vp]
+            L.dg_w4_quantize.argtypes = [vp, vp, i64, vp, vp]
             L.dg_w4_pack.argtypes = [vp, vp, vp, vp]
-            L.dg_w4_read.argtypes = [vp, vp, i32, vp]
-            L.dg_w4_matvec.argtypes = [vp, vp, i32, i32, vp, ct.c_float, vp, i32, vp, i32, i32, vp]
+            L.dg_w4_read.argtypes = [vp, vp, i64, vp]
+            L.dg_w4_matvec.argtypes = [vp, vp, i64, i32, vp, ct.c_float, vp, i64, vp, i64, i32, vp]
             L.dg_w4_status.argtypes = [ct.POINTER(i32), vp]
-            L.dg_qk_norm_rope.argtypes = [vp, ct.c_int64, ct.c_int64] + [vp] * 6 + [i32] * 5 + [ct.c_float] * 2 + [vp]
+            L.dg_qk_norm_rope.argtypes = [vp, i64, i64] + [vp] * 6 + [i32] * 5 + [ct.c_float] * 2 + [vp]
             L.dg_moe_tokens_workspace.argtypes = [vp, i32, ct.POINTER(ct.c_size_t)]
             L.dg_moe_tokens.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp, ct.c_size_t, vp]
-            L.dg_sample.argtypes = [vp, i32, ct.c_int64, i32, i32, vp, vp, vp, vp, vp, vp]
+            L.dg_sample.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp]
             _lib = L
     return _lib
 

@@ -491,22 +491,22 @@ DG_API dg_status dg_w4_bytes(int32_t N, int32_t K, int32_t group, size_t* codes,
  * bf16, c = 8 + (w / s rounded to nearest even, within +-7); a group whose s is zero
  * has codes 8.  Infinities are stored as +-7 and NaN as 0 on the scale of the finite
  * values, with DG_ERR_VALUE in *status (device word, zeroed by the caller).         */
-DG_API dg_status dg_w4_quantize(const dg_w4* w, const void* W, int32_t ldw, int32_t* status, void* stream);
+DG_API dg_status dg_w4_quantize(const dg_w4* w, const void* W, int64_t ldw, int32_t* status, void* stream);
 
 /* Lays out given codes (uint8 [N][K], one to a byte, the low four bits count) and
  * scales (bf16 [N][K / group]).                                                  */
 DG_API dg_status dg_w4_pack(const dg_w4* w, const void* codes, const void* scales, void* stream);
 
 /* The weights as float32 [N][ldo], ldo >= K (exact).                              */
-DG_API dg_status dg_w4_read(const dg_w4* w, float* out, int32_t ldo, void* stream);
+DG_API dg_status dg_w4_read(const dg_w4* w, float* out, int64_t ldo, void* stream);
 
 /* y[m][n] = coef * alpha[m] * sum_k x[m][k] w[n][k] + resid[m][n] for M rows, 1 <= M
  * <= 32.  x bf16 [M][ldx], 16-byte aligned, ldx a multiple of 8; alpha float32 [M] or
  * NULL for ones; resid bf16 [M][ldr] or NULL; y [M][ldy], bf16, or float32 where
  * y_f32 is set (the LM head's logits).  y may be resid itself (same pitch); it must not
  * overlap anything else.  Products are exact, sums fp32, rounded once.             */
-DG_API dg_status dg_w4_matvec(const dg_w4* w, const void* x, int32_t ldx, int32_t M, const float* alpha, float coef,
-                              const void* resid, int32_t ldr, void* y, int32_t ldy, int32_t y_f32, void* stream);
+DG_API dg_status dg_w4_matvec(const dg_w4* w, const void* x, int64_t ldx, int32_t M, const float* alpha, float coef,
+                              const void* resid, int64_t ldr, void* y, int64_t ldy, int32_t y_f32, void* stream);
 
 /* Status word of the products on the current device (dg_read_status): DG_ERR_TIMEOUT once
  * a bounded wait of one of them ran out (its rows were not written), else DG_OK.     */
