@@ -745,6 +745,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _i32(what, *sizes):
+    """Sizes go to the library as 32 bits, and ctypes cuts larger ones: they are refused as it refuses what is too large."""
+    for v in sizes:
+        if not -1 << 31 <= v < 1 << 31:
+            raise DgError(DG_ERR_SHAPE, what)
+
+
 def _rows_of(t, dtype, width, what, index):
     """(rows, pitch) of a 2-D tensor whose rows of `width` elements are contiguous."""
     _on(t, dtype, what, index)
@@ -760,6 +767,7 @@ class W4Matrix:
 
     def __init__(self, N, K, group, device="cuda"):
         self._lib = load()
+        _i32("dg_w4_bytes", N, K, group)
         nc, ns = ct.c_size_t(), ct.c_size_t()
         _check(self._lib.dg_w4_bytes(N, K, group, ct.byref(nc), ct.byref(ns)), "dg_w4_bytes")
         self.codes = torch.empty(nc.value, dtype=torch.uint8, device=device)
@@ -939,6 +947,7 @@ class MoeFfn:
             _need(_on(t, torch.bfloat16, what, i).shape == shape and t.is_contiguous(), f"{what}: contiguous bf16 {list(shape)}")
         self.Wr, self.We1, self.We2 = Wr, We1, We2
         self.d, self.n_exp, self.top_k, self.Fe, self.rms_eps = d, n, int(top_k), Fe, float(rms_eps)
+        _i32("dg_moe_tokens", d, n, self.top_k, Fe)
         self.s = dg_model()
         self.s.dims = dg_dims(d=d, n_exp=n, top_k=self.top_k, Fe=Fe, rms_eps=self.rms_eps, L=1)
         self.s.Wr, self.s.We1, self.s.We2 = Wr.data_ptr(), We1.data_ptr(), We2.data_ptr()
@@ -959,6 +968,7 @@ class MoeFfn:
         """Bytes of workspace of moe_tokens with M tokens."""
         n = self._ws_bytes.get(M)
         if n is None:
+            _i32("dg_moe_tokens_workspace", M)
             z = ct.c_size_t()
             _check(self._lib.dg_moe_tokens_workspace(self._ref, M, ct.byref(z)), "dg_moe_tokens_workspace")
             n = self._ws_bytes[M] = z.value
@@ -1058,6 +1068,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     if i < 0 or (dt is not _F32 and dt is not _BF16) or logits.dim() != 2:
         raise ValueError(f"logits: float32 or bfloat16 [R, V] on a CUDA device, got {dt} {tuple(logits.shape)} on {logits.device}")
     R, V = logits.shape
+    if (R | V) >> 31:
+        _i32("dg_sample", R, V)
     ld = V if logits.is_contiguous() else _rows_of(logits, dt, V, "logits", i)[1]
     if u.dtype is not _F32 or u.get_device() != i or u.shape != (R,) or not u.is_contiguous():
         raise ValueError(f"u: contiguous float32 [{R}] on cuda:{i}")

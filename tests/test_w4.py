@@ -89,3 +89,10 @@ def test_quantised_weights_are_within_half_a_step(group):
 
 def test_status_refuses_null(dg):
     assert dg.load().dg_w4_status(None, None) == 1
+
+
+def test_sizes_beyond_32_bits_are_not_cut(dg):
+    for N, K, group in (((1 << 32) + 16, 64, 64), (16, (1 << 32) + 64, 64), (16, 64, (1 << 32) + 64), (-(1 << 32) + 16, 64, 64)):
+        with pytest.raises(dg.DgError) as e:
+            dg.W4Matrix(N, K, group)
+        assert e.value.code == dg.DG_ERR_SHAPE
