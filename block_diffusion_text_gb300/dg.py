@@ -1014,7 +1014,9 @@ def moe_tokens(ffn: MoeFfn, h: torch.Tensor, out: torch.Tensor | None = None, ro
             t = _moe_workspaces.get((i, st))
             if t is None or t.numel() < wn:
                 with torch.cuda.stream(stream):
-                    t = torch.zeros(wn, dtype=torch.uint8, device=i)
+                    was, t = t, torch.zeros(wn, dtype=torch.uint8, device=i)
+                    if was is not None:
+                        t[:4].copy_(was[:4])  # the status word goes along
                 _moe_workspaces[i, st] = t
             rc = call(ffn._ref, 0, hp, op, M, ip, gp, t.data_ptr(), wn, st)
     if rc:
@@ -1023,8 +1025,9 @@ def moe_tokens(ffn: MoeFfn, h: torch.Tensor, out: torch.Tensor | None = None, ro
 
 
 def moe_tokens_status(device=None, stream=None) -> int:
-    """The status word of the workspace that moe_tokens keeps for the stream (synchronises it): DG_OK, or what the
-    calls since it was made have met.  After DG_ERR_TIMEOUT it is let go of, and the next call takes a new one."""
+    """The status word of the workspace that moe_tokens keeps for the stream (synchronises it): DG_OK, or what its
+    calls have met since moe_release_workspaces.  After DG_ERR_TIMEOUT the workspace is let go of, and the next call
+    takes a new one."""
     i = torch.cuda.current_device() if device is None else torch.device(device).index
     key = (i, _raw_stream(i, stream))
     with _moe_lock:

@@ -53,3 +53,18 @@ def test_the_barrier_goes_on_from_any_round():
     for _ in range(3):
         assert torch.equal(dg.moe_tokens(f, h, ws=ws), want)
     assert int(ws[:4].view(torch.int32)) == dg.DG_OK
+
+
+def test_what_a_call_met_outlives_a_larger_workspace():
+    g = torch.Generator().manual_seed(4)
+    f = ffn_of(drawn(g, 256, 8, 128), 2)
+    h = torch.randn(32, 256, generator=g).to(BF).cuda()
+    dg.moe_release_workspaces()
+    want = dg.moe_tokens(f, h)
+    dg.moe_release_workspaces()
+    assert dg.moe_tokens_status() == dg.DG_OK
+    dg.moe_tokens(f, h[:1] * float("nan"))
+    assert torch.equal(dg.moe_tokens(f, h), want)
+    assert dg.moe_tokens_status() == dg.DG_ERR_VALUE
+    dg.moe_release_workspaces()
+    assert torch.equal(dg.moe_tokens(f, h), want) and dg.moe_tokens_status() == dg.DG_OK
