@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(MtArgs a) {
     if (tid < a.M) {
       float sum = 0.f;
       for (int p = 0; p < per; ++p) sum += s.squares[tid][p];
+      // (beyond fp32 the row would come out as zeros, and the routing as that of zeros)
+      if (!(sum <= FLT_MAX) && cta == 0) atomicCAS(a.status, 0, kStatusValue);
       s.inv[tid] = 1.0f / sqrtf(sum / (float)a.d + a.eps);
     }
     // (read after the barrier before the units' sums)

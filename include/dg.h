@@ -544,7 +544,8 @@ DG_API dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int64_t 
  *           either may be NULL
  *   ws      dg_moe_tokens_workspace bytes, 256-byte aligned, zeroed before its first use;
  *           the first 4 bytes are the status word (dg_read_status): DG_ERR_VALUE for
- *           router logits that are not finite (the token's output is not to be used),
+ *           router logits that are not finite or a token whose squares' sum is beyond fp32
+ *           (values of 2^56 are within it; the token's output is not to be used),
  *           DG_ERR_TIMEOUT if a bounded wait ran out (outputs not to be used; calls after
  *           that one are right again, the word stays).  Calls (and graphs) that may overlap
  *           on the GPU need one each.

@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from test_gpu_moe_tokens import BF, drawn, ffn_of
+import moe_tokens_ref
+from test_gpu_moe_tokens import BF, check, drawn, ffn_of
 from block_diffusion_text_gb300 import dg
 
 pytestmark = pytest.mark.gpu
@@ -68,3 +69,22 @@ def test_what_a_call_met_outlives_a_larger_workspace():
     assert dg.moe_tokens_status() == dg.DG_ERR_VALUE
     dg.moe_release_workspaces()
     assert torch.equal(dg.moe_tokens(f, h), want) and dg.moe_tokens_status() == dg.DG_OK
+
+
+@pytest.mark.parametrize("d", [256, 16384])
+@pytest.mark.parametrize("M", [2, 20])
+def test_rows_whose_squares_leave_fp32_are_told(M, d):
+    """2^56 is within the range at the widest row (2^14 squares of 2^112 at most); 2^70 is not."""
+    g = torch.Generator().manual_seed(5)
+    w = drawn(g, d, 8, 128)
+    f = ffn_of(w, 2)
+    h = torch.randn(M, d, generator=g).clamp(-1, 1).to(BF)
+    h[1] *= 2.0 ** 56
+    ws = torch.zeros(f.workspace_bytes(M), dtype=torch.uint8, device="cuda")
+    check(w, h, 2, ffn=f, ws=ws)
+    assert int(ws[:4].view(torch.int32)) == dg.DG_OK
+    h[1] *= 2.0 ** 14
+    got = dg.moe_tokens(f, h.cuda(), ws=ws)
+    assert int(ws[:4].view(torch.int32)) == dg.DG_ERR_VALUE
+    out, tol, *_ = moe_tokens_ref.block(h[:1], *w, 2)
+    assert bool(((got[:1].double().cpu() - out).abs() <= tol).all())
