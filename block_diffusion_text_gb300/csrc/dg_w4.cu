@@ -448,12 +448,13 @@ __global__ void __launch_bounds__(kW4WideWarps * 32, 1) w4_wide_kernel(W4Args a)
   __syncthreads();
   pdl_wait();
 
+  bool ok = true;
   int ppass = 0, pchunk = 0, pslot = 0;  // what is copied next, and where it lies
   auto issue = [&]() {
     if (ppass >= passes) return;
     int n;
     const int rt = tile_of(ppass, n);
-    if (lane == 0 && n > 0) {
+    if (lane == 0 && n > 0 && ok) {
       const int kb = pchunk * kW4Chunk, nk = min(kW4Chunk, KB - kb);
       const int g0 = SG == 2 ? 2 * kb : kb >> sg_shift, ng = SG == 2 ? 2 * nk : nk >> sg_shift;
       uint64_t* bar = &full[warp][pslot];
@@ -485,7 +486,6 @@ __global__ void __launch_bounds__(kW4WideWarps * 32, 1) w4_wide_kernel(W4Args a)
   issue();
   issue();
   unsigned it = 0;  // chunks gone through
-  bool ok = true;
   auto next_x = [&](int pass, int chunk) {
     cp_async_wait<0>();
     __syncthreads();  // this chunk's x is there, and the one before is done with
@@ -574,6 +574,9 @@ __global__ void __launch_bounds__(kW4WideWarps * 32, 1) w4_wide_kernel(W4Args a)
       for (int chunk = 0; chunk < chunks; ++chunk, ++it) next_x(pass, chunk);
     }
   }
+  // after a wait that ran out no copies are begun; the ones on their way are given as long again
+  if (!ok)
+    for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < kWaitLimitNs;) __nanosleep(1000);
 }
 
 template <int NT, int SG>
