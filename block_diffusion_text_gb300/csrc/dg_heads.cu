@@ -180,8 +180,8 @@ extern "C" dg_status dg_qk_norm_rope(const void* qkv, int64_t batch_stride, int6
   const int items = (Hq + 2 * Hkv) * (hd / 16);
   int per = items >= kHeadThreads ? 1 : kHeadThreads / items;
   // with many tokens, a sine and cosine for every thread (16 / 8 heads of 128: 608 tokens
-  // 3.9 us against 3.2 without, 1216 5.0 against 5.2, 4096 12.4 against 16.7, 16384 48.8
-  // against 65.1)
+  // 3.9 us against 3.2 without, 1216 4.9 against 5.2, 4096 12.4 against 16.5, 16384 48.8
+  // against 64.9)
   const int fill = kHeadThreads / (hd / 2);
   if (per < fill && a.tokens >= 2 * kTargetCtas * fill) per = fill;
   const dim3 grid(cdiv(a.tokens, per)), block(kHeadThreads);

@@ -1123,10 +1123,11 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(SpArgs a, SpTable
   }
 }
 
-// CTAs of a row's cluster: slices of 65536 values at most (256 rows of 262144: 4 CTAs
-// 290 us, 8 353, 1 461), shorter ones of 2048 values at least while that gives every SM
-// no more than one CTA (8 rows of 262144: 16 CTAs 43 us, 4 63), and of 16384 up to two
-// (64 rows of 151936: 4 CTAs 68 us, 2 75; 32 of 50257 in 8 CTAs 40, in 4 36).
+// CTAs of a row's cluster: slices of 65536 values at most, of which a run's sample fits its
+// place (256 rows of 262144: 4 CTAs 305 us, 8 347, 16 502), shorter ones of 2048 values at
+// least while that gives every SM no more than one CTA (8 rows of 262144: 16 CTAs 36 us, 8
+// 40, 4 53), and of 16384 up to two (64 rows of 151936: 4 CTAs 60 us, 8 78; 32 of 50257:
+// 4 CTAs 34, 2 44, 8 37; 160 of 50257: 1 CTA 72, 2 81).
 int sample_ctas(int R, int V) {
   int c = 1;
   while (c < kSpMaxCluster && (int64_t)c * 65536 < V) c *= 2;

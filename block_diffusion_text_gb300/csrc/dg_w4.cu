@@ -52,7 +52,9 @@ struct W4StoreArgs {
 };
 
 // A warp writes the tiles of one group of columns (two tiles where the group is
-// 128): rows rt * 16 .., bound by reading the matrix once.
+// 128): rows rt * 16 ...  A matrix is laid out once, so this is the simplest form: loads of
+// one element, and quantising reads the matrix twice (262144 x 2816: quantising 1.32 ms,
+// given codes 0.66, reading back 0.62).
 constexpr int kStoreWarps = 8;
 
 template <bool kQuantize>
@@ -184,9 +186,11 @@ DG_DEV void cp_async4(void* dst, const void* src) {
 }
 
 // Warps that share a unit: as few as leave the waves of sets on an SM's `ctas`
-// CTAs within 5 % of full (fewer barriers), all eight otherwise (one row, K = 2816:
-// 2816 rows with 8, 4, 2, 1 warps 3.9, 5.1, 8.4, 14.3 us; 9728 rows 6.3, 5.8, 8.7,
-// 14.5; 262144 rows 79.7, 76.0, 74.6, 79.8).
+// CTAs within 5 % of full (fewer barriers), all eight otherwise (one row, K = 2816,
+// codes from HBM: 2816 rows with 8, 4, 2, 1 warps 4.6, 7.9, 14.7, 19.6 us; 9728 rows 6.4,
+// 10.0, 16.8, 26.9; 262144 rows 78.3, 75.7, 72.6, 77.7, of which it takes 4).  It does
+// not see that few columns leave warps without any: 262144 x 64 with 8, which it
+// takes, 4, 2, 1 warps 17.7, 14.0, 13.2, 6.2 us, x 256 20.2, 17.9, 17.5, 12.3.
 int w4_split(int units, int KB, int ctas) {
   for (int wk = 1; wk < kW4Warps && wk < KB; wk *= 2) {
     const int sets = cdiv(units, kW4Warps / wk), slots = ctas * kTargetCtas;
@@ -384,7 +388,7 @@ cudaError_t launch_w4(const W4Args& args, cudaStream_t st) {
 // (it would come from L2 twice as often as the codes from HBM), so all warps of a CTA
 // work on the same columns at the same time, on row tiles of their own, and x lies in
 // shared memory for kW4Chunk tiles of columns at a time, in the order of the products'
-// operands (32 rows over 262144 x 2816: 166 us, 203 MB of codes and scales in 89 us at
+// operands (32 rows over 262144 x 2816: 167 us, 203 MB of codes and scales in 89 us at
 // 131072; the MMAs alone are 8 cycles each of a quarter SM, 79 us of it).  A warp has a pair of neighbouring row tiles, whose codes of a tile of
 // columns are one piece of memory: one lane copies a chunk's (cp.async.bulk, two chunks
 // to a warp), so that little but the codes' own work is left to the others.  A CTA has
@@ -588,11 +592,11 @@ cudaError_t launch_w4_wide(const W4Args& a, cudaStream_t st) {
 }
 
 // Four row tiles to a unit (x is read once for them, and their scales in one piece) where
-// there are units enough for all SMs (K = 2816, one row: 9728 rows 5.7 us both ways,
-// 19456 rows 7.9 against 10.9, 38912 rows 15.0 against 22.5; 4864 rows 5.5 against
-// 4.1).  Above eight rows the kernel that keeps x in shared memory, from six pairs of
-// row tiles to an SM on (32 rows of x: 29184 rows 27.3 us against 32.0, 19456 rows
-// 22.5 against 19.9; 16 rows: 19.4 against 21.9, 16.3 against 13.3).
+// there are units enough for all SMs (K = 2816, one row, codes from HBM: 9728 rows 6.4 us
+// against 7.7, 19456 rows 9.5 against 13.1, 38912 rows 14.3 against 19.3; 4864 rows 5.9
+// against 4.9).  Above eight rows the kernel that keeps x in shared memory, from six
+// pairs of row tiles to an SM on (32 rows of x: 29184 rows 26.8 us against 31.5, 19456
+// rows 22.5 against 20.5; 16 rows: 19.1 against 20.9, 16.2 against 15.2).
 template <int SG>
 cudaError_t launch_w4_rows(const W4Args& a, cudaStream_t st) {
   const bool wide = cdiv(a.N, kW4Rows) >= (a.M <= 8 ? 4 : 12) * kTargetCtas;

@@ -504,7 +504,8 @@ DG_API dg_status dg_w4_read(const dg_w4* w, float* out, int64_t ldo, void* strea
  * <= 32.  x bf16 [M][ldx], 16-byte aligned, ldx a multiple of 8; alpha float32 [M] or
  * NULL for ones; resid bf16 [M][ldr] or NULL; y [M][ldy], bf16, or float32 where
  * y_f32 is set (the LM head's logits).  y may be resid itself (same pitch); it must not
- * overlap anything else.  Products are exact, sums fp32, rounded once.             */
+ * overlap anything else.  Products are exact, sums fp32, rounded once.  A group's sum is
+ * taken before its scale, so values of x up to 2^117 leave it within fp32.         */
 DG_API dg_status dg_w4_matvec(const dg_w4* w, const void* x, int64_t ldx, int32_t M, const float* alpha, float coef,
                               const void* resid, int64_t ldr, void* y, int64_t ldy, int32_t y_f32, void* stream);
 
@@ -588,7 +589,8 @@ typedef struct dg_sampling {
  * range gets token -1, logprob NaN and kept 0.
  * Weights are whole numbers of 30 bits and an exponent, down to 2^-42 of the largest
  * (smaller ones count as kept, but are not drawn), and their sums exact: the same bits
- * every time.                                                                      */
+ * every time.  Up to a temperature of 2^112 a weight is good to 2^-28; above, 1 / T
+ * itself has fewer bits.                                                           */
 DG_API dg_status dg_sample(const void* logits, int32_t bf16, int64_t ld, int32_t R, int32_t V, const dg_sampling* how,
                            const float* u, int32_t* token, float* logprob, int32_t* kept, void* stream);
 
